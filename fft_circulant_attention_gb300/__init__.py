@@ -20,7 +20,12 @@ The functions carry the C names: ``cat_plan_create``, ``cat_forward``,
 ``cat_plan_timing``, ``cat_plan_stage_times``, ``cat_plan_pass_times``,
 ``cat_plan_describe``, ``cat_plan_set_stream``, ``cat_plan_destroy`` and
 ``cat_status_string``.  ``Plan`` (1-D) and ``Plan2D`` (token grid) wrap them
-for convenience.
+for convenience.  The operators around a CAT layer in a training step are
+``cat_plan_create_attn``, ``cat_attn_forward``, ``cat_attn_backward``
+(softmax attention over packed sequences, ``AttnPlan``),
+``cat_plan_create_layernorm``, ``cat_layernorm_forward``,
+``cat_layernorm_backward`` (``LayerNormPlan``), ``cat_plan_create_clip``,
+``cat_grad_norm`` and ``cat_grad_clip`` (``ClipPlan``).
 """
 import ctypes
 import os
@@ -42,6 +47,8 @@ for _code, _name in STATUS.items():
 # Every symbol include/cat.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 SIGNATURES = {
     "cat_plan_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _P]),
     "cat_plan_destroy": (_I, [_P]),
@@ -67,6 +74,15 @@ SIGNATURES = {
     "cat2d_forward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I]),
     "cat2d_scores": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I]),
     "cat_probe_dft32": (_I, [_P, _P, _I, _I, _I, _P]),
+    "cat_plan_create_attn": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _I, _I, _F, _P]),
+    "cat_attn_forward": (_I, [_P] * 7 + [_I, _I] + [_L] * 3),
+    "cat_attn_backward": (_I, [_P] * 11 + [_I, _I] + [_L] * 6),
+    "cat_plan_create_layernorm": (_I, [ctypes.POINTER(_P), _I, _I, _I, _F, _P]),
+    "cat_layernorm_forward": (_I, [_P] * 7 + [_I]),
+    "cat_layernorm_backward": (_I, [_P] * 9 + [_I]),
+    "cat_plan_create_clip": (_I, [ctypes.POINTER(_P), _I, _P, _P, _P]),
+    "cat_grad_norm": (_I, [_P, _P, _P]),
+    "cat_grad_clip": (_I, [_P, _P, _P, _F, _P]),
     "cat_status_string": (ctypes.c_char_p, [_I]),
 }
 
@@ -233,6 +249,74 @@ def cat2d_forward(plan, Q, K, V, O, B, h, w, D, H, dtype):
 def cat2d_scores(plan, Q, K, a, B, h, w, D, H, dtype):
     _check(lib().cat2d_scores(plan, _ptr(Q), _ptr(K), _ptr(a), B, h, w, D, H,
                               dtype_code(dtype)), "cat2d_scores")
+
+
+def cat_plan_create_attn(max_tokens, max_seqs, Hq, Hkv, dh, dtype, causal=True, scale=0.0,
+                         stream=None):
+    """Create a softmax-attention plan (packed sequences); returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_attn(ctypes.byref(h), max_tokens, max_seqs, Hq, Hkv, dh,
+                                      dtype_code(dtype), int(causal), scale, _stream(stream)),
+           "cat_plan_create_attn")
+    return h.value
+
+
+def cat_attn_forward(plan, Q, K, V, O, lse, cu_seqlens, T, S, ldq, ldk, ldv):
+    _check(lib().cat_attn_forward(plan, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
+                                  _ptr(cu_seqlens), T, S, ldq, ldk, ldv), "cat_attn_forward")
+
+
+def cat_attn_backward(plan, Q, K, V, O, lse, dO, dQ, dK, dV, cu_seqlens, T, S, ldq, ldk, ldv,
+                      lddq, lddk, lddv):
+    _check(lib().cat_attn_backward(plan, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), _ptr(dO),
+                                   _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(cu_seqlens), T, S, ldq, ldk,
+                                   ldv, lddq, lddk, lddv), "cat_attn_backward")
+
+
+def cat_plan_create_layernorm(max_rows, D, dtype, eps=1e-5, stream=None):
+    """Create a layer-norm plan; returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_layernorm(ctypes.byref(h), max_rows, D, dtype_code(dtype), eps,
+                                           _stream(stream)), "cat_plan_create_layernorm")
+    return h.value
+
+
+def cat_layernorm_forward(plan, X, gamma, beta, Y, mean, rstd, rows):
+    _check(lib().cat_layernorm_forward(plan, _ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y),
+                                       _ptr(mean), _ptr(rstd), rows), "cat_layernorm_forward")
+
+
+def cat_layernorm_backward(plan, X, gamma, mean, rstd, dY, dX, dgamma, dbeta, rows):
+    _check(lib().cat_layernorm_backward(plan, _ptr(X), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                        _ptr(dY), _ptr(dX), _ptr(dgamma), _ptr(dbeta), rows),
+           "cat_layernorm_backward")
+
+
+def cat_plan_create_clip(sizes, dtypes, stream=None):
+    """Create a gradient-clipping plan for tensors of these sizes and dtypes;
+    returns its handle."""
+    n = len(sizes)
+    if len(dtypes) != n:
+        raise ValueError("sizes and dtypes differ in length")
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_clip(ctypes.byref(h), n, (_L * n)(*sizes),
+                                      (_I * n)(*[dtype_code(d) for d in dtypes]),
+                                      _stream(stream)), "cat_plan_create_clip")
+    return h.value
+
+
+def _addresses(tensors):
+    return (_P * len(tensors))(*[_ptr(t) for t in tensors])
+
+
+def cat_grad_norm(plan, grads, norm):
+    _check(lib().cat_grad_norm(plan, _addresses(grads), _ptr(norm)), "cat_grad_norm")
+
+
+def cat_grad_clip(plan, grads, outs, max_norm, norm):
+    a = _addresses(grads)
+    _check(lib().cat_grad_clip(plan, a, a if outs is grads else _addresses(outs), max_norm,
+                               _ptr(norm)), "cat_grad_clip")
 
 
 def cat_plan_sync(plan):
@@ -437,7 +521,271 @@ class Plan2D:
             pass
 
 
-__all__ = ["CatError", "Plan", "Plan2D", "lib", "dtype_code", "cat_plan_create", "cat_plan_destroy",
+class _OpPlan:
+    """What the operator plans share.  With a stream given, every call runs on
+    it; without one, on torch's current stream at the call."""
+
+    def _open(self, device, stream):
+        import torch
+        if device is None:
+            device = torch.cuda.current_device() if torch.cuda.is_available() else 0
+        self.device = torch.device("cuda", device) if isinstance(device, int) else \
+            torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self._fixed = stream is not None
+        self._on = _stream(stream) if self._fixed else None
+
+    def _use(self):
+        """Point the plan at the stream this call runs on."""
+        if not self._fixed:
+            import torch
+            s = torch.cuda.current_stream(self.device).cuda_stream
+            if s != self._on:
+                cat_plan_set_stream(self.handle, s)
+                self._on = s
+
+    def _tensor(self, t, name, dtype, shape=None, rows=False):
+        """`t` on the plan's device, of `dtype` and `shape`, contiguous (`rows`:
+        contiguous within each token row)."""
+        if t.device != self.device:
+            raise ValueError("%s is on %s, the plan on %s" % (name, t.device, self.device))
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s" % (name, dtype))
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+        if rows:
+            st, w = t.stride(), t.shape[2]
+            if t.numel() and ((w > 1 and st[2] != 1) or (t.shape[1] > 1 and st[1] != w)):
+                raise ValueError("%s: the heads of a token row must be contiguous" % name)
+        elif not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return t
+
+    def sync(self):
+        cat_plan_sync(self.handle)
+
+    def describe(self):
+        return cat_plan_describe(self.handle)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            cat_plan_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _on_device(device):
+    import contextlib
+
+    import torch
+    return torch.cuda.device(device) if torch.cuda.is_available() else contextlib.nullcontext()
+
+
+class AttnPlan(_OpPlan):
+    """Softmax attention over packed sequences: up to ``max_tokens`` rows and
+    ``max_seqs`` sequences a call, ``Hq`` query heads over ``Hkv`` key heads of
+    width ``dh``.
+
+    ``forward(Q, K, V, cu_seqlens)`` -> (O, lse) and ``backward(Q, K, V, O,
+    lse, dO, cu_seqlens)`` -> (dQ, dK, dV); Q, O, dO [T, Hq, dh], K, V
+    [T, Hkv, dh], lse fp32 [Hq, T], cu_seqlens int32 [S + 1] on the device.
+    Q, K, V (and dQ, dK, dV where given) may be column ranges of wider rows.
+    """
+
+    def __init__(self, max_tokens, max_seqs, Hq, Hkv, dh, dtype, causal=True, scale=None,
+                 stream=None, device=None):
+        import torch
+        self.Hq, self.Hkv, self.dh = Hq, Hkv, dh
+        self.dtype = dtype_code(dtype)
+        self.torch_dtype = torch.bfloat16 if self.dtype == CAT_BF16 else torch.float32
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_attn(max_tokens, max_seqs, Hq, Hkv, dh, self.dtype,
+                                               causal, 0.0 if scale is None else scale, self._on)
+
+    def _inputs(self, Q, K, V, cu_seqlens):
+        import torch
+        T = Q.shape[0]
+        self._tensor(Q, "Q", self.torch_dtype, (T, self.Hq, self.dh), rows=True)
+        self._tensor(K, "K", self.torch_dtype, (T, self.Hkv, self.dh), rows=True)
+        self._tensor(V, "V", self.torch_dtype, (T, self.Hkv, self.dh), rows=True)
+        self._tensor(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must have S + 1 entries")
+        return T, cu_seqlens.shape[0] - 1
+
+    def _ld(self, t):
+        # A single row has no stride of its own (torch may report any).
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+    def forward(self, Q, K, V, cu_seqlens, O=None, lse=None):
+        import torch
+        T, S = self._inputs(Q, K, V, cu_seqlens)
+        if O is None:
+            O = torch.empty((T, self.Hq, self.dh), dtype=self.torch_dtype, device=self.device)
+        else:
+            self._tensor(O, "O", self.torch_dtype, (T, self.Hq, self.dh))
+        if lse is None:
+            lse = torch.empty((self.Hq, T), dtype=torch.float32, device=self.device)
+        else:
+            self._tensor(lse, "lse", torch.float32, (self.Hq, T))
+        self._use()
+        cat_attn_forward(self.handle, Q, K, V, O, lse, cu_seqlens, T, S, self._ld(Q), self._ld(K),
+                         self._ld(V))
+        return O, lse
+
+    def backward(self, Q, K, V, O, lse, dO, cu_seqlens, dQ=None, dK=None, dV=None):
+        import torch
+        T, S = self._inputs(Q, K, V, cu_seqlens)
+        q, k = (T, self.Hq, self.dh), (T, self.Hkv, self.dh)
+        self._tensor(O, "O", self.torch_dtype, q)
+        self._tensor(dO, "dO", self.torch_dtype, q)
+        self._tensor(lse, "lse", torch.float32, (self.Hq, T))
+        out = []
+        for t, name, shape in ((dQ, "dQ", q), (dK, "dK", k), (dV, "dV", k)):
+            if t is None:
+                t = torch.empty(shape, dtype=self.torch_dtype, device=self.device)
+            else:
+                self._tensor(t, name, self.torch_dtype, shape, rows=True)
+            out.append(t)
+        self._use()
+        cat_attn_backward(self.handle, Q, K, V, O, lse, dO, out[0], out[1], out[2], cu_seqlens, T,
+                          S, self._ld(Q), self._ld(K), self._ld(V), self._ld(out[0]),
+                          self._ld(out[1]), self._ld(out[2]))
+        return tuple(out)
+
+
+class LayerNormPlan(_OpPlan):
+    """Layer norm over the last dimension (``D``) of up to ``max_rows`` rows.
+
+    ``forward(X, gamma=None, beta=None)`` -> (Y, mean, rstd) and ``backward(X,
+    gamma, mean, rstd, dY)`` -> (dX, dgamma, dbeta); X, Y, dY, dX [..., D],
+    mean and rstd fp32 [...].
+    """
+
+    def __init__(self, max_rows, D, dtype, eps=1e-5, stream=None, device=None):
+        import torch
+        self.D = D
+        self.dtype = dtype_code(dtype)
+        self.torch_dtype = torch.bfloat16 if self.dtype == CAT_BF16 else torch.float32
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_layernorm(max_rows, D, self.dtype, eps, self._on)
+
+    def _rows(self, X, gamma, beta=None):
+        if X.dim() < 1 or X.shape[-1] != self.D:
+            raise ValueError("the last dimension must be %d" % self.D)
+        self._tensor(X, "X", self.torch_dtype)
+        for t, name in ((gamma, "gamma"), (beta, "beta")):
+            if t is not None:
+                self._tensor(t, name, self.torch_dtype, (self.D,))
+        return X.numel() // self.D
+
+    def forward(self, X, gamma=None, beta=None, Y=None, mean=None, rstd=None):
+        import torch
+        rows = self._rows(X, gamma, beta)
+        if Y is None:
+            Y = torch.empty_like(X)
+        else:
+            self._tensor(Y, "Y", self.torch_dtype, X.shape)
+        stats = []
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is None:
+                t = torch.empty(X.shape[:-1], dtype=torch.float32, device=self.device)
+            else:
+                self._tensor(t, name, torch.float32, X.shape[:-1])
+            stats.append(t)
+        self._use()
+        cat_layernorm_forward(self.handle, X, gamma, beta, Y, stats[0], stats[1], rows)
+        return Y, stats[0], stats[1]
+
+    def backward(self, X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None):
+        import torch
+        rows = self._rows(X, gamma)
+        self._tensor(dY, "dY", self.torch_dtype, X.shape)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            self._tensor(t, name, torch.float32, X.shape[:-1])
+        if dX is None:
+            dX = torch.empty_like(X)
+        else:
+            self._tensor(dX, "dX", self.torch_dtype, X.shape)
+        grads = []
+        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+            if t is None:
+                t = torch.empty((self.D,), dtype=self.torch_dtype, device=self.device)
+            else:
+                self._tensor(t, name, self.torch_dtype, (self.D,))
+            grads.append(t)
+        self._use()
+        cat_layernorm_backward(self.handle, X, gamma, mean, rstd, dY, dX, grads[0], grads[1], rows)
+        return dX, grads[0], grads[1]
+
+
+class ClipPlan(_OpPlan):
+    """The global norm of a list of gradients of these ``sizes`` (elements) and
+    ``dtypes``, and clipping by it.
+
+    ``norm(grads)`` -> fp32 scalar tensor; ``clip(grads, max_norm, out=None)``
+    scales the gradients in place (or into ``out``) by max_norm / norm where
+    the norm is larger, and returns the norm before clipping.
+    """
+
+    def __init__(self, sizes, dtypes, stream=None, device=None):
+        import torch
+        self.sizes = [int(n) for n in sizes]
+        self.dtypes = [torch.bfloat16 if dtype_code(d) == CAT_BF16 else torch.float32
+                       for d in dtypes]
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_clip(self.sizes, self.dtypes, self._on)
+
+    def _list(self, tensors, name):
+        if len(tensors) != len(self.sizes):
+            raise ValueError("%d %s for a plan of %d" % (len(tensors), name, len(self.sizes)))
+        for t, n, d in zip(tensors, self.sizes, self.dtypes):
+            if t.dtype != d or t.numel() != n or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("%s must be contiguous, of the plan's sizes, dtypes and device"
+                                 % name)
+
+    def norm(self, grads, norm=None):
+        import torch
+        self._list(grads, "grads")
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        self._use()
+        cat_grad_norm(self.handle, grads, norm)
+        return norm
+
+    def clip(self, grads, max_norm, out=None, norm=None):
+        import torch
+        self._list(grads, "grads")
+        if out is None:
+            out = grads
+        else:
+            self._list(out, "out")
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        self._use()
+        cat_grad_clip(self.handle, grads, out, max_norm, norm)
+        return norm
+
+
+__all__ = ["AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",
+           "cat_attn_backward", "cat_plan_create_layernorm", "cat_layernorm_forward",
+           "cat_layernorm_backward", "cat_plan_create_clip", "cat_grad_norm", "cat_grad_clip",
+           "CatError", "Plan", "Plan2D", "lib", "dtype_code", "cat_plan_create", "cat_plan_destroy",
            "cat_plan_set_stream", "cat_forward", "cat_forward_zstar", "cat_forward_host",
            "cat_plan_sync", "cat_plan_describe", "cat_plan_timing", "cat_plan_stage_times",
            "cat_plan_pass_times", "cat_forward_noalloc", "cat_backward", "cat_backward_dz",

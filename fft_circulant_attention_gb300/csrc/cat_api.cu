@@ -84,6 +84,7 @@ bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 int check_shape(const cat_plan_s* p, int B, int N, int D, int H, int dtype) {
+  if (p->op) return CAT_ERR_PLAN_MISMATCH;
   if (B != p->B || N != p->N || D != p->D || H != p->H || dtype != p->dtype)
     return CAT_ERR_PLAN_MISMATCH;
   return CAT_OK;
@@ -164,6 +165,7 @@ void free_plan(cat_plan_s* p) {
   }
   cudaFree(p->hwa);
   cudaFree(p->pj_wt);
+  cat::free_op(p);
   delete p;
 }
 
@@ -1391,6 +1393,10 @@ int cat2d_forward(cat_plan_t p, const void* Q, const void* K, const void* V, voi
 
 int cat_plan_sync(cat_plan_t p) {
   if (!p) return CAT_ERR_INVALID_ARG;
+  // The NULL stream and the copies below are the current device's; the
+  // operator plans may be used with another device current.
+  cat::DeviceGuard dev(p->op ? p->device : -1);
+  if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   if (cudaStreamSynchronize(p->stream) != cudaSuccess) return CAT_ERR_CUDA;
   // The plan's own status word and those of its host-buffer sub-plans.
   int st = CAT_OK;
@@ -1410,6 +1416,7 @@ int cat_plan_sync(cat_plan_t p) {
 
 int cat_plan_timing(cat_plan_t p, int max_calls) {
   if (!p || max_calls < 0) return CAT_ERR_INVALID_ARG;
+  if (p->op) return CAT_ERR_PLAN_MISMATCH;
   if (cudaStreamSynchronize(p->stream) != cudaSuccess) return CAT_ERR_CUDA;
   free_events(p);
   if (max_calls == 0) return CAT_OK;
@@ -1429,6 +1436,7 @@ int cat_plan_timing(cat_plan_t p, int max_calls) {
 
 int cat_plan_stage_times(cat_plan_t p, float* ms, int cap, int* ncalls) {
   if (!p || !ms || cap < 3) return CAT_ERR_INVALID_ARG;
+  if (p->op) return CAT_ERR_PLAN_MISMATCH;
   if (cudaStreamSynchronize(p->stream) != cudaSuccess) return CAT_ERR_CUDA;
   ms[0] = ms[1] = ms[2] = 0.f;
   for (int c = 0; c < p->timing_n; ++c) {
@@ -1446,6 +1454,7 @@ int cat_plan_stage_times(cat_plan_t p, float* ms, int cap, int* ncalls) {
 
 int cat_plan_pass_times(cat_plan_t p, float* ms, int cap, int* launches) {
   if (!p || !ms || cap < 3) return CAT_ERR_INVALID_ARG;
+  if (p->op) return CAT_ERR_PLAN_MISMATCH;
   if (p->path != cat::PATH_FAST) return CAT_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(p->stream) != cudaSuccess) return CAT_ERR_CUDA;
   ms[0] = ms[1] = ms[2] = 0.f;

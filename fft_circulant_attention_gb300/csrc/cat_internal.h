@@ -81,6 +81,48 @@ struct BwCfg {
   size_t scratch_bytes;
 };
 
+// Layer norm call (layernorm.cu).
+struct NormArgs {
+  const void* x; const void* gamma; const void* beta; const void* dy;
+  void* y; void* dx; void* dgamma; void* dbeta;
+  float* mean; float* rstd;
+  float* part;             // [max_parts][2][D] partial sums of dgamma and dbeta
+  int max_parts, rows, D;
+  float eps;
+};
+
+// A run of at most 32 KB of one gradient (gradclip.cu).
+struct ClipChunk {
+  int tensor, bf16, count;
+  long long offset;        // first element
+};
+
+// Gradient list of a clipping plan.
+struct ClipCfg {
+  int count;               // tensors
+  int grid;                // CTAs of a launch
+  const int* first_chunk;  // host [count + 1]
+  const long long* sizes;  // host [count]
+  const int* dtypes;       // host [count]
+  ClipChunk* chunks;       // device
+  double* part;            // device, a sum of squares a CTA
+};
+
+struct AttnArgs;
+
+// What the plans of cat_plan_create_attn, _layernorm and _clip hold.
+enum Op { OP_CIRCULANT = 0, OP_ATTN = 1, OP_LAYERNORM = 2, OP_CLIP = 3 };
+struct AttnCfg {
+  int max_tokens, max_seqs, Hq, Hkv, dh, causal;
+  float scale;
+  float* delta;            // [Hq][max_tokens]
+};
+struct NormCfg {
+  int max_rows, max_parts;
+  float eps;
+  float* part;
+};
+
 }  // namespace cat
 
 struct cat_plan_s {
@@ -163,6 +205,12 @@ struct cat_plan_s {
   float* bw_dzs;            // [B, H, N] dL/dz*
   float* bw_dz;             // [B, H, N] dL/dz
   float* bw_wpart;          // [wsplit, H, D] partial sums of dW_A
+  // plans of other operators (cat::Op): only the fields below, dtype, D,
+  // device, sms, stream, status and desc are theirs
+  int op;
+  cat::AttnCfg at;
+  cat::NormCfg ln;
+  cat::ClipCfg cl;
   char desc[512];
 };
 
@@ -190,6 +238,27 @@ struct Span {
   bool own = false;              // true: use st instead of the plan's stream
   int nb(const cat_plan_s* p) const { return nbat < 0 ? p->B - b0 : nbat; }
   cudaStream_t stream(const cat_plan_s* p) const { return own ? st : p->stream; }
+};
+
+// Makes `device` current for a scope (device < 0: leaves it), and the one
+// that was current again at its end.
+struct DeviceGuard {
+  int prev = -1;
+  cudaError_t status = cudaSuccess;
+  explicit DeviceGuard(int device) {
+    if (device < 0) return;
+    int cur = -1;
+    status = cudaGetDevice(&cur);
+    if (status == cudaSuccess && cur != device) {
+      status = cudaSetDevice(device);
+      if (status == cudaSuccess) prev = cur;
+    }
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+  DeviceGuard(const DeviceGuard&) = delete;
+  DeviceGuard& operator=(const DeviceGuard&) = delete;
 };
 
 // Let `kernel` use all the dynamic shared memory the current device allows
@@ -306,6 +375,25 @@ size_t project_workspace_bytes(int D);
 cudaError_t setup_project_kernels();
 cudaError_t launch_project(const cat_plan_s* p, const void* X, const void* WV, const void* WA,
                            void* V, void* wt);
+
+// Softmax attention over packed sequences (attn.cu).
+cudaError_t setup_attn();
+cudaError_t launch_attn_forward(const cat_plan_s* p, const AttnArgs& a);
+cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a);
+
+// Layer norm (layernorm.cu).  layernorm_parts: partial rows of the weight
+// gradients, at most one a CTA.
+int layernorm_parts(int sms);
+cudaError_t launch_layernorm(const NormArgs& a, int dtype, bool backward, cudaStream_t st);
+
+// Gradient norm and clipping (gradclip.cu).
+int clip_chunk_elems(int dtype);
+int clip_grid(int sms);
+int clip_max_parts(int count, int sms);
+cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
+                        float* norm, bool scale, cudaStream_t st);
+// Device and host memory of a plan's operator (block_api.cu).
+void free_op(cat_plan_s* p);
 
 // Shape validation and shared-memory-path configuration without allocation.
 int validate(int B, int N, int D, int H, int dtype);

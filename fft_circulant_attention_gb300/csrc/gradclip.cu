@@ -1,0 +1,306 @@
+// The global gradient norm over many tensors, and clipping by it.
+//   n = sqrt(Σ_t Σ_k g_t[k]²), c = max_norm / n if n > max_norm else 1,
+//   out_t[k] = c·g_t[k]; with an infinity or NaN among the gradients c = 1.
+//
+// Bound by memory: one read for the norm, one read and one write for the
+// scaling.  Tensors are cut into chunks of 32 KB; the chunk table is built
+// once a plan (sizes and types), the addresses travel in the launch
+// parameters of every call.  Kernel 1 gives each CTA's sum over every
+// gridDim-th chunk; kernel 2 adds those sums (every CTA for itself, in the
+// same fixed order: no atomics, results repeat bit for bit) and scales its
+// chunks, last chunk first, since the last ones read are still in L2.
+//
+// Squares leave the fp32 range long before the values do, so a vector whose
+// largest magnitude is beyond 2^±50 is scaled by 2^∓80 before squaring and
+// summed apart; the three sums meet in fp64.
+#include "cat_internal.h"
+#include "elem.cuh"
+#include "../../include/cat.h"
+
+namespace cat {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kFew = 64, kMany = 1000;      // tensors of one launch
+constexpr int kUnroll = 4;      // 16-byte loads in flight a thread: 512·4·16 = one chunk
+
+template <int N>
+struct Ptrs {
+  const void* in[N];
+  void* out[N];
+};
+
+struct Sums {
+  float big, mid, small;
+};
+
+// The squares of v[0 .. N - 1] to the sum of their range.  (fmaxf drops a
+// NaN, whose square then reaches whichever sum the others choose.)
+template <int N>
+__device__ __forceinline__ void add_group(Sums& s, const float* v) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
+  if (top > 0x1p50f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = v[i] * 0x1p-80f;
+      s.big = fmaf(x, x, s.big);
+    }
+  } else if (top < 0x1p-50f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = v[i] * 0x1p80f;
+      s.small = fmaf(x, x, s.small);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s.mid = fmaf(v[i], v[i], s.mid);
+  }
+}
+
+// 16 bytes of a tensor as fp32.
+template <typename T>
+struct Pack;
+template <>
+struct Pack<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void widen(uint4 x, float* v) {
+    v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+    v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+  }
+  static __device__ __forceinline__ uint4 narrow(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void widen(uint4 x, float* v) {
+    const unsigned int w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 narrow(const float* v) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    return *reinterpret_cast<uint4*>(h);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void sum_chunk(Sums& s, const T* p, int n) {
+  constexpr int kN = Pack<T>::kN;
+  // Elements before the first 16-byte boundary, then vectors, then the rest.
+  int head = (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T));
+  if (head > n) head = n;
+  const int nv = (n - head) / kN;
+  const uint4* q = reinterpret_cast<const uint4*>(p + head);
+  for (int i0 = 0; i0 < nv; i0 += kThreads * kUnroll) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + threadIdx.x;
+      x[u] = i < nv ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float v[kN];
+      Pack<T>::widen(x[u], v);
+      add_group<kN>(s, v);
+    }
+  }
+  const int rest = n - head - nv * kN;
+  if ((int)threadIdx.x < head) {
+    const float v = ld_elem(p + threadIdx.x);
+    add_group<1>(s, &v);
+  }
+  if ((int)threadIdx.x < rest) {
+    const float v = ld_elem(p + head + nv * kN + threadIdx.x);
+    add_group<1>(s, &v);
+  }
+}
+
+// o = c·p; clips = false: the bits as they are (a NaN's too).
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float c, bool clips) {
+  constexpr int kN = Pack<T>::kN;
+  if (((uintptr_t)p | (uintptr_t)o) & 15) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      if (clips) st_elem(o + i, c * ld_elem(p + i));
+      else o[i] = p[i];
+    }
+    return;
+  }
+  const int nv = n / kN;
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  uint4* w = reinterpret_cast<uint4*>(o);
+  for (int i0 = 0; i0 < nv; i0 += kThreads * kUnroll) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + threadIdx.x;
+      if (i < nv) x[u] = q[i];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + threadIdx.x;
+      if (i < nv) {
+        if (clips) {
+          float v[kN];
+          Pack<T>::widen(x[u], v);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) v[e] *= c;
+          x[u] = Pack<T>::narrow(v);
+        }
+        w[i] = x[u];
+      }
+    }
+  }
+  const int i = nv * kN + threadIdx.x;
+  if (i < n) {
+    if (clips) st_elem(o + i, c * ld_elem(p + i));
+    else o[i] = p[i];
+  }
+}
+
+// Sum over the CTA, the same value in every thread.
+__device__ __forceinline__ double block_total(double v, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int i = 0; i < kThreads / 32; ++i) v += red[i];
+  return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_norm_kernel(const __grid_constant__ Ptrs<N> ptrs, const ClipChunk* __restrict__ chunks,
+                 int nchunks, int first, double* __restrict__ part) {
+  __shared__ double red[kThreads / 32];
+  Sums s = {0.f, 0.f, 0.f};
+  for (int i = blockIdx.x; i < nchunks; i += gridDim.x) {
+    const ClipChunk c = chunks[i];
+    const void* base = ptrs.in[c.tensor - first];
+    if (c.bf16)
+      sum_chunk(s, static_cast<const __nv_bfloat16*>(base) + c.offset, c.count);
+    else
+      sum_chunk(s, static_cast<const float*>(base) + c.offset, c.count);
+  }
+  const double v = (double)s.mid + (double)s.big * 0x1p160 + (double)s.small * 0x1p-160;
+  const double t = block_total(v, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = t;
+  pdl_trigger();
+}
+
+// The norm from the CTAs' sums, the same value in every thread.
+__device__ __forceinline__ double total_norm(const double* part, int nparts, double* red) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < nparts; i += kThreads) v += __ldcg(part + i);
+  return sqrt(block_total(v, red));
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_scale_kernel(const __grid_constant__ Ptrs<N> ptrs, const ClipChunk* __restrict__ chunks,
+                  int nchunks, int first, const double* part, int nparts, float max_norm,
+                  float* norm) {
+  __shared__ double red[kThreads / 32];
+  pdl_wait();
+  const double n = total_norm(part, nparts, red);
+  if (first == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+  const bool clips = n > (double)max_norm && n <= 1.7976931348623157e308;
+  const float c = clips ? (float)((double)max_norm / n) : 1.f;
+  for (int i = nchunks - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+    const ClipChunk k = chunks[i];
+    const void* in = ptrs.in[k.tensor - first];
+    void* out = ptrs.out[k.tensor - first];
+    if (!clips && in == out) continue;          // unchanged, where it is
+    if (k.bf16)
+      scale_chunk(static_cast<const __nv_bfloat16*>(in) + k.offset,
+                  static_cast<__nv_bfloat16*>(out) + k.offset, k.count, c, clips);
+    else
+      scale_chunk(static_cast<const float*>(in) + k.offset, static_cast<float*>(out) + k.offset,
+                  k.count, c, clips);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+clip_finish_kernel(const double* part, int nparts, float* norm) {
+  __shared__ double red[kThreads / 32];
+  pdl_wait();
+  const double n = total_norm(part, nparts, red);
+  if (threadIdx.x == 0) *norm = (float)n;
+}
+
+template <int N>
+cudaError_t run(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
+                float* norm, bool scale, cudaStream_t st) {
+  const int groups = (c.count + N - 1) / N;
+  Ptrs<N> ptrs = {};
+  auto fill = [&](int g, int* first) {
+    *first = g * N;
+    const int n = c.count - *first < N ? c.count - *first : N;
+    for (int i = 0; i < n; ++i) {
+      ptrs.in[i] = in[*first + i];
+      ptrs.out[i] = out ? out[*first + i] : nullptr;
+    }
+    return n;
+  };
+  cudaError_t e = cudaSuccess;
+  int nparts = 0;
+  for (int g = 0; g < groups && e == cudaSuccess; ++g) {
+    int first;
+    const int n = fill(g, &first);
+    const int c0 = c.first_chunk[first], nc = c.first_chunk[first + n] - c0;
+    if (nc == 0) continue;
+    const int grid = nc < c.grid ? nc : c.grid;
+    clip_norm_kernel<N><<<grid, kThreads, 0, st>>>(ptrs, c.chunks + c0, nc, first,
+                                                   c.part + nparts);
+    nparts += grid;
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  if (!scale || groups == 0)
+    return launch_dependent(clip_finish_kernel, dim3(1), dim3(kThreads), 0, st,
+                            (const double*)c.part, nparts, norm);
+  for (int g = 0; g < groups && e == cudaSuccess; ++g) {
+    int first;
+    const int n = fill(g, &first);
+    const int c0 = c.first_chunk[first], nc = c.first_chunk[first + n] - c0;
+    if (nc == 0 && g > 0) continue;             // (group 0 always writes the norm)
+    const int grid = nc < 1 ? 1 : nc < c.grid ? nc : c.grid;
+    if (g == 0) {
+      e = launch_dependent(clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, st, ptrs,
+                           (const ClipChunk*)(c.chunks + c0), nc, first, (const double*)c.part,
+                           nparts, max_norm, norm);
+    } else {
+      clip_scale_kernel<N><<<grid, kThreads, 0, st>>>(ptrs, c.chunks + c0, nc, first, c.part,
+                                                      nparts, max_norm, norm);
+      e = cudaGetLastError();
+    }
+  }
+  return e;
+}
+
+}  // namespace
+
+int clip_chunk_elems(int dtype) { return dtype == CAT_BF16 ? 16384 : 8192; }
+int clip_grid(int sms) { return 2 * sms; }
+int clip_max_parts(int count, int sms) { return ((count + kMany - 1) / kMany + 1) * clip_grid(sms); }
+
+cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
+                        float* norm, bool scale, cudaStream_t st) {
+  return c.count <= kFew ? run<kFew>(c, in, out, max_norm, norm, scale, st)
+                         : run<kMany>(c, in, out, max_norm, norm, scale, st);
+}
+
+}  // namespace cat

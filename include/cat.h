@@ -259,6 +259,150 @@ int cat2d_scores(cat_plan_t plan, const void *Q, const void *K, float *a,
                  int B, int h, int w, int D, int H, int dtype);
 
 /*
+ * Operators around a CAT layer in a training step: the notes page cited
+ * above alternates CAT layers with ordinary softmax attention (CAT-Alter) in
+ * pre-norm ViT and GPT-2 stacks trained by a clipped optimiser.  Their plans
+ * are cat_plan_t too: cat_plan_sync, cat_plan_describe, cat_plan_set_stream
+ * and cat_plan_destroy serve them, every other plan call returns
+ * CAT_ERR_PLAN_MISMATCH for them.  Calls are asynchronous on the plan's
+ * stream, may be captured into a CUDA graph, and run on the plan's device
+ * whichever device is current.  A plan's workspace is reused by every call
+ * (and by every graph captured from it), so the calls and replays of one
+ * plan must not run concurrently.  Results repeat bit for bit.
+ */
+
+/* Widest head of the softmax attention. */
+#define CAT_ATTN_MAX_DH 128
+
+/*
+ * cat_plan_create_attn — softmax attention over packed sequences: T token
+ * rows hold S sequences of different lengths one after another, sequence s
+ * in rows cu_seqlens[s] .. cu_seqlens[s+1] - 1, each attending to itself
+ * only.  Hq query heads share Hkv key heads, query head h reads key head
+ * h / (Hq / Hkv).
+ *
+ *   max_tokens, max_seqs : the largest T and S of a call, >= 0 (their blocks,
+ *            (max_tokens / 64 + max_seqs)·Hq, and max_tokens·Hq within 2^31)
+ *   Hq, Hkv, dh : heads and head width, Hq % Hkv == 0, 1 <= dh <=
+ *            CAT_ATTN_MAX_DH, Hq·dh <= 2^20
+ *   dtype  : of Q, K, V, O and the gradients; products accumulate in fp32,
+ *            lse is fp32
+ *   causal : 1: row i of a sequence sees rows 0 .. i of it; 0: all of it
+ *   scale  : factor of the scores, > 0; 0 means 1/sqrt(dh)
+ *   stream : as for cat_plan_create
+ * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_attn(cat_plan_t *out, int max_tokens, int max_seqs, int Hq,
+                         int Hkv, int dh, int dtype, int causal, float scale,
+                         void *stream);
+
+/*
+ * cat_attn_forward — per sequence and head, with its rows i, j:
+ *   s_ij = scale·q_i·k_j (j <= i if causal), lse_i = log Σ_j exp(s_ij),
+ *   o_i  = Σ_j exp(s_ij - lse_i) v_j.
+ *
+ * Q [T, Hq, dh], K and V [T, Hkv, dh]: token rows ldq, ldk, ldv elements
+ * apart (>= the row's own width; heads dense in a row), so that they may be
+ * columns of one projection's output.  O [T, Hq, dh] and lse [Hq, T] (fp32,
+ * for the backward): dense, written.  cu_seqlens: device array of S + 1
+ * ascending int values within 0 .. T.  Rows that no sequence holds (before
+ * cu_seqlens[0], from cu_seqlens[S] on) are neither read into any result nor
+ * written; a sequence may be empty.  Pointers need the alignment of their
+ * element type; bf16 data whose rows and heads all start on 16-byte
+ * boundaries takes the faster tensor-core kernels.  A pair the mask excludes
+ * contributes nothing, whatever its rows hold.  If cu_seqlens is not
+ * ascending within 0 .. T, the sequences concerned are skipped and
+ * cat_plan_sync returns CAT_ERR_DEVICE_STATUS.
+ * Errors: CAT_ERR_PLAN_MISMATCH (not an attention plan, T or S above the
+ * plan's), CAT_ERR_INVALID_ARG, CAT_ERR_MISALIGNED, CAT_ERR_ALIAS (an output
+ * meets an input or another output), CAT_ERR_CUDA.  T = 0 or S = 0: no-op.
+ */
+int cat_attn_forward(cat_plan_t plan, const void *Q, const void *K,
+                     const void *V, void *O, float *lse, const int *cu_seqlens,
+                     int T, int S, long long ldq, long long ldk, long long ldv);
+
+/*
+ * cat_attn_backward — gradients for the upstream gradient dO = dL/dO, from
+ * the forward's inputs and its O and lse:
+ *   p_ij = exp(s_ij - lse_i), ds_ij = p_ij (dO_i·v_j - dO_i·o_i),
+ *   dQ_i = scale Σ_j ds_ij k_j, dK_j = scale Σ_i ds_ij q_i, dV_j = Σ_i p_ij dO_i,
+ * dK and dV summed over the query heads that share the key head.  O and dO
+ * dense; dQ, dK, dV with token strides lddq, lddk, lddv (they may be columns
+ * of one buffer), overwritten, not accumulated into.  Other arguments and
+ * errors as for cat_attn_forward.
+ */
+int cat_attn_backward(cat_plan_t plan, const void *Q, const void *K,
+                      const void *V, const void *O, const float *lse,
+                      const void *dO, void *dQ, void *dK, void *dV,
+                      const int *cu_seqlens, int T, int S, long long ldq,
+                      long long ldk, long long ldv, long long lddq,
+                      long long lddk, long long lddv);
+
+/*
+ * cat_plan_create_layernorm — layer norm over rows of D elements
+ * (1 <= D <= CAT_MAX_D), at most max_rows of them a call (>= 0); eps >= 0.
+ * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_layernorm(cat_plan_t *out, int max_rows, int D, int dtype,
+                              float eps, void *stream);
+
+/*
+ * cat_layernorm_forward — per row of X [rows, D], with its mean and
+ * rstd = 1/sqrt(variance + eps) (the variance over D, not D - 1):
+ *   Y = (X - mean)·rstd·gamma + beta.
+ * gamma and beta [D] may be NULL (1 and 0).  mean and rstd [rows] (fp32) are
+ * written for the backward.  X, gamma, beta, Y: the plan's dtype, dense,
+ * 16-byte aligned; outputs must not overlap inputs or each other
+ * (CAT_ERR_ALIAS).  rows above the plan's: CAT_ERR_PLAN_MISMATCH.
+ */
+int cat_layernorm_forward(cat_plan_t plan, const void *X, const void *gamma,
+                          const void *beta, void *Y, float *mean, float *rstd,
+                          int rows);
+
+/*
+ * cat_layernorm_backward — with x̂ = (X - mean)·rstd and g = dY·gamma:
+ *   dX = rstd (g - mean_D(g) - x̂·mean_D(g·x̂)),
+ *   dgamma = Σ_rows dY·x̂, dbeta = Σ_rows dY (fp32 sums, rounded once).
+ * dgamma and dbeta may each be NULL (not wanted) and are overwritten.
+ * rows = 0 writes zeros to them.  Other arguments and errors as above.
+ */
+int cat_layernorm_backward(cat_plan_t plan, const void *X, const void *gamma,
+                           const float *mean, const float *rstd, const void *dY,
+                           void *dX, void *dgamma, void *dbeta, int rows);
+
+/* Most tensors of one clipping plan. */
+#define CAT_CLIP_MAX_TENSORS (1 << 20)
+
+/*
+ * cat_plan_create_clip — the global norm of a list of gradients, and clipping
+ * by it.  count >= 0 tensors, tensor i of sizes[i] >= 0 elements (dense) and
+ * type dtypes[i] (host arrays, copied).  Errors: CAT_ERR_INVALID_ARG,
+ * CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_clip(cat_plan_t *out, int count, const long long *sizes,
+                         const int *dtypes, void *stream);
+
+/*
+ * cat_grad_norm — *norm (device, fp32) = sqrt(Σ_i Σ_k grads[i][k]²).  grads:
+ * host array of the plan's count device pointers (read during the call), each
+ * aligned to its element type; tensors of size 0 may be NULL.  Sums keep
+ * values from 1e-30 to 1e30 apart from fp32's limits.
+ */
+int cat_grad_norm(cat_plan_t plan, const void *const *grads, float *norm);
+
+/*
+ * cat_grad_clip — *norm as above, then outs[i] = c·grads[i] with
+ * c = max_norm / norm where norm > max_norm, else 1.  outs[i] may be grads[i]
+ * (in place); apart from that no output may overlap a gradient, another
+ * output or norm (CAT_ERR_ALIAS: the same tensor twice in place, too).
+ * max_norm >= 0, infinity allowed.  If a gradient holds an infinity or NaN,
+ * *norm is not finite and c = 1: the caller sees it and the gradients keep
+ * their values.
+ */
+int cat_grad_clip(cat_plan_t plan, const void *const *grads, void *const *outs,
+                  float max_norm, float *norm);
+
+/*
  * cat_plan_sync — wait for the plan's stream, then read the device status
  * word the kernels set when an internal check fails (a bad index that was
  * skipped instead of accessed).  Returns CAT_OK, CAT_ERR_DEVICE_STATUS
