@@ -513,6 +513,7 @@ cudaError_t setup_attn() {
 }
 
 cudaError_t launch_attn_forward(const cat_plan_s* p, const AttnArgs& a) {
+  if (a.tc) return launch_attn_tc_forward(a, p->stream);
   return p->dtype == CAT_BF16 ? fwd_t<__nv_bfloat16>(a, p->stream) : fwd_t<float>(a, p->stream);
 }
 

@@ -30,6 +30,7 @@ struct AttnArgs {
   int T, S, Hq, Hkv, dh, causal;
   float scale;
   int vec;                 // every row start is aligned for 4-element accesses
+  int tc;                  // bf16, every row and head starts on a 16-byte boundary
   unsigned int* status;
 };
 

@@ -1,0 +1,466 @@
+// Forward softmax attention over packed sequences on the tensor cores
+// (tcgen05), for bf16 rows that start on 16-byte boundaries, head width a
+// multiple of 8 up to 128 (padded to 64 or 128 by the copies' zero fill).
+//
+// A CTA takes 256 query rows of one head as two tiles of 128 (the MMA's M,
+// one tensor-memory lane a row) and walks their keys in blocks of 128, from
+// the diagonal (or the sequence's end) down to row 0, in one pass with a
+// running maximum and sum.  Roles:
+//   - warps 0-3 and 4-7, one warpgroup a tile, one thread a row: scores from
+//     tensor memory to registers, mask, maximum, exponentials, and the
+//     probabilities back to tensor memory as bf16 pairs;
+//   - warp 8 issues the tensor copies of Q, K and V (ring of key blocks);
+//   - warp 9 issues the MMAs: S = Q·K^T into 128 columns a tile, and
+//     O += P·V with P as the tensor-memory operand A;
+//   - warps 10 and 11 look for infinities and NaN in V blocks that the mask
+//     cuts (below).
+// While one tile's warpgroup works on its scores the tensor core runs the
+// other tile's products.  At head width 64 P has columns of its own and the
+// next block's scores are computed while P is still being made; at 128 the
+// 512 columns are full and P takes the place of its scores.
+//
+// The maximum is followed lazily: while a block raises it by less than 2^8
+// the old one stays (probabilities up to 2^8 and their fp32 sum lose nothing
+// by it), so O in tensor memory is hardly ever rescaled.
+//
+// P is rounded to bf16 (half a step 2^-8 of each probability) as the
+// MMA's operand; its row sum, the maximum, O and the scores are fp32.
+//
+// A masked pair has p = 0, but 0·inf and 0·NaN would reach the row through
+// the MMA.  So in the one or two blocks of V that the mask cuts, values that
+// are not finite are set to zero in shared memory, and, if a row of the
+// sequence itself held one, added to the rows that see it at the end.
+#include <cuda_bf16.h>
+
+#include "../../include/cat.h"
+#include "attn.cuh"
+#include "cat_internal.h"
+#include "tc.cuh"
+
+namespace cat {
+
+namespace {
+
+constexpr int kTile = 128;                 // rows of a query tile, keys of a block
+constexpr int kFwdThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;               // log2 of the growth that is let pass
+
+template <int DP>
+struct FwdCfg {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kTileBytes = kTile * DP * 2;
+  static constexpr int kStages = DP == 64 ? 8 : 4;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 256;
+  static constexpr bool kOwnP = DP == 64;  // P beside the scores, not in their place
+  // Tensor-memory columns.
+  static constexpr int s(int t) { return kTile * t; }
+  static constexpr int p(int t) { return kOwnP ? 256 + 64 * t : kTile * t; }
+  static constexpr int o(int t) { return kOwnP ? 384 + 64 * t : 256 + kTile * t; }
+};
+
+// a·b + c on two fp32 values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Whether either bf16 half of w is an infinity or NaN.
+__device__ __forceinline__ bool odd2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Half a [kTile][DP] tile in shared memory (half = 0, 1; one warp): values
+// that are not finite become zero.  True if one of them lay in a row below
+// `rows`.
+template <int DP>
+__device__ __forceinline__ bool clean_tile(unsigned char* tile, int half, int rows) {
+  constexpr int kVec = kTile * DP * 2 / 16 / 2;       // 16-byte pieces of a half
+  uint4* v = reinterpret_cast<uint4*>(tile) + half * kVec;
+  bool found = false;
+#pragma unroll 8
+  for (int i = threadIdx.x & 31; i < kVec; i += 32) {
+    uint4 x = v[i];
+    if (odd2(x.x) || odd2(x.y) || odd2(x.z) || odd2(x.w)) {
+      // 8 pieces a row, kTile rows a box of 64 columns.
+      if (((half * kVec + i) / 8) % kTile < rows) found = true;
+      v[i] = make_uint4(drop_odd(x.x), drop_odd(x.y), drop_odd(x.z), drop_odd(x.w));
+    }
+  }
+  return __any_sync(0xffffffffu, found);
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+  using C = FwdCfg<DP>;
+  extern __shared__ unsigned char fa_raw[];
+  const uint32_t raw = smem_addr(fa_raw);
+  unsigned char* sm = fa_raw + (((raw + 1023u) & ~1023u) - raw);
+  unsigned char* q_sm = sm;                                       // [2][kTileBytes]
+  unsigned char* kv_sm = sm + 2 * C::kTileBytes;                  // [kStages][kTileBytes]
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(kv_sm + C::kStages * C::kTileBytes);
+  uint64_t* full = qfull + 2;                // [kStages] key block landed
+  uint64_t* empty = full + C::kStages;       // [kStages] its MMAs are done
+  uint64_t* sfull = empty + C::kStages;      // [2] scores are in tensor memory
+  uint64_t* sempty = sfull + 2;              // [2] ... and in registers
+  uint64_t* pfull = sempty + 2;              // [2] probabilities are in tensor memory
+  uint64_t* odone = pfull + 2;               // [2] P·V is done
+  uint64_t* vclean = odone + 2;              // [2] a cut V block has been looked through (one
+                                             // barrier each: both may pass before the first wait)
+  uint64_t* done = vclean + 2;               // every MMA is done
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* vodd = tslot + 1;                // a cut block's own rows held non-finite values
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (blockIdx.x == 0) attn_check_sequences(a);
+  const int h = blockIdx.x % a.Hq;
+  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
+  AttnBlock b;
+  if (!attn_find_block(a, slot, 8, &b)) return;
+  const int g = h / (a.Hq / a.Hkv);
+  // Key blocks of tile t: top[t] - 1 .. 0 (0: the tile has no rows).
+  const int nblk = (b.len + kTile - 1) / kTile;
+  int top[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int qb = b.row0 / kTile + t;
+    top[t] = qb >= nblk ? 0 : a.causal ? qb + 1 : nblk;
+  }
+  const int n = max(top[0], top[1]);           // blocks of the CTA: n - 1 .. 0
+  // Blocks from `cut` on are cut by the mask for some row.
+  const int cut = a.causal ? b.row0 / kTile : (b.len % kTile ? nblk - 1 : nblk);
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(qfull + t, 1);
+      mbar_init(sfull + t, 1);
+      mbar_init(sempty + t, 4);
+      mbar_init(pfull + t, 4);
+      mbar_init(odone + t, 1);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int c = 0; c < 2; ++c) mbar_init(vclean + c, 2);
+    mbar_init(done, 1);
+    *vodd = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  // Ring position of K and V of the j-th block: K0, K1, V0, K2, V1, ...
+  auto kpos = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+  auto vpos = [n](int j) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; };
+
+  // The roles of the third warpgroup hand registers to the two that hold a
+  // row of scores: 2·128·208 + 128·88 = 384·168, the launch's own.
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
+    if (lane == 0) {
+      auto load = [&](const CUtensorMap* m, int pos, int blk) {
+        const int st = pos % C::kStages;
+        if (pos >= C::kStages &&
+            !mbar_wait(empty + st, ((pos / C::kStages) - 1) & 1, a.status, 0x711))
+          return false;
+        mbar_expect_tx(full + st, C::kTileBytes);
+        for (int x = 0; x < C::kBoxes; ++x)
+          tma_load_3d(kv_sm + st * C::kTileBytes + x * (kTile * 128), m, 64 * x, g,
+                      b.start + blk * kTile, full + st);
+        return true;
+      };
+      for (int t = 0; t < 2; ++t)
+        if (top[t]) {
+          mbar_expect_tx(qfull + t, C::kTileBytes);
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
+                        b.start + b.row0 + t * kTile, qfull + t);
+        }
+      bool ok = load(&tmK, 0, n - 1);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) ok = load(&tmK, kpos(j + 1), n - 2 - j);
+        if (ok) ok = load(&tmV, vpos(j), n - 1 - j);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_o = idesc_bf16_f32_bmn(kTile, DP);
+      int ns[2] = {0, 0}, np[2] = {0, 0};       // S and P products issued of each tile
+      auto scores = [&](int t, int pos) {
+        const unsigned char* qs = q_sm + t * C::kTileBytes;
+        const unsigned char* ks = kv_sm + (pos % C::kStages) * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const int at = (k / 4) * (kTile * 128) + (k % 4) * 32;
+          tc_mma_bf16(tmem + C::s(t), sdesc_k128(qs + at), sdesc_k128(ks + at), id_s, k > 0);
+        }
+        tc_commit(sfull + t);
+        ++ns[t];
+      };
+      auto values = [&](int t, int pos) {
+        const unsigned char* vs = kv_sm + (pos % C::kStages) * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc_mma_bf16_ts(tmem + C::o(t), tmem + C::p(t) + 8 * k,
+                         sdesc_mn128(vs + 2048 * k, kTile * 128), id_o, np[t] > 0 || k > 0);
+        tc_commit(odone + t);
+        ++np[t];
+      };
+      bool ok = mbar_wait(full, 0, a.status, 0x712);
+      for (int t = 0; t < 2 && ok; ++t)
+        if (top[t] == n) {
+          ok = mbar_wait(qfull + t, 0, a.status, 0x713);
+          if (ok) scores(t, 0);
+        }
+      tc_commit(empty);
+      int ncut = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        const int blk = n - 1 - j, kp = kpos(j + 1), vp = vpos(j);
+        const bool more = j + 1 < n;
+        if (more) ok = mbar_wait(full + kp % C::kStages, (kp / C::kStages) & 1, a.status, 0x714);
+        bool vready = false;
+        for (int t = 0; t < 2 && ok; ++t) {
+          auto next_scores = [&]() {
+            if (!more || blk - 1 >= top[t]) return;
+            if (ns[t] == 0) {
+              ok = mbar_wait(qfull + t, 0, a.status, 0x713);
+            } else if (C::kOwnP) {
+              ok = mbar_wait(sempty + t, (ns[t] - 1) & 1, a.status, 0x715);
+              tc_fence_after();
+            }
+            if (ok) scores(t, kp);
+          };
+          if (C::kOwnP) next_scores();
+          if (ok && blk < top[t]) {
+            if (!vready) {
+              ok = mbar_wait(full + vp % C::kStages, (vp / C::kStages) & 1, a.status, 0x716);
+              if (ok && blk >= cut) ok = mbar_wait(vclean + ncut++, 0, a.status, 0x717);
+              vready = true;
+            }
+            if (ok) ok = mbar_wait(pfull + t, np[t] & 1, a.status, 0x718);
+            tc_fence_after();
+            if (ok) values(t, vp);
+          }
+          if (!C::kOwnP && ok) next_scores();
+        }
+        if (more) tc_commit(empty + kp % C::kStages);
+        tc_commit(empty + vp % C::kStages);
+      }
+      tc_commit(done);
+    }
+    __syncwarp();
+  } else {
+    for (int j = 0; j < n; ++j) {
+      const int blk = n - 1 - j, vp = vpos(j);
+      if (blk < cut) break;
+      const bool ok = mbar_wait(full + vp % C::kStages, (vp / C::kStages) & 1, a.status, 0x719);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (clean_tile<DP>(kv_sm + (vp % C::kStages) * C::kTileBytes, warp - 10,
+                         b.len - blk * kTile) && lane == 0)
+        atomicOr(vodd, 1u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vclean + j);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2, quad = warp & 3;
+    const int row = b.row0 + t * kTile + 32 * quad + lane;     // within the sequence
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const float sc = a.scale * kLog2e;
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f);
+    bool ok = true;
+    for (int blk = top[t] - 1, it = 0; blk >= 0; --blk, ++it) {
+      ok = __all_sync(0xffffffffu, mbar_wait(sfull + t, it & 1, a.status, 0x71a));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tc_ld32(tmem + lanes + C::s(t) + c, r + c);
+      tc_wait_ld();
+      if (C::kOwnP) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty + t);
+      }
+      if (blk >= cut) {
+        // The last key this row sees, within the block.
+        const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - blk * kTile;
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (c > last) r[c] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
+#pragma unroll
+      for (int c = 4; c < kTile; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])),
+                        c + 4 + i < kTile ? __uint_as_float(r[(c + 4 + i) % kTile]) : mx[i]);
+      const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const bool grow = __any_sync(0xffffffffu, top_s > m + kLazy);
+      float f = 1.f;
+      if (grow) {
+        const float nm = fmaxf(m, top_s);
+        f = ex2(m - (nm == -INFINITY ? 0.f : nm));
+        m = nm;
+        l2.x *= f;
+        l2.y *= f;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+      uint32_t p[kTile / 2];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 2) {
+        float2 x = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nb2);
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        l2 = add2(l2, x);
+        p[c / 2] = bf16x2(x.x, x.y);
+      }
+      if (it > 0) {
+        // The product of the block before has read P and written O.
+        ok = __all_sync(0xffffffffu, mbar_wait(odone + t, (it - 1) & 1, a.status, 0x71b));
+        if (!ok) break;
+        if (grow) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < DP; c += 32) {
+            uint32_t o[32];
+            tc_ld32(tmem + lanes + C::o(t) + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc_st32(tmem + lanes + C::o(t) + c, o);
+          }
+        }
+      }
+      tc_fence_after();
+      tc_st32(tmem + lanes + C::p(t), p);
+      tc_st32(tmem + lanes + C::p(t) + 32, p + 32);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull + t);
+    }
+    if (ok && top[t] > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(odone + t, (top[t] - 1) & 1, a.status, 0x71c));
+      if (ok) {
+        tc_fence_after();
+        const float l = l2.x + l2.y;
+        const float inv = 1.f / l;
+        const long long tok = (long long)b.start + row;
+        const bool live = row < b.len;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                             (tok * a.Hq + h) * (long long)a.dh;
+        const bool odd = *reinterpret_cast<volatile uint32_t*>(vodd) != 0;
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+          if (c >= a.dh) break;
+          uint32_t o[32];
+          tc_ld32(tmem + lanes + C::o(t) + c, o);
+          tc_wait_ld();
+          if (odd && live) {
+            // What was taken out of the cut blocks of V, for the rows that
+            // see it (an infinity or NaN times a positive probability).
+            for (int j = cut * kTile; j < b.len && j < n * kTile; ++j) {
+              if (a.causal && j > row) break;
+              const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
+                                       (b.start + (long long)j) * a.ldv + (long long)g * a.dh + c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c + i < a.dh) {
+                  const float x = __bfloat162float(v[i]);
+                  if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                }
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (c + i < a.dh) {
+                uint4 w;
+                w.x = bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                w.y = bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                w.z = bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                w.w = bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                *reinterpret_cast<uint4*>(dst + c + i) = w;
+              }
+          }
+        }
+        if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    // The columns are freed only after every MMA has completed (bounded).
+    mbar_wait(done, 0, a.status, 0x71d);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DP>
+cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
+  CUtensorMap q, k, v;
+  if (!encode_map_heads_sw128(&q, a.q, a.dh, a.Hq, a.T, (unsigned long long)a.ldq * 2, kTile) ||
+      !encode_map_heads_sw128(&k, a.k, a.dh, a.Hkv, a.T, (unsigned long long)a.ldk * 2, kTile) ||
+      !encode_map_heads_sw128(&v, a.v, a.dh, a.Hkv, a.T, (unsigned long long)a.ldv * 2, kTile))
+    return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)(attn_slots(a.T, a.S, 8) * a.Hq);
+  attn_tc_fwd_kernel<DP><<<grid, kFwdThreads, FwdCfg<DP>::kSmem, st>>>(q, k, v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t setup_attn_tc() {
+  cudaError_t e = allow_max_smem(attn_tc_fwd_kernel<64>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_fwd_kernel<128>);
+  return e;
+}
+
+cudaError_t launch_attn_tc_forward(const AttnArgs& a, cudaStream_t st) {
+  return a.dh <= 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+}
+
+}  // namespace cat

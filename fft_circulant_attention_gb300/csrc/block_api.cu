@@ -143,7 +143,7 @@ int cat_plan_create_attn(cat_plan_t* out, int max_tokens, int max_seqs, int Hq, 
   p->at.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)dh));
   if (!alloc_status(p) || !alloc(p, &p->at.delta, (size_t)Hq * max_tokens))
     return fail(p, CAT_ERR_ALLOC);
-  if (cat::setup_attn() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
+  if (cat::setup_attn() != cudaSuccess || cat::setup_attn_tc() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
   std::snprintf(p->desc, sizeof(p->desc),
                 "op=attn max_tokens=%d max_seqs=%d Hq=%d Hkv=%d dh=%d causal=%d scale=%g "
                 "workspace=%zu",
@@ -222,6 +222,7 @@ int cat_attn_forward(cat_plan_t p, const void* Q, const void* K, const void* V, 
   a.out = O;
   a.lse = lse;
   a.vec = rows_aligned(p, {Q, K, V, O}, {ldq, ldk, ldv}, 4 * es);
+  a.tc = es == 2 && rows_aligned(p, {Q, K, V, O}, {ldq, ldk, ldv}, 16);
   DeviceGuard dev(p->device);
   if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   return status_of(cat::launch_attn_forward(p, a));

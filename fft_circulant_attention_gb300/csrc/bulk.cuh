@@ -97,6 +97,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Tiled 3-D tensor copy (TMA) of the box at (c0, c1, c2) into shared memory.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // L2 cache policies.  evict_last marks data that is read again soon (the
 // four-step scratch), evict_first data that streams through once (V, O, X).
 __device__ __forceinline__ uint64_t policy_evict_last() {
@@ -168,6 +178,14 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
 bool encode_map_2d_sw128(CUtensorMap* map, const void* base, unsigned long long cols,
                          unsigned long long rows, unsigned long long row_bytes,
                          unsigned int box_cols, unsigned int box_rows);
+
+// Host: encode the heads of token rows, bf16 [rows][heads][width] with rows
+// row_bytes apart, as a 3-D map (width, heads, rows) with 128-byte swizzle and
+// a box of 64 columns of one head by box_rows rows (columns from `width` on
+// and rows outside are filled with zeros).
+bool encode_map_heads_sw128(CUtensorMap* map, const void* base, unsigned long long width,
+                            unsigned long long heads, unsigned long long rows,
+                            unsigned long long row_bytes, unsigned int box_rows);
 
 // Host: encode a 4-D tiled tensor map (no interleave, no swizzle).  dims and
 // box are innermost first; strides are the byte strides of dims 1..3.

@@ -380,6 +380,9 @@ cudaError_t launch_project(const cat_plan_s* p, const void* X, const void* WV, c
 cudaError_t setup_attn();
 cudaError_t launch_attn_forward(const cat_plan_s* p, const AttnArgs& a);
 cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a);
+// Its tensor-core kernels (attn_tc.cu), where AttnArgs::tc.
+cudaError_t setup_attn_tc();
+cudaError_t launch_attn_tc_forward(const AttnArgs& a, cudaStream_t st);
 
 // Layer norm (layernorm.cu).  layernorm_parts: partial rows of the weight
 // gradients, at most one a CTA.
