@@ -10,10 +10,10 @@
 //     tensor memory to registers, mask, maximum, exponentials, and the
 //     probabilities back to tensor memory as bf16 pairs;
 //   - warp 8 issues the tensor copies of Q, K and V (ring of key blocks);
-//   - warp 9 issues the MMAs: S = Q·K^T into 128 columns a tile, and
-//     O += P·V with P as the tensor-memory operand A;
-//   - warps 10 and 11 look for infinities and NaN in V blocks that the mask
-//     cuts (below).
+//   - warps 9 and 10, one a tile, issue the MMAs: S = Q·K^T into 128 columns,
+//     and O += P·V with P as the tensor-memory operand A;
+//   - warp 11 looks for infinities and NaN in V blocks that the mask cuts
+//     (below).
 // While one tile's warpgroup works on its scores the tensor core runs the
 // other tile's products.  At head width 64 P has columns of its own and the
 // next block's scores are computed while P is still being made; at 128 the
@@ -44,6 +44,7 @@ namespace {
 constexpr int kTile = 128;                 // rows of a query tile, keys of a block
 constexpr int kFwdThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kNumBars = 64;               // room for every barrier
 constexpr float kLazy = 8.f;               // log2 of the growth that is let pass
 
 template <int DP>
@@ -51,7 +52,8 @@ struct FwdCfg {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kTile * DP * 2;
   static constexpr int kStages = DP == 64 ? 8 : 4;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + 256;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes +
+                                   kNumBars * 8 + 16;
   static constexpr bool kOwnP = DP == 64;  // P beside the scores, not in their place
   // Tensor-memory columns.
   static constexpr int s(int t) { return kTile * t; }
@@ -95,20 +97,18 @@ __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
   return w;
 }
 
-// Half a [kTile][DP] tile in shared memory (half = 0, 1; one warp): values
-// that are not finite become zero.  True if one of them lay in a row below
-// `rows`.
+// A [kTile][DP] tile in shared memory, by one warp: values that are not
+// finite become zero.  True if one of them lay in a row below `rows`.
 template <int DP>
-__device__ __forceinline__ bool clean_tile(unsigned char* tile, int half, int rows) {
-  constexpr int kVec = kTile * DP * 2 / 16 / 2;       // 16-byte pieces of a half
-  uint4* v = reinterpret_cast<uint4*>(tile) + half * kVec;
+__device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
+  uint4* v = reinterpret_cast<uint4*>(tile);
   bool found = false;
 #pragma unroll 8
-  for (int i = threadIdx.x & 31; i < kVec; i += 32) {
+  for (int i = threadIdx.x & 31; i < kTile * DP * 2 / 16; i += 32) {
     uint4 x = v[i];
     if (odd2(x.x) || odd2(x.y) || odd2(x.z) || odd2(x.w)) {
       // 8 pieces a row, kTile rows a box of 64 columns.
-      if (((half * kVec + i) / 8) % kTile < rows) found = true;
+      if ((i / 8) % kTile < rows) found = true;
       v[i] = make_uint4(drop_odd(x.x), drop_odd(x.y), drop_odd(x.z), drop_odd(x.w));
     }
   }
@@ -125,18 +125,23 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   unsigned char* sm = fa_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* q_sm = sm;                                       // [2][kTileBytes]
   unsigned char* kv_sm = sm + 2 * C::kTileBytes;                  // [kStages][kTileBytes]
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(kv_sm + C::kStages * C::kTileBytes);
-  uint64_t* full = qfull + 2;                // [kStages] key block landed
-  uint64_t* empty = full + C::kStages;       // [kStages] its MMAs are done
-  uint64_t* sfull = empty + C::kStages;      // [2] scores are in tensor memory
-  uint64_t* sempty = sfull + 2;              // [2] ... and in registers
-  uint64_t* pfull = sempty + 2;              // [2] probabilities are in tensor memory
-  uint64_t* odone = pfull + 2;               // [2] P·V is done
-  uint64_t* vclean = odone + 2;              // [2] a cut V block has been looked through (one
-                                             // barrier each: both may pass before the first wait)
-  uint64_t* done = vclean + 2;               // every MMA is done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(kv_sm + C::kStages * C::kTileBytes);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   uint32_t* vodd = tslot + 1;                // a cut block's own rows held non-finite values
+  // Barriers by address.
+  const uint32_t bar0 = smem_addr(bars);
+  auto qfull = [&](int t) { return bar0 + 8 * t; };
+  auto sfull = [&](int t) { return bar0 + 16 + 8 * t; };    // scores are in tensor memory
+  auto sempty = [&](int t) { return bar0 + 32 + 8 * t; };   // ... and in registers
+  auto pfull = [&](int t) { return bar0 + 48 + 8 * t; };    // probabilities in tensor memory
+  auto odone = [&](int t) { return bar0 + 64 + 8 * t; };    // P·V is done
+  auto done = [&](int t) { return bar0 + 80 + 8 * t; };     // every MMA is done
+  // A cut V block has been looked through (one barrier each: both may have
+  // passed before the first is waited for).
+  auto vclean = [&](int c) { return bar0 + 96 + 8 * c; };
+  auto full = [&](int pos) { return bar0 + 112 + 8 * (pos % C::kStages); };
+  auto empty = [&](int pos) { return bar0 + 112 + 8 * (C::kStages + pos % C::kStages); };
+  auto round = [](int pos) { return (uint32_t)(pos / C::kStages) & 1u; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0) attn_check_sequences(a);
@@ -159,18 +164,18 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(qfull + t, 1);
-      mbar_init(sfull + t, 1);
-      mbar_init(sempty + t, 4);
-      mbar_init(pfull + t, 4);
-      mbar_init(odone + t, 1);
+      mbar_init(bars + t, 1);                        // qfull
+      mbar_init(bars + 2 + t, 1);                    // sfull
+      mbar_init(bars + 4 + t, 4);                    // sempty
+      mbar_init(bars + 6 + t, 4);                    // pfull
+      mbar_init(bars + 8 + t, 1);                    // odone
+      mbar_init(bars + 10 + t, 1);                   // done
+      mbar_init(bars + 12 + t, 1);                   // vclean
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
+      mbar_init(bars + 14 + s, 1);                   // full
+      mbar_init(bars + 14 + C::kStages + s, top[1] ? 2 : 1);   // empty: each tile's MMAs
     }
-    for (int c = 0; c < 2; ++c) mbar_init(vclean + c, 2);
-    mbar_init(done, 1);
     *vodd = 0;
     mbar_fence_init();
   }
@@ -185,117 +190,113 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   // The roles of the third warpgroup hand registers to the two that hold a
   // row of scores: 2·128·208 + 128·88 = 384·168, the launch's own.
+  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
-    if (lane == 0) {
-      auto load = [&](const CUtensorMap* m, int pos, int blk) {
-        const int st = pos % C::kStages;
-        if (pos >= C::kStages &&
-            !mbar_wait(empty + st, ((pos / C::kStages) - 1) & 1, a.status, 0x711))
-          return false;
-        mbar_expect_tx(full + st, C::kTileBytes);
-        for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_3d(kv_sm + st * C::kTileBytes + x * (kTile * 128), m, 64 * x, g,
-                      b.start + blk * kTile, full + st);
-        return true;
-      };
-      for (int t = 0; t < 2; ++t)
-        if (top[t]) {
-          mbar_expect_tx(qfull + t, C::kTileBytes);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      if (lane == 0) {
+        uint64_t* qb = bars;
+        auto load = [&](const CUtensorMap* m, int pos, int blk) {
+          if (pos >= C::kStages) mbar_poll(empty(pos), round(pos) ^ 1u, limit);
+          if (limit == 0) return;
+          const int st = pos % C::kStages;
+          uint64_t* bar = bars + 14 + st;
+          mbar_expect_tx(bar, C::kTileBytes);
+#pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
-                        b.start + b.row0 + t * kTile, qfull + t);
+            tma_load_3d(kv_sm + st * C::kTileBytes + x * (kTile * 128), m, 64 * x, g,
+                        b.start + blk * kTile, bar);
+        };
+        for (int t = 0; t < 2; ++t)
+          if (top[t]) {
+            mbar_expect_tx(qb + t, C::kTileBytes);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
+                          b.start + b.row0 + t * kTile, qb + t);
+          }
+        load(&tmK, 0, n - 1);
+        for (int j = 0; j < n; ++j) {
+          if (j + 1 < n) load(&tmK, kpos(j + 1), n - 2 - j);
+          load(&tmV, vpos(j), n - 1 - j);
         }
-      bool ok = load(&tmK, 0, n - 1);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) ok = load(&tmK, kpos(j + 1), n - 2 - j);
-        if (ok) ok = load(&tmV, vpos(j), n - 1 - j);
       }
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0) {
+      __syncwarp();
+    } else if (warp < 11) {
+      // MMAs of one tile.  The whole warp follows the waits (so that the loop
+      // stays uniform), one lane of it issues.
+      const int t = warp - 9;
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t id_o = idesc_bf16_f32_bmn(kTile, DP);
-      int ns[2] = {0, 0}, np[2] = {0, 0};       // S and P products issued of each tile
-      auto scores = [&](int t, int pos) {
-        const unsigned char* qs = q_sm + t * C::kTileBytes;
-        const unsigned char* ks = kv_sm + (pos % C::kStages) * C::kTileBytes;
+      const uint64_t qd = sdesc_k128(q_sm + t * C::kTileBytes), kd = sdesc_k128(kv_sm);
+      const uint64_t vd = sdesc_mn128(kv_sm, kTile * 128);
+      const uint32_t ts = tmem + C::s(t), tp = tmem + C::p(t), to = tmem + C::o(t);
+      auto scores = [&](int pos) {
+        const uint64_t k0 = kd + (uint64_t)((pos % C::kStages) * (C::kTileBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const int at = (k / 4) * (kTile * 128) + (k % 4) * 32;
-          tc_mma_bf16(tmem + C::s(t), sdesc_k128(qs + at), sdesc_k128(ks + at), id_s, k > 0);
-        }
-        tc_commit(sfull + t);
-        ++ns[t];
-      };
-      auto values = [&](int t, int pos) {
-        const unsigned char* vs = kv_sm + (pos % C::kStages) * C::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc_mma_bf16_ts(tmem + C::o(t), tmem + C::p(t) + 8 * k,
-                         sdesc_mn128(vs + 2048 * k, kTile * 128), id_o, np[t] > 0 || k > 0);
-        tc_commit(odone + t);
-        ++np[t];
-      };
-      bool ok = mbar_wait(full, 0, a.status, 0x712);
-      for (int t = 0; t < 2 && ok; ++t)
-        if (top[t] == n) {
-          ok = mbar_wait(qfull + t, 0, a.status, 0x713);
-          if (ok) scores(t, 0);
-        }
-      tc_commit(empty);
-      int ncut = 0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int blk = n - 1 - j, kp = kpos(j + 1), vp = vpos(j);
-        const bool more = j + 1 < n;
-        if (more) ok = mbar_wait(full + kp % C::kStages, (kp / C::kStages) & 1, a.status, 0x714);
-        bool vready = false;
-        for (int t = 0; t < 2 && ok; ++t) {
-          auto next_scores = [&]() {
-            if (!more || blk - 1 >= top[t]) return;
-            if (ns[t] == 0) {
-              ok = mbar_wait(qfull + t, 0, a.status, 0x713);
-            } else if (C::kOwnP) {
-              ok = mbar_wait(sempty + t, (ns[t] - 1) & 1, a.status, 0x715);
-              tc_fence_after();
-            }
-            if (ok) scores(t, kp);
-          };
-          if (C::kOwnP) next_scores();
-          if (ok && blk < top[t]) {
-            if (!vready) {
-              ok = mbar_wait(full + vp % C::kStages, (vp / C::kStages) & 1, a.status, 0x716);
-              if (ok && blk >= cut) ok = mbar_wait(vclean + ncut++, 0, a.status, 0x717);
-              vready = true;
-            }
-            if (ok) ok = mbar_wait(pfull + t, np[t] & 1, a.status, 0x718);
-            tc_fence_after();
-            if (ok) values(t, vp);
+          for (int k = 0; k < DP / 16; ++k) {
+            const int at = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+            tc_mma_bf16(ts, qd + at, k0 + at, id_s, k > 0);
           }
-          if (!C::kOwnP && ok) next_scores();
+          tc_commit(sfull(t));
+          tc_commit(empty(pos));
         }
-        if (more) tc_commit(empty + kp % C::kStages);
-        tc_commit(empty + vp % C::kStages);
+        __syncwarp();
+      };
+      if (top[t]) {
+        const int j0 = n - top[t];             // blocks ahead that only the other tile sees
+        for (int j = 0; j < j0; ++j)
+          if (elect_one()) {
+            mbar_arrive(empty(kpos(j)));
+            mbar_arrive(empty(vpos(j)));
+          }
+        mbar_poll(qfull(t), 0, limit);
+        mbar_poll(full(kpos(j0)), round(kpos(j0)), limit);
+        scores(kpos(j0));
+        uint32_t par = 0;                      // parity of the tile's block
+        for (int j = j0; j < n; ++j, par ^= 1u) {
+          const int kp = kpos(j + 1), vp = vpos(j);
+          if (C::kOwnP && j + 1 < n) {
+            mbar_poll(full(kp), round(kp), limit);
+            mbar_poll(sempty(t), par, limit);
+            tc_fence_after();
+            scores(kp);
+          }
+          if (n - 1 - j >= cut) mbar_poll(vclean(j), 0, limit);
+          mbar_poll(full(vp), round(vp), limit);
+          mbar_poll(pfull(t), par, limit);
+          tc_fence_after();
+          const uint64_t v0 = vd + (uint64_t)((vp % C::kStages) * (C::kTileBytes >> 4));
+          if (elect_one()) {
+            tc_mma_bf16_ts(to, tp, v0, id_o, j > j0);
+#pragma unroll
+            for (int k = 1; k < kTile / 16; ++k)
+              tc_mma_bf16_ts(to, tp + 8 * k, v0 + ((2048 * k) >> 4), id_o, 1);
+            tc_commit(odone(t));
+            tc_commit(empty(vp));
+          }
+          __syncwarp();
+          if (!C::kOwnP && j + 1 < n) {
+            // P took the place of the scores: the next ones follow its product.
+            mbar_poll(full(kp), round(kp), limit);
+            scores(kp);
+          }
+        }
       }
-      tc_commit(done);
-    }
-    __syncwarp();
-  } else {
-    for (int j = 0; j < n; ++j) {
-      const int blk = n - 1 - j, vp = vpos(j);
-      if (blk < cut) break;
-      const bool ok = mbar_wait(full + vp % C::kStages, (vp / C::kStages) & 1, a.status, 0x719);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (clean_tile<DP>(kv_sm + (vp % C::kStages) * C::kTileBytes, warp - 10,
-                         b.len - blk * kTile) && lane == 0)
-        atomicOr(vodd, 1u);
-      fence_proxy_async_smem();
+      if (elect_one()) tc_commit(done(t));
       __syncwarp();
-      if (lane == 0) mbar_arrive(vclean + j);
+    } else {
+      for (int j = 0; j < n && n - 1 - j >= cut; ++j) {
+        const int vp = vpos(j);
+        mbar_poll(full(vp), round(vp), limit);
+        if (clean_tile<DP>(kv_sm + (vp % C::kStages) * C::kTileBytes,
+                           b.len - (n - 1 - j) * kTile) && lane == 0)
+          *vodd = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vclean(j));
+      }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2, quad = warp & 3;
@@ -304,10 +305,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const float sc = a.scale * kLog2e;
     float m = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f);
-    bool ok = true;
     for (int blk = top[t] - 1, it = 0; blk >= 0; --blk, ++it) {
-      ok = __all_sync(0xffffffffu, mbar_wait(sfull + t, it & 1, a.status, 0x71a));
-      if (!ok) break;
+      mbar_poll(sfull(t), it & 1, limit);
       tc_fence_after();
       uint32_t r[kTile];
 #pragma unroll
@@ -316,7 +315,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (C::kOwnP) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sempty + t);
+        if (lane == 0) mbar_arrive(sempty(t));
       }
       if (blk >= cut) {
         // The last key this row sees, within the block.
@@ -357,8 +356,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       if (it > 0) {
         // The product of the block before has read P and written O.
-        ok = __all_sync(0xffffffffu, mbar_wait(odone + t, (it - 1) & 1, a.status, 0x71b));
-        if (!ok) break;
+        mbar_poll(odone(t), (it - 1) & 1, limit);
         if (grow) {
           tc_fence_after();
 #pragma unroll
@@ -378,11 +376,12 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pfull + t);
+      if (lane == 0) mbar_arrive(pfull(t));
     }
-    if (ok && top[t] > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(odone + t, (top[t] - 1) & 1, a.status, 0x71c));
-      if (ok) {
+    if (top[t] > 0) {
+      mbar_poll(odone(t), (top[t] - 1) & 1, limit);
+      // (rows of a CTA that lost a wait are not written)
+      if (__all_sync(0xffffffffu, limit != 0)) {
         tc_fence_after();
         const float l = l2.x + l2.y;
         const float inv = 1.f / l;
@@ -429,11 +428,14 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   }
+  if (limit == 0) report(a.status, 0x711);
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
     // The columns are freed only after every MMA has completed (bounded).
-    mbar_wait(done, 0, a.status, 0x71d);
+    mbar_poll(done(0), 0, limit);
+    mbar_poll(done(1), 0, limit);
+    if (limit == 0) report(a.status, 0x712);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

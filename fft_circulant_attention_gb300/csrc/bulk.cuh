@@ -64,6 +64,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return false;
 }
 
+// A wait without a branch on its outcome, for roles whose loops must stay
+// short: polls at most `limit` times; a wait that is lost sets limit to 0, so
+// that the role's later waits pass at once and its loop ends (the caller
+// reports a limit of 0 there).  bar: shared-memory address.
+__device__ __forceinline__ void mbar_poll(uint32_t bar, uint32_t parity, uint32_t& limit) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra END;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 p, n, %0;\n\t"
+      "@p bra POLL;\n\t"
+      "mov.u32 %0, 0;\n"
+      "END:\n\t}"
+      : "+r"(limit)
+      : "r"(bar), "r"(parity)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Bulk copy of `bytes` bytes from global `src` to shared `dst`, completing
 // on `bar`.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,
