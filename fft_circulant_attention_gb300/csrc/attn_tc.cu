@@ -51,8 +51,8 @@ template <int DP>
 struct FwdCfg {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = DP == 64 ? 8 : 4;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes +
+  static constexpr int kStages = DP == 64 ? 5 : 2;   // K and V of a key block each
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kStages) * kTileBytes +
                                    kNumBars * 8 + 16;
   static constexpr bool kOwnP = DP == 64;  // P beside the scores, not in their place
   // Tensor-memory columns.
@@ -85,6 +85,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Named barrier `id` of the two tiles' warpgroups: one arrives, the other waits.
+__device__ __forceinline__ void pass_turn(int id) {
+  asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void take_turn(int id) {
+  asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory");
 }
 
 // Whether either bf16 half of w is an infinity or NaN.
@@ -124,8 +132,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const uint32_t raw = smem_addr(fa_raw);
   unsigned char* sm = fa_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* q_sm = sm;                                       // [2][kTileBytes]
-  unsigned char* kv_sm = sm + 2 * C::kTileBytes;                  // [kStages][kTileBytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(kv_sm + C::kStages * C::kTileBytes);
+  unsigned char* kv_sm = sm + 2 * C::kTileBytes;                  // [kStages][K, V][kTileBytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(kv_sm + 2 * C::kStages * C::kTileBytes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   uint32_t* vodd = tslot + 1;                // a cut block's own rows held non-finite values
   // Barriers by address.
@@ -139,9 +147,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // A cut V block has been looked through (one barrier each: both may have
   // passed before the first is waited for).
   auto vclean = [&](int c) { return bar0 + 96 + 8 * c; };
-  auto full = [&](int pos) { return bar0 + 112 + 8 * (pos % C::kStages); };
-  auto empty = [&](int pos) { return bar0 + 112 + 8 * (C::kStages + pos % C::kStages); };
-  auto round = [](int pos) { return (uint32_t)(pos / C::kStages) & 1u; };
+  auto full = [&](int st) { return bar0 + 112 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 112 + 8 * (C::kStages + st); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0) attn_check_sequences(a);
@@ -184,40 +191,39 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  // Ring position of K and V of the j-th block: K0, K1, V0, K2, V1, ...
-  auto kpos = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
-  auto vpos = [n](int j) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; };
-
-  // The roles of the third warpgroup hand registers to the two that hold a
-  // row of scores: 2·128·208 + 128·88 = 384·168, the launch's own.
+  // The roles of the last warpgroup hand registers to the two that hold a row
+  // of scores: 2·128·208 + 128·88 = 384·168, the launch's own.
   uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       if (lane == 0) {
-        uint64_t* qb = bars;
-        auto load = [&](const CUtensorMap* m, int pos, int blk) {
-          if (pos >= C::kStages) mbar_poll(empty(pos), round(pos) ^ 1u, limit);
-          if (limit == 0) return;
-          const int st = pos % C::kStages;
-          uint64_t* bar = bars + 14 + st;
-          mbar_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(kv_sm + st * C::kTileBytes + x * (kTile * 128), m, 64 * x, g,
-                        b.start + blk * kTile, bar);
-        };
         for (int t = 0; t < 2; ++t)
           if (top[t]) {
-            mbar_expect_tx(qb + t, C::kTileBytes);
+            mbar_expect_tx(bars + t, C::kTileBytes);
             for (int x = 0; x < C::kBoxes; ++x)
               tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
-                          b.start + b.row0 + t * kTile, qb + t);
+                          b.start + b.row0 + t * kTile, bars + t);
           }
-        load(&tmK, 0, n - 1);
+        int st = 0;
+        uint32_t round = 0;
         for (int j = 0; j < n; ++j) {
-          if (j + 1 < n) load(&tmK, kpos(j + 1), n - 2 - j);
-          load(&tmV, vpos(j), n - 1 - j);
+          if (j >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+          if (limit == 0) break;
+          uint64_t* bar = bars + 14 + st;
+          unsigned char* k_sm = kv_sm + 2 * st * C::kTileBytes;
+          const int row = b.start + (n - 1 - j) * kTile;
+          mbar_expect_tx(bar, 2 * C::kTileBytes);
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
         }
       }
       __syncwarp();
@@ -228,10 +234,11 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t id_o = idesc_bf16_f32_bmn(kTile, DP);
       const uint64_t qd = sdesc_k128(q_sm + t * C::kTileBytes), kd = sdesc_k128(kv_sm);
-      const uint64_t vd = sdesc_mn128(kv_sm, kTile * 128);
+      const uint64_t vd = sdesc_mn128(kv_sm + C::kTileBytes, kTile * 128);
       const uint32_t ts = tmem + C::s(t), tp = tmem + C::p(t), to = tmem + C::o(t);
-      auto scores = [&](int pos) {
-        const uint64_t k0 = kd + (uint64_t)((pos % C::kStages) * (C::kTileBytes >> 4));
+      constexpr uint64_t kStep = 2 * C::kTileBytes >> 4;       // from stage to stage
+      auto scores = [&](int st) {
+        const uint64_t k0 = kd + st * kStep;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
@@ -239,58 +246,61 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tc_mma_bf16(ts, qd + at, k0 + at, id_s, k > 0);
           }
           tc_commit(sfull(t));
-          tc_commit(empty(pos));
         }
         __syncwarp();
       };
       if (top[t]) {
-        const int j0 = n - top[t];             // blocks ahead that only the other tile sees
-        for (int j = 0; j < j0; ++j)
-          if (elect_one()) {
-            mbar_arrive(empty(kpos(j)));
-            mbar_arrive(empty(vpos(j)));
-          }
+        int st = 0;
+        uint32_t round = 0;                    // parity of the ring's stage st
+        if (top[t] < n) {
+          // The first block is the other tile's alone.
+          if (elect_one()) mbar_arrive(empty(0));
+          st = 1;
+        }
         mbar_poll(qfull(t), 0, limit);
-        mbar_poll(full(kpos(j0)), round(kpos(j0)), limit);
-        scores(kpos(j0));
+        mbar_poll(full(st), 0, limit);
+        scores(st);
         uint32_t par = 0;                      // parity of the tile's block
-        for (int j = j0; j < n; ++j, par ^= 1u) {
-          const int kp = kpos(j + 1), vp = vpos(j);
-          if (C::kOwnP && j + 1 < n) {
-            mbar_poll(full(kp), round(kp), limit);
+        for (int blk = top[t] - 1; blk >= 0; --blk, par ^= 1u) {
+          const uint64_t v0 = vd + st * kStep;
+          const uint32_t done_v = empty(st);
+          if (blk >= cut) mbar_poll(vclean(n - 1 - blk), 0, limit);
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
+          if (C::kOwnP && blk > 0) {
+            mbar_poll(full(st), round, limit);
             mbar_poll(sempty(t), par, limit);
             tc_fence_after();
-            scores(kp);
+            scores(st);
           }
-          if (n - 1 - j >= cut) mbar_poll(vclean(j), 0, limit);
-          mbar_poll(full(vp), round(vp), limit);
           mbar_poll(pfull(t), par, limit);
           tc_fence_after();
-          const uint64_t v0 = vd + (uint64_t)((vp % C::kStages) * (C::kTileBytes >> 4));
           if (elect_one()) {
-            tc_mma_bf16_ts(to, tp, v0, id_o, j > j0);
+            tc_mma_bf16_ts(to, tp, v0, id_o, blk < top[t] - 1);
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k)
               tc_mma_bf16_ts(to, tp + 8 * k, v0 + ((2048 * k) >> 4), id_o, 1);
             tc_commit(odone(t));
-            tc_commit(empty(vp));
+            tc_commit(done_v);
           }
           __syncwarp();
-          if (!C::kOwnP && j + 1 < n) {
+          if (!C::kOwnP && blk > 0) {
             // P took the place of the scores: the next ones follow its product.
-            mbar_poll(full(kp), round(kp), limit);
-            scores(kp);
+            mbar_poll(full(st), round, limit);
+            scores(st);
           }
         }
       }
       if (elect_one()) tc_commit(done(t));
       __syncwarp();
     } else {
+      // (at most two cut blocks: the first two stages)
       for (int j = 0; j < n && n - 1 - j >= cut; ++j) {
-        const int vp = vpos(j);
-        mbar_poll(full(vp), round(vp), limit);
-        if (clean_tile<DP>(kv_sm + (vp % C::kStages) * C::kTileBytes,
-                           b.len - (n - 1 - j) * kTile) && lane == 0)
+        mbar_poll(full(j), 0, limit);
+        if (clean_tile<DP>(kv_sm + (2 * j + 1) * C::kTileBytes, b.len - (n - 1 - j) * kTile) &&
+            lane == 0)
           *vodd = 1;
         fence_proxy_async_smem();
         __syncwarp();
@@ -302,15 +312,17 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int t = warp >> 2, quad = warp & 3;
     const int row = b.row0 + t * kTile + 32 * quad + lane;     // within the sequence
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t ts = tmem + lanes + C::s(t), tp = tmem + lanes + C::p(t);
+    const uint32_t to = tmem + lanes + C::o(t);
     const float sc = a.scale * kLog2e;
     float m = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
+    float2 l2 = make_float2(0.f, 0.f), k2 = l2;      // row sum, in four parts
     for (int blk = top[t] - 1, it = 0; blk >= 0; --blk, ++it) {
       mbar_poll(sfull(t), it & 1, limit);
       tc_fence_after();
       uint32_t r[kTile];
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tc_ld32(tmem + lanes + C::s(t) + c, r + c);
+      for (int c = 0; c < kTile; c += 32) tc_ld32(ts + c, r + c);
       tc_wait_ld();
       if (C::kOwnP) {
         tc_fence_before();
@@ -326,13 +338,12 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       float mx[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(r[i]);
+      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(r[i]), __uint_as_float(r[4 + i]));
 #pragma unroll
-      for (int c = 4; c < kTile; c += 8)
+      for (int c = 8; c < kTile; c += 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])),
-                        c + 4 + i < kTile ? __uint_as_float(r[(c + 4 + i) % kTile]) : mx[i]);
+          mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])), __uint_as_float(r[c + 4 + i]));
       const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
       const bool grow = __any_sync(0xffffffffu, top_s > m + kLazy);
       float f = 1.f;
@@ -342,48 +353,65 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         m = nm;
         l2.x *= f;
         l2.y *= f;
+        k2.x *= f;
+        k2.y *= f;
       }
       const float base = m == -INFINITY ? 0.f : m;
       const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
-      uint32_t p[kTile / 2];
+      // At head width 128 the tiles' warpgroups take turns at the
+      // exponentials, tile 1 first (it has as many blocks as tile 0 or one
+      // more): the MMAs of both tiles otherwise finish together and leave the
+      // tensor core idle while both make probabilities (16 x 16384 tokens:
+      // 1614 us, 1735 without turns; at 64, where the next scores are ready
+      // ahead, 1272 and 1130).
+      if (!C::kOwnP && (t == 0 ? top[1] > 0 : it > 0)) take_turn(1 + t);
 #pragma unroll
-      for (int c = 0; c < kTile; c += 2) {
-        float2 x = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nb2);
-        x.x = ex2(x.x);
-        x.y = ex2(x.y);
-        l2 = add2(l2, x);
-        p[c / 2] = bf16x2(x.x, x.y);
-      }
-      if (it > 0) {
-        // The product of the block before has read P and written O.
-        mbar_poll(odone(t), (it - 1) & 1, limit);
-        if (grow) {
-          tc_fence_after();
+      for (int c0 = 0; c0 < kTile; c0 += 32) {
+        uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < DP; c += 32) {
-            uint32_t o[32];
-            tc_ld32(tmem + lanes + C::o(t) + c, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc_st32(tmem + lanes + C::o(t) + c, o);
-          }
+        for (int c = 0; c < 32; c += 2) {
+          float2 x = fma2(make_float2(__uint_as_float(r[c0 + c]), __uint_as_float(r[c0 + c + 1])),
+                          sc2, nb2);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          if (c & 2)
+            l2 = add2(l2, x);
+          else
+            k2 = add2(k2, x);
+          p[c / 2] = bf16x2(x.x, x.y);
         }
+        if (c0 == 0) {
+          if (it > 0) {
+            // The product of the block before has read P and written O.
+            mbar_poll(odone(t), (it - 1) & 1, limit);
+            if (grow) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < DP; d += 16) {
+                float o[16];
+                tc_ld16(to + d, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tc_st16(to + d, reinterpret_cast<uint32_t*>(o));
+              }
+            }
+          }
+          tc_fence_after();
+        }
+        tc_st16(tp + c0 / 2, p);
       }
-      tc_fence_after();
-      tc_st32(tmem + lanes + C::p(t), p);
-      tc_st32(tmem + lanes + C::p(t) + 32, p + 32);
+      if (!C::kOwnP && (t == 0 ? it + 1 < top[1] : it < top[0])) pass_turn(2 - t);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pfull(t));
     }
     if (top[t] > 0) {
+      const float l = (l2.x + l2.y) + (k2.x + k2.y);
       mbar_poll(odone(t), (top[t] - 1) & 1, limit);
       // (rows of a CTA that lost a wait are not written)
       if (__all_sync(0xffffffffu, limit != 0)) {
         tc_fence_after();
-        const float l = l2.x + l2.y;
         const float inv = 1.f / l;
         const long long tok = (long long)b.start + row;
         const bool live = row < b.len;
@@ -391,11 +419,9 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                              (tok * a.Hq + h) * (long long)a.dh;
         const bool odd = *reinterpret_cast<volatile uint32_t*>(vodd) != 0;
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 32) {
-          if (c >= a.dh) break;
-          uint32_t o[32];
-          tc_ld32(tmem + lanes + C::o(t) + c, o);
-          tc_wait_ld();
+        for (int c = 0; c < a.dh; c += 16) {
+          float o[16];
+          tc_ld16(to + c, o);
           if (odd && live) {
             // What was taken out of the cut blocks of V, for the rows that
             // see it (an infinity or NaN times a positive probability).
@@ -404,22 +430,22 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
                                        (b.start + (long long)j) * a.ldv + (long long)g * a.dh + c;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < 16; ++i)
                 if (c + i < a.dh) {
                   const float x = __bfloat162float(v[i]);
-                  if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                  if (!isfinite(x)) o[i] += x;
                 }
             }
           }
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
+            for (int i = 0; i < 16; i += 8)
               if (c + i < a.dh) {
                 uint4 w;
-                w.x = bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                w.y = bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                w.z = bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                w.w = bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                w.x = bf16x2(o[i] * inv, o[i + 1] * inv);
+                w.y = bf16x2(o[i + 2] * inv, o[i + 3] * inv);
+                w.z = bf16x2(o[i + 4] * inv, o[i + 5] * inv);
+                w.w = bf16x2(o[i + 6] * inv, o[i + 7] * inv);
                 *reinterpret_cast<uint4*>(dst + c + i) = w;
               }
           }
