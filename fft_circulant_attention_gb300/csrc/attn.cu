@@ -518,6 +518,7 @@ cudaError_t launch_attn_forward(const cat_plan_s* p, const AttnArgs& a) {
 }
 
 cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a) {
+  if (a.tc) return launch_attn_tc_backward(a, p->stream);
   const long long rows = (long long)a.T * a.Hq;
   const unsigned grid = (unsigned)((rows + kThr / 32 - 1) / (kThr / 32));
   if (p->dtype == CAT_BF16)

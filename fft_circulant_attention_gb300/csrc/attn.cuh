@@ -25,6 +25,8 @@ struct AttnArgs {
   void* dq; void* dk; void* dv;
   float* lse;              // [Hq][T], natural logarithm
   float* delta;            // [Hq][T] Σ_c dO·O (backward workspace)
+  float* stats;            // [Hq][slots of 128 rows][2][128] lse·log2 e, then delta
+                           // (backward workspace of the tensor-core kernels)
   const int* cu;
   long long ldq, ldk, ldv, lddq, lddk, lddv;
   int T, S, Hq, Hkv, dh, causal;
@@ -35,7 +37,8 @@ struct AttnArgs {
 };
 
 struct AttnBlock {
-  int start, len;          // the sequence's first row and its length
+  int seq;                 // the sequence
+  int start, len;          // its first row and its length
   int row0;                // the block's first row within the sequence
 };
 
@@ -66,6 +69,7 @@ __device__ __forceinline__ bool attn_find_block(const AttnArgs& a, int slot, int
   const int c0 = __ldg(a.cu + lo), c1 = __ldg(a.cu + lo + 1);
   if (c0 < 0 || c1 < c0 || c1 > a.T) return false;
   const int blk = slot - ((c0 >> shift) + lo);
+  b->seq = lo;
   b->start = c0;
   b->len = c1 - c0;
   b->row0 = blk << shift;

@@ -105,6 +105,7 @@ namespace cat {
 
 void free_op(cat_plan_s* p) {
   cudaFree(p->at.delta);
+  cudaFree(p->at.stats);
   cudaFree(p->ln.part);
   cudaFree(p->cl.chunks);
   cudaFree(p->cl.part);
@@ -143,7 +144,11 @@ int cat_plan_create_attn(cat_plan_t* out, int max_tokens, int max_seqs, int Hq, 
   p->at.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)dh));
   if (!alloc_status(p) || !alloc(p, &p->at.delta, (size_t)Hq * max_tokens))
     return fail(p, CAT_ERR_ALLOC);
-  if (cat::setup_attn() != cudaSuccess || cat::setup_attn_tc() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
+  if (dtype == CAT_BF16 && dh % 8 == 0 &&
+      !alloc(p, &p->at.stats, cat::attn_tc_stats_count(max_tokens, max_seqs, Hq)))
+    return fail(p, CAT_ERR_ALLOC);
+  if (cat::setup_attn() != cudaSuccess || cat::setup_attn_tc() != cudaSuccess ||
+      cat::setup_attn_tc_bwd() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
   std::snprintf(p->desc, sizeof(p->desc),
                 "op=attn max_tokens=%d max_seqs=%d Hq=%d Hkv=%d dh=%d causal=%d scale=%g "
                 "workspace=%zu",
@@ -183,6 +188,7 @@ int attn_prepare(cat_plan_s* p, const void* Q, const void* K, const void* V, con
   a->causal = c.causal;
   a->scale = c.scale;
   a->delta = c.delta;
+  a->stats = c.stats;
   a->status = p->status;
   *run = true;
   return CAT_OK;
@@ -264,6 +270,8 @@ int cat_attn_backward(cat_plan_t p, const void* Q, const void* K, const void* V,
   a.dq = dQ; a.dk = dK; a.dv = dV;
   a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
   a.vec = rows_aligned(p, {Q, K, V, O, dO, dQ, dK, dV}, {ldq, ldk, ldv, lddq, lddk, lddv}, 4 * es);
+  a.tc = es == 2 &&
+         rows_aligned(p, {Q, K, V, O, dO, dQ, dK, dV}, {ldq, ldk, ldv, lddq, lddk, lddv}, 16);
   DeviceGuard dev(p->device);
   if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   return status_of(cat::launch_attn_backward(p, a));

@@ -116,6 +116,7 @@ struct AttnCfg {
   int max_tokens, max_seqs, Hq, Hkv, dh, causal;
   float scale;
   float* delta;            // [Hq][max_tokens]
+  float* stats;            // the tensor-core backward's (bf16, dh a multiple of 8)
 };
 struct NormCfg {
   int max_rows, max_parts;
@@ -383,6 +384,10 @@ cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a);
 // Its tensor-core kernels (attn_tc.cu), where AttnArgs::tc.
 cudaError_t setup_attn_tc();
 cudaError_t launch_attn_tc_forward(const AttnArgs& a, cudaStream_t st);
+// (attn_tc_bwd.cu; floats of AttnArgs::stats)
+size_t attn_tc_stats_count(int max_tokens, int max_seqs, int Hq);
+cudaError_t setup_attn_tc_bwd();
+cudaError_t launch_attn_tc_backward(const AttnArgs& a, cudaStream_t st);
 
 // Layer norm (layernorm.cu).  layernorm_parts: partial rows of the weight
 // gradients, at most one a CTA.
