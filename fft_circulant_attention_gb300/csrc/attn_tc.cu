@@ -358,6 +358,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const bool live = row < b.len;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                              (tok * a.Hq + h) * (long long)a.dh;
+        const bool wide = wide_rows(a.out, (long long)a.Hq * a.dh, a.dh);
         const bool odd = *reinterpret_cast<volatile uint32_t*>(vodd) != 0;
 #pragma unroll 1
         for (int c = 0; c < a.dh; c += 16) {
@@ -378,18 +379,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
             }
           }
-          if (live) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              if (c + i < a.dh) {
-                uint4 w;
-                w.x = bf16x2(o[i] * inv, o[i + 1] * inv);
-                w.y = bf16x2(o[i + 2] * inv, o[i + 3] * inv);
-                w.z = bf16x2(o[i + 4] * inv, o[i + 5] * inv);
-                w.w = bf16x2(o[i + 6] * inv, o[i + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + c + i) = w;
-              }
-          }
+          if (live) store16(dst + c, o, inv, a.dh - c, wide);
         }
         if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
       }

@@ -37,32 +37,67 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Whether either bf16 half of w is an infinity or NaN.
-__device__ __forceinline__ bool odd2(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// A bf16 half whose exponent is all ones (an infinity or NaN) sets the high
+// bit of its half: adding one to the exponent carries there.
+__device__ __forceinline__ uint32_t odd2(uint32_t w) {
+  return (w & 0x7f807f80u) + 0x00800080u;
 }
 __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
+  const uint32_t o = odd2(w);
+  return w & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
 }
 
 // A [kTile][DP] tile in shared memory, by one warp: values that are not
-// finite become zero.  True if one of them lay in a row below `rows`.
+// finite become zero.  True if one of them lay in a row below `rows`.  The
+// first pass only looks (9 operations per 8 values: about 0.3 us a tile of 64
+// columns, hidden behind the block's scores).
 template <int DP>
 __device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
+  constexpr int kVec = kTile * DP * 2 / 16;
   uint4* v = reinterpret_cast<uint4*>(tile);
+  uint32_t any = 0;
+#pragma unroll 16
+  for (int i = threadIdx.x & 31; i < kVec; i += 32) {
+    const uint4 x = v[i];
+    any |= odd2(x.x) | odd2(x.y) | odd2(x.z) | odd2(x.w);
+  }
+  if (!__any_sync(0xffffffffu, (any & 0x80008000u) != 0)) return false;
   bool found = false;
-#pragma unroll 8
-  for (int i = threadIdx.x & 31; i < kTile * DP * 2 / 16; i += 32) {
-    uint4 x = v[i];
-    if (odd2(x.x) || odd2(x.y) || odd2(x.z) || odd2(x.w)) {
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < kVec; i += 32) {
+    const uint4 x = v[i];
+    if (((odd2(x.x) | odd2(x.y) | odd2(x.z) | odd2(x.w)) & 0x80008000u) != 0) {
       // 8 pieces a row, kTile rows a box of 64 columns.
       if ((i / 8) % kTile < rows) found = true;
       v[i] = make_uint4(drop_odd(x.x), drop_odd(x.y), drop_odd(x.z), drop_odd(x.w));
     }
   }
   return __any_sync(0xffffffffu, found);
+}
+
+// f · 16 fp32 values as bf16 to a row, its first `cols` (a multiple of 8).
+// wide: 32-byte aligned rows, one store of a whole sector (the lanes of a warp
+// write 32 different rows, so the number of stores is what counts).
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, float f, int cols,
+                                        bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                     __cvta_generic_to_global(dst)),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                 "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (cols > 8) *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// Whether store16 may take whole sectors: head rows of 16·k elements that
+// start on 32-byte boundaries.
+__device__ __forceinline__ bool wide_rows(const void* base, long long ld, int dh) {
+  return ((uintptr_t)base & 31) == 0 && ld % 16 == 0 && dh % 16 == 0;
 }
 
 }  // namespace cat

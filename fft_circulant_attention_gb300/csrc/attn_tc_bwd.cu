@@ -106,25 +106,14 @@ __device__ __forceinline__ void store_half(uint32_t taddr, const float* v) {
   tc_wait_st();
 }
 
-// f · DP accumulator columns c0 .. c1 - 1 of this thread's lane to a bf16 row.
+// f · accumulator columns c0 .. c1 - 1 of this thread's lane to a bf16 row.
 __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, int c0, int c1,
-                                          float f, bool live) {
+                                          float f, bool live, bool wide) {
 #pragma unroll 1
   for (int c = c0; c < c1; c += 16) {
     float o[16];
     tc_ld16(taddr + c, o);
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < 16; i += 8)
-        if (c + i < c1) {
-          uint4 w;
-          w.x = bf16x2(o[i] * f, o[i + 1] * f);
-          w.y = bf16x2(o[i + 2] * f, o[i + 3] * f);
-          w.z = bf16x2(o[i + 4] * f, o[i + 5] * f);
-          w.w = bf16x2(o[i + 6] * f, o[i + 7] * f);
-          *reinterpret_cast<uint4*>(dst + c + i) = w;
-        }
-    }
+    if (live) store16(dst + c, o, f, c1 - c, wide);
   }
 }
 
@@ -433,7 +422,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (half == 0) {
         __nv_bfloat16* dv =
             static_cast<__nv_bfloat16*>(a.dv) + tok * a.lddv + (long long)g * a.dh;
-        store_row(tmem + lanes + C::kDv, dv, 0, a.dh, 1.f, live);
+        store_row(tmem + lanes + C::kDv, dv, 0, a.dh, 1.f, live,
+                  wide_rows(a.dv, a.lddv, a.dh));
         if (*reinterpret_cast<volatile uint32_t*>(godd) != 0 && live) {
           // What was taken out of the cut blocks of dO, for the keys that its
           // rows see (an infinity or NaN times a positive probability).
@@ -452,7 +442,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       } else {
         __nv_bfloat16* dk =
             static_cast<__nv_bfloat16*>(a.dk) + tok * a.lddk + (long long)g * a.dh;
-        store_row(tmem + lanes + C::kDk, dk, 0, a.dh, a.scale, live);
+        store_row(tmem + lanes + C::kDk, dk, 0, a.dh, a.scale, live,
+                  wide_rows(a.dk, a.lddk, a.dh));
       }
     }
   }
@@ -655,7 +646,8 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) +
                            ((long long)b.start + row) * a.lddq + (long long)h * a.dh;
       const int c0 = half * (DP / 2);
-      store_row(tmem + lanes + C::kDq, dst, c0, min(a.dh, c0 + DP / 2), a.scale, row < b.len);
+      store_row(tmem + lanes + C::kDq, dst, c0, min(a.dh, c0 + DP / 2), a.scale, row < b.len,
+                wide_rows(a.dq, a.lddq, a.dh));
     }
   }
   if (limit == 0) report(a.status, 0x731);
