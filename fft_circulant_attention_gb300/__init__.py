@@ -27,6 +27,7 @@ for convenience.  The operators around a CAT layer in a training step are
 ``cat_layernorm_backward`` (``LayerNormPlan``), ``cat_plan_create_clip``,
 ``cat_grad_norm`` and ``cat_grad_clip`` (``ClipPlan``).
 """
+import array
 import ctypes
 import os
 
@@ -533,26 +534,28 @@ class _OpPlan:
             torch.device(device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._empty = torch.empty          # (Tensor.new_empty takes twice the time)
         self._fixed = stream is not None
         self._on = _stream(stream) if self._fixed else None
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
 
     def _use(self):
         """Point the plan at the stream this call runs on."""
         if not self._fixed:
-            import torch
-            s = torch.cuda.current_stream(self.device).cuda_stream
+            s = self._current(self.device.index)
             if s != self._on:
                 cat_plan_set_stream(self.handle, s)
                 self._on = s
 
     def _tensor(self, t, name, dtype, shape=None, rows=False):
         """`t` on the plan's device, of `dtype` and `shape`, contiguous (`rows`:
-        contiguous within each token row)."""
+        contiguous within each token row).  Returns its address."""
         if t.device != self.device:
             raise ValueError("%s is on %s, the plan on %s" % (name, t.device, self.device))
         if t.dtype != dtype:
             raise ValueError("%s must be %s" % (name, dtype))
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError("%s must have shape %s" % (name, tuple(shape)))
         if rows:
             st, w = t.stride(), t.shape[2]
@@ -560,7 +563,7 @@ class _OpPlan:
                 raise ValueError("%s: the heads of a token row must be contiguous" % name)
         elif not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        return t
+        return t.data_ptr()
 
     def sync(self):
         cat_plan_sync(self.handle)
@@ -614,57 +617,62 @@ class AttnPlan(_OpPlan):
         with _on_device(self.device):
             self.handle = cat_plan_create_attn(max_tokens, max_seqs, Hq, Hkv, dh, self.dtype,
                                                causal, 0.0 if scale is None else scale, self._on)
+        self._fwd, self._bwd = lib().cat_attn_forward, lib().cat_attn_backward
+        self._f32, self._i32 = torch.float32, torch.int32
+
+    def _rows(self, t, name, shape):
+        """Address and row stride of a [T, heads, dh] operand."""
+        p = self._tensor(t, name, self.torch_dtype, shape, rows=True)
+        # A single row has no stride of its own (torch may report any).
+        return p, t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
 
     def _inputs(self, Q, K, V, cu_seqlens):
-        import torch
         T = Q.shape[0]
-        self._tensor(Q, "Q", self.torch_dtype, (T, self.Hq, self.dh), rows=True)
-        self._tensor(K, "K", self.torch_dtype, (T, self.Hkv, self.dh), rows=True)
-        self._tensor(V, "V", self.torch_dtype, (T, self.Hkv, self.dh), rows=True)
-        self._tensor(cu_seqlens, "cu_seqlens", torch.int32)
+        kv = (T, self.Hkv, self.dh)
+        q, ldq = self._rows(Q, "Q", (T, self.Hq, self.dh))
+        k, ldk = self._rows(K, "K", kv)
+        v, ldv = self._rows(V, "V", kv)
+        cu = self._tensor(cu_seqlens, "cu_seqlens", self._i32)
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must have S + 1 entries")
-        return T, cu_seqlens.shape[0] - 1
-
-    def _ld(self, t):
-        # A single row has no stride of its own (torch may report any).
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        return T, cu_seqlens.shape[0] - 1, cu, (q, k, v), (ldq, ldk, ldv)
 
     def forward(self, Q, K, V, cu_seqlens, O=None, lse=None):
-        import torch
-        T, S = self._inputs(Q, K, V, cu_seqlens)
+        T, S, cu, ptrs, lds = self._inputs(Q, K, V, cu_seqlens)
         if O is None:
-            O = torch.empty((T, self.Hq, self.dh), dtype=self.torch_dtype, device=self.device)
+            O = self._empty((T, self.Hq, self.dh), dtype=self.torch_dtype, device=self.device)
+            o = O.data_ptr()
         else:
-            self._tensor(O, "O", self.torch_dtype, (T, self.Hq, self.dh))
+            o = self._tensor(O, "O", self.torch_dtype, (T, self.Hq, self.dh))
         if lse is None:
-            lse = torch.empty((self.Hq, T), dtype=torch.float32, device=self.device)
+            lse = self._empty((self.Hq, T), dtype=self._f32, device=self.device)
+            z = lse.data_ptr()
         else:
-            self._tensor(lse, "lse", torch.float32, (self.Hq, T))
+            z = self._tensor(lse, "lse", self._f32, (self.Hq, T))
         self._use()
-        cat_attn_forward(self.handle, Q, K, V, O, lse, cu_seqlens, T, S, self._ld(Q), self._ld(K),
-                         self._ld(V))
+        st = self._fwd(self.handle, *ptrs, o, z, cu, T, S, *lds)
+        if st:
+            raise CatError(st, "cat_attn_forward")
         return O, lse
 
     def backward(self, Q, K, V, O, lse, dO, cu_seqlens, dQ=None, dK=None, dV=None):
-        import torch
-        T, S = self._inputs(Q, K, V, cu_seqlens)
-        q, k = (T, self.Hq, self.dh), (T, self.Hkv, self.dh)
-        self._tensor(O, "O", self.torch_dtype, q)
-        self._tensor(dO, "dO", self.torch_dtype, q)
-        self._tensor(lse, "lse", torch.float32, (self.Hq, T))
-        out = []
-        for t, name, shape in ((dQ, "dQ", q), (dK, "dK", k), (dV, "dV", k)):
-            if t is None:
-                t = torch.empty(shape, dtype=self.torch_dtype, device=self.device)
-            else:
-                self._tensor(t, name, self.torch_dtype, shape, rows=True)
-            out.append(t)
+        T, S, cu, ptrs, lds = self._inputs(Q, K, V, cu_seqlens)
+        q, kv = (T, self.Hq, self.dh), (T, self.Hkv, self.dh)
+        o = self._tensor(O, "O", self.torch_dtype, q)
+        do = self._tensor(dO, "dO", self.torch_dtype, q)
+        z = self._tensor(lse, "lse", self._f32, (self.Hq, T))
+        kind = dict(dtype=self.torch_dtype, device=self.device)
+        dQ = self._empty(q, **kind) if dQ is None else dQ
+        dK = self._empty(kv, **kind) if dK is None else dK
+        dV = self._empty(kv, **kind) if dV is None else dV
+        dq, lddq = self._rows(dQ, "dQ", q)
+        dk, lddk = self._rows(dK, "dK", kv)
+        dv, lddv = self._rows(dV, "dV", kv)
         self._use()
-        cat_attn_backward(self.handle, Q, K, V, O, lse, dO, out[0], out[1], out[2], cu_seqlens, T,
-                          S, self._ld(Q), self._ld(K), self._ld(V), self._ld(out[0]),
-                          self._ld(out[1]), self._ld(out[2]))
-        return tuple(out)
+        st = self._bwd(self.handle, *ptrs, o, z, do, dq, dk, dv, cu, T, S, *lds, lddq, lddk, lddv)
+        if st:
+            raise CatError(st, "cat_attn_backward")
+        return dQ, dK, dV
 
 
 class LayerNormPlan(_OpPlan):
@@ -683,54 +691,49 @@ class LayerNormPlan(_OpPlan):
         self._open(device, stream)
         with _on_device(self.device):
             self.handle = cat_plan_create_layernorm(max_rows, D, self.dtype, eps, self._on)
+        self._fwd, self._bwd = lib().cat_layernorm_forward, lib().cat_layernorm_backward
+        self._f32 = torch.float32
 
-    def _rows(self, X, gamma, beta=None):
+    def _inputs(self, X, gamma, beta=None):
         if X.dim() < 1 or X.shape[-1] != self.D:
             raise ValueError("the last dimension must be %d" % self.D)
-        self._tensor(X, "X", self.torch_dtype)
-        for t, name in ((gamma, "gamma"), (beta, "beta")):
-            if t is not None:
-                self._tensor(t, name, self.torch_dtype, (self.D,))
-        return X.numel() // self.D
+        x = self._tensor(X, "X", self.torch_dtype)
+        w = None if gamma is None else self._tensor(gamma, "gamma", self.torch_dtype, (self.D,))
+        b = None if beta is None else self._tensor(beta, "beta", self.torch_dtype, (self.D,))
+        return X.numel() // self.D, x, w, b
+
+    def _out(self, t, name, shape, dtype):
+        if t is None:
+            t = self._empty(shape, dtype=dtype, device=self.device)
+            return t, t.data_ptr()
+        return t, self._tensor(t, name, dtype, shape)
 
     def forward(self, X, gamma=None, beta=None, Y=None, mean=None, rstd=None):
-        import torch
-        rows = self._rows(X, gamma, beta)
-        if Y is None:
-            Y = torch.empty_like(X)
-        else:
-            self._tensor(Y, "Y", self.torch_dtype, X.shape)
-        stats = []
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is None:
-                t = torch.empty(X.shape[:-1], dtype=torch.float32, device=self.device)
-            else:
-                self._tensor(t, name, torch.float32, X.shape[:-1])
-            stats.append(t)
+        rows, x, w, b = self._inputs(X, gamma, beta)
+        lead = X.shape[:-1]
+        Y, y = self._out(Y, "Y", X.shape, self.torch_dtype)
+        mean, m = self._out(mean, "mean", lead, self._f32)
+        rstd, r = self._out(rstd, "rstd", lead, self._f32)
         self._use()
-        cat_layernorm_forward(self.handle, X, gamma, beta, Y, stats[0], stats[1], rows)
-        return Y, stats[0], stats[1]
+        st = self._fwd(self.handle, x, w, b, y, m, r, rows)
+        if st:
+            raise CatError(st, "cat_layernorm_forward")
+        return Y, mean, rstd
 
     def backward(self, X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None):
-        import torch
-        rows = self._rows(X, gamma)
-        self._tensor(dY, "dY", self.torch_dtype, X.shape)
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            self._tensor(t, name, torch.float32, X.shape[:-1])
-        if dX is None:
-            dX = torch.empty_like(X)
-        else:
-            self._tensor(dX, "dX", self.torch_dtype, X.shape)
-        grads = []
-        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
-            if t is None:
-                t = torch.empty((self.D,), dtype=self.torch_dtype, device=self.device)
-            else:
-                self._tensor(t, name, self.torch_dtype, (self.D,))
-            grads.append(t)
+        rows, x, w, _ = self._inputs(X, gamma)
+        lead = X.shape[:-1]
+        dy = self._tensor(dY, "dY", self.torch_dtype, X.shape)
+        m = self._tensor(mean, "mean", self._f32, lead)
+        r = self._tensor(rstd, "rstd", self._f32, lead)
+        dX, dx = self._out(dX, "dX", X.shape, self.torch_dtype)
+        dgamma, dg = self._out(dgamma, "dgamma", (self.D,), self.torch_dtype)
+        dbeta, db = self._out(dbeta, "dbeta", (self.D,), self.torch_dtype)
         self._use()
-        cat_layernorm_backward(self.handle, X, gamma, mean, rstd, dY, dX, grads[0], grads[1], rows)
-        return dX, grads[0], grads[1]
+        st = self._bwd(self.handle, x, w, m, r, dy, dx, dg, db, rows)
+        if st:
+            raise CatError(st, "cat_layernorm_backward")
+        return dX, dgamma, dbeta
 
 
 class ClipPlan(_OpPlan):
@@ -750,35 +753,45 @@ class ClipPlan(_OpPlan):
         self._open(device, stream)
         with _on_device(self.device):
             self.handle = cat_plan_create_clip(self.sizes, self.dtypes, self._on)
+        self._norm, self._clip = lib().cat_grad_norm, lib().cat_grad_clip
+        self._f32 = torch.float32
 
     def _list(self, tensors, name):
+        """The tensors' addresses, as an array of the C interface."""
         if len(tensors) != len(self.sizes):
             raise ValueError("%d %s for a plan of %d" % (len(tensors), name, len(self.sizes)))
+        ptrs = array.array("Q")
+        device = self.device
         for t, n, d in zip(tensors, self.sizes, self.dtypes):
-            if t.dtype != d or t.numel() != n or not t.is_contiguous() or t.device != self.device:
+            if t.dtype is not d or t.numel() != n or not t.is_contiguous() or t.device != device:
                 raise ValueError("%s must be contiguous, of the plan's sizes, dtypes and device"
                                  % name)
+            ptrs.append(t.data_ptr())
+        return ptrs
+
+    def _scalar(self, norm):
+        if norm is None:
+            norm = self._empty((), dtype=self._f32, device=self.device)
+            return norm, norm.data_ptr()
+        return norm, self._tensor(norm, "norm", self._f32, ())
 
     def norm(self, grads, norm=None):
-        import torch
-        self._list(grads, "grads")
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        ptrs = self._list(grads, "grads")
+        norm, n = self._scalar(norm)
         self._use()
-        cat_grad_norm(self.handle, grads, norm)
+        st = self._norm(self.handle, ptrs.buffer_info()[0], n)
+        if st:
+            raise CatError(st, "cat_grad_norm")
         return norm
 
     def clip(self, grads, max_norm, out=None, norm=None):
-        import torch
-        self._list(grads, "grads")
-        if out is None:
-            out = grads
-        else:
-            self._list(out, "out")
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
+        ptrs = self._list(grads, "grads")
+        outs = ptrs if out is None or out is grads else self._list(out, "out")
+        norm, n = self._scalar(norm)
         self._use()
-        cat_grad_clip(self.handle, grads, out, max_norm, norm)
+        st = self._clip(self.handle, ptrs.buffer_info()[0], outs.buffer_info()[0], max_norm, n)
+        if st:
+            raise CatError(st, "cat_grad_clip")
         return norm
 
 
