@@ -29,6 +29,7 @@ for convenience.  The operators around a CAT layer in a training step are
 """
 import array
 import ctypes
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -754,20 +755,21 @@ class ClipPlan(_OpPlan):
         with _on_device(self.device):
             self.handle = cat_plan_create_clip(self.sizes, self.dtypes, self._on)
         self._norm, self._clip = lib().cat_grad_norm, lib().cat_grad_clip
-        self._f32 = torch.float32
+        self._f32, self._T = torch.float32, torch.Tensor
+        self._dtype_of = operator.attrgetter("dtype")
 
     def _list(self, tensors, name):
         """The tensors' addresses, as an array of the C interface."""
         if len(tensors) != len(self.sizes):
             raise ValueError("%d %s for a plan of %d" % (len(tensors), name, len(self.sizes)))
-        ptrs = array.array("Q")
-        device = self.device
-        for t, n, d in zip(tensors, self.sizes, self.dtypes):
-            if t.dtype is not d or t.numel() != n or not t.is_contiguous() or t.device != device:
-                raise ValueError("%s must be contiguous, of the plan's sizes, dtypes and device"
-                                 % name)
-            ptrs.append(t.data_ptr())
-        return ptrs
+        # (one attribute of all tensors at a time: half the time of a loop)
+        T = self._T
+        if (list(map(T.numel, tensors)) != self.sizes or
+                list(map(self._dtype_of, tensors)) != self.dtypes or
+                not all(map(T.is_contiguous, tensors)) or
+                set(map(T.get_device, tensors)) - {self.device.index}):
+            raise ValueError("%s must be contiguous, of the plan's sizes, dtypes and device" % name)
+        return array.array("Q", map(T.data_ptr, tensors))
 
     def _scalar(self, norm):
         if norm is None:

@@ -24,28 +24,32 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// VEC adjacent elements, aligned to their total size.
+// VEC adjacent elements, aligned to their total size: as loaded, and as fp32.
 template <typename T, int VEC>
 struct Vec;
 template <>
 struct Vec<float, 1> {
-  static __device__ __forceinline__ void ld(const float* p, float* v) { v[0] = __ldg(p); }
+  using Raw = float;
+  static __device__ __forceinline__ Raw ldr(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ void widen(Raw x, float* v) { v[0] = x; }
   static __device__ __forceinline__ void st(float* p, const float* v) { p[0] = v[0]; }
 };
 template <>
 struct Vec<float, 2> {
-  static __device__ __forceinline__ void ld(const float* p, float* v) {
-    const float2 x = ld_pair(p);
-    v[0] = x.x; v[1] = x.y;
-  }
+  using Raw = float2;
+  static __device__ __forceinline__ Raw ldr(const float* p) { return ld_pair(p); }
+  static __device__ __forceinline__ void widen(Raw x, float* v) { v[0] = x.x; v[1] = x.y; }
   static __device__ __forceinline__ void st(float* p, const float* v) {
     st_pair(p, make_float2(v[0], v[1]));
   }
 };
 template <>
 struct Vec<float, 4> {
-  static __device__ __forceinline__ void ld(const float* p, float* v) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+  using Raw = float4;
+  static __device__ __forceinline__ Raw ldr(const float* p) {
+    return __ldg(reinterpret_cast<const float4*>(p));
+  }
+  static __device__ __forceinline__ void widen(Raw x, float* v) {
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
   }
   static __device__ __forceinline__ void st(float* p, const float* v) {
@@ -54,8 +58,12 @@ struct Vec<float, 4> {
 };
 template <>
 struct Vec<__nv_bfloat16, 1> {
-  static __device__ __forceinline__ void ld(const __nv_bfloat16* p, float* v) {
-    v[0] = ld_elem(p);
+  using Raw = unsigned short;
+  static __device__ __forceinline__ Raw ldr(const __nv_bfloat16* p) {
+    return __ldg(reinterpret_cast<const unsigned short*>(p));
+  }
+  static __device__ __forceinline__ void widen(Raw x, float* v) {
+    v[0] = __uint_as_float((unsigned int)x << 16);
   }
   static __device__ __forceinline__ void st(__nv_bfloat16* p, const float* v) {
     st_elem(p, v[0]);
@@ -63,9 +71,13 @@ struct Vec<__nv_bfloat16, 1> {
 };
 template <>
 struct Vec<__nv_bfloat16, 2> {
-  static __device__ __forceinline__ void ld(const __nv_bfloat16* p, float* v) {
-    const float2 x = ld_pair(p);
-    v[0] = x.x; v[1] = x.y;
+  using Raw = unsigned int;
+  static __device__ __forceinline__ Raw ldr(const __nv_bfloat16* p) {
+    return __ldg(reinterpret_cast<const unsigned int*>(p));
+  }
+  static __device__ __forceinline__ void widen(Raw x, float* v) {
+    v[0] = __uint_as_float(x << 16);
+    v[1] = __uint_as_float(x & 0xffff0000u);
   }
   static __device__ __forceinline__ void st(__nv_bfloat16* p, const float* v) {
     st_pair(p, make_float2(v[0], v[1]));
@@ -73,8 +85,11 @@ struct Vec<__nv_bfloat16, 2> {
 };
 template <>
 struct Vec<__nv_bfloat16, 8> {
-  static __device__ __forceinline__ void ld(const __nv_bfloat16* p, float* v) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw ldr(const __nv_bfloat16* p) {
+    return __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  static __device__ __forceinline__ void widen(Raw x, float* v) {
     const unsigned int w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -89,6 +104,10 @@ struct Vec<__nv_bfloat16, 8> {
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
   }
 };
+template <typename T, int VEC>
+__device__ __forceinline__ void load(const T* p, float* v) {
+  Vec<T, VEC>::widen(Vec<T, VEC>::ldr(p), v);
+}
 
 // Sum over the threads of a row: a warp, or the CTA (TPR = 256) through
 // `red` (one float a warp; two barriers, so `red` can be used again at once).
@@ -106,6 +125,30 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     __syncthreads();
   }
   return v;
+}
+
+// Two sums at once over the TPR threads of row group `sub`; `red` holds two
+// floats a warp for each of two uses in turn (`use`), so that one barrier a
+// call (the group's own) is enough.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int sub, int use) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (TPR > 32) {
+    red += use * (kThreads / 32);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(TPR) : "memory");
+    red += sub * (TPR / 32);
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) {
+      a += red[i].x;
+      b += red[i].y;
+    }
+  }
 }
 
 // E elements a thread in vectors of VEC: vector k of thread t covers columns
@@ -128,7 +171,7 @@ ln_fwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const T* __r
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + t) * VEC;
     if (c < D) {
-      Vec<T, VEC>::ld(x + c, v[k]);
+      load<T, VEC>(x + c, v[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[k][e] = 0.f;
@@ -155,8 +198,8 @@ ln_fwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const T* __r
     const int c = (k * TPR + t) * VEC;
     if (c < D) {
       float w[VEC], b[VEC];
-      if (gamma) Vec<T, VEC>::ld(gamma + c, w);
-      if (beta) Vec<T, VEC>::ld(beta + c, b);
+      if (gamma) load<T, VEC>(gamma + c, w);
+      if (beta) load<T, VEC>(beta + c, b);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float u = v[k][e] * r;
@@ -173,44 +216,68 @@ ln_fwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const T* __r
   }
 }
 
+// CTAs of the backward that an SM holds: its persistent grid is that many an
+// SM, so that none waits for another to end.
+template <typename T, int VEC, int E>
+constexpr int bwd_per_sm() {
+  return E == 8 ? (sizeof(T) == 2 && VEC == 8 ? 4 : 3) : E == 16 ? 2 : 1;
+}
+
 // part: [gridDim.x][2][D] sums of dy·x̂ and dy over the CTA's rows (null: none).
 template <typename T, int VEC, int TPR, int E>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, bwd_per_sm<T, VEC, E>())
 ln_bwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const float* __restrict__ mean,
               const float* __restrict__ rstd, const T* __restrict__ dY, T* __restrict__ dX,
               float* __restrict__ part, int rows, int D) {
+  using V = Vec<T, VEC>;
+  using Raw = typename V::Raw;
   constexpr int NV = E / VEC;
   constexpr int kRows = kThreads / TPR;         // rows a CTA works on at once
-  extern __shared__ float sm[];                 // [2][D] sums of the CTA's warps (TPR = 32)
-  __shared__ float red[kThreads / 32];
-  const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  const int sub = TPR == 32 ? (threadIdx.x >> 5) : 0;
+  extern __shared__ float sm[];                 // [2][D] sums of the CTA's row groups
+  __shared__ float2 red[2 * (kThreads / 32)];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   float sg[NV][VEC], sb[NV][VEC];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sg[k][e] = sb[k][e] = 0.f;
   const float inv = 1.f / (float)D;
-  for (int row = blockIdx.x * kRows + sub; row < rows; row += gridDim.x * kRows) {
+  // The next row is on its way while this one is worked on.
+  Raw nx[NV], ng[NV];
+  float nmu = 0.f, nr = 0.f;
+  auto fetch = [&](int row) {
+    if (row >= rows) return;
     const T* x = X + (size_t)row * D;
     const T* dy = dY + (size_t)row * D;
-    float xh[NV][VEC], g[NV][VEC];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
-        Vec<T, VEC>::ld(x + c, xh[k]);
-        Vec<T, VEC>::ld(dy + c, g[k]);
+        nx[k] = V::ldr(x + c);
+        ng[k] = V::ldr(dy + c);
       }
     }
-    const float mu = mean[row], r = rstd[row];
+    nmu = __ldg(mean + row);
+    nr = __ldg(rstd + row);
+  };
+  int row = blockIdx.x * kRows + sub;
+  fetch(row);
+  for (int use = 0; row < rows; row += gridDim.x * kRows, use ^= 1) {
+    float xh[NV][VEC], g[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      V::widen(nx[k], xh[k]);
+      V::widen(ng[k], g[k]);
+    }
+    const float mu = nmu, r = nr;
+    fetch(row + gridDim.x * kRows);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
         float w[VEC];
-        if (gamma) Vec<T, VEC>::ld(gamma + c, w);
+        if (gamma) load<T, VEC>(gamma + c, w);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           xh[k][e] = (xh[k][e] - mu) * r;
@@ -222,8 +289,9 @@ ln_bwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const float*
         }
       }
     }
-    s1 = row_sum<TPR>(s1, red) * inv;
-    s2 = row_sum<TPR>(s2, red) * inv;
+    row_sum2<TPR>(s1, s2, red, sub, use);
+    s1 *= inv;
+    s2 *= inv;
     T* dx = dX + (size_t)row * D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -232,14 +300,14 @@ ln_bwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const float*
         float u[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) u[e] = r * (g[k][e] - s1 - xh[k][e] * s2);
-        Vec<T, VEC>::st(dx + c, u);
+        V::st(dx + c, u);
       }
     }
   }
   if (!part) return;
   float* pg = part + (size_t)blockIdx.x * 2 * D;
-  if (TPR == 32) {
-    // The CTA's warps one after another, in warp order.
+  if (kRows > 1) {
+    // The CTA's row groups one after another.
     for (int w = 0; w < kRows; ++w) {
       if (sub == w) {
 #pragma unroll
@@ -273,23 +341,27 @@ ln_bwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma, const float*
 }
 
 // dgamma and dbeta (either may be null) from the partial rows: a CTA takes 32
-// of the 2·D columns, its 8 warps every 8th partial row each.
+// of the 2·D columns, its 32 warps every 32nd partial row each.
+constexpr int kRedWarps = 32;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-ln_reduce_kernel(const float* __restrict__ part, int nparts, T* __restrict__ dgamma,
-                 T* __restrict__ dbeta, int D) {
-  __shared__ float s[kThreads / 32][33];
+__global__ void __launch_bounds__(32 * kRedWarps)
+ln_reduce_kernel(const float* part, int nparts, T* __restrict__ dgamma, T* __restrict__ dbeta,
+                 int D) {
+  __shared__ float s[kRedWarps][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  pdl_wait();
   float v = 0.f;
-  if (c < 2 * D)
-    for (int i = w; i < nparts; i += kThreads / 32) v += part[(size_t)i * 2 * D + c];
+  if (c < 2 * D) {
+#pragma unroll 8
+    for (int i = w; i < nparts; i += kRedWarps) v += __ldcg(part + (size_t)i * 2 * D + c);
+  }
   s[w][lane] = v;
   __syncthreads();
   if (w == 0 && c < 2 * D) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v += s[i][lane];
+    for (int i = 0; i < kRedWarps; ++i) v += s[i][lane];
     if (c < D) {
       if (dgamma) st_elem(dgamma + c, v);
     } else {
@@ -311,30 +383,44 @@ template <typename T, int VEC, int TPR, int E>
 cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
   const int per = kThreads / TPR;
   const int need = (a.rows + per - 1) / per;
-  const int grid = need < a.max_parts ? need : a.max_parts;
+  const int most = a.max_parts / 4 * bwd_per_sm<T, VEC, E>();
+  const int grid = need < most ? need : most;
   const bool weights = a.dgamma || a.dbeta;
-  const size_t smem = TPR == 32 && weights ? (size_t)2 * a.D * sizeof(float) : 0;
+  const size_t smem = per > 1 && weights ? (size_t)2 * a.D * sizeof(float) : 0;
   ln_bwd_kernel<T, VEC, TPR, E><<<grid, kThreads, smem, st>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), a.mean, a.rstd,
       static_cast<const T*>(a.dy), static_cast<T*>(a.dx), weights ? a.part : nullptr, a.rows, a.D);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !weights) return e;
-  ln_reduce_kernel<T><<<(2 * a.D + 31) / 32, kThreads, 0, st>>>(
-      a.part, grid, static_cast<T*>(a.dgamma), static_cast<T*>(a.dbeta), a.D);
-  return cudaGetLastError();
+  return launch_dependent(ln_reduce_kernel<T>, dim3((2 * a.D + 31) / 32), dim3(32 * kRedWarps), 0,
+                          st, (const float*)a.part, grid, static_cast<T*>(a.dgamma),
+                          static_cast<T*>(a.dbeta), a.D);
 }
 
-// Threads a row and elements a thread: a warp while its lanes hold the row in
-// at most 32 registers each, else the CTA.
+// Threads a row and elements a thread.  Forward: a warp while its lanes hold
+// the row in at most 32 registers each (by eighths), else the CTA.  Backward:
+// as many threads as leave 8 elements each (up to the CTA): it holds four
+// values an element (x̂, dy and the two column sums), and rows in flight are
+// what it needs (16384 x 768 bf16: 39.6 us with a warp a row, 163 registers
+// and 8 warps an SM, against 16.7 with 128 threads a row).
 template <typename T, int VEC>
 cudaError_t pick(const NormArgs& a, bool backward, cudaStream_t st) {
   const int D = a.D;
-#define CAT_LN(TPR, E) (backward ? bwd<T, VEC, TPR, E>(a, st) : fwd<T, VEC, TPR, E>(a, st))
-  if (D <= 32 * 8) return CAT_LN(32, 8);
-  if (D <= 32 * 32) return CAT_LN(32, 32);
-  if (D <= kThreads * 8) return CAT_LN(256, 8);
-  return CAT_LN(256, 32);
-#undef CAT_LN
+  if (backward) {
+    if (D <= 32 * 8) return bwd<T, VEC, 32, 8>(a, st);
+    if (D <= 64 * 8) return bwd<T, VEC, 64, 8>(a, st);
+    if (D <= 128 * 8) return bwd<T, VEC, 128, 8>(a, st);
+    if (D <= 256 * 8) return bwd<T, VEC, 256, 8>(a, st);
+    if (D <= 256 * 16) return bwd<T, VEC, 256, 16>(a, st);
+    return bwd<T, VEC, 256, 32>(a, st);
+  }
+  if (D <= 32 * 8) return fwd<T, VEC, 32, 8>(a, st);
+  if (D <= 32 * 16) return fwd<T, VEC, 32, 16>(a, st);
+  if (D <= 32 * 24) return fwd<T, VEC, 32, 24>(a, st);
+  if (D <= 32 * 32) return fwd<T, VEC, 32, 32>(a, st);
+  if (D <= 256 * 8) return fwd<T, VEC, 256, 8>(a, st);
+  if (D <= 256 * 16) return fwd<T, VEC, 256, 16>(a, st);
+  return fwd<T, VEC, 256, 32>(a, st);
 }
 
 template <typename T, int FULL>
@@ -347,7 +433,7 @@ cudaError_t by_width(const NormArgs& a, bool backward, cudaStream_t st) {
 
 }  // namespace
 
-int layernorm_parts(int sms) { return 2 * sms; }
+int layernorm_parts(int sms) { return 4 * sms; }
 
 cudaError_t launch_layernorm(const NormArgs& a, int dtype, bool backward, cudaStream_t st) {
   return dtype == CAT_BF16 ? by_width<__nv_bfloat16, 8>(a, backward, st)
