@@ -1,6 +1,7 @@
-// Softmax attention over packed sequences on the FP32 pipe: every dtype and
-// head width up to 128, any element-aligned rows.  fp32 storage and shapes
-// that the tensor-core kernels do not take run here.
+// Softmax attention over packed sequences on the FP32 pipe: what the
+// tensor-core kernels do not take.  That is bf16 whose rows or heads do not
+// all start on 16-byte boundaries (any head width up to 128), and the
+// backward of fp32 heads wider than 64.  Also the choice between the kernels.
 //
 // Per sequence and query head h (key head g = h / (Hq/Hkv)), with rows i, j:
 //   s_ij = scale·q_i·k_j (j <= i if causal), lse_i = log Σ_j exp s_ij,
@@ -467,17 +468,18 @@ constexpr size_t dkv_smem(int DP) {
   return ((size_t)4 * kBlk * (DP + 4) + 2 * kBlk * kPs) * sizeof(float);
 }
 
-template <typename T, int DP>
+template <int DP>
 cudaError_t setup_one() {
-  cudaError_t e = allow_max_smem(attn_fwd_kernel<T, DP>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_dq_kernel<T, DP>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_dkv_kernel<T, DP>);
+  cudaError_t e = allow_max_smem(attn_fwd_kernel<__nv_bfloat16, DP>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_dq_kernel<__nv_bfloat16, DP>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_dkv_kernel<__nv_bfloat16, DP>);
   return e;
 }
 
-template <typename T, int DP>
+template <int DP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
-  attn_fwd_kernel<T, DP><<<(unsigned)(attn_slots(a.T, a.S, 6) * a.Hq), kThr, fwd_smem(DP), st>>>(a);
+  attn_fwd_kernel<__nv_bfloat16, DP>
+      <<<(unsigned)(attn_slots(a.T, a.S, 6) * a.Hq), kThr, fwd_smem(DP), st>>>(a);
   return cudaGetLastError();
 }
 
@@ -491,30 +493,23 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t fwd_t(const AttnArgs& a, cudaStream_t st) {
-  return a.dh <= 32 ? fwd<T, 32>(a, st) : a.dh <= 64 ? fwd<T, 64>(a, st) : fwd<T, 128>(a, st);
-}
-template <typename T>
-cudaError_t bwd_t(const AttnArgs& a, cudaStream_t st) {
-  return a.dh <= 32 ? bwd<T, 32>(a, st) : a.dh <= 64 ? bwd<T, 64>(a, st) : bwd<T, 128>(a, st);
-}
-
 }  // namespace
 
 cudaError_t setup_attn() {
-  cudaError_t e = setup_one<float, 32>();
-  if (e == cudaSuccess) e = setup_one<float, 64>();
-  if (e == cudaSuccess) e = setup_one<float, 128>();
-  if (e == cudaSuccess) e = setup_one<__nv_bfloat16, 32>();
-  if (e == cudaSuccess) e = setup_one<__nv_bfloat16, 64>();
-  if (e == cudaSuccess) e = setup_one<__nv_bfloat16, 128>();
+  cudaError_t e = setup_one<32>();
+  if (e == cudaSuccess) e = setup_one<64>();
+  if (e == cudaSuccess) e = setup_one<128>();
+  if (e == cudaSuccess) e = allow_max_smem(attn_dq_kernel<float, 128>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_dkv_kernel<float, 128>);
   return e;
 }
 
 cudaError_t launch_attn_forward(const cat_plan_s* p, const AttnArgs& a) {
+  if (p->dtype == CAT_F32) return launch_attn_tc32_forward(a, p->stream);
   if (a.tc) return launch_attn_tc_forward(a, p->stream);
-  return p->dtype == CAT_BF16 ? fwd_t<__nv_bfloat16>(a, p->stream) : fwd_t<float>(a, p->stream);
+  return a.dh <= 32   ? fwd<32>(a, p->stream)
+         : a.dh <= 64 ? fwd<64>(a, p->stream)
+                      : fwd<128>(a, p->stream);
 }
 
 cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a) {
@@ -527,7 +522,11 @@ cudaError_t launch_attn_backward(const cat_plan_s* p, const AttnArgs& a) {
     attn_delta_kernel<float><<<grid, kThr, 0, p->stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return p->dtype == CAT_BF16 ? bwd_t<__nv_bfloat16>(a, p->stream) : bwd_t<float>(a, p->stream);
+  if (p->dtype == CAT_F32)
+    return a.dh <= 64 ? launch_attn_tc32_backward(a, p->stream) : bwd<float, 128>(a, p->stream);
+  return a.dh <= 32   ? bwd<__nv_bfloat16, 32>(a, p->stream)
+         : a.dh <= 64 ? bwd<__nv_bfloat16, 64>(a, p->stream)
+                      : bwd<__nv_bfloat16, 128>(a, p->stream);
 }
 
 }  // namespace cat

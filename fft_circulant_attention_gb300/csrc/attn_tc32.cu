@@ -1,0 +1,969 @@
+// Softmax attention over packed sequences on the tensor cores (tcgen05) for
+// fp32 storage: the forward for head widths up to 128, the backward up to 64,
+// any strides and alignment.
+//
+// Every operand is split into three bf16 terms, x = x0 + x1 + x2 with
+// |x1| <= 2^-9 |x|, |x2| <= 2^-17 |x| and a remainder of 2^-25 |x|, and a
+// product A·B becomes the six products A_i·B_j with i + j <= 2, smallest
+// first, into one fp32 accumulator; what is left out is below 2^-24 of
+// |a||b|, half a rounding step of fp32.  bf16 MMAs at a sixth of their rate
+// are still four times what the FP32 pipe could do at best.
+//
+// The tensor core's fp32 accumulator drops what does not fit instead of
+// rounding, always toward zero, so a long chain of MMAs drifts (4·10^-6 of the
+// result after 240 of them).  An accumulator therefore holds one block's
+// product, four full-size terms; the blocks are added in registers.
+//
+// A CTA takes 128 rows (the MMA's M, one tensor-memory lane each) and walks
+// the other side in blocks of 64 rows.  Roles (384 threads):
+//   - warps 0-3, one thread a row: scores from tensor memory, softmax or its
+//     gradient, and the results back as three planes of bf16 pairs (the A
+//     operand of the next product);
+//   - warps 4-7: load operands with ordinary loads, split them and write the
+//     planes to shared memory in the 128-byte swizzle the MMA reads; rows
+//     outside the sequence and columns beyond the head width become zeros;
+//   - warp 8: issues the MMAs (warps 9-11 only complete its warpgroup).
+// Bound by the MMAs (six times 128·64·64 a product) with the splitting of the
+// operands and of the probabilities beside them.
+//
+// Values that are not finite (or too large for bf16) do not split.  A CTA
+// that met one, or whose masks could have hidden one, computes its rows again
+// at the end by a plain loop over the pairs that count, straight from the
+// definition: slow, exact in what is NaN and what is not, and never taken by
+// ordinary data.
+#include "../../include/cat.h"
+#include "attn_tc.cuh"
+#include "cat_internal.h"
+
+namespace cat {
+
+namespace {
+
+constexpr int kThreads32 = 384;
+constexpr int kB = 64;                     // rows of a block of the other side
+constexpr int kNumBars = 24;
+constexpr float kLazy = 8.f;               // log2 of the maximum's growth that is let pass
+
+template <int DP>
+struct Cfg32 {              // (the backward's shared memory holds DP = 64 only)
+  static constexpr int kTilePlane = kTile * DP * 2;      // bytes of one plane of 128 rows
+  static constexpr int kBlkPlane = kB * DP * 2;          // ... of 64 rows
+  static constexpr int kStages = DP == 64 ? 2 : 1;
+  static constexpr size_t kFwdSmem =
+      1024 + 3 * (size_t)kTilePlane + kStages * 6 * (size_t)kBlkPlane + kNumBars * 8 + 16;
+};
+constexpr size_t kBwdSmem32 = 1024 + 6 * (size_t)Cfg32<64>::kTilePlane +
+                              Cfg32<64>::kStages * (6 * (size_t)Cfg32<64>::kBlkPlane + 2 * kB * 4) +
+                              kNumBars * 8 + 16;
+
+// Two values as three packed bf16 pairs.
+__device__ __forceinline__ void split2(float a, float b, uint32_t* p0, uint32_t* p1, uint32_t* p2) {
+  const uint32_t h = bf16x2(a, b);
+  a -= __uint_as_float(h << 16);
+  b -= __uint_as_float(h & 0xffff0000u);
+  const uint32_t m = bf16x2(a, b);
+  a -= __uint_as_float(m << 16);
+  b -= __uint_as_float(m & 0xffff0000u);
+  *p0 = h;
+  *p1 = m;
+  *p2 = bf16x2(a, b);
+}
+
+// ROWS rows of a [.., dh] fp32 operand as three bf16 planes of [DP/64][ROWS]
+// 128-byte rows, 128-byte swizzle; rows from `rows` and columns from dh on are
+// zero.  By the 128 threads tid.  Returns whether a value did not split.
+template <int DP, int ROWS>
+__device__ __forceinline__ bool split_rows(unsigned char* dst, const float* src, long long ld,
+                                           int rows, int dh, int vec, int tid) {
+  constexpr int kPlane = ROWS * DP * 2, kChunks = DP / 8;
+  uint32_t odd = 0;
+#pragma unroll 2
+  for (int i = tid; i < ROWS * kChunks; i += 128) {
+    const int r = i / kChunks, ch = i % kChunks, c = 8 * ch;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (r < rows) {
+      const float* p = src + (long long)r * ld + c;
+      if (vec) {
+        if (c < dh) {
+          const float4 y = __ldg(reinterpret_cast<const float4*>(p));
+          x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+        }
+        if (c + 4 < dh) {
+          const float4 y = __ldg(reinterpret_cast<const float4*>(p + 4));
+          x[4] = y.x; x[5] = y.y; x[6] = y.z; x[7] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < dh) x[e] = __ldg(p + e);
+      }
+    }
+    uint32_t w[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      split2(x[2 * e], x[2 * e + 1], &w[0][e], &w[1][e], &w[2][e]);
+      odd |= odd2(w[0][e]);
+    }
+    unsigned char* q = dst + (ch / 8) * (ROWS * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint4*>(q + k * kPlane) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+  }
+  return (odd & 0x80008000u) != 0;
+}
+
+// The planes (i, j) with i + j <= 2, smallest products first.
+__device__ constexpr int kPi[6] = {0, 2, 1, 0, 1, 0};
+__device__ constexpr int kPj[6] = {2, 0, 1, 1, 0, 0};
+
+// D[128 x 64] = A·B^T, both K-major planes in shared memory (128 and 64 rows).
+template <int DP>
+__device__ __forceinline__ void mma_kk3(uint32_t d, uint64_t a, uint64_t b) {
+  using C = Cfg32<DP>;
+  constexpr uint32_t id = idesc_bf16_f32(kTile, kB);
+#pragma unroll
+  for (int x = 0; x < 6; ++x)
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+      tc_mma_bf16(d, a + ((kPi[x] * C::kTilePlane + (k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                  b + ((kPj[x] * C::kBlkPlane + (k / 4) * (kB * 128) + (k % 4) * 32) >> 4), id,
+                  x > 0 || k > 0);
+}
+// D[128 x DP] = A·B: A three planes of 32 packed columns in tensor memory
+// (128 x 64), B planes of 64 rows.
+template <int DP>
+__device__ __forceinline__ void mma_tn3(uint32_t d, uint32_t a, uint64_t b) {
+  using C = Cfg32<DP>;
+  constexpr uint32_t id = idesc_bf16_f32_bmn(kTile, DP);
+#pragma unroll
+  for (int x = 0; x < 6; ++x)
+#pragma unroll
+    for (int k = 0; k < kB / 16; ++k)
+      tc_mma_bf16_ts(d, a + kPi[x] * (kB / 2) + 8 * k,
+                     b + ((kPj[x] * C::kBlkPlane + 2048 * k) >> 4), id, x > 0 || k > 0);
+}
+
+// 64 fp32 values of this thread's lane to three planes of 32 packed columns.
+__device__ __forceinline__ void store_planes(uint32_t taddr, const float* v) {
+#pragma unroll
+  for (int c = 0; c < kB; c += 32) {
+    uint32_t p[3][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      split2(v[c + 2 * i], v[c + 2 * i + 1], &p[0][i], &p[1][i], &p[2][i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) tc_st16(taddr + k * (kB / 2) + c / 2, p[k]);
+  }
+  tc_wait_st();
+}
+
+// acc += DP accumulator columns of this thread's lane.
+template <int DP>
+__device__ __forceinline__ void add_columns(float* acc, uint32_t taddr) {
+#pragma unroll
+  for (int c = 0; c < DP; c += 16) {
+    float o[16];
+    tc_ld16(taddr + c, o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[c + i] += o[i];
+  }
+}
+
+// f · acc to an fp32 row.
+template <int DP>
+__device__ __forceinline__ void store_row32(const float* acc, float* dst, int dh, int vec,
+                                            float f) {
+#pragma unroll
+  for (int c = 0; c < DP; c += 4) {
+    if (vec) {
+      if (c < dh)
+        *reinterpret_cast<float4*>(dst + c) =
+            make_float4(acc[c] * f, acc[c + 1] * f, acc[c + 2] * f, acc[c + 3] * f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < dh) dst[c + e] = acc[c + e] * f;
+    }
+  }
+}
+
+__device__ __forceinline__ float dot_rows(const float* x, const float* y, int dh) {
+  float s = 0.f;
+  for (int d = 0; d < dh; ++d) s = fmaf(__ldg(x + d), __ldg(y + d), s);
+  return s;
+}
+
+// One row of the forward by the definition (see the top of the file).
+__device__ __noinline__ void plain_fwd_row(const AttnArgs& a, const AttnBlock& b, int h, int g,
+                                           int row) {
+  const float sc = a.scale * kLog2e;
+  const float* q = static_cast<const float*>(a.q) + (b.start + (long long)row) * a.ldq +
+                   (long long)h * a.dh;
+  const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+  const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+  float* o = static_cast<float*>(a.out) + ((b.start + (long long)row) * a.Hq + h) * a.dh;
+  const int n = a.causal ? row + 1 : b.len;
+  float m = -INFINITY, l = 0.f;
+  for (int j = 0; j < n; ++j) m = fmaxf(m, dot_rows(q, k + j * a.ldk, a.dh) * sc);
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int j = 0; j < n; ++j) l += ex2(dot_rows(q, k + j * a.ldk, a.dh) * sc - base);
+  for (int c = 0; c < a.dh; c += 8) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const float p = ex2(dot_rows(q, k + j * a.ldk, a.dh) * sc - base);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < a.dh) acc[e] = fmaf(p, __ldg(v + j * a.ldv + c + e), acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < a.dh) o[c + e] = acc[e] / l;
+  }
+  a.lse[(long long)h * a.T + b.start + row] = (m + log2f(l)) * kLn2;
+}
+
+// Rows row (as query i or key j) of the backward by the definition.
+__device__ __noinline__ void plain_dq_row(const AttnArgs& a, const AttnBlock& b, int h, int g,
+                                          int row) {
+  const long long t = b.start + (long long)row, ldo = (long long)a.Hq * a.dh;
+  const float* q = static_cast<const float*>(a.q) + t * a.ldq + (long long)h * a.dh;
+  const float* go = static_cast<const float*>(a.dO) + t * ldo + (long long)h * a.dh;
+  const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+  const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+  float* dq = static_cast<float*>(a.dq) + t * a.lddq + (long long)h * a.dh;
+  const float lse = a.lse[(long long)h * a.T + t], del = a.delta[(long long)h * a.T + t];
+  const int n = a.causal ? row + 1 : b.len;
+  for (int c = 0; c < a.dh; c += 8) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const float p = ex2((dot_rows(q, k + j * a.ldk, a.dh) * a.scale - lse) * kLog2e);
+      const float ds = p * (dot_rows(go, v + j * a.ldv, a.dh) - del);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < a.dh) acc[e] = fmaf(ds, __ldg(k + j * a.ldk + c + e), acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < a.dh) dq[c + e] = acc[e] * a.scale;
+  }
+}
+__device__ __noinline__ void plain_dkv_row(const AttnArgs& a, const AttnBlock& b, int g, int row) {
+  const long long t = b.start + (long long)row, ldo = (long long)a.Hq * a.dh;
+  const float* k = static_cast<const float*>(a.k) + t * a.ldk + (long long)g * a.dh;
+  const float* v = static_cast<const float*>(a.v) + t * a.ldv + (long long)g * a.dh;
+  float* dk = static_cast<float*>(a.dk) + t * a.lddk + (long long)g * a.dh;
+  float* dv = static_cast<float*>(a.dv) + t * a.lddv + (long long)g * a.dh;
+  const int rep = a.Hq / a.Hkv;
+  for (int c = 0; c < a.dh; c += 8) {
+    float ak[8], av[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ak[e] = av[e] = 0.f;
+    for (int h = g * rep; h < (g + 1) * rep; ++h)
+      for (int i = a.causal ? row : 0; i < b.len; ++i) {
+        const long long ti = b.start + (long long)i;
+        const float* q = static_cast<const float*>(a.q) + ti * a.ldq + (long long)h * a.dh;
+        const float* go = static_cast<const float*>(a.dO) + ti * ldo + (long long)h * a.dh;
+        const float p = ex2((dot_rows(q, k, a.dh) * a.scale - a.lse[(long long)h * a.T + ti]) *
+                            kLog2e);
+        const float ds = p * (dot_rows(go, v, a.dh) - a.delta[(long long)h * a.T + ti]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.dh) {
+            ak[e] = fmaf(ds, __ldg(q + c + e), ak[e]);
+            av[e] = fmaf(p, __ldg(go + c + e), av[e]);
+          }
+      }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < a.dh) {
+        dk[c + e] = ak[e] * a.scale;
+        dv[c + e] = av[e];
+      }
+  }
+}
+
+// This warp's writes to shared memory are visible to the MMA; one arrival.
+__device__ __forceinline__ void planes_ready(uint32_t bar) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads32, 1)
+attn_tc32_fwd_kernel(const AttnArgs a) {
+  using C = Cfg32<DP>;
+  extern __shared__ unsigned char f32_raw[];
+  const uint32_t raw = smem_addr(f32_raw);
+  unsigned char* sm = f32_raw + (((raw + 1023u) & ~1023u) - raw);
+  unsigned char* q_sm = sm;                                    // 3 planes of 128 rows
+  unsigned char* k_sm = sm + 3 * C::kTilePlane;                // [kStages] 3 planes of 64
+  unsigned char* v_sm = k_sm + C::kStages * 3 * C::kBlkPlane;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(v_sm + C::kStages * 3 * C::kBlkPlane);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  uint32_t* odd = tslot + 1;
+  const uint32_t bar0 = smem_addr(bars);
+  const uint32_t qready = bar0, pready = bar0 + 8, odone = bar0 + 16, done = bar0 + 24;
+  auto sfull = [&](int i) { return bar0 + 32 + 8 * i; };
+  auto kready = [&](int st) { return bar0 + 48 + 8 * st; };
+  auto vready = [&](int st) { return bar0 + 64 + 8 * st; };
+  auto kempty = [&](int st) { return bar0 + 80 + 8 * st; };
+  auto vempty = [&](int st) { return bar0 + 96 + 8 * st; };
+  // Tensor memory: scores (two buffers), probabilities, O.
+  constexpr int kP = 128, kO = 256;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (blockIdx.x == 0) attn_check_sequences(a);
+  const int h = blockIdx.x % a.Hq;
+  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
+  AttnBlock b;
+  if (!attn_find_block(a, slot, 7, &b)) return;
+  const int g = h / (a.Hq / a.Hkv);
+  const int rows = min(kTile, b.len - b.row0);
+  // Key blocks n - 1 .. 0.
+  const int n = ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i)   // qready, pready, kready, vready: a warp each
+      mbar_init(bars + i, i == 0 || i == 1 || (i >= 6 && i < 10) ? 4 : 1);
+    *odd = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+
+  // Registers of the three warpgroups: 240 + 168 + 96 = 3·168, the launch's own.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == 8) {
+      const uint64_t qd = sdesc_k128(q_sm), kd = sdesc_k128(k_sm);
+      const uint64_t vd = sdesc_mn128(v_sm, kB * 128);
+      constexpr uint64_t kStep = 3 * C::kBlkPlane >> 4;
+      auto scores = [&](int j) {
+        const int st = j % C::kStages;
+        mbar_poll(kready(st), (j / C::kStages) & 1, limit);
+        if (elect_one()) {
+          mma_kk3<DP>(tmem + kB * (j & 1), qd, kd + st * kStep);
+          tc_commit(sfull(j & 1));
+          tc_commit(kempty(st));
+        }
+        __syncwarp();
+      };
+      mbar_poll(qready, 0, limit);
+      scores(0);
+      for (int j = 0; j < n; ++j) {
+        // (the buffer of block j + 1 was read before P of block j - 1 was ready)
+        if (j + 1 < n) scores(j + 1);
+        const int st = j % C::kStages;
+        mbar_poll(vready(st), (j / C::kStages) & 1, limit);
+        mbar_poll(pready, j & 1, limit);
+        tc_fence_after();
+        if (elect_one()) {
+          mma_tn3<DP>(tmem + kO, tmem + kP, vd + st * kStep);
+          tc_commit(odone);
+          tc_commit(vempty(st));
+        }
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit(done);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    const int tid = threadIdx.x - 128;
+    const float* q = static_cast<const float*>(a.q) + (b.start + (long long)b.row0) * a.ldq +
+                     (long long)h * a.dh;
+    const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+    const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+    bool bad = split_rows<DP, kTile>(q_sm, q, a.ldq, rows, a.dh, a.vec, tid);
+    planes_ready(qready);
+    auto put = [&](bool is_k, int j) {
+      const int st = j % C::kStages;
+      if (j >= C::kStages)
+        mbar_poll(is_k ? kempty(st) : vempty(st), ((j / C::kStages) - 1) & 1, limit);
+      const long long r0 = (long long)(n - 1 - j) * kB;
+      const int have = b.len - (int)r0;
+      bad |= is_k ? split_rows<DP, kB>(k_sm + st * 3 * C::kBlkPlane, k + r0 * a.ldk, a.ldk, have,
+                                       a.dh, a.vec, tid)
+                  : split_rows<DP, kB>(v_sm + st * 3 * C::kBlkPlane, v + r0 * a.ldv, a.ldv, have,
+                                       a.dh, a.vec, tid);
+      if (bad) *odd = 1;
+      planes_ready(is_k ? kready(st) : vready(st));
+    };
+    put(true, 0);
+    for (int j = 0; j < n; ++j) {
+      if (j + 1 < n) put(true, j + 1);
+      put(false, j);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const uint32_t to = tmem + lanes + kO;
+    const float sc = a.scale * kLog2e;
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f), k2 = l2;
+    float o[DP];
+#pragma unroll
+    for (int c = 0; c < DP; ++c) o[c] = 0.f;
+    for (int j = 0; j < n; ++j) {
+      // The product of the block before: beside this block's scores at head
+      // width 128 (registers), beside its probabilities at 64.
+      if (DP == 128 && j > 0) {
+        mbar_poll(odone, (j - 1) & 1, limit);
+        tc_fence_after();
+        add_columns<DP>(o, to);
+      }
+      mbar_poll(sfull(j & 1), (j >> 1) & 1, limit);
+      tc_fence_after();
+      uint32_t r[kB];
+      tc_ld32(tmem + lanes + kB * (j & 1), r);
+      tc_ld32(tmem + lanes + kB * (j & 1) + 32, r + 32);
+      tc_wait_ld();
+      // The last key this row sees, within the block.
+      const int k0 = (n - 1 - j) * kB;
+      const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - k0;
+      if (k0 + kB > b.len || (a.causal && k0 + kB > b.row0)) {
+#pragma unroll
+        for (int c = 0; c < kB; ++c)
+          if (c > last) r[c] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(r[i]), __uint_as_float(r[4 + i]));
+#pragma unroll
+      for (int c = 8; c < kB; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(r[c + i])), __uint_as_float(r[c + 4 + i]));
+      const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const bool grow = __any_sync(0xffffffffu, top_s > m + kLazy);
+      float f = 1.f;
+      if (grow) {
+        const float nm = fmaxf(m, top_s);
+        f = ex2(m - (nm == -INFINITY ? 0.f : nm));
+        m = nm;
+        l2.x *= f;
+        l2.y *= f;
+        k2.x *= f;
+        k2.y *= f;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+      float p[kB];
+#pragma unroll
+      for (int c = 0; c < kB; c += 2) {
+        float2 x = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nb2);
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        if (c & 2)
+          l2 = add2(l2, x);
+        else
+          k2 = add2(k2, x);
+        p[c] = x.x;
+        p[c + 1] = x.y;
+      }
+      if (DP == 64 && j > 0) {
+        mbar_poll(odone, (j - 1) & 1, limit);
+        tc_fence_after();
+        add_columns<DP>(o, to);
+      }
+      if (grow) {
+#pragma unroll
+        for (int c = 0; c < DP; ++c) o[c] *= f;
+      }
+      store_planes(tmem + lanes + kP, p);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready);
+    }
+    mbar_poll(done, 0, limit);
+    // (rows of a CTA that lost a wait are not written)
+    if (__all_sync(0xffffffffu, limit != 0)) {
+      tc_fence_after();
+      const bool live = row < b.len;
+      const float l = (l2.x + l2.y) + (k2.x + k2.y);
+      const long long tok = (long long)b.start + row;
+      add_columns<DP>(o, to);
+      if (live)
+        store_row32<DP>(o, static_cast<float*>(a.out) + (tok * a.Hq + h) * a.dh, a.dh, a.vec,
+                        1.f / l);
+      if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
+      if (live && *reinterpret_cast<volatile uint32_t*>(odd) != 0)
+        plain_fwd_row(a, b, h, g, row);
+    }
+  }
+  if (limit == 0) report(a.status, 0x741);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    // The columns are freed only after every MMA has completed (bounded).
+    mbar_poll(done, 0, limit);
+    if (limit == 0) report(a.status, 0x742);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK and dV of 128 keys: S^T = K·Q^T, dP^T = V·dO^T, dV += P^T·dO, dK += dS^T·Q.
+template <int DP>
+__global__ void __launch_bounds__(kThreads32, 1)
+attn_tc32_dkv_kernel(const AttnArgs a) {
+  using C = Cfg32<DP>;
+  extern __shared__ unsigned char f32_raw[];
+  const uint32_t raw = smem_addr(f32_raw);
+  unsigned char* sm = f32_raw + (((raw + 1023u) & ~1023u) - raw);
+  unsigned char* k_sm = sm;                                    // 3 planes of 128 rows
+  unsigned char* v_sm = sm + 3 * C::kTilePlane;
+  unsigned char* ring = sm + 6 * C::kTilePlane;                // [kStages] Q, dO: 3 planes of 64
+  float* stat = reinterpret_cast<float*>(ring + C::kStages * 6 * C::kBlkPlane);  // lse, delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + C::kStages * 2 * kB);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  uint32_t* odd = tslot + 1;
+  const uint32_t bar0 = smem_addr(bars);
+  const uint32_t kvready = bar0, pready = bar0 + 8, dsready = bar0 + 16, done = bar0 + 24;
+  const uint32_t sfull = bar0 + 32, dpfull = bar0 + 40, dvdone = bar0 + 48, dkdone = bar0 + 56;
+  auto ready = [&](int st) { return bar0 + 64 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 80 + 8 * st; };
+  const uint32_t dvread = bar0 + 96, dkread = bar0 + 104;      // added to the registers
+  // Tensor memory: scores, probabilities, dP, dS, dV, dK.
+  constexpr int kP = 64, kDp = 160, kDs = 224, kDv = 320, kDk = 384;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int g = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
+  AttnBlock b;
+  if (!attn_find_block(a, slot, 7, &b)) return;
+  const int rep = a.Hq / a.Hkv;
+  const int nqb = (b.len + kB - 1) / kB, qb0 = a.causal ? b.row0 / kB : 0;
+  const int n = rep * (nqb - qb0);
+  const int keys = min(kTile, b.len - b.row0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i)   // those that four warps arrive on
+      mbar_init(bars + i, i < 3 || i == 8 || i == 9 || i == 12 || i == 13 ? 4 : 1);
+    *odd = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+
+  // Registers of the three warpgroups: 168 + 232 + 104 = 3·168, the launch's own.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8) {
+      const uint64_t kd = sdesc_k128(k_sm), vd = sdesc_k128(v_sm);
+      const uint64_t qk = sdesc_k128(ring), gk = sdesc_k128(ring + 3 * C::kBlkPlane);
+      const uint64_t qn = sdesc_mn128(ring, kB * 128);
+      const uint64_t gn = sdesc_mn128(ring + 3 * C::kBlkPlane, kB * 128);
+      constexpr uint64_t kStep = 6 * C::kBlkPlane >> 4;
+      mbar_poll(kvready, 0, limit);
+      mbar_poll(ready(0), 0, limit);
+      if (elect_one()) {
+        mma_kk3<DP>(tmem, kd, qk);
+        tc_commit(sfull);
+        mma_kk3<DP>(tmem + kDp, vd, gk);
+        tc_commit(dpfull);
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j) {
+        const int st = j % C::kStages, nx = (j + 1) % C::kStages;
+        mbar_poll(pready, j & 1, limit);       // P is there, the scores are read
+        if (j + 1 < n) mbar_poll(ready(nx), ((j + 1) / C::kStages) & 1, limit);
+        if (j > 0) mbar_poll(dvread, (j - 1) & 1, limit);
+        tc_fence_after();
+        if (elect_one()) {
+          if (j + 1 < n) {
+            mma_kk3<DP>(tmem, kd, qk + nx * kStep);
+            tc_commit(sfull);
+          }
+          mma_tn3<DP>(tmem + kDv, tmem + kP, gn + st * kStep);
+          tc_commit(dvdone);
+        }
+        __syncwarp();
+        mbar_poll(dsready, j & 1, limit);      // dS is there, dP is read
+        if (j > 0) mbar_poll(dkread, (j - 1) & 1, limit);
+        tc_fence_after();
+        if (elect_one()) {
+          if (j + 1 < n) {
+            mma_kk3<DP>(tmem + kDp, vd, gk + nx * kStep);
+            tc_commit(dpfull);
+          }
+          mma_tn3<DP>(tmem + kDk, tmem + kDs, qn + st * kStep);
+          tc_commit(dkdone);
+          tc_commit(empty(st));
+        }
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit(done);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int tid = threadIdx.x - 128;
+    const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
+    bool bad = split_rows<DP, kTile>(
+        k_sm, static_cast<const float*>(a.k) + t0 * a.ldk + (long long)g * a.dh, a.ldk, keys, a.dh,
+        a.vec, tid);
+    bad |= split_rows<DP, kTile>(
+        v_sm, static_cast<const float*>(a.v) + t0 * a.ldv + (long long)g * a.dh, a.ldv, keys, a.dh,
+        a.vec, tid);
+    planes_ready(kvready);
+    // This warpgroup also adds the blocks' dV and dK, one thread a key.
+    const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
+    float dv[DP], dk[DP];
+#pragma unroll
+    for (int c = 0; c < DP; ++c) dv[c] = dk[c] = 0.f;
+    auto add_block = [&](int j) {
+      mbar_poll(dvdone, j & 1, limit);
+      tc_fence_after();
+      add_columns<DP>(dv, tmem + lanes + kDv);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dvread);
+      mbar_poll(dkdone, j & 1, limit);
+      tc_fence_after();
+      add_columns<DP>(dk, tmem + lanes + kDk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dkread);
+    };
+    int qb = qb0, h = g * rep;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % C::kStages;
+      if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
+      const long long r = b.start + (long long)qb * kB;
+      const int have = b.len - qb * kB;
+      unsigned char* q_sm = ring + st * 6 * C::kBlkPlane;
+      bad |= split_rows<DP, kB>(q_sm, static_cast<const float*>(a.q) + r * a.ldq +
+                                          (long long)h * a.dh, a.ldq, have, a.dh, a.vec, tid);
+      bad |= split_rows<DP, kB>(q_sm + 3 * C::kBlkPlane,
+                                static_cast<const float*>(a.dO) + r * ldo + (long long)h * a.dh,
+                                ldo, have, a.dh, a.vec, tid);
+      if (tid < kB) {
+        const long long i = (long long)h * a.T + r + tid;
+        const float l = tid < have ? a.lse[i] * kLog2e : 0.f;
+        const float d = tid < have ? a.delta[i] : 0.f;
+        stat[st * 2 * kB + tid] = l;
+        stat[st * 2 * kB + kB + tid] = d;
+        bad |= !isfinite(l) || !isfinite(d);
+      }
+      if (bad) *odd = 1;
+      planes_ready(ready(st));
+      if (++qb == nqb) {
+        qb = qb0;
+        ++h;
+      }
+      if (j > 0) add_block(j - 1);
+    }
+    add_block(n - 1);
+    // (rows of a CTA that lost a wait are not written)
+    const int key = b.row0 + 32 * (warp - 4) + lane;
+    if (limit != 0 && key < b.len) {
+      const long long tok = (long long)b.start + key;
+      store_row32<DP>(dv, static_cast<float*>(a.dv) + tok * a.lddv + (long long)g * a.dh, a.dh,
+                      a.vec, 1.f);
+      store_row32<DP>(dk, static_cast<float*>(a.dk) + tok * a.lddk + (long long)g * a.dh, a.dh,
+                      a.vec, a.scale);
+      if (*reinterpret_cast<volatile uint32_t*>(odd) != 0) plain_dkv_row(a, b, g, key);
+    }
+  } else {
+    const int key = b.row0 + 32 * warp + lane;                 // within the sequence
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const float sc = a.scale * kLog2e;
+    const float2 sc2 = make_float2(sc, sc);
+    int qb = qb0;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % C::kStages;
+      const float4* lse = reinterpret_cast<const float4*>(stat + st * 2 * kB);
+      const float4* del = lse + kB / 4;
+      mbar_poll(sfull, j & 1, limit);
+      tc_fence_after();
+      uint32_t r[kB];
+      tc_ld32(tmem + lanes, r);
+      tc_ld32(tmem + lanes + 32, r + 32);
+      mbar_poll(ready(st), (j / C::kStages) & 1, limit);       // (lse and delta: long there)
+      tc_wait_ld();
+      float p[kB];
+#pragma unroll
+      for (int c = 0; c < kB; c += 4) {
+        const float4 l = lse[c / 4];
+        const float2 x = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2,
+                              make_float2(-l.x, -l.y));
+        const float2 y = fma2(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])),
+                              sc2, make_float2(-l.z, -l.w));
+        p[c] = ex2(x.x);
+        p[c + 1] = ex2(x.y);
+        p[c + 2] = ex2(y.x);
+        p[c + 3] = ex2(y.y);
+      }
+      // Columns lo .. hi - 1 are queries that see this key.
+      const int q0 = qb * kB, lo = a.causal ? key - q0 : 0, hi = b.len - q0;
+      const bool cut = q0 + kB > b.len || (a.causal && q0 < b.row0 + kTile);
+      if (cut) {
+#pragma unroll
+        for (int c = 0; c < kB; ++c)
+          if (c < lo || c >= hi) p[c] = 0.f;
+      }
+      if (j > 0) mbar_poll(dvdone, (j - 1) & 1, limit);        // P of before has been used
+      tc_fence_after();
+      store_planes(tmem + lanes + kP, p);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready);
+      mbar_poll(dpfull, j & 1, limit);
+      tc_fence_after();
+      tc_ld32(tmem + lanes + kDp, r);
+      tc_ld32(tmem + lanes + kDp + 32, r + 32);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < kB; c += 4) {
+        const float4 d = del[c / 4];
+        p[c] *= __uint_as_float(r[c]) - d.x;
+        p[c + 1] *= __uint_as_float(r[c + 1]) - d.y;
+        p[c + 2] *= __uint_as_float(r[c + 2]) - d.z;
+        p[c + 3] *= __uint_as_float(r[c + 3]) - d.w;
+      }
+      if (j > 0) mbar_poll(dkdone, (j - 1) & 1, limit);        // dS of before has been used
+      tc_fence_after();
+      store_planes(tmem + lanes + kDs, p);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dsready);
+      if (++qb == nqb) qb = qb0;
+    }
+  }
+  if (limit == 0) report(a.status, 0x751);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    // The columns are freed only after every MMA has completed (bounded).
+    mbar_poll(done, 0, limit);
+    if (limit == 0) report(a.status, 0x752);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dQ of 128 queries: S = Q·K^T, dP = dO·V^T, dQ += dS·K.
+template <int DP>
+__global__ void __launch_bounds__(kThreads32, 1)
+attn_tc32_dq_kernel(const AttnArgs a) {
+  using C = Cfg32<DP>;
+  extern __shared__ unsigned char f32_raw[];
+  const uint32_t raw = smem_addr(f32_raw);
+  unsigned char* sm = f32_raw + (((raw + 1023u) & ~1023u) - raw);
+  unsigned char* q_sm = sm;                                    // 3 planes of 128 rows
+  unsigned char* g_sm = sm + 3 * C::kTilePlane;
+  unsigned char* ring = sm + 6 * C::kTilePlane;                // [kStages] K, V: 3 planes of 64
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::kStages * 6 * C::kBlkPlane);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  uint32_t* odd = tslot + 1;
+  const uint32_t bar0 = smem_addr(bars);
+  const uint32_t qready = bar0, dsready = bar0 + 8, dqdone = bar0 + 16, done = bar0 + 24;
+  auto sfull = [&](int i) { return bar0 + 32 + 8 * i; };       // S and dP of a block
+  auto ready = [&](int st) { return bar0 + 48 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 64 + 8 * st; };
+  // Tensor memory: scores and dP (two buffers each), dS, dQ.
+  constexpr int kDp = 128, kDs = 256, kDq = 384;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int h = blockIdx.x % a.Hq;
+  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
+  AttnBlock b;
+  if (!attn_find_block(a, slot, 7, &b)) return;
+  const int g = h / (a.Hq / a.Hkv);
+  const int rows = min(kTile, b.len - b.row0);
+  const int n = ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i)   // qready, dsready, ready: a warp each
+      mbar_init(bars + i, i < 2 || i == 6 || i == 7 ? 4 : 1);
+    *odd = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+
+  // Registers of the three warpgroups: 216 + 168 + 120 = 3·168, the launch's own.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 8) {
+      const uint64_t qd = sdesc_k128(q_sm), gd = sdesc_k128(g_sm);
+      const uint64_t kk = sdesc_k128(ring), vk = sdesc_k128(ring + 3 * C::kBlkPlane);
+      const uint64_t kn = sdesc_mn128(ring, kB * 128);
+      constexpr uint64_t kStep = 6 * C::kBlkPlane >> 4;
+      auto front = [&](int j) {
+        const int st = j % C::kStages;
+        mbar_poll(ready(st), (j / C::kStages) & 1, limit);
+        if (elect_one()) {
+          mma_kk3<DP>(tmem + kB * (j & 1), qd, kk + st * kStep);
+          mma_kk3<DP>(tmem + kDp + kB * (j & 1), gd, vk + st * kStep);
+          tc_commit(sfull(j & 1));
+        }
+        __syncwarp();
+      };
+      mbar_poll(qready, 0, limit);
+      front(0);
+      for (int j = 0; j < n; ++j) {
+        // (the buffers of block j + 1 were read before dS of block j - 1 was ready)
+        if (j + 1 < n) front(j + 1);
+        const int st = j % C::kStages;
+        mbar_poll(dsready, j & 1, limit);
+        tc_fence_after();
+        if (elect_one()) {
+          mma_tn3<DP>(tmem + kDq, tmem + kDs, kn + st * kStep);
+          tc_commit(dqdone);
+          tc_commit(empty(st));
+        }
+        __syncwarp();
+      }
+      if (elect_one()) tc_commit(done);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    const int tid = threadIdx.x - 128;
+    const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
+    bool bad = split_rows<DP, kTile>(
+        q_sm, static_cast<const float*>(a.q) + t0 * a.ldq + (long long)h * a.dh, a.ldq, rows, a.dh,
+        a.vec, tid);
+    bad |= split_rows<DP, kTile>(
+        g_sm, static_cast<const float*>(a.dO) + t0 * ldo + (long long)h * a.dh, ldo, rows, a.dh,
+        a.vec, tid);
+    planes_ready(qready);
+    const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+    const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % C::kStages;
+      if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
+      const long long r0 = (long long)(n - 1 - j) * kB;
+      const int have = b.len - (int)r0;
+      unsigned char* k_sm = ring + st * 6 * C::kBlkPlane;
+      bad |= split_rows<DP, kB>(k_sm, k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
+      bad |= split_rows<DP, kB>(k_sm + 3 * C::kBlkPlane, v + r0 * a.ldv, a.ldv, have, a.dh, a.vec,
+                                tid);
+      if (bad) *odd = 1;
+      planes_ready(ready(st));
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const float sc = a.scale * kLog2e;
+    const bool live = row < b.len;
+    const long long at = (long long)h * a.T + b.start + row;
+    const float lse = live ? a.lse[at] * kLog2e : 0.f, del = live ? a.delta[at] : 0.f;
+    const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(-lse, -lse);
+    float dq[DP];
+#pragma unroll
+    for (int c = 0; c < DP; ++c) dq[c] = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t ts = tmem + lanes + kB * (j & 1);
+      mbar_poll(sfull(j & 1), (j >> 1) & 1, limit);
+      tc_fence_after();
+      uint32_t r[kB];
+      tc_ld32(ts, r);
+      tc_ld32(ts + 32, r + 32);
+      tc_wait_ld();
+      float p[kB];
+#pragma unroll
+      for (int c = 0; c < kB; c += 2) {
+        const float2 x =
+            fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nl2);
+        p[c] = ex2(x.x);
+        p[c + 1] = ex2(x.y);
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < kB; c0 += 32) {
+        tc_ld32(ts + kDp + c0, r);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) p[c0 + c] *= __uint_as_float(r[c]) - del;
+      }
+      const int k0 = (n - 1 - j) * kB;
+      const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - k0;
+      if (k0 + kB > b.len || (a.causal && k0 + kB > b.row0)) {
+#pragma unroll
+        for (int c = 0; c < kB; ++c)
+          if (c > last) p[c] = 0.f;
+      }
+      if (j > 0) {
+        mbar_poll(dqdone, (j - 1) & 1, limit);                 // dS of before has been used
+        tc_fence_after();
+        add_columns<DP>(dq, tmem + lanes + kDq);
+      }
+      store_planes(tmem + lanes + kDs, p);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dsready);
+    }
+    mbar_poll(done, 0, limit);
+    // (rows of a CTA that lost a wait are not written)
+    if (__all_sync(0xffffffffu, limit != 0)) {
+      tc_fence_after();
+      add_columns<DP>(dq, tmem + lanes + kDq);
+      if (live)
+        store_row32<DP>(dq, static_cast<float*>(a.dq) + ((long long)b.start + row) * a.lddq +
+                                (long long)h * a.dh, a.dh, a.vec, a.scale);
+      if (live && *reinterpret_cast<volatile uint32_t*>(odd) != 0) plain_dq_row(a, b, h, g, row);
+    }
+  }
+  if (limit == 0) report(a.status, 0x761);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    // The columns are freed only after every MMA has completed (bounded).
+    mbar_poll(done, 0, limit);
+    if (limit == 0) report(a.status, 0x762);
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DP>
+cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)(attn_slots(a.T, a.S, 7) * a.Hq);
+  attn_tc32_fwd_kernel<DP><<<grid, kThreads32, Cfg32<DP>::kFwdSmem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t setup_attn_tc32() {
+  cudaError_t e = allow_max_smem(attn_tc32_fwd_kernel<64>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc32_fwd_kernel<128>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc32_dkv_kernel<64>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc32_dq_kernel<64>);
+  return e;
+}
+
+cudaError_t launch_attn_tc32_forward(const AttnArgs& a, cudaStream_t st) {
+  return a.dh <= 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+}
+
+cudaError_t launch_attn_tc32_backward(const AttnArgs& a, cudaStream_t st) {
+  const long long slots = attn_slots(a.T, a.S, 7);
+  attn_tc32_dkv_kernel<64><<<(unsigned)(slots * a.Hkv), kThreads32, kBwdSmem32, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_tc32_dq_kernel<64><<<(unsigned)(slots * a.Hq), kThreads32, kBwdSmem32, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace cat

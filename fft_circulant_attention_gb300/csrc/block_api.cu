@@ -148,7 +148,7 @@ int cat_plan_create_attn(cat_plan_t* out, int max_tokens, int max_seqs, int Hq, 
       !alloc(p, &p->at.stats, cat::attn_tc_stats_count(max_tokens, max_seqs, Hq)))
     return fail(p, CAT_ERR_ALLOC);
   if (cat::setup_attn() != cudaSuccess || cat::setup_attn_tc() != cudaSuccess ||
-      cat::setup_attn_tc_bwd() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
+      cat::setup_attn_tc_bwd() != cudaSuccess || cat::setup_attn_tc32() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
   std::snprintf(p->desc, sizeof(p->desc),
                 "op=attn max_tokens=%d max_seqs=%d Hq=%d Hkv=%d dh=%d causal=%d scale=%g "
                 "workspace=%zu",

@@ -388,6 +388,11 @@ cudaError_t launch_attn_tc_forward(const AttnArgs& a, cudaStream_t st);
 size_t attn_tc_stats_count(int max_tokens, int max_seqs, int Hq);
 cudaError_t setup_attn_tc_bwd();
 cudaError_t launch_attn_tc_backward(const AttnArgs& a, cudaStream_t st);
+// fp32 storage (attn_tc32.cu): the forward, and the backward up to dh = 64
+// (AttnArgs::delta filled).
+cudaError_t setup_attn_tc32();
+cudaError_t launch_attn_tc32_forward(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_tc32_backward(const AttnArgs& a, cudaStream_t st);
 
 // Layer norm (layernorm.cu).  layernorm_parts: partial rows of the weight
 // gradients, at most one a CTA.
