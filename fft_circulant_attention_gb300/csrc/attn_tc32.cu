@@ -69,49 +69,71 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* p0, uint32_t*
   *p2 = bf16x2(a, b);
 }
 
-// ROWS rows of a [.., dh] fp32 operand as three bf16 planes of [DP/64][ROWS]
-// 128-byte rows, 128-byte swizzle; rows from `rows` and columns from dh on are
-// zero.  By the 128 threads tid.  Returns whether a value did not split.
-template <int DP, int ROWS>
-__device__ __forceinline__ bool split_rows(unsigned char* dst, const float* src, long long ld,
-                                           int rows, int dh, int vec, int tid) {
-  constexpr int kPlane = ROWS * DP * 2, kChunks = DP / 8;
-  uint32_t odd = 0;
-#pragma unroll 2
-  for (int i = tid; i < ROWS * kChunks; i += 128) {
-    const int r = i / kChunks, ch = i % kChunks, c = 8 * ch;
-    float x[8];
+// A thread's share of 64 rows of a [.., dh] fp32 operand: pieces of 8 columns,
+// zeros in rows from `rows` and columns from dh on.  By the 128 threads tid.
+template <int DP>
+struct Piece {
+  float x[DP / 16][8];
+  __device__ __forceinline__ void fetch(const float* src, long long ld, int rows, int dh, int vec,
+                                        int tid) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (r < rows) {
-      const float* p = src + (long long)r * ld + c;
-      if (vec) {
-        if (c < dh) {
-          const float4 y = __ldg(reinterpret_cast<const float4*>(p));
-          x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-        }
-        if (c + 4 < dh) {
-          const float4 y = __ldg(reinterpret_cast<const float4*>(p + 4));
-          x[4] = y.x; x[5] = y.y; x[6] = y.z; x[7] = y.w;
-        }
-      } else {
+    for (int i = 0; i < DP / 16; ++i) {
+      const int at = tid + 128 * i, r = at / (DP / 8), c = 8 * (at % (DP / 8));
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < dh) x[e] = __ldg(p + e);
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      if (r < rows) {
+        const float* p = src + (long long)r * ld + c;
+        if (vec) {
+          if (c < dh) {
+            const float4 y = __ldg(reinterpret_cast<const float4*>(p));
+            x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+          }
+          if (c + 4 < dh) {
+            const float4 y = __ldg(reinterpret_cast<const float4*>(p + 4));
+            x[i][4] = y.x; x[i][5] = y.y; x[i][6] = y.z; x[i][7] = y.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < dh) x[i][e] = __ldg(p + e);
+        }
       }
     }
-    uint32_t w[3][4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      split2(x[2 * e], x[2 * e + 1], &w[0][e], &w[1][e], &w[2][e]);
-      odd |= odd2(w[0][e]);
-    }
-    unsigned char* q = dst + (ch / 8) * (ROWS * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      *reinterpret_cast<uint4*>(q + k * kPlane) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
   }
-  return (odd & 0x80008000u) != 0;
+  // As rows row0 .. row0 + 63 of three bf16 planes of [DP/64][ROWS] 128-byte
+  // rows, 128-byte swizzle.  Returns whether a value did not split.
+  template <int ROWS>
+  __device__ __forceinline__ bool put(unsigned char* dst, int row0, int tid) const {
+    constexpr int kPlane = ROWS * DP * 2;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int at = tid + 128 * i, r = row0 + at / (DP / 8), ch = at % (DP / 8);
+      uint32_t w[3][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        split2(x[i][2 * e], x[i][2 * e + 1], &w[0][e], &w[1][e], &w[2][e]);
+        odd |= odd2(w[0][e]);
+      }
+      unsigned char* q = dst + (ch / 8) * (ROWS * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(q + k * kPlane) =
+            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    }
+    return (odd & 0x80008000u) != 0;
+  }
+};
+// A tile of 128 rows.
+template <int DP>
+__device__ __forceinline__ bool put_tile(unsigned char* dst, const float* src, long long ld,
+                                         int rows, int dh, int vec, int tid) {
+  Piece<DP> lo, hi;
+  lo.fetch(src, ld, rows, dh, vec, tid);
+  if (DP == 64) hi.fetch(src + 64 * ld, ld, rows - 64, dh, vec, tid);
+  const bool bad = lo.template put<kTile>(dst, 0, tid);
+  if (DP != 64) hi.fetch(src + 64 * ld, ld, rows - 64, dh, vec, tid);
+  return hi.template put<kTile>(dst, 64, tid) || bad;
 }
 
 // The planes (i, j) with i + j <= 2, smallest products first.
@@ -384,25 +406,37 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
                      (long long)h * a.dh;
     const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
     const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
-    bool bad = split_rows<DP, kTile>(q_sm, q, a.ldq, rows, a.dh, a.vec, tid);
-    planes_ready(qready);
-    auto put = [&](bool is_k, int j) {
-      const int st = j % C::kStages;
-      if (j >= C::kStages)
-        mbar_poll(is_k ? kempty(st) : vempty(st), ((j / C::kStages) - 1) & 1, limit);
-      const long long r0 = (long long)(n - 1 - j) * kB;
+    // Tiles in the order of their use, K0 K1 V0 K2 V1 ..; at head width 64 each
+    // is fetched while the one before is split and written (at 128 the
+    // registers hold one).
+    auto is_k = [&](int i) { return i == 0 || ((i & 1) && i < 2 * n - 1); };
+    auto block = [&](int i) { return i == 2 * n - 1 ? n - 1 : is_k(i) ? (i + 1) / 2 : i / 2 - 1; };
+    Piece<DP> now, next;
+    auto fetch = [&](Piece<DP>& x, int i) {
+      const long long r0 = (long long)(n - 1 - block(i)) * kB;
       const int have = b.len - (int)r0;
-      bad |= is_k ? split_rows<DP, kB>(k_sm + st * 3 * C::kBlkPlane, k + r0 * a.ldk, a.ldk, have,
-                                       a.dh, a.vec, tid)
-                  : split_rows<DP, kB>(v_sm + st * 3 * C::kBlkPlane, v + r0 * a.ldv, a.ldv, have,
-                                       a.dh, a.vec, tid);
-      if (bad) *odd = 1;
-      planes_ready(is_k ? kready(st) : vready(st));
+      if (is_k(i))
+        x.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
+      else
+        x.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
     };
-    put(true, 0);
-    for (int j = 0; j < n; ++j) {
-      if (j + 1 < n) put(true, j + 1);
-      put(false, j);
+    if (DP == 64) fetch(next, 0);
+    bool bad = put_tile<DP>(q_sm, q, a.ldq, rows, a.dh, a.vec, tid);
+    planes_ready(qready);
+    for (int i = 0; i < 2 * n; ++i) {
+      const int j = block(i), st = j % C::kStages;
+      const bool ik = is_k(i);
+      if (DP == 64) {
+        now = next;
+        if (i + 1 < 2 * n) fetch(next, i + 1);
+      } else {
+        fetch(now, i);
+      }
+      if (j >= C::kStages)
+        mbar_poll(ik ? kempty(st) : vempty(st), ((j / C::kStages) - 1) & 1, limit);
+      bad |= now.template put<kB>((ik ? k_sm : v_sm) + st * 3 * C::kBlkPlane, 0, tid);
+      if (bad) *odd = 1;
+      planes_ready(ik ? kready(st) : vready(st));
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
@@ -614,12 +648,21 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int tid = threadIdx.x - 128;
     const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
-    bool bad = split_rows<DP, kTile>(
-        k_sm, static_cast<const float*>(a.k) + t0 * a.ldk + (long long)g * a.dh, a.ldk, keys, a.dh,
-        a.vec, tid);
-    bad |= split_rows<DP, kTile>(
-        v_sm, static_cast<const float*>(a.v) + t0 * a.ldv + (long long)g * a.dh, a.ldv, keys, a.dh,
-        a.vec, tid);
+    int qb = qb0, h = g * rep;
+    Piece<DP> xq, xg;
+    auto fetch = [&]() {
+      const long long r = b.start + (long long)qb * kB;
+      const int have = b.len - qb * kB;
+      xq.fetch(static_cast<const float*>(a.q) + r * a.ldq + (long long)h * a.dh, a.ldq, have, a.dh,
+               a.vec, tid);
+      xg.fetch(static_cast<const float*>(a.dO) + r * ldo + (long long)h * a.dh, ldo, have, a.dh,
+               a.vec, tid);
+    };
+    bool bad = put_tile<DP>(k_sm, static_cast<const float*>(a.k) + t0 * a.ldk +
+                                      (long long)g * a.dh, a.ldk, keys, a.dh, a.vec, tid);
+    bad |= put_tile<DP>(v_sm, static_cast<const float*>(a.v) + t0 * a.ldv + (long long)g * a.dh,
+                        a.ldv, keys, a.dh, a.vec, tid);
+    fetch();
     planes_ready(kvready);
     // This warpgroup also adds the blocks' dV and dK, one thread a key.
     const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
@@ -640,18 +683,14 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(dkread);
     };
-    int qb = qb0, h = g * rep;
     for (int j = 0; j < n; ++j) {
       const int st = j % C::kStages;
       if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
       const long long r = b.start + (long long)qb * kB;
       const int have = b.len - qb * kB;
       unsigned char* q_sm = ring + st * 6 * C::kBlkPlane;
-      bad |= split_rows<DP, kB>(q_sm, static_cast<const float*>(a.q) + r * a.ldq +
-                                          (long long)h * a.dh, a.ldq, have, a.dh, a.vec, tid);
-      bad |= split_rows<DP, kB>(q_sm + 3 * C::kBlkPlane,
-                                static_cast<const float*>(a.dO) + r * ldo + (long long)h * a.dh,
-                                ldo, have, a.dh, a.vec, tid);
+      bad |= xq.template put<kB>(q_sm, 0, tid);
+      bad |= xg.template put<kB>(q_sm + 3 * C::kBlkPlane, 0, tid);
       if (tid < kB) {
         const long long i = (long long)h * a.T + r + tid;
         const float l = tid < have ? a.lse[i] * kLog2e : 0.f;
@@ -666,6 +705,8 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
         qb = qb0;
         ++h;
       }
+      // The next block's rows are on their way while this one's sums come in.
+      if (j + 1 < n) fetch();
       if (j > 0) add_block(j - 1);
     }
     add_block(n - 1);
@@ -840,26 +881,30 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   } else if (warp >= 4) {
     const int tid = threadIdx.x - 128;
     const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
-    bool bad = split_rows<DP, kTile>(
-        q_sm, static_cast<const float*>(a.q) + t0 * a.ldq + (long long)h * a.dh, a.ldq, rows, a.dh,
-        a.vec, tid);
-    bad |= split_rows<DP, kTile>(
-        g_sm, static_cast<const float*>(a.dO) + t0 * ldo + (long long)h * a.dh, ldo, rows, a.dh,
-        a.vec, tid);
-    planes_ready(qready);
     const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
     const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+    Piece<DP> xk, xv;
+    auto fetch = [&](int j) {
+      const long long r0 = (long long)(n - 1 - j) * kB;
+      const int have = b.len - (int)r0;
+      xk.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
+      xv.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
+    };
+    bool bad = put_tile<DP>(q_sm, static_cast<const float*>(a.q) + t0 * a.ldq +
+                                      (long long)h * a.dh, a.ldq, rows, a.dh, a.vec, tid);
+    bad |= put_tile<DP>(g_sm, static_cast<const float*>(a.dO) + t0 * ldo + (long long)h * a.dh,
+                        ldo, rows, a.dh, a.vec, tid);
+    fetch(0);
+    planes_ready(qready);
     for (int j = 0; j < n; ++j) {
       const int st = j % C::kStages;
       if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
-      const long long r0 = (long long)(n - 1 - j) * kB;
-      const int have = b.len - (int)r0;
-      unsigned char* k_sm = ring + st * 6 * C::kBlkPlane;
-      bad |= split_rows<DP, kB>(k_sm, k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
-      bad |= split_rows<DP, kB>(k_sm + 3 * C::kBlkPlane, v + r0 * a.ldv, a.ldv, have, a.dh, a.vec,
-                                tid);
+      unsigned char* k_to = ring + st * 6 * C::kBlkPlane;
+      bad |= xk.template put<kB>(k_to, 0, tid);
+      bad |= xv.template put<kB>(k_to + 3 * C::kBlkPlane, 0, tid);
       if (bad) *odd = 1;
       planes_ready(ready(st));
+      if (j + 1 < n) fetch(j + 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
