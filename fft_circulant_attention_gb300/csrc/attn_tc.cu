@@ -38,147 +38,163 @@ namespace cat {
 
 namespace {
 
-constexpr int kFwdThreads = 384;
 constexpr int kNumBars = 64;               // room for every barrier
+constexpr int kLongRows = 4096;            // average length from which a CTA takes two tiles
 constexpr float kLazy = 8.f;               // log2 of the growth that is let pass
 
-template <int DP>
+template <int DP, int NT>
 struct FwdCfg {
+  static constexpr int kThreads = 128 * (NT + 1);
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = DP == 64 ? 5 : 2;   // K and V of a key block each
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kStages) * kTileBytes +
-                                   kNumBars * 8 + 16;
+  static constexpr int kStages = DP == 64 && NT == 2 ? 5 : 2;   // K and V of a key block each
+  static constexpr size_t kSmem = 1024 + (size_t)(NT + 2 * kStages) * kTileBytes +
+                                   kNumBars * 8 + 96;
   static constexpr bool kOwnP = DP == 64;  // P beside the scores, not in their place
   // Tensor-memory columns.
+  static constexpr int kCols = 256 * NT;
   static constexpr int s(int t) { return kTile * t; }
-  static constexpr int p(int t) { return kOwnP ? 256 + 64 * t : kTile * t; }
-  static constexpr int o(int t) { return kOwnP ? 384 + 64 * t : 256 + kTile * t; }
+  static constexpr int p(int t) { return kOwnP ? NT * kTile + 64 * t : kTile * t; }
+  static constexpr int o(int t) { return kOwnP ? NT * (kTile + 64) + 64 * t : 256 + kTile * t; }
 };
 
-// Named barrier `id` of the two tiles' warpgroups: one arrives, the other waits.
-__device__ __forceinline__ void pass_turn(int id) {
-  asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ void take_turn(int id) {
-  asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory");
-}
+// What a block of work means for the forward.
+struct FwdWork {
+  int top[2];              // key blocks of tile t: top[t] - 1 .. 0 (0: the tile has no rows)
+  int n;                   // blocks of the CTA: n - 1 .. 0
+  int cut;                 // blocks from here on are cut by the mask for some row
+  template <int NT>
+  static __device__ __forceinline__ FwdWork of(const AttnBlock& b, int causal) {
+    FwdWork w;
+    const int nblk = (b.len + kTile - 1) / kTile;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int qb = b.row0 / kTile + t;
+      w.top[t] = t >= NT || qb >= nblk ? 0 : causal ? qb + 1 : nblk;
+    }
+    w.n = max(w.top[0], w.top[1]);
+    w.cut = causal ? b.row0 / kTile : (b.len % kTile ? nblk - 1 : nblk);
+    return w;
+  }
+};
 
-template <int DP>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+template <int DP, int NT>
+__global__ void __launch_bounds__(FwdCfg<DP, NT>::kThreads, NT == 2 ? 1 : 2)
 attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
-  using C = FwdCfg<DP>;
+  using C = FwdCfg<DP, NT>;
+  constexpr int kHelp = 4 * NT;              // first warp of the copy and MMA roles
   extern __shared__ unsigned char fa_raw[];
   const uint32_t raw = smem_addr(fa_raw);
   unsigned char* sm = fa_raw + (((raw + 1023u) & ~1023u) - raw);
-  unsigned char* q_sm = sm;                                       // [2][kTileBytes]
-  unsigned char* kv_sm = sm + 2 * C::kTileBytes;                  // [kStages][K, V][kTileBytes]
+  unsigned char* q_sm = sm;                                       // [NT][kTileBytes]
+  unsigned char* kv_sm = sm + NT * C::kTileBytes;                 // [kStages][K, V][kTileBytes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(kv_sm + 2 * C::kStages * C::kTileBytes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  uint32_t* vodd = tslot + 1;                // a cut block's own rows held non-finite values
   // Barriers by address.
   const uint32_t bar0 = smem_addr(bars);
   auto qfull = [&](int t) { return bar0 + 8 * t; };
-  auto sfull = [&](int t) { return bar0 + 16 + 8 * t; };    // scores are in tensor memory
-  auto sempty = [&](int t) { return bar0 + 32 + 8 * t; };   // ... and in registers
-  auto pfull = [&](int t) { return bar0 + 48 + 8 * t; };    // probabilities in tensor memory
-  auto odone = [&](int t) { return bar0 + 64 + 8 * t; };    // P·V is done
-  auto done = [&](int t) { return bar0 + 80 + 8 * t; };     // every MMA is done
-  // A cut V block has been looked through (one barrier each: both may have
-  // passed before the first is waited for).
-  auto vclean = [&](int c) { return bar0 + 96 + 8 * c; };
-  auto full = [&](int st) { return bar0 + 112 + 8 * st; };
-  auto empty = [&](int st) { return bar0 + 112 + 8 * (C::kStages + st); };
+  auto qempty = [&](int t) { return bar0 + 16 + 8 * t; };   // its last scores are done
+  auto sfull = [&](int t) { return bar0 + 32 + 8 * t; };    // scores are in tensor memory
+  auto sempty = [&](int t) { return bar0 + 48 + 8 * t; };   // ... and in registers
+  auto pfull = [&](int t) { return bar0 + 64 + 8 * t; };    // probabilities in tensor memory
+  auto odone = [&](int t) { return bar0 + 80 + 8 * t; };    // P·V is done
+  auto done = [&](int t) { return bar0 + 96 + 8 * t; };     // every MMA is done
+  auto turn = [&](int t) { return bar0 + 112 + 8 * t; };
+  auto full = [&](int st) { return bar0 + 168 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 168 + 8 * (C::kStages + st); };
+  // The V block of a stage has been looked through, where the mask cuts it.
+  auto clean = [&](int st) { return bar0 + 168 + 8 * (2 * C::kStages + st); };
+  const WorkRing ring = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 128,
+                         smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (blockIdx.x == 0) attn_check_sequences(a);
-  const int h = blockIdx.x % a.Hq;
-  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 8, &b)) return;
-  const int g = h / (a.Hq / a.Hkv);
-  // Key blocks of tile t: top[t] - 1 .. 0 (0: the tile has no rows).
-  const int nblk = (b.len + kTile - 1) / kTile;
-  int top[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int qb = b.row0 / kTile + t;
-    top[t] = qb >= nblk ? 0 : a.causal ? qb + 1 : nblk;
-  }
-  const int n = max(top[0], top[1]);           // blocks of the CTA: n - 1 .. 0
-  // Blocks from `cut` on are cut by the mask for some row.
-  const int cut = a.causal ? b.row0 / kTile : (b.len % kTile ? nblk - 1 : nblk);
-
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 21 + 3 * C::kStages; ++i) mbar_init(bars + i, 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bars + t, 1);                        // qfull
-      mbar_init(bars + 2 + t, 1);                    // sfull
-      mbar_init(bars + 4 + t, 4);                    // sempty
-      mbar_init(bars + 6 + t, 4);                    // pfull
-      mbar_init(bars + 8 + t, 1);                    // odone
-      mbar_init(bars + 10 + t, 1);                   // done
-      mbar_init(bars + 12 + t, 1);                   // vclean
+      mbar_init(bars + 6 + t, 4);                    // sempty, pfull, turn: a tile's warps
+      mbar_init(bars + 8 + t, 4);
+      mbar_init(bars + 14 + t, 4);
+      mbar_init(bars + 18 + t, 4 * NT + NT + 1);     // a slot's readers
     }
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bars + 14 + s, 1);                   // full
-      mbar_init(bars + 14 + C::kStages + s, top[1] ? 2 : 1);   // empty: each tile's MMAs
-    }
-    *vodd = 0;
+    for (int s = 0; s < C::kStages; ++s)
+      mbar_init(bars + 21 + C::kStages + s, NT);     // empty: each tile's MMAs
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(tslot, 512);
+  if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  // The roles of the last warpgroup hand registers to the two that hold a row
-  // of scores: 2·128·208 + 128·88 = 384·168, the launch's own.
+  // The roles of the last warpgroup hand registers to those that hold a row of
+  // scores: 2·208 + 88 = 3·168 and 208 + 48 = 2·128, the launch's own.
   uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-      if (lane == 0) {
-        for (int t = 0; t < 2; ++t)
-          if (top[t]) {
-            mbar_expect_tx(bars + t, C::kTileBytes);
-            for (int x = 0; x < C::kBoxes; ++x)
-              tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
-                          b.start + b.row0 + t * kTile, bars + t);
+  if (warp >= kHelp) {
+    if (NT == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kHelp) {
+      int st = 0, used = 0, nq[2] = {0, 0};
+      uint32_t round = 0;
+      give_work(a, a.Hq, NT == 2 ? 8 : 7, true, ring, limit, [&](const AttnBlock& b, int h) {
+        const FwdWork w = FwdWork::of<NT>(b, a.causal);
+        const int g = h / (a.Hq / a.Hkv);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (w.top[t]) {
+            if (nq[t] > 0) mbar_poll(qempty(t), (nq[t] - 1) & 1, limit);
+            ++nq[t];
+            if (lane == 0) {
+              mbar_expect_tx(bars + t, C::kTileBytes);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(q_sm + t * C::kTileBytes + x * (kTile * 128), &tmQ, 64 * x, h,
+                            b.start + b.row0 + t * kTile, bars + t);
+            }
           }
-        int st = 0;
-        uint32_t round = 0;
-        for (int j = 0; j < n; ++j) {
-          if (j >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+        for (int blk = w.n - 1; blk >= 0; --blk) {
+          if (used >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+          ++used;
           if (limit == 0) break;
-          uint64_t* bar = bars + 14 + st;
-          unsigned char* k_sm = kv_sm + 2 * st * C::kTileBytes;
-          const int row = b.start + (n - 1 - j) * kTile;
-          mbar_expect_tx(bar, 2 * C::kTileBytes);
+          if (lane == 0) {
+            uint64_t* bar = bars + 21 + st;
+            unsigned char* k_sm = kv_sm + 2 * st * C::kTileBytes;
+            const int row = b.start + blk * kTile;
+            mbar_expect_tx(bar, 2 * C::kTileBytes);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+          }
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;
           }
         }
-      }
-      __syncwarp();
-    } else if (warp < 11) {
+      });
+    } else if (warp < kHelp + 1 + NT) {
       // MMAs of one tile.  The whole warp follows the waits (so that the loop
       // stays uniform), one lane of it issues.
-      const int t = warp - 9;
+      const int t = NT == 2 ? warp - kHelp - 1 : 0;
       constexpr uint32_t id_s = idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t id_o = idesc_bf16_f32_bmn(kTile, DP);
       const uint64_t qd = sdesc_k128(q_sm + t * C::kTileBytes), kd = sdesc_k128(kv_sm);
       const uint64_t vd = sdesc_mn128(kv_sm + C::kTileBytes, kTile * 128);
       const uint32_t ts = tmem + C::s(t), tp = tmem + C::p(t), to = tmem + C::o(t);
       constexpr uint64_t kStep = 2 * C::kTileBytes >> 4;       // from stage to stage
-      auto scores = [&](int st) {
+      int st = 0;
+      uint32_t round = 0;                      // parity of the ring's stage st
+      uint32_t c = 0, nq = 0;                  // the tile's blocks and query tiles so far
+      auto advance = [&]() {
+        if (++st == C::kStages) {
+          st = 0;
+          round ^= 1u;
+        }
+      };
+      auto scores = [&](bool last) {
         const uint64_t k0 = kd + st * kStep;
         if (elect_one()) {
 #pragma unroll
@@ -187,39 +203,42 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tc_mma_bf16(ts, qd + at, k0 + at, id_s, k > 0);
           }
           tc_commit(sfull(t));
+          if (last) tc_commit(qempty(t));
         }
         __syncwarp();
       };
-      if (top[t]) {
-        int st = 0;
-        uint32_t round = 0;                    // parity of the ring's stage st
-        if (top[t] < n) {
-          // The first block is the other tile's alone.
-          if (elect_one()) mbar_arrive(empty(0));
-          st = 1;
-        }
-        mbar_poll(qfull(t), 0, limit);
-        mbar_poll(full(st), 0, limit);
-        scores(st);
-        uint32_t par = 0;                      // parity of the tile's block
-        for (int blk = top[t] - 1; blk >= 0; --blk, par ^= 1u) {
+      // A block that only the other tile sees.
+      auto pass_block = [&]() {
+        mbar_poll(full(st), round, limit);
+        if (elect_one()) mbar_arrive(empty(st));
+        __syncwarp();
+        advance();
+      };
+      take_work(ring, limit, [&](const WorkSlot* slot) {
+        const FwdWork w = FwdWork::of<NT>(slot->b, a.causal);
+        const int top = w.top[t];
+        for (int j = top; j < w.n; ++j) pass_block();
+        if (top == 0) return;
+        mbar_poll(qfull(t), nq++ & 1, limit);
+        mbar_poll(full(st), round, limit);
+        if (C::kOwnP && c > 0) mbar_poll(sempty(t), (c - 1) & 1, limit);
+        tc_fence_after();
+        scores(top == 1);
+        for (int blk = top - 1; blk >= 0; --blk, ++c) {
           const uint64_t v0 = vd + st * kStep;
           const uint32_t done_v = empty(st);
-          if (blk >= cut) mbar_poll(vclean(n - 1 - blk), 0, limit);
-          if (++st == C::kStages) {
-            st = 0;
-            round ^= 1u;
-          }
+          if (blk >= w.cut) mbar_poll(clean(st), round, limit);
+          advance();
           if (C::kOwnP && blk > 0) {
             mbar_poll(full(st), round, limit);
-            mbar_poll(sempty(t), par, limit);
+            mbar_poll(sempty(t), c & 1, limit);
             tc_fence_after();
-            scores(st);
+            scores(blk == 1);
           }
-          mbar_poll(pfull(t), par, limit);
+          mbar_poll(pfull(t), c & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            tc_mma_bf16_ts(to, tp, v0, id_o, blk < top[t] - 1);
+            tc_mma_bf16_ts(to, tp, v0, id_o, blk < top - 1);
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k)
               tc_mma_bf16_ts(to, tp + 8 * k, v0 + ((2048 * k) >> 4), id_o, 1);
@@ -230,36 +249,51 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (!C::kOwnP && blk > 0) {
             // P took the place of the scores: the next ones follow its product.
             mbar_poll(full(st), round, limit);
-            scores(st);
+            scores(blk == 1);
           }
         }
-      }
+      });
       if (elect_one()) tc_commit(done(t));
       __syncwarp();
-    } else {
-      // (at most two cut blocks: the first two stages)
-      for (int j = 0; j < n && n - 1 - j >= cut; ++j) {
-        mbar_poll(full(j), 0, limit);
-        if (clean_tile<DP>(kv_sm + (2 * j + 1) * C::kTileBytes, b.len - (n - 1 - j) * kTile) &&
-            lane == 0)
-          *vodd = 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vclean(j));
-      }
+    } else if (warp == kHelp + 3) {
+      int st = 0;
+      uint32_t round = 0;
+      take_work(ring, limit, [&](const WorkSlot* slot) {
+        const FwdWork w = FwdWork::of<NT>(slot->b, a.causal);
+        for (int blk = w.n - 1; blk >= 0; --blk) {
+          mbar_poll(full(st), round, limit);
+          if (blk >= w.cut) {
+            if (clean_tile<DP>(kv_sm + (2 * st + 1) * C::kTileBytes,
+                               slot->b.len - blk * kTile) && lane == 0)
+              const_cast<WorkSlot*>(slot)->odd = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(clean(st));
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
+        }
+      });
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int t = warp >> 2, quad = warp & 3;
-    const int row = b.row0 + t * kTile + 32 * quad + lane;     // within the sequence
+    const int t = NT == 2 ? warp >> 2 : 0, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t ts = tmem + lanes + C::s(t), tp = tmem + lanes + C::p(t);
     const uint32_t to = tmem + lanes + C::o(t);
     const float sc = a.scale * kLog2e;
+    uint32_t nb = 0, nturn = 0;                // the tile's blocks and turns so far
+    take_work(ring, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int h = slot->h, g = h / (a.Hq / a.Hkv);
+    const FwdWork w = FwdWork::of<NT>(b, a.causal);
+    const int row = b.row0 + t * kTile + 32 * quad + lane;     // within the sequence
     float m = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f), k2 = l2;      // row sum, in four parts
-    for (int blk = top[t] - 1, it = 0; blk >= 0; --blk, ++it) {
-      mbar_poll(sfull(t), it & 1, limit);
+    for (int blk = w.top[t] - 1, it = 0; blk >= 0; --blk, ++it, ++nb) {
+      mbar_poll(sfull(t), nb & 1, limit);
       tc_fence_after();
       uint32_t r[kTile];
 #pragma unroll
@@ -270,7 +304,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty(t));
       }
-      if (blk >= cut) {
+      if (blk >= w.cut) {
         // The last key this row sees, within the block.
         const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - blk * kTile;
 #pragma unroll
@@ -305,7 +339,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // tensor core idle while both make probabilities (16 x 16384 tokens:
       // 1614 us, 1735 without turns; at 64, where the next scores are ready
       // ahead, 1272 and 1130).
-      if (!C::kOwnP && (t == 0 ? top[1] > 0 : it > 0)) take_turn(1 + t);
+      if (!C::kOwnP && (t == 0 ? w.top[1] > 0 : it > 0)) mbar_poll(turn(t), nturn++ & 1, limit);
 #pragma unroll
       for (int c0 = 0; c0 < kTile; c0 += 32) {
         uint32_t p[16];
@@ -324,7 +358,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (c0 == 0) {
           if (it > 0) {
             // The product of the block before has read P and written O.
-            mbar_poll(odone(t), (it - 1) & 1, limit);
+            mbar_poll(odone(t), (nb - 1) & 1, limit);
             if (grow) {
               tc_fence_after();
 #pragma unroll 1
@@ -341,15 +375,16 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         tc_st16(tp + c0 / 2, p);
       }
-      if (!C::kOwnP && (t == 0 ? it + 1 < top[1] : it < top[0])) pass_turn(2 - t);
+      if (!C::kOwnP && (t == 0 ? it + 1 < w.top[1] : it < w.top[0]) && lane == 0)
+        mbar_arrive(turn(1 - t));
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pfull(t));
     }
-    if (top[t] > 0) {
+    if (w.top[t] > 0) {
       const float l = (l2.x + l2.y) + (k2.x + k2.y);
-      mbar_poll(odone(t), (top[t] - 1) & 1, limit);
+      mbar_poll(odone(t), (nb - 1) & 1, limit);
       // (rows of a CTA that lost a wait are not written)
       if (__all_sync(0xffffffffu, limit != 0)) {
         tc_fence_after();
@@ -359,7 +394,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                              (tok * a.Hq + h) * (long long)a.dh;
         const bool wide = wide_rows(a.out, (long long)a.Hq * a.dh, a.dh);
-        const bool odd = *reinterpret_cast<volatile uint32_t*>(vodd) != 0;
+        const bool odd = *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0;
 #pragma unroll 1
         for (int c = 0; c < a.dh; c += 16) {
           float o[16];
@@ -367,7 +402,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (odd && live) {
             // What was taken out of the cut blocks of V, for the rows that
             // see it (an infinity or NaN times a positive probability).
-            for (int j = cut * kTile; j < b.len && j < n * kTile; ++j) {
+            for (int j = w.cut * kTile; j < b.len && j < w.n * kTile; ++j) {
               if (a.causal && j > row) break;
               const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
                                        (b.start + (long long)j) * a.ldv + (long long)g * a.dh + c;
@@ -382,44 +417,49 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (live) store16(dst + c, o, inv, a.dh - c, wide);
         }
         if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
+        tc_fence_before();                     // O is read before the next block's products
       }
     }
+    });
   }
   if (limit == 0) report(a.status, 0x711);
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kHelp + 1) {
     // The columns are freed only after every MMA has completed (bounded).
     mbar_poll(done(0), 0, limit);
-    mbar_poll(done(1), 0, limit);
+    if (NT == 2) mbar_poll(done(1), 0, limit);
     if (limit == 0) report(a.status, 0x712);
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
-template <int DP>
+template <int DP, int NT>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
+  using C = FwdCfg<DP, NT>;
   CUtensorMap q, k, v;
   if (!encode_map_heads_sw128(&q, a.q, a.dh, a.Hq, a.T, (unsigned long long)a.ldq * 2, kTile) ||
       !encode_map_heads_sw128(&k, a.k, a.dh, a.Hkv, a.T, (unsigned long long)a.ldk * 2, kTile) ||
       !encode_map_heads_sw128(&v, a.v, a.dh, a.Hkv, a.T, (unsigned long long)a.ldv * 2, kTile))
     return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)(attn_slots(a.T, a.S, 8) * a.Hq);
-  attn_tc_fwd_kernel<DP><<<grid, kFwdThreads, FwdCfg<DP>::kSmem, st>>>(q, k, v, a);
+  const unsigned grid = (unsigned)(attn_slots(a.T, a.S, NT == 2 ? 8 : 7) * a.Hq);
+  attn_tc_fwd_kernel<DP, NT><<<grid, C::kThreads, C::kSmem, st>>>(q, k, v, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t setup_attn_tc() {
-  cudaError_t e = allow_max_smem(attn_tc_fwd_kernel<64>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_tc_fwd_kernel<128>);
+  cudaError_t e = allow_max_smem(attn_tc_fwd_kernel<64, 1>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_fwd_kernel<64, 2>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_fwd_kernel<128, 2>);
   return e;
 }
 
 cudaError_t launch_attn_tc_forward(const AttnArgs& a, cudaStream_t st) {
-  return a.dh <= 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+  if (a.dh > 64) return fwd<128, 2>(a, st);
+  return a.T / a.S < kLongRows ? fwd<64, 1>(a, st) : fwd<64, 2>(a, st);
 }
 
 }  // namespace cat

@@ -100,4 +100,103 @@ __device__ __forceinline__ bool wide_rows(const void* base, long long ld, int dh
   return ((uintptr_t)base & 31) == 0 && ld % 16 == 0 && dh % 16 == 0;
 }
 
+// Work of a persistent CTA.  The grid has one CTA for every slot and head; a
+// CTA that runs takes over CTAs that have not started yet (cluster launch
+// control: the hardware's own queue, no counter in memory that calls or
+// graphs could share), so that the copies and first products of its next
+// block run beside the last ones of this block, and the set-up of a CTA is
+// paid once an SM.  The copy warp finds the blocks and hands them to the other
+// roles through two slots in shared memory.
+struct WorkSlot {
+  AttnBlock b;
+  int h, valid;
+  uint32_t odd;            // a cut block's own rows held values that are not finite
+  int pad;
+};
+
+// Barriers at `bars`: [0, 1] slot filled, [2, 3] slot released, [4] the queue's
+// answer, which lands in `answer` (16 bytes).
+struct WorkRing {
+  WorkSlot* slots;
+  uint32_t bars, answer;
+  __device__ __forceinline__ uint32_t filled(int s) const { return bars + 8 * s; }
+  __device__ __forceinline__ uint32_t released(int s) const { return bars + 16 + 8 * s; }
+  __device__ __forceinline__ uint32_t answered() const { return bars + 32; }
+};
+
+// The copy warp's loop: load(block, head) for each of the CTA's blocks, in
+// slots of 2^shift rows by `heads` heads, the last slots first if `reverse`.
+template <typename F>
+__device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shift, bool reverse,
+                                          const WorkRing& ring, uint32_t& limit, F load) {
+  const int lane = threadIdx.x & 31;
+  int item = blockIdx.x, count = 0;
+  auto publish = [&](const AttnBlock& b, int h, int valid) {
+    const int s = count & 1;
+    if (count >= 2) mbar_poll(ring.released(s), ((count >> 1) - 1) & 1, limit);
+    if (lane == 0) {
+      ring.slots[s].b = b;
+      ring.slots[s].h = h;
+      ring.slots[s].valid = valid;
+      ring.slots[s].odd = 0;
+      mbar_arrive(ring.filled(s));
+    }
+    __syncwarp();
+    ++count;
+  };
+  for (uint32_t par = 0;; par ^= 1u) {
+    if (lane == 0) {
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(ring.answered())
+                   : "memory");
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+          "[%0], [%1];" ::"r"(ring.answer),
+          "r"(ring.answered())
+          : "memory");
+    }
+    const int h = item % heads;
+    int slot = item / heads;
+    if (reverse) slot = (int)(gridDim.x / heads) - 1 - slot;
+    AttnBlock b;
+    if (attn_find_block(a, slot, shift, &b)) {
+      publish(b, h, 1);
+      load(b, h);
+      __syncwarp();
+    }
+    mbar_poll(ring.answered(), par, limit);
+    uint32_t more, next;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(more), "=r"(next)
+        : "r"(ring.answer)
+        : "memory");
+    fence_proxy_async_smem();                // the answer is read before the next one lands
+    __syncwarp();
+    if (!more || __any_sync(0xffffffffu, limit == 0)) break;
+    item = (int)next;
+  }
+  publish(AttnBlock{0, 0, 0, 0}, 0, 0);
+}
+
+// Another role's loop: work(slot) for each of the CTA's blocks.  One arrival
+// a warp gives the slot back.
+template <typename F>
+__device__ __forceinline__ void take_work(const WorkRing& ring, uint32_t& limit, F work) {
+  for (int i = 0;; ++i) {
+    const int s = i & 1;
+    mbar_poll(ring.filled(s), (i >> 1) & 1, limit);
+    if (__any_sync(0xffffffffu, limit == 0)) break;
+    const WorkSlot* w = ring.slots + s;
+    if (!w->valid) break;
+    work(w);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(ring.released(s));
+  }
+}
+
 }  // namespace cat
