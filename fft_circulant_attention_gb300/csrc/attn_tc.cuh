@@ -145,15 +145,6 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
     ++count;
   };
   for (uint32_t par = 0;; par ^= 1u) {
-    if (lane == 0) {
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(ring.answered())
-                   : "memory");
-      asm volatile(
-          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
-          "[%0], [%1];" ::"r"(ring.answer),
-          "r"(ring.answered())
-          : "memory");
-    }
     const int h = item % heads;
     int slot = item / heads;
     if (reverse) slot = (int)(gridDim.x / heads) - 1 - slot;
@@ -162,6 +153,17 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
       publish(b, h, 1);
       load(b, h);
       __syncwarp();
+    }
+    // Asked only now, with this block's copies issued: a block taken over early
+    // would wait here while another SM ran dry.
+    if (lane == 0) {
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(ring.answered())
+                   : "memory");
+      asm volatile(
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+          "[%0], [%1];" ::"r"(ring.answer),
+          "r"(ring.answered())
+          : "memory");
     }
     mbar_poll(ring.answered(), par, limit);
     uint32_t more, next;

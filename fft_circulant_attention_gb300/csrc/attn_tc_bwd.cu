@@ -48,7 +48,7 @@ namespace {
 constexpr int kBwdThreads = 384;
 constexpr int kHalf = kTile / 2;           // columns of a block that a row's thread takes
 constexpr int kStatBytes = 2 * kTile * 4;
-constexpr int kNumBars = 32;
+constexpr int kNumBars = 32;               // room for every barrier
 
 template <int DP>
 struct DkvCfg {
@@ -57,7 +57,7 @@ struct DkvCfg {
   static constexpr int kStages = DP == 64 ? 4 : 2;
   static constexpr int kStageBytes = 2 * kTileBytes + kStatBytes;    // Q, dO, lse and delta
   static constexpr size_t kSmem =
-      1024 + 2 * kTileBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 16;
+      1024 + 2 * kTileBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 96;
   static constexpr int kSBufs = DP == 64 ? 2 : 1;
   // Tensor-memory columns.
   static constexpr int s(int b) { return kTile * b; }
@@ -71,7 +71,7 @@ struct DqCfg {
   static constexpr int kStages = DP == 64 ? 5 : 2;
   static constexpr int kStageBytes = 2 * kTileBytes;                  // K, V
   static constexpr size_t kSmem =
-      1024 + 2 * kTileBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 16;
+      1024 + 2 * kTileBytes + 2 * kStatBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 96;
   static constexpr int s(int b) { return kTile * b; }
   static constexpr int kDp = 2 * kTile, kDq = 3 * kTile;
 };
@@ -175,6 +175,21 @@ attn_stats_kernel(const AttnArgs a, int slots) {
   }
 }
 
+// What a block of 128 keys means for dK and dV.
+struct DkvWork {
+  int nqb, qb0;            // query blocks qb0 .. nqb - 1 of every head see it
+  int diag, last;          // those that the mask cuts (-1: none)
+  static __device__ __forceinline__ DkvWork of(const AttnBlock& b, int causal) {
+    DkvWork w;
+    w.nqb = (b.len + kTile - 1) / kTile;
+    w.diag = causal ? b.row0 / kTile : -1;
+    w.qb0 = causal ? w.diag : 0;
+    w.last = b.len % kTile ? w.nqb - 1 : -1;
+    return w;
+  }
+  __device__ __forceinline__ bool is_cut(int qb) const { return qb == diag || qb == last; }
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -189,32 +204,23 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   unsigned char* stat = ring + C::kStages * 2 * C::kTileBytes; // [kStages] lse, delta
   uint64_t* bars = reinterpret_cast<uint64_t*>(stat + C::kStages * kStatBytes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  uint32_t* godd = tslot + 1;                // a cut block's own rows of dO held odd values
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t kvfull = bar0, dpfull = bar0 + 8, dsready = bar0 + 16, dkdone = bar0 + 24;
   const uint32_t clean = bar0 + 32, done = bar0 + 40;
   auto sfull = [&](int i) { return bar0 + 48 + 8 * i; };
   auto pready = [&](int i) { return bar0 + 64 + 8 * i; };
   auto dvdone = [&](int i) { return bar0 + 80 + 8 * i; };
-  auto full = [&](int st) { return bar0 + 96 + 8 * st; };
-  auto empty = [&](int st) { return bar0 + 96 + 8 * (C::kStages + st); };
-  const uint32_t cutgo = bar0 + 8 * (kNumBars - 1);
+  const uint32_t cutgo = bar0 + 96, kvempty = bar0 + 104;
+  auto full = [&](int st) { return bar0 + 152 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 152 + 8 * (C::kStages + st); };
+  const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 112,
+                           smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const int g = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 7, &b)) return;
   const int rep = a.Hq / a.Hkv;
-  const int kb = b.row0 / kTile, nqb = (b.len + kTile - 1) / kTile;
-  const int qb0 = a.causal ? kb : 0;
-  const int per = nqb - qb0;                 // query blocks of each head
-  const int n = rep * per;
-  const bool ragged = b.len % kTile != 0;    // the last query block is cut
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 8 : 1);      // dsready, pready: 8 warps
-    *godd = 0;
+    for (int i = 0; i < kNumBars; ++i)       // dsready, pready: 8 warps; a slot's readers
+      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 8 : i == 16 || i == 17 ? 11 : 1);
     mbar_fence_init();
   }
   if (warp == 9) tmem_alloc(tslot, 512);
@@ -227,139 +233,168 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      if (lane == 0) {
-        mbar_expect_tx(bars, 2 * C::kTileBytes);
-        for (int x = 0; x < C::kBoxes; ++x) {
-          tma_load_3d(kv_sm + x * (kTile * 128), &tmK, 64 * x, g, b.start + b.row0, bars);
-          tma_load_3d(kv_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g,
-                      b.start + b.row0, bars);
+      int st = 0, used = 0, items = 0;
+      uint32_t round = 0;
+      give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock& b, int g) {
+        const DkvWork w = DkvWork::of(b, a.causal);
+        if (items > 0) mbar_poll(kvempty, (items - 1) & 1, limit);
+        ++items;
+        if (lane == 0) {
+          mbar_expect_tx(bars, 2 * C::kTileBytes);
+          for (int x = 0; x < C::kBoxes; ++x) {
+            tma_load_3d(kv_sm + x * (kTile * 128), &tmK, 64 * x, g, b.start + b.row0, bars);
+            tma_load_3d(kv_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g,
+                        b.start + b.row0, bars);
+          }
         }
-        int st = 0, qb = qb0, h = g * rep;
-        uint32_t round = 0;
         const int slot0 = (b.start >> 7) + b.seq;
-        for (int j = 0; j < n; ++j) {
-          if (j >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
-          if (limit == 0) break;
-          uint64_t* bar = bars + 12 + st;
-          unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
-          const int row = b.start + qb * kTile;
-          mbar_expect_tx(bar, 2 * C::kTileBytes + kStatBytes);
+        for (int h = g * rep; h < (g + 1) * rep; ++h)
+          for (int qb = w.qb0; qb < w.nqb; ++qb) {
+            if (used >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+            ++used;
+            if (limit == 0) return;
+            if (lane == 0) {
+              uint64_t* bar = bars + 19 + st;
+              unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
+              const int row = b.start + qb * kTile;
+              mbar_expect_tx(bar, 2 * C::kTileBytes + kStatBytes);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, row, bar);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, row, bar);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h, row, bar);
-          bulk_g2s(stat + st * kStatBytes,
-                   a.stats + ((long long)h * slots + slot0 + qb) * (2 * kTile), kStatBytes, bar);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h, row, bar);
+              bulk_g2s(stat + st * kStatBytes,
+                       a.stats + ((long long)h * slots + slot0 + qb) * (2 * kTile), kStatBytes,
+                       bar);
+            }
+            if (++st == C::kStages) {
+              st = 0;
+              round ^= 1u;
+            }
+          }
+      });
+    } else if (warp == 9) {
+      const uint64_t kd = sdesc_k128(kv_sm), vd = sdesc_k128(kv_sm + C::kTileBytes);
+      const uint64_t qd = sdesc_k128(ring), gd = sdesc_k128(ring + C::kTileBytes);
+      int st = 0, sb = 0, items = 0;
+      uint32_t round = 0, sround = 0, c = 0;
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        mbar_poll(kvfull, items++ & 1, limit);
+        const int n = rep * (w.nqb - w.qb0);
+        int qb = w.qb0;
+        for (int j = 0; j < n; ++j, ++c) {
+          const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
+          mbar_poll(full(st), round, limit);
+          // S's buffer is free once the dV product has read P from it.
+          if (c >= (uint32_t)C::kSBufs) mbar_poll(dvdone(sb), sround ^ 1u, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_kk<DP>(tmem + C::s(sb), kd, qd + at);
+            tc_commit(sfull(sb));
+          }
+          __syncwarp();
+          // dP's columns are free once the dK product has read dS from them.
+          if (c >= 1) mbar_poll(dkdone, (c - 1) & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_kk<DP>(tmem + C::kDp, vd, gd + at);
+            tc_commit(dpfull);
+            // A cut block has served as it came: it can be cleaned.
+            if (w.is_cut(qb)) tc_commit(cutgo);
+            if (j == n - 1) tc_commit(kvempty);
+          }
+          __syncwarp();
+          if (++qb == w.nqb) qb = w.qb0;
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;
           }
-          if (++qb == nqb) {
-            qb = qb0;
-            ++h;
+          if (++sb == C::kSBufs) {
+            sb = 0;
+            sround ^= 1u;
           }
         }
-      }
-      __syncwarp();
-    } else if (warp == 9) {
-      const uint64_t kd = sdesc_k128(kv_sm), vd = sdesc_k128(kv_sm + C::kTileBytes);
-      const uint64_t qd = sdesc_k128(ring), gd = sdesc_k128(ring + C::kTileBytes);
-      int st = 0, sb = 0, qb = qb0;
-      uint32_t round = 0, sround = 0;
-      mbar_poll(kvfull, 0, limit);
-      for (int j = 0; j < n; ++j) {
-        const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
-        mbar_poll(full(st), round, limit);
-        // S's buffer is free once the dV product has read P from it.
-        if (j >= C::kSBufs) mbar_poll(dvdone(sb), sround ^ 1u, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_kk<DP>(tmem + C::s(sb), kd, qd + at);
-          tc_commit(sfull(sb));
-        }
-        __syncwarp();
-        // dP's columns are free once the dK product has read dS from them.
-        if (j >= 1) mbar_poll(dkdone, (j - 1) & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_kk<DP>(tmem + C::kDp, vd, gd + at);
-          tc_commit(dpfull);
-          // A cut block has served as it came: it can be cleaned.
-          if ((a.causal && qb == kb) || (ragged && qb == nqb - 1)) tc_commit(cutgo);
-        }
-        __syncwarp();
-        if (++qb == nqb) qb = qb0;
-        if (++st == C::kStages) {
-          st = 0;
-          round ^= 1u;
-        }
-        if (++sb == C::kSBufs) {
-          sb = 0;
-          sround ^= 1u;
-        }
-      }
+      });
     } else if (warp == 10) {
       const uint64_t qd = sdesc_mn128(ring, kTile * 128);
       const uint64_t gd = sdesc_mn128(ring + C::kTileBytes, kTile * 128);
-      int st = 0, sb = 0, qb = qb0;
-      uint32_t ncut = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
-        if ((a.causal && qb == kb) || (ragged && qb == nqb - 1)) mbar_poll(clean, ncut++ & 1, limit);
-        mbar_poll(pready(j & 1), (j >> 1) & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_tn<DP>(tmem + C::kDv, tmem + C::s(sb), gd + at, j > 0);
-          tc_commit(dvdone(sb));
+      int st = 0, sb = 0;
+      uint32_t ncut = 0, c = 0;
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        const int n = rep * (w.nqb - w.qb0);
+        int qb = w.qb0;
+        for (int j = 0; j < n; ++j, ++c) {
+          const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
+          if (w.is_cut(qb)) mbar_poll(clean, ncut++ & 1, limit);
+          // (the first of a block: both warpgroups have read the last one's dV, dK)
+          mbar_poll(pready(c & 1), (c >> 1) & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tn<DP>(tmem + C::kDv, tmem + C::s(sb), gd + at, j > 0);
+            tc_commit(dvdone(sb));
+          }
+          __syncwarp();
+          mbar_poll(dsready, c & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tn<DP>(tmem + C::kDk, tmem + C::kDp, qd + at, j > 0);
+            mma_tn<DP>(tmem + C::kDk, tmem + C::kDp + kHalf / 2, qd + at, 1);
+            tc_commit(dkdone);
+            tc_commit(empty(st));
+          }
+          __syncwarp();
+          if (++st == C::kStages) st = 0;
+          if (++sb == C::kSBufs) sb = 0;
+          if (++qb == w.nqb) qb = w.qb0;
         }
-        __syncwarp();
-        mbar_poll(dsready, j & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_tn<DP>(tmem + C::kDk, tmem + C::kDp, qd + at, j > 0);
-          mma_tn<DP>(tmem + C::kDk, tmem + C::kDp + kHalf / 2, qd + at, 1);
-          tc_commit(dkdone);
-          tc_commit(empty(st));
-        }
-        __syncwarp();
-        if (++st == C::kStages) st = 0;
-        if (++sb == C::kSBufs) sb = 0;
-        if (++qb == nqb) qb = qb0;
-      }
+      });
       if (elect_one()) tc_commit(done);
       __syncwarp();
     } else {
       // (the next cut block waits for the products of this one, so the phases
       // of cutgo and clean are taken one by one)
-      int st = 0, qb = qb0;
+      int st = 0;
       uint32_t ncut = 0;
-      for (int j = 0; j < n; ++j) {
-        if ((a.causal && qb == kb) || (ragged && qb == nqb - 1)) {
-          mbar_poll(cutgo, ncut++ & 1, limit);
-          unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
-          const int rows = b.len - qb * kTile;
-          clean_tile<DP>(q_sm, rows);
-          if (clean_tile<DP>(q_sm + C::kTileBytes, rows) && lane == 0) *godd = 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(clean);
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        const int n = rep * (w.nqb - w.qb0);
+        int qb = w.qb0;
+        for (int j = 0; j < n; ++j) {
+          if (w.is_cut(qb)) {
+            mbar_poll(cutgo, ncut++ & 1, limit);
+            unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
+            const int rows = slot->b.len - qb * kTile;
+            clean_tile<DP>(q_sm, rows);
+            if (clean_tile<DP>(q_sm + C::kTileBytes, rows) && lane == 0)
+              const_cast<WorkSlot*>(slot)->odd = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(clean);
+          }
+          if (++st == C::kStages) st = 0;
+          if (++qb == w.nqb) qb = w.qb0;
         }
-        if (++st == C::kStages) st = 0;
-        if (++qb == nqb) qb = qb0;
-      }
+      });
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int half = warp >> 2, quad = warp & 3;
-    const int key = b.row0 + 32 * quad + lane;                 // within the sequence
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const float sc = a.scale * kLog2e;
     const float2 sc2 = make_float2(sc, sc);
-    int st = 0, sb = 0, qb = qb0;
-    uint32_t round = 0, sround = 0;
-    for (int j = 0; j < n; ++j) {
+    int st = 0, sb = 0;
+    uint32_t round = 0, sround = 0, nb = 0;
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int g = slot->h;
+    const DkvWork w = DkvWork::of(b, a.causal);
+    const int key = b.row0 + 32 * quad + lane;                 // within the sequence
+    const int n = rep * (w.nqb - w.qb0);
+    int qb = w.qb0;
+    for (int j = 0; j < n; ++j, ++nb) {
       const uint32_t ts = tmem + lanes + C::s(sb) + half * kHalf;
       const uint32_t tdp = tmem + lanes + C::kDp + half * kHalf;
       const float4* lse = reinterpret_cast<const float4*>(stat + st * kStatBytes) + half * 16;
@@ -385,7 +420,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         p[c + 3] = ex2(y.y);
       }
       // Columns lo .. hi - 1 of the half are queries that see this key.
-      const bool cut = (a.causal && qb == kb) || (ragged && qb == nqb - 1);
+      const bool cut = w.is_cut(qb);
       const int q0 = qb * kTile + half * kHalf;
       const int lo = a.causal ? key - q0 : 0, hi = b.len - q0;
       if (cut) {
@@ -396,8 +431,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       store_half(ts, p);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pready(j & 1));
-      mbar_poll(dpfull, j & 1, limit);
+      if (lane == 0) mbar_arrive(pready(nb & 1));
+      mbar_poll(dpfull, nb & 1, limit);
       tc_fence_after();
       tc_ld32(tdp, r);
       tc_ld32(tdp + 32, r + 32);
@@ -432,9 +467,9 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         sb = 0;
         sround ^= 1u;
       }
-      if (++qb == nqb) qb = qb0;
+      if (++qb == w.nqb) qb = w.qb0;
     }
-    mbar_poll(done, 0, limit);
+    mbar_poll(dkdone, (nb - 1) & 1, limit);    // the block's last product
     // (rows of a CTA that lost a wait are not written)
     if (__all_sync(0xffffffffu, limit != 0)) {
       tc_fence_after();
@@ -445,13 +480,12 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             static_cast<__nv_bfloat16*>(a.dv) + tok * a.lddv + (long long)g * a.dh;
         store_row(tmem + lanes + C::kDv, dv, 0, a.dh, 1.f, live,
                   wide_rows(a.dv, a.lddv, a.dh));
-        if (*reinterpret_cast<volatile uint32_t*>(godd) != 0 && live) {
+        if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0 && live) {
           // What was taken out of the cut blocks of dO, for the keys that its
           // rows see (an infinity or NaN times a positive probability).
           for (int h = g * rep; h < (g + 1) * rep; ++h)
-            for (int i = a.causal ? key : (nqb - 1) * kTile; i < b.len; ++i) {
-              const int ib = i / kTile;
-              if (!(a.causal && ib == kb) && !(ragged && ib == nqb - 1)) continue;
+            for (int i = a.causal ? key : (w.nqb - 1) * kTile; i < b.len; ++i) {
+              if (!w.is_cut(i / kTile)) continue;
               const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.dO) +
                                         (((long long)b.start + i) * a.Hq + h) * a.dh;
               for (int c = 0; c < a.dh; ++c) {
@@ -466,7 +500,9 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         store_row(tmem + lanes + C::kDk, dk, 0, a.dh, a.scale, live,
                   wide_rows(a.dk, a.lddk, a.dh));
       }
+      tc_fence_before();                       // read before the next block's products
     }
+    });
   }
   if (limit == 0) report(a.status, 0x721);
   tc_fence_before();
@@ -491,28 +527,33 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   unsigned char* sm = dq_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* q_sm = sm;                                    // Q, dO
   unsigned char* ring = sm + 2 * C::kTileBytes;                // [kStages] K, V
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::kStages * C::kStageBytes);
+  float* stat = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);  // [2] lse, delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 2 * 2 * kTile);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
-  const uint32_t qfull = bar0, dpfull = bar0 + 8, dsready = bar0 + 16, dqdone = bar0 + 24;
-  const uint32_t clean = bar0 + 32, done = bar0 + 40;
+  const uint32_t dpfull = bar0 + 8, dsready = bar0 + 16, dqdone = bar0 + 24;
+  const uint32_t qempty = bar0 + 32, done = bar0 + 40;
+  // Q, dO, lse and delta have landed (two barriers in turn: the warpgroups may
+  // come to a block's after the next block's are there).
+  constexpr int kQ1 = 17 + 2 * C::kStages;
+  auto qfull = [&](int i) { return bar0 + 8 * (i & 1 ? kQ1 : 0); };
   auto sfull = [&](int i) { return bar0 + 48 + 8 * i; };
-  auto full = [&](int st) { return bar0 + 64 + 8 * st; };
-  auto empty = [&](int st) { return bar0 + 64 + 8 * (C::kStages + st); };
+  auto cutgo = [&](int i) { return bar0 + 64 + 8 * i; };
+  auto clean = [&](int i) { return bar0 + 80 + 8 * i; };
+  auto full = [&](int st) { return bar0 + 136 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 136 + 8 * (C::kStages + st); };
+  const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 96,
+                           smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const int h = blockIdx.x % a.Hq;
-  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 7, &b)) return;
-  const int g = h / (a.Hq / a.Hkv);
-  const int qb = b.row0 / kTile;
   // Key blocks n - 1 .. 0; only the first of them can be cut by the mask.
-  const int n = a.causal ? qb + 1 : (b.len + kTile - 1) / kTile;
-  const bool cut0 = a.causal || b.len % kTile != 0;
+  auto blocks = [&](const AttnBlock& b) {
+    return a.causal ? b.row0 / kTile + 1 : (b.len + kTile - 1) / kTile;
+  };
+  auto is_cut = [&](const AttnBlock& b) { return a.causal || b.len % kTile != 0; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bars + i, i == 2 ? 8 : 1);   // dsready: 8 warps
+    for (int i = 0; i < kNumBars; ++i)       // dsready: 8 warps; a slot's readers
+      mbar_init(bars + i, i == 2 ? 8 : i == 14 || i == 15 ? 11 : 1);
     mbar_fence_init();
   }
   if (warp == 9) tmem_alloc(tslot, 512);
@@ -525,104 +566,151 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      if (lane == 0) {
-        mbar_expect_tx(bars, 2 * C::kTileBytes);
-        for (int x = 0; x < C::kBoxes; ++x) {
-          tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, b.start + b.row0, bars);
-          tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h,
-                      b.start + b.row0, bars);
+      int st = 0, used = 0, items = 0;
+      uint32_t round = 0;
+      give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock& b, int h) {
+        const int g = h / (a.Hq / a.Hkv);
+        if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+        if (lane == 0) {
+          uint64_t* bar = bars + (items & 1 ? kQ1 : 0);
+          mbar_expect_tx(bar, 2 * C::kTileBytes + kStatBytes);
+          for (int x = 0; x < C::kBoxes; ++x) {
+            tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, b.start + b.row0, bar);
+            tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h,
+                        b.start + b.row0, bar);
+          }
+          // (its buffer's last reader has given back the slot of two blocks ago)
+          const int slot = (b.start >> 7) + b.seq + b.row0 / kTile;
+          bulk_g2s(stat + (items & 1) * 2 * kTile,
+                   a.stats + ((long long)h * slots + slot) * (2 * kTile), kStatBytes, bar);
         }
-        int st = 0;
-        uint32_t round = 0;
-        for (int j = 0; j < n; ++j) {
-          if (j >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+        ++items;
+        for (int blk = blocks(b) - 1; blk >= 0; --blk) {
+          if (used >= C::kStages) mbar_poll(empty(st), round ^ 1u, limit);
+          ++used;
           if (limit == 0) break;
-          uint64_t* bar = bars + 8 + st;
-          unsigned char* k_sm = ring + st * C::kStageBytes;
-          const int row = b.start + (n - 1 - j) * kTile;
-          mbar_expect_tx(bar, C::kStageBytes);
+          if (lane == 0) {
+            uint64_t* bar = bars + 17 + st;
+            unsigned char* k_sm = ring + st * C::kStageBytes;
+            const int row = b.start + blk * kTile;
+            mbar_expect_tx(bar, C::kStageBytes);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+          }
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;
           }
         }
-      }
-      __syncwarp();
+      });
     } else if (warp == 9) {
       const uint64_t qd = sdesc_k128(q_sm), gd = sdesc_k128(q_sm + C::kTileBytes);
       const uint64_t kd = sdesc_k128(ring), vd = sdesc_k128(ring + C::kTileBytes);
-      int st = 0;
-      uint32_t round = 0;
-      mbar_poll(qfull, 0, limit);
-      for (int j = 0; j < n; ++j) {
-        const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
-        mbar_poll(full(st), round, limit);
-        // (S's buffer was read before dS of two blocks ago was ready, which the
-        // wait below for the product of that dS has shown.)
-        if (elect_one()) {
-          mma_kk<DP>(tmem + C::s(j & 1), qd, kd + at);
-          tc_commit(sfull(j & 1));
+      int st = 0, items = 0;
+      uint32_t round = 0, c = 0, ncut = 0;
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const int n = blocks(slot->b);
+        const bool cut = is_cut(slot->b);
+        mbar_poll(qfull(items), (items >> 1) & 1, limit);
+        ++items;
+        for (int j = 0; j < n; ++j, ++c) {
+          const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
+          mbar_poll(full(st), round, limit);
+          // (S's buffer was read before dS of two blocks ago was ready, which the
+          // wait below for the product of that dS has shown.)
+          if (elect_one()) {
+            mma_kk<DP>(tmem + C::s(c & 1), qd, kd + at);
+            tc_commit(sfull(c & 1));
+            // K of a cut block has served as it came: it can be cleaned.
+            if (j == 0 && cut) tc_commit(cutgo(ncut & 1));
+          }
+          __syncwarp();
+          if (j == 0 && cut) ++ncut;
+          // dP's columns are free once the dQ product has read dS from them.
+          if (c >= 1) mbar_poll(dqdone, (c - 1) & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_kk<DP>(tmem + C::kDp, gd, vd + at);
+            tc_commit(dpfull);
+            if (j == n - 1) tc_commit(qempty);
+          }
+          __syncwarp();
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
         }
-        __syncwarp();
-        // dP's columns are free once the dQ product has read dS from them.
-        if (j >= 1) mbar_poll(dqdone, (j - 1) & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_kk<DP>(tmem + C::kDp, gd, vd + at);
-          tc_commit(dpfull);
-        }
-        __syncwarp();
-        if (++st == C::kStages) {
-          st = 0;
-          round ^= 1u;
-        }
-      }
+      });
     } else if (warp == 10) {
       const uint64_t kd = sdesc_mn128(ring, kTile * 128);
       int st = 0;
-      if (cut0) mbar_poll(clean, 0, limit);
-      for (int j = 0; j < n; ++j) {
-        const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
-        mbar_poll(dsready, j & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_tn<DP>(tmem + C::kDq, tmem + C::kDp, kd + at, j > 0);
-          mma_tn<DP>(tmem + C::kDq, tmem + C::kDp + kHalf / 2, kd + at, 1);
-          tc_commit(dqdone);
-          tc_commit(empty(st));
+      uint32_t c = 0, ncut = 0;
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const int n = blocks(slot->b);
+        if (is_cut(slot->b)) {
+          mbar_poll(clean(ncut & 1), (ncut >> 1) & 1, limit);
+          ++ncut;
         }
-        __syncwarp();
-        if (++st == C::kStages) st = 0;
-      }
+        for (int j = 0; j < n; ++j, ++c) {
+          const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
+          // (the first of a block: both warpgroups have read the last one's dQ)
+          mbar_poll(dsready, c & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tn<DP>(tmem + C::kDq, tmem + C::kDp, kd + at, j > 0);
+            mma_tn<DP>(tmem + C::kDq, tmem + C::kDp + kHalf / 2, kd + at, 1);
+            tc_commit(dqdone);
+            tc_commit(empty(st));
+          }
+          __syncwarp();
+          if (++st == C::kStages) st = 0;
+        }
+      });
       if (elect_one()) tc_commit(done);
       __syncwarp();
-    } else if (cut0) {
-      mbar_poll(sfull(0), 0, limit);           // S has been computed from the block as it came
-      clean_tile<DP>(ring, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(clean);
+    } else {
+      // A cut block's scores may be there before the one before is cleaned, but
+      // not those of the block after it: two barriers in turn.
+      int first = 0;
+      uint32_t ncut = 0;
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        if (is_cut(slot->b)) {
+          mbar_poll(cutgo(ncut & 1), (ncut >> 1) & 1, limit);
+          clean_tile<DP>(ring + first * C::kStageBytes, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(clean(ncut & 1));
+          ++ncut;
+        }
+        first = (first + blocks(slot->b)) % C::kStages;
+      });
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int half = warp >> 2, quad = warp & 3;
-    const int lrow = 32 * quad + lane, row = b.row0 + lrow;    // within tile and sequence
+    const int lrow = 32 * quad + lane;                         // within the tile
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t tdp = tmem + lanes + C::kDp + half * kHalf;
     const float sc = a.scale * kLog2e;
-    const float* stats = a.stats + ((long long)h * slots + slot) * (2 * kTile) + lrow;
-    const float lse = stats[0], del = stats[kTile];
-    const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(-lse, -lse);
-    const float2 nd2 = make_float2(-del, -del);
-    for (int j = 0; j < n; ++j) {
-      const uint32_t ts = tmem + lanes + C::s(j & 1) + half * kHalf;
-      mbar_poll(sfull(j & 1), (j >> 1) & 1, limit);
+    const float2 sc2 = make_float2(sc, sc);
+    uint32_t nb = 0, items = 0;
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int h = slot->h, n = blocks(b);
+    const bool cut0 = is_cut(b);
+    const int row = b.row0 + lrow;                             // within the sequence
+    mbar_poll(qfull(items), (items >> 1) & 1, limit);
+    const float lse = stat[(items & 1) * 2 * kTile + lrow];
+    const float del = stat[(items & 1) * 2 * kTile + kTile + lrow];
+    ++items;
+    const float2 nl2 = make_float2(-lse, -lse), nd2 = make_float2(-del, -del);
+    for (int j = 0; j < n; ++j, ++nb) {
+      const uint32_t ts = tmem + lanes + C::s(nb & 1) + half * kHalf;
+      mbar_poll(sfull(nb & 1), (nb >> 1) & 1, limit);
       tc_fence_after();
       uint32_t r[kHalf];
       tc_ld32(ts, r);
@@ -636,7 +724,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         p[c] = ex2(x.x);
         p[c + 1] = ex2(x.y);
       }
-      mbar_poll(dpfull, j & 1, limit);
+      mbar_poll(dpfull, nb & 1, limit);
       tc_fence_after();
       tc_ld32(tdp, r);
       tc_ld32(tdp + 32, r + 32);
@@ -661,7 +749,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(dsready);
     }
-    mbar_poll(done, 0, limit);
+    mbar_poll(dqdone, (nb - 1) & 1, limit);    // the block's last product
     // (rows of a CTA that lost a wait are not written)
     if (__all_sync(0xffffffffu, limit != 0)) {
       tc_fence_after();
@@ -670,7 +758,9 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int c0 = half * (DP / 2);
       store_row(tmem + lanes + C::kDq, dst, c0, min(a.dh, c0 + DP / 2), a.scale, row < b.len,
                 wide_rows(a.dq, a.lddq, a.dh));
+      tc_fence_before();                       // read before the next block's products
     }
+    });
   }
   if (limit == 0) report(a.status, 0x731);
   tc_fence_before();
