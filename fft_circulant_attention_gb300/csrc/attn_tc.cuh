@@ -47,13 +47,13 @@ __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
   return w & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
 }
 
-// A [kTile][DP] tile in shared memory, by one warp: values that are not
+// A [ROWS][DP] tile in shared memory, by one warp: values that are not
 // finite become zero.  True if one of them lay in a row below `rows`.  The
 // first pass only looks (9 operations per 8 values: about 0.3 us a tile of 64
 // columns, hidden behind the block's scores).
-template <int DP>
+template <int DP, int ROWS = kTile>
 __device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
-  constexpr int kVec = kTile * DP * 2 / 16;
+  constexpr int kVec = ROWS * DP * 2 / 16;
   uint4* v = reinterpret_cast<uint4*>(tile);
   uint32_t any = 0;
 #pragma unroll 16
@@ -67,8 +67,8 @@ __device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
   for (int i = threadIdx.x & 31; i < kVec; i += 32) {
     const uint4 x = v[i];
     if (((odd2(x.x) | odd2(x.y) | odd2(x.z) | odd2(x.w)) & 0x80008000u) != 0) {
-      // 8 pieces a row, kTile rows a box of 64 columns.
-      if ((i / 8) % kTile < rows) found = true;
+      // 8 pieces a row, ROWS rows a box of 64 columns.
+      if ((i / 8) % ROWS < rows) found = true;
       v[i] = make_uint4(drop_odd(x.x), drop_odd(x.y), drop_odd(x.z), drop_odd(x.w));
     }
   }

@@ -14,16 +14,22 @@
 // atomics: results repeat bit for bit, and neither kernel's accumulators
 // leave tensor memory.
 //
-// Roles of a CTA (384 threads, one CTA an SM):
-//   - warps 0-7, two warpgroups, one thread a row, each with 64 of a block's
-//     128 columns: scores and dP from tensor memory, P and dS back to tensor
-//     memory as bf16 pairs, in the columns of its own half;
-//   - warp 8: tensor copies;  warp 9: the MMAs S and dP;  warp 10: the MMAs
-//     whose A operand is P or dS (accumulators dV, dK or dQ);
-//   - warp 11: values that are not finite in blocks that the mask cuts.
-// P takes the place of S, dS that of dP.  S has two buffers where 512
-// columns allow it (always for dQ; for dK and dV at head width 64), so the
+// Roles of a CTA:
+//   - one or two warpgroups, one thread a row, each with 64 columns of a
+//     block: scores and dP from tensor memory, P and dS back to tensor memory
+//     as bf16 pairs, in the columns of its own half;
+//   - four warps more: tensor copies;  the MMAs S and dP;  the MMAs whose A
+//     operand is P or dS (accumulators dV, dK or dQ);  values that are not
+//     finite in blocks that the mask cuts.
+// P takes the place of S, dS that of dP; dQ's S has two buffers, so that the
 // next scores are computed while this block's probabilities are made.
+//
+// At head width 64 a CTA has one warpgroup of rows, works on blocks of 64 of
+// the other side and takes half of the 512 columns, so that two CTAs share an
+// SM and one's chain of waits runs beside the other's (12 heads, 16 documents
+// up to 1024 tokens: dK and dV 56.5 us with one CTA of two warpgroups, 54.4
+// with two; dQ 41.4 and 37.7; 8192 tokens: 212 and 204, 193 and 165).  At 128
+// the accumulators fill the columns: two warpgroups, blocks of 128.
 //
 // P is rounded to bf16 (half a step 2^-8 of each value) as an MMA operand, dS
 // to two bf16 terms whose sum is within 2^-16: a row of dS sums to zero, and
@@ -45,54 +51,61 @@ namespace cat {
 
 namespace {
 
-constexpr int kBwdThreads = 384;
-constexpr int kHalf = kTile / 2;           // columns of a block that a row's thread takes
-constexpr int kStatBytes = 2 * kTile * 4;
+constexpr int kHalf = 64;                  // columns of a block that a row's thread takes
 constexpr int kNumBars = 32;               // room for every barrier
 
-template <int DP>
-struct DkvCfg {
-  static constexpr int kBoxes = DP / 64;
-  static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = DP == 64 ? 4 : 2;
-  static constexpr int kStageBytes = 2 * kTileBytes + kStatBytes;    // Q, dO, lse and delta
-  static constexpr size_t kSmem =
-      1024 + 2 * kTileBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 96;
-  static constexpr int kSBufs = DP == 64 ? 2 : 1;
-  // Tensor-memory columns.
-  static constexpr int s(int b) { return kTile * b; }
-  static constexpr int kDp = kTile * kSBufs, kDv = kDp + kTile, kDk = kDv + DP;
+// NH: warpgroups of a CTA, and blocks of 64·NH on the other side.
+template <int NH>
+struct Shape {
+  static constexpr int kW = kHalf * NH;                  // rows of a block
+  static constexpr int kThreads = 128 * (NH + 1);
+  static constexpr int kHelp = 4 * NH;                   // first warp of the other roles
+  static constexpr int kCols = 256 * NH;                 // tensor-memory columns
+  static constexpr int kStatBytes = 2 * kW * 4;          // lse and delta of a block
 };
 
-template <int DP>
-struct DqCfg {
+template <int DP, int NH>
+struct DkvCfg : Shape<NH> {
+  using S = Shape<NH>;
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kTile * DP * 2;
-  static constexpr int kStages = DP == 64 ? 5 : 2;
-  static constexpr int kStageBytes = 2 * kTileBytes;                  // K, V
+  static constexpr int kBlkBytes = S::kW * DP * 2;
+  static constexpr int kStages = DP == 64 ? 4 : 2;       // Q, dO, lse and delta
   static constexpr size_t kSmem =
-      1024 + 2 * kTileBytes + 2 * kStatBytes + (size_t)kStages * kStageBytes + kNumBars * 8 + 96;
-  static constexpr int s(int b) { return kTile * b; }
-  static constexpr int kDp = 2 * kTile, kDq = 3 * kTile;
+      1024 + 2 * kTileBytes + (size_t)kStages * (2 * kBlkBytes + S::kStatBytes) + kNumBars * 8 + 96;
+  // Tensor-memory columns, after those of S.
+  static constexpr int kDp = S::kW, kDv = kDp + S::kW, kDk = kDv + DP;
 };
 
-// A product of two K-major tiles: D[128 x 128] = A·B^T over DP columns.
-template <int DP>
+template <int DP, int NH>
+struct DqCfg : Shape<NH> {
+  using S = Shape<NH>;
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kTileBytes = kTile * DP * 2;
+  static constexpr int kBlkBytes = S::kW * DP * 2;
+  static constexpr int kStages = DP == 64 ? 4 : 2;       // K, V
+  static constexpr size_t kSmem = 1024 + 2 * kTileBytes + 2 * (2 * kTile * 4) +
+                                  (size_t)kStages * 2 * kBlkBytes + kNumBars * 8 + 96;
+  static constexpr int s(int b) { return S::kW * b; }
+  static constexpr int kDp = 2 * S::kW, kDq = 3 * S::kW;
+};
+
+// D[128 x W] = A·B^T over DP columns: K-major tiles of 128 and W rows.
+template <int DP, int W>
 __device__ __forceinline__ void mma_kk(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t id = idesc_bf16_f32(kTile, kTile);
+  constexpr uint32_t id = idesc_bf16_f32(kTile, W);
 #pragma unroll
-  for (int k = 0; k < DP / 16; ++k) {
-    const int at = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-    tc_mma_bf16(d, a + at, b + at, id, k > 0);
-  }
+  for (int k = 0; k < DP / 16; ++k)
+    tc_mma_bf16(d, a + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                b + (((k / 4) * (W * 128) + (k % 4) * 32) >> 4), id, k > 0);
 }
-// D[128 x DP] (+)= A·B, A 128 x 128 in tensor memory (each half of its 128
-// columns as 32 packed columns at the start of 64), B a tile of 128 rows.
-template <int DP>
+// D[128 x DP] (+)= A·B, A 128 x W in tensor memory (64 columns each as 32
+// packed columns at the start of 64), B a tile of W rows.
+template <int DP, int W>
 __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
   constexpr uint32_t id = idesc_bf16_f32_bmn(kTile, DP);
 #pragma unroll
-  for (int k = 0; k < kTile / 16; ++k)
+  for (int k = 0; k < W / 16; ++k)
     tc_mma_bf16_ts(d, a + (k / 4) * kHalf + (k % 4) * 8, b + ((2048 * k) >> 4), id,
                    k > 0 ? 1u : add);
 }
@@ -140,6 +153,7 @@ __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, in
 // One (slot of 128 rows, head): 8 lanes a row.
 __global__ void __launch_bounds__(256)
 attn_stats_kernel(const AttnArgs a, int slots) {
+  pdl_trigger();
   if (blockIdx.x == 0) attn_check_sequences(a);
   const int slot = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
   AttnBlock b;
@@ -175,41 +189,42 @@ attn_stats_kernel(const AttnArgs a, int slots) {
   }
 }
 
-// What a block of 128 keys means for dK and dV.
+// What a tile of 128 keys means for dK and dV, in query blocks of W rows.
+template <int W>
 struct DkvWork {
   int nqb, qb0;            // query blocks qb0 .. nqb - 1 of every head see it
-  int diag, last;          // those that the mask cuts (-1: none)
+  int diag, last;          // cut by the mask: those below diag, and last (-1: none)
   static __device__ __forceinline__ DkvWork of(const AttnBlock& b, int causal) {
     DkvWork w;
-    w.nqb = (b.len + kTile - 1) / kTile;
-    w.diag = causal ? b.row0 / kTile : -1;
-    w.qb0 = causal ? w.diag : 0;
-    w.last = b.len % kTile ? w.nqb - 1 : -1;
+    w.nqb = (b.len + W - 1) / W;
+    w.qb0 = causal ? b.row0 / W : 0;
+    w.diag = causal ? w.qb0 + kTile / W : -1;
+    w.last = b.len % W ? w.nqb - 1 : -1;
     return w;
   }
-  __device__ __forceinline__ bool is_cut(int qb) const { return qb == diag || qb == last; }
+  __device__ __forceinline__ bool is_cut(int qb) const { return qb < diag || qb == last; }
 };
 
-template <int DP>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+template <int DP, int NH>
+__global__ void __launch_bounds__(Shape<NH>::kThreads, NH == 2 ? 1 : 2)
 attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                    const AttnArgs a, int slots) {
-  using C = DkvCfg<DP>;
+  using C = DkvCfg<DP, NH>;
+  constexpr int kHelp = C::kHelp, W = C::kW;
   extern __shared__ unsigned char dkv_raw[];
   const uint32_t raw = smem_addr(dkv_raw);
   unsigned char* sm = dkv_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* kv_sm = sm;                                   // K, V
   unsigned char* ring = sm + 2 * C::kTileBytes;                // [kStages] Q, dO
-  unsigned char* stat = ring + C::kStages * 2 * C::kTileBytes; // [kStages] lse, delta
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + C::kStages * kStatBytes);
+  unsigned char* stat = ring + C::kStages * 2 * C::kBlkBytes;  // [kStages] lse, delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stat + C::kStages * C::kStatBytes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t kvfull = bar0, dpfull = bar0 + 8, dsready = bar0 + 16, dkdone = bar0 + 24;
   const uint32_t clean = bar0 + 32, done = bar0 + 40;
-  auto sfull = [&](int i) { return bar0 + 48 + 8 * i; };
+  const uint32_t sfull = bar0 + 48, dvdone = bar0 + 80;
   auto pready = [&](int i) { return bar0 + 64 + 8 * i; };
-  auto dvdone = [&](int i) { return bar0 + 80 + 8 * i; };
   const uint32_t cutgo = bar0 + 96, kvempty = bar0 + 104;
   auto full = [&](int st) { return bar0 + 152 + 8 * st; };
   auto empty = [&](int st) { return bar0 + 152 + 8 * (C::kStages + st); };
@@ -219,24 +234,32 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const int rep = a.Hq / a.Hkv;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)       // dsready, pready: 8 warps; a slot's readers
-      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 8 : i == 16 || i == 17 ? 11 : 1);
+    for (int i = 0; i < kNumBars; ++i)       // dsready, pready; a slot's readers
+      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 4 * NH : i == 16 || i == 17 ? 4 * NH + 3 : 1);
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(tslot, 512);
+  if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
 
   uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
+  if (warp >= kHelp) {
+    // (registers: 2·208 + 88 = 3·168 and 208 + 48 = 2·128, the launch's own)
+    if (NH == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kHelp) {
+      // The kernel ahead made lse and delta; the next one needs them too, so it
+      // may start from here on.
+      pdl_wait();
+      if (lane == 0) pdl_trigger();
       int st = 0, used = 0, items = 0;
       uint32_t round = 0;
       give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock& b, int g) {
-        const DkvWork w = DkvWork::of(b, a.causal);
+        const DkvWork<W> w = DkvWork<W>::of(b, a.causal);
         if (items > 0) mbar_poll(kvempty, (items - 1) & 1, limit);
         ++items;
         if (lane == 0) {
@@ -255,18 +278,20 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (limit == 0) return;
             if (lane == 0) {
               uint64_t* bar = bars + 19 + st;
-              unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
-              const int row = b.start + qb * kTile;
-              mbar_expect_tx(bar, 2 * C::kTileBytes + kStatBytes);
+              unsigned char* q_sm = ring + st * 2 * C::kBlkBytes;
+              const int row = b.start + qb * W;
+              mbar_expect_tx(bar, 2 * C::kBlkBytes + C::kStatBytes);
 #pragma unroll
               for (int x = 0; x < C::kBoxes; ++x)
-                tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, row, bar);
+                tma_load_3d(q_sm + x * (W * 128), &tmQ, 64 * x, h, row, bar);
 #pragma unroll
               for (int x = 0; x < C::kBoxes; ++x)
-                tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h, row, bar);
-              bulk_g2s(stat + st * kStatBytes,
-                       a.stats + ((long long)h * slots + slot0 + qb) * (2 * kTile), kStatBytes,
-                       bar);
+                tma_load_3d(q_sm + C::kBlkBytes + x * (W * 128), &tmG, 64 * x, h, row, bar);
+              const float* src = a.stats +
+                                 ((long long)h * slots + slot0 + qb * W / kTile) * (2 * kTile) +
+                                 qb * W % kTile;
+              bulk_g2s(stat + st * C::kStatBytes, src, W * 4, bar);
+              bulk_g2s(stat + st * C::kStatBytes + W * 4, src + kTile, W * 4, bar);
             }
             if (++st == C::kStages) {
               st = 0;
@@ -274,32 +299,32 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
           }
       });
-    } else if (warp == 9) {
+    } else if (warp == kHelp + 1) {
       const uint64_t kd = sdesc_k128(kv_sm), vd = sdesc_k128(kv_sm + C::kTileBytes);
-      const uint64_t qd = sdesc_k128(ring), gd = sdesc_k128(ring + C::kTileBytes);
-      int st = 0, sb = 0, items = 0;
-      uint32_t round = 0, sround = 0, c = 0;
+      const uint64_t qd = sdesc_k128(ring), gd = sdesc_k128(ring + C::kBlkBytes);
+      int st = 0, items = 0;
+      uint32_t round = 0, c = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
-        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         mbar_poll(kvfull, items++ & 1, limit);
         const int n = rep * (w.nqb - w.qb0);
         int qb = w.qb0;
         for (int j = 0; j < n; ++j, ++c) {
-          const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
+          const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
           mbar_poll(full(st), round, limit);
-          // S's buffer is free once the dV product has read P from it.
-          if (c >= (uint32_t)C::kSBufs) mbar_poll(dvdone(sb), sround ^ 1u, limit);
+          // S's columns are free once the dV product has read P from them.
+          if (c >= 1) mbar_poll(dvdone, (c - 1) & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_kk<DP>(tmem + C::s(sb), kd, qd + at);
-            tc_commit(sfull(sb));
+            mma_kk<DP, W>(tmem, kd, qd + at);
+            tc_commit(sfull);
           }
           __syncwarp();
           // dP's columns are free once the dK product has read dS from them.
           if (c >= 1) mbar_poll(dkdone, (c - 1) & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_kk<DP>(tmem + C::kDp, vd, gd + at);
+            mma_kk<DP, W>(tmem + C::kDp, vd, gd + at);
             tc_commit(dpfull);
             // A cut block has served as it came: it can be cleaned.
             if (w.is_cut(qb)) tc_commit(cutgo);
@@ -311,43 +336,38 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             st = 0;
             round ^= 1u;
           }
-          if (++sb == C::kSBufs) {
-            sb = 0;
-            sround ^= 1u;
-          }
         }
       });
-    } else if (warp == 10) {
-      const uint64_t qd = sdesc_mn128(ring, kTile * 128);
-      const uint64_t gd = sdesc_mn128(ring + C::kTileBytes, kTile * 128);
-      int st = 0, sb = 0;
+    } else if (warp == kHelp + 2) {
+      const uint64_t qd = sdesc_mn128(ring, W * 128);
+      const uint64_t gd = sdesc_mn128(ring + C::kBlkBytes, W * 128);
+      int st = 0;
       uint32_t ncut = 0, c = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
-        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         const int n = rep * (w.nqb - w.qb0);
         int qb = w.qb0;
         for (int j = 0; j < n; ++j, ++c) {
-          const uint64_t at = st * (uint64_t)(2 * C::kTileBytes >> 4);
+          const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
           if (w.is_cut(qb)) mbar_poll(clean, ncut++ & 1, limit);
           // (the first of a block: both warpgroups have read the last one's dV, dK)
           mbar_poll(pready(c & 1), (c >> 1) & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_tn<DP>(tmem + C::kDv, tmem + C::s(sb), gd + at, j > 0);
-            tc_commit(dvdone(sb));
+            mma_tn<DP, W>(tmem + C::kDv, tmem, gd + at, j > 0);
+            tc_commit(dvdone);
           }
           __syncwarp();
           mbar_poll(dsready, c & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_tn<DP>(tmem + C::kDk, tmem + C::kDp, qd + at, j > 0);
-            mma_tn<DP>(tmem + C::kDk, tmem + C::kDp + kHalf / 2, qd + at, 1);
+            mma_tn<DP, W>(tmem + C::kDk, tmem + C::kDp, qd + at, j > 0);
+            mma_tn<DP, W>(tmem + C::kDk, tmem + C::kDp + kHalf / 2, qd + at, 1);
             tc_commit(dkdone);
             tc_commit(empty(st));
           }
           __syncwarp();
           if (++st == C::kStages) st = 0;
-          if (++sb == C::kSBufs) sb = 0;
           if (++qb == w.nqb) qb = w.qb0;
         }
       });
@@ -359,16 +379,16 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       int st = 0;
       uint32_t ncut = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
-        const DkvWork w = DkvWork::of(slot->b, a.causal);
+        const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         const int n = rep * (w.nqb - w.qb0);
         int qb = w.qb0;
         for (int j = 0; j < n; ++j) {
           if (w.is_cut(qb)) {
             mbar_poll(cutgo, ncut++ & 1, limit);
-            unsigned char* q_sm = ring + st * 2 * C::kTileBytes;
-            const int rows = slot->b.len - qb * kTile;
-            clean_tile<DP>(q_sm, rows);
-            if (clean_tile<DP>(q_sm + C::kTileBytes, rows) && lane == 0)
+            unsigned char* q_sm = ring + st * 2 * C::kBlkBytes;
+            const int rows = slot->b.len - qb * W;
+            clean_tile<DP, W>(q_sm, rows);
+            if (clean_tile<DP, W>(q_sm + C::kBlkBytes, rows) && lane == 0)
               const_cast<WorkSlot*>(slot)->odd = 1;
             fence_proxy_async_smem();
             __syncwarp();
@@ -381,25 +401,26 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int half = warp >> 2, quad = warp & 3;
+    const int half = NH == 2 ? warp >> 2 : 0, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const float sc = a.scale * kLog2e;
     const float2 sc2 = make_float2(sc, sc);
-    int st = 0, sb = 0;
-    uint32_t round = 0, sround = 0, nb = 0;
+    int st = 0;
+    uint32_t round = 0, nb = 0;
+    const uint32_t ts = tmem + lanes + half * kHalf;
+    const uint32_t tdp = ts + C::kDp;
     take_work(ring_w, limit, [&](const WorkSlot* slot) {
     const AttnBlock b = slot->b;
     const int g = slot->h;
-    const DkvWork w = DkvWork::of(b, a.causal);
+    const DkvWork<W> w = DkvWork<W>::of(b, a.causal);
     const int key = b.row0 + 32 * quad + lane;                 // within the sequence
     const int n = rep * (w.nqb - w.qb0);
     int qb = w.qb0;
     for (int j = 0; j < n; ++j, ++nb) {
-      const uint32_t ts = tmem + lanes + C::s(sb) + half * kHalf;
-      const uint32_t tdp = tmem + lanes + C::kDp + half * kHalf;
-      const float4* lse = reinterpret_cast<const float4*>(stat + st * kStatBytes) + half * 16;
-      const float4* del = lse + kTile / 4;
-      mbar_poll(sfull(sb), sround, limit);
+      const float4* lse =
+          reinterpret_cast<const float4*>(stat + st * C::kStatBytes) + half * 16;
+      const float4* del = lse + W / 4;
+      mbar_poll(sfull, nb & 1, limit);
       tc_fence_after();
       uint32_t r[kHalf];
       tc_ld32(ts, r);
@@ -421,7 +442,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       // Columns lo .. hi - 1 of the half are queries that see this key.
       const bool cut = w.is_cut(qb);
-      const int q0 = qb * kTile + half * kHalf;
+      const int q0 = qb * W + half * kHalf;
       const int lo = a.causal ? key - q0 : 0, hi = b.len - q0;
       if (cut) {
 #pragma unroll
@@ -463,10 +484,6 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         st = 0;
         round ^= 1u;
       }
-      if (++sb == C::kSBufs) {
-        sb = 0;
-        sround ^= 1u;
-      }
       if (++qb == w.nqb) qb = w.qb0;
     }
     mbar_poll(dkdone, (nb - 1) & 1, limit);    // the block's last product
@@ -484,8 +501,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           // What was taken out of the cut blocks of dO, for the keys that its
           // rows see (an infinity or NaN times a positive probability).
           for (int h = g * rep; h < (g + 1) * rep; ++h)
-            for (int i = a.causal ? key : (w.nqb - 1) * kTile; i < b.len; ++i) {
-              if (!w.is_cut(i / kTile)) continue;
+            for (int i = a.causal ? key : (w.nqb - 1) * W; i < b.len; ++i) {
+              if (!w.is_cut(i / W)) continue;
               const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.dO) +
                                         (((long long)b.start + i) * a.Hq + h) * a.dh;
               for (int c = 0; c < a.dh; ++c) {
@@ -494,7 +511,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               }
             }
         }
-      } else {
+      }
+      if (half == NH - 1) {
         __nv_bfloat16* dk =
             static_cast<__nv_bfloat16*>(a.dk) + tok * a.lddk + (long long)g * a.dh;
         store_row(tmem + lanes + C::kDk, dk, 0, a.dh, a.scale, live,
@@ -507,27 +525,28 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (limit == 0) report(a.status, 0x721);
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kHelp + 1) {
     // The columns are freed only after every MMA has completed (bounded).
     mbar_poll(done, 0, limit);
     if (limit == 0) report(a.status, 0x722);
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+template <int DP, int NH>
+__global__ void __launch_bounds__(Shape<NH>::kThreads, NH == 2 ? 1 : 2)
 attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                   const AttnArgs a, int slots) {
-  using C = DqCfg<DP>;
+  using C = DqCfg<DP, NH>;
+  constexpr int kHelp = C::kHelp, W = C::kW;
   extern __shared__ unsigned char dq_raw[];
   const uint32_t raw = smem_addr(dq_raw);
   unsigned char* sm = dq_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* q_sm = sm;                                    // Q, dO
   unsigned char* ring = sm + 2 * C::kTileBytes;                // [kStages] K, V
-  float* stat = reinterpret_cast<float*>(ring + C::kStages * C::kStageBytes);  // [2] lse, delta
+  float* stat = reinterpret_cast<float*>(ring + C::kStages * 2 * C::kBlkBytes);  // [2] lse, delta
   uint64_t* bars = reinterpret_cast<uint64_t*>(stat + 2 * 2 * kTile);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
@@ -545,27 +564,33 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 96,
                            smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Key blocks n - 1 .. 0; only the first of them can be cut by the mask.
+  // Key blocks n - 1 .. 0, of which the mask cuts some row of the first few.
   auto blocks = [&](const AttnBlock& b) {
-    return a.causal ? b.row0 / kTile + 1 : (b.len + kTile - 1) / kTile;
+    return ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + W - 1) / W;
   };
-  auto is_cut = [&](const AttnBlock& b) { return a.causal || b.len % kTile != 0; };
+  auto is_cut = [&](const AttnBlock& b, int blk) {
+    return (blk + 1) * W > b.len || (a.causal && (blk + 1) * W > b.row0 + 1);
+  };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)       // dsready: 8 warps; a slot's readers
-      mbar_init(bars + i, i == 2 ? 8 : i == 14 || i == 15 ? 11 : 1);
+    for (int i = 0; i < kNumBars; ++i)       // dsready; a slot's readers
+      mbar_init(bars + i, i == 2 ? 4 * NH : i == 14 || i == 15 ? 4 * NH + 3 : 1);
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(tslot, 512);
+  if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
 
   uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
+  if (warp >= kHelp) {
+    // (registers: 2·208 + 88 = 3·168 and 208 + 48 = 2·128, the launch's own)
+    if (NH == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kHelp) {
       int st = 0, used = 0, items = 0;
       uint32_t round = 0;
       give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock& b, int h) {
@@ -573,7 +598,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
         if (lane == 0) {
           uint64_t* bar = bars + (items & 1 ? kQ1 : 0);
-          mbar_expect_tx(bar, 2 * C::kTileBytes + kStatBytes);
+          mbar_expect_tx(bar, 2 * C::kTileBytes + 2 * kTile * 4);
           for (int x = 0; x < C::kBoxes; ++x) {
             tma_load_3d(q_sm + x * (kTile * 128), &tmQ, 64 * x, h, b.start + b.row0, bar);
             tma_load_3d(q_sm + C::kTileBytes + x * (kTile * 128), &tmG, 64 * x, h,
@@ -582,7 +607,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           // (its buffer's last reader has given back the slot of two blocks ago)
           const int slot = (b.start >> 7) + b.seq + b.row0 / kTile;
           bulk_g2s(stat + (items & 1) * 2 * kTile,
-                   a.stats + ((long long)h * slots + slot) * (2 * kTile), kStatBytes, bar);
+                   a.stats + ((long long)h * slots + slot) * (2 * kTile), 2 * kTile * 4, bar);
         }
         ++items;
         for (int blk = blocks(b) - 1; blk >= 0; --blk) {
@@ -591,15 +616,15 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (limit == 0) break;
           if (lane == 0) {
             uint64_t* bar = bars + 17 + st;
-            unsigned char* k_sm = ring + st * C::kStageBytes;
-            const int row = b.start + blk * kTile;
-            mbar_expect_tx(bar, C::kStageBytes);
+            unsigned char* k_sm = ring + st * 2 * C::kBlkBytes;
+            const int row = b.start + blk * W;
+            mbar_expect_tx(bar, 2 * C::kBlkBytes);
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
-              tma_load_3d(k_sm + x * (kTile * 128), &tmK, 64 * x, g, row, bar);
+              tma_load_3d(k_sm + x * (W * 128), &tmK, 64 * x, g, row, bar);
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
-              tma_load_3d(k_sm + C::kTileBytes + x * (kTile * 128), &tmV, 64 * x, g, row, bar);
+              tma_load_3d(k_sm + C::kBlkBytes + x * (W * 128), &tmV, 64 * x, g, row, bar);
           }
           if (++st == C::kStages) {
             st = 0;
@@ -607,34 +632,34 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
         }
       });
-    } else if (warp == 9) {
+    } else if (warp == kHelp + 1) {
       const uint64_t qd = sdesc_k128(q_sm), gd = sdesc_k128(q_sm + C::kTileBytes);
-      const uint64_t kd = sdesc_k128(ring), vd = sdesc_k128(ring + C::kTileBytes);
+      const uint64_t kd = sdesc_k128(ring), vd = sdesc_k128(ring + C::kBlkBytes);
       int st = 0, items = 0;
       uint32_t round = 0, c = 0, ncut = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const int n = blocks(slot->b);
-        const bool cut = is_cut(slot->b);
         mbar_poll(qfull(items), (items >> 1) & 1, limit);
         ++items;
         for (int j = 0; j < n; ++j, ++c) {
-          const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
+          const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
+          const bool cut = is_cut(slot->b, n - 1 - j);
           mbar_poll(full(st), round, limit);
           // (S's buffer was read before dS of two blocks ago was ready, which the
           // wait below for the product of that dS has shown.)
           if (elect_one()) {
-            mma_kk<DP>(tmem + C::s(c & 1), qd, kd + at);
+            mma_kk<DP, W>(tmem + C::s(c & 1), qd, kd + at);
             tc_commit(sfull(c & 1));
             // K of a cut block has served as it came: it can be cleaned.
-            if (j == 0 && cut) tc_commit(cutgo(ncut & 1));
+            if (cut) tc_commit(cutgo(ncut & 1));
           }
           __syncwarp();
-          if (j == 0 && cut) ++ncut;
+          if (cut) ++ncut;
           // dP's columns are free once the dQ product has read dS from them.
           if (c >= 1) mbar_poll(dqdone, (c - 1) & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_kk<DP>(tmem + C::kDp, gd, vd + at);
+            mma_kk<DP, W>(tmem + C::kDp, gd, vd + at);
             tc_commit(dpfull);
             if (j == n - 1) tc_commit(qempty);
           }
@@ -645,24 +670,24 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
         }
       });
-    } else if (warp == 10) {
-      const uint64_t kd = sdesc_mn128(ring, kTile * 128);
+    } else if (warp == kHelp + 2) {
+      const uint64_t kd = sdesc_mn128(ring, W * 128);
       int st = 0;
       uint32_t c = 0, ncut = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const int n = blocks(slot->b);
-        if (is_cut(slot->b)) {
-          mbar_poll(clean(ncut & 1), (ncut >> 1) & 1, limit);
-          ++ncut;
-        }
         for (int j = 0; j < n; ++j, ++c) {
-          const uint64_t at = st * (uint64_t)(C::kStageBytes >> 4);
+          const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
+          if (is_cut(slot->b, n - 1 - j)) {
+            mbar_poll(clean(ncut & 1), (ncut >> 1) & 1, limit);
+            ++ncut;
+          }
           // (the first of a block: both warpgroups have read the last one's dQ)
           mbar_poll(dsready, c & 1, limit);
           tc_fence_after();
           if (elect_one()) {
-            mma_tn<DP>(tmem + C::kDq, tmem + C::kDp, kd + at, j > 0);
-            mma_tn<DP>(tmem + C::kDq, tmem + C::kDp + kHalf / 2, kd + at, 1);
+            mma_tn<DP, W>(tmem + C::kDq, tmem + C::kDp, kd + at, j > 0);
+            mma_tn<DP, W>(tmem + C::kDq, tmem + C::kDp + kHalf / 2, kd + at, 1);
             tc_commit(dqdone);
             tc_commit(empty(st));
           }
@@ -675,23 +700,25 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     } else {
       // A cut block's scores may be there before the one before is cleaned, but
       // not those of the block after it: two barriers in turn.
-      int first = 0;
+      int st = 0;
       uint32_t ncut = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
-        if (is_cut(slot->b)) {
-          mbar_poll(cutgo(ncut & 1), (ncut >> 1) & 1, limit);
-          clean_tile<DP>(ring + first * C::kStageBytes, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(clean(ncut & 1));
-          ++ncut;
+        for (int blk = blocks(slot->b) - 1; blk >= 0; --blk) {
+          if (is_cut(slot->b, blk)) {
+            mbar_poll(cutgo(ncut & 1), (ncut >> 1) & 1, limit);
+            clean_tile<DP, W>(ring + st * 2 * C::kBlkBytes, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(clean(ncut & 1));
+            ++ncut;
+          }
+          if (++st == C::kStages) st = 0;
         }
-        first = (first + blocks(slot->b)) % C::kStages;
       });
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int half = warp >> 2, quad = warp & 3;
+    const int half = NH == 2 ? warp >> 2 : 0, quad = warp & 3;
     const int lrow = 32 * quad + lane;                         // within the tile
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t tdp = tmem + lanes + C::kDp + half * kHalf;
@@ -701,7 +728,6 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     take_work(ring_w, limit, [&](const WorkSlot* slot) {
     const AttnBlock b = slot->b;
     const int h = slot->h, n = blocks(b);
-    const bool cut0 = is_cut(b);
     const int row = b.row0 + lrow;                             // within the sequence
     mbar_poll(qfull(items), (items >> 1) & 1, limit);
     const float lse = stat[(items & 1) * 2 * kTile + lrow];
@@ -736,10 +762,10 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         p[c] *= x.x;
         p[c + 1] *= x.y;
       }
-      if (j == 0 && cut0) {
+      if (is_cut(b, n - 1 - j)) {
         // The last key this row sees, within the half block.
-        const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - (n - 1) * kTile -
-                         half * kHalf;
+        const int last =
+            (a.causal ? min(row, b.len - 1) : b.len - 1) - (n - 1 - j) * W - half * kHalf;
 #pragma unroll
         for (int c = 0; c < kHalf; ++c)
           if (c > last) p[c] = 0.f;
@@ -755,45 +781,54 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       tc_fence_after();
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) +
                            ((long long)b.start + row) * a.lddq + (long long)h * a.dh;
-      const int c0 = half * (DP / 2);
-      store_row(tmem + lanes + C::kDq, dst, c0, min(a.dh, c0 + DP / 2), a.scale, row < b.len,
+      const int c0 = half * (DP / NH);
+      store_row(tmem + lanes + C::kDq, dst, c0, min(a.dh, c0 + DP / NH), a.scale, row < b.len,
                 wide_rows(a.dq, a.lddq, a.dh));
       tc_fence_before();                       // read before the next block's products
     }
     });
   }
   if (limit == 0) report(a.status, 0x731);
+  // The kernel ahead (dK, dV) may still run: this one does not end before it.
+  if (threadIdx.x == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kHelp + 1) {
     // The columns are freed only after every MMA has completed (bounded).
     mbar_poll(done, 0, limit);
     if (limit == 0) report(a.status, 0x732);
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
-template <int DP>
+template <int DP, int NH>
 cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
-  CUtensorMap q, k, v, g;
+  constexpr int W = Shape<NH>::kW;
+  // Tiles of 128 rows, and blocks of W on the other side.
+  CUtensorMap q, k, v, g, qw, kw, vw, gw;
   const unsigned long long ldo = (unsigned long long)a.Hq * a.dh * 2;
-  if (!encode_map_heads_sw128(&q, a.q, a.dh, a.Hq, a.T, (unsigned long long)a.ldq * 2, kTile) ||
-      !encode_map_heads_sw128(&k, a.k, a.dh, a.Hkv, a.T, (unsigned long long)a.ldk * 2, kTile) ||
-      !encode_map_heads_sw128(&v, a.v, a.dh, a.Hkv, a.T, (unsigned long long)a.ldv * 2, kTile) ||
-      !encode_map_heads_sw128(&g, a.dO, a.dh, a.Hq, a.T, ldo, kTile))
+  auto map = [&](CUtensorMap* m, const void* p, int heads, unsigned long long bytes, int rows) {
+    return encode_map_heads_sw128(m, p, a.dh, heads, a.T, bytes, rows);
+  };
+  const unsigned long long lq = (unsigned long long)a.ldq * 2, lk = (unsigned long long)a.ldk * 2,
+                           lv = (unsigned long long)a.ldv * 2;
+  if (!map(&q, a.q, a.Hq, lq, kTile) || !map(&k, a.k, a.Hkv, lk, kTile) ||
+      !map(&v, a.v, a.Hkv, lv, kTile) || !map(&g, a.dO, a.Hq, ldo, kTile) ||
+      !map(&qw, a.q, a.Hq, lq, W) || !map(&kw, a.k, a.Hkv, lk, W) ||
+      !map(&vw, a.v, a.Hkv, lv, W) || !map(&gw, a.dO, a.Hq, ldo, W))
     return cudaErrorInvalidValue;
   const int slots = (int)attn_slots(a.T, a.S, 7);
   attn_stats_kernel<<<(unsigned)(slots * a.Hq), 256, 0, st>>>(a, slots);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_tc_dkv_kernel<DP><<<(unsigned)(slots * a.Hkv), kBwdThreads, DkvCfg<DP>::kSmem, st>>>(
-      q, k, v, g, a, slots);
-  e = cudaGetLastError();
+  e = launch_dependent(attn_tc_dkv_kernel<DP, NH>, dim3((unsigned)(slots * a.Hkv)),
+                       dim3(Shape<NH>::kThreads), DkvCfg<DP, NH>::kSmem, st, qw, k, v, gw, a,
+                       slots);
   if (e != cudaSuccess) return e;
-  attn_tc_dq_kernel<DP><<<(unsigned)(slots * a.Hq), kBwdThreads, DqCfg<DP>::kSmem, st>>>(
-      q, k, v, g, a, slots);
-  return cudaGetLastError();
+  return launch_dependent(attn_tc_dq_kernel<DP, NH>, dim3((unsigned)(slots * a.Hq)),
+                          dim3(Shape<NH>::kThreads), DqCfg<DP, NH>::kSmem, st, q, kw, vw, g, a,
+                          slots);
 }
 
 }  // namespace
@@ -803,15 +838,16 @@ size_t attn_tc_stats_count(int max_tokens, int max_seqs, int Hq) {
 }
 
 cudaError_t setup_attn_tc_bwd() {
-  cudaError_t e = allow_max_smem(attn_tc_dkv_kernel<64>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dkv_kernel<128>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dq_kernel<64>);
-  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dq_kernel<128>);
+  cudaError_t e = allow_max_smem(attn_tc_dkv_kernel<64, 1>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dkv_kernel<128, 2>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dq_kernel<64, 1>);
+  if (e == cudaSuccess) e = allow_max_smem(attn_tc_dq_kernel<128, 2>);
   return e;
 }
 
 cudaError_t launch_attn_tc_backward(const AttnArgs& a, cudaStream_t st) {
-  return a.dh <= 64 ? bwd<64>(a, st) : bwd<128>(a, st);
+  if (a.dh > 64) return bwd<128, 2>(a, st);
+  return bwd<64, 1>(a, st);
 }
 
 }  // namespace cat
