@@ -138,7 +138,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     if (warp == kHelp) {
       int st = 0, used = 0, nq[2] = {0, 0};
       uint32_t round = 0;
-      give_work(a, a.Hq, NT == 2 ? 8 : 7, true, ring, limit, [&](const AttnBlock& b, int h) {
+      give_work(a, a.Hq, NT == 2 ? 8 : 7, true, ring, limit, [&](const AttnBlock& b, int h, WorkSlot*) {
         const FwdWork w = FwdWork::of<NT>(b, a.causal);
         const int g = h / (a.Hq / a.Hkv);
 #pragma unroll

@@ -124,8 +124,8 @@ struct WorkRing {
   __device__ __forceinline__ uint32_t answered() const { return bars + 32; }
 };
 
-// The copy warp's loop: load(block, head) for each of the CTA's blocks, in
-// slots of 2^shift rows by `heads` heads, the last slots first if `reverse`.
+// The copy warp's loop: load(block, head, slot) for each of the CTA's blocks,
+// in slots of 2^shift rows by `heads` heads, the last slots first if `reverse`.
 template <typename F>
 __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shift, bool reverse,
                                           const WorkRing& ring, uint32_t& limit, F load) {
@@ -151,7 +151,7 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
     AttnBlock b;
     if (attn_find_block(a, slot, shift, &b)) {
       publish(b, h, 1);
-      load(b, h);
+      load(b, h, ring.slots + ((count - 1) & 1));
       __syncwarp();
     }
     // Asked only now, with this block's copies issued: a block taken over early

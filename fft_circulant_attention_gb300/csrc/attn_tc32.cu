@@ -22,7 +22,8 @@
 //   - warps 4-7: load operands with ordinary loads, split them and write the
 //     planes to shared memory in the 128-byte swizzle the MMA reads; rows
 //     outside the sequence and columns beyond the head width become zeros;
-//   - warp 8: issues the MMAs (warps 9-11 only complete its warpgroup).
+//   - warp 8 issues the MMAs, warp 9 finds the work (10 and 11 only complete
+//     the warpgroup).
 // Bound by the MMAs (six times 128·64·64 a product) with the splitting of the
 // operands and of the probabilities beside them.
 //
@@ -41,7 +42,7 @@ namespace {
 
 constexpr int kThreads32 = 384;
 constexpr int kB = 64;                     // rows of a block of the other side
-constexpr int kNumBars = 24;
+constexpr int kNumBars = 32;               // room for every barrier
 constexpr float kLazy = 8.f;               // log2 of the maximum's growth that is let pass
 
 template <int DP>
@@ -50,11 +51,11 @@ struct Cfg32 {              // (the backward's shared memory holds DP = 64 only)
   static constexpr int kBlkPlane = kB * DP * 2;          // ... of 64 rows
   static constexpr int kStages = DP == 64 ? 2 : 1;
   static constexpr size_t kFwdSmem =
-      1024 + 3 * (size_t)kTilePlane + kStages * 6 * (size_t)kBlkPlane + kNumBars * 8 + 16;
+      1024 + 3 * (size_t)kTilePlane + kStages * 6 * (size_t)kBlkPlane + kNumBars * 8 + 96;
 };
 constexpr size_t kBwdSmem32 = 1024 + 6 * (size_t)Cfg32<64>::kTilePlane +
                               Cfg32<64>::kStages * (6 * (size_t)Cfg32<64>::kBlkPlane + 2 * kB * 4) +
-                              kNumBars * 8 + 16;
+                              kNumBars * 8 + 96;
 
 // Two values as three packed bf16 pairs.
 __device__ __forceinline__ void split2(float a, float b, uint32_t* p0, uint32_t* p1, uint32_t* p2) {
@@ -329,7 +330,6 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   unsigned char* v_sm = k_sm + C::kStages * 3 * C::kBlkPlane;
   uint64_t* bars = reinterpret_cast<uint64_t*>(v_sm + C::kStages * 3 * C::kBlkPlane);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  uint32_t* odd = tslot + 1;
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t qready = bar0, pready = bar0 + 8, odone = bar0 + 16, done = bar0 + 24;
   auto sfull = [&](int i) { return bar0 + 32 + 8 * i; };
@@ -337,24 +337,24 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   auto vready = [&](int st) { return bar0 + 64 + 8 * st; };
   auto kempty = [&](int st) { return bar0 + 80 + 8 * st; };
   auto vempty = [&](int st) { return bar0 + 96 + 8 * st; };
+  const uint32_t qempty = bar0 + 112;
+  const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
+  const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
+                           smem_addr(tslot + 4)};
   // Tensor memory: scores (two buffers), probabilities, O.
   constexpr int kP = 128, kO = 256;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Key blocks n - 1 .. 0.
+  auto blocks = [&](const AttnBlock& b) {
+    return ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
+  };
 
   if (blockIdx.x == 0) attn_check_sequences(a);
-  const int h = blockIdx.x % a.Hq;
-  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 7, &b)) return;
-  const int g = h / (a.Hq / a.Hkv);
-  const int rows = min(kTile, b.len - b.row0);
-  // Key blocks n - 1 .. 0.
-  const int n = ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)   // qready, pready, kready, vready: a warp each
       mbar_init(bars + i, i == 0 || i == 1 || (i >= 6 && i < 10) ? 4 : 1);
-    *odd = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
+    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tslot, 512);
@@ -371,97 +371,122 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
       const uint64_t qd = sdesc_k128(q_sm), kd = sdesc_k128(k_sm);
       const uint64_t vd = sdesc_mn128(v_sm, kB * 128);
       constexpr uint64_t kStep = 3 * C::kBlkPlane >> 4;
-      auto scores = [&](int j) {
-        const int st = j % C::kStages;
-        mbar_poll(kready(st), (j / C::kStages) & 1, limit);
+      uint32_t c = 0, items = 0;               // blocks and query tiles so far
+      auto scores = [&](uint32_t x, bool last) {
+        const int st = x % C::kStages;
+        mbar_poll(kready(st), (x / C::kStages) & 1, limit);
         if (elect_one()) {
-          mma_kk3<DP>(tmem + kB * (j & 1), qd, kd + st * kStep);
-          tc_commit(sfull(j & 1));
+          mma_kk3<DP>(tmem + kB * (x & 1), qd, kd + st * kStep);
+          tc_commit(sfull(x & 1));
           tc_commit(kempty(st));
+          if (last) tc_commit(qempty);
         }
         __syncwarp();
       };
-      mbar_poll(qready, 0, limit);
-      scores(0);
-      for (int j = 0; j < n; ++j) {
-        // (the buffer of block j + 1 was read before P of block j - 1 was ready)
-        if (j + 1 < n) scores(j + 1);
-        const int st = j % C::kStages;
-        mbar_poll(vready(st), (j / C::kStages) & 1, limit);
-        mbar_poll(pready, j & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_tn3<DP>(tmem + kO, tmem + kP, vd + st * kStep);
-          tc_commit(odone);
-          tc_commit(vempty(st));
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const int n = blocks(slot->b);
+        mbar_poll(qready, items++ & 1, limit);
+        scores(c, n == 1);
+        for (int j = 0; j < n; ++j, ++c) {
+          // (the buffer of the next block was read before P of the one before was ready)
+          if (j + 1 < n) scores(c + 1, j + 2 == n);
+          const int st = c % C::kStages;
+          mbar_poll(vready(st), (c / C::kStages) & 1, limit);
+          mbar_poll(pready, c & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tn3<DP>(tmem + kO, tmem + kP, vd + st * kStep);
+            tc_commit(odone);
+            tc_commit(vempty(st));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
+      });
       if (elect_one()) tc_commit(done);
       __syncwarp();
+    } else if (warp == 9) {
+      // Finds the work, the next block once this one's operands are split.
+      uint32_t items = 0;
+      give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
+        mbar_poll(splitdone, items++ & 1, limit);
+      });
     }
   } else if (warp >= 4) {
     const int tid = threadIdx.x - 128;
-    const float* q = static_cast<const float*>(a.q) + (b.start + (long long)b.row0) * a.ldq +
-                     (long long)h * a.dh;
-    const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
-    const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
-    // Tiles in the order of their use, K0 K1 V0 K2 V1 ..; at head width 64 each
-    // is fetched while the one before is split and written (at 128 the
-    // registers hold one).
-    auto is_k = [&](int i) { return i == 0 || ((i & 1) && i < 2 * n - 1); };
-    auto block = [&](int i) { return i == 2 * n - 1 ? n - 1 : is_k(i) ? (i + 1) / 2 : i / 2 - 1; };
-    Piece<DP> now, next;
-    auto fetch = [&](Piece<DP>& x, int i) {
-      const long long r0 = (long long)(n - 1 - block(i)) * kB;
-      const int have = b.len - (int)r0;
-      if (is_k(i))
-        x.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
-      else
-        x.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
-    };
-    if (DP == 64) fetch(next, 0);
-    bool bad = put_tile<DP>(q_sm, q, a.ldq, rows, a.dh, a.vec, tid);
-    planes_ready(qready);
-    for (int i = 0; i < 2 * n; ++i) {
-      const int j = block(i), st = j % C::kStages;
-      const bool ik = is_k(i);
-      if (DP == 64) {
-        now = next;
-        if (i + 1 < 2 * n) fetch(next, i + 1);
-      } else {
-        fetch(now, i);
+    uint32_t c = 0, items = 0;
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+      const AttnBlock b = slot->b;
+      const int h = slot->h;
+      const int g = h / (a.Hq / a.Hkv), n = blocks(b);
+      const float* q = static_cast<const float*>(a.q) + (b.start + (long long)b.row0) * a.ldq +
+                       (long long)h * a.dh;
+      const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+      const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+      // Tiles in the order of their use, K0 K1 V0 K2 V1 ..; at head width 64 each
+      // is fetched while the one before is split and written (at 128 the
+      // registers hold one).
+      auto is_k = [&](int i) { return i == 0 || ((i & 1) && i < 2 * n - 1); };
+      auto block = [&](int i) { return i == 2 * n - 1 ? n - 1 : is_k(i) ? (i + 1) / 2 : i / 2 - 1; };
+      Piece<DP> now, next;
+      auto fetch = [&](Piece<DP>& x, int i) {
+        const long long r0 = (long long)(n - 1 - block(i)) * kB;
+        const int have = b.len - (int)r0;
+        if (is_k(i))
+          x.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
+        else
+          x.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
+      };
+      if (DP == 64) fetch(next, 0);
+      if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+      ++items;
+      bool bad = put_tile<DP>(q_sm, q, a.ldq, min(kTile, b.len - b.row0), a.dh, a.vec, tid);
+      planes_ready(qready);
+      for (int i = 0; i < 2 * n; ++i) {
+        const uint32_t x = c + block(i), st = x % C::kStages;
+        const bool ik = is_k(i);
+        if (DP == 64) {
+          now = next;
+          if (i + 1 < 2 * n) fetch(next, i + 1);
+        } else {
+          fetch(now, i);
+        }
+        if (x >= C::kStages)
+          mbar_poll(ik ? kempty(st) : vempty(st), ((x / C::kStages) - 1) & 1, limit);
+        bad |= now.template put<kB>((ik ? k_sm : v_sm) + st * 3 * C::kBlkPlane, 0, tid);
+        if (bad) const_cast<WorkSlot*>(slot)->odd = 1;
+        planes_ready(ik ? kready(st) : vready(st));
       }
-      if (j >= C::kStages)
-        mbar_poll(ik ? kempty(st) : vempty(st), ((j / C::kStages) - 1) & 1, limit);
-      bad |= now.template put<kB>((ik ? k_sm : v_sm) + st * 3 * C::kBlkPlane, 0, tid);
-      if (bad) *odd = 1;
-      planes_ready(ik ? kready(st) : vready(st));
-    }
+      c += n;
+      if (lane == 0) mbar_arrive(splitdone);
+    });
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
-    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t to = tmem + lanes + kO;
     const float sc = a.scale * kLog2e;
+    uint32_t nb = 0;                           // blocks so far
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int h = slot->h, g = h / (a.Hq / a.Hkv), n = blocks(b);
+    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     float m = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f), k2 = l2;
     float o[DP];
 #pragma unroll
     for (int c = 0; c < DP; ++c) o[c] = 0.f;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < n; ++j, ++nb) {
       // The product of the block before: beside this block's scores at head
       // width 128 (registers), beside its probabilities at 64.
       if (DP == 128 && j > 0) {
-        mbar_poll(odone, (j - 1) & 1, limit);
+        mbar_poll(odone, (nb - 1) & 1, limit);
         tc_fence_after();
         add_columns<DP>(o, to);
       }
-      mbar_poll(sfull(j & 1), (j >> 1) & 1, limit);
+      mbar_poll(sfull(nb & 1), (nb >> 1) & 1, limit);
       tc_fence_after();
       uint32_t r[kB];
-      tc_ld32(tmem + lanes + kB * (j & 1), r);
-      tc_ld32(tmem + lanes + kB * (j & 1) + 32, r + 32);
+      tc_ld32(tmem + lanes + kB * (nb & 1), r);
+      tc_ld32(tmem + lanes + kB * (nb & 1) + 32, r + 32);
       tc_wait_ld();
       // The last key this row sees, within the block.
       const int k0 = (n - 1 - j) * kB;
@@ -507,7 +532,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
         p[c + 1] = x.y;
       }
       if (DP == 64 && j > 0) {
-        mbar_poll(odone, (j - 1) & 1, limit);
+        mbar_poll(odone, (nb - 1) & 1, limit);
         tc_fence_after();
         add_columns<DP>(o, to);
       }
@@ -520,7 +545,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(pready);
     }
-    mbar_poll(done, 0, limit);
+    mbar_poll(odone, (nb - 1) & 1, limit);
     // (rows of a CTA that lost a wait are not written)
     if (__all_sync(0xffffffffu, limit != 0)) {
       tc_fence_after();
@@ -532,9 +557,11 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
         store_row32<DP>(o, static_cast<float*>(a.out) + (tok * a.Hq + h) * a.dh, a.dh, a.vec,
                         1.f / l);
       if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
-      if (live && *reinterpret_cast<volatile uint32_t*>(odd) != 0)
+      if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
         plain_fwd_row(a, b, h, g, row);
+      tc_fence_before();                       // read before the next block's products
     }
+    });
   }
   if (limit == 0) report(a.status, 0x741);
   tc_fence_before();
@@ -562,29 +589,29 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
   float* stat = reinterpret_cast<float*>(ring + C::kStages * 6 * C::kBlkPlane);  // lse, delta
   uint64_t* bars = reinterpret_cast<uint64_t*>(stat + C::kStages * 2 * kB);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  uint32_t* odd = tslot + 1;
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t kvready = bar0, pready = bar0 + 8, dsready = bar0 + 16, done = bar0 + 24;
   const uint32_t sfull = bar0 + 32, dpfull = bar0 + 40, dvdone = bar0 + 48, dkdone = bar0 + 56;
   auto ready = [&](int st) { return bar0 + 64 + 8 * st; };
   auto empty = [&](int st) { return bar0 + 80 + 8 * st; };
   const uint32_t dvread = bar0 + 96, dkread = bar0 + 104;      // added to the registers
+  const uint32_t kvempty = bar0 + 112;
+  const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
+  const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
+                           smem_addr(tslot + 4)};
   // Tensor memory: scores, probabilities, dP, dS, dV, dK.
   constexpr int kP = 64, kDp = 160, kDs = 224, kDv = 320, kDk = 384;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const int g = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 7, &b)) return;
   const int rep = a.Hq / a.Hkv;
-  const int nqb = (b.len + kB - 1) / kB, qb0 = a.causal ? b.row0 / kB : 0;
-  const int n = rep * (nqb - qb0);
-  const int keys = min(kTile, b.len - b.row0);
+  // Query blocks qb0 .. nqb - 1 of every head.
+  auto first_block = [&](const AttnBlock& b) { return a.causal ? b.row0 / kB : 0; };
+  auto blocks = [&](const AttnBlock& b) { return (b.len + kB - 1) / kB; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)   // those that four warps arrive on
       mbar_init(bars + i, i < 3 || i == 8 || i == 9 || i == 12 || i == 13 ? 4 : 1);
-    *odd = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
+    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tslot, 512);
@@ -603,139 +630,169 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
       const uint64_t qn = sdesc_mn128(ring, kB * 128);
       const uint64_t gn = sdesc_mn128(ring + 3 * C::kBlkPlane, kB * 128);
       constexpr uint64_t kStep = 6 * C::kBlkPlane >> 4;
-      mbar_poll(kvready, 0, limit);
-      mbar_poll(ready(0), 0, limit);
-      if (elect_one()) {
-        mma_kk3<DP>(tmem, kd, qk);
-        tc_commit(sfull);
-        mma_kk3<DP>(tmem + kDp, vd, gk);
-        tc_commit(dpfull);
-      }
-      __syncwarp();
-      for (int j = 0; j < n; ++j) {
-        const int st = j % C::kStages, nx = (j + 1) % C::kStages;
-        mbar_poll(pready, j & 1, limit);       // P is there, the scores are read
-        if (j + 1 < n) mbar_poll(ready(nx), ((j + 1) / C::kStages) & 1, limit);
-        if (j > 0) mbar_poll(dvread, (j - 1) & 1, limit);
+      uint32_t c = 0, items = 0;               // blocks and key tiles so far
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const int n = rep * (blocks(slot->b) - first_block(slot->b));
+        mbar_poll(kvready, items++ & 1, limit);
+        mbar_poll(ready(c % C::kStages), (c / C::kStages) & 1, limit);
         tc_fence_after();
         if (elect_one()) {
-          if (j + 1 < n) {
-            mma_kk3<DP>(tmem, kd, qk + nx * kStep);
-            tc_commit(sfull);
-          }
-          mma_tn3<DP>(tmem + kDv, tmem + kP, gn + st * kStep);
-          tc_commit(dvdone);
+          const uint64_t at = c % C::kStages * kStep;
+          mma_kk3<DP>(tmem, kd, qk + at);
+          tc_commit(sfull);
+          mma_kk3<DP>(tmem + kDp, vd, gk + at);
+          tc_commit(dpfull);
+          if (n == 1) tc_commit(kvempty);
         }
         __syncwarp();
-        mbar_poll(dsready, j & 1, limit);      // dS is there, dP is read
-        if (j > 0) mbar_poll(dkread, (j - 1) & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          if (j + 1 < n) {
-            mma_kk3<DP>(tmem + kDp, vd, gk + nx * kStep);
-            tc_commit(dpfull);
+        for (int j = 0; j < n; ++j, ++c) {
+          const int st = c % C::kStages, nx = (c + 1) % C::kStages;
+          mbar_poll(pready, c & 1, limit);     // P is there, the scores are read
+          if (j + 1 < n) mbar_poll(ready(nx), ((c + 1) / C::kStages) & 1, limit);
+          if (c > 0) mbar_poll(dvread, (c - 1) & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            if (j + 1 < n) {
+              mma_kk3<DP>(tmem, kd, qk + nx * kStep);
+              tc_commit(sfull);
+            }
+            mma_tn3<DP>(tmem + kDv, tmem + kP, gn + st * kStep);
+            tc_commit(dvdone);
           }
-          mma_tn3<DP>(tmem + kDk, tmem + kDs, qn + st * kStep);
-          tc_commit(dkdone);
-          tc_commit(empty(st));
+          __syncwarp();
+          mbar_poll(dsready, c & 1, limit);    // dS is there, dP is read
+          if (c > 0) mbar_poll(dkread, (c - 1) & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            if (j + 1 < n) {
+              mma_kk3<DP>(tmem + kDp, vd, gk + nx * kStep);
+              tc_commit(dpfull);
+              if (j + 2 == n) tc_commit(kvempty);
+            }
+            mma_tn3<DP>(tmem + kDk, tmem + kDs, qn + st * kStep);
+            tc_commit(dkdone);
+            tc_commit(empty(st));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
+      });
       if (elect_one()) tc_commit(done);
       __syncwarp();
+    } else if (warp == 9) {
+      // Finds the work, the next block once this one's operands are split.
+      uint32_t items = 0;
+      give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
+        mbar_poll(splitdone, items++ & 1, limit);
+      });
     }
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int tid = threadIdx.x - 128;
-    const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
-    int qb = qb0, h = g * rep;
-    Piece<DP> xq, xg;
-    auto fetch = [&]() {
-      const long long r = b.start + (long long)qb * kB;
-      const int have = b.len - qb * kB;
-      xq.fetch(static_cast<const float*>(a.q) + r * a.ldq + (long long)h * a.dh, a.ldq, have, a.dh,
-               a.vec, tid);
-      xg.fetch(static_cast<const float*>(a.dO) + r * ldo + (long long)h * a.dh, ldo, have, a.dh,
-               a.vec, tid);
-    };
-    bool bad = put_tile<DP>(k_sm, static_cast<const float*>(a.k) + t0 * a.ldk +
-                                      (long long)g * a.dh, a.ldk, keys, a.dh, a.vec, tid);
-    bad |= put_tile<DP>(v_sm, static_cast<const float*>(a.v) + t0 * a.ldv + (long long)g * a.dh,
-                        a.ldv, keys, a.dh, a.vec, tid);
-    fetch();
-    planes_ready(kvready);
+    const long long ldo = (long long)a.Hq * a.dh;
     // This warpgroup also adds the blocks' dV and dK, one thread a key.
     const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
-    float dv[DP], dk[DP];
+    uint32_t c = 0, items = 0;
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+      const AttnBlock b = slot->b;
+      const int g = slot->h;
+      const long long t0 = b.start + (long long)b.row0;
+      const int keys = min(kTile, b.len - b.row0), qb0 = first_block(b), nqb = blocks(b);
+      const int n = rep * (nqb - qb0);
+      float dv[DP], dk[DP];
 #pragma unroll
-    for (int c = 0; c < DP; ++c) dv[c] = dk[c] = 0.f;
-    auto add_block = [&](int j) {
-      mbar_poll(dvdone, j & 1, limit);
-      tc_fence_after();
-      add_columns<DP>(dv, tmem + lanes + kDv);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(dvread);
-      mbar_poll(dkdone, j & 1, limit);
-      tc_fence_after();
-      add_columns<DP>(dk, tmem + lanes + kDk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(dkread);
-    };
-    for (int j = 0; j < n; ++j) {
-      const int st = j % C::kStages;
-      if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
-      const long long r = b.start + (long long)qb * kB;
-      const int have = b.len - qb * kB;
-      unsigned char* q_sm = ring + st * 6 * C::kBlkPlane;
-      bad |= xq.template put<kB>(q_sm, 0, tid);
-      bad |= xg.template put<kB>(q_sm + 3 * C::kBlkPlane, 0, tid);
-      if (tid < kB) {
-        const long long i = (long long)h * a.T + r + tid;
-        const float l = tid < have ? a.lse[i] * kLog2e : 0.f;
-        const float d = tid < have ? a.delta[i] : 0.f;
-        stat[st * 2 * kB + tid] = l;
-        stat[st * 2 * kB + kB + tid] = d;
-        bad |= !isfinite(l) || !isfinite(d);
+      for (int x = 0; x < DP; ++x) dv[x] = dk[x] = 0.f;
+      auto add_block = [&](uint32_t x) {
+        mbar_poll(dvdone, x & 1, limit);
+        tc_fence_after();
+        add_columns<DP>(dv, tmem + lanes + kDv);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dvread);
+        mbar_poll(dkdone, x & 1, limit);
+        tc_fence_after();
+        add_columns<DP>(dk, tmem + lanes + kDk);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dkread);
+      };
+      int qb = qb0, h = g * rep;
+      Piece<DP> xq, xg;
+      auto fetch = [&]() {
+        const long long r = b.start + (long long)qb * kB;
+        const int have = b.len - qb * kB;
+        xq.fetch(static_cast<const float*>(a.q) + r * a.ldq + (long long)h * a.dh, a.ldq, have,
+                 a.dh, a.vec, tid);
+        xg.fetch(static_cast<const float*>(a.dO) + r * ldo + (long long)h * a.dh, ldo, have, a.dh,
+                 a.vec, tid);
+      };
+      if (items > 0) mbar_poll(kvempty, (items - 1) & 1, limit);
+      ++items;
+      bool bad = put_tile<DP>(k_sm, static_cast<const float*>(a.k) + t0 * a.ldk +
+                                        (long long)g * a.dh, a.ldk, keys, a.dh, a.vec, tid);
+      bad |= put_tile<DP>(v_sm, static_cast<const float*>(a.v) + t0 * a.ldv + (long long)g * a.dh,
+                          a.ldv, keys, a.dh, a.vec, tid);
+      fetch();
+      planes_ready(kvready);
+      for (int j = 0; j < n; ++j, ++c) {
+        const uint32_t st = c % C::kStages;
+        if (c >= C::kStages) mbar_poll(empty(st), ((c / C::kStages) - 1) & 1, limit);
+        const long long r = b.start + (long long)qb * kB;
+        const int have = b.len - qb * kB;
+        unsigned char* q_sm = ring + st * 6 * C::kBlkPlane;
+        bad |= xq.template put<kB>(q_sm, 0, tid);
+        bad |= xg.template put<kB>(q_sm + 3 * C::kBlkPlane, 0, tid);
+        if (tid < kB) {
+          const long long i = (long long)h * a.T + r + tid;
+          const float l = tid < have ? a.lse[i] * kLog2e : 0.f;
+          const float d = tid < have ? a.delta[i] : 0.f;
+          stat[st * 2 * kB + tid] = l;
+          stat[st * 2 * kB + kB + tid] = d;
+          bad |= !isfinite(l) || !isfinite(d);
+        }
+        if (bad) const_cast<WorkSlot*>(slot)->odd = 1;
+        planes_ready(ready(st));
+        if (++qb == nqb) {
+          qb = qb0;
+          ++h;
+        }
+        // The next block's rows are on their way while this one's sums come in.
+        if (j + 1 < n) fetch();
+        if (j > 0) add_block(c - 1);
       }
-      if (bad) *odd = 1;
-      planes_ready(ready(st));
-      if (++qb == nqb) {
-        qb = qb0;
-        ++h;
+      if (lane == 0) mbar_arrive(splitdone);
+      add_block(c - 1);
+      // (rows of a CTA that lost a wait are not written)
+      const int key = b.row0 + 32 * (warp - 4) + lane;
+      if (limit != 0 && key < b.len) {
+        const long long tok = (long long)b.start + key;
+        store_row32<DP>(dv, static_cast<float*>(a.dv) + tok * a.lddv + (long long)g * a.dh, a.dh,
+                        a.vec, 1.f);
+        store_row32<DP>(dk, static_cast<float*>(a.dk) + tok * a.lddk + (long long)g * a.dh, a.dh,
+                        a.vec, a.scale);
+        if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0) plain_dkv_row(a, b, g, key);
       }
-      // The next block's rows are on their way while this one's sums come in.
-      if (j + 1 < n) fetch();
-      if (j > 0) add_block(j - 1);
-    }
-    add_block(n - 1);
-    // (rows of a CTA that lost a wait are not written)
-    const int key = b.row0 + 32 * (warp - 4) + lane;
-    if (limit != 0 && key < b.len) {
-      const long long tok = (long long)b.start + key;
-      store_row32<DP>(dv, static_cast<float*>(a.dv) + tok * a.lddv + (long long)g * a.dh, a.dh,
-                      a.vec, 1.f);
-      store_row32<DP>(dk, static_cast<float*>(a.dk) + tok * a.lddk + (long long)g * a.dh, a.dh,
-                      a.vec, a.scale);
-      if (*reinterpret_cast<volatile uint32_t*>(odd) != 0) plain_dkv_row(a, b, g, key);
-    }
+      __syncwarp();
+    });
   } else {
-    const int key = b.row0 + 32 * warp + lane;                 // within the sequence
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const float sc = a.scale * kLog2e;
     const float2 sc2 = make_float2(sc, sc);
+    uint32_t nb = 0;                           // blocks so far
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int key = b.row0 + 32 * warp + lane;                 // within the sequence
+    const int qb0 = first_block(b), nqb = blocks(b), n = rep * (nqb - qb0);
     int qb = qb0;
-    for (int j = 0; j < n; ++j) {
-      const int st = j % C::kStages;
+    for (int j = 0; j < n; ++j, ++nb) {
+      const int st = nb % C::kStages;
       const float4* lse = reinterpret_cast<const float4*>(stat + st * 2 * kB);
       const float4* del = lse + kB / 4;
-      mbar_poll(sfull, j & 1, limit);
+      mbar_poll(sfull, nb & 1, limit);
       tc_fence_after();
       uint32_t r[kB];
       tc_ld32(tmem + lanes, r);
       tc_ld32(tmem + lanes + 32, r + 32);
-      mbar_poll(ready(st), (j / C::kStages) & 1, limit);       // (lse and delta: long there)
+      mbar_poll(ready(st), (nb / C::kStages) & 1, limit);      // (lse and delta: long there)
       tc_wait_ld();
       float p[kB];
 #pragma unroll
@@ -758,13 +815,13 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
         for (int c = 0; c < kB; ++c)
           if (c < lo || c >= hi) p[c] = 0.f;
       }
-      if (j > 0) mbar_poll(dvdone, (j - 1) & 1, limit);        // P of before has been used
+      if (nb > 0) mbar_poll(dvdone, (nb - 1) & 1, limit);      // P of before has been used
       tc_fence_after();
       store_planes(tmem + lanes + kP, p);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pready);
-      mbar_poll(dpfull, j & 1, limit);
+      mbar_poll(dpfull, nb & 1, limit);
       tc_fence_after();
       tc_ld32(tmem + lanes + kDp, r);
       tc_ld32(tmem + lanes + kDp + 32, r + 32);
@@ -777,7 +834,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
         p[c + 2] *= __uint_as_float(r[c + 2]) - d.z;
         p[c + 3] *= __uint_as_float(r[c + 3]) - d.w;
       }
-      if (j > 0) mbar_poll(dkdone, (j - 1) & 1, limit);        // dS of before has been used
+      if (nb > 0) mbar_poll(dkdone, (nb - 1) & 1, limit);      // dS of before has been used
       tc_fence_after();
       store_planes(tmem + lanes + kDs, p);
       tc_fence_before();
@@ -785,6 +842,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
       if (lane == 0) mbar_arrive(dsready);
       if (++qb == nqb) qb = qb0;
     }
+    });
   }
   if (limit == 0) report(a.status, 0x751);
   tc_fence_before();
@@ -811,28 +869,27 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   unsigned char* ring = sm + 6 * C::kTilePlane;                // [kStages] K, V: 3 planes of 64
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::kStages * 6 * C::kBlkPlane);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  uint32_t* odd = tslot + 1;
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t qready = bar0, dsready = bar0 + 8, dqdone = bar0 + 16, done = bar0 + 24;
   auto sfull = [&](int i) { return bar0 + 32 + 8 * i; };       // S and dP of a block
   auto ready = [&](int st) { return bar0 + 48 + 8 * st; };
   auto empty = [&](int st) { return bar0 + 64 + 8 * st; };
+  const uint32_t qempty = bar0 + 80;
+  const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
+  const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
+                           smem_addr(tslot + 4)};
   // Tensor memory: scores and dP (two buffers each), dS, dQ.
   constexpr int kDp = 128, kDs = 256, kDq = 384;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const int h = blockIdx.x % a.Hq;
-  const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
-  AttnBlock b;
-  if (!attn_find_block(a, slot, 7, &b)) return;
-  const int g = h / (a.Hq / a.Hkv);
-  const int rows = min(kTile, b.len - b.row0);
-  const int n = ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
+  auto blocks = [&](const AttnBlock& b) {
+    return ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)   // qready, dsready, ready: a warp each
       mbar_init(bars + i, i < 2 || i == 6 || i == 7 ? 4 : 1);
-    *odd = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
+    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tslot, 512);
@@ -850,67 +907,92 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       const uint64_t kk = sdesc_k128(ring), vk = sdesc_k128(ring + 3 * C::kBlkPlane);
       const uint64_t kn = sdesc_mn128(ring, kB * 128);
       constexpr uint64_t kStep = 6 * C::kBlkPlane >> 4;
-      auto front = [&](int j) {
-        const int st = j % C::kStages;
-        mbar_poll(ready(st), (j / C::kStages) & 1, limit);
+      uint32_t c = 0, items = 0;               // blocks and query tiles so far
+      auto front = [&](uint32_t x, bool last) {
+        const int st = x % C::kStages;
+        mbar_poll(ready(st), (x / C::kStages) & 1, limit);
         if (elect_one()) {
-          mma_kk3<DP>(tmem + kB * (j & 1), qd, kk + st * kStep);
-          mma_kk3<DP>(tmem + kDp + kB * (j & 1), gd, vk + st * kStep);
-          tc_commit(sfull(j & 1));
+          mma_kk3<DP>(tmem + kB * (x & 1), qd, kk + st * kStep);
+          mma_kk3<DP>(tmem + kDp + kB * (x & 1), gd, vk + st * kStep);
+          tc_commit(sfull(x & 1));
+          if (last) tc_commit(qempty);
         }
         __syncwarp();
       };
-      mbar_poll(qready, 0, limit);
-      front(0);
-      for (int j = 0; j < n; ++j) {
-        // (the buffers of block j + 1 were read before dS of block j - 1 was ready)
-        if (j + 1 < n) front(j + 1);
-        const int st = j % C::kStages;
-        mbar_poll(dsready, j & 1, limit);
-        tc_fence_after();
-        if (elect_one()) {
-          mma_tn3<DP>(tmem + kDq, tmem + kDs, kn + st * kStep);
-          tc_commit(dqdone);
-          tc_commit(empty(st));
+      take_work(ring_w, limit, [&](const WorkSlot* slot) {
+        const int n = blocks(slot->b);
+        mbar_poll(qready, items++ & 1, limit);
+        front(c, n == 1);
+        for (int j = 0; j < n; ++j, ++c) {
+          // (the buffers of the next block were read before dS of the one before was ready)
+          if (j + 1 < n) front(c + 1, j + 2 == n);
+          const int st = c % C::kStages;
+          mbar_poll(dsready, c & 1, limit);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tn3<DP>(tmem + kDq, tmem + kDs, kn + st * kStep);
+            tc_commit(dqdone);
+            tc_commit(empty(st));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
+      });
       if (elect_one()) tc_commit(done);
       __syncwarp();
+    } else if (warp == 9) {
+      // Finds the work, the next block once this one's operands are split.
+      uint32_t items = 0;
+      give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
+        mbar_poll(splitdone, items++ & 1, limit);
+      });
     }
   } else if (warp >= 4) {
     const int tid = threadIdx.x - 128;
-    const long long t0 = b.start + (long long)b.row0, ldo = (long long)a.Hq * a.dh;
-    const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
-    const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
-    Piece<DP> xk, xv;
-    auto fetch = [&](int j) {
-      const long long r0 = (long long)(n - 1 - j) * kB;
-      const int have = b.len - (int)r0;
-      xk.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
-      xv.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
-    };
-    bool bad = put_tile<DP>(q_sm, static_cast<const float*>(a.q) + t0 * a.ldq +
-                                      (long long)h * a.dh, a.ldq, rows, a.dh, a.vec, tid);
-    bad |= put_tile<DP>(g_sm, static_cast<const float*>(a.dO) + t0 * ldo + (long long)h * a.dh,
-                        ldo, rows, a.dh, a.vec, tid);
-    fetch(0);
-    planes_ready(qready);
-    for (int j = 0; j < n; ++j) {
-      const int st = j % C::kStages;
-      if (j >= C::kStages) mbar_poll(empty(st), ((j / C::kStages) - 1) & 1, limit);
-      unsigned char* k_to = ring + st * 6 * C::kBlkPlane;
-      bad |= xk.template put<kB>(k_to, 0, tid);
-      bad |= xv.template put<kB>(k_to + 3 * C::kBlkPlane, 0, tid);
-      if (bad) *odd = 1;
-      planes_ready(ready(st));
-      if (j + 1 < n) fetch(j + 1);
-    }
+    const long long ldo = (long long)a.Hq * a.dh;
+    uint32_t c = 0, items = 0;
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+      const AttnBlock b = slot->b;
+      const int h = slot->h;
+      const int g = h / (a.Hq / a.Hkv), n = blocks(b), rows = min(kTile, b.len - b.row0);
+      const long long t0 = b.start + (long long)b.row0;
+      const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
+      const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
+      Piece<DP> xk, xv;
+      auto fetch = [&](int j) {
+        const long long r0 = (long long)(n - 1 - j) * kB;
+        const int have = b.len - (int)r0;
+        xk.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
+        xv.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
+      };
+      if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+      ++items;
+      bool bad = put_tile<DP>(q_sm, static_cast<const float*>(a.q) + t0 * a.ldq +
+                                        (long long)h * a.dh, a.ldq, rows, a.dh, a.vec, tid);
+      bad |= put_tile<DP>(g_sm, static_cast<const float*>(a.dO) + t0 * ldo + (long long)h * a.dh,
+                          ldo, rows, a.dh, a.vec, tid);
+      fetch(0);
+      planes_ready(qready);
+      for (int j = 0; j < n; ++j, ++c) {
+        const uint32_t st = c % C::kStages;
+        if (c >= C::kStages) mbar_poll(empty(st), ((c / C::kStages) - 1) & 1, limit);
+        unsigned char* k_to = ring + st * 6 * C::kBlkPlane;
+        bad |= xk.template put<kB>(k_to, 0, tid);
+        bad |= xv.template put<kB>(k_to + 3 * C::kBlkPlane, 0, tid);
+        if (bad) const_cast<WorkSlot*>(slot)->odd = 1;
+        planes_ready(ready(st));
+        if (j + 1 < n) fetch(j + 1);
+      }
+      if (lane == 0) mbar_arrive(splitdone);
+    });
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const float sc = a.scale * kLog2e;
+    uint32_t nb = 0;                           // blocks so far
+    take_work(ring_w, limit, [&](const WorkSlot* slot) {
+    const AttnBlock b = slot->b;
+    const int h = slot->h, g = h / (a.Hq / a.Hkv), n = blocks(b);
+    const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     const bool live = row < b.len;
     const long long at = (long long)h * a.T + b.start + row;
     const float lse = live ? a.lse[at] * kLog2e : 0.f, del = live ? a.delta[at] : 0.f;
@@ -918,9 +1000,9 @@ attn_tc32_dq_kernel(const AttnArgs a) {
     float dq[DP];
 #pragma unroll
     for (int c = 0; c < DP; ++c) dq[c] = 0.f;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t ts = tmem + lanes + kB * (j & 1);
-      mbar_poll(sfull(j & 1), (j >> 1) & 1, limit);
+    for (int j = 0; j < n; ++j, ++nb) {
+      const uint32_t ts = tmem + lanes + kB * (nb & 1);
+      mbar_poll(sfull(nb & 1), (nb >> 1) & 1, limit);
       tc_fence_after();
       uint32_t r[kB];
       tc_ld32(ts, r);
@@ -949,7 +1031,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
           if (c > last) p[c] = 0.f;
       }
       if (j > 0) {
-        mbar_poll(dqdone, (j - 1) & 1, limit);                 // dS of before has been used
+        mbar_poll(dqdone, (nb - 1) & 1, limit);                // dS of before has been used
         tc_fence_after();
         add_columns<DP>(dq, tmem + lanes + kDq);
       }
@@ -958,7 +1040,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(dsready);
     }
-    mbar_poll(done, 0, limit);
+    mbar_poll(dqdone, (nb - 1) & 1, limit);
     // (rows of a CTA that lost a wait are not written)
     if (__all_sync(0xffffffffu, limit != 0)) {
       tc_fence_after();
@@ -966,8 +1048,11 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       if (live)
         store_row32<DP>(dq, static_cast<float*>(a.dq) + ((long long)b.start + row) * a.lddq +
                                 (long long)h * a.dh, a.dh, a.vec, a.scale);
-      if (live && *reinterpret_cast<volatile uint32_t*>(odd) != 0) plain_dq_row(a, b, h, g, row);
+      if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
+        plain_dq_row(a, b, h, g, row);
+      tc_fence_before();                       // read before the next block's products
     }
+    });
   }
   if (limit == 0) report(a.status, 0x761);
   tc_fence_before();

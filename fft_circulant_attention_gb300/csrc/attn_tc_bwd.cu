@@ -258,7 +258,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (lane == 0) pdl_trigger();
       int st = 0, used = 0, items = 0;
       uint32_t round = 0;
-      give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock& b, int g) {
+      give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock& b, int g, WorkSlot*) {
         const DkvWork<W> w = DkvWork<W>::of(b, a.causal);
         if (items > 0) mbar_poll(kvempty, (items - 1) & 1, limit);
         ++items;
@@ -593,7 +593,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (warp == kHelp) {
       int st = 0, used = 0, items = 0;
       uint32_t round = 0;
-      give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock& b, int h) {
+      give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock& b, int h, WorkSlot*) {
         const int g = h / (a.Hq / a.Hkv);
         if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
         if (lane == 0) {
