@@ -182,7 +182,7 @@ attn_fwd_kernel(const AttnArgs a) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int h = blockIdx.x % a.Hq;
   const int slot = (int)(gridDim.x / a.Hq) - 1 - (int)(blockIdx.x / a.Hq);
-  if (blockIdx.x == 0) attn_check_sequences(a);
+  if (blockIdx.x == 0) attn_check_sequences(a, threadIdx.x, kThr);
   AttnBlock b;
   if (!attn_find_block(a, slot, 6, &b)) return;
   const int g = h / (a.Hq / a.Hkv);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThr)
 attn_delta_kernel(const AttnArgs a) {
   const long long i = (long long)blockIdx.x * (kThr / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) attn_check_sequences(a);
+  if (blockIdx.x == 0) attn_check_sequences(a, threadIdx.x, kThr);
   if (i >= (long long)a.T * a.Hq) return;
   const T* o = static_cast<const T*>(a.o) + i * a.dh;
   const T* d = static_cast<const T*>(a.dO) + i * a.dh;

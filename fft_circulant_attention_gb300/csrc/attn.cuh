@@ -42,10 +42,11 @@ struct AttnBlock {
   int row0;                // the block's first row within the sequence
 };
 
-// The grid's first CTA looks over the whole of cu (the search below may pass
-// over a fault): entries that do not ascend within 0 .. T are reported.
-__device__ __forceinline__ void attn_check_sequences(const AttnArgs& a) {
-  for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
+// Looks over the whole of cu (the search below may pass over a fault), `step`
+// threads from thread `first` on: entries that do not ascend within 0 .. T are
+// reported.
+__device__ __forceinline__ void attn_check_sequences(const AttnArgs& a, int first, int step) {
+  for (int i = first; i < a.S; i += step) {
     const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
     if (c0 < 0 || c1 < c0 || c1 > a.T) report(a.status, 0x701);
   }

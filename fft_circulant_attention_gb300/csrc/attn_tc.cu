@@ -109,7 +109,6 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                          smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (blockIdx.x == 0) attn_check_sequences(a);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 21 + 3 * C::kStages; ++i) mbar_init(bars + i, 1);
     for (int t = 0; t < 2; ++t) {

@@ -154,6 +154,7 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
       load(b, h, ring.slots + ((count - 1) & 1));
       __syncwarp();
     }
+    if (item == 0) attn_check_sequences(a, lane, 32);
     // Asked only now, with this block's copies issued: a block taken over early
     // would wait here while another SM ran dry.
     if (lane == 0) {

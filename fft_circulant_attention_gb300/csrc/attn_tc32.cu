@@ -349,7 +349,6 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
     return ((a.causal ? min(b.len, b.row0 + kTile) : b.len) + kB - 1) / kB;
   };
 
-  if (blockIdx.x == 0) attn_check_sequences(a);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)   // qready, pready, kready, vready: a warp each
       mbar_init(bars + i, i == 0 || i == 1 || (i >= 6 && i < 10) ? 4 : 1);

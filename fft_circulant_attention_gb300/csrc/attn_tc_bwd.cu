@@ -154,7 +154,7 @@ __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, in
 __global__ void __launch_bounds__(256)
 attn_stats_kernel(const AttnArgs a, int slots) {
   pdl_trigger();
-  if (blockIdx.x == 0) attn_check_sequences(a);
+  if (blockIdx.x == 0) attn_check_sequences(a, threadIdx.x, 256);
   const int slot = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
   AttnBlock b;
   if (!attn_find_block(a, slot, 7, &b)) return;

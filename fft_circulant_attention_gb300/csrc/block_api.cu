@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -206,6 +207,13 @@ bool rows_aligned(const cat_plan_s* p, std::initializer_list<const void*> ptrs,
   return true;
 }
 
+// Whether bf16 rows this far apart fit a tensor map (strides below 2^40 bytes).
+bool mappable(std::initializer_list<long long> lds) {
+  for (long long l : lds)
+    if (l >= (1ll << 39)) return false;
+  return true;
+}
+
 }  // namespace
 
 int cat_attn_forward(cat_plan_t p, const void* Q, const void* K, const void* V, void* O,
@@ -228,7 +236,8 @@ int cat_attn_forward(cat_plan_t p, const void* Q, const void* K, const void* V, 
   a.out = O;
   a.lse = lse;
   a.vec = rows_aligned(p, {Q, K, V, O}, {ldq, ldk, ldv}, 4 * es);
-  a.tc = es == 2 && rows_aligned(p, {Q, K, V, O}, {ldq, ldk, ldv}, 16);
+  a.tc = es == 2 && rows_aligned(p, {Q, K, V, O}, {ldq, ldk, ldv}, 16) &&
+         mappable({ldq, ldk, ldv});
   DeviceGuard dev(p->device);
   if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   return status_of(cat::launch_attn_forward(p, a));
@@ -271,7 +280,8 @@ int cat_attn_backward(cat_plan_t p, const void* Q, const void* K, const void* V,
   a.lddq = lddq; a.lddk = lddk; a.lddv = lddv;
   a.vec = rows_aligned(p, {Q, K, V, O, dO, dQ, dK, dV}, {ldq, ldk, ldv, lddq, lddk, lddv}, 4 * es);
   a.tc = es == 2 &&
-         rows_aligned(p, {Q, K, V, O, dO, dQ, dK, dV}, {ldq, ldk, ldv, lddq, lddk, lddv}, 16);
+         rows_aligned(p, {Q, K, V, O, dO, dQ, dK, dV}, {ldq, ldk, ldv, lddq, lddk, lddv}, 16) &&
+         mappable({ldq, ldk, ldv});
   DeviceGuard dev(p->device);
   if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   return status_of(cat::launch_attn_backward(p, a));
@@ -281,7 +291,8 @@ int cat_plan_create_layernorm(cat_plan_t* out, int max_rows, int D, int dtype, f
                               void* stream) {
   if (!out) return CAT_ERR_INVALID_ARG;
   *out = nullptr;
-  if (max_rows < 0 || D < 1 || D > CAT_MAX_D) return CAT_ERR_INVALID_ARG;
+  if (max_rows < 0 || max_rows > CAT_NORM_MAX_ROWS || D < 1 || D > CAT_MAX_D)
+    return CAT_ERR_INVALID_ARG;
   if (dtype != CAT_F32 && dtype != CAT_BF16) return CAT_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.f) return CAT_ERR_INVALID_ARG;
   int st;

@@ -308,9 +308,12 @@ int cat_plan_create_attn(cat_plan_t *out, int max_tokens, int max_seqs, int Hq,
  * ascending int values within 0 .. T.  Rows that no sequence holds (before
  * cu_seqlens[0], from cu_seqlens[S] on) are neither read into any result nor
  * written; a sequence may be empty.  Pointers need the alignment of their
- * element type; bf16 data whose rows and heads all start on 16-byte
- * boundaries takes the faster tensor-core kernels.  A pair the mask excludes
- * contributes nothing, whatever its rows hold.  If cu_seqlens is not
+ * element type.  bf16 data whose rows and heads all start on 16-byte
+ * boundaries, and fp32 data (its backward up to dh = 64), take the tensor
+ * cores; the rest takes the FP32 pipe, an order of magnitude slower.  On the
+ * tensor cores bf16 probabilities are rounded to bf16 and fp32 operands are
+ * split into three bf16 terms (errors of fp32's own size).  A pair the mask
+ * excludes contributes nothing, whatever its rows hold.  If cu_seqlens is not
  * ascending within 0 .. T, the sequences concerned are skipped and
  * cat_plan_sync returns CAT_ERR_DEVICE_STATUS.
  * Errors: CAT_ERR_PLAN_MISMATCH (not an attention plan, T or S above the
@@ -338,9 +341,13 @@ int cat_attn_backward(cat_plan_t plan, const void *Q, const void *K,
                       long long ldk, long long ldv, long long lddq,
                       long long lddk, long long lddv);
 
+/* Most rows of one layer-norm call. */
+#define CAT_NORM_MAX_ROWS (1 << 30)
+
 /*
  * cat_plan_create_layernorm — layer norm over rows of D elements
- * (1 <= D <= CAT_MAX_D), at most max_rows of them a call (>= 0); eps >= 0.
+ * (1 <= D <= CAT_MAX_D), at most max_rows of them a call (0 ..
+ * CAT_NORM_MAX_ROWS); eps >= 0.
  * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
  */
 int cat_plan_create_layernorm(cat_plan_t *out, int max_rows, int D, int dtype,

@@ -44,7 +44,7 @@ def test_attn_plan_refuses(lib, args):
 
 @pytest.mark.parametrize("args", [
     (-1, 64, 0, 1e-5), (4, 0, 0, 1e-5), (4, 8193, 0, 1e-5), (4, 64, 5, 1e-5), (4, 64, 0, -1e-5),
-    (4, 64, 0, math.nan), (4, 64, 0, math.inf),
+    (4, 64, 0, math.nan), (4, 64, 0, math.inf), (2**30 + 1, 1, 0, 1e-5),
 ])
 def test_layernorm_plan_refuses(lib, args):
     h = ctypes.c_void_p()
