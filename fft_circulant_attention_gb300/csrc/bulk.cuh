@@ -64,30 +64,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return false;
 }
 
-// A wait without a branch on its outcome, for roles whose loops must stay
-// short: polls at most `limit` times; a wait that is lost sets limit to 0, so
-// that the role's later waits pass at once and its loop ends (the caller
-// reports a limit of 0 there).  bar: shared-memory address.
-__device__ __forceinline__ void mbar_poll(uint32_t bar, uint32_t parity, uint32_t& limit) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n"
-      "POLL:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra END;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 p, n, %0;\n\t"
-      "@p bra POLL;\n\t"
-      "mov.u32 %0, 0;\n"
-      "END:\n\t}"
-      : "+r"(limit)
-      : "r"(bar), "r"(parity)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // Bulk copy of `bytes` bytes from global `src` to shared `dst`, completing
 // on `bar`.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,
@@ -118,16 +94,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Tiled 3-D tensor copy (TMA) of the box at (c0, c1, c2) into shared memory.
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1,
-                                            int c2, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
       : "memory");
 }
 
@@ -202,14 +168,6 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
 bool encode_map_2d_sw128(CUtensorMap* map, const void* base, unsigned long long cols,
                          unsigned long long rows, unsigned long long row_bytes,
                          unsigned int box_cols, unsigned int box_rows);
-
-// Host: encode the heads of token rows, bf16 [rows][heads][width] with rows
-// row_bytes apart, as a 3-D map (width, heads, rows) with 128-byte swizzle and
-// a box of 64 columns of one head by box_rows rows (columns from `width` on
-// and rows outside are filled with zeros).
-bool encode_map_heads_sw128(CUtensorMap* map, const void* base, unsigned long long width,
-                            unsigned long long heads, unsigned long long rows,
-                            unsigned long long row_bytes, unsigned int box_rows);
 
 // Host: encode a 4-D tiled tensor map (no interleave, no swizzle).  dims and
 // box are innermost first; strides are the byte strides of dims 1..3.

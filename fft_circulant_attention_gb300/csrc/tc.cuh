@@ -10,6 +10,48 @@
 
 namespace cat {
 
+// A wait without a branch on its outcome, for roles whose loops must stay
+// short: polls at most `limit` times; a wait that is lost sets limit to 0, so
+// that the role's later waits pass at once and its loop ends (the caller
+// reports a limit of 0 there).  bar: shared-memory address.
+__device__ __forceinline__ void mbar_poll(uint32_t bar, uint32_t parity, uint32_t& limit) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra END;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 p, n, %0;\n\t"
+      "@p bra POLL;\n\t"
+      "mov.u32 %0, 0;\n"
+      "END:\n\t}"
+      : "+r"(limit)
+      : "r"(bar), "r"(parity)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiled 3-D tensor copy (TMA) of the box at (c0, c1, c2) into shared memory.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Host: encode the heads of token rows, bf16 [rows][heads][width] with rows
+// row_bytes apart, as a 3-D map (width, heads, rows) with 128-byte swizzle and
+// a box of 64 columns of one head by box_rows rows (columns from `width` on
+// and rows outside are filled with zeros).
+bool encode_map_heads_sw128(CUtensorMap* map, const void* base, unsigned long long width,
+                            unsigned long long heads, unsigned long long rows,
+                            unsigned long long row_bytes, unsigned int box_rows);
+
 // Tensor memory: one warp allocates `ncols` columns (a power of two, >= 32)
 // for all 128 lanes and writes the base address to shared memory; the same
 // warp frees them.  The permit is given up right after so that other CTAs

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "bulk.cuh"
+#include "tc.cuh"
 
 namespace cat {
 
