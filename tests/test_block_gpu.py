@@ -75,6 +75,91 @@ def test_attn_longer(dtype, dh, causal):
     attn_parity([1111, 640, 383], 2, 1, dh, dtype, causal, seed=5)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,dh", [
+    ([4096], 64), ([4097], 64), ([4351], 64), ([5003, 3200], 64), ([4500], 40), ([4200, 4000], 8),
+], ids=str)
+def test_attn_long_sequences(lens, dh, causal):
+    # From 4096 rows a sequence (on average) a CTA of the bf16 forward takes
+    # two tiles of rows; sequences that end in either tile.
+    attn_parity(lens, 2, 1, dh, "bf16", causal, seed=sum(lens) + dh)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("at", [3, 4100, 4239, 4299])
+def test_attn_long_masked_values_do_not_leak(value, at):
+    # As in short sequences: a value of one token reaches the rows that see it.
+    n = 4300
+    q, k, v, do, cu = ref.attn_inputs([n], 1, 1, 64, "bf16", 12, extra=30)
+    val, b = ref.attention(q, k, v, do, cu, True, "bf16")["o"]
+    for which in ("k", "v"):
+        t = dict(k=k.clone(), v=v.clone())
+        for x in t.values():
+            x[n:] = value
+        t[which][at, :, 3] = value
+        got = run_attn(q, t["k"], t["v"], do, cu, True, "bf16", backward=False)
+        check("o", got["o"][:at], (val[:at], b[:at]))
+        if which == "v":
+            assert not got["o"][at:n, 0, 3].isfinite().any()
+            check("o", got["o"][at:n, 0, 4:], (val[at:n, 0, 4:], b[at:n, 0, 4:]))
+
+
+@pytest.mark.parametrize("lens", [[300], [4400]])
+def test_attn_full_masked_tail(lens):
+    # Not causal: what lies behind the sequence, in its last block, is not read.
+    n = lens[0]
+    q, k, v, do, cu = ref.attn_inputs(lens, 2, 2, 64, "bf16", 13, extra=200)
+    want = ref.attention(q, k, v, do, cu, False, "bf16")
+    for t in (q, k, v, do):
+        t[n:] = math.inf
+    got = run_attn(q, k, v, do, cu, False, "bf16")
+    for name in want:
+        check(name, got[name], want[name])
+
+
+def test_attn_f32_wide_heads_masked_values_do_not_leak():
+    # fp32 rows wider than 64, forward and backward.
+    n, at = 200, 130
+    q, k, v, do, cu = ref.attn_inputs([n, 40], 2, 1, 96, "f32", 14)
+    want = ref.attention(q, k, v, do, cu, True, "f32")
+    for which in ("k", "v"):
+        t = dict(k=k.clone(), v=v.clone())
+        t[which][at, :, 70] = math.nan
+        got = run_attn(q, t["k"], t["v"], do, cu, True, "f32")
+        for name in ("o", "dq"):
+            for rows in (slice(0, at), slice(n, None)):
+                check(name, got[name][rows], tuple(x[rows] for x in want[name]))
+        for name in ("dk", "dv"):
+            check(name, got[name][n:], tuple(x[n:] for x in want[name]))
+        assert not got["o"][at:n, :, 70 if which == "v" else 0].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attn_two_plans_on_two_streams(dtype):
+    # Each plan has its own workspace: calls that run at the same time.
+    lens = [333, 90, 257]
+    q, k, v, do, cu = ref.attn_inputs(lens, 4, 2, 64, dtype, 15)
+    ins = [t.to(DEV) for t in (q, k, v, do)]
+    cd = cu.to(DEV)
+    want = run_attn(q, k, v, do, cu, True, dtype)
+    T = q.shape[0]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    plans = [cat.AttnPlan(T, 3, 4, 2, 64, dtype, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s, plan in zip(streams, plans):
+            with torch.cuda.stream(s):
+                o, lse = plan.forward(*ins[:3], cd)
+                got.append((o, lse) + tuple(plan.backward(*ins[:3], o, lse, ins[3], cd)))
+    torch.cuda.synchronize()
+    for r in got:
+        for name, t in zip(("o", "lse", "dq", "dk", "dv"), r):
+            assert torch.equal(t, want[name]), name
+    for plan in plans:
+        plan.close()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attn_peaked_and_scaled(dtype):
     # Near one-hot rows: scores of some tens; and a scale of the caller's own.
