@@ -7,7 +7,7 @@ Circular-Convolutional Attention for Sub-Quadratic Transformers", section
 tokens, and O_h = circ(z*)·V_h = IFFT(FFT(z*) ⊙ FFT(V_h)).
 
 This module only marshals arguments (tensor -> device pointer, stream ->
-handle, status -> exception).  Every step of the computation runs in the
+handle, status -> exception; the operator plans' calls do it natively).  Every step of the computation runs in the
 CUDA kernels of ``libcat.so``; there is no other implementation behind it,
 and importing it fails loudly when the library has not been built.
 
@@ -27,9 +27,7 @@ for convenience.  The operators around a CAT layer in a training step are
 ``cat_layernorm_backward`` (``LayerNormPlan``), ``cat_plan_create_clip``,
 ``cat_grad_norm`` and ``cat_grad_clip`` (``ClipPlan``).
 """
-import array
 import ctypes
-import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -523,9 +521,35 @@ class Plan2D:
             pass
 
 
+_MARSHAL = None
+
+
+def _marshal():
+    """The native marshalling of the operator plans' calls (csrc/marshal.cpp),
+    built for the running torch.  Raises if it has not been built."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        import importlib.machinery
+        import importlib.util
+
+        from .build import marshal_path
+        path = marshal_path()
+        if not os.path.exists(path):
+            raise RuntimeError(
+                "%s is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`" % path)
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(m)
+        _MARSHAL = m
+    return _MARSHAL
+
+
 class _OpPlan:
     """What the operator plans share.  With a stream given, every call runs on
     it; without one, on torch's current stream at the call."""
+
+    handle = None
 
     def _open(self, device, stream):
         import torch
@@ -535,36 +559,30 @@ class _OpPlan:
             torch.device(device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self._empty = torch.empty          # (Tensor.new_empty takes twice the time)
         self._fixed = stream is not None
         self._on = _stream(stream) if self._fixed else None
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self._index = self.device.index
+
+    def _native(self, names, dims=(0, 0, 0), dtype=CAT_F32):
+        """What the native calls need: the plan, its shape, the C functions."""
+        fns = [ctypes.cast(getattr(lib(), n), _P).value for n in names]
+        self._names = names
+        self._args = _marshal().make(*fns, self.handle, *dims, dtype, self._index)
 
     def _use(self):
         """Point the plan at the stream this call runs on."""
-        if not self._fixed:
-            s = self._current(self.device.index)
-            if s != self._on:
-                cat_plan_set_stream(self.handle, s)
-                self._on = s
+        s = self._current(self._index)
+        if s != self._on:
+            cat_plan_set_stream(self.handle, s)
+            self._on = s
 
-    def _tensor(self, t, name, dtype, shape=None, rows=False):
-        """`t` on the plan's device, of `dtype` and `shape`, contiguous (`rows`:
-        contiguous within each token row).  Returns its address."""
-        if t.device != self.device:
-            raise ValueError("%s is on %s, the plan on %s" % (name, t.device, self.device))
-        if t.dtype != dtype:
-            raise ValueError("%s must be %s" % (name, dtype))
-        if shape is not None and t.shape != shape:
-            raise ValueError("%s must have shape %s" % (name, tuple(shape)))
-        if rows:
-            st, w = t.stride(), t.shape[2]
-            if t.numel() and ((w > 1 and st[2] != 1) or (t.shape[1] > 1 and st[1] != w)):
-                raise ValueError("%s: the heads of a token row must be contiguous" % name)
-        elif not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return t.data_ptr()
+    def _done(self, r, which):
+        """The outputs of a native call, or its error."""
+        if r.__class__ is int:
+            raise CatError(r, self._names[which])
+        return r
 
     def sync(self):
         cat_plan_sync(self.handle)
@@ -573,7 +591,8 @@ class _OpPlan:
         return cat_plan_describe(self.handle)
 
     def close(self):
-        if getattr(self, "handle", None):
+        if self.handle:
+            self._args = None                 # (a later call is refused)
             cat_plan_destroy(self.handle)
             self.handle = None
 
@@ -610,70 +629,24 @@ class AttnPlan(_OpPlan):
 
     def __init__(self, max_tokens, max_seqs, Hq, Hkv, dh, dtype, causal=True, scale=None,
                  stream=None, device=None):
-        import torch
         self.Hq, self.Hkv, self.dh = Hq, Hkv, dh
         self.dtype = dtype_code(dtype)
-        self.torch_dtype = torch.bfloat16 if self.dtype == CAT_BF16 else torch.float32
         self._open(device, stream)
         with _on_device(self.device):
             self.handle = cat_plan_create_attn(max_tokens, max_seqs, Hq, Hkv, dh, self.dtype,
                                                causal, 0.0 if scale is None else scale, self._on)
-        self._fwd, self._bwd = lib().cat_attn_forward, lib().cat_attn_backward
-        self._f32, self._i32 = torch.float32, torch.int32
-
-    def _rows(self, t, name, shape):
-        """Address and row stride of a [T, heads, dh] operand."""
-        p = self._tensor(t, name, self.torch_dtype, shape, rows=True)
-        # A single row has no stride of its own (torch may report any).
-        return p, t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
-
-    def _inputs(self, Q, K, V, cu_seqlens):
-        T = Q.shape[0]
-        kv = (T, self.Hkv, self.dh)
-        q, ldq = self._rows(Q, "Q", (T, self.Hq, self.dh))
-        k, ldk = self._rows(K, "K", kv)
-        v, ldv = self._rows(V, "V", kv)
-        cu = self._tensor(cu_seqlens, "cu_seqlens", self._i32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens must have S + 1 entries")
-        return T, cu_seqlens.shape[0] - 1, cu, (q, k, v), (ldq, ldk, ldv)
+        self._native(("cat_attn_forward", "cat_attn_backward"), (Hq, Hkv, dh), self.dtype)
+        self._fwd, self._bwd = _marshal().attn_forward, _marshal().attn_backward
 
     def forward(self, Q, K, V, cu_seqlens, O=None, lse=None):
-        T, S, cu, ptrs, lds = self._inputs(Q, K, V, cu_seqlens)
-        if O is None:
-            O = self._empty((T, self.Hq, self.dh), dtype=self.torch_dtype, device=self.device)
-            o = O.data_ptr()
-        else:
-            o = self._tensor(O, "O", self.torch_dtype, (T, self.Hq, self.dh))
-        if lse is None:
-            lse = self._empty((self.Hq, T), dtype=self._f32, device=self.device)
-            z = lse.data_ptr()
-        else:
-            z = self._tensor(lse, "lse", self._f32, (self.Hq, T))
-        self._use()
-        st = self._fwd(self.handle, *ptrs, o, z, cu, T, S, *lds)
-        if st:
-            raise CatError(st, "cat_attn_forward")
-        return O, lse
+        if not self._fixed:
+            self._use()
+        return self._done(self._fwd(self._args, Q, K, V, cu_seqlens, O, lse), 0)
 
     def backward(self, Q, K, V, O, lse, dO, cu_seqlens, dQ=None, dK=None, dV=None):
-        T, S, cu, ptrs, lds = self._inputs(Q, K, V, cu_seqlens)
-        q, kv = (T, self.Hq, self.dh), (T, self.Hkv, self.dh)
-        o = self._tensor(O, "O", self.torch_dtype, q)
-        do = self._tensor(dO, "dO", self.torch_dtype, q)
-        z = self._tensor(lse, "lse", self._f32, (self.Hq, T))
-        kind = dict(dtype=self.torch_dtype, device=self.device)
-        dQ = self._empty(q, **kind) if dQ is None else dQ
-        dK = self._empty(kv, **kind) if dK is None else dK
-        dV = self._empty(kv, **kind) if dV is None else dV
-        dq, lddq = self._rows(dQ, "dQ", q)
-        dk, lddk = self._rows(dK, "dK", kv)
-        dv, lddv = self._rows(dV, "dV", kv)
-        self._use()
-        st = self._bwd(self.handle, *ptrs, o, z, do, dq, dk, dv, cu, T, S, *lds, lddq, lddk, lddv)
-        if st:
-            raise CatError(st, "cat_attn_backward")
-        return dQ, dK, dV
+        if not self._fixed:
+            self._use()
+        return self._done(self._bwd(self._args, Q, K, V, O, lse, dO, cu_seqlens, dQ, dK, dV), 1)
 
 
 class LayerNormPlan(_OpPlan):
@@ -685,56 +658,23 @@ class LayerNormPlan(_OpPlan):
     """
 
     def __init__(self, max_rows, D, dtype, eps=1e-5, stream=None, device=None):
-        import torch
         self.D = D
         self.dtype = dtype_code(dtype)
-        self.torch_dtype = torch.bfloat16 if self.dtype == CAT_BF16 else torch.float32
         self._open(device, stream)
         with _on_device(self.device):
             self.handle = cat_plan_create_layernorm(max_rows, D, self.dtype, eps, self._on)
-        self._fwd, self._bwd = lib().cat_layernorm_forward, lib().cat_layernorm_backward
-        self._f32 = torch.float32
-
-    def _inputs(self, X, gamma, beta=None):
-        if X.dim() < 1 or X.shape[-1] != self.D:
-            raise ValueError("the last dimension must be %d" % self.D)
-        x = self._tensor(X, "X", self.torch_dtype)
-        w = None if gamma is None else self._tensor(gamma, "gamma", self.torch_dtype, (self.D,))
-        b = None if beta is None else self._tensor(beta, "beta", self.torch_dtype, (self.D,))
-        return X.numel() // self.D, x, w, b
-
-    def _out(self, t, name, shape, dtype):
-        if t is None:
-            t = self._empty(shape, dtype=dtype, device=self.device)
-            return t, t.data_ptr()
-        return t, self._tensor(t, name, dtype, shape)
+        self._native(("cat_layernorm_forward", "cat_layernorm_backward"), (D, 0, 0), self.dtype)
+        self._fwd, self._bwd = _marshal().ln_forward, _marshal().ln_backward
 
     def forward(self, X, gamma=None, beta=None, Y=None, mean=None, rstd=None):
-        rows, x, w, b = self._inputs(X, gamma, beta)
-        lead = X.shape[:-1]
-        Y, y = self._out(Y, "Y", X.shape, self.torch_dtype)
-        mean, m = self._out(mean, "mean", lead, self._f32)
-        rstd, r = self._out(rstd, "rstd", lead, self._f32)
-        self._use()
-        st = self._fwd(self.handle, x, w, b, y, m, r, rows)
-        if st:
-            raise CatError(st, "cat_layernorm_forward")
-        return Y, mean, rstd
+        if not self._fixed:
+            self._use()
+        return self._done(self._fwd(self._args, X, gamma, beta, Y, mean, rstd), 0)
 
     def backward(self, X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None):
-        rows, x, w, _ = self._inputs(X, gamma)
-        lead = X.shape[:-1]
-        dy = self._tensor(dY, "dY", self.torch_dtype, X.shape)
-        m = self._tensor(mean, "mean", self._f32, lead)
-        r = self._tensor(rstd, "rstd", self._f32, lead)
-        dX, dx = self._out(dX, "dX", X.shape, self.torch_dtype)
-        dgamma, dg = self._out(dgamma, "dgamma", (self.D,), self.torch_dtype)
-        dbeta, db = self._out(dbeta, "dbeta", (self.D,), self.torch_dtype)
-        self._use()
-        st = self._bwd(self.handle, x, w, m, r, dy, dx, dg, db, rows)
-        if st:
-            raise CatError(st, "cat_layernorm_backward")
-        return dX, dgamma, dbeta
+        if not self._fixed:
+            self._use()
+        return self._done(self._bwd(self._args, X, gamma, mean, rstd, dY, dX, dgamma, dbeta), 1)
 
 
 class ClipPlan(_OpPlan):
@@ -747,54 +687,24 @@ class ClipPlan(_OpPlan):
     """
 
     def __init__(self, sizes, dtypes, stream=None, device=None):
-        import torch
         self.sizes = [int(n) for n in sizes]
-        self.dtypes = [torch.bfloat16 if dtype_code(d) == CAT_BF16 else torch.float32
-                       for d in dtypes]
+        self.dtypes = [dtype_code(d) for d in dtypes]
         self._open(device, stream)
         with _on_device(self.device):
             self.handle = cat_plan_create_clip(self.sizes, self.dtypes, self._on)
-        self._norm, self._clip = lib().cat_grad_norm, lib().cat_grad_clip
-        self._f32, self._T = torch.float32, torch.Tensor
-        self._dtype_of = operator.attrgetter("dtype")
-
-    def _list(self, tensors, name):
-        """The tensors' addresses, as an array of the C interface."""
-        if len(tensors) != len(self.sizes):
-            raise ValueError("%d %s for a plan of %d" % (len(tensors), name, len(self.sizes)))
-        # (one attribute of all tensors at a time: half the time of a loop)
-        T = self._T
-        if (list(map(T.numel, tensors)) != self.sizes or
-                list(map(self._dtype_of, tensors)) != self.dtypes or
-                not all(map(T.is_contiguous, tensors)) or
-                set(map(T.get_device, tensors)) - {self.device.index}):
-            raise ValueError("%s must be contiguous, of the plan's sizes, dtypes and device" % name)
-        return array.array("Q", map(T.data_ptr, tensors))
-
-    def _scalar(self, norm):
-        if norm is None:
-            norm = self._empty((), dtype=self._f32, device=self.device)
-            return norm, norm.data_ptr()
-        return norm, self._tensor(norm, "norm", self._f32, ())
+        self._native(("cat_grad_norm", "cat_grad_clip"))
+        _marshal().set_list(self._args, self.sizes, self.dtypes)
+        self._clip = _marshal().clip
 
     def norm(self, grads, norm=None):
-        ptrs = self._list(grads, "grads")
-        norm, n = self._scalar(norm)
-        self._use()
-        st = self._norm(self.handle, ptrs.buffer_info()[0], n)
-        if st:
-            raise CatError(st, "cat_grad_norm")
-        return norm
+        if not self._fixed:
+            self._use()
+        return self._done(self._clip(self._args, grads, None, None, norm), 0)
 
     def clip(self, grads, max_norm, out=None, norm=None):
-        ptrs = self._list(grads, "grads")
-        outs = ptrs if out is None or out is grads else self._list(out, "out")
-        norm, n = self._scalar(norm)
-        self._use()
-        st = self._clip(self.handle, ptrs.buffer_info()[0], outs.buffer_info()[0], max_norm, n)
-        if st:
-            raise CatError(st, "cat_grad_clip")
-        return norm
+        if not self._fixed:
+            self._use()
+        return self._done(self._clip(self._args, grads, out, float(max_norm), norm), 1)
 
 
 __all__ = ["AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",

@@ -1,8 +1,11 @@
-"""Build libcat.so (the CUDA library behind include/cat.h) in-tree.
+"""Build libcat.so (the CUDA library behind include/cat.h) in-tree, and the
+native marshalling of the Python binding's operator plans beside it.
 
 Each translation unit is compiled by nvcc for sm_103a in parallel, then
 linked into ``fft_circulant_attention_gb300/libcat.so``.  The CUDA runtime
 is linked statically, so the library depends only on the driver.
+``_marshal-<torch version>.so`` is a Python extension without kernels,
+compiled against the running torch.
 """
 import concurrent.futures as cf
 import os
@@ -32,8 +35,34 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def marshal_path():
+    import torch
+    return os.path.join(HERE, "_marshal-%s.so" % torch.__version__)
+
+
+def _build_marshal():
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    src, out = os.path.join(CSRC, "marshal.cpp"), marshal_path()
+    if os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):
+        return
+    tmp = out + ".tmp.%d" % os.getpid()
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + sysconfig.get_paths()["include"], *("-isystem" + i for i in inc), src,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, out)
+
+
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     files.append(os.path.join(INCLUDE, "cat.h"))
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
@@ -42,6 +71,7 @@ def _deps():
 def build(force=False, verbose=False, extra=()):
     """Compile every .cu under csrc/ and link libcat.so; return its path."""
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+        _build_marshal()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -59,8 +89,10 @@ def build(force=False, verbose=False, extra=()):
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, srcs))
+        marshal.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
