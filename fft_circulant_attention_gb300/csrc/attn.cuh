@@ -77,6 +77,71 @@ __device__ __forceinline__ bool attn_find_block(const AttnArgs& a, int slot, int
   return blk >= 0 && blk <= ((c1 - c0) >> shift) && b->row0 < b->len;
 }
 
+// The block of rank `r`, the largest amount of work first, by one whole warp;
+// for up to kSortedSeqs sequences.  A causal sequence of m blocks has one
+// block of each size 1 .. m (rising: the last row's block is the largest,
+// else the first one's), one that is not causal m blocks of size m.  So the
+// number of blocks above a size k is a sum over the sequences, and size and
+// sequence of rank r are found from such sums, without a sorted list in
+// memory that another call's kernel could be reading.
+constexpr int kSortedSeqs = 128;
+__device__ __forceinline__ bool attn_find_by_size(const AttnArgs& a, int r, int shift, bool rising,
+                                                  AttnBlock* b) {
+  const int lane = threadIdx.x & 31;
+  int m[kSortedSeqs / 32];
+#pragma unroll
+  for (int i = 0; i < kSortedSeqs / 32; ++i) {
+    const int s = 32 * i + lane;
+    m[i] = 0;
+    if (s < a.S) {
+      const int c0 = __ldg(a.cu + s), c1 = __ldg(a.cu + s + 1);
+      if (c0 >= 0 && c1 >= c0 && c1 <= a.T) m[i] = (c1 - c0 + (1 << shift) - 1) >> shift;
+    }
+  }
+  auto above = [&](int k) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kSortedSeqs / 32; ++i)
+      n += a.causal ? max(m[i] - k, 0) : m[i] > k ? m[i] : 0;
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  if (r >= above(0)) return false;
+  int lo = 0, size = 0;                      // above(lo) > r >= above(size)
+#pragma unroll
+  for (int i = 0; i < kSortedSeqs / 32; ++i) size = max(size, m[i]);
+  size = __reduce_max_sync(0xffffffffu, size);
+  while (size - lo > 1) {
+    const int mid = (lo + size) >> 1;
+    if (above(mid) > r)
+      lo = mid;
+    else
+      size = mid;
+  }
+  r -= above(size);
+  int blk = 0, seq = -1;
+  if (!a.causal) {
+    blk = r % size;
+    r /= size;
+  }
+  // The r-th of the sequences that have blocks of this size.
+#pragma unroll
+  for (int i = 0; i < kSortedSeqs / 32; ++i) {
+    const bool in = a.causal ? m[i] >= size : m[i] == size;
+    const unsigned mask = __ballot_sync(0xffffffffu, in);
+    const unsigned at = __ballot_sync(
+        0xffffffffu, in && __popc(mask & ((1u << lane) - 1u)) == r);
+    if (at) seq = 32 * i + __ffs(at) - 1;
+    r -= __popc(mask);
+  }
+  if (seq < 0) return false;
+  b->seq = seq;
+  b->start = __ldg(a.cu + seq);
+  b->len = __ldg(a.cu + seq + 1) - b->start;
+  if (a.causal) blk = rising ? size - 1 : ((b->len + (1 << shift) - 1) >> shift) - size;
+  b->row0 = blk << shift;
+  return true;
+}
+
 __host__ __device__ inline long long attn_slots(int T, int S, int shift) {
   return (long long)(T >> shift) + S;
 }

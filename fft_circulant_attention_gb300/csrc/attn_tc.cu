@@ -303,12 +303,22 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty(t));
       }
-      if (blk >= w.cut) {
-        // The last key this row sees, within the block.
-        const int last = (a.causal ? min(row, b.len - 1) : b.len - 1) - blk * kTile;
+      int kind[kTile / 32];
 #pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c > last) r[c] = 0xff800000u;
+      for (int x = 0; x < kTile / 32; ++x) kind[x] = kEveryColumn;
+      if (blk >= w.cut) {
+        // The keys this row sees end before column hi of the block.
+        const int hi = (a.causal ? min(row + 1, b.len) : b.len) - blk * kTile;
+#pragma unroll
+        for (int x = 0; x < kTile / 32; ++x) {
+          kind[x] = chunk_kind(0, hi - 32 * x);
+          if (kind[x] != kEveryColumn) {
+            const uint32_t bits = chunk_bits(0, hi - 32 * x);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(bits >> c & 1u)) r[32 * x + c] = 0xff800000u;
+          }
+        }
       }
       float mx[4];
 #pragma unroll

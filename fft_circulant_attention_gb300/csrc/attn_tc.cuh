@@ -37,6 +37,23 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// A mask cuts a block of scores along a row's columns lo .. hi - 1.  Chunks of
+// 32 columns are told apart by whole warps, so that only those that the edge
+// runs through are masked value by value (a compare and a select on the pipe
+// of half rate, which for 64 columns took longer than their exponentials) and
+// those behind it are not computed at all.
+enum Chunk { kNoColumn = 0, kSomeColumns = 1, kEveryColumn = 2 };
+__device__ __forceinline__ int chunk_kind(int lo, int hi) {
+  if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) return kEveryColumn;
+  return __all_sync(0xffffffffu, lo >= 32 || hi <= 0 || hi <= lo) ? kNoColumn : kSomeColumns;
+}
+// The chunk's columns as bits.
+__device__ __forceinline__ uint32_t chunk_bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+}
+
 // A bf16 half whose exponent is all ones (an infinity or NaN) sets the high
 // bit of its half: adding one to the exponent carries there.
 __device__ __forceinline__ uint32_t odd2(uint32_t w) {
@@ -125,9 +142,12 @@ struct WorkRing {
 };
 
 // The copy warp's loop: load(block, head, slot) for each of the CTA's blocks,
-// in slots of 2^shift rows by `heads` heads, the last slots first if `reverse`.
+// in blocks of 2^shift rows by `heads` heads.  rising: under a causal mask the
+// work of a block grows with its row.  The largest blocks come first where
+// there are few sequences; where there are many, blocks are small beside the
+// work of an SM, and they are taken as they lie.
 template <typename F>
-__device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shift, bool reverse,
+__device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shift, bool rising,
                                           const WorkRing& ring, uint32_t& limit, F load) {
   const int lane = threadIdx.x & 31;
   int item = blockIdx.x, count = 0;
@@ -147,9 +167,15 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
   for (uint32_t par = 0;; par ^= 1u) {
     const int h = item % heads;
     int slot = item / heads;
-    if (reverse) slot = (int)(gridDim.x / heads) - 1 - slot;
     AttnBlock b;
-    if (attn_find_block(a, slot, shift, &b)) {
+    bool found;
+    if (a.S <= kSortedSeqs) {
+      found = attn_find_by_size(a, slot, shift, rising, &b);
+    } else {
+      if (rising) slot = (int)(gridDim.x / heads) - 1 - slot;
+      found = attn_find_block(a, slot, shift, &b);
+    }
+    if (found) {
       publish(b, h, 1);
       load(b, h, ring.slots + ((count - 1) & 1));
       __syncwarp();

@@ -139,6 +139,19 @@ __device__ __forceinline__ void store_half2(uint32_t taddr, const float* v) {
   tc_wait_st();
 }
 
+// Columns outside lo .. hi - 1 of a half become zero, in chunks of 32.
+__device__ __forceinline__ void mask_half(float* p, int lo, int hi) {
+#pragma unroll
+  for (int c0 = 0; c0 < kHalf; c0 += 32) {
+    const int kind = chunk_kind(lo - c0, hi - c0);
+    if (kind == kEveryColumn) continue;
+    const uint32_t bits = chunk_bits(lo - c0, hi - c0);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!(bits >> c & 1u)) p[c0 + c] = 0.f;
+  }
+}
+
 // f · accumulator columns c0 .. c1 - 1 of this thread's lane to a bf16 row.
 __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, int c0, int c1,
                                           float f, bool live, bool wide) {
@@ -444,11 +457,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const bool cut = w.is_cut(qb);
       const int q0 = qb * W + half * kHalf;
       const int lo = a.causal ? key - q0 : 0, hi = b.len - q0;
-      if (cut) {
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c)
-          if (c < lo || c >= hi) p[c] = 0.f;
-      }
+      if (cut) mask_half(p, lo, hi);
       store_half(ts, p);
       tc_fence_before();
       __syncwarp();
@@ -470,12 +479,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         p[c + 2] *= y.x;
         p[c + 3] *= y.y;
       }
-      if (cut) {
-        // (0 times a delta or dP that is not finite)
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c)
-          if (c < lo || c >= hi) p[c] = 0.f;
-      }
+      if (cut) mask_half(p, lo, hi);           // (0 times a delta or dP that is not finite)
       store_half2(tdp, p);
       tc_fence_before();
       __syncwarp();
@@ -763,12 +767,8 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         p[c + 1] *= x.y;
       }
       if (is_cut(b, n - 1 - j)) {
-        // The last key this row sees, within the half block.
-        const int last =
-            (a.causal ? min(row, b.len - 1) : b.len - 1) - (n - 1 - j) * W - half * kHalf;
-#pragma unroll
-        for (int c = 0; c < kHalf; ++c)
-          if (c > last) p[c] = 0.f;
+        // The keys this row sees end before this column of the half block.
+        mask_half(p, 0, (a.causal ? min(row + 1, b.len) : b.len) - (n - 1 - j) * W - half * kHalf);
       }
       store_half2(tdp, p);
       tc_fence_before();
