@@ -262,11 +262,13 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int blk = w.n - 1; blk >= 0; --blk) {
           mbar_poll(full(st), round, limit);
           if (blk >= w.cut) {
-            if (clean_tile<DP>(kv_sm + (2 * st + 1) * C::kTileBytes,
-                               slot->b.len - blk * kTile) && lane == 0)
-              const_cast<WorkSlot*>(slot)->odd = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
+            unsigned char* v_sm = kv_sm + (2 * st + 1) * C::kTileBytes;
+            if (odd_tile<DP>(v_sm)) {
+              if (clean_tile<DP>(v_sm, slot->b.len - blk * kTile) && lane == 0)
+                const_cast<WorkSlot*>(slot)->odd = 1;
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
           if (lane == 0) mbar_arrive(clean(st));
           if (++st == C::kStages) {

@@ -64,21 +64,27 @@ __device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
   return w & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
 }
 
-// A [ROWS][DP] tile in shared memory, by one warp: values that are not
-// finite become zero.  True if one of them lay in a row below `rows`.  The
-// first pass only looks (9 operations per 8 values: about 0.3 us a tile of 64
-// columns, hidden behind the block's scores).
+// Whether a [ROWS][DP] tile in shared memory holds a value that is not finite,
+// by one warp (9 operations per 8 values: about 0.3 us a tile of 128 x 64).
 template <int DP, int ROWS = kTile>
-__device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
+__device__ __forceinline__ bool odd_tile(const unsigned char* tile) {
   constexpr int kVec = ROWS * DP * 2 / 16;
-  uint4* v = reinterpret_cast<uint4*>(tile);
+  const uint4* v = reinterpret_cast<const uint4*>(tile);
   uint32_t any = 0;
 #pragma unroll 16
   for (int i = threadIdx.x & 31; i < kVec; i += 32) {
     const uint4 x = v[i];
     any |= odd2(x.x) | odd2(x.y) | odd2(x.z) | odd2(x.w);
   }
-  if (!__any_sync(0xffffffffu, (any & 0x80008000u) != 0)) return false;
+  return __any_sync(0xffffffffu, (any & 0x80008000u) != 0);
+}
+
+// Values of the tile that are not finite become zero.  True if one of them lay
+// in a row below `rows`.
+template <int DP, int ROWS = kTile>
+__device__ __forceinline__ bool clean_tile(unsigned char* tile, int rows) {
+  constexpr int kVec = ROWS * DP * 2 / 16;
+  uint4* v = reinterpret_cast<uint4*>(tile);
   bool found = false;
 #pragma unroll 1
   for (int i = threadIdx.x & 31; i < kVec; i += 32) {

@@ -52,7 +52,7 @@ namespace cat {
 namespace {
 
 constexpr int kHalf = 64;                  // columns of a block that a row's thread takes
-constexpr int kNumBars = 32;               // room for every barrier
+constexpr int kNumBars = 40;               // room for every barrier
 
 // NH: warpgroups of a CTA, and blocks of 64·NH on the other side.
 template <int NH>
@@ -235,12 +235,15 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t kvfull = bar0, dpfull = bar0 + 8, dsready = bar0 + 16, dkdone = bar0 + 24;
-  const uint32_t clean = bar0 + 32, done = bar0 + 40;
+  const uint32_t done = bar0 + 40;
   const uint32_t sfull = bar0 + 48, dvdone = bar0 + 80;
   auto pready = [&](int i) { return bar0 + 64 + 8 * i; };
-  const uint32_t cutgo = bar0 + 96, kvempty = bar0 + 104;
+  const uint32_t kvempty = bar0 + 104;
   auto full = [&](int st) { return bar0 + 152 + 8 * st; };
   auto empty = [&](int st) { return bar0 + 152 + 8 * (C::kStages + st); };
+  // A stage's blocks have been looked through; S and dP have been made of them.
+  auto clean = [&](int st) { return bar0 + 152 + 8 * (2 * C::kStages + st); };
+  auto used_up = [&](int st) { return bar0 + 152 + 8 * (3 * C::kStages + st); };
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 112,
                            smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -321,7 +324,6 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         mbar_poll(kvfull, items++ & 1, limit);
         const int n = rep * (w.nqb - w.qb0);
-        int qb = w.qb0;
         for (int j = 0; j < n; ++j, ++c) {
           const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
           mbar_poll(full(st), round, limit);
@@ -338,13 +340,11 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           tc_fence_after();
           if (elect_one()) {
             mma_kk<DP, W>(tmem + C::kDp, vd, gd + at);
+            tc_commit(used_up(st));
             tc_commit(dpfull);
-            // A cut block has served as it came: it can be cleaned.
-            if (w.is_cut(qb)) tc_commit(cutgo);
             if (j == n - 1) tc_commit(kvempty);
           }
           __syncwarp();
-          if (++qb == w.nqb) qb = w.qb0;
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;
@@ -355,14 +355,14 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const uint64_t qd = sdesc_mn128(ring, W * 128);
       const uint64_t gd = sdesc_mn128(ring + C::kBlkBytes, W * 128);
       int st = 0;
-      uint32_t ncut = 0, c = 0;
+      uint32_t round = 0, c = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         const int n = rep * (w.nqb - w.qb0);
         int qb = w.qb0;
         for (int j = 0; j < n; ++j, ++c) {
           const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
-          if (w.is_cut(qb)) mbar_poll(clean, ncut++ & 1, limit);
+          if (w.is_cut(qb)) mbar_poll(clean(st), round, limit);
           // (the first of a block: both warpgroups have read the last one's dV, dK)
           mbar_poll(pready(c & 1), (c >> 1) & 1, limit);
           tc_fence_after();
@@ -380,34 +380,44 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tc_commit(empty(st));
           }
           __syncwarp();
-          if (++st == C::kStages) st = 0;
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
           if (++qb == w.nqb) qb = w.qb0;
         }
       });
       if (elect_one()) tc_commit(done);
       __syncwarp();
     } else {
-      // (the next cut block waits for the products of this one, so the phases
-      // of cutgo and clean are taken one by one)
+      // Cut blocks are looked through as they land, ahead of their products;
+      // what has to be taken out waits until S and dP have been made of it.
       int st = 0;
-      uint32_t ncut = 0;
+      uint32_t round = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const DkvWork<W> w = DkvWork<W>::of(slot->b, a.causal);
         const int n = rep * (w.nqb - w.qb0);
         int qb = w.qb0;
         for (int j = 0; j < n; ++j) {
+          mbar_poll(full(st), round, limit);
           if (w.is_cut(qb)) {
-            mbar_poll(cutgo, ncut++ & 1, limit);
             unsigned char* q_sm = ring + st * 2 * C::kBlkBytes;
-            const int rows = slot->b.len - qb * W;
-            clean_tile<DP, W>(q_sm, rows);
-            if (clean_tile<DP, W>(q_sm + C::kBlkBytes, rows) && lane == 0)
-              const_cast<WorkSlot*>(slot)->odd = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(clean);
+            const bool q_odd = odd_tile<DP, W>(q_sm), g_odd = odd_tile<DP, W>(q_sm + C::kBlkBytes);
+            if (q_odd || g_odd) {
+              mbar_poll(used_up(st), round, limit);
+              const int rows = slot->b.len - qb * W;
+              clean_tile<DP, W>(q_sm, rows);
+              if (clean_tile<DP, W>(q_sm + C::kBlkBytes, rows) && lane == 0)
+                const_cast<WorkSlot*>(slot)->odd = 1;
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
-          if (++st == C::kStages) st = 0;
+          if (lane == 0) mbar_arrive(clean(st));
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
           if (++qb == w.nqb) qb = w.qb0;
         }
       });
@@ -561,10 +571,11 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   constexpr int kQ1 = 17 + 2 * C::kStages;
   auto qfull = [&](int i) { return bar0 + 8 * (i & 1 ? kQ1 : 0); };
   auto sfull = [&](int i) { return bar0 + 48 + 8 * i; };
-  auto cutgo = [&](int i) { return bar0 + 64 + 8 * i; };
-  auto clean = [&](int i) { return bar0 + 80 + 8 * i; };
   auto full = [&](int st) { return bar0 + 136 + 8 * st; };
   auto empty = [&](int st) { return bar0 + 136 + 8 * (C::kStages + st); };
+  // A stage's K has been looked through; S has been made of it.
+  auto clean = [&](int st) { return bar0 + 8 * (kQ1 + 1) + 8 * st; };
+  auto used_up = [&](int st) { return bar0 + 8 * (kQ1 + 1) + 8 * (C::kStages + st); };
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 96,
                            smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -640,25 +651,22 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const uint64_t qd = sdesc_k128(q_sm), gd = sdesc_k128(q_sm + C::kTileBytes);
       const uint64_t kd = sdesc_k128(ring), vd = sdesc_k128(ring + C::kBlkBytes);
       int st = 0, items = 0;
-      uint32_t round = 0, c = 0, ncut = 0;
+      uint32_t round = 0, c = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const int n = blocks(slot->b);
         mbar_poll(qfull(items), (items >> 1) & 1, limit);
         ++items;
         for (int j = 0; j < n; ++j, ++c) {
           const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
-          const bool cut = is_cut(slot->b, n - 1 - j);
           mbar_poll(full(st), round, limit);
           // (S's buffer was read before dS of two blocks ago was ready, which the
           // wait below for the product of that dS has shown.)
           if (elect_one()) {
             mma_kk<DP, W>(tmem + C::s(c & 1), qd, kd + at);
+            tc_commit(used_up(st));
             tc_commit(sfull(c & 1));
-            // K of a cut block has served as it came: it can be cleaned.
-            if (cut) tc_commit(cutgo(ncut & 1));
           }
           __syncwarp();
-          if (cut) ++ncut;
           // dP's columns are free once the dQ product has read dS from them.
           if (c >= 1) mbar_poll(dqdone, (c - 1) & 1, limit);
           tc_fence_after();
@@ -677,15 +685,12 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     } else if (warp == kHelp + 2) {
       const uint64_t kd = sdesc_mn128(ring, W * 128);
       int st = 0;
-      uint32_t c = 0, ncut = 0;
+      uint32_t round = 0, c = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         const int n = blocks(slot->b);
         for (int j = 0; j < n; ++j, ++c) {
           const uint64_t at = st * (uint64_t)(2 * C::kBlkBytes >> 4);
-          if (is_cut(slot->b, n - 1 - j)) {
-            mbar_poll(clean(ncut & 1), (ncut >> 1) & 1, limit);
-            ++ncut;
-          }
+          if (is_cut(slot->b, n - 1 - j)) mbar_poll(clean(st), round, limit);
           // (the first of a block: both warpgroups have read the last one's dQ)
           mbar_poll(dsready, c & 1, limit);
           tc_fence_after();
@@ -696,27 +701,32 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tc_commit(empty(st));
           }
           __syncwarp();
-          if (++st == C::kStages) st = 0;
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
         }
       });
       if (elect_one()) tc_commit(done);
       __syncwarp();
     } else {
-      // A cut block's scores may be there before the one before is cleaned, but
-      // not those of the block after it: two barriers in turn.
       int st = 0;
-      uint32_t ncut = 0;
+      uint32_t round = 0;
       take_work(ring_w, limit, [&](const WorkSlot* slot) {
         for (int blk = blocks(slot->b) - 1; blk >= 0; --blk) {
-          if (is_cut(slot->b, blk)) {
-            mbar_poll(cutgo(ncut & 1), (ncut >> 1) & 1, limit);
-            clean_tile<DP, W>(ring + st * 2 * C::kBlkBytes, 0);
+          mbar_poll(full(st), round, limit);
+          unsigned char* k_sm = ring + st * 2 * C::kBlkBytes;
+          if (is_cut(slot->b, blk) && odd_tile<DP, W>(k_sm)) {
+            mbar_poll(used_up(st), round, limit);
+            clean_tile<DP, W>(k_sm, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(clean(ncut & 1));
-            ++ncut;
           }
-          if (++st == C::kStages) st = 0;
+          if (lane == 0) mbar_arrive(clean(st));
+          if (++st == C::kStages) {
+            st = 0;
+            round ^= 1u;
+          }
         }
       });
     }
