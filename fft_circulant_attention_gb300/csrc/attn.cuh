@@ -84,6 +84,12 @@ __device__ __forceinline__ bool attn_find_block(const AttnArgs& a, int slot, int
 // number of blocks above a size k is a sum over the sequences, and size and
 // sequence of rank r are found from such sums, without a sorted list in
 // memory that another call's kernel could be reading.
+//
+// Against blocks as they lie (12 heads of 64, bf16 forward and backward, us):
+// 16 documents of 57 .. 1024 tokens 25.0 for 27.8, 84.0 for 92.1; 8 x 1024 24.8
+// for 27.2, 79.2 for 89.2; 128 documents of 20 .. 200 tokens 30.9 for 31.0, 92.9
+// for 92.9, where the last block is small whatever the order: so this search,
+// whose cost grows with the sequences, ends there.
 constexpr int kSortedSeqs = 128;
 __device__ __forceinline__ bool attn_find_by_size(const AttnArgs& a, int r, int shift, bool rising,
                                                   AttnBlock* b) {

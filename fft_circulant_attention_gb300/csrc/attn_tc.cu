@@ -2,22 +2,35 @@
 // (tcgen05), for bf16 rows that start on 16-byte boundaries, head width a
 // multiple of 8 up to 128 (padded to 64 or 128 by the copies' zero fill).
 //
-// A CTA takes 256 query rows of one head as two tiles of 128 (the MMA's M,
-// one tensor-memory lane a row) and walks their keys in blocks of 128, from
-// the diagonal (or the sequence's end) down to row 0, in one pass with a
-// running maximum and sum.  Roles:
-//   - warps 0-3 and 4-7, one warpgroup a tile, one thread a row: scores from
-//     tensor memory to registers, mask, maximum, exponentials, and the
-//     probabilities back to tensor memory as bf16 pairs;
-//   - warp 8 issues the tensor copies of Q, K and V (ring of key blocks);
-//   - warps 9 and 10, one a tile, issue the MMAs: S = Q·K^T into 128 columns,
-//     and O += P·V with P as the tensor-memory operand A;
-//   - warp 11 looks for infinities and NaN in V blocks that the mask cuts
+// A CTA works on NT tiles of 128 query rows of one head (the MMA's M, one
+// tensor-memory lane a row) and walks their keys in blocks of 128, from the
+// diagonal (or the sequence's end) down to row 0, in one pass with a running
+// maximum and sum.  CTAs are persistent: the next block of work is loaded
+// while this one's last products run.  Roles, after NT warpgroups of rows:
+//   - a warpgroup a tile, one thread a row: scores from tensor memory to
+//     registers, mask, maximum, exponentials, and the probabilities back to
+//     tensor memory as bf16 pairs;
+//   - one warp finds the work and issues the tensor copies of Q, K and V (ring
+//     of key blocks);
+//   - a warp a tile issues the MMAs: S = Q·K^T into 128 columns, and O += P·V
+//     with P as the tensor-memory operand A;
+//   - one warp looks for infinities and NaN in V blocks that the mask cuts
 //     (below).
 // While one tile's warpgroup works on its scores the tensor core runs the
-// other tile's products.  At head width 64 P has columns of its own and the
-// next block's scores are computed while P is still being made; at 128 the
-// 512 columns are full and P takes the place of its scores.
+// other tile's products; with NT = 1 the two tiles are two CTAs on an SM.  At
+// head width 64 P has columns of its own and the next block's scores are
+// computed while P is still being made; at 128 the 512 columns are full and P
+// takes the place of its scores.
+//
+// Bound by the row warps: 16384 causal tokens of 16 heads over 4 (two such
+// sequences and one of 4999) take 928 us, 1.24 PFLOP/s or 65 % of the measured
+// bf16 rate; a block takes two tiles 2200 clocks, of which their 32768
+// exponentials alone want 1024 of each of the four units' time twice over with
+// the scaling, maxima, sums and packing beside them (1520 measured without any
+// wait), and the MMAs and copies alone 1505.  Four row warpgroups (two a tile)
+// gained nothing.  Short documents (16 up to 1024 tokens, 12 heads) take 21 us
+// against 7.5 for their bytes: each CTA has three blocks of work, and the
+// first copies, the last products and the rows' stores of each are a chain.
 //
 // The maximum is followed lazily: while a block raises it by less than 2^8
 // the old one stays (probabilities up to 2^8 and their fp32 sum lose nothing
@@ -38,8 +51,14 @@ namespace cat {
 
 namespace {
 
-constexpr int kNumBars = 64;               // room for every barrier
-constexpr int kLongRows = 4096;            // average length from which a CTA takes two tiles
+constexpr int kNumBars = 40;               // room for every barrier
+// Average length from which a CTA of head width 64 takes two tiles: they share
+// the copies of K and V, but the work comes in larger pieces.  12 heads, causal,
+// one tile against two (us): 16 documents of 57 .. 1024 tokens 25.2, 26.9;
+// 8 x 1024 24.8, 24.9; 4 x 2048 35.0, 35.1; 4 x 4096 111.3, 103.6; 8192 102.3,
+// 100.7; 16384 372.9, 347.3.  (At 128 a tile's tensor memory fills half the SM's
+// and two tiles are one CTA.)
+constexpr int kLongRows = 4096;
 constexpr float kLazy = 8.f;               // log2 of the growth that is let pass
 
 template <int DP, int NT>
@@ -100,25 +119,23 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   auto pfull = [&](int t) { return bar0 + 64 + 8 * t; };    // probabilities in tensor memory
   auto odone = [&](int t) { return bar0 + 80 + 8 * t; };    // P·V is done
   auto done = [&](int t) { return bar0 + 96 + 8 * t; };     // every MMA is done
-  auto turn = [&](int t) { return bar0 + 112 + 8 * t; };
-  auto full = [&](int st) { return bar0 + 168 + 8 * st; };
-  auto empty = [&](int st) { return bar0 + 168 + 8 * (C::kStages + st); };
+  auto full = [&](int st) { return bar0 + 152 + 8 * st; };
+  auto empty = [&](int st) { return bar0 + 152 + 8 * (C::kStages + st); };
   // The V block of a stage has been looked through, where the mask cuts it.
-  auto clean = [&](int st) { return bar0 + 168 + 8 * (2 * C::kStages + st); };
-  const WorkRing ring = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 128,
+  auto clean = [&](int st) { return bar0 + 152 + 8 * (2 * C::kStages + st); };
+  const WorkRing ring = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 112,
                          smem_addr(tslot + 4)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 21 + 3 * C::kStages; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 19 + 3 * C::kStages; ++i) mbar_init(bars + i, 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bars + 6 + t, 4);                    // sempty, pfull, turn: a tile's warps
+      mbar_init(bars + 6 + t, 4);                    // sempty, pfull: a tile's warps
       mbar_init(bars + 8 + t, 4);
-      mbar_init(bars + 14 + t, 4);
-      mbar_init(bars + 18 + t, 4 * NT + NT + 1);     // a slot's readers
+      mbar_init(bars + 16 + t, 4 * NT + NT + 1);     // a slot's readers
     }
     for (int s = 0; s < C::kStages; ++s)
-      mbar_init(bars + 21 + C::kStages + s, NT);     // empty: each tile's MMAs
+      mbar_init(bars + 19 + C::kStages + s, NT);     // empty: each tile's MMAs
     mbar_fence_init();
   }
   if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
@@ -157,7 +174,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           ++used;
           if (limit == 0) break;
           if (lane == 0) {
-            uint64_t* bar = bars + 21 + st;
+            uint64_t* bar = bars + 19 + st;
             unsigned char* k_sm = kv_sm + 2 * st * C::kTileBytes;
             const int row = b.start + blk * kTile;
             mbar_expect_tx(bar, 2 * C::kTileBytes);
@@ -285,7 +302,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t ts = tmem + lanes + C::s(t), tp = tmem + lanes + C::p(t);
     const uint32_t to = tmem + lanes + C::o(t);
     const float sc = a.scale * kLog2e;
-    uint32_t nb = 0, nturn = 0;                // the tile's blocks and turns so far
+    uint32_t nb = 0;                           // the tile's blocks so far
     take_work(ring, limit, [&](const WorkSlot* slot) {
     const AttnBlock b = slot->b;
     const int h = slot->h, g = h / (a.Hq / a.Hkv);
@@ -344,13 +361,6 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       const float base = m == -INFINITY ? 0.f : m;
       const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
-      // At head width 128 the tiles' warpgroups take turns at the
-      // exponentials, tile 1 first (it has as many blocks as tile 0 or one
-      // more): the MMAs of both tiles otherwise finish together and leave the
-      // tensor core idle while both make probabilities (16 x 16384 tokens:
-      // 1614 us, 1735 without turns; at 64, where the next scores are ready
-      // ahead, 1272 and 1130).
-      if (!C::kOwnP && (t == 0 ? w.top[1] > 0 : it > 0)) mbar_poll(turn(t), nturn++ & 1, limit);
 #pragma unroll
       for (int c0 = 0; c0 < kTile; c0 += 32) {
         uint32_t p[16];
@@ -386,8 +396,6 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         tc_st16(tp + c0 / 2, p);
       }
-      if (!C::kOwnP && (t == 0 ? it + 1 < w.top[1] : it < w.top[0]) && lane == 0)
-        mbar_arrive(turn(1 - t));
       tc_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -27,9 +27,17 @@
 // At head width 64 a CTA has one warpgroup of rows, works on blocks of 64 of
 // the other side and takes half of the 512 columns, so that two CTAs share an
 // SM and one's chain of waits runs beside the other's (12 heads, 16 documents
-// up to 1024 tokens: dK and dV 56.5 us with one CTA of two warpgroups, 54.4
-// with two; dQ 41.4 and 37.7; 8192 tokens: 212 and 204, 193 and 165).  At 128
-// the accumulators fill the columns: two warpgroups, blocks of 128.
+// up to 1024 tokens: all three kernels 83.6 us, 91.3 with one CTA of two
+// warpgroups; 8192 tokens: 371 and 396).  At 128 the accumulators fill the
+// columns: two warpgroups, blocks of 128.
+//
+// Bound by the row warps' chain at 64: a block of 64 takes an SM 1150 clocks
+// where the exponentials want 512 and the MMAs 640 (8192 tokens: 1.28 PFLOP/s
+// counting nine products, 67 % of the measured bf16 rate), and by the MMAs, at
+// the card's power limit, at 128 (16 heads over 4, 8192 + 4095 + 3757 tokens:
+// 574 us for dK and dV, 493 for dQ, 1.5 PFLOP/s counting the nine products).
+// Short documents: 48 us for dK and dV and 34 for dQ, with 2.3 us of each
+// block of work between its last product and the next one's first.
 //
 // P is rounded to bf16 (half a step 2^-8 of each value) as an MMA operand, dS
 // to two bf16 terms whose sum is within 2^-16: a row of dS sums to zero, and
