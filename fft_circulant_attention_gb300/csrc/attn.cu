@@ -22,6 +22,11 @@
 //
 // A masked pair contributes nothing even where the masked row holds an
 // infinity or NaN: blocks that the mask cuts take the guarded product loops.
+//
+// Bound by shared-memory reads beside the FP32 pipe.  Measured, 12 heads of 64,
+// 16 documents of 57 .. 1024 tokens: forward 444 us and backward 1413 us in bf16
+// at odd addresses, where the tensor-core kernels take 25 and 84 us; backward of
+// fp32 heads of 128 3128 us (of 64, on the tensor cores, 414).
 #include "attn.cuh"
 #include "../../include/cat.h"
 #include "cat_internal.h"

@@ -24,8 +24,15 @@
 //     outside the sequence and columns beyond the head width become zeros;
 //   - warp 8 issues the MMAs, warp 9 finds the work (10 and 11 only complete
 //     the warpgroup).
-// Bound by the MMAs (six times 128·64·64 a product) with the splitting of the
-// operands and of the probabilities beside them.
+// Bound by the MMAs (six times 128·64·64 a product): at 64 columns each takes
+// about 51 clocks, not the 32 of its operations, whether its A operand comes
+// from shared or tensor memory (Q's planes in tensor memory: 671 us for 632).
+// The splitting of operands and probabilities runs beside them: having K and V
+// under way together gained 2 % there and lost 2 % in short sequences.
+// Measured: 12 heads of 64,
+// 8192 causal tokens, 632 us forward, 1329 for dK and dV, 869 for dQ (1.9, 4.1
+// and 2.6 us a block of 128 x 64); 64 images of 196 tokens, 6 heads, 69 us
+// forward (223 us a pass on the FP32 pipe).
 //
 // Values that are not finite (or too large for bf16) do not split.  A CTA
 // that met one, or whose masks could have hidden one, computes its rows again

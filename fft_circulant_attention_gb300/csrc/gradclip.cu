@@ -9,6 +9,9 @@
 // gridDim-th chunk; kernel 2 adds those sums (every CTA for itself, in the
 // same fixed order: no atomics, results repeat bit for bit) and scales its
 // chunks, last chunk first, since the last ones read are still in L2.
+// Measured on 133 tensors of 85 M elements, nearly all bf16: 34 us for the norm
+// (5.0 TB/s, 73 % of the measured copy rate; 37 with two CTAs an SM) and 54 us
+// for the scaling (6.3 TB/s, 93 %).
 //
 // Squares leave the fp32 range long before the values do, so a vector whose
 // largest magnitude is beyond 2^±50 is scaled by 2^∓80 before squaring and
@@ -24,6 +27,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kFew = 64, kMany = 1000;      // tensors of one launch
 constexpr int kUnroll = 4;      // 16-byte loads in flight a thread: 512·4·16 = one chunk
+constexpr int kNormPerSm = 4, kScalePerSm = 2;   // CTAs an SM holds (by their registers)
 
 template <int N>
 struct Ptrs {
@@ -277,7 +281,8 @@ cudaError_t run(const ClipCfg& c, const void* const* in, void* const* out, float
     const int n = fill(g, &first);
     const int c0 = c.first_chunk[first], nc = c.first_chunk[first + n] - c0;
     if (nc == 0 && g > 0) continue;             // (group 0 always writes the norm)
-    const int grid = nc < 1 ? 1 : nc < c.grid ? nc : c.grid;
+    const int most = c.grid / kNormPerSm * kScalePerSm;
+    const int grid = nc < 1 ? 1 : nc < most ? nc : most;
     if (g == 0) {
       e = launch_dependent(clip_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, st, ptrs,
                            (const ClipChunk*)(c.chunks + c0), nc, first, (const double*)c.part,
@@ -294,7 +299,7 @@ cudaError_t run(const ClipCfg& c, const void* const* in, void* const* out, float
 }  // namespace
 
 int clip_chunk_elems(int dtype) { return dtype == CAT_BF16 ? 16384 : 8192; }
-int clip_grid(int sms) { return 2 * sms; }
+int clip_grid(int sms) { return kNormPerSm * sms; }
 int clip_max_parts(int count, int sms) { return ((count + kMany - 1) / kMany + 1) * clip_grid(sms); }
 
 cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
