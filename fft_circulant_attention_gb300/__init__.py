@@ -547,7 +547,8 @@ def _marshal():
 
 class _OpPlan:
     """What the operator plans share.  With a stream given, every call runs on
-    it; without one, on torch's current stream at the call."""
+    it, and outputs that the call allocates belong to it; without one, all is
+    on torch's current stream at the call."""
 
     handle = None
 
@@ -561,6 +562,11 @@ class _OpPlan:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._fixed = stream is not None
         self._on = _stream(stream) if self._fixed else None
+        if self._fixed:
+            self._under = torch.cuda.stream
+            self._own = stream if hasattr(stream, "cuda_stream") else \
+                torch.cuda.ExternalStream(self._on, self.device) if self._on else \
+                torch.cuda.default_stream(self.device)
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
         self._index = self.device.index
@@ -578,8 +584,14 @@ class _OpPlan:
             cat_plan_set_stream(self.handle, s)
             self._on = s
 
-    def _done(self, r, which):
-        """The outputs of a native call, or its error."""
+    def _call(self, which, fn, *tensors):
+        """The outputs of a native call on the plan's stream, or its error."""
+        if self._fixed:
+            with self._under(self._own):
+                r = fn(self._args, *tensors)
+        else:
+            self._use()
+            r = fn(self._args, *tensors)
         if r.__class__ is int:
             raise CatError(r, self._names[which])
         return r
@@ -639,14 +651,10 @@ class AttnPlan(_OpPlan):
         self._fwd, self._bwd = _marshal().attn_forward, _marshal().attn_backward
 
     def forward(self, Q, K, V, cu_seqlens, O=None, lse=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._fwd(self._args, Q, K, V, cu_seqlens, O, lse), 0)
+        return self._call(0, self._fwd, Q, K, V, cu_seqlens, O, lse)
 
     def backward(self, Q, K, V, O, lse, dO, cu_seqlens, dQ=None, dK=None, dV=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._bwd(self._args, Q, K, V, O, lse, dO, cu_seqlens, dQ, dK, dV), 1)
+        return self._call(1, self._bwd, Q, K, V, O, lse, dO, cu_seqlens, dQ, dK, dV)
 
 
 class LayerNormPlan(_OpPlan):
@@ -667,14 +675,10 @@ class LayerNormPlan(_OpPlan):
         self._fwd, self._bwd = _marshal().ln_forward, _marshal().ln_backward
 
     def forward(self, X, gamma=None, beta=None, Y=None, mean=None, rstd=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._fwd(self._args, X, gamma, beta, Y, mean, rstd), 0)
+        return self._call(0, self._fwd, X, gamma, beta, Y, mean, rstd)
 
     def backward(self, X, gamma, mean, rstd, dY, dX=None, dgamma=None, dbeta=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._bwd(self._args, X, gamma, mean, rstd, dY, dX, dgamma, dbeta), 1)
+        return self._call(1, self._bwd, X, gamma, mean, rstd, dY, dX, dgamma, dbeta)
 
 
 class ClipPlan(_OpPlan):
@@ -697,14 +701,10 @@ class ClipPlan(_OpPlan):
         self._clip = _marshal().clip
 
     def norm(self, grads, norm=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._clip(self._args, grads, None, None, norm), 0)
+        return self._call(0, self._clip, grads, None, None, norm)
 
     def clip(self, grads, max_norm, out=None, norm=None):
-        if not self._fixed:
-            self._use()
-        return self._done(self._clip(self._args, grads, out, float(max_norm), norm), 1)
+        return self._call(1, self._clip, grads, out, float(max_norm), norm)
 
 
 __all__ = ["AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",

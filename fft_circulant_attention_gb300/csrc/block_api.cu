@@ -123,7 +123,7 @@ int cat_plan_create_attn(cat_plan_t* out, int max_tokens, int max_seqs, int Hq, 
                          int dtype, int causal, float scale, void* stream) {
   if (!out) return CAT_ERR_INVALID_ARG;
   *out = nullptr;
-  if (max_tokens < 0 || max_seqs < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || dh < 1 ||
+  if (max_tokens < 0 || max_tokens > CAT_ATTN_MAX_TOKENS || max_seqs < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || dh < 1 ||
       dh > CAT_ATTN_MAX_DH || (long long)Hq * dh > (1 << 20))
     return CAT_ERR_INVALID_ARG;
   if (dtype != CAT_F32 && dtype != CAT_BF16) return CAT_ERR_INVALID_ARG;
@@ -452,6 +452,10 @@ int clip_prepare(cat_plan_s* p, const void* const* grads, const float* norm) {
 int cat_grad_norm(cat_plan_t p, const void* const* grads, float* norm) {
   const int st = clip_prepare(p, grads, norm);
   if (st != CAT_OK) return st;
+  const Span2 to = flat(norm, sizeof(float));
+  for (int i = 0; i < p->cl.count; ++i)
+    if (overlap(to, flat(grads[i], (size_t)p->cl.sizes[i] * elem_size(p->cl.dtypes[i]))))
+      return CAT_ERR_ALIAS;
   DeviceGuard dev(p->device);
   if (dev.status != cudaSuccess) return CAT_ERR_CUDA;
   return status_of(cat::launch_clip(p->cl, grads, nullptr, 0.f, norm, false, p->stream));

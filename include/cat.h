@@ -271,8 +271,9 @@ int cat2d_scores(cat_plan_t plan, const void *Q, const void *K, float *a,
  * plan must not run concurrently.  Results repeat bit for bit.
  */
 
-/* Widest head of the softmax attention. */
+/* Widest head and most token rows of the softmax attention. */
 #define CAT_ATTN_MAX_DH 128
+#define CAT_ATTN_MAX_TOKENS (1 << 30)
 
 /*
  * cat_plan_create_attn — softmax attention over packed sequences: T token
@@ -281,8 +282,9 @@ int cat2d_scores(cat_plan_t plan, const void *Q, const void *K, float *a,
  * only.  Hq query heads share Hkv key heads, query head h reads key head
  * h / (Hq / Hkv).
  *
- *   max_tokens, max_seqs : the largest T and S of a call, >= 0 (their blocks,
- *            (max_tokens / 64 + max_seqs)·Hq, and max_tokens·Hq within 2^31)
+ *   max_tokens, max_seqs : the largest T and S of a call, >= 0 (max_tokens <=
+ *            CAT_ATTN_MAX_TOKENS; their blocks, (max_tokens / 64 +
+ *            max_seqs)·Hq, and max_tokens·Hq within 2^31)
  *   Hq, Hkv, dh : heads and head width, Hq % Hkv == 0, 1 <= dh <=
  *            CAT_ATTN_MAX_DH, Hq·dh <= 2^20
  *   dtype  : of Q, K, V, O and the gradients; products accumulate in fp32,
@@ -313,7 +315,9 @@ int cat_plan_create_attn(cat_plan_t *out, int max_tokens, int max_seqs, int Hq,
  * cores; the rest takes the FP32 pipe, an order of magnitude slower.  On the
  * tensor cores bf16 probabilities are rounded to bf16 and fp32 operands are
  * split into three bf16 terms (errors of fp32's own size).  A pair the mask
- * excludes contributes nothing, whatever its rows hold.  If cu_seqlens is not
+ * excludes contributes nothing, whatever its rows hold; fp32 rows that meet an
+ * infinity or NaN are computed one by one, which takes far longer.  If
+ * cu_seqlens is not
  * ascending within 0 .. T, the sequences concerned are skipped and
  * cat_plan_sync returns CAT_ERR_DEVICE_STATUS.
  * Errors: CAT_ERR_PLAN_MISMATCH (not an attention plan, T or S above the
@@ -392,8 +396,9 @@ int cat_plan_create_clip(cat_plan_t *out, int count, const long long *sizes,
 /*
  * cat_grad_norm — *norm (device, fp32) = sqrt(Σ_i Σ_k grads[i][k]²).  grads:
  * host array of the plan's count device pointers (read during the call), each
- * aligned to its element type; tensors of size 0 may be NULL.  Sums keep
- * values from 1e-30 to 1e30 apart from fp32's limits.
+ * aligned to its element type; tensors of size 0 may be NULL.  norm must not
+ * lie in a gradient (CAT_ERR_ALIAS).  Sums keep values from 1e-30 to 1e30 apart
+ * from fp32's limits.
  */
 int cat_grad_norm(cat_plan_t plan, const void *const *grads, float *norm);
 

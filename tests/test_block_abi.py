@@ -33,6 +33,7 @@ def lib():
     (16, 4, 4, 4, 64, 0, 1, math.nan),
     (16, 4, 4, 4, 64, 0, 1, math.inf),
     (2**31 - 1, 4, 64, 4, 64, 0, 1, 0.0),   # max_tokens·Hq past 2^31
+    (2**30 + 1, 4, 1, 1, 64, 0, 1, 0.0),    # max_tokens above the limit
     (16, 2**31 - 1, 4, 4, 64, 0, 1, 0.0),   # blocks past 2^31
 ])
 def test_attn_plan_refuses(lib, args):

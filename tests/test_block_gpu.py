@@ -160,6 +160,52 @@ def test_attn_two_plans_on_two_streams(dtype):
         plan.close()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [31, 128, 129, 300])
+def test_attn_many_sequences(S, dtype, causal):
+    # Blocks are taken largest first up to 128 sequences, as they lie beyond;
+    # empty sequences among them, and lengths either side of a block.
+    r = np.random.default_rng(S)
+    lens = r.integers(0, 90, S)
+    lens[r.integers(0, S, S // 8)] = 0
+    lens[r.integers(0, S, 4)] = [127, 128, 129, 260]
+    attn_parity([int(n) for n in lens], 2, 1, 64, dtype, causal, seed=S)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attn_many_wide_heads(dtype):
+    attn_parity([40, 0, 130, 3] * 40, 2, 2, 128, dtype, True, seed=6)
+
+
+def test_plans_with_a_stream_of_their_own():
+    # Outputs that a call allocates belong to the plan's stream.
+    n = 1 << 22
+    s = torch.cuda.Stream()
+    x = torch.randn(n // 64, 64, device=DEV)
+    g = [torch.randn(1000, device=DEV)]
+    torch.cuda.synchronize()
+    with cat.LayerNormPlan(n // 64, 64, "f32", stream=s) as plan, \
+            cat.ClipPlan([1000], ["f32"], stream=s.cuda_stream) as clip:
+        want = torch.nn.functional.layer_norm(x, (64,))
+        ok = []
+        for _ in range(10):
+            # Work on the default stream whose memory is free again behind it.
+            t = x * 3.0
+            for _ in range(4):
+                t = t * 0.5
+            del t
+            y, _, _ = plan.forward(x)
+            total = clip.norm(g)
+            s.synchronize()
+            ok.append(torch.allclose(y, want, atol=1e-4))
+            assert abs(float(total) - float(g[0].norm())) < 1e-3
+            plan.sync()
+        assert all(ok)
+    with cat.ClipPlan([1000], ["f32"], stream=0) as clip:      # the default stream
+        assert abs(float(clip.norm(g)) - float(g[0].norm())) < 1e-3
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attn_peaked_and_scaled(dtype):
     # Near one-hot rows: scores of some tens; and a scale of the caller's own.
@@ -751,6 +797,9 @@ def test_clip_refusals():
         plan.clip([g[1], g[0]], 1.0)
     with pytest.raises(ValueError):
         plan.clip([g[0][::2], g[1]], 1.0)
+    with pytest.raises(cat.CatError) as e:
+        plan.norm(g, norm=g[0].view(-1)[3])
+    assert e.value.status == cat.CAT_ERR_ALIAS
     # Two tensors of one list may be the same for reading.
     same = cat.ClipPlan([64, 64], ["f32", "f32"])
     assert abs(float(same.norm([g[0], g[0]])) - math.sqrt(128)) < 1e-5
