@@ -37,8 +37,9 @@
 // Values that are not finite (or too large for bf16) do not split.  A CTA
 // that met one, or whose masks could have hidden one, computes its rows again
 // at the end by a plain loop over the pairs that count, straight from the
-// definition: slow, exact in what is NaN and what is not, and never taken by
-// ordinary data.
+// definition: exact in what is NaN and what is not, and never taken by ordinary
+// data (8192 causal tokens, 4 heads, with a NaN in the first key: 50 ms forward
+// and about 170 ms backward, instead of 0.27 and 0.87).
 #include "../../include/cat.h"
 #include "attn_tc.cuh"
 #include "cat_internal.h"
@@ -219,102 +220,146 @@ __device__ __forceinline__ void store_row32(const float* acc, float* dst, int dh
   }
 }
 
-__device__ __forceinline__ float dot_rows(const float* x, const float* y, int dh) {
+// Rows by the definition (see the top of the file), one thread a row.  The
+// thread's own operands stay with it, the other side's rows are the same for
+// all lanes of a warp (one broadcast a load), and C columns of a result are
+// made at a time.
+template <int DP>
+__device__ __forceinline__ void own_row(float* v, const float* x, int dh) {
+#pragma unroll
+  for (int c = 0; c < DP; ++c) v[c] = c < dh ? __ldg(x + c) : 0.f;
+}
+// Four columns from c on of a row, zeros from dh on.
+__device__ __forceinline__ float4 four(const float* x, int c, int dh, int vec) {
+  if (vec) return __ldg(reinterpret_cast<const float4*>(x + c));
+  return make_float4(__ldg(x + c), c + 1 < dh ? __ldg(x + c + 1) : 0.f,
+                     c + 2 < dh ? __ldg(x + c + 2) : 0.f, c + 3 < dh ? __ldg(x + c + 3) : 0.f);
+}
+template <int DP>
+__device__ __forceinline__ float dot_row(const float* v, const float* x, int dh, int vec) {
   float s = 0.f;
-  for (int d = 0; d < dh; ++d) s = fmaf(__ldg(x + d), __ldg(y + d), s);
+#pragma unroll
+  for (int c = 0; c < DP; c += 4)
+    if (c < dh) {
+      const float4 y = four(x, c, dh, vec);
+      s = fmaf(v[c], y.x, s);
+      if (c + 1 < dh) s = fmaf(v[c + 1], y.y, s);
+      if (c + 2 < dh) s = fmaf(v[c + 2], y.z, s);
+      if (c + 3 < dh) s = fmaf(v[c + 3], y.w, s);
+    }
   return s;
 }
+// acc += p · columns c0 .. c0 + C - 1 of a row.
+template <int C>
+__device__ __forceinline__ void add_row(float* acc, float p, const float* x, int c0, int dh,
+                                        int vec) {
+#pragma unroll
+  for (int e = 0; e < C; e += 4)
+    if (c0 + e < dh) {
+      const float4 y = four(x, c0 + e, dh, vec);
+      acc[e] = fmaf(p, y.x, acc[e]);
+      acc[e + 1] = fmaf(p, y.y, acc[e + 1]);
+      acc[e + 2] = fmaf(p, y.z, acc[e + 2]);
+      acc[e + 3] = fmaf(p, y.w, acc[e + 3]);
+    }
+}
+template <int C>
+__device__ __forceinline__ void put_row(const float* acc, float f, float* dst, int c0, int dh) {
+#pragma unroll
+  for (int e = 0; e < C; ++e)
+    if (c0 + e < dh) dst[c0 + e] = acc[e] * f;
+}
 
-// One row of the forward by the definition (see the top of the file).
+// One row of the forward.
+template <int DP>
 __device__ __noinline__ void plain_fwd_row(const AttnArgs& a, const AttnBlock& b, int h, int g,
                                            int row) {
+  constexpr int C = 64;
   const float sc = a.scale * kLog2e;
-  const float* q = static_cast<const float*>(a.q) + (b.start + (long long)row) * a.ldq +
-                   (long long)h * a.dh;
   const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
   const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
   float* o = static_cast<float*>(a.out) + ((b.start + (long long)row) * a.Hq + h) * a.dh;
+  float q[DP];
+  own_row<DP>(q, static_cast<const float*>(a.q) + (b.start + (long long)row) * a.ldq +
+                     (long long)h * a.dh, a.dh);
   const int n = a.causal ? row + 1 : b.len;
   float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) m = fmaxf(m, dot_rows(q, k + j * a.ldk, a.dh) * sc);
+  for (int j = 0; j < n; ++j) m = fmaxf(m, dot_row<DP>(q, k + j * a.ldk, a.dh, a.vec) * sc);
   const float base = m == -INFINITY ? 0.f : m;
-  for (int j = 0; j < n; ++j) l += ex2(dot_rows(q, k + j * a.ldk, a.dh) * sc - base);
-  for (int c = 0; c < a.dh; c += 8) {
-    float acc[8];
+  for (int c0 = 0; c0 < a.dh; c0 += C) {
+    float acc[C];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int e = 0; e < C; ++e) acc[e] = 0.f;
+    l = 0.f;
     for (int j = 0; j < n; ++j) {
-      const float p = ex2(dot_rows(q, k + j * a.ldk, a.dh) * sc - base);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < a.dh) acc[e] = fmaf(p, __ldg(v + j * a.ldv + c + e), acc[e]);
+      const float p = ex2(dot_row<DP>(q, k + j * a.ldk, a.dh, a.vec) * sc - base);
+      l += p;
+      add_row<C>(acc, p, v + j * a.ldv, c0, a.dh, a.vec);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < a.dh) o[c + e] = acc[e] / l;
+    for (int e = 0; e < C; ++e)
+      if (c0 + e < a.dh) o[c0 + e] = acc[e] / l;
   }
   a.lse[(long long)h * a.T + b.start + row] = (m + log2f(l)) * kLn2;
 }
 
-// Rows row (as query i or key j) of the backward by the definition.
+// Rows row (as query i or key j) of the backward.
+template <int DP>
 __device__ __noinline__ void plain_dq_row(const AttnArgs& a, const AttnBlock& b, int h, int g,
                                           int row) {
+  constexpr int C = 32;
   const long long t = b.start + (long long)row, ldo = (long long)a.Hq * a.dh;
-  const float* q = static_cast<const float*>(a.q) + t * a.ldq + (long long)h * a.dh;
-  const float* go = static_cast<const float*>(a.dO) + t * ldo + (long long)h * a.dh;
   const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
   const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
   float* dq = static_cast<float*>(a.dq) + t * a.lddq + (long long)h * a.dh;
+  float q[DP], go[DP];
+  own_row<DP>(q, static_cast<const float*>(a.q) + t * a.ldq + (long long)h * a.dh, a.dh);
+  own_row<DP>(go, static_cast<const float*>(a.dO) + t * ldo + (long long)h * a.dh, a.dh);
   const float lse = a.lse[(long long)h * a.T + t], del = a.delta[(long long)h * a.T + t];
   const int n = a.causal ? row + 1 : b.len;
-  for (int c = 0; c < a.dh; c += 8) {
-    float acc[8];
+  for (int c0 = 0; c0 < a.dh; c0 += C) {
+    float acc[C];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int e = 0; e < C; ++e) acc[e] = 0.f;
     for (int j = 0; j < n; ++j) {
-      const float p = ex2((dot_rows(q, k + j * a.ldk, a.dh) * a.scale - lse) * kLog2e);
-      const float ds = p * (dot_rows(go, v + j * a.ldv, a.dh) - del);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < a.dh) acc[e] = fmaf(ds, __ldg(k + j * a.ldk + c + e), acc[e]);
+      const float p =
+          ex2((dot_row<DP>(q, k + j * a.ldk, a.dh, a.vec) * a.scale - lse) * kLog2e);
+      const float ds = p * (dot_row<DP>(go, v + j * a.ldv, a.dh, a.vec) - del);
+      add_row<C>(acc, ds, k + j * a.ldk, c0, a.dh, a.vec);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < a.dh) dq[c + e] = acc[e] * a.scale;
+    put_row<C>(acc, a.scale, dq, c0, a.dh);
   }
 }
+template <int DP>
 __device__ __noinline__ void plain_dkv_row(const AttnArgs& a, const AttnBlock& b, int g, int row) {
+  constexpr int C = 16;                    // (more take registers from the main loop)
   const long long t = b.start + (long long)row, ldo = (long long)a.Hq * a.dh;
-  const float* k = static_cast<const float*>(a.k) + t * a.ldk + (long long)g * a.dh;
-  const float* v = static_cast<const float*>(a.v) + t * a.ldv + (long long)g * a.dh;
   float* dk = static_cast<float*>(a.dk) + t * a.lddk + (long long)g * a.dh;
   float* dv = static_cast<float*>(a.dv) + t * a.lddv + (long long)g * a.dh;
+  float k[DP], v[DP];
+  own_row<DP>(k, static_cast<const float*>(a.k) + t * a.ldk + (long long)g * a.dh, a.dh);
+  own_row<DP>(v, static_cast<const float*>(a.v) + t * a.ldv + (long long)g * a.dh, a.dh);
   const int rep = a.Hq / a.Hkv;
-  for (int c = 0; c < a.dh; c += 8) {
-    float ak[8], av[8];
+  for (int c0 = 0; c0 < a.dh; c0 += C) {
+    float ak[C], av[C];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ak[e] = av[e] = 0.f;
+    for (int e = 0; e < C; ++e) ak[e] = av[e] = 0.f;
     for (int h = g * rep; h < (g + 1) * rep; ++h)
-      for (int i = a.causal ? row : 0; i < b.len; ++i) {
+      // (from the tile's first row on, so that the warp's lanes stay together)
+      for (int i = a.causal ? b.row0 : 0; i < b.len; ++i) {
+        if (a.causal && i < row) continue;
         const long long ti = b.start + (long long)i;
         const float* q = static_cast<const float*>(a.q) + ti * a.ldq + (long long)h * a.dh;
         const float* go = static_cast<const float*>(a.dO) + ti * ldo + (long long)h * a.dh;
-        const float p = ex2((dot_rows(q, k, a.dh) * a.scale - a.lse[(long long)h * a.T + ti]) *
-                            kLog2e);
-        const float ds = p * (dot_rows(go, v, a.dh) - a.delta[(long long)h * a.T + ti]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < a.dh) {
-            ak[e] = fmaf(ds, __ldg(q + c + e), ak[e]);
-            av[e] = fmaf(p, __ldg(go + c + e), av[e]);
-          }
+        const float p = ex2((dot_row<DP>(k, q, a.dh, a.vec) * a.scale -
+                             a.lse[(long long)h * a.T + ti]) * kLog2e);
+        const float ds =
+            p * (dot_row<DP>(v, go, a.dh, a.vec) - a.delta[(long long)h * a.T + ti]);
+        add_row<C>(ak, ds, q, c0, a.dh, a.vec);
+        add_row<C>(av, p, go, c0, a.dh, a.vec);
       }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < a.dh) {
-        dk[c + e] = ak[e] * a.scale;
-        dv[c + e] = av[e];
-      }
+    put_row<C>(ak, a.scale, dk, c0, a.dh);
+    put_row<C>(av, 1.f, dv, c0, a.dh);
   }
 }
 
@@ -564,7 +609,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
                         1.f / l);
       if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
       if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
-        plain_fwd_row(a, b, h, g, row);
+        plain_fwd_row<DP>(a, b, h, g, row);
       tc_fence_before();                       // read before the next block's products
     }
     });
@@ -775,7 +820,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
                         a.vec, 1.f);
         store_row32<DP>(dk, static_cast<float*>(a.dk) + tok * a.lddk + (long long)g * a.dh, a.dh,
                         a.vec, a.scale);
-        if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0) plain_dkv_row(a, b, g, key);
+        if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0) plain_dkv_row<DP>(a, b, g, key);
       }
       __syncwarp();
     });
@@ -1055,7 +1100,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
         store_row32<DP>(dq, static_cast<float*>(a.dq) + ((long long)b.start + row) * a.lddq +
                                 (long long)h * a.dh, a.dh, a.vec, a.scale);
       if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
-        plain_dq_row(a, b, h, g, row);
+        plain_dq_row<DP>(a, b, h, g, row);
       tc_fence_before();                       // read before the next block's products
     }
     });

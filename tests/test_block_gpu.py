@@ -134,6 +134,39 @@ def test_attn_f32_wide_heads_masked_values_do_not_leak():
         assert not got["o"][at:n, :, 70 if which == "v" else 0].isfinite().any()
 
 
+@pytest.mark.parametrize("dh", [3, 33, 40, 64])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attn_f32_odd_widths_with_a_nan(dh, causal):
+    # Rows that are computed again by the definition, whatever their alignment:
+    # those that do not see the token's value keep theirs.
+    n, at = 300, 170
+    lens = [n, 50]
+    q, k, v, do, cu = ref.attn_inputs(lens, 2, 1, dh, "f32", 15)
+    want = ref.attention(q, k, v, do, cu, causal, "f32")
+    c = dh - 1
+    for which in ("v", "do"):
+        t = dict(v=v.clone(), do=do.clone())
+        t[which][at, :, c] = math.nan
+        got = run_attn(q, k, t["v"], t["do"], cu, causal, "f32")
+        if which == "v":
+            rows = torch.ones(350, dtype=torch.bool)
+            rows[at if causal else 0:n] = False
+            for name in ("o", "dq"):
+                check(name, got[name][rows.to(DEV)], tuple(x[rows] for x in want[name]))
+            # The other columns of o are as they were in every row.
+            check("o", got["o"][..., :c], tuple(x[..., :c] for x in want["o"]))
+            assert got["o"][at:n, :, c].isnan().all()
+        else:
+            check("o", got["o"], want["o"])
+            rows = torch.ones(350, dtype=torch.bool)
+            rows[at] = False
+            check("dq", got["dq"][rows.to(DEV)], tuple(x[rows] for x in want["dq"]))
+            check("dv", got["dv"][..., :c], tuple(x[..., :c] for x in want["dv"]))
+            assert got["dv"][:at + 1, :, c].isnan().all()
+        for name in ("dk", "dv"):
+            check(name, got[name][n:], tuple(x[n:] for x in want[name]))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attn_two_plans_on_two_streams(dtype):
     # Each plan has its own workspace: calls that run at the same time.
