@@ -58,8 +58,14 @@ struct Cfg32 {              // (the backward's shared memory holds DP = 64 only)
   static constexpr int kTilePlane = kTile * DP * 2;      // bytes of one plane of 128 rows
   static constexpr int kBlkPlane = kB * DP * 2;          // ... of 64 rows
   static constexpr int kStages = DP == 64 ? 2 : 1;
-  static constexpr size_t kFwdSmem =
-      1024 + 3 * (size_t)kTilePlane + kStages * 6 * (size_t)kBlkPlane + kNumBars * 8 + 96;
+  // The forward's warpgroups that load and split, and the tiles that each has
+  // under way or in work, as loaded (at 128 there is no room left).
+  static constexpr int kGroups = DP == 64 ? 2 : 1, kAhead = DP == 64 ? 2 : 0;
+  static constexpr int kPieceBytes = kB * DP * 4;
+  static constexpr int kFwdThreads = 128 * (2 + kGroups);
+  static constexpr size_t kFwdSmem = 1024 + 3 * (size_t)kTilePlane +
+                                     kStages * 6 * (size_t)kBlkPlane +
+                                     kGroups * kAhead * (size_t)kPieceBytes + kNumBars * 8 + 96;
 };
 constexpr size_t kBwdSmem32 = 1024 + 6 * (size_t)Cfg32<64>::kTilePlane +
                               Cfg32<64>::kStages * (6 * (size_t)Cfg32<64>::kBlkPlane + 2 * kB * 4) +
@@ -108,6 +114,43 @@ struct Piece {
         }
       }
     }
+  }
+  // The same by way of shared memory, where a thread writes and later reads
+  // pieces of its own: copies that take no registers while they are under way.
+  // (`base`: an address in the tensor, for copies of no bytes.)
+  static __device__ __forceinline__ void fetch_ahead(uint32_t to, const float* src,
+                                                     const float* base, long long ld, int rows,
+                                                     int dh, int vec, int tid) {
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int at = tid + 128 * i, r = at / (DP / 8), c = 8 * (at % (DP / 8));
+      const uint32_t q = to + 2 * i * 2048 + tid * 16;
+      const float* p = src + (long long)r * ld + c;
+      if (vec) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const bool in = r < rows && c + e < dh;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q + e * 512),
+                       "l"(__cvta_generic_to_global(in ? p + e : base)), "r"(in ? 16 : 0)
+                       : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool in = r < rows && c + e < dh;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           q + e / 4 * 2048 + e % 4 * 4),
+                       "l"(__cvta_generic_to_global(in ? p + e : base)), "r"(in ? 4 : 0)
+                       : "memory");
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void take(const unsigned char* from, int tid) {
+#pragma unroll
+    for (int i = 0; i < 2 * (DP / 16); ++i)
+      *reinterpret_cast<float4*>(&x[i / 2][4 * (i % 2)]) =
+          *reinterpret_cast<const float4*>(from + i * 2048 + tid * 16);
   }
   // As rows row0 .. row0 + 63 of three bf16 planes of [DP/64][ROWS] 128-byte
   // rows, 128-byte swizzle.  Returns whether a value did not split.
@@ -371,16 +414,19 @@ __device__ __forceinline__ void planes_ready(uint32_t bar) {
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads32, 1)
+__global__ void __launch_bounds__(Cfg32<DP>::kFwdThreads, 1)
 attn_tc32_fwd_kernel(const AttnArgs a) {
   using C = Cfg32<DP>;
+  constexpr int kHelp = 4 + 4 * C::kGroups;                    // first warp of the other roles
   extern __shared__ unsigned char f32_raw[];
   const uint32_t raw = smem_addr(f32_raw);
   unsigned char* sm = f32_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* q_sm = sm;                                    // 3 planes of 128 rows
   unsigned char* k_sm = sm + 3 * C::kTilePlane;                // [kStages] 3 planes of 64
   unsigned char* v_sm = k_sm + C::kStages * 3 * C::kBlkPlane;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(v_sm + C::kStages * 3 * C::kBlkPlane);
+  unsigned char* raw_sm = v_sm + C::kStages * 3 * C::kBlkPlane;   // [kGroups][kAhead]
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(raw_sm + C::kGroups * C::kAhead * C::kPieceBytes);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t qready = bar0, pready = bar0 + 8, odone = bar0 + 16, done = bar0 + 24;
@@ -403,22 +449,27 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)   // qready, pready, kready, vready: a warp each
-      mbar_init(bars + i, i == 0 || i == 1 || (i >= 6 && i < 10) ? 4 : 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
-    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
+      mbar_init(bars + i, i == 0 ? 4 * C::kGroups : i == 1 || (i >= 6 && i < 10) ? 4 : 1);
+    for (int i = 0; i < 2; ++i)                                          // a slot's readers
+      mbar_init(bars + kNumBars - 3 + i, 5 + 4 * C::kGroups);
+    mbar_init(bars + kNumBars - 6, 4 * C::kGroups);                      // splitdone
     mbar_fence_init();
   }
-  if (warp == 8) tmem_alloc(tslot, 512);
+  if (warp == kHelp) tmem_alloc(tslot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
   uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
 
-  // Registers of the three warpgroups: 240 + 168 + 96 = 3·168, the launch's own.
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (warp == 8) {
+  // Registers of the warpgroups: 208 + 2·112 + 80 = 4·128 and 240 + 168 + 96 =
+  // 3·168, the launch's own.
+  if (warp >= kHelp) {
+    if (DP == 64)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == kHelp) {
       const uint64_t qd = sdesc_k128(q_sm), kd = sdesc_k128(k_sm);
       const uint64_t vd = sdesc_mn128(v_sm, kB * 128);
       constexpr uint64_t kStep = 3 * C::kBlkPlane >> 4;
@@ -455,15 +506,16 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
       });
       if (elect_one()) tc_commit(done);
       __syncwarp();
-    } else if (warp == 9) {
-      // Finds the work, the next block once this one's operands are split.
+    } else if (warp == kHelp + 1) {
+      // Finds the work, the next block when this one's operands are all but split.
       uint32_t items = 0;
       give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
         mbar_poll(splitdone, items++ & 1, limit);
       });
     }
   } else if (warp >= 4) {
-    const int tid = threadIdx.x - 128;
+    if (DP == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    const int group = (warp - 4) >> 2, tid = threadIdx.x - 128 * (1 + group);
     uint32_t c = 0, items = 0;
     take_work(ring_w, limit, [&](const WorkSlot* slot) {
       const AttnBlock b = slot->b;
@@ -473,45 +525,76 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
                        (long long)h * a.dh;
       const float* k = static_cast<const float*>(a.k) + b.start * a.ldk + (long long)g * a.dh;
       const float* v = static_cast<const float*>(a.v) + b.start * a.ldv + (long long)g * a.dh;
-      // Tiles in the order of their use, K0 K1 V0 K2 V1 ..; at head width 64 each
-      // is fetched while the one before is split and written (at 128 the
-      // registers hold one).
-      auto is_k = [&](int i) { return i == 0 || ((i & 1) && i < 2 * n - 1); };
-      auto block = [&](int i) { return i == 2 * n - 1 ? n - 1 : is_k(i) ? (i + 1) / 2 : i / 2 - 1; };
-      Piece<DP> now, next;
-      auto fetch = [&](Piece<DP>& x, int i) {
-        const long long r0 = (long long)(n - 1 - block(i)) * kB;
-        const int have = b.len - (int)r0;
-        if (is_k(i))
-          x.fetch(k + r0 * a.ldk, a.ldk, have, a.dh, a.vec, tid);
-        else
-          x.fetch(v + r0 * a.ldv, a.ldv, have, a.dh, a.vec, tid);
-      };
-      if (DP == 64) fetch(next, 0);
-      if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
-      ++items;
-      bool bad = put_tile<DP>(q_sm, q, a.ldq, min(kTile, b.len - b.row0), a.dh, a.vec, tid);
-      planes_ready(qready);
-      for (int i = 0; i < 2 * n; ++i) {
-        const uint32_t x = c + block(i), st = x % C::kStages;
-        const bool ik = is_k(i);
-        if (DP == 64) {
-          now = next;
-          if (i + 1 < 2 * n) fetch(next, i + 1);
-        } else {
-          fetch(now, i);
-        }
-        if (x >= C::kStages)
-          mbar_poll(ik ? kempty(st) : vempty(st), ((x / C::kStages) - 1) & 1, limit);
-        bad |= now.template put<kB>((ik ? k_sm : v_sm) + st * 3 * C::kBlkPlane, 0, tid);
+      bool bad = false;
+      // K's or V's block j to its stage, split.
+      auto put = [&](const Piece<DP>& x, bool ik, int j) {
+        const uint32_t at = c + j, st = at % C::kStages;
+        if (at >= C::kStages)
+          mbar_poll(ik ? kempty(st) : vempty(st), ((at / C::kStages) - 1) & 1, limit);
+        bad |= x.template put<kB>((ik ? k_sm : v_sm) + st * 3 * C::kBlkPlane, 0, tid);
         if (bad) const_cast<WorkSlot*>(slot)->odd = 1;
         planes_ready(ik ? kready(st) : vready(st));
+      };
+      if constexpr (DP == 64) {
+        // One warpgroup takes Q's first half and K, the other Q's second half and
+        // V; the next tile is under way while one is split and written.
+        const bool ik = group == 0;
+        const float* src = ik ? k : v;
+        const long long ld = ik ? a.ldk : a.ldv;
+        unsigned char* mine = raw_sm + group * C::kAhead * C::kPieceBytes;
+        auto fetch = [&](int u) {
+          const uint32_t to = smem_addr(mine) + u % C::kAhead * C::kPieceBytes;
+          if (u == 0) {
+            Piece<DP>::fetch_ahead(to, q + 64 * group * a.ldq, q, a.ldq,
+                                   b.len - b.row0 - 64 * group, a.dh, a.vec, tid);
+          } else if (u <= n) {
+            const long long r0 = (long long)(n - u) * kB;
+            Piece<DP>::fetch_ahead(to, src + r0 * ld, src, ld, b.len - (int)r0, a.dh, a.vec, tid);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch(0);
+        if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+        for (int u = 0; u <= n; ++u) {
+          // The next block of work is looked for beside the last two tiles.
+          if (u == max(n - 1, 0) && lane == 0) mbar_arrive(splitdone);
+          fetch(u + 1);                      // (its place was read a tile ago)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          Piece<DP> x;
+          x.take(mine + u % C::kAhead * C::kPieceBytes, tid);
+          if (u > 0) {
+            put(x, ik, u - 1);
+          } else {
+            bad = x.template put<kTile>(q_sm, 64 * group, tid);
+            planes_ready(qready);
+          }
+        }
+      } else {
+        // K0 K1 V0 K2 V1 .. (the registers hold one tile).
+        auto load = [&](bool ik, int j) {
+          const long long r0 = (long long)(n - 1 - j) * kB, ld = ik ? a.ldk : a.ldv;
+          Piece<DP> x;
+          x.fetch((ik ? k : v) + r0 * ld, ld, b.len - (int)r0, a.dh, a.vec, tid);
+          put(x, ik, j);
+        };
+        if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+        bad = put_tile<DP>(q_sm, q, a.ldq, min(kTile, b.len - b.row0), a.dh, a.vec, tid);
+        planes_ready(qready);
+        load(true, 0);
+        for (int j = 0; j < n; ++j) {
+          if (j + 1 < n) load(true, j + 1);
+          load(false, j);
+        }
       }
+      ++items;
       c += n;
-      if (lane == 0) mbar_arrive(splitdone);
+      if (DP != 64 && lane == 0) mbar_arrive(splitdone);
     });
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    if (DP == 64)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t to = tmem + lanes + kO;
     const float sc = a.scale * kLog2e;
@@ -617,7 +700,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   if (limit == 0) report(a.status, 0x741);
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kHelp) {
     // The columns are freed only after every MMA has completed (bounded).
     mbar_poll(done, 0, limit);
     if (limit == 0) report(a.status, 0x742);
@@ -1120,7 +1203,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
 template <int DP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)(attn_slots(a.T, a.S, 7) * a.Hq);
-  attn_tc32_fwd_kernel<DP><<<grid, kThreads32, Cfg32<DP>::kFwdSmem, st>>>(a);
+  attn_tc32_fwd_kernel<DP><<<grid, Cfg32<DP>::kFwdThreads, Cfg32<DP>::kFwdSmem, st>>>(a);
   return cudaGetLastError();
 }
 
