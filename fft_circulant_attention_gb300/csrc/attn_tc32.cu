@@ -15,24 +15,26 @@
 // product, four full-size terms; the blocks are added in registers.
 //
 // A CTA takes 128 rows (the MMA's M, one tensor-memory lane each) and walks
-// the other side in blocks of 64 rows.  Roles (384 threads):
+// the other side in blocks of 64 rows.  Roles:
 //   - warps 0-3, one thread a row: scores from tensor memory, softmax or its
 //     gradient, and the results back as three planes of bf16 pairs (the A
 //     operand of the next product);
-//   - warps 4-7: load operands with ordinary loads, split them and write the
-//     planes to shared memory in the 128-byte swizzle the MMA reads; rows
-//     outside the sequence and columns beyond the head width become zeros;
-//   - warp 8 issues the MMAs, warp 9 finds the work (10 and 11 only complete
-//     the warpgroup).
-// Bound by the MMAs (six times 128·64·64 a product): at 64 columns each takes
-// about 51 clocks, not the 32 of its operations, whether its A operand comes
-// from shared or tensor memory (Q's planes in tensor memory: 671 us for 632).
-// The splitting of operands and probabilities runs beside them: having K and V
-// under way together gained 2 % there and lost 2 % in short sequences.
-// Measured: 12 heads of 64,
-// 8192 causal tokens, 632 us forward, 1329 for dK and dV, 869 for dQ (1.9, 4.1
-// and 2.6 us a block of 128 x 64); 64 images of 196 tokens, 6 heads, 69 us
-// forward (223 us a pass on the FP32 pipe).
+//   - one warpgroup more (two in the forward at head width 64): load operands,
+//     split them and write the planes to shared memory in the 128-byte swizzle
+//     the MMA reads; rows outside the sequence and columns beyond the head
+//     width become zeros;
+//   - one warp issues the MMAs, one finds the work (two more only complete the
+//     warpgroup).
+//
+// Bound by the chain of MMAs (six times 128·64·64 a product, 32 clocks each by
+// their operations, about 51 as issued, whether the A operand comes from shared
+// or tensor memory) and the row warps, with the splitting beside them.
+// Measured, 12 heads of 64: 8192 causal tokens 499 us forward (632 with one
+// splitting warpgroup, which took 1800 clocks a block for K and V), 1360 for dK
+// and dV (1345 with two, but 10 % slower in short sequences for the registers
+// that the second one takes), 875 for dQ; 16 documents of 57 .. 1024 tokens 99,
+// 237 and 149 us; 64 images of 196 tokens, 6 heads, 58 us forward (223 us a pass
+// on the FP32 pipe).
 //
 // Values that are not finite (or too large for bf16) do not split.  A CTA
 // that met one, or whose masks could have hidden one, computes its rows again
@@ -1108,6 +1110,8 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       planes_ready(qready);
       for (int j = 0; j < n; ++j, ++c) {
         const uint32_t st = c % C::kStages;
+        // (the next block of work is looked for beside the last two blocks)
+        if (j == max(n - 2, 0) && lane == 0) mbar_arrive(splitdone);
         if (c >= C::kStages) mbar_poll(empty(st), ((c / C::kStages) - 1) & 1, limit);
         unsigned char* k_to = ring + st * 6 * C::kBlkPlane;
         bad |= xk.template put<kB>(k_to, 0, tid);
@@ -1116,7 +1120,6 @@ attn_tc32_dq_kernel(const AttnArgs a) {
         planes_ready(ready(st));
         if (j + 1 < n) fetch(j + 1);
       }
-      if (lane == 0) mbar_arrive(splitdone);
     });
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
