@@ -96,8 +96,9 @@ int fail(cat_plan_s* p, int st) {
 }
 
 bool alloc_status(cat_plan_s* p) {
-  return alloc(p, &p->status, 1) &&
-         cudaMemset(p->status, 0, sizeof(unsigned int)) == cudaSuccess;
+  return alloc(p, &p->status, 1) && cat::settled([&](cudaStream_t s) {
+           return cudaMemsetAsync(p->status, 0, sizeof(unsigned int), s);
+         }) == cudaSuccess;
 }
 
 }  // namespace
@@ -421,8 +422,10 @@ int cat_plan_create_clip(cat_plan_t* out, int count, const long long* sizes, con
     delete[] host;
     return fail(p, CAT_ERR_ALLOC);
   }
-  const cudaError_t e =
-      cudaMemcpy(c.chunks, host, (size_t)n * sizeof(cat::ClipChunk), cudaMemcpyHostToDevice);
+  const cudaError_t e = cat::settled([&](cudaStream_t s) {
+    return cudaMemcpyAsync(c.chunks, host, (size_t)n * sizeof(cat::ClipChunk),
+                           cudaMemcpyHostToDevice, s);
+  });
   delete[] host;
   if (e != cudaSuccess) return fail(p, CAT_ERR_CUDA);
   std::snprintf(p->desc, sizeof(p->desc), "op=clip tensors=%d chunks=%d workspace=%zu", count, n,

@@ -262,6 +262,22 @@ struct DeviceGuard {
   DeviceGuard& operator=(const DeviceGuard&) = delete;
 };
 
+// Runs fill(stream) on a stream of its own and waits for it.  What a plan holds
+// from its creation on (tables, a cleared status word) is written this way:
+// work of the legacy stream is not ordered before that of a non-blocking stream,
+// and a copy from pageable memory may return with its last part still under way,
+// so without the wait a plan's first call could read what is not there yet.
+template <typename F>
+cudaError_t settled(F fill) {
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = fill(s);
+  const cudaError_t w = cudaStreamSynchronize(s);
+  cudaStreamDestroy(s);
+  return e == cudaSuccess ? w : e;
+}
+
 // Let `kernel` use all the dynamic shared memory the current device allows
 // a block (its opt-in limit minus the kernel's static shared memory).  The
 // limit is a property of the kernel, shared by every plan in the process,
