@@ -829,8 +829,11 @@ int create_plan(cat_plan_t* out, int B, int N, int D, int H, int dtype, void* st
     double a = -two_pi * (double)j / (double)N;
     tw[j] = make_float2((float)std::cos(a), (float)std::sin(a));
   }
-  cudaError_t e = cudaMemcpy(p->tw, tw.data(), (size_t)N * sizeof(float2), cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) e = cudaMemset(p->status, 0, sizeof(unsigned int));
+  cudaError_t e = cat::settled([&](cudaStream_t s) {
+    cudaError_t c = cudaMemcpyAsync(p->tw, tw.data(), (size_t)N * sizeof(float2),
+                                    cudaMemcpyHostToDevice, s);
+    return c == cudaSuccess ? cudaMemsetAsync(p->status, 0, sizeof(unsigned int), s) : c;
+  });
   if (e == cudaSuccess) e = cat::setup_score_kernels(p);
   if (e == cudaSuccess)
     e = p->path == cat::PATH_SMEM       ? cat::setup_smem_kernels(p)
@@ -1407,7 +1410,10 @@ int cat_plan_sync(cat_plan_t p) {
       return CAT_ERR_CUDA;
     if (word != 0) {
       if (std::getenv("CAT_LOG")) std::fprintf(stderr, "[cat] device status 0x%x\n", word);
-      cudaMemset(q->status, 0, sizeof(unsigned int));
+      // (cleared when this returns: the next call may report again)
+      cat::settled([&](cudaStream_t s) {
+        return cudaMemsetAsync(q->status, 0, sizeof(unsigned int), s);
+      });
       st = CAT_ERR_DEVICE_STATUS;
     }
   }

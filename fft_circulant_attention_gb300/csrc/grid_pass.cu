@@ -552,7 +552,9 @@ cudaError_t setup_grid_pass(const cat_plan_s* p) {
     const double a = -two_pi * (double)m / (double)M;
     host[m] = make_float2((float)std::cos(a), (float)std::sin(a));
   }
-  return cudaMemcpy(p->scratch, host, (size_t)M * sizeof(float2), cudaMemcpyHostToDevice);
+  return settled([&](cudaStream_t s) {
+    return cudaMemcpyAsync(p->scratch, host, (size_t)M * sizeof(float2), cudaMemcpyHostToDevice, s);
+  });
 }
 
 cudaError_t launch_grid_pass(const cat_plan_s* p, const void* Q, const void* K, const void* V,

@@ -66,3 +66,60 @@ def test_clip_plans_are_ready_at_once_on_a_side_stream(count):
             check("norm", got, want)
             for t, o in zip(to, outs):
                 check("out", t, o)
+
+
+@pytest.mark.parametrize("B,N,D,H,dtype", [(2, 196, 64, 2, "f32"), (1, 16384, 128, 2, "bf16"),
+                                           (1, 1000, 24, 3, "f32")])
+def test_cat_plans_are_ready_at_once_on_a_side_stream(B, N, D, H, dtype):
+    # A CAT plan's tables as well: made and used while the default stream is busy.
+    g = torch.Generator().manual_seed(N)
+    X, V = (torch.randn((B, N, D), generator=g).to(ref.TORCH[dtype]).to(DEV) for _ in range(2))
+    W = (0.1 * torch.randn((D, H), generator=g)).to(ref.TORCH[dtype]).to(DEV)
+    with cat.Plan(B, N, D, H, dtype) as plan:
+        torch.cuda.synchronize()
+        want = plan.forward(X, W, V)
+        plan.sync()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        torch.cuda._sleep(2_000_000)
+        O = torch.empty_like(V)
+        with cat.Plan(B, N, D, H, dtype, stream=side) as plan:
+            plan.forward(X, W, V, O)
+            plan.sync()
+        assert torch.equal(O, want)
+
+
+def test_2d_plans_are_ready_at_once_on_a_side_stream():
+    g = torch.Generator().manual_seed(2)
+    B, h, w, D, H = 1, 16, 16, 64, 2
+    Q, K, V = (torch.randn((B, h * w, D), generator=g).to(DEV) for _ in range(3))
+    with cat.Plan2D(B, h, w, D, H, "f32") as plan:
+        torch.cuda.synchronize()
+        want = plan.forward(Q, K, V)
+        plan.sync()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        torch.cuda._sleep(2_000_000)
+        O = torch.empty_like(V)
+        with cat.Plan2D(B, h, w, D, H, "f32", stream=side) as plan:
+            plan.forward(Q, K, V, O)
+            plan.sync()
+        assert torch.equal(O, want)
+
+
+def test_a_status_is_reported_once_and_again():
+    # Reported, cleared, and reported again by the next call.
+    q, k, v, _, _ = ref.attn_inputs([100], 2, 2, 64, "bf16", 7)
+    ins = [t.to(DEV) for t in (q, k, v)]
+    bad = torch.tensor([0, 50, 20, 100], dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with cat.AttnPlan(100, 3, 2, 2, 64, "bf16", stream=side) as plan:
+        for _ in range(20):
+            plan.forward(*ins, bad)
+            with pytest.raises(cat.CatError) as e:
+                plan.sync()
+            assert e.value.status == cat.CAT_ERR_DEVICE_STATUS
+        plan.sync()
