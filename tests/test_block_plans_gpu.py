@@ -123,3 +123,28 @@ def test_a_status_is_reported_once_and_again():
                 plan.sync()
             assert e.value.status == cat.CAT_ERR_DEVICE_STATUS
         plan.sync()
+
+
+@pytest.mark.parametrize("hq,hkv,dh", [(4, 2, 64), (4, 1, 128)])
+def test_backward_calls_one_after_another(hq, hkv, dh):
+    # Calls of one plan without a wait in between, with other inputs, other
+    # sequences and other widths of the row statistics each time: none sees
+    # what the one before it left in the plan's workspace.
+    sets = []
+    T = 900
+    plan = cat.AttnPlan(T, 8, hq, hkv, dh, "bf16")
+    for i, lens in enumerate(([900], [1, 898, 1], [300, 299, 301], [113] * 7 + [109])):
+        q, k, v, do, cu = (t.to(DEV) for t in ref.attn_inputs(lens, hq, hkv, dh, "bf16", i))
+        o, lse = plan.forward(q, k, v, cu)
+        sets.append((q, k, v, o, lse, do * (1.0 + 3 * i), cu))
+    want = []
+    for s in sets:
+        torch.cuda.synchronize()
+        want.append(plan.backward(*s))
+        plan.sync()
+    got = [plan.backward(*sets[i % len(sets)]) for i in range(60)]
+    plan.sync()
+    for i, r in enumerate(got):
+        for a, b in zip(r, want[i % len(sets)]):
+            assert torch.equal(a, b), i
+    plan.close()
