@@ -135,7 +135,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mbar_init(bars + 16 + t, 4 * NT + NT + 1);     // a slot's readers
     }
     for (int s = 0; s < C::kStages; ++s)
-      mbar_init(bars + 19 + C::kStages + s, NT);     // empty: each tile's MMAs
+      mbar_init(bars + 19 + C::kStages + s, NT + 1); // empty: each tile's MMAs, the look
     mbar_fence_init();
   }
   if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
@@ -287,7 +287,12 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               __syncwarp();
             }
           }
-          if (lane == 0) mbar_arrive(clean(st));
+          // Given back here too: were the stage filled again without this warp, it
+          // could come to a turn of the ring behind and stay there.
+          if (lane == 0) {
+            mbar_arrive(clean(st));
+            mbar_arrive(empty(st));
+          }
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;

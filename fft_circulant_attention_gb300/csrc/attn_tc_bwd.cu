@@ -308,8 +308,12 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const int rep = a.Hq / a.Hkv;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)       // dsready, pready; a slot's readers
-      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 4 * NH : i == 16 || i == 17 ? 4 * NH + 3 : 1);
+    // dsready, pready; a slot's readers; empty: the products and the look
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i == 2 || i == 8 || i == 9 ? 4 * NH
+                          : i == 16 || i == 17 ? 4 * NH + 3
+                          : i >= 19 + C::kStages && i < 19 + 2 * C::kStages ? 2
+                          : 1);
     mbar_fence_init();
   }
   if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
@@ -471,7 +475,12 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               __syncwarp();
             }
           }
-          if (lane == 0) mbar_arrive(clean(st));
+          // Given back here too: were the stage filled again without this warp, it
+          // could come to a turn of the ring behind and stay there.
+          if (lane == 0) {
+            mbar_arrive(clean(st));
+            mbar_arrive(empty(st));
+          }
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;
@@ -646,8 +655,12 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)       // dsready; a slot's readers
-      mbar_init(bars + i, i == 2 ? 4 * NH : i == 14 || i == 15 ? 4 * NH + 3 : 1);
+    // dsready; a slot's readers; empty: the products and the look
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i == 2 ? 4 * NH
+                          : i == 14 || i == 15 ? 4 * NH + 3
+                          : i >= 17 + C::kStages && i < 17 + 2 * C::kStages ? 2
+                          : 1);
     mbar_fence_init();
   }
   if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);
@@ -784,7 +797,12 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive(clean(st));
+          // Given back here too: were the stage filled again without this warp, it
+          // could come to a turn of the ring behind and stay there.
+          if (lane == 0) {
+            mbar_arrive(clean(st));
+            mbar_arrive(empty(st));
+          }
           if (++st == C::kStages) {
             st = 0;
             round ^= 1u;

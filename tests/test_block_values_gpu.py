@@ -1,0 +1,78 @@
+"""GPU tests of what the operators around a CAT layer do with values and rows
+that must not count: values that are not finite behind a mask, in long and in
+many sequences, and rows that no sequence holds."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fft_circulant_attention_gb300 as cat
+import _block_ref as ref
+from _block_ref import TORCH, check
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def _built(cuda_device):
+    from fft_circulant_attention_gb300 import build
+    build.build()
+    cat.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def run(q, k, v, do, cu, causal, dtype, scale=None):
+    T, hq, dh = q.shape
+    ins = [t.to(DEV) for t in (q, k, v, do)]
+    cd = cu.to(DEV)
+    with cat.AttnPlan(T, len(cu) - 1, hq, k.shape[1], dh, dtype, causal=causal,
+                      scale=scale) as plan:
+        o, lse = plan.forward(*ins[:3], cd)
+        grads = plan.backward(*ins[:3], o, lse, ins[3], cd)
+        plan.sync()
+    return dict(zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads))
+
+
+@pytest.mark.parametrize("dh,hkv", [(64, 2), (128, 1)])
+def test_values_behind_the_mask_after_many_blocks(dh, hkv):
+    # Blocks that the mask cuts come after whole turns of the ring of key (query)
+    # blocks, in every sequence and head: each is looked through.  A value of v
+    # (of dO) that is not finite changes nothing, not a bit, in the rows (the
+    # keys) that do not see it, and every one that does.
+    lens = [1500, 700, 2049, 130, 1111, 300, 4100, 64, 900, 1023]
+    hq = 4
+    q, k, v, do, cu = ref.attn_inputs(lens, hq, hkv, dh, "bf16", 21)
+    clean = run(q, k, v, do, cu, True, "bf16")
+    r = np.random.default_rng(3)
+    at = [int(s + r.integers(n // 2, n)) for s, n in zip(cu[:-1].tolist(), lens)]
+    hidden = torch.zeros(sum(lens), dtype=torch.bool)         # rows before their sequence's value
+    after = torch.zeros(sum(lens), dtype=torch.bool)
+    for a, s, e in zip(at, cu[:-1].tolist(), cu[1:].tolist()):
+        hidden[s:a] = True
+        after[a + 1:e] = True
+    c = 5
+    for value in (math.nan, math.inf):
+        bad = v.clone()
+        bad[at, :, c] = value
+        got = run(q, k, bad, do, cu, True, "bf16")
+        for name in ("o", "dq"):
+            assert torch.equal(got[name][hidden], clean[name][hidden]), name
+        assert torch.equal(got["lse"], clean["lse"])
+        seen = ~hidden
+        assert not got["o"][seen][:, :, c].isfinite().any()
+        keep = [i for i in range(dh) if i != c]
+        assert torch.equal(got["o"][:, :, keep], clean["o"][:, :, keep])
+        bad = do.clone()
+        bad[at, :, c] = value
+        got = run(q, k, v, bad, cu, True, "bf16")
+        assert torch.equal(got["o"], clean["o"])
+        rows = torch.ones(sum(lens), dtype=torch.bool)
+        rows[at] = False
+        assert torch.equal(got["dq"][rows], clean["dq"][rows])
+        for name in ("dk", "dv"):
+            assert torch.equal(got[name][after], clean[name][after]), name
+        assert not got["dv"][~after][:, :, c].isfinite().any()
+        assert torch.equal(got["dv"][:, :, keep], clean["dv"][:, :, keep])
