@@ -128,14 +128,13 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 19 + 3 * C::kStages; ++i) mbar_init(bars + i, 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bars + 6 + t, 4);                    // sempty, pfull: a tile's warps
-      mbar_init(bars + 8 + t, 4);
-      mbar_init(bars + 16 + t, 4 * NT + NT + 1);     // a slot's readers
-    }
-    for (int s = 0; s < C::kStages; ++s)
-      mbar_init(bars + 19 + C::kStages + s, NT + 1); // empty: each tile's MMAs, the look
+    // sempty and pfull: a tile's warps; a slot's readers; empty: each tile's MMAs
+    // and the look
+    for (int i = 0; i < 19 + 3 * C::kStages; ++i)
+      mbar_init(bars + i, i >= 6 && i < 10 ? 4
+                          : i == 16 || i == 17 ? 4 * NT + NT + 1
+                          : i >= 19 + C::kStages && i < 19 + 2 * C::kStages ? NT + 1
+                          : 1);
     mbar_fence_init();
   }
   if (warp == kHelp + 1) tmem_alloc(tslot, C::kCols);

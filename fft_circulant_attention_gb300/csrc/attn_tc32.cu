@@ -450,11 +450,13 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)   // qready, pready, kready, vready: a warp each
-      mbar_init(bars + i, i == 0 ? 4 * C::kGroups : i == 1 || (i >= 6 && i < 10) ? 4 : 1);
-    for (int i = 0; i < 2; ++i)                                          // a slot's readers
-      mbar_init(bars + kNumBars - 3 + i, 5 + 4 * C::kGroups);
-    mbar_init(bars + kNumBars - 6, 4 * C::kGroups);                      // splitdone
+    // pready, kready and vready: four warps; qready and splitdone: the splitting
+    // warps; a slot's readers
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i == 0 || i == kNumBars - 6 ? 4 * C::kGroups
+                          : i == 1 || (i >= 6 && i < 10) ? 4
+                          : i == kNumBars - 3 || i == kNumBars - 2 ? 5 + 4 * C::kGroups
+                          : 1);
     mbar_fence_init();
   }
   if (warp == kHelp) tmem_alloc(tslot, 512);
@@ -744,10 +746,11 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
   auto blocks = [&](const AttnBlock& b) { return (b.len + kB - 1) / kB; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)   // those that four warps arrive on
-      mbar_init(bars + i, i < 3 || i == 8 || i == 9 || i == 12 || i == 13 ? 4 : 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
-    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
+    // those that four warps arrive on, splitdone among them; a slot's readers
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i < 3 || i == 8 || i == 9 || i == 12 || i == 13 || i == kNumBars - 6 ? 4
+                          : i == kNumBars - 3 || i == kNumBars - 2 ? 9
+                          : 1);
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tslot, 512);
@@ -1022,10 +1025,11 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)   // qready, dsready, ready: a warp each
-      mbar_init(bars + i, i < 2 || i == 6 || i == 7 ? 4 : 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bars + kNumBars - 3 + i, 9);   // a slot's readers
-    mbar_init(bars + kNumBars - 6, 4);                                   // splitdone
+    // qready, dsready, ready, splitdone: a warp each; a slot's readers
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bars + i, i < 2 || i == 6 || i == 7 || i == kNumBars - 6 ? 4
+                          : i == kNumBars - 3 || i == kNumBars - 2 ? 9
+                          : 1);
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tslot, 512);
