@@ -161,6 +161,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (w.top[t]) {
             if (nq[t] > 0) mbar_poll(qempty(t), (nq[t] - 1) & 1, limit);
             ++nq[t];
+            if (limit == 0) return;
             if (lane == 0) {
               mbar_expect_tx(bars + t, C::kTileBytes);
               for (int x = 0; x < C::kBoxes; ++x)
@@ -445,14 +446,11 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     });
   }
-  if (limit == 0) report(a.status, 0x711);
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x711);
   if (warp == kHelp + 1) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done(0), 0, limit);
-    if (NT == 2) mbar_poll(done(1), 0, limit);
-    if (limit == 0) report(a.status, 0x712);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done(0), a.status, 0x712);
+    if (NT == 2) last_wait(done(1), a.status, 0x712);
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }

@@ -187,6 +187,7 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
       __syncwarp();
     }
     if (item == 0) attn_check_sequences(a, lane, 32);
+    if (__any_sync(0xffffffffu, limit == 0)) break;
     // Asked only now, with this block's copies issued: a block taken over early
     // would wait here while another SM ran dry.
     if (lane == 0) {
@@ -216,6 +217,24 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
     item = (int)next;
   }
   publish(AttnBlock{0, 0, 0, 0}, 0, 0);
+}
+
+// Where the roles of a CTA meet at the end.  A lost wait is reported, and then
+// the CTA stays on for 2 ms: copies and the queue's answer that it no longer
+// waited for take microseconds, and land in shared memory that is still its own.
+__device__ __forceinline__ void join_roles(unsigned int* status, uint32_t limit,
+                                           unsigned int code) {
+  if (limit == 0) report(status, code);
+  tc_fence_before();
+  if (__syncthreads_or(limit == 0))
+    for (int i = 0; i < 4; ++i) __nanosleep(500000);
+}
+// A wait of its own limit, whatever has been lost before: for MMAs that must
+// have completed before their columns are freed.
+__device__ __forceinline__ void last_wait(uint32_t bar, unsigned int* status, unsigned int code) {
+  uint32_t limit = kMaxPolls;
+  mbar_poll(bar, 0, limit);
+  if (limit == 0) report(status, code);
 }
 
 // Another role's loop: work(slot) for each of the CTA's blocks.  One arrival

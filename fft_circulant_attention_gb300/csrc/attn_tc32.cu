@@ -701,13 +701,10 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
     }
     });
   }
-  if (limit == 0) report(a.status, 0x741);
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x741);
   if (warp == kHelp) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done, 0, limit);
-    if (limit == 0) report(a.status, 0x742);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done, a.status, 0x742);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -983,13 +980,10 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
     }
     });
   }
-  if (limit == 0) report(a.status, 0x751);
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x751);
   if (warp == 8) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done, 0, limit);
-    if (limit == 0) report(a.status, 0x752);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done, a.status, 0x752);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1195,13 +1189,10 @@ attn_tc32_dq_kernel(const AttnArgs a) {
     }
     });
   }
-  if (limit == 0) report(a.status, 0x761);
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x761);
   if (warp == 8) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done, 0, limit);
-    if (limit == 0) report(a.status, 0x762);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done, a.status, 0x762);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -293,7 +293,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t kvfull = bar0, dpfull = bar0 + 8, dsready = bar0 + 16, dkdone = bar0 + 24;
-  const uint32_t done = bar0 + 40;
+  const uint32_t done = bar0 + 40, sdone = bar0 + 32;           // all of either MMA warp's
   const uint32_t sfull = bar0 + 48, dvdone = bar0 + 80;
   auto pready = [&](int i) { return bar0 + 64 + 8 * i; };
   const uint32_t kvempty = bar0 + 104;
@@ -340,6 +340,7 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const DkvWork<W> w = DkvWork<W>::of(b, a.causal);
         if (items > 0) mbar_poll(kvempty, (items - 1) & 1, limit);
         ++items;
+        if (limit == 0) return;
         if (lane == 0) {
           mbar_expect_tx(bars, 2 * C::kTileBytes);
           for (int x = 0; x < C::kBoxes; ++x) {
@@ -413,6 +414,8 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
       });
+      if (elect_one()) tc_commit(sdone);
+      __syncwarp();
     } else if (warp == kHelp + 2) {
       const uint64_t qd = sdesc_mn128(ring, W * 128);
       const uint64_t gd = sdesc_mn128(ring + C::kBlkBytes, W * 128);
@@ -603,13 +606,11 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     });
   }
-  if (limit == 0) report(a.status, 0x721);
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x721);
   if (warp == kHelp + 1) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done, 0, limit);
-    if (limit == 0) report(a.status, 0x722);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done, a.status, 0x722);
+    last_wait(sdone, a.status, 0x722);
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
@@ -632,7 +633,8 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t dpfull = bar0 + 8, dsready = bar0 + 16, dqdone = bar0 + 24;
-  const uint32_t qempty = bar0 + 32, done = bar0 + 40;
+  const uint32_t qempty = bar0 + 32;
+  const uint32_t done = bar0 + 40, sdone = bar0 + 64;           // all of either MMA warp's
   // Q, dO, lse and delta have landed (two barriers in turn: the warpgroups may
   // come to a block's after the next block's are there).
   constexpr int kQ1 = 17 + 2 * C::kStages;
@@ -682,6 +684,7 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock& b, int h, WorkSlot*) {
         const int g = h / (a.Hq / a.Hkv);
         if (items > 0) mbar_poll(qempty, (items - 1) & 1, limit);
+        if (limit == 0) return;
         // From here on lse and delta come from the workspace: the kernels ahead,
         // which fill it, are waited for.
         if (items == 1) pdl_wait();
@@ -757,6 +760,8 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
         }
       });
+      if (elect_one()) tc_commit(sdone);
+      __syncwarp();
     } else if (warp == kHelp + 2) {
       const uint64_t kd = sdesc_mn128(ring, W * 128);
       int st = 0;
@@ -888,15 +893,13 @@ attn_tc_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     });
   }
-  if (limit == 0) report(a.status, 0x731);
   // The kernel ahead (dK, dV) may still run: this one does not end before it.
   if (threadIdx.x == 0) pdl_wait();
-  tc_fence_before();
-  __syncthreads();
+  join_roles(a.status, limit, 0x731);
   if (warp == kHelp + 1) {
-    // The columns are freed only after every MMA has completed (bounded).
-    mbar_poll(done, 0, limit);
-    if (limit == 0) report(a.status, 0x732);
+    // The columns are freed only after every MMA has completed.
+    last_wait(done, a.status, 0x732);
+    last_wait(sdone, a.status, 0x732);
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
