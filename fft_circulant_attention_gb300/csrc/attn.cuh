@@ -34,7 +34,11 @@ struct AttnArgs {
   int vec;                 // every row start is aligned for 4-element accesses
   int tc;                  // bf16, every row and head starts on a 16-byte boundary
   unsigned int* status;
+  int* link;               // [slots of 128 rows · Hq] blocks to compute again (fp32
+                           // workspace)
+  unsigned int polls;      // of a wait of the fp32 kernels until it is lost (3.8 us each)
 };
+constexpr unsigned int kWaitPolls = 1u << 22;
 
 struct AttnBlock {
   int seq;                 // the sequence

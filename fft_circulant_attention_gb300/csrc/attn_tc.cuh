@@ -133,8 +133,9 @@ __device__ __forceinline__ bool wide_rows(const void* base, long long ld, int dh
 struct WorkSlot {
   AttnBlock b;
   int h, valid;
-  uint32_t odd;            // a cut block's own rows held values that are not finite
-  int pad;
+  uint32_t odd;            // values that are not finite have been met (bf16: in a cut
+                           // block's own rows)
+  int item;                // the block's number (find_work)
 };
 
 // Barriers at `bars`: [0, 1] slot filled, [2, 3] slot released, [4] the queue's
@@ -147,11 +148,21 @@ struct WorkRing {
   __device__ __forceinline__ uint32_t answered() const { return bars + 32; }
 };
 
-// The copy warp's loop: load(block, head, slot) for each of the CTA's blocks,
-// in blocks of 2^shift rows by `heads` heads.  rising: under a causal mask the
+// Block and head of work item `item`, in blocks of 2^shift rows by `heads` heads, by
+// one whole warp; false where there is none.  rising: under a causal mask the
 // work of a block grows with its row.  The largest blocks come first where
 // there are few sequences; where there are many, blocks are small beside the
 // work of an SM, and they are taken as they lie.
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int heads, int shift, bool rising,
+                                          int item, AttnBlock* b, int* h) {
+  *h = item % heads;
+  int slot = item / heads;
+  if (a.S <= kSortedSeqs) return attn_find_by_size(a, slot, shift, rising, b);
+  if (rising) slot = (int)(gridDim.x / heads) - 1 - slot;
+  return attn_find_block(a, slot, shift, b);
+}
+
+// The copy warp's loop: load(block, head, slot) for each of the CTA's blocks.
 template <typename F>
 __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shift, bool rising,
                                           const WorkRing& ring, uint32_t& limit, F load) {
@@ -165,23 +176,16 @@ __device__ __forceinline__ void give_work(const AttnArgs& a, int heads, int shif
       ring.slots[s].h = h;
       ring.slots[s].valid = valid;
       ring.slots[s].odd = 0;
+      ring.slots[s].item = item;
       mbar_arrive(ring.filled(s));
     }
     __syncwarp();
     ++count;
   };
   for (uint32_t par = 0;; par ^= 1u) {
-    const int h = item % heads;
-    int slot = item / heads;
     AttnBlock b;
-    bool found;
-    if (a.S <= kSortedSeqs) {
-      found = attn_find_by_size(a, slot, shift, rising, &b);
-    } else {
-      if (rising) slot = (int)(gridDim.x / heads) - 1 - slot;
-      found = attn_find_block(a, slot, shift, &b);
-    }
-    if (found) {
+    int h;
+    if (find_work(a, heads, shift, rising, item, &b, &h)) {
       publish(b, h, 1);
       load(b, h, ring.slots + ((count - 1) & 1));
       __syncwarp();

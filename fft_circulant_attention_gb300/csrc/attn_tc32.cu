@@ -38,7 +38,7 @@
 //
 // Values that are not finite (or too large for bf16) do not split.  A CTA
 // that met one, or whose masks could have hidden one, computes its rows again
-// at the end by a plain loop over the pairs that count, straight from the
+// at its end by a plain loop over the pairs that count, straight from the
 // definition: exact in what is NaN and what is not, and never taken by ordinary
 // data (8192 causal tokens, 4 heads, with a NaN in the first key: 50 ms forward
 // and about 170 ms backward, instead of 0.27 and 0.87).
@@ -408,6 +408,49 @@ __device__ __noinline__ void plain_dkv_row(const AttnArgs& a, const AttnBlock& b
   }
 }
 
+// Words that the roles of a CTA share.
+enum Shared {
+  kOddItems,               // the last item to be computed again (a.link leads to the one
+                           // before), -1: none
+  kLostWait,               // a role has lost a wait
+};
+
+// The wait for a whole block of work, however long its sequence: it ends with the
+// roles it waits for, which either get there or lose a wait of their own.
+__device__ __forceinline__ void wait_block(uint32_t bar, uint32_t parity, uint32_t polls,
+                                           const volatile int* shared, uint32_t& limit) {
+  if (limit == 0) return;
+  do {
+    limit = polls;
+    mbar_poll(bar, parity, limit);
+  } while (limit == 0 && shared[kLostWait] == 0);
+}
+
+// By one thread: puts a block that met a value that is not finite on the CTA's
+// list of those to compute again.
+__device__ __forceinline__ void note_odd(const AttnArgs& a, const WorkSlot* slot,
+                                         volatile int* shared) {
+  if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) == 0) return;
+  a.link[slot->item] = shared[kOddItems];
+  shared[kOddItems] = slot->item;
+}
+// By the four warps that keep the list, once they have done all their blocks:
+// again(block, head) for each of the list.  No other role waits for them any
+// more but at the CTA's end, so no wait has to last as long as these loops.
+template <typename F>
+__device__ __forceinline__ void redo_odd(const AttnArgs& a, int heads, bool rising, uint32_t limit,
+                                         const volatile int* shared, F again) {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  if (__any_sync(0xffffffffu, limit == 0)) return;
+  for (int item = shared[kOddItems]; item >= 0;
+       item = *reinterpret_cast<const volatile int*>(a.link + item)) {
+    AttnBlock b;
+    int h;
+    if (find_work(a, heads, 7, rising, item, &b, &h)) again(b, h);
+    __syncwarp();
+  }
+}
+
 // This warp's writes to shared memory are visible to the MMA; one arrival.
 __device__ __forceinline__ void planes_ready(uint32_t bar) {
   fence_proxy_async_smem();
@@ -441,6 +484,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
                            smem_addr(tslot + 4)};
+  volatile int* shared = reinterpret_cast<volatile int*>(tslot + 1);   // see Shared
   // Tensor memory: scores (two buffers), probabilities, O.
   constexpr int kP = 128, kO = 256;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -450,6 +494,8 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   };
 
   if (threadIdx.x == 0) {
+    shared[kOddItems] = -1;
+    shared[kLostWait] = 0;
     // pready, kready and vready: four warps; qready and splitdone: the splitting
     // warps; a slot's readers
     for (int i = 0; i < kNumBars; ++i)
@@ -464,7 +510,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+  uint32_t limit = a.polls;                  // 0 once a wait of this thread is lost
 
   // Registers of the warpgroups: 208 + 2·112 + 80 = 4·128 and 240 + 168 + 96 =
   // 3·168, the launch's own.
@@ -514,7 +560,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
       // Finds the work, the next block when this one's operands are all but split.
       uint32_t items = 0;
       give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
-        mbar_poll(splitdone, items++ & 1, limit);
+        wait_block(splitdone, items++ & 1, a.polls, shared, limit);
       });
     }
   } else if (warp >= 4) {
@@ -605,7 +651,7 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
     uint32_t nb = 0;                           // blocks so far
     take_work(ring_w, limit, [&](const WorkSlot* slot) {
     const AttnBlock b = slot->b;
-    const int h = slot->h, g = h / (a.Hq / a.Hkv), n = blocks(b);
+    const int h = slot->h, n = blocks(b);
     const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     float m = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f), k2 = l2;
@@ -695,12 +741,16 @@ attn_tc32_fwd_kernel(const AttnArgs a) {
         store_row32<DP>(o, static_cast<float*>(a.out) + (tok * a.Hq + h) * a.dh, a.dh, a.vec,
                         1.f / l);
       if (live) a.lse[(long long)h * a.T + tok] = (m + log2f(l)) * kLn2;
-      if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
-        plain_fwd_row<DP>(a, b, h, g, row);
+      if (threadIdx.x == 0) note_odd(a, slot, shared);
       tc_fence_before();                       // read before the next block's products
     }
     });
+    redo_odd(a, a.Hq, true, limit, shared, [&](const AttnBlock& b, int h) {
+      const int row = b.row0 + 32 * warp + lane;
+      if (row < b.len) plain_fwd_row<DP>(a, b, h, h / (a.Hq / a.Hkv), row);
+    });
   }
+  if (limit == 0) shared[kLostWait] = 1;
   join_roles(a.status, limit, 0x741);
   if (warp == kHelp) {
     // The columns are freed only after every MMA has completed.
@@ -734,6 +784,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
   const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
                            smem_addr(tslot + 4)};
+  volatile int* shared = reinterpret_cast<volatile int*>(tslot + 1);   // see Shared
   // Tensor memory: scores, probabilities, dP, dS, dV, dK.
   constexpr int kP = 64, kDp = 160, kDs = 224, kDv = 320, kDk = 384;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -743,6 +794,8 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
   auto blocks = [&](const AttnBlock& b) { return (b.len + kB - 1) / kB; };
 
   if (threadIdx.x == 0) {
+    shared[kOddItems] = -1;
+    shared[kLostWait] = 0;
     // those that four warps arrive on, splitdone among them; a slot's readers
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(bars + i, i < 3 || i == 8 || i == 9 || i == 12 || i == 13 || i == kNumBars - 6 ? 4
@@ -755,7 +808,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+  uint32_t limit = a.polls;                  // 0 once a wait of this thread is lost
 
   // Registers of the three warpgroups: 168 + 232 + 104 = 3·168, the launch's own.
   if (warp >= 8) {
@@ -818,7 +871,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
       // Finds the work, the next block once this one's operands are split.
       uint32_t items = 0;
       give_work(a, a.Hkv, 7, false, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
-        mbar_poll(splitdone, items++ & 1, limit);
+        wait_block(splitdone, items++ & 1, a.polls, shared, limit);
       });
     }
   } else if (warp >= 4) {
@@ -905,9 +958,13 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
                         a.vec, 1.f);
         store_row32<DP>(dk, static_cast<float*>(a.dk) + tok * a.lddk + (long long)g * a.dh, a.dh,
                         a.vec, a.scale);
-        if (*reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0) plain_dkv_row<DP>(a, b, g, key);
       }
+      if (limit != 0 && tid == 0) note_odd(a, slot, shared);
       __syncwarp();
+    });
+    redo_odd(a, a.Hkv, false, limit, shared, [&](const AttnBlock& b, int g) {
+      const int key = b.row0 + 32 * (warp - 4) + lane;
+      if (key < b.len) plain_dkv_row<DP>(a, b, g, key);
     });
   } else {
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
@@ -980,6 +1037,7 @@ attn_tc32_dkv_kernel(const AttnArgs a) {
     }
     });
   }
+  if (limit == 0) shared[kLostWait] = 1;
   join_roles(a.status, limit, 0x751);
   if (warp == 8) {
     // The columns are freed only after every MMA has completed.
@@ -1011,6 +1069,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   const uint32_t splitdone = bar0 + 8 * (kNumBars - 6);
   const WorkRing ring_w = {reinterpret_cast<WorkSlot*>(tslot + 8), bar0 + 8 * (kNumBars - 5),
                            smem_addr(tslot + 4)};
+  volatile int* shared = reinterpret_cast<volatile int*>(tslot + 1);   // see Shared
   // Tensor memory: scores and dP (two buffers each), dS, dQ.
   constexpr int kDp = 128, kDs = 256, kDq = 384;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1019,6 +1078,8 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   };
 
   if (threadIdx.x == 0) {
+    shared[kOddItems] = -1;
+    shared[kLostWait] = 0;
     // qready, dsready, ready, splitdone: a warp each; a slot's readers
     for (int i = 0; i < kNumBars; ++i)
       mbar_init(bars + i, i < 2 || i == 6 || i == 7 || i == kNumBars - 6 ? 4
@@ -1031,7 +1092,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  uint32_t limit = kMaxPolls;                // 0 once a wait of this thread is lost
+  uint32_t limit = a.polls;                  // 0 once a wait of this thread is lost
 
   // Registers of the three warpgroups: 216 + 168 + 120 = 3·168, the launch's own.
   if (warp >= 8) {
@@ -1077,7 +1138,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       // Finds the work, the next block once this one's operands are split.
       uint32_t items = 0;
       give_work(a, a.Hq, 7, true, ring_w, limit, [&](const AttnBlock&, int, WorkSlot*) {
-        mbar_poll(splitdone, items++ & 1, limit);
+        wait_block(splitdone, items++ & 1, a.polls, shared, limit);
       });
     }
   } else if (warp >= 4) {
@@ -1126,7 +1187,7 @@ attn_tc32_dq_kernel(const AttnArgs a) {
     uint32_t nb = 0;                           // blocks so far
     take_work(ring_w, limit, [&](const WorkSlot* slot) {
     const AttnBlock b = slot->b;
-    const int h = slot->h, g = h / (a.Hq / a.Hkv), n = blocks(b);
+    const int h = slot->h, n = blocks(b);
     const int row = b.row0 + 32 * warp + lane;                 // within the sequence
     const bool live = row < b.len;
     const long long at = (long long)h * a.T + b.start + row;
@@ -1183,12 +1244,16 @@ attn_tc32_dq_kernel(const AttnArgs a) {
       if (live)
         store_row32<DP>(dq, static_cast<float*>(a.dq) + ((long long)b.start + row) * a.lddq +
                                 (long long)h * a.dh, a.dh, a.vec, a.scale);
-      if (live && *reinterpret_cast<const volatile uint32_t*>(&slot->odd) != 0)
-        plain_dq_row<DP>(a, b, h, g, row);
+      if (threadIdx.x == 0) note_odd(a, slot, shared);
       tc_fence_before();                       // read before the next block's products
     }
     });
+    redo_odd(a, a.Hq, true, limit, shared, [&](const AttnBlock& b, int h) {
+      const int row = b.row0 + 32 * warp + lane;
+      if (row < b.len) plain_dq_row<DP>(a, b, h, h / (a.Hq / a.Hkv), row);
+    });
   }
+  if (limit == 0) shared[kLostWait] = 1;
   join_roles(a.status, limit, 0x761);
   if (warp == 8) {
     // The columns are freed only after every MMA has completed.

@@ -6,6 +6,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <initializer_list>
 #include <new>
@@ -108,6 +109,7 @@ namespace cat {
 void free_op(cat_plan_s* p) {
   cudaFree(p->at.delta);
   cudaFree(p->at.stats);
+  cudaFree(p->at.link);
   cudaFree(p->ln.part);
   cudaFree(p->cl.chunks);
   cudaFree(p->cl.part);
@@ -143,11 +145,20 @@ int cat_plan_create_attn(cat_plan_t* out, int max_tokens, int max_seqs, int Hq, 
   p->at.Hkv = Hkv;
   p->at.dh = dh;
   p->at.causal = causal;
+  // CAT_ATTN_POLLS: a shorter limit of the fp32 kernels' waits (256 or more).
+  p->at.polls = cat::kWaitPolls;
+  if (const char* e = std::getenv("CAT_ATTN_POLLS")) {
+    const long v = std::atol(e);
+    if (v >= 256 && v < (long)cat::kWaitPolls) p->at.polls = (unsigned int)v;
+  }
   p->at.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)dh));
   if (!alloc_status(p) || !alloc(p, &p->at.delta, (size_t)Hq * max_tokens))
     return fail(p, CAT_ERR_ALLOC);
   if (dtype == CAT_BF16 && dh % 8 == 0 &&
       !alloc(p, &p->at.stats, cat::attn_tc_stats_count(max_tokens, max_seqs, Hq)))
+    return fail(p, CAT_ERR_ALLOC);
+  if (dtype == CAT_F32 &&
+      !alloc(p, &p->at.link, (size_t)cat::attn_slots(max_tokens, max_seqs, 7) * Hq))
     return fail(p, CAT_ERR_ALLOC);
   if (cat::setup_attn() != cudaSuccess || cat::setup_attn_tc() != cudaSuccess ||
       cat::setup_attn_tc_bwd() != cudaSuccess || cat::setup_attn_tc32() != cudaSuccess) return fail(p, CAT_ERR_CUDA);
@@ -192,6 +203,8 @@ int attn_prepare(cat_plan_s* p, const void* Q, const void* K, const void* V, con
   a->delta = c.delta;
   a->stats = c.stats;
   a->status = p->status;
+  a->link = c.link;
+  a->polls = c.polls;
   *run = true;
   return CAT_OK;
 }

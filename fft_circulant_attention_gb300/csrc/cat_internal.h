@@ -115,6 +115,8 @@ enum Op { OP_CIRCULANT = 0, OP_ATTN = 1, OP_LAYERNORM = 2, OP_CLIP = 3 };
 struct AttnCfg {
   int max_tokens, max_seqs, Hq, Hkv, dh, causal;
   float scale;
+  int* link;               // the fp32 kernels'
+  unsigned int polls;      // AttnArgs::polls
   float* delta;            // [Hq][max_tokens]
   float* stats;            // the tensor-core backward's (bf16, dh a multiple of 8)
 };

@@ -148,3 +148,70 @@ def test_backward_calls_one_after_another(hq, hkv, dh):
         for a, b in zip(r, want[i % len(sets)]):
             assert torch.equal(a, b), i
     plan.close()
+
+
+@pytest.mark.parametrize("hq,n,which", [
+    (1, 16384, "v"), (1, 16384, "do"), (32, 4096, "v"), (32, 4096, "do"), (32, 4096, None),
+])
+def test_f32_waits_last_as_long_as_the_work(monkeypatch, hq, n, which):
+    # Rows that meet a NaN are computed one by one, and the role that finds the
+    # work waits for a whole block of it: with a limit of 2048 polls (8 ms) in
+    # place of two million, both take far longer than one wait, and no wait is
+    # lost as long as there is progress.
+    dh, at, last, c = 64, n - 70, n - 128, 3       # `last`: the first row of the last tile
+    g = torch.Generator(device=DEV).manual_seed(n + hq)
+    q, k, v, do = (torch.randn((n, h, dh), generator=g, device=DEV) for h in (hq, 1, 1, hq))
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    with cat.AttnPlan(n, 1, hq, 1, dh, "f32") as plan:
+        o, lse = plan.forward(q, k, v, cu)
+        dq, dk, dv = plan.backward(q, k, v, o, lse, do, cu)
+        plan.sync()
+    if which == "v":
+        v = v.clone()
+        v[at, :, c] = float("nan")
+    elif which == "do":
+        do = do.clone()
+        do[at, :, c] = float("nan")
+    monkeypatch.setenv("CAT_ATTN_POLLS", "2048")
+    with cat.AttnPlan(n, 1, hq, 1, dh, "f32") as plan:
+        o2, lse2 = plan.forward(q, k, v, cu)
+        plan.sync()
+        dq2, dk2, dv2 = plan.backward(q, k, v, o2, lse2, do, cu)
+        plan.sync()
+    assert torch.equal(lse2[:, :last], lse[:, :last])
+    assert torch.equal(o2[:last], o[:last]) and torch.equal(dq2[:last], dq[:last])
+    if which is None:
+        for a, b in ((o2, o), (lse2, lse), (dq2, dq), (dk2, dk), (dv2, dv)):
+            assert torch.equal(a, b)
+        return
+    keep = [x for x in range(dh) if x != c]
+    # Some rows and keys that were computed one by one, against 64 bits.  A score
+    # is off by (dh + 4) steps of its absolute products, an exponential by four
+    # steps of its exponent's terms more, a sum of N products by N + 8 steps.
+    H, sc = 2.0 ** -24, dh ** -0.5
+    if which == "v":
+        assert o2[at:, :, c].isnan().all() and dk2.isnan().all()
+        for i in (last, last + 31, at - 1, n - 1):
+            Q, K, V = q[i].double(), k[:i + 1, 0].double(), v[:i + 1, 0].double()[:, keep]
+            s = sc * (Q @ K.T)
+            p = torch.softmax(s, 1)
+            es = (dh + 4) * H * sc * (Q.abs() @ K.abs().T) + 4 * H * (s.abs() + 1)
+            ep = es + es.amax(1, keepdim=True) + 8 * H
+            out = p @ V
+            bound = (p * (ep + 2 * (n + 8) * H)) @ V.abs() + H * out.abs()
+            assert ((o2[i][:, keep].double() - out).abs() <= bound).all(), i
+    else:
+        assert torch.equal(o2, o)
+        assert dv2[:at + 1, :, c].isnan().all() and dk2[:at + 1].isnan().all()
+        assert dk2[at + 1:].isfinite().all()
+        for j in (5, last, at, n - 1):
+            Q, D = q[j:].double(), do[j:].double()[:, :, keep]
+            s = sc * (Q @ k[j, 0].double())                             # [rows, hq]
+            L = lse[:, j:].T.double()
+            p = torch.exp(s - L)
+            ep = (dh + 4) * H * sc * (Q.abs() @ k[j, 0].double().abs()) + \
+                4 * H * (s.abs() + L.abs() + 1)
+            want = (p[:, :, None] * D).sum((0, 1))
+            bound = ((p * (ep + (hq * n + 8) * H))[:, :, None] * D.abs()).sum((0, 1)) + \
+                H * want.abs()
+            assert ((dv2[j, 0, keep].double() - want).abs() <= bound).all(), j
