@@ -586,7 +586,10 @@ attn_tc_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           // rows see (an infinity or NaN times a positive probability).
           for (int h = g * rep; h < (g + 1) * rep; ++h)
             for (int i = a.causal ? key : (w.nqb - 1) * W; i < b.len; ++i) {
-              if (!w.is_cut(i / W)) continue;
+              if (!w.is_cut(i / W)) {          // on to the last block, if that is cut
+                if (w.last < 0) break;
+                i = w.last * W;
+              }
               const __nv_bfloat16* go = static_cast<const __nv_bfloat16*>(a.dO) +
                                         (((long long)b.start + i) * a.Hq + h) * a.dh;
               for (int c = 0; c < a.dh; ++c) {

@@ -76,3 +76,28 @@ def test_values_behind_the_mask_after_many_blocks(dh, hkv):
             assert torch.equal(got[name][after], clean[name][after]), name
         assert not got["dv"][~after][:, :, c].isfinite().any()
         assert torch.equal(got["dv"][:, :, keep], clean["dv"][:, :, keep])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_dv_of_values_in_the_first_and_the_last_cut_block(dh, causal):
+    # Rows of dO that are not finite at the diagonal, between, and in a last
+    # block that is cut or full: each reaches the dv of the keys its row sees,
+    # in its column, and no other; many query heads to the key head.
+    lens = [647, 640, 1281, 64, 65]
+    hq, T = 16, sum(lens)
+    q, k, v, do, cu = ref.attn_inputs(lens, hq, 1, dh, "bf16", 8)
+    clean = run(q, k, v, do, cu, causal, "bf16")
+    starts = cu[:-1].tolist()
+    for back in (1, 5, 70, 200, 639):                          # rows from the end
+        bad = do.clone()
+        want = torch.zeros((T, dh), dtype=torch.bool)
+        for x, (s, n) in enumerate(zip(starts, lens)):
+            if back > n:
+                continue
+            i = n - back
+            bad[s + i, (3 * x) % hq, 7 + x] = math.inf
+            want[s:s + (i + 1 if causal else n), 7 + x] = True
+        got = run(q, k, v, bad, cu, causal, "bf16")["dv"][:, 0].cpu()
+        assert not got[want].isfinite().any()
+        assert torch.equal(got[~want], clean["dv"][:, 0].cpu()[~want])
