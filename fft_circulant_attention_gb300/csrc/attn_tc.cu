@@ -313,7 +313,9 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int h = slot->h, g = h / (a.Hq / a.Hkv);
     const FwdWork w = FwdWork::of<NT>(b, a.causal);
     const int row = b.row0 + t * kTile + 32 * quad + lane;     // within the sequence
-    float m = -INFINITY;
+    // (a row behind the sequence never makes its warp follow: the others' roundings
+    // do not depend on what lies there)
+    float m = row < b.len ? -INFINITY : INFINITY;
     float2 l2 = make_float2(0.f, 0.f), k2 = l2;      // row sum, in four parts
     for (int blk = w.top[t] - 1, it = 0; blk >= 0; --blk, ++it, ++nb) {
       mbar_poll(sfull(t), nb & 1, limit);

@@ -101,3 +101,32 @@ def test_dv_of_values_in_the_first_and_the_last_cut_block(dh, causal):
         got = run(q, k, v, bad, cu, causal, "bf16")["dv"][:, 0].cpu()
         assert not got[want].isfinite().any()
         assert torch.equal(got[~want], clean["dv"][:, 0].cpu()[~want])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_behind_a_sequence_do_not_touch_a_bit(dtype, dh, causal):
+    # The rows behind a sequence (padding, or the next sequence) share its last
+    # tile: whatever they hold, its results are the same bit for bit.
+    lens = [356, 227, 700, 33]
+    extra = 64
+    q, k, v, do, cu = ref.attn_inputs(lens, 2, 1, dh, dtype, 11, extra=extra)
+    want = run(q, k, v, do, cu, causal, dtype)
+    n = sum(lens)
+    for f in (0.0, 40.0, math.inf):
+        pad = [t.clone() for t in (q, k, v, do)]
+        for t in pad:
+            t[n:] = t[n:] * f if f != math.inf else math.inf
+        got = run(*pad, cu, causal, dtype)
+        for name in want:
+            a, b = (r[name][:, :n] if name == "lse" else r[name][:n] for r in (got, want))
+            assert torch.equal(a, b), (name, f)
+    # Another sequence behind the first one.
+    one = [t.clone() for t in (q, k, v, do)]
+    for t in one:
+        t[lens[0]:] *= 17.0
+    got = run(*one, cu, causal, dtype)
+    for name in want:
+        a, b = (r[name][:, :lens[0]] if name == "lse" else r[name][:lens[0]] for r in (got, want))
+        assert torch.equal(a, b), name
