@@ -365,16 +365,28 @@ PyObject* ln_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The addresses of a clipping plan's list of tensors.
-bool list_of(const Handle& p, PyObject* o, const char* name, std::vector<void*>* ptrs) {
-  PyObject* seq = PySequence_Fast(o, "a list of tensors is wanted");
-  if (!seq) return false;
-  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+// A clipping plan's list of tensors: their addresses, and the tensors themselves
+// for as long as it lives (the argument may be a generator that made them, or a
+// list that another thread changes while the C call runs).
+struct List {
+  PyObject* seq = nullptr;
+  std::vector<void*> ptrs;
+  List() = default;
+  List(const List&) = delete;
+  List& operator=(const List&) = delete;
+  ~List() { Py_XDECREF(seq); }
+};
+bool list_of(const Handle& p, PyObject* o, const char* name, List* list) {
+  list->seq = PySequence_Tuple(o);
+  if (!list->seq) return false;
+  PyObject* seq = list->seq;
+  std::vector<void*>* ptrs = &list->ptrs;
+  const Py_ssize_t n = PyTuple_GET_SIZE(seq);
   bool ok = n == (Py_ssize_t)p.sizes.size();
   if (!ok) bad(name, "does not have as many tensors as the plan");
   ptrs->resize(p.sizes.size());
   for (Py_ssize_t i = 0; ok && i < n; ++i) {
-    PyObject* e = PySequence_Fast_GET_ITEM(seq, i);
+    PyObject* e = PyTuple_GET_ITEM(seq, i);
     if (!THPVariable_Check(e)) {
       ok = bad(name, "must hold tensors");
       break;
@@ -386,7 +398,6 @@ bool list_of(const Handle& p, PyObject* o, const char* name, std::vector<void*>*
     else
       (*ptrs)[i] = t.data_ptr();
   }
-  Py_DECREF(seq);
   return ok;
 }
 
@@ -397,7 +408,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Handle* p = handle_of(a[0]);
     if (!p) return nullptr;
-    std::vector<void*> in, out;
+    List in, out;
     if (!list_of(*p, a[1], "grads", &in)) return nullptr;
     const bool apart = a[2] != Py_None && a[2] != a[1];
     if (apart && !list_of(*p, a[2], "out", &out)) return nullptr;
@@ -411,8 +422,9 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* to = static_cast<float*>(norm.data_ptr());
     const int st =
         a[3] == Py_None
-            ? call<ClipNorm>(p->fn[0], p->plan, in.data(), to)
-            : call<ClipScale>(p->fn[1], p->plan, in.data(), (apart ? out : in).data(), most, to);
+            ? call<ClipNorm>(p->fn[0], p->plan, in.ptrs.data(), to)
+            : call<ClipScale>(p->fn[1], p->plan, in.ptrs.data(), (apart ? out : in).ptrs.data(),
+                              most, to);
     return st ? PyLong_FromLong(st) : THPVariable_Wrap(norm);
   });
 }

@@ -215,3 +215,26 @@ def test_f32_waits_last_as_long_as_the_work(monkeypatch, hq, n, which):
             bound = ((p * (ep + (hq * n + 8) * H))[:, :, None] * D.abs()).sum((0, 1)) + \
                 H * want.abs()
             assert ((dv2[j, 0, keep].double() - want).abs() <= bound).all(), j
+
+
+def test_clip_holds_the_tensors_of_a_generator():
+    # The tensors that a generator makes live until the call has used them: the
+    # norm that the call allocates does not take their place.
+    sizes = [5, 100, 3, 77]
+    host = [torch.randn(n, generator=torch.Generator().manual_seed(n)) for n in sizes]
+    want, outs = ref.clip(host, 0.5)
+    grads = [t.to(DEV) for t in host]
+    to = [torch.empty_like(t) for t in grads]
+    with cat.ClipPlan(sizes, ["f32"] * 4) as plan:
+        for _ in range(3):
+            check("norm", plan.norm(t * 1.0 for t in grads), want)
+            n = plan.clip((t * 1.0 for t in grads), 0.5, out=(t for t in to))
+            plan.sync()
+            check("norm", n, want)
+            for t, o in zip(to, outs):
+                check("out", t, o)
+                t.zero_()
+        with pytest.raises(TypeError):
+            plan.norm(3)
+        with pytest.raises(ValueError):
+            plan.norm(t for t in grads[:2])
