@@ -537,7 +537,8 @@ def _marshal():
         if not os.path.exists(path):
             raise RuntimeError(
                 "%s is missing: build it with "
-                "`python -c 'import __graft_entry__ as g; g.build()'`" % path)
+                "`python -c 'import __graft_entry__ as g; g.build()'` "
+                "(needs torch's headers and a C++ compiler)" % path)
         loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
         loader.exec_module(m)

@@ -10,6 +10,7 @@ compiled against the running torch.
 import concurrent.futures as cf
 import os
 import subprocess
+import warnings
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,13 +42,21 @@ def marshal_path():
 
 
 def _build_marshal():
-    import sysconfig
-
-    import torch
-    base = os.path.dirname(torch.__file__)
-    src, out = os.path.join(CSRC, "marshal.cpp"), marshal_path()
+    """Compile the marshalling module.  libcat.so and its other callers do
+    without it: where torch, its headers or a C++ compiler are missing, a
+    warning says so, and the operator plans of the binding raise when used."""
+    try:
+        import torch
+    except ImportError as e:
+        return _no_marshal(e)
+    out = marshal_path()
+    src = os.path.join(CSRC, "marshal.cpp")
     if os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):
         return
+    if os.path.exists(out):
+        os.remove(out)                       # (never one of an earlier interface)
+    import sysconfig
+    base = os.path.dirname(torch.__file__)
     tmp = out + ".tmp.%d" % os.getpid()
     inc = [os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include")]
@@ -55,10 +64,18 @@ def _build_marshal():
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
            "-I" + sysconfig.get_paths()["include"], *("-isystem" + i for i in inc), src,
            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return _no_marshal(e)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+        return _no_marshal("%s failed for %s:\n%s\n%s" % (cmd[0], src, r.stdout, r.stderr))
     os.replace(tmp, out)
+
+
+def _no_marshal(why):
+    warnings.warn("libcat.so is complete, but AttnPlan, LayerNormPlan and ClipPlan have no "
+                  "marshalling module: %s" % why, RuntimeWarning, stacklevel=3)
 
 
 def _deps():
