@@ -1,5 +1,5 @@
 """GPU tests of how near the attention kernels come to their definition: the two
-terms of dS in the bf16 backward."""
+terms of dS in the bf16 backward, and kernels over lengths of a thousand and more."""
 import pytest
 import torch
 
@@ -51,3 +51,35 @@ def test_ds_keeps_two_terms(n, hq, hkv, dh, causal, pipe):
     bounds = ref.attention(q, k, v, do, cu, causal, "bf16", rounds=2.0 ** -16)
     for name, g in zip(("dq", "dk"), got):
         check(name, g, bounds[name])
+
+
+def parity(lens, hq, hkv, dh, dtype, causal, seed, put=lambda x: x.to(DEV)):
+    q, k, v, do, cu = ref.attn_inputs(lens, hq, hkv, dh, dtype, seed)
+    ins = [put(x) for x in (q, k, v)]
+    with cat.AttnPlan(q.shape[0], len(lens), hq, hkv, dh, dtype, causal=causal) as plan:
+        o, lse = plan.forward(*ins, cu.to(DEV))
+        grads = plan.backward(*ins, o, lse, do.to(DEV), cu.to(DEV))
+        plan.sync()
+    want = ref.attention(q, k, v, do, cu, causal, dtype)
+    for name, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+        check(name, x, want[name])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,dh", [([1111, 640, 383], 128), ([2049, 130], 96), ([1500], 72),
+                                     ([1025, 1024, 7], 100)], ids=str)
+def test_f32_wide_heads_over_long_sequences(lens, dh, causal):
+    parity(lens, 2, 1, dh, "f32", causal, sum(lens) + dh)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,dh", [([1111, 640, 383], 64), ([2049, 130], 128), ([1500], 33),
+                                     ([1025, 1024, 7], 5)], ids=str)
+def test_bf16_rows_off_a_boundary_over_long_sequences(lens, dh, causal):
+    parity(lens, 2, 1, dh, "bf16", causal, sum(lens) + dh, off_boundary)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dh", [72, 80, 96, 120])
+def test_bf16_padded_heads_over_long_sequences(dh, causal):
+    parity([1111, 640, 383], 4, 2, dh, "bf16", causal, dh)
