@@ -642,6 +642,8 @@ class AttnPlan(_OpPlan):
 
     def __init__(self, max_tokens, max_seqs, Hq, Hkv, dh, dtype, causal=True, scale=None,
                  stream=None, device=None):
+        if scale is not None and not scale > 0:      # (0 is the C interface's 1/sqrt(dh))
+            raise ValueError("scale must be positive, or None for 1/sqrt(dh)")
         self.Hq, self.Hkv, self.dh = Hq, Hkv, dh
         self.dtype = dtype_code(dtype)
         self._open(device, stream)
