@@ -638,6 +638,10 @@ class AttnPlan(_OpPlan):
     lse, dO, cu_seqlens)`` -> (dQ, dK, dV); Q, O, dO [T, Hq, dh], K, V
     [T, Hkv, dh], lse fp32 [Hq, T], cu_seqlens int32 [S + 1] on the device.
     Q, K, V (and dQ, dK, dV where given) may be column ranges of wider rows.
+    Rows that no sequence holds (padding) are not written: in outputs that the
+    call allocates they are undefined, so pass zeroed ones (``O=``, ``dQ=`` ..)
+    where a later product runs over them.  ``scale``: positive, or None for
+    1/sqrt(dh).
     """
 
     def __init__(self, max_tokens, max_seqs, Hq, Hkv, dh, dtype, causal=True, scale=None,

@@ -26,7 +26,7 @@
 // Bound by shared-memory reads beside the FP32 pipe.  Measured, 12 heads of 64,
 // 16 documents of 57 .. 1024 tokens: forward 444 us and backward 1413 us in bf16
 // at odd addresses, where the tensor-core kernels take 25 and 84 us; backward of
-// fp32 heads of 128 3128 us (of 64, on the tensor cores, 414).
+// fp32 heads of 128 3139 us (of 64, on the tensor cores, 425).
 #include "attn.cuh"
 #include "../../include/cat.h"
 #include "cat_internal.h"

@@ -22,13 +22,14 @@
 // computed while P is still being made; at 128 the 512 columns are full and P
 // takes the place of its scores.
 //
-// Bound by the row warps: 16384 causal tokens of 16 heads over 4 (two such
-// sequences and one of 4999) take 928 us, 1.24 PFLOP/s or 65 % of the measured
-// bf16 rate; a block takes two tiles 2200 clocks, of which their 32768
-// exponentials alone want 1024 of each of the four units' time twice over with
-// the scaling, maxima, sums and packing beside them (1520 measured without any
-// wait), and the MMAs and copies alone 1505.  Four row warpgroups (two a tile)
-// gained nothing.  Short documents (16 up to 1024 tokens, 12 heads) take 21 us
+// No unit is full: 16384 causal tokens of 16 heads over 4 (two such sequences
+// and one of 4999) take 928 us, 1.24 PFLOP/s or 65 % of the measured bf16 rate; a
+// block takes two tiles 2200 clocks, of which the row warps want 1520 (their
+// exponentials, scaling, maxima, sums and packing, measured without any wait)
+// and the MMAs and copies alone 1505.  The rest is waits of the roles for one
+// another, not told apart yet (each tile has one buffer of scores, so its next
+// ones are made only when the last have been read).  Four row warpgroups (two a
+// tile) gained nothing.  Short documents (16 up to 1024 tokens, 12 heads) take 21 us
 // against 7.5 for their bytes: each CTA has three blocks of work, and the
 // first copies, the last products and the rows' stores of each are a chain.
 //

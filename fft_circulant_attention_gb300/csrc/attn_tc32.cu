@@ -3,10 +3,11 @@
 // any strides and alignment.
 //
 // Every operand is split into three bf16 terms, x = x0 + x1 + x2 with
-// |x1| <= 2^-9 |x|, |x2| <= 2^-17 |x| and a remainder of 2^-25 |x|, and a
-// product A·B becomes the six products A_i·B_j with i + j <= 2, smallest
-// first, into one fp32 accumulator; what is left out is below 2^-24 of
-// |a||b|, half a rounding step of fp32.  bf16 MMAs at a sixth of their rate
+// |x1| <= 2^-8 |x| and |x2| <= 2^-17 |x| (half steps of 8 bits, the second with a
+// sign of its own), and no remainder short of underflow: 24 bits in three terms
+// of 8.  A product A·B becomes the six products A_i·B_j with i + j <= 2,
+// smallest first, into one fp32 accumulator; what is left out, A_1·B_2, A_2·B_1
+// and A_2·B_2, is within 2·2^-25 = 2^-24 of |a||b|, half a rounding step of fp32.  bf16 MMAs at a sixth of their rate
 // are still four times what the FP32 pipe could do at best.
 //
 // The tensor core's fp32 accumulator drops what does not fit instead of
@@ -29,19 +30,19 @@
 // Bound by the chain of MMAs (six times 128·64·64 a product, 32 clocks each by
 // their operations, about 51 as issued, whether the A operand comes from shared
 // or tensor memory) and the row warps, with the splitting beside them.
-// Measured, 12 heads of 64: 8192 causal tokens 499 us forward (632 with one
-// splitting warpgroup, which took 1800 clocks a block for K and V), 1360 for dK
-// and dV (1345 with two, but 10 % slower in short sequences for the registers
-// that the second one takes), 875 for dQ; 16 documents of 57 .. 1024 tokens 99,
-// 237 and 149 us; 64 images of 196 tokens, 6 heads, 58 us forward (223 us a pass
-// on the FP32 pipe).
+// Measured, 12 heads of 64: 8192 causal tokens 501 us forward (632 with one
+// splitting warpgroup, which took 1800 clocks a block for K and V), 1353 for dK
+// and dV (two splitting warpgroups: 1 % faster here, but 10 % slower in short
+// sequences for the registers that the second one takes), 882 for dQ; 16
+// documents of 57 .. 1024 tokens 102, 243 and 153 us; 64 images of 196 tokens, 6
+// heads, 59 us forward (223 us a pass on the FP32 pipe).
 //
 // Values that are not finite (or too large for bf16) do not split.  A CTA
 // that met one, or whose masks could have hidden one, computes its rows again
 // at its end by a plain loop over the pairs that count, straight from the
 // definition: exact in what is NaN and what is not, and never taken by ordinary
 // data (8192 causal tokens, 4 heads, with a NaN in the first key: 50 ms forward
-// and about 170 ms backward, instead of 0.27 and 0.87).
+// and 234 ms backward, instead of 0.20 and 0.83).
 #include "../../include/cat.h"
 #include "attn_tc.cuh"
 #include "cat_internal.h"

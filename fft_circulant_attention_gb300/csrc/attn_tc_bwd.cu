@@ -13,8 +13,8 @@
 // It starts beside the last CTAs of the kernel ahead, where what the kernels
 // ahead write is not visible yet: a CTA's first block makes lse and delta anew
 // from the call's own inputs, the later ones wait for the kernels ahead and
-// read them from the workspace (the backward of 16 documents 78.0 us, of 8192
-// tokens 379; 78.6 and 386 with the wait before the first block too).
+// read them from the workspace (a backward of 16 documents 78.0 us, of 8192
+// tokens 376; 78.6 and 386 with the wait before the first block too).
 // Seven products instead of the five of one joint kernel, but dQ needs no
 // atomics: results repeat bit for bit, and neither kernel's accumulators
 // leave tensor memory.
@@ -32,16 +32,16 @@
 // At head width 64 a CTA has one warpgroup of rows, works on blocks of 64 of
 // the other side and takes half of the 512 columns, so that two CTAs share an
 // SM and one's chain of waits runs beside the other's (12 heads, 16 documents
-// up to 1024 tokens: all three kernels 83.6 us, 91.3 with one CTA of two
-// warpgroups; 8192 tokens: 371 and 396).  At 128 the accumulators fill the
+// up to 1024 tokens: all three kernels 86 us; 7.7 more with one CTA of two
+// warpgroups; 8192 tokens: 373 and 25 more).  At 128 the accumulators fill the
 // columns: two warpgroups, blocks of 128.
 //
 // Bound by the row warps' chain at 64: a block of 64 takes an SM 1150 clocks
 // where the exponentials want 512 and the MMAs 640 (8192 tokens: 1.28 PFLOP/s
 // counting nine products, 67 % of the measured bf16 rate), and by the MMAs, at
-// the card's power limit, at 128 (16 heads over 4, 8192 + 4095 + 3757 tokens:
-// 574 us for dK and dV, 493 for dQ, 1.5 PFLOP/s counting the nine products).
-// Short documents: 48 us for dK and dV and 34 for dQ, with 2.3 us of each
+// the card's power limit, at 128 (16 heads over 4, 8192 + 4095 + 2049 + 1000 + ..
+// tokens: 577 us for dK and dV, 498 for dQ, 1.5 PFLOP/s counting the nine products).
+// Short documents: 47 us for dK and dV and 37 for dQ, with 2.3 us of each
 // block of work between its last product and the next one's first.
 //
 // P is rounded to bf16 (half a step 2^-8 of each value) as an MMA operand, dS

@@ -3,8 +3,8 @@
 // given and calls the C interface.  In Python these steps take longer than
 // the kernels of a small call (82 tokens in 3 sequences, 2 heads of 32, GB300:
 // 16 us a call from Python, 7.2 us from here, of which the C call takes 5.2;
-// layer norm of 256 short rows 15 and 7.8 us; clipping 133 tensors 97 us, all
-// of it the host's, and 88 us, the kernels' time).
+// layer norm of 256 short rows 15 us and, by the machine, 6.4 to 9; clipping 133
+// tensors 97 us, all of it the host's, and 88 us, the kernels' time).
 //
 // make(...) -> a handle that holds a plan's shape and entry points; the calls
 // return their outputs, or the status of a failed C call as an int.  Tensors
