@@ -7,8 +7,9 @@
 // sign of its own), and no remainder short of underflow: 24 bits in three terms
 // of 8.  A product A·B becomes the six products A_i·B_j with i + j <= 2,
 // smallest first, into one fp32 accumulator; what is left out, A_1·B_2, A_2·B_1
-// and A_2·B_2, is within 2·2^-25 = 2^-24 of |a||b|, half a rounding step of fp32.  bf16 MMAs at a sixth of their rate
-// are still four times what the FP32 pipe could do at best.
+// and A_2·B_2, is within 2·2^-25 = 2^-24 of |a||b|, half a rounding step of fp32.
+// bf16 MMAs at a sixth of their rate are still four times what the FP32 pipe could
+// do at best.
 //
 // The tensor core's fp32 accumulator drops what does not fit instead of
 // rounding, always toward zero, so a long chain of MMAs drifts (4·10^-6 of the

@@ -130,3 +130,38 @@ def test_rows_behind_a_sequence_do_not_touch_a_bit(dtype, dh, causal):
     for name in want:
         a, b = (r[name][:, :lens[0]] if name == "lse" else r[name][:lens[0]] for r in (got, want))
         assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("S", [100, 150])
+@pytest.mark.parametrize("causal", [True, False])
+def test_f32_values_in_some_of_many_sequences(S, causal):
+    # Blocks that are computed again are found like the others, largest first or
+    # as they lie: the sequences that hold a NaN have it where their rows see it,
+    # the others keep every bit.
+    r = np.random.default_rng(S)
+    lens = [int(n) for n in r.integers(1, 300, S)]
+    hq, hkv, dh, c = 4, 2, 40, 11
+    T = sum(lens)
+    q, k, v, do, cu = ref.attn_inputs(lens, hq, hkv, dh, "f32", S)
+    clean = run(q, k, v, do, cu, causal, "f32")
+    struck = sorted(int(s) for s in r.choice(S, 7, replace=False))
+    starts = cu[:-1].tolist()
+    at = [starts[s] + int(r.integers(0, lens[s])) for s in struck]
+    whole = torch.ones(T, dtype=torch.bool)
+    sees = torch.zeros(T, dtype=torch.bool)
+    for s, i in zip(struck, at):
+        whole[starts[s]:starts[s] + lens[s]] = False
+        sees[(i if causal else starts[s]):starts[s] + lens[s]] = True
+    bad = v.clone()
+    bad[at, :, c] = math.nan
+    got = run(q, k, bad, do, cu, causal, "f32")
+    for name in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[name][whole], clean[name][whole]), name
+    assert got["o"][sees][:, :, c].isnan().all() and got["dq"][sees].isnan().all()
+    want = ref.attention(q, k, v, do, cu, causal, "f32")
+    hidden = ~sees
+    for name in ("o", "dq"):
+        check(name, got[name].cpu()[hidden], tuple(t[hidden] for t in want[name]))
+    keep = [x for x in range(dh) if x != c]
+    check("o", got["o"][:, :, keep], tuple(t[:, :, keep] for t in want["o"]))
+    check("dv", got["dv"], want["dv"])
