@@ -25,7 +25,12 @@ for convenience.  The operators around a CAT layer in a training step are
 (softmax attention over packed sequences, ``AttnPlan``),
 ``cat_plan_create_layernorm``, ``cat_layernorm_forward``,
 ``cat_layernorm_backward`` (``LayerNormPlan``), ``cat_plan_create_clip``,
-``cat_grad_norm`` and ``cat_grad_clip`` (``ClipPlan``).
+``cat_grad_norm`` and ``cat_grad_clip`` (``ClipPlan``); those at its ends and
+between its layers are ``cat_plan_create_embed``, ``cat_embed_forward``,
+``cat_embed_backward`` (``EmbedPlan``), ``cat_plan_create_resnorm``,
+``cat_resnorm_forward``, ``cat_resnorm_backward`` (``ResNormPlan``),
+``cat_plan_create_xent``, ``cat_xent_forward`` and ``cat_xent_backward``
+(``XentPlan``).
 """
 import ctypes
 import os
@@ -34,6 +39,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcat.so")
 
 CAT_F32, CAT_BF16 = 0, 1
+CAT_I32, CAT_I64 = 2, 3
 CAT_OK = 0
 STATUS = {
     0: "CAT_OK", -1: "CAT_ERR_INVALID_ARG", -2: "CAT_ERR_UNSUPPORTED_N",
@@ -83,6 +89,15 @@ SIGNATURES = {
     "cat_plan_create_clip": (_I, [ctypes.POINTER(_P), _I, _P, _P, _P]),
     "cat_grad_norm": (_I, [_P, _P, _P]),
     "cat_grad_clip": (_I, [_P, _P, _P, _F, _P]),
+    "cat_plan_create_embed": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _F, _P]),
+    "cat_embed_forward": (_I, [_P, _P, _I, _P, _P, _I]),
+    "cat_embed_backward": (_I, [_P, _P, _I, _P, _P, _I, _I]),
+    "cat_plan_create_resnorm": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _F, _F, _P]),
+    "cat_resnorm_forward": (_I, [_P, _P, _P, _P, _I] + [_P] * 7 + [_I]),
+    "cat_resnorm_backward": (_I, [_P, _P, _P, _P, _I] + [_P] * 13 + [_I]),
+    "cat_plan_create_xent": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _P]),
+    "cat_xent_forward": (_I, [_P, _P, _P, _P, _I, _P, _P, _I]),
+    "cat_xent_backward": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _P, _P, _I]),
     "cat_status_string": (ctypes.c_char_p, [_I]),
 }
 
@@ -317,6 +332,78 @@ def cat_grad_clip(plan, grads, outs, max_norm, norm):
     a = _addresses(grads)
     _check(lib().cat_grad_clip(plan, a, a if outs is grads else _addresses(outs), max_norm,
                                _ptr(norm)), "cat_grad_clip")
+
+
+def id_code(dtype):
+    """CAT_I32 / CAT_I64 from a code or a torch dtype."""
+    if isinstance(dtype, int):
+        return dtype
+    name = str(dtype).replace("torch.", "")
+    if name in ("int32", "int64"):
+        return CAT_I32 if name == "int32" else CAT_I64
+    raise ValueError("ids must be int32 or int64, not %r" % (dtype,))
+
+
+def cat_plan_create_embed(max_tokens, V, D, dtype, scale=1.0, stream=None):
+    """Create an embedding plan; returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_embed(ctypes.byref(h), max_tokens, V, D, dtype_code(dtype),
+                                       scale, _stream(stream)), "cat_plan_create_embed")
+    return h.value
+
+
+def cat_embed_forward(plan, ids, id_type, W, Y, T):
+    _check(lib().cat_embed_forward(plan, _ptr(ids), id_code(id_type), _ptr(W), _ptr(Y), T),
+           "cat_embed_forward")
+
+
+def cat_embed_backward(plan, ids, id_type, dY, dW, accumulate, T):
+    _check(lib().cat_embed_backward(plan, _ptr(ids), id_code(id_type), _ptr(dY), _ptr(dW),
+                                    int(accumulate), T), "cat_embed_backward")
+
+
+def cat_plan_create_resnorm(max_rows, D, dtype, post=False, eps=1e-5, scale=1.0, stream=None):
+    """Create a plan for the residual stream between two blocks; returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_resnorm(ctypes.byref(h), max_rows, D, dtype_code(dtype),
+                                         int(post), eps, scale, _stream(stream)),
+           "cat_plan_create_resnorm")
+    return h.value
+
+
+def cat_resnorm_forward(plan, R, B, gate, gate_rows, post_gamma, post_beta, gamma, beta, H, Y,
+                        stats, rows):
+    _check(lib().cat_resnorm_forward(plan, _ptr(R), _ptr(B), _ptr(gate), int(gate_rows),
+                                     _ptr(post_gamma), _ptr(post_beta), _ptr(gamma), _ptr(beta),
+                                     _ptr(H), _ptr(Y), _ptr(stats), rows), "cat_resnorm_forward")
+
+
+def cat_resnorm_backward(plan, H, B, gate, gate_rows, post_gamma, post_beta, gamma, stats, dH, dY,
+                         dR, dB, dgate, dpost_gamma, dpost_beta, dgamma, dbeta, rows):
+    _check(lib().cat_resnorm_backward(plan, _ptr(H), _ptr(B), _ptr(gate), int(gate_rows),
+                                      _ptr(post_gamma), _ptr(post_beta), _ptr(gamma), _ptr(stats),
+                                      _ptr(dH), _ptr(dY), _ptr(dR), _ptr(dB), _ptr(dgate),
+                                      _ptr(dpost_gamma), _ptr(dpost_beta), _ptr(dgamma),
+                                      _ptr(dbeta), rows), "cat_resnorm_backward")
+
+
+def cat_plan_create_xent(max_tokens, V, D, dtype, grad=True, stream=None):
+    """Create a cross entropy plan; returns its handle."""
+    h = ctypes.c_void_p()
+    _check(lib().cat_plan_create_xent(ctypes.byref(h), max_tokens, V, D, dtype_code(dtype),
+                                      int(grad), _stream(stream)), "cat_plan_create_xent")
+    return h.value
+
+
+def cat_xent_forward(plan, X, W, targets, id_type, loss, lse, T):
+    _check(lib().cat_xent_forward(plan, _ptr(X), _ptr(W), _ptr(targets), id_code(id_type),
+                                  _ptr(loss), _ptr(lse), T), "cat_xent_forward")
+
+
+def cat_xent_backward(plan, X, W, targets, id_type, lse, dloss, dloss_each, dX, dW, T):
+    _check(lib().cat_xent_backward(plan, _ptr(X), _ptr(W), _ptr(targets), id_code(id_type),
+                                   _ptr(lse), _ptr(dloss), int(dloss_each), _ptr(dX), _ptr(dW),
+                                   T), "cat_xent_backward")
 
 
 def cat_plan_sync(plan):
@@ -714,7 +801,100 @@ class ClipPlan(_OpPlan):
         return self._call(1, self._clip, grads, out, float(max_norm), norm)
 
 
-__all__ = ["AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",
+class EmbedPlan(_OpPlan):
+    """Rows of a table W [V, D] looked up by token, for up to ``max_tokens``
+    tokens a call.
+
+    ``forward(ids, W)`` -> Y [..., D] = scale·W[ids], zeros where an id is
+    negative; ``backward(ids, dY)`` -> dW [V, D], the sum of the rows of each
+    id's tokens times scale.  With ``accumulate=True`` the sums are added to the
+    ``dW`` given (the gradient of output weights tied to the table, say), and
+    rows of other ids keep their values.  ids: int32 or int64 of any shape.
+    """
+
+    def __init__(self, max_tokens, V, D, dtype, scale=1.0, stream=None, device=None):
+        self.V, self.D = V, D
+        self.dtype = dtype_code(dtype)
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_embed(max_tokens, V, D, self.dtype, scale, self._on)
+        self._native(("cat_embed_forward", "cat_embed_backward"), (V, D, 0), self.dtype)
+        self._fwd, self._bwd = _marshal().embed_forward, _marshal().embed_backward
+
+    def forward(self, ids, W, Y=None):
+        return self._call(0, self._fwd, ids, W, Y)
+
+    def backward(self, ids, dY, dW=None, accumulate=False):
+        return self._call(1, self._bwd, ids, dY, dW, accumulate)
+
+
+class ResNormPlan(_OpPlan):
+    """The residual stream between two blocks: up to ``max_rows`` rows of D.
+
+    ``forward(R, B, gate, gamma, beta, post_gamma, post_beta)`` -> (H, Y, stats):
+    H = R + scale·gate·u with u = LN(B)·post_gamma + post_beta (``post=True``) or
+    u = B, and Y = LN(H)·gamma + beta.  gate: None, [D], or the shape of B; every
+    norm weight may be None.  ``backward(H, B, gate, gamma, post_gamma,
+    post_beta, stats, dH, dY)`` -> (dR, dB, dgate, dgamma, dbeta, dpost_gamma,
+    dpost_beta), None where there is no gate or no norm behind the block; dH may
+    be None.  stats: fp32 [2 or 4, ...], mean and rstd of H, and of B.
+    """
+
+    def __init__(self, max_rows, D, dtype, eps=1e-5, scale=1.0, post=False, stream=None,
+                 device=None):
+        self.D, self.post = D, bool(post)
+        self.dtype = dtype_code(dtype)
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_resnorm(max_rows, D, self.dtype, self.post, eps, scale,
+                                                  self._on)
+        self._native(("cat_resnorm_forward", "cat_resnorm_backward"), (D, int(self.post), 0),
+                     self.dtype)
+        self._fwd, self._bwd = _marshal().resnorm_forward, _marshal().resnorm_backward
+
+    def forward(self, R, B, gate=None, gamma=None, beta=None, post_gamma=None, post_beta=None,
+                H=None, Y=None, stats=None):
+        return self._call(0, self._fwd, R, B, gate, gamma, beta, post_gamma, post_beta, H, Y,
+                          stats)
+
+    def backward(self, H, B, gate, gamma, post_gamma, post_beta, stats, dH, dY, dR=None, dB=None,
+                 dgate=None, dgamma=None, dbeta=None, dpost_gamma=None, dpost_beta=None):
+        return self._call(1, self._bwd, H, B, gate, gamma, post_gamma, post_beta, stats, dH, dY,
+                          dR, dB, dgate, dgamma, dbeta, dpost_gamma, dpost_beta)
+
+
+class XentPlan(_OpPlan):
+    """Softmax cross entropy over a vocabulary of V from hidden states of width
+    D, for up to ``max_tokens`` tokens a call, without keeping the logits.
+
+    ``forward(X, W, targets)`` -> (loss, lse), fp32 [...]; X [..., D], W [V, D],
+    targets int32 or int64 [...], negative where a token has none (loss and lse
+    are 0 there).  ``backward(X, W, targets, lse, dloss)`` -> (dX, dW); dloss:
+    fp32, one value or the shape of targets.  ``dX=False`` or ``dW=False``: not
+    wanted (None).  ``grad=False``: a plan for the forward alone, with far less
+    workspace.
+    """
+
+    def __init__(self, max_tokens, V, D, dtype, grad=True, stream=None, device=None):
+        self.V, self.D = V, D
+        self.dtype = dtype_code(dtype)
+        self._open(device, stream)
+        with _on_device(self.device):
+            self.handle = cat_plan_create_xent(max_tokens, V, D, self.dtype, grad, self._on)
+        self._native(("cat_xent_forward", "cat_xent_backward"), (V, D, 0), self.dtype)
+        self._fwd, self._bwd = _marshal().xent_forward, _marshal().xent_backward
+
+    def forward(self, X, W, targets, loss=None, lse=None):
+        return self._call(0, self._fwd, X, W, targets, loss, lse)
+
+    def backward(self, X, W, targets, lse, dloss, dX=None, dW=None):
+        return self._call(1, self._bwd, X, W, targets, lse, dloss, dX, dW)
+
+
+__all__ = ["EmbedPlan", "ResNormPlan", "XentPlan", "cat_plan_create_embed", "cat_embed_forward",
+           "cat_embed_backward", "cat_plan_create_resnorm", "cat_resnorm_forward",
+           "cat_resnorm_backward", "cat_plan_create_xent", "cat_xent_forward",
+           "cat_xent_backward", "id_code", "CAT_I32", "CAT_I64", "AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",
            "cat_attn_backward", "cat_plan_create_layernorm", "cat_layernorm_forward",
            "cat_layernorm_backward", "cat_plan_create_clip", "cat_grad_norm", "cat_grad_clip",
            "CatError", "Plan", "Plan2D", "lib", "dtype_code", "cat_plan_create", "cat_plan_destroy",

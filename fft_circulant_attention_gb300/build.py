@@ -74,7 +74,7 @@ def _build_marshal():
 
 
 def _no_marshal(why):
-    warnings.warn("libcat.so is complete, but AttnPlan, LayerNormPlan and ClipPlan have no "
+    warnings.warn("libcat.so is complete, but the operator plans (AttnPlan and the like) have no "
                   "marshalling module: %s" % why, RuntimeWarning, stacklevel=3)
 
 

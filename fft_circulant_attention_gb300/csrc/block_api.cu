@@ -15,92 +15,21 @@
 #include "../../include/cat.h"
 #include "attn.cuh"
 #include "cat_internal.h"
+#include "op_api.cuh"
 
 namespace {
 
 using cat::DeviceGuard;
-
-int status_of(cudaError_t e) { return e == cudaSuccess ? CAT_OK : CAT_ERR_CUDA; }
-
-size_t elem_size(int dtype) { return dtype == CAT_BF16 ? 2 : 4; }
-
-// One operand: `rows` rows of `width` bytes, `stride` bytes apart.
-struct Span2 {
-  const void* p;
-  size_t rows, width, stride;
-};
-
-Span2 flat(const void* p, size_t bytes) { return Span2{p, 1, bytes, bytes}; }
-
-// Whether two operands share a byte.  Rows of the same stride may interleave
-// (the columns of one projection's output): they meet only if their columns
-// do.  Different strides count as meeting wherever the ranges do.
-bool overlap(const Span2& a, const Span2& b) {
-  if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
-  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  const size_t nx = (a.rows - 1) * a.stride + a.width, ny = (b.rows - 1) * b.stride + b.width;
-  if (x >= y + ny || y >= x + nx) return false;
-  if (a.stride != b.stride || a.rows == 1) return true;
-  const size_t s = a.stride;
-  const size_t d = y >= x ? (y - x) % s : (s - (x - y) % s) % s;   // b's column offset from a's
-  return d < a.width || d + b.width > s;
-}
-
-// No output meets an input or another output.
-bool aliased(const Span2* in, int nin, const Span2* out, int nout) {
-  for (int o = 0; o < nout; ++o) {
-    for (int i = 0; i < nin; ++i)
-      if (overlap(out[o], in[i])) return true;
-    for (int q = o + 1; q < nout; ++q)
-      if (overlap(out[o], out[q])) return true;
-  }
-  return false;
-}
-
-cat_plan_s* new_plan(int op, int dtype, void* stream, int* st) {
-  cat_plan_s* p = new (std::nothrow) cat_plan_s();
-  if (!p) {
-    *st = CAT_ERR_ALLOC;
-    return nullptr;
-  }
-  p->op = op;
-  p->dtype = dtype;
-  p->stream = (cudaStream_t)stream;
-  *st = CAT_OK;
-  if (cudaGetDevice(&p->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
-    cudaGetLastError();
-    delete p;
-    *st = CAT_ERR_CUDA;
-    return nullptr;
-  }
-  return p;
-}
-
-template <typename T>
-bool alloc(cat_plan_s* p, T** ptr, size_t count) {
-  const size_t bytes = count ? count * sizeof(T) : 16;
-  if (cudaMalloc((void**)ptr, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    *ptr = nullptr;
-    return false;
-  }
-  p->workspace_bytes += bytes;
-  return true;
-}
-
-// The status word, cleared; `fail` releases the half-built plan.
-int fail(cat_plan_s* p, int st) {
-  cudaGetLastError();
-  cat_plan_destroy(p);
-  return st;
-}
-
-bool alloc_status(cat_plan_s* p) {
-  return alloc(p, &p->status, 1) && cat::settled([&](cudaStream_t s) {
-           return cudaMemsetAsync(p->status, 0, sizeof(unsigned int), s);
-         }) == cudaSuccess;
-}
+using cat::Span2;
+using cat::alloc;
+using cat::alloc_status;
+using cat::aliased;
+using cat::elem_size;
+using cat::fail;
+using cat::flat;
+using cat::new_plan;
+using cat::overlap;
+using cat::status_of;
 
 }  // namespace
 
@@ -113,6 +42,19 @@ void free_op(cat_plan_s* p) {
   cudaFree(p->ln.part);
   cudaFree(p->cl.chunks);
   cudaFree(p->cl.part);
+  cudaFree(p->em.first);
+  cudaFree(p->em.order);
+  cudaFree(p->em.sid);
+  cudaFree(p->em.part);
+  cudaFree(p->rn.part);
+  cudaFree(p->xe.count);
+  cudaFree(p->xe.rows);
+  cudaFree(p->xe.tgt);
+  cudaFree(p->xe.hit);
+  cudaFree(p->xe.part);
+  cudaFree(p->xe.stat);
+  cudaFree(p->xe.d);
+  cudaFree(p->xe.dxacc);
   delete[] p->cl.first_chunk;
   delete[] p->cl.sizes;
   delete[] p->cl.dtypes;

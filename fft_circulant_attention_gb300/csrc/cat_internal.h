@@ -6,6 +6,7 @@
 #include <stddef.h>
 
 #include "fft_device.cuh"
+#include "ids.cuh"
 
 namespace cat {
 
@@ -108,10 +109,73 @@ struct ClipCfg {
   double* part;            // device, a sum of squares a CTA
 };
 
+// Embedding call (embed.cu): rows x looked up into y, or (backward) rows x
+// summed into y, added to it where `add`.
+struct EmbedArgs {
+  Ids ids;
+  const void* x; void* y;
+  int tokens, add;
+};
+
+// Residual addition with its norms (resnorm_fwd.cu, resnorm_bwd.cu).
+struct ResNormArgs {
+  const void* r; const void* b; const void* gate;
+  const void* pg; const void* pb; const void* gamma; const void* beta;
+  void* h; void* y;
+  float* stats;            // [2 or 4][rows]: mean and rstd of H, of B
+  const void* hin; const void* dh; const void* dy;
+  void* dr; void* db; void* dgate; void* dpg; void* dpb; void* dgamma; void* dbeta;
+  float* part;             // [max_parts][5][D] partial sums over the rows
+  int gate_kind;           // 0 none, 1 a value a channel, 2 a row a token
+  int post, max_parts, rows, D;
+  float eps, scale;
+};
+
+// Cross entropy call (xent.cu).
+struct XentArgs {
+  const void* x; const void* w;
+  float* loss; float* lse; const float* dloss;
+  void* dx; void* dw;
+  int dloss_each;          // 1: dloss holds a value a token, 0: one for all
+  // filled from the plan
+  int V, D, ld;
+  const int* count; const int* rows; const int* tgt;
+  const float2* stat;
+  float* hit;
+  float2* part;
+};
+
 struct AttnArgs;
 
-// What the plans of cat_plan_create_attn, _layernorm and _clip hold.
-enum Op { OP_CIRCULANT = 0, OP_ATTN = 1, OP_LAYERNORM = 2, OP_CLIP = 3 };
+// What the plans of the operators hold.
+enum Op {
+  OP_CIRCULANT = 0, OP_ATTN = 1, OP_LAYERNORM = 2, OP_CLIP = 3, OP_EMBED = 4, OP_RESNORM = 5,
+  OP_XENT = 6
+};
+struct EmbedCfg {
+  int max_tokens, V, range;
+  float scale;
+  int* first;              // [V + 1]: where an id's tokens start in the sorted list
+  int* order;              // [max_tokens] the tokens, sorted by id
+  int* sid;                // [max_tokens] their ids
+  float* part;             // [pieces][2][D] partial rows
+};
+struct ResNormCfg {
+  int max_rows, post, max_parts;
+  float eps, scale;
+  float* part;
+};
+struct XentCfg {
+  int max_tokens, V, grad, piece;
+  int* count;              // how many tokens have a target
+  int* rows;               // [max_tokens] these tokens
+  int* tgt;                // [max_tokens] their targets
+  float* hit;              // [max_tokens] their targets' logits
+  float2* part;            // [runs][max_tokens] maximum and sum over a run of the vocabulary
+  float2* stat;            // [max_tokens] lse and upstream gradient
+  float* d;                // [max_tokens][piece]
+  float* dxacc;            // [max_tokens][D]
+};
 struct AttnCfg {
   int max_tokens, max_seqs, Hq, Hkv, dh, causal;
   float scale;
@@ -214,6 +278,9 @@ struct cat_plan_s {
   cat::AttnCfg at;
   cat::NormCfg ln;
   cat::ClipCfg cl;
+  cat::EmbedCfg em;
+  cat::ResNormCfg rn;
+  cat::XentCfg xe;
   char desc[512];
 };
 
@@ -423,6 +490,25 @@ int clip_grid(int sms);
 int clip_max_parts(int count, int sms);
 cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
                         float* norm, bool scale, cudaStream_t st);
+// Embedding (embed.cu).  embed_range: ids a sorting CTA owns; embed_piece: places
+// of the sorted list a group of threads sums.
+int embed_range(int V, int sms);
+size_t embed_part_count(int max_tokens, int D);
+cudaError_t setup_embed();
+cudaError_t launch_embed(const cat_plan_s* p, const EmbedArgs& a, bool backward);
+
+// Residual addition with its norms (resnorm_fwd.cu, resnorm_bwd.cu).
+int resnorm_parts(int sms);
+size_t resnorm_part_count(int sms, int D);
+cudaError_t setup_resnorm(int D, int dtype, int post);
+cudaError_t launch_resnorm_forward(const ResNormArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_resnorm_backward(const ResNormArgs& a, int dtype, cudaStream_t st);
+
+// Cross entropy over a vocabulary (xent.cu).
+int xent_piece(int max_tokens, int V);
+size_t xent_part_count(int max_tokens, int V);
+cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens, bool back);
+
 // Device and host memory of a plan's operator (block_api.cu).
 void free_op(cat_plan_s* p);
 

@@ -1,0 +1,358 @@
+// Embedding: rows of a table looked up by token, and the table's gradient.
+//   Y[i] = scale·W[id_i],   dW[v] = scale·Σ_{i: id_i = v} dY[i],
+// tokens without an id (negative) give rows of zeros and no gradient.
+//
+// Bound by memory: each row is read once and written once.  For the gradient
+// the tokens are first sorted by id, so that every row of dW is summed in the
+// order of its tokens and written once: no atomics on values, results repeat
+// bit for bit.  Three launches:
+//   sort:  a CTA owns a range of ids.  It reads all ids, counts those below its
+//          range (where its part of the sorted list starts) and those of each id
+//          of its own by warp (each warp has a stretch of the tokens), and puts
+//          its tokens in place, in order.  No CTA waits for another.
+//   sum:   the sorted list in pieces of equal length, a group of threads each; a
+//          run of equal ids within a piece is a finished row, a run that crosses
+//          pieces leaves partial rows (fp32).  Beside it the rows without tokens
+//          are cleared.
+//   join:  the partial rows of each run that crosses pieces, first piece first.
+#include "cat_internal.h"
+#include "ids.cuh"
+#include "rows.cuh"
+#include "../../include/cat.h"
+
+namespace cat {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRange = 1024;        // most ids of a sorting CTA
+constexpr int kZeroRows = 64;           // ids whose rows a clearing CTA looks at
+constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
+
+// A CTA copies `per` rows.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads)
+embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens, int V, int D,
+                 int per, float scale, unsigned int* status) {
+  using Vc = Vec<T, VEC>;
+  const int nv = D / VEC;
+  const int row0 = blockIdx.x * per;
+  const int n = min(per, tokens - row0) * nv;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int r = i / nv, c = (i - r * nv) * VEC, row = row0 + r;
+    const int id = id_at(ids, row, V);
+    float v[VEC];
+    if (id >= 0) {
+      load<T, VEC>(W + (size_t)id * D + c, v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] *= scale;
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+      if (id == -2 && c == 0) report(status, 0x701);
+    }
+    Vc::st(Y + (size_t)row * D + c, v);
+  }
+}
+
+// Block-wide exclusive sum over threads 0 .. kSortThreads - 1; *total: of all.
+__device__ __forceinline__ int block_scan(int v, int* red, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = red[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    red[lane] = w;
+  }
+  __syncthreads();
+  *total = red[kSortWarps - 1];
+  return x - v + (warp ? red[warp - 1] : 0);
+}
+
+// first[v]: where id v's tokens start in the sorted list (first[V]: its length);
+// order: the tokens; sid: their ids.
+__global__ void __launch_bounds__(kSortThreads)
+embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first,
+                  int* __restrict__ order, int* __restrict__ sid, unsigned int* status) {
+  extern __shared__ int hist[];                 // [kSortWarps][range]
+  __shared__ int red[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lo = blockIdx.x * range, n = min(range, V - lo);
+  for (int i = threadIdx.x; i < kSortWarps * range; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+  // This warp's stretch of the tokens.
+  const int steps = (tokens + 32 * kSortWarps - 1) / (32 * kSortWarps);
+  const long long t0 = (long long)warp * steps * 32;
+  int* h = hist + warp * range;
+  int below = 0;
+  bool bad = false;
+#pragma unroll 4
+  for (int s = 0; s < steps; ++s) {
+    const long long t = t0 + 32 * s + lane;
+    const int id = t < tokens ? id_at(ids, t, V) : -1;
+    bad |= id == -2;
+    below += id >= 0 && id < lo;
+    const bool mine = id >= lo && id < lo + n;
+    const unsigned any = __ballot_sync(0xffffffffu, mine);
+    if (any) {
+      if (mine) {
+        const unsigned same = __match_any_sync(any, id);
+        if (lane == __ffs(same) - 1) h[id - lo] += __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+  if (bad && blockIdx.x == 0) report(status, 0x702);
+  __syncthreads();
+  int base, count = 0, own;
+  block_scan(below, red, &base);
+  __syncthreads();
+  for (int w = 0; (int)threadIdx.x < n && w < kSortWarps; ++w) count += hist[w * range + threadIdx.x];
+  int at = base + block_scan(count, red, &own);
+  if ((int)threadIdx.x < n) {
+    first[lo + threadIdx.x] = at;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = hist[w * range + threadIdx.x];
+      hist[w * range + threadIdx.x] = at;
+      at += c;
+    }
+  }
+  if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
+  __syncthreads();
+  if (own == 0) return;
+#pragma unroll 4
+  for (int s = 0; s < steps; ++s) {
+    const long long t = t0 + 32 * s + lane;
+    const int id = t < tokens ? id_at(ids, t, V) : -1;
+    const bool mine = id >= lo && id < lo + n;
+    const unsigned any = __ballot_sync(0xffffffffu, mine);
+    if (any) {
+      if (mine) {
+        const unsigned same = __match_any_sync(any, id);
+        const int start = h[id - lo];
+        const int pos = start + __popc(same & ((1u << lane) - 1));
+        order[pos] = (int)t;
+        sid[pos] = id;
+        __syncwarp(any);
+        if (lane == __ffs(same) - 1) h[id - lo] = start + __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// dst = scale·acc, or dst + scale·acc.
+template <typename T, int VEC>
+__device__ __forceinline__ void put(T* dst, const float* acc, float scale, bool add) {
+  float v[VEC];
+  if (add) {
+    using Raw = typename Vec<T, VEC>::Raw;
+    Vec<T, VEC>::widen(__ldcg(reinterpret_cast<const Raw*>(dst)), v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf(scale, acc[e], v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = scale * acc[e];
+  }
+  Vec<T, VEC>::st(dst, v);
+}
+
+// Pieces of P places of the sorted list, a group of TPR threads each (gridDim.y
+// blocks of TPR vectors cover a row), then CTAs that clear rows without tokens.
+template <typename T, int VEC, int TPR>
+__global__ void __launch_bounds__(kThreads)
+embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __restrict__ dY,
+                 T* dW, float* __restrict__ part, int V, int D, int P, int piece_ctas, float scale,
+                 int add) {
+  constexpr int kGroups = kThreads / TPR;
+  using Vc = Vec<T, VEC>;
+  const int c = (blockIdx.y * TPR + threadIdx.x % TPR) * VEC;
+  const bool in = c < D;
+  pdl_wait();
+  if ((int)blockIdx.x >= piece_ctas) {
+    const int v0 = (blockIdx.x - piece_ctas) * kZeroRows;
+    float z[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) z[e] = 0.f;
+    for (int v = v0 + threadIdx.x / TPR; v < min(V, v0 + kZeroRows); v += kGroups)
+      if (in && __ldcg(first + v) == __ldcg(first + v + 1)) Vc::st(dW + (size_t)v * D + c, z);
+    return;
+  }
+  const int piece = blockIdx.x * kGroups + threadIdx.x / TPR;
+  const int total = __ldcg(first + V);
+  const long long q0 = (long long)piece * P;
+  if (q0 >= total) return;
+  const int p0 = (int)q0, p1 = (int)min((long long)total, q0 + P);
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  int cur = __ldcg(sid + p0);
+  // The run of `cur` ends here (or at the piece's end).
+  auto flush = [&] {
+    if (in) {
+      const int a = __ldcg(first + cur), b = __ldcg(first + cur + 1);
+      if (a >= p0 && b <= p1) {
+        put<T, VEC>(dW + (size_t)cur * D + c, acc, scale, add);
+      } else {
+        float* q = part + ((size_t)piece * 2 + (a >= p0)) * D + c;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q[e] = acc[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  };
+  constexpr int U = 4;
+  for (int p = p0; p < p1; p += U) {
+    typename Vc::Raw raw[U];
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = min(p + u, p1 - 1);
+      id[u] = __ldcg(sid + q);
+      if (in) raw[u] = Vc::ldr(dY + (size_t)__ldcg(order + q) * D + c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p + u >= p1) break;
+      if (id[u] != cur) {
+        flush();
+        cur = id[u];
+      }
+      float v[VEC];
+      if (in) {
+        Vc::widen(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += v[e];
+      }
+    }
+  }
+  flush();
+}
+
+// A piece whose last run starts in it and goes on joins that run.
+template <typename T, int VEC, int TPR>
+__global__ void __launch_bounds__(kThreads)
+embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, int V, int D, int P,
+                  float scale, int add) {
+  constexpr int kGroups = kThreads / TPR;
+  const int c = (blockIdx.y * TPR + threadIdx.x % TPR) * VEC;
+  pdl_wait();
+  const int piece = blockIdx.x * kGroups + threadIdx.x / TPR;
+  const int total = __ldcg(first + V);
+  const long long q0 = (long long)piece * P;
+  if (c >= D || q0 + P >= total) return;
+  const int p0 = (int)q0, p1 = p0 + P;
+  const int v = __ldcg(sid + p1 - 1);
+  const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
+  if (a < p0 || b <= p1) return;
+  const float* q = part + ((size_t)piece * 2 + 1) * D + c;
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = __ldcg(q + e);
+  const int last = (b - 1) / P;
+#pragma unroll 8
+  for (int i = piece + 1; i <= last; ++i) {
+    q = part + (size_t)i * 2 * D + c;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] += __ldcg(q + e);
+  }
+  put<T, VEC>(dW + (size_t)v * D + c, acc, scale, add);
+}
+
+// Places of a piece: at most 1024 pieces, so that a run of them all is joined
+// in a bounded time, and at least 16 places, so that partial rows stay few.
+int piece_length(int tokens) {
+  const int p = (tokens + 1023) / 1024;
+  return p < 16 ? 16 : p;
+}
+
+// Ids of a sorting CTA: an equal share of the vocabulary, at most kSortRange.
+int sort_range(int V, int sms) {
+  const int r = (V + sms - 1) / sms;
+  return r < 32 ? 32 : r > kSortRange ? kSortRange : r;
+}
+
+template <typename T, int VEC, int TPR>
+cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) {
+  const int groups = kThreads / TPR;
+  const int P = piece_length(a.tokens), pieces = (a.tokens + P - 1) / P;
+  const int ctas = (pieces + groups - 1) / groups;
+  const int cols = (D / VEC + TPR - 1) / TPR;
+  const int zero = a.add ? 0 : (c.V + kZeroRows - 1) / kZeroRows;
+  cudaError_t e = launch_dependent(
+      embed_sum_kernel<T, VEC, TPR>, dim3(ctas + zero, cols), dim3(kThreads), 0, st,
+      (const int*)c.first, (const int*)c.order, (const int*)c.sid, static_cast<const T*>(a.x),
+      static_cast<T*>(a.y), c.part, c.V, D, P, ctas, c.scale, a.add);
+  if (e != cudaSuccess || pieces < 2) return e;
+  return launch_dependent(embed_join_kernel<T, VEC, TPR>, dim3(ctas, cols), dim3(kThreads), 0, st,
+                          (const int*)c.first, (const int*)c.sid, (const float*)c.part,
+                          static_cast<T*>(a.y), c.V, D, P, c.scale, a.add);
+}
+
+template <typename T, int VEC>
+cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, unsigned int* status,
+                cudaStream_t st) {
+  const int nv = D / VEC;
+  if (!backward) {
+    const int per = nv >= kLookup ? 1 : kLookup / nv;
+    embed_fwd_kernel<T, VEC><<<(a.tokens + per - 1) / per, kThreads, 0, st>>>(
+        a.ids, static_cast<const T*>(a.x), static_cast<T*>(a.y), a.tokens, c.V, D, per, c.scale,
+        status);
+    return cudaGetLastError();
+  }
+  embed_sort_kernel<<<(c.V + c.range - 1) / c.range, kSortThreads,
+                      (size_t)kSortWarps * c.range * sizeof(int), st>>>(
+      a.ids, a.tokens, c.V, c.range, c.first, c.order, c.sid, status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (nv <= 8) return sums<T, VEC, 8>(c, a, D, st);
+  if (nv <= 32) return sums<T, VEC, 32>(c, a, D, st);
+  if (nv <= 64) return sums<T, VEC, 64>(c, a, D, st);
+  if (nv <= 128) return sums<T, VEC, 128>(c, a, D, st);
+  return sums<T, VEC, 256>(c, a, D, st);
+}
+
+template <typename T, int FULL>
+cudaError_t by_width(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward,
+                     unsigned int* status, cudaStream_t st) {
+  // The widest vector that divides the rows keeps every row start aligned.
+  if (D % FULL == 0) return run<T, FULL>(c, a, D, backward, status, st);
+  if (D % 2 == 0) return run<T, 2>(c, a, D, backward, status, st);
+  return run<T, 1>(c, a, D, backward, status, st);
+}
+
+}  // namespace
+
+int embed_range(int V, int sms) { return sort_range(V, sms); }
+
+size_t embed_part_count(int max_tokens, int D) {
+  const int P = piece_length(max_tokens);
+  // (Fewer tokens have at most as many pieces: below 1024 of them, one in 16.)
+  const size_t pieces = max_tokens > 16 * 1024 ? 1024 : (max_tokens + P - 1) / P;
+  return pieces * 2 * D;
+}
+
+cudaError_t setup_embed() { return allow_max_smem(embed_sort_kernel); }
+
+cudaError_t launch_embed(const cat_plan_s* p, const EmbedArgs& a, bool backward) {
+  return p->dtype == CAT_BF16
+             ? by_width<__nv_bfloat16, 8>(p->em, a, p->D, backward, p->status, p->stream)
+             : by_width<float, 4>(p->em, a, p->D, backward, p->status, p->stream);
+}
+
+}  // namespace cat

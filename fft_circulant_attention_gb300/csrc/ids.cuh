@@ -1,0 +1,23 @@
+// Token ids: 32- or 64-bit integers on the device.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace cat {
+
+struct Ids {
+  const void* p;
+  int wide;                // 64 bits each
+};
+
+// Id i of a call: -1 where the token has none (a negative id), -2 where the id
+// is outside the vocabulary.
+__device__ __forceinline__ int id_at(const Ids& ids, long long i, int vocab) {
+  if (ids.wide) {
+    const long long v = __ldg(static_cast<const long long*>(ids.p) + i);
+    return v < 0 ? -1 : v >= vocab ? -2 : (int)v;
+  }
+  const int v = __ldg(static_cast<const int*>(ids.p) + i);
+  return v < 0 ? -1 : v >= vocab ? -2 : v;
+}
+
+}  // namespace cat

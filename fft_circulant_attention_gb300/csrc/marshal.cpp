@@ -1,5 +1,5 @@
 // Native marshalling of the operator plans' Python calls (attention, layer
-// norm, clipping): checks the tensors, allocates the outputs that were not
+// norm, clipping, embedding, residual norms, cross entropy): checks the tensors, allocates the outputs that were not
 // given and calls the C interface.  In Python these steps take longer than
 // the kernels of a small call (82 tokens in 3 sequences, 2 heads of 32, GB300:
 // 16 us a call from Python, 7.2 us from here, of which the C call takes 5.2;
@@ -29,6 +29,16 @@ using NormBwd = int (*)(void*, const void*, const void*, const float*, const flo
                         void*, void*, void*, int);
 using ClipNorm = int (*)(void*, void* const*, float*);
 using ClipScale = int (*)(void*, void* const*, void* const*, float, float*);
+using EmbedFwd = int (*)(void*, const void*, int, const void*, void*, int);
+using EmbedBwd = int (*)(void*, const void*, int, const void*, void*, int, int);
+using ResFwd = int (*)(void*, const void*, const void*, const void*, int, const void*, const void*,
+                       const void*, const void*, void*, void*, float*, int);
+using ResBwd = int (*)(void*, const void*, const void*, const void*, int, const void*, const void*,
+                       const void*, const float*, const void*, const void*, void*, void*, void*,
+                       void*, void*, void*, void*, int);
+using XentFwd = int (*)(void*, const void*, const void*, const void*, int, float*, float*, int);
+using XentBwd = int (*)(void*, const void*, const void*, const void*, int, const float*,
+                        const float*, int, void*, void*, int);
 
 struct Handle {
   void* fn[2];
@@ -153,7 +163,8 @@ PyObject* result(int status, std::initializer_list<at::Tensor*> outs) {
   PyObject* r = PyTuple_New((Py_ssize_t)outs.size());
   Py_ssize_t i = 0;
   for (at::Tensor* t : outs) {
-    PyObject* w = r ? THPVariable_Wrap(*t) : nullptr;
+    // An output that the call does not have is None.
+    PyObject* w = !r ? nullptr : t->defined() ? THPVariable_Wrap(*t) : Py_NewRef(Py_None);
     if (!w) {
       Py_XDECREF(r);
       return nullptr;
@@ -292,16 +303,16 @@ PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// X and its rows; gamma, beta or null pointers.
-const at::Tensor* norm_input(const Handle& p, PyObject* o, int64_t* nrows) {
-  const at::Tensor* x = tensor(p, o, "X", p.type);
+// A norm's input (of that name) and its rows; gamma, beta or null pointers.
+const at::Tensor* norm_input(const Handle& p, PyObject* o, const char* name, int64_t* nrows) {
+  const at::Tensor* x = tensor(p, o, name, p.type);
   if (!x) return nullptr;
   if (x->dim() < 1 || x->size(-1) != p.dims[0]) {
-    bad("X", "does not have the plan's width as its last dimension");
+    bad(name, "does not have the plan's width as its last dimension");
     return nullptr;
   }
   if (!x->is_contiguous()) {
-    bad("X", "must be contiguous");
+    bad(name, "must be contiguous");
     return nullptr;
   }
   *nrows = x->numel() / p.dims[0];
@@ -321,7 +332,7 @@ PyObject* ln_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Handle* p = handle_of(a[0]);
     int64_t nrows = 0;
-    const at::Tensor* x = p ? norm_input(*p, a[1], &nrows) : nullptr;
+    const at::Tensor* x = p ? norm_input(*p, a[1], "X", &nrows) : nullptr;
     const void *w, *b;
     if (!x || !weight(*p, a[2], "gamma", &w) || !weight(*p, a[3], "beta", &b)) return nullptr;
     const auto lead = x->sizes().slice(0, x->dim() - 1);
@@ -344,7 +355,7 @@ PyObject* ln_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Handle* p = handle_of(a[0]);
     int64_t nrows = 0;
-    const at::Tensor* x = p ? norm_input(*p, a[1], &nrows) : nullptr;
+    const at::Tensor* x = p ? norm_input(*p, a[1], "X", &nrows) : nullptr;
     const void* w;
     if (!x || !weight(*p, a[2], "gamma", &w)) return nullptr;
     const auto lead = x->sizes().slice(0, x->dim() - 1);
@@ -429,11 +440,245 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Token ids: int32 or int64, of any shape; their C type code.
+const at::Tensor* token_ids(const Handle& p, PyObject* o, const char* name, int* code) {
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s must be a tensor", name);
+    return nullptr;
+  }
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong) {
+    bad(name, "must be int32 or int64");
+    return nullptr;
+  }
+  if (t.device() != p.device) {
+    bad(name, "is not on the plan's device");
+    return nullptr;
+  }
+  if (!t.is_contiguous()) {
+    bad(name, "must be contiguous");
+    return nullptr;
+  }
+  if (t.numel() > INT32_MAX) {
+    bad(name, "has too many tokens");
+    return nullptr;
+  }
+  *code = t.scalar_type() == at::kInt ? 2 : 3;       // CAT_I32, CAT_I64
+  return &t;
+}
+
+// The shape of one row of `width` for each token.
+std::vector<int64_t> rows_of(const at::Tensor& ids, int64_t width) {
+  std::vector<int64_t> s(ids.sizes().begin(), ids.sizes().end());
+  s.push_back(width);
+  return s;
+}
+
+// embed_forward(handle, ids, W, Y)
+PyObject* embed_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 4)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    int code = 0;
+    const at::Tensor* ids = p ? token_ids(*p, a[1], "ids", &code) : nullptr;
+    const at::Tensor* w =
+        ids ? dense(*p, a[2], "W", p->type, {p->dims[0], p->dims[1]}) : nullptr;
+    at::Tensor y;
+    if (!w || !output(*p, a[3], "Y", p->type, rows_of(*ids, p->dims[1]), &y)) return nullptr;
+    const int st = call<EmbedFwd>(p->fn[0], p->plan, ids->data_ptr(), code, w->data_ptr(),
+                                  y.data_ptr(), (int)ids->numel());
+    return st ? PyLong_FromLong(st) : THPVariable_Wrap(y);
+  });
+}
+
+// embed_backward(handle, ids, dY, dW, accumulate)
+PyObject* embed_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    int code = 0;
+    const at::Tensor* ids = p ? token_ids(*p, a[1], "ids", &code) : nullptr;
+    const at::Tensor* g =
+        ids ? dense(*p, a[2], "dY", p->type, rows_of(*ids, p->dims[1])) : nullptr;
+    const int add = g ? PyObject_IsTrue(a[4]) : -1;
+    if (add < 0) return nullptr;
+    if (add && a[3] == Py_None)
+      return bad("dW", "must be given to add to"), nullptr;
+    at::Tensor dw;
+    if (!output(*p, a[3], "dW", p->type, {p->dims[0], p->dims[1]}, &dw)) return nullptr;
+    const int st = call<EmbedBwd>(p->fn[1], p->plan, ids->data_ptr(), code, g->data_ptr(),
+                                  dw.data_ptr(), add, (int)ids->numel());
+    return st ? PyLong_FromLong(st) : THPVariable_Wrap(dw);
+  });
+}
+
+// A gate: none, a value a channel, or a row a token (*each).
+bool gate_of(const Handle& p, PyObject* o, at::IntArrayRef shape, const void** ptr, int* each,
+             std::vector<int64_t>* own) {
+  *ptr = nullptr;
+  *each = 0;
+  if (o == Py_None) return true;
+  const at::Tensor* t = tensor(p, o, "gate", p.type);
+  if (!t) return false;
+  if (t->dim() == 1 && t->size(0) == p.dims[0] && shape.size() != 1) {
+    *each = 0;
+  } else if (t->sizes() == shape) {
+    *each = shape.size() != 1;
+  } else {
+    return bad("gate", "must have one value a channel or the shape of B");
+  }
+  if (!t->is_contiguous()) return bad("gate", "must be contiguous");
+  own->assign(t->sizes().begin(), t->sizes().end());
+  *ptr = t->data_ptr();
+  return true;
+}
+
+std::vector<int64_t> stats_shape(const Handle& p, const at::Tensor& x) {
+  std::vector<int64_t> s{p.dims[1] ? 4 : 2};
+  s.insert(s.end(), x.sizes().begin(), x.sizes().end() - 1);
+  return s;
+}
+
+// resnorm_forward(handle, R, B, gate, gamma, beta, post_gamma, post_beta, H, Y, stats)
+PyObject* resnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    int64_t nrows = 0;
+    const at::Tensor* b = p ? norm_input(*p, a[2], "B", &nrows) : nullptr;
+    const at::Tensor* r = b ? dense(*p, a[1], "R", p->type, b->sizes()) : nullptr;
+    const void *gate, *w, *s, *pw, *ps;
+    int each;
+    std::vector<int64_t> shape;
+    if (!r || !gate_of(*p, a[3], b->sizes(), &gate, &each, &shape) ||
+        !weight(*p, a[4], "gamma", &w) || !weight(*p, a[5], "beta", &s) ||
+        !weight(*p, a[6], "post_gamma", &pw) || !weight(*p, a[7], "post_beta", &ps))
+      return nullptr;
+    at::Tensor h, y, stats;
+    if (!output(*p, a[8], "H", p->type, b->sizes(), &h) ||
+        !output(*p, a[9], "Y", p->type, b->sizes(), &y) ||
+        !output(*p, a[10], "stats", at::kFloat, stats_shape(*p, *b), &stats))
+      return nullptr;
+    if (nrows > INT32_MAX) return bad("B", "has too many rows"), nullptr;
+    const int st = call<ResFwd>(p->fn[0], p->plan, r->data_ptr(), b->data_ptr(), gate, each, pw,
+                                ps, w, s, h.data_ptr(), y.data_ptr(),
+                                static_cast<float*>(stats.data_ptr()), (int)nrows);
+    return result(st, {&h, &y, &stats});
+  });
+}
+
+// resnorm_backward(handle, H, B, gate, gamma, post_gamma, post_beta, stats, dH, dY,
+//                  dR, dB, dgate, dgamma, dbeta, dpost_gamma, dpost_beta)
+PyObject* resnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 17)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    int64_t nrows = 0;
+    const at::Tensor* h = p ? norm_input(*p, a[1], "H", &nrows) : nullptr;
+    const at::Tensor* b = h ? dense(*p, a[2], "B", p->type, h->sizes()) : nullptr;
+    const void *gate, *w, *pw, *ps;
+    int each;
+    std::vector<int64_t> shape;
+    if (!b || !gate_of(*p, a[3], h->sizes(), &gate, &each, &shape) ||
+        !weight(*p, a[4], "gamma", &w) || !weight(*p, a[5], "post_gamma", &pw) ||
+        !weight(*p, a[6], "post_beta", &ps))
+      return nullptr;
+    const at::Tensor* stats = dense(*p, a[7], "stats", at::kFloat, stats_shape(*p, *h));
+    if (!stats) return nullptr;
+    const void* dh = nullptr;
+    if (a[8] != Py_None) {
+      const at::Tensor* t = dense(*p, a[8], "dH", p->type, h->sizes());
+      if (!t) return nullptr;
+      dh = t->data_ptr();
+    }
+    const at::Tensor* dy = dense(*p, a[9], "dY", p->type, h->sizes());
+    at::Tensor dr, db, dg, dw, ds, dpw, dps;
+    if (!dy || !output(*p, a[10], "dR", p->type, h->sizes(), &dr) ||
+        !output(*p, a[11], "dB", p->type, h->sizes(), &db) ||
+        !output(*p, a[13], "dgamma", p->type, {p->dims[0]}, &dw) ||
+        !output(*p, a[14], "dbeta", p->type, {p->dims[0]}, &ds))
+      return nullptr;
+    if (gate ? !output(*p, a[12], "dgate", p->type, shape, &dg) : a[12] != Py_None)
+      return gate ? nullptr : (bad("dgate", "is given without a gate"), nullptr);
+    if (p->dims[1]) {
+      if (!output(*p, a[15], "dpost_gamma", p->type, {p->dims[0]}, &dpw) ||
+          !output(*p, a[16], "dpost_beta", p->type, {p->dims[0]}, &dps))
+        return nullptr;
+    } else if (a[15] != Py_None || a[16] != Py_None) {
+      return bad("dpost_gamma or dpost_beta", "is given to a plan without a norm behind the block"),
+             nullptr;
+    }
+    if (nrows > INT32_MAX) return bad("H", "has too many rows"), nullptr;
+    auto at_ = [](at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    const int st = call<ResBwd>(p->fn[1], p->plan, h->data_ptr(), b->data_ptr(), gate, each, pw,
+                                ps, w, static_cast<const float*>(stats->data_ptr()), dh,
+                                dy->data_ptr(), dr.data_ptr(), db.data_ptr(), at_(dg), at_(dpw),
+                                at_(dps), dw.data_ptr(), ds.data_ptr(), (int)nrows);
+    return result(st, {&dr, &db, &dg, &dw, &ds, &dpw, &dps});
+  });
+}
+
+// X [..., D], W [V, D] and targets [...] of a cross entropy call.
+bool xent_inputs(const Handle& p, PyObject* const* a, const at::Tensor** x, const at::Tensor** w,
+                 const at::Tensor** targets, int* code) {
+  *targets = token_ids(p, a[3], "targets", code);
+  *x = *targets ? dense(p, a[1], "X", p.type, rows_of(**targets, p.dims[1])) : nullptr;
+  *w = *x ? dense(p, a[2], "W", p.type, {p.dims[0], p.dims[1]}) : nullptr;
+  return *w != nullptr;
+}
+
+// xent_forward(handle, X, W, targets, loss, lse)
+PyObject* xent_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    const at::Tensor *x, *w, *t;
+    int code = 0;
+    if (!p || !xent_inputs(*p, a, &x, &w, &t, &code)) return nullptr;
+    at::Tensor loss, lse;
+    if (!output(*p, a[4], "loss", at::kFloat, t->sizes(), &loss) ||
+        !output(*p, a[5], "lse", at::kFloat, t->sizes(), &lse))
+      return nullptr;
+    const int st = call<XentFwd>(p->fn[0], p->plan, x->data_ptr(), w->data_ptr(), t->data_ptr(),
+                                 code, static_cast<float*>(loss.data_ptr()),
+                                 static_cast<float*>(lse.data_ptr()), (int)t->numel());
+    return result(st, {&loss, &lse});
+  });
+}
+
+// xent_backward(handle, X, W, targets, lse, dloss, dX, dW): dX, dW False: not wanted.
+PyObject* xent_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Handle* p = handle_of(a[0]);
+    const at::Tensor *x, *w, *t;
+    int code = 0;
+    if (!p || !xent_inputs(*p, a, &x, &w, &t, &code)) return nullptr;
+    const at::Tensor* lse = dense(*p, a[4], "lse", at::kFloat, t->sizes());
+    const at::Tensor* g = lse ? tensor(*p, a[5], "dloss", at::kFloat) : nullptr;
+    if (!g) return nullptr;
+    if (g->numel() != 1 && g->sizes() != t->sizes())
+      return bad("dloss", "must have one value, or the shape of targets"), nullptr;
+    if (!g->is_contiguous()) return bad("dloss", "must be contiguous"), nullptr;
+    at::Tensor dx, dw;
+    if (a[6] != Py_False && !output(*p, a[6], "dX", p->type, x->sizes(), &dx)) return nullptr;
+    if (a[7] != Py_False && !output(*p, a[7], "dW", p->type, w->sizes(), &dw)) return nullptr;
+    const int st = call<XentBwd>(
+        p->fn[1], p->plan, x->data_ptr(), w->data_ptr(), t->data_ptr(), code,
+        static_cast<const float*>(lse->data_ptr()), static_cast<const float*>(g->data_ptr()),
+        (int)(g->numel() != 1), dx.defined() ? dx.data_ptr() : nullptr,
+        dw.defined() ? dw.data_ptr() : nullptr, (int)t->numel());
+    return result(st, {&dx, &dw});
+  });
+}
+
 #define FAST(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(make),       FAST(set_list),   FAST(attn_forward),
                           FAST(attn_backward), FAST(ln_forward), FAST(ln_backward),
-                          FAST(clip),       {nullptr, nullptr, 0, nullptr}};
+                          FAST(clip),       FAST(embed_forward), FAST(embed_backward),
+                          FAST(resnorm_forward), FAST(resnorm_backward), FAST(xent_forward),
+                          FAST(xent_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,321 @@
+// Residual addition with gate, scale and the norms before and after a block,
+// backward.  With x̂ = (H - mean_H)·rstd_H, g = dY·gamma, b̂ = (B - mean_B)·rstd_B:
+//   dh = dH + rstd_H·(g - mean(g) - x̂·mean(g·x̂)),   dR = dh,
+//   u = post ? b̂·pg + pb : B,   dgate = scale·u·dh,   du = scale·gate·dh,
+//   dB = post ? rstd_B·(w - mean(w) - b̂·mean(w·b̂)) with w = du·pg : du,
+//   dgamma = Σ dY·x̂, dbeta = Σ dY, dpg = Σ du·b̂, dpb = Σ du over the rows, and
+//   dgate too where the gate is one of channels.
+//
+// Bound by memory: H, B, dH, dY (and a gate of rows) are read once, dR, dB (and
+// its gradient) written once.  A row is spread over as many threads as leave 8
+// elements each, so that a thread's columns of the five sums over the rows stay
+// in registers while its persistent CTA goes through its rows; above D = 2048
+// the sums are in shared memory, each column its thread's own.  A CTA writes one
+// partial row of each sum, a second kernel adds those in a fixed order: no
+// atomics, results repeat bit for bit.
+#include "resnorm.cuh"
+
+namespace cat {
+
+namespace {
+
+// The sums over the rows, as they lie in a partial row.
+enum { S_GAMMA = 0, S_BETA = 1, S_GATE = 2, S_PG = 3, S_PB = 4, kSums = 5 };
+
+// a and b summed over the TPR threads of row group `sub`; `red` holds two
+// floats a warp for each of four uses in turn, so that one barrier a call is
+// enough.
+template <int TPR, int BT>
+__device__ __forceinline__ void sum2(float& a, float& b, float2* red, int sub, int use) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (TPR > 32) {
+    red += use * (BT / 32);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(TPR) : "memory");
+    red += sub * (TPR / 32);
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) {
+      a += red[i].x;
+      b += red[i].y;
+    }
+  }
+}
+
+template <int TPR>
+constexpr int block_threads() {
+  return TPR > 256 ? TPR : 256;
+}
+template <int TPR, int E>
+constexpr int per_sm() {
+  return TPR > 256 ? 1 : 2;
+}
+
+// part: [gridDim.x][kSums][D].
+template <typename T, int VEC, int TPR, int E, int POST>
+__global__ void __launch_bounds__(block_threads<TPR>(), per_sm<TPR, E>())
+resnorm_bwd_kernel(ResNormArgs a) {
+  using V = Vec<T, VEC>;
+  using Raw = typename V::Raw;
+  constexpr int NV = E / VEC, BT = block_threads<TPR>(), kRows = BT / TPR;
+  constexpr bool kShared = TPR > 256;           // sums in shared memory
+  extern __shared__ float sm[];                 // [kSums][D]
+  __shared__ float2 red[4 * (BT / 32)];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, D = a.D;
+  float acc[kSums][kShared ? 1 : NV][VEC];
+  if (kShared) {
+    for (int c = threadIdx.x; c < kSums * D; c += BT) sm[c] = 0.f;
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSums; ++s)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[s][kShared ? 0 : k][e] = 0.f;
+  }
+  auto sum_to = [&](int s, int k, int c, int e, float v) {
+    if (kShared)
+      sm[s * D + c + e] += v;
+    else
+      acc[s][kShared ? 0 : k][e] += v;
+  };
+  const float inv = 1.f / (float)D, scale = a.scale;
+  const T* gamma = static_cast<const T*>(a.gamma);
+  const T* pg = static_cast<const T*>(a.pg);
+  const T* pb = static_cast<const T*>(a.pb);
+  int use = 0;
+  for (int row = blockIdx.x * kRows + sub; row < a.rows; row += gridDim.x * kRows, use ^= 2) {
+    const size_t off = (size_t)row * D;
+    const T* H = static_cast<const T*>(a.hin) + off;
+    const T* B = static_cast<const T*>(a.b) + off;
+    const T* dH = a.dh ? static_cast<const T*>(a.dh) + off : nullptr;
+    const T* dY = static_cast<const T*>(a.dy) + off;
+    const T* G = static_cast<const T*>(a.gate);
+    if (a.gate_kind == GATE_ROW) G += off;
+    Raw rb[NV], rh[NV];
+    float xh[NV][VEC], g[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + t) * VEC;
+      if (c < D) {
+        load<T, VEC>(H + c, xh[k]);
+        load<T, VEC>(dY + c, g[k]);
+        rb[k] = V::ldr(B + c);
+        if (dH) rh[k] = V::ldr(dH + c);
+      }
+    }
+    const float* st = a.stats + row;
+    const float mh = __ldg(st), rsh = __ldg(st + (size_t)a.rows);
+    const float mb = POST ? __ldg(st + 2 * (size_t)a.rows) : 0.f;
+    const float rsb = POST ? __ldg(st + 3 * (size_t)a.rows) : 0.f;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + t) * VEC;
+      if (c < D) {
+        float w[VEC];
+        load_or<T, VEC>(gamma, c, 1.f, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          xh[k][e] = (xh[k][e] - mh) * rsh;
+          sum_to(S_GAMMA, k, c, e, g[k][e] * xh[k][e]);
+          sum_to(S_BETA, k, c, e, g[k][e]);
+          g[k][e] *= w[e];
+          s1 += g[k][e];
+          s2 = fmaf(g[k][e], xh[k][e], s2);
+        }
+      }
+    }
+    sum2<TPR, BT>(s1, s2, red, sub, use);
+    s1 *= inv;
+    s2 *= inv;
+    // g becomes dh, then du·pg; xh becomes b̂.
+    float t1 = 0.f, t2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + t) * VEC;
+      if (c < D) {
+        float w[VEC], b[VEC], u[VEC];
+        if (dH) {
+          V::widen(rh[k], w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) w[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[k][e] = w[e] + rsh * (g[k][e] - s1 - xh[k][e] * s2);
+        V::st(static_cast<T*>(a.dr) + off + c, g[k]);
+        V::widen(rb[k], b);
+        if (POST) {
+          load_or<T, VEC>(pg, c, 1.f, w);
+          load_or<T, VEC>(pb, c, 0.f, u);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            b[e] = (b[e] - mb) * rsb;
+            u[e] = fmaf(b[e], w[e], u[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) u[e] = b[e];
+        }
+        if (a.gate_kind == GATE_ROW) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) u[e] *= scale * g[k][e];
+          if (a.dgate) V::st(static_cast<T*>(a.dgate) + off + c, u);
+        } else if (a.gate_kind == GATE_CHANNEL) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) sum_to(S_GATE, k, c, e, scale * u[e] * g[k][e]);
+        }
+        load_or<T, VEC>(G, c, 1.f, u);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          g[k][e] *= scale * u[e];
+          if (POST) {
+            sum_to(S_PG, k, c, e, g[k][e] * b[e]);
+            sum_to(S_PB, k, c, e, g[k][e]);
+            g[k][e] *= w[e];
+            t1 += g[k][e];
+            t2 = fmaf(g[k][e], b[e], t2);
+            xh[k][e] = b[e];
+          }
+        }
+      }
+    }
+    if (POST) {
+      sum2<TPR, BT>(t1, t2, red, sub, use + 1);
+      t1 *= inv;
+      t2 *= inv;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + t) * VEC;
+      if (c < D) {
+        if (POST) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) g[k][e] = rsb * (g[k][e] - t1 - xh[k][e] * t2);
+        }
+        V::st(static_cast<T*>(a.db) + off + c, g[k]);
+      }
+    }
+  }
+  float* to = a.part + (size_t)blockIdx.x * kSums * D;
+  if (!kShared) {
+    // The CTA's row groups one after another.
+    for (int w = 0; w < kRows; ++w) {
+      if (sub == w) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int c = (k * TPR + t) * VEC;
+          if (c < D) {
+#pragma unroll
+            for (int s = 0; s < kSums; ++s)
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                float* q = sm + s * D + c + e;
+                *q = (w ? *q : 0.f) + acc[s][kShared ? 0 : k][e];
+              }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < kSums * D; c += BT) to[c] = sm[c];
+}
+
+// The sums from the partial rows: a CTA takes 32 columns of one sum, its 32
+// warps every 32nd partial row each.
+constexpr int kRedWarps = 32;
+template <typename T>
+__global__ void __launch_bounds__(32 * kRedWarps)
+resnorm_reduce_kernel(const float* part, int nparts, ResNormArgs a) {
+  __shared__ float s[kRedWarps][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, D = a.D;
+  const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+  void* const outs[kSums] = {a.dgamma, a.dbeta, a.gate_kind == GATE_CHANNEL ? a.dgate : nullptr,
+                             a.dpg, a.dpb};
+  T* out = static_cast<T*>(outs[which]);
+  pdl_wait();
+  if (!out) return;
+  float v = 0.f;
+  if (c < D) {
+#pragma unroll 8
+    for (int i = w; i < nparts; i += kRedWarps)
+      v += __ldcg(part + ((size_t)i * kSums + which) * D + c);
+  }
+  s[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && c < D) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRedWarps; ++i) v += s[i][lane];
+    st_elem(out + c, v);
+  }
+}
+
+template <typename T, int VEC, int TPR, int E, int POST>
+cudaError_t bwd(const ResNormArgs& a, cudaStream_t st, bool setup) {
+  constexpr int BT = block_threads<TPR>();
+  const int per = BT / TPR, need = (a.rows + per - 1) / per;
+  const int most = a.max_parts / 2 * per_sm<TPR, E>();
+  const int grid = need < most ? need : most;
+  const size_t smem = (size_t)kSums * a.D * sizeof(float);
+  if (setup)
+    return smem > 40 * 1024 ? allow_max_smem(resnorm_bwd_kernel<T, VEC, TPR, E, POST>)
+                            : cudaSuccess;
+  resnorm_bwd_kernel<T, VEC, TPR, E, POST><<<grid, BT, smem, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(resnorm_reduce_kernel<T>, dim3((a.D + 31) / 32, kSums),
+                          dim3(32 * kRedWarps), 0, st, (const float*)a.part, grid, a);
+}
+
+template <typename T, int VEC, int POST>
+cudaError_t pick(const ResNormArgs& a, cudaStream_t st, bool setup) {
+  const int D = a.D;
+  if (D <= 32 * 8) return bwd<T, VEC, 32, 8, POST>(a, st, setup);
+  if (D <= 64 * 8) return bwd<T, VEC, 64, 8, POST>(a, st, setup);
+  if (D <= 128 * 8) return bwd<T, VEC, 128, 8, POST>(a, st, setup);
+  if (D <= 256 * 8) return bwd<T, VEC, 256, 8, POST>(a, st, setup);
+  if (D <= 512 * 8) return bwd<T, VEC, 512, 8, POST>(a, st, setup);
+  return bwd<T, VEC, 512, 16, POST>(a, st, setup);
+}
+
+template <typename T, int VEC>
+cudaError_t by_post(const ResNormArgs& a, cudaStream_t st, bool setup) {
+  return a.post ? pick<T, VEC, 1>(a, st, setup) : pick<T, VEC, 0>(a, st, setup);
+}
+
+}  // namespace
+
+int resnorm_parts(int sms) { return 2 * sms; }
+size_t resnorm_part_count(int sms, int D) { return (size_t)resnorm_parts(sms) * kSums * D; }
+
+// One call's launches; setup: only raises its kernel's shared-memory limit.
+static cudaError_t dispatch(const ResNormArgs& a, int dtype, cudaStream_t st, bool setup) {
+  // Full vectors where they divide the rows (every row start aligned).
+  if (dtype == CAT_BF16)
+    return a.D % 8 == 0 ? by_post<__nv_bfloat16, 8>(a, st, setup)
+                        : by_post<__nv_bfloat16, 1>(a, st, setup);
+  return a.D % 4 == 0 ? by_post<float, 4>(a, st, setup) : by_post<float, 1>(a, st, setup);
+}
+
+cudaError_t launch_resnorm_backward(const ResNormArgs& a, int dtype, cudaStream_t st) {
+  return dispatch(a, dtype, st, false);
+}
+
+cudaError_t setup_resnorm(int D, int dtype, int post) {
+  ResNormArgs a = {};
+  a.D = D;
+  a.post = post;
+  return dispatch(a, dtype, nullptr, true);
+}
+
+}  // namespace cat

@@ -44,6 +44,9 @@ typedef struct cat_plan_s *cat_plan_t;
 /* Storage type of X, W_A, V and O. */
 typedef enum { CAT_F32 = 0, CAT_BF16 = 1 } cat_dtype_t;
 
+/* Type of token ids and targets. */
+typedef enum { CAT_I32 = 2, CAT_I64 = 3 } cat_id_type_t;
+
 /* Status codes. */
 enum {
   CAT_OK = 0,
@@ -414,6 +417,131 @@ int cat_grad_norm(cat_plan_t plan, const void *const *grads, float *norm);
  */
 int cat_grad_clip(cat_plan_t plan, const void *const *grads, void *const *outs,
                   float max_norm, float *norm);
+
+/*
+ * The rest of a language model's training step: the embedding at its start, the
+ * residual stream between its layers, the cross entropy over the vocabulary at
+ * its end.  The conventions of the operators above hold.  Ids and targets are
+ * device arrays of 32- or 64-bit integers (id_type CAT_I32 or CAT_I64, aligned
+ * to their size); a negative one marks a token that has none (padding, no
+ * target), one of V or more is treated the same way and cat_plan_sync returns
+ * CAT_ERR_DEVICE_STATUS.  Arrays of the plan's dtype are dense and 16-byte
+ * aligned (CAT_ERR_MISALIGNED); outputs overlap neither inputs nor each other
+ * (CAT_ERR_ALIAS); T or rows above the plan's: CAT_ERR_PLAN_MISMATCH.
+ */
+
+/* Largest vocabulary, most tokens of an embedding and of a cross entropy call. */
+#define CAT_MAX_VOCAB (1 << 24)
+#define CAT_STEP_MAX_TOKENS (1 << 24)
+#define CAT_XENT_MAX_TOKENS (1 << 20)
+
+/*
+ * cat_plan_create_embed — rows of a table W [V, D], looked up by token, for at
+ * most max_tokens tokens a call (0 .. CAT_STEP_MAX_TOKENS); 1 <= V <=
+ * CAT_MAX_VOCAB, 1 <= D <= CAT_MAX_D, scale finite.
+ * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_embed(cat_plan_t *out, int max_tokens, int V, int D,
+                          int dtype, float scale, void *stream);
+
+/*
+ * cat_embed_forward — Y[i] = scale·W[ids[i]] for T tokens (Y [T, D]); a row of
+ * zeros where the token has no id.  T = 0: no-op.
+ */
+int cat_embed_forward(cat_plan_t plan, const void *ids, int id_type,
+                      const void *W, void *Y, int T);
+
+/*
+ * cat_embed_backward — dW[v] = scale·Σ dY[i] over the tokens i with ids[i] = v
+ * (fp32 sums in a fixed order, rounded once); dY [T, D], dW [V, D].
+ * accumulate = 1: the sums are added to dW (which may hold the gradient of
+ * output weights tied to the table), rows of ids that no token has keep their
+ * bits; 0: dW is overwritten, those rows with zeros.  Rows of dY whose token
+ * has no id are not read.
+ */
+int cat_embed_backward(cat_plan_t plan, const void *ids, int id_type,
+                       const void *dY, void *dW, int accumulate, int T);
+
+/*
+ * cat_plan_create_resnorm — what lies between two blocks of a residual stream:
+ * the block's output B, with a norm of its own (post = 1) or without (0), a
+ * gate and a scale, is added to the stream R, and the sum is normed for the next
+ * block.  At most max_rows rows a call (0 .. CAT_NORM_MAX_ROWS) of 1 <= D <=
+ * CAT_MAX_D elements; eps >= 0 (both norms'), scale finite.
+ * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_resnorm(cat_plan_t *out, int max_rows, int D, int dtype,
+                            int post, float eps, float scale, void *stream);
+
+/*
+ * cat_resnorm_forward — per row, with the layer norm LN of cat_layernorm_forward:
+ *   u = post ? LN(B; post_gamma, post_beta) : B,
+ *   H = R + scale·gate·u,   Y = LN(H; gamma, beta).
+ * gate: NULL (1), [D] (gate_rows = 0) or [rows, D] (gate_rows = 1).  The weights
+ * of the norms ([D] each) may be NULL (1 and 0); without post, post_gamma and
+ * post_beta must be.  stats (fp32, for the backward): [2][rows], or [4][rows]
+ * with post: mean and rstd of H, mean and rstd of B.  Y and stats are those of H
+ * before its rounding to the plan's dtype.
+ */
+int cat_resnorm_forward(cat_plan_t plan, const void *R, const void *B,
+                        const void *gate, int gate_rows, const void *post_gamma,
+                        const void *post_beta, const void *gamma,
+                        const void *beta, void *H, void *Y, float *stats,
+                        int rows);
+
+/*
+ * cat_resnorm_backward — from the forward's inputs, its H and stats, and the
+ * upstream gradients dH (NULL: zero) and dY of its outputs:
+ *   dh = dH + (gradient of LN at H for dY),  dR = dh,
+ *   dgate = scale·u·dh (summed over the rows where the gate is [D]),
+ *   du = scale·gate·dh,  dB = post ? (gradient of LN at B for du) : du,
+ * and the weights' gradients (fp32 sums over the rows, rounded once).  dgate and
+ * the weights' gradients may each be NULL (not wanted), all are overwritten.
+ * rows = 0 writes zeros to the sums over the rows.
+ */
+int cat_resnorm_backward(cat_plan_t plan, const void *H, const void *B,
+                         const void *gate, int gate_rows,
+                         const void *post_gamma, const void *post_beta,
+                         const void *gamma, const float *stats, const void *dH,
+                         const void *dY, void *dR, void *dB, void *dgate,
+                         void *dpost_gamma, void *dpost_beta, void *dgamma,
+                         void *dbeta, int rows);
+
+/*
+ * cat_plan_create_xent — softmax cross entropy over a vocabulary of V, from
+ * hidden states of width D (1 <= V <= CAT_MAX_VOCAB, 1 <= D <= CAT_MAX_D) and
+ * the output weights, for at most max_tokens tokens a call (0 ..
+ * CAT_XENT_MAX_TOKENS).  grad = 0: a plan for the forward alone, which needs
+ * far less workspace.
+ * Errors: CAT_ERR_INVALID_ARG, CAT_ERR_ALLOC, CAT_ERR_CUDA.
+ */
+int cat_plan_create_xent(cat_plan_t *out, int max_tokens, int V, int D,
+                         int dtype, int grad, void *stream);
+
+/*
+ * cat_xent_forward — for T tokens, X [T, D], W [V, D] and targets [T]:
+ *   l_iv = X_i·W_v,  lse[i] = log Σ_v exp(l_iv),  loss[i] = lse[i] - l_{i,targets[i]}
+ * (fp32).  Tokens without a target: both are 0, their rows of X are not read.
+ * The logits are not kept.  T = 0: no-op.
+ */
+int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
+                     const void *targets, int id_type, float *loss, float *lse,
+                     int T);
+
+/*
+ * cat_xent_backward — from the forward's inputs and its lse, for the upstream
+ * gradient dloss of the losses (fp32: one value for all tokens, dloss_each = 0,
+ * or [T], dloss_each = 1):
+ *   d_iv = dloss_i (exp(l_iv - lse_i) - [v = targets_i]),  dX = d·W,  dW = dᵀ·X.
+ * The logits are made again, a piece of the vocabulary at a time.  dX [T, D]
+ * and dW [V, D] are overwritten; either may be NULL (not wanted).  Tokens
+ * without a target have a zero row in dX and no part in dW.
+ * CAT_ERR_PLAN_MISMATCH too for a plan with grad = 0.
+ */
+int cat_xent_backward(cat_plan_t plan, const void *X, const void *W,
+                      const void *targets, int id_type, const float *lse,
+                      const float *dloss, int dloss_each, void *dX, void *dW,
+                      int T);
 
 /*
  * cat_plan_sync — wait for the plan's stream, then read the device status
