@@ -53,6 +53,9 @@ void free_op(cat_plan_s* p) {
   cudaFree(p->xe.hit);
   cudaFree(p->xe.part);
   cudaFree(p->xe.stat);
+  cudaFree(p->xe.inv);
+  cudaFree(p->xe.xp);
+  cudaFree(p->xe.wp);
   cudaFree(p->xe.d);
   cudaFree(p->xe.dxacc);
   delete[] p->cl.first_chunk;

@@ -137,12 +137,6 @@ struct XentArgs {
   float* loss; float* lse; const float* dloss;
   void* dx; void* dw;
   int dloss_each;          // 1: dloss holds a value a token, 0: one for all
-  // filled from the plan
-  int V, D, ld;
-  const int* count; const int* rows; const int* tgt;
-  const float2* stat;
-  float* hit;
-  float2* part;
 };
 
 struct AttnArgs;
@@ -166,15 +160,23 @@ struct ResNormCfg {
   float* part;
 };
 struct XentCfg {
-  int max_tokens, V, grad, piece;
-  int* count;              // how many tokens have a target
+  int max_tokens, V, grad;
+  int pairs;               // pairs of CTAs of a launch
+  int terms, pack;         // bf16 terms of an operand; 1: X and W are packed
+  int pitch, acc_pitch;    // columns of a packed row, of a row of dxacc
+  int rows_alloc;          // max_tokens, to a multiple of a tile's rows
+  int piece, pieces;       // ids of a piece of the vocabulary, how many of them
+  int* count;              // how many tokens have a target; 1: all, and X itself serves
   int* rows;               // [max_tokens] these tokens
   int* tgt;                // [max_tokens] their targets
+  int* inv;                // [max_tokens] a token's place among them, or -1
   float* hit;              // [max_tokens] their targets' logits
-  float2* part;            // [runs][max_tokens] maximum and sum over a run of the vocabulary
+  float2* part;            // [parts][max_tokens] maximum and sum over a part of the vocabulary
   float2* stat;            // [max_tokens] lse and upstream gradient
-  float* d;                // [max_tokens][piece]
-  float* dxacc;            // [max_tokens][D]
+  void* xp;                // [rows_alloc][terms][pitch] their rows of X
+  void* wp;                // [V][terms][pitch]
+  void* d;                 // [1 or 2 pieces][rows_alloc][terms][piece]
+  float* dxacc;            // [rows_alloc][acc_pitch]
 };
 struct AttnCfg {
   int max_tokens, max_seqs, Hq, Hkv, dh, causal;
@@ -504,9 +506,11 @@ cudaError_t setup_resnorm(int D, int dtype, int post);
 cudaError_t launch_resnorm_forward(const ResNormArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_resnorm_backward(const ResNormArgs& a, int dtype, cudaStream_t st);
 
-// Cross entropy over a vocabulary (xent.cu).
-int xent_piece(int max_tokens, int V);
-size_t xent_part_count(int max_tokens, int V);
+// Cross entropy over a vocabulary (xent.cu).  xent_shape: the workspace's shapes,
+// for max_tokens and V and that many pairs of CTAs.
+cudaError_t setup_xent_mma(int dtype, int sms, int* pairs);
+void xent_shape(XentCfg* c, int D, int dtype, int pairs);
+size_t xent_part_count(const XentCfg& c);
 cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens, bool back);
 
 // Device and host memory of a plan's operator (block_api.cu).

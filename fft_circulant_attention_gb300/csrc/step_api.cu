@@ -276,13 +276,20 @@ int cat_plan_create_xent(cat_plan_t* out, int max_tokens, int V, int D, int dtyp
   c.max_tokens = max_tokens;
   c.V = V;
   c.grad = grad;
-  c.piece = cat::xent_piece(max_tokens, V);
-  const size_t n = (size_t)max_tokens;
+  int pairs = 0;
+  if (cat::setup_xent_mma(dtype, p->sms, &pairs) != cudaSuccess) return fail(p, CAT_ERR_CUDA);
+  cat::xent_shape(&c, D, dtype, pairs);
+  const size_t n = (size_t)max_tokens, rows = (size_t)c.rows_alloc;
+  const size_t row = (size_t)c.terms * c.pitch * 2;        // bytes of a packed row
+  auto bytes = [&](void** q, size_t count) { return alloc(p, (unsigned char**)q, count); };
   bool ok = alloc_status(p) && alloc(p, &c.count, 4) && alloc(p, &c.rows, n) &&
             alloc(p, &c.tgt, n) && alloc(p, &c.hit, n) &&
-            alloc(p, &c.part, cat::xent_part_count(max_tokens, V));
+            alloc(p, &c.part, cat::xent_part_count(c)) && bytes(&c.xp, rows * row);
+  if (ok && c.pack) ok = bytes(&c.wp, (size_t)V * row);
   if (ok && grad)
-    ok = alloc(p, &c.stat, n) && alloc(p, &c.d, n * c.piece) && alloc(p, &c.dxacc, n * D);
+    ok = alloc(p, &c.stat, n) && alloc(p, &c.inv, n) &&
+         bytes(&c.d, rows * c.piece * 2 * c.terms * (c.pieces > 1 ? 2 : 1)) &&
+         alloc(p, &c.dxacc, rows * c.acc_pitch);
   if (!ok) return fail(p, CAT_ERR_ALLOC);
   std::snprintf(p->desc, sizeof(p->desc), "op=xent max_tokens=%d V=%d D=%d grad=%d piece=%d "
                 "workspace=%zu", max_tokens, V, D, grad, c.piece, p->workspace_bytes);

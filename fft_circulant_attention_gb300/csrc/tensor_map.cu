@@ -8,6 +8,7 @@
 
 #include "bulk.cuh"
 #include "tc.cuh"
+#include "xent_mma.cuh"
 
 namespace cat {
 
@@ -67,6 +68,24 @@ bool encode_map_heads_sw128(CUtensorMap* map, const void* base, unsigned long lo
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gd, gs,
                         bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_map_planes_sw128(CUtensorMap* map, const void* base, bool f32, unsigned long long width,
+                             unsigned long long planes, unsigned long long rows,
+                             unsigned long long row_bytes, unsigned int box_rows) {
+  std::call_once(g_once, find_encode);
+  if (!g_encode) return false;
+  const unsigned int es1 = f32 ? 4 : 2;
+  cuuint64_t gd[3] = {width, planes, rows};
+  cuuint64_t gs[2] = {planes > 1 ? width * es1 : row_bytes, row_bytes};
+  cuuint32_t bx[3] = {128 / es1, 1, box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(
+      map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -6,340 +6,357 @@
 // exponentials of each row, the backward makes them again, a piece of the
 // vocabulary at a time.  Tokens without a target (a negative one) take no part:
 // the others' rows are worked on as one dense list.
+#include <cuda_bf16.h>
+
 #include "cat_internal.h"
 #include "elem.cuh"
 #include "ids.cuh"
+#include "xent_mma.cuh"
 #include "../../include/cat.h"
 
 namespace cat {
 
 namespace {
 
-constexpr int kPrep = 1024;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The list of the tokens that have a target (rows, tgt; count: how many), with
-// their statistics for the backward (stat: lse·log2(e) and the upstream
-// gradient).  A CTA takes kPrep tokens and counts those before them itself.
-// loss, lse: forward, zero for the tokens without a target.
-__global__ void __launch_bounds__(kPrep)
-xent_prepare_kernel(Ids targets, int tokens, int V, int* __restrict__ rows, int* __restrict__ tgt,
-                    int* __restrict__ count, float* loss, float* lse_out, const float* lse,
-                    const float* dloss, int dloss_each, float2* __restrict__ stat,
-                    unsigned int* status) {
-  __shared__ int red[kPrep / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * kPrep, t = t0 + threadIdx.x;
-  int before = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < t0; i += kPrep) before += id_at(targets, i, V) >= 0;
-  const int id = t < tokens ? id_at(targets, t, V) : -1;
-  if (id == -2) report(status, 0x801);
-  const unsigned held = __ballot_sync(0xffffffffu, id >= 0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if (lane == 0) red[warp] = before;
-  __syncthreads();
-  int base = 0;
-#pragma unroll
-  for (int w = 0; w < kPrep / 32; ++w) base += red[w];
-  __syncthreads();
-  if (lane == 0) red[warp] = __popc(held);
-  __syncthreads();
-  int mine = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kPrep / 32; ++w) {
-    if (w < warp) mine += red[w];
-    all += red[w];
-  }
-  const int pos = base + mine + __popc(held & ((1u << lane) - 1));
-  if (id >= 0) {
-    rows[pos] = t;
-    tgt[pos] = id;
-    if (stat) stat[pos] = make_float2(__ldg(lse + t) * kLog2e, __ldg(dloss + (dloss_each ? t : 0)));
-  } else if (t < tokens && loss) {
-    loss[t] = 0.f;
-    lse_out[t] = 0.f;
-  }
-  if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) *count = base + all;
-}
+// What the call's first kernel prepares.
+struct Prep {
+  Ids targets;
+  int tokens, per, V, D, pitch, terms;   // per: tokens of a CTA; pitch: columns of a packed row
+  int direct;                            // 1: X itself serves where every token has a target
+  int list_ctas;                         // CTAs of the list; the others pack W
+  const void* x; const void* w;
+  void* xp; void* wp;                    // packed rows: [row][term][pitch] bf16
+  int* rows; int* tgt; int* inv; int* count;
+  float* loss; float* lse;               // forward: 0 for the tokens without a target
+  const float* lse_in; const float* dloss;
+  int dloss_each;
+  float2* stat;
+  unsigned int* status;
+};
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
-
-// One 64 x 64 tile of A·Bᵀ: 256 threads, 4 x 4 values each (rows 4·ty .., columns
-// 4·tx ..).  A(m, k), B(n, k): elements, zero outside; *_mn: their rows run along
-// m (n) in memory.
-template <bool A_MN, bool B_MN, typename FA, typename FB>
-__device__ __forceinline__ void tile_product(FA A, FB B, int K, float (&c)[4][4],
-                                             float (*sa)[kTile + 4], float (*sb)[kTile + 4]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      const int m = A_MN ? i % kTile : i / kStep, k = A_MN ? i / kTile : i % kStep;
-      sa[k][m] = A(m, k0 + k);
-    }
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      const int n = B_MN ? i % kTile : i / kStep, k = B_MN ? i / kTile : i % kStep;
-      sb[k][n] = B(n, k0 + k);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      float x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = sa[k][4 * ty + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = sb[k][4 * tx + j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(x[i], y[j], c[i][j]);
-    }
-    __syncthreads();
-  }
-}
-
-__device__ __forceinline__ float half_warp_max(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float half_warp_sum(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// part[run][pos]: maximum and sum of exponentials of 64·run_tiles logits.
+// `terms` bf16 terms of 8 columns from c on of a row (zeros from D on).
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-xent_lse_kernel(XentArgs a, int run_tiles) {
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const T* X = static_cast<const T*>(a.x);
-  const T* W = static_cast<const T*>(a.w);
-  const int n = __ldg(a.count), m0 = blockIdx.x * kTile;
-  if (m0 >= n) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float mx[4], sum[4];
+__device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, int D, int pitch,
+                                      int terms) {
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    mx[i] = -INFINITY;
-    sum[i] = 0.f;
-  }
-  for (int r = 0; r < run_tiles; ++r) {
-    const int v0 = (blockIdx.y * run_tiles + r) * kTile;
-    if (v0 >= a.V) break;
-    float c[4][4];
-    tile_product<false, false>(
-        [&](int m, int k) {
-          return m0 + m < n && k < a.D ? ld_elem(X + (size_t)a.rows[m0 + m] * a.D + k) : 0.f;
-        },
-        [&](int v, int k) {
-          return v0 + v < a.V && k < a.D ? ld_elem(W + (size_t)(v0 + v) * a.D + k) : 0.f;
-        },
-        a.D, c, sa, sb);
+  for (int e = 0; e < 8; ++e) v[e] = src && c + e < D ? ld_elem(src + c + e) : 0.f;
+  for (int t = 0; t < terms; ++t) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4*>(dst + (size_t)t * pitch + c) = *reinterpret_cast<uint4*>(h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int pos = m0 + 4 * ty + i;
-      const int t = pos < n ? a.tgt[pos] : -1;
-      float top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = v0 + 4 * tx + j;
-        if (v >= a.V) c[i][j] = -INFINITY;
-        if (v == t) a.hit[pos] = c[i][j];
-        top = fmaxf(top, c[i][j]);
-      }
-      top = fmaxf(mx[i], half_warp_max(top));
-      const float sh = top == -INFINITY ? 0.f : top;
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s += exp2f((c[i][j] - sh) * kLog2e);
-      sum[i] = sum[i] * exp2f((mx[i] - sh) * kLog2e) + half_warp_sum(s);
-      mx[i] = top;
+      v[2 * i] -= __bfloat162float(h[i].x);
+      v[2 * i + 1] -= __bfloat162float(h[i].y);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pos = m0 + 4 * ty + i;
-    if (tx == 0 && pos < n) a.part[(size_t)blockIdx.y * a.ld + pos] = make_float2(mx[i], sum[i]);
   }
 }
 
-__global__ void __launch_bounds__(256)
-xent_finish_kernel(XentArgs a, int nparts) {
-  const int pos = blockIdx.x * 256 + threadIdx.x;
-  if (pos >= __ldg(a.count)) return;
+// The list of the tokens that have a target (rows, tgt; inv: a token's place in
+// it; count: its length and whether X itself serves as its rows), their
+// statistics for the backward (stat: lse·log2(e) and the upstream gradient) and
+// their rows of X, dense and, for fp32, as bf16 terms; rows of zeros up to a
+// multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
+// other CTAs pack W.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
+  const int vecs = p.pitch / 8;
+  if ((int)blockIdx.x >= p.list_ctas) {
+    const long long n = (long long)p.V * vecs;
+    const long long step = (long long)(gridDim.x - p.list_ctas) * kThreads;
+    for (long long i = (long long)(blockIdx.x - p.list_ctas) * kThreads + threadIdx.x; i < n;
+         i += step) {
+      const long long v = i / vecs;
+      pack8(static_cast<const T*>(p.w) + v * p.D,
+            static_cast<__nv_bfloat16*>(p.wp) + v * p.terms * p.pitch, (int)(i - v * vecs) * 8,
+            p.D, p.pitch, p.terms);
+    }
+    return;
+  }
+  __shared__ int red[2][kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t0 = blockIdx.x * p.per, t1 = min(p.tokens, t0 + p.per);
+  int before = 0, all = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.tokens; i += kThreads) {
+    const int held = id_at(p.targets, i, p.V) >= 0;
+    all += held;
+    before += i < t0 ? held : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    red[0][warp] = before;
+    red[1][warp] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    before += red[0][w];
+    all += red[1][w];
+  }
+  const int direct = p.direct && all == p.tokens;
+  int place = before;
+  for (int b = t0; b < t1; b += kThreads) {
+    const int t = b + threadIdx.x;
+    const int id = t < t1 ? id_at(p.targets, t, p.V) : -1;
+    if (id == -2) report(p.status, 0x801);
+    const unsigned held = __ballot_sync(0xffffffffu, id >= 0);
+    __syncthreads();
+    if (lane == 0) red[0][warp] = __popc(held);
+    __syncthreads();
+    int mine = place;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) mine += red[0][w];
+      place += red[0][w];
+    }
+    const int pos = mine + __popc(held & ((1u << lane) - 1));
+    if (id >= 0) {
+      p.rows[pos] = t;
+      p.tgt[pos] = id;
+      if (p.stat)
+        p.stat[pos] = make_float2(__ldg(p.lse_in + t) * kLog2e,
+                                  __ldg(p.dloss + (p.dloss_each ? t : 0)));
+    } else if (t < t1 && p.loss) {
+      p.loss[t] = 0.f;
+      p.lse[t] = 0.f;
+    }
+    if (p.inv && t < t1) p.inv[t] = id >= 0 ? pos : -1;
+  }
+  if (threadIdx.x == 0 && blockIdx.x == p.list_ctas - 1) {
+    p.count[0] = all;
+    p.count[1] = direct;
+  }
+  if (direct) return;
+  __syncthreads();
+  // This CTA's rows of the list, the last CTA those behind it too.
+  const bool tail = (int)blockIdx.x == p.list_ctas - 1;
+  const int end = tail ? (all + 255) / 256 * 256 : place;
+  const int n = (end - before) * vecs;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int r = i / vecs, pos = before + r;
+    const T* src = pos < all ? static_cast<const T*>(p.x) + (size_t)p.rows[pos] * p.D : nullptr;
+    pack8(src, static_cast<__nv_bfloat16*>(p.xp) + (size_t)pos * p.terms * p.pitch,
+          (i - r * vecs) * 8, p.D, p.pitch, p.terms);
+  }
+}
+
+// loss and lse from the parts' maxima (times log2(e)) and sums.
+__global__ void __launch_bounds__(kThreads)
+xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, const int* rows,
+                   const float* hit, float* __restrict__ loss, float* __restrict__ lse) {
+  const int pos = blockIdx.x * kThreads + threadIdx.x;
+  pdl_wait();
+  if (pos >= __ldcg(count)) return;
   float top = -INFINITY, s = 0.f;
-  for (int i = 0; i < nparts; ++i) top = fmaxf(top, a.part[(size_t)i * a.ld + pos].x);
-  const float sh = top == -INFINITY ? 0.f : top;
+#pragma unroll 8
   for (int i = 0; i < nparts; ++i) {
-    const float2 q = a.part[(size_t)i * a.ld + pos];
-    s += q.y * exp2f((q.x - sh) * kLog2e);
+    const float2 q = __ldcg(part + (size_t)i * ld + pos);
+    const float m = fmaxf(top, q.x), sh = m == -INFINITY ? 0.f : m;
+    s = s * exp2f(top - sh) + q.y * exp2f(q.x - sh);
+    top = m;
   }
-  const float z = top + logf(s);
-  const int t = a.rows[pos];
-  a.lse[t] = z;
-  a.loss[t] = z - a.hit[pos];
+  const float z = (top + log2f(s)) * kLn2;
+  const int t = __ldcg(rows + pos);
+  lse[t] = z;
+  loss[t] = z - __ldcg(hit + pos);
 }
 
-// d of a piece of the vocabulary: fp32 [pos][piece].
+// dX's rows from the list's, zeros for the tokens without a target.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-xent_dlog_kernel(XentArgs a, float* __restrict__ d, int v0p, int width) {
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const T* X = static_cast<const T*>(a.x);
-  const T* W = static_cast<const T*>(a.w);
-  const int n = __ldg(a.count), m0 = blockIdx.x * kTile, v0 = v0p + blockIdx.y * kTile;
-  if (m0 >= n) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float c[4][4];
-  tile_product<false, false>(
-      [&](int m, int k) {
-        return m0 + m < n && k < a.D ? ld_elem(X + (size_t)a.rows[m0 + m] * a.D + k) : 0.f;
-      },
-      [&](int v, int k) {
-        return v0 + v < a.V && k < a.D ? ld_elem(W + (size_t)(v0 + v) * a.D + k) : 0.f;
-      },
-      a.D, c, sa, sb);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pos = m0 + 4 * ty + i;
-    if (pos >= n) continue;
-    const int t = a.tgt[pos];
-    const float2 st = a.stat[pos];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = v0 + 4 * tx + j;
-      float p = 0.f;
-      if (v < a.V) p = st.y * (exp2f(c[i][j] * kLog2e - st.x) - (v == t ? 1.f : 0.f));
-      d[(size_t)pos * width + v - v0p] = p;
-    }
+xent_dx_kernel(const float* acc, int pitch, const int* inv, T* __restrict__ dX, int tokens, int D,
+               int per) {
+  pdl_wait();
+  const int row0 = blockIdx.x * per, n = min(per, tokens - row0) * D;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int r = i / D, c = i - r * D, pos = __ldcg(inv + row0 + r);
+    st_elem(dX + (size_t)(row0 + r) * D + c,
+            pos >= 0 ? __ldcg(acc + (size_t)pos * pitch + c) : 0.f);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-xent_dx_kernel(XentArgs a, const float* __restrict__ d, float* __restrict__ acc, int v0p,
-               int width, int first, int last) {
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const T* W = static_cast<const T*>(a.w);
-  const int n = __ldg(a.count), m0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
-  if (m0 >= n) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float c[4][4];
-  tile_product<false, true>(
-      [&](int m, int k) { return m0 + m < n ? d[(size_t)(m0 + m) * width + k] : 0.f; },
-      [&](int j, int k) {
-        return n0 + j < a.D && v0p + k < a.V ? ld_elem(W + (size_t)(v0p + k) * a.D + n0 + j) : 0.f;
-      },
-      width, c, sa, sb);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pos = m0 + 4 * ty + i;
-    if (pos >= n) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int q = n0 + 4 * tx + j;
-      if (q >= a.D) continue;
-      float* to = acc + (size_t)pos * a.D + q;
-      const float v = first ? c[i][j] : *to + c[i][j];
-      if (last)
-        st_elem(static_cast<T*>(a.dx) + (size_t)a.rows[pos] * a.D + q, v);
-      else
-        *to = v;
-    }
-  }
-}
+int tiles(long long n, int m) { return (int)((n + m - 1) / m); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-xent_dw_kernel(XentArgs a, const float* __restrict__ d, int v0p, int width) {
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const T* X = static_cast<const T*>(a.x);
-  const int n = __ldg(a.count), m0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float c[4][4];
-  tile_product<true, true>(
-      [&](int m, int k) { return k < n ? d[(size_t)k * width + m0 + m] : 0.f; },
-      [&](int j, int k) {
-        return n0 + j < a.D && k < n ? ld_elem(X + (size_t)a.rows[k] * a.D + n0 + j) : 0.f;
-      },
-      n, c, sa, sb);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int v = v0p + m0 + 4 * ty + i;
-    if (v >= a.V) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int q = n0 + 4 * tx + j;
-      if (q < a.D) st_elem(static_cast<T*>(a.dw) + (size_t)v * a.D + q, c[i][j]);
-    }
-  }
-}
-
-template <typename T>
-cudaError_t forward(const XentCfg& c, const XentArgs& a, int T_, cudaStream_t st) {
-  const int tiles = (c.V + kTile - 1) / kTile, run = 16, runs = (tiles + run - 1) / run;
-  xent_lse_kernel<T><<<dim3((T_ + kTile - 1) / kTile, runs), kThreads, 0, st>>>(a, run);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  xent_finish_kernel<<<(T_ + 255) / 256, 256, 0, st>>>(a, runs);
-  return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t backward(const XentCfg& c, const XentArgs& a, int T_, cudaStream_t st) {
-  const int mt = (T_ + kTile - 1) / kTile, nt = (a.D + kTile - 1) / kTile;
-  if (a.dx) {
-    const cudaError_t e = cudaMemsetAsync(a.dx, 0, (size_t)T_ * a.D * sizeof(T), st);
-    if (e != cudaSuccess) return e;
-  }
-  for (int v0 = 0; v0 < c.V; v0 += c.piece) {
-    const int last = v0 + c.piece >= c.V;
-    xent_dlog_kernel<T><<<dim3(mt, c.piece / kTile), kThreads, 0, st>>>(a, c.d, v0, c.piece);
-    if (a.dx)
-      xent_dx_kernel<T><<<dim3(mt, nt), kThreads, 0, st>>>(a, c.d, c.dxacc, v0, c.piece, v0 == 0,
-                                                           last);
-    if (a.dw)
-      xent_dw_kernel<T><<<dim3(c.piece / kTile, nt), kThreads, 0, st>>>(a, c.d, v0, c.piece);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+// Tiles of the vocabulary in a forward part: as many as leave each pair of CTAs
+// eight parts, at most eight.
+int run_length(int V, int tokens, int pairs) {
+  const long long all = (long long)tiles(V, kXtN) * tiles(tokens, kXtM);
+  const long long r = all / (8ll * pairs);
+  return r < 1 ? 1 : r > 8 ? 8 : (int)r;
 }
 
 }  // namespace
 
-int xent_piece(int max_tokens, int V) {
-  const int most = (V + kTile - 1) / kTile * kTile;
-  return most < 4096 ? most : 4096;
+// Shapes of a plan's workspace.
+void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
+  c->pairs = pairs;
+  c->terms = dtype == CAT_F32 ? 3 : 1;
+  c->pitch = (D + 7) / 8 * 8;
+  c->acc_pitch = (D + 3) / 4 * 4;
+  c->pack = dtype == CAT_F32 || D % 8 != 0;
+  c->rows_alloc = tiles(c->max_tokens, kXtM) * kXtM;
+  if (c->rows_alloc == 0) c->rows_alloc = kXtM;
+  // A piece of the vocabulary: dW's tiles (of the piece by D) are the longest of a
+  // launch, so that their number is a multiple of the pairs, or just below; more
+  // of the vocabulary at once where there are few tokens, and less where two
+  // pieces' d would take more than 2 GB.
+  const int nt = tiles(D, kXtN), vt = tiles(c->V, kXtN);
+  long long w = 16384 / c->rows_alloc;
+  if (w < 1) w = 1;
+  long long pt = w * pairs / nt;
+  const long long tile_bytes = (long long)c->rows_alloc * kXtN * 2 * c->terms;
+  const long long most = (2ll << 30) / (2 * tile_bytes);
+  if (pt > most) pt = most;
+  if (pt < 1) pt = 1;
+  if (pt > vt) pt = vt;
+  c->piece = (int)pt * kXtN;
+  c->pieces = tiles(c->V, c->piece);
 }
-size_t xent_part_count(int max_tokens, int V) {
-  return (size_t)((V + 16 * kTile - 1) / (16 * kTile)) * max_tokens;
+size_t xent_part_count(const XentCfg& c) {
+  // (The longest list of parts is that of the shortest runs.)
+  size_t most = 0;
+  for (long long t = kXtM;; t *= 2) {
+    const long long tokens = t < c.max_tokens ? t : c.max_tokens;
+    const int run = run_length(c.V, (int)tokens, c.pairs);
+    const size_t n = 2 * (size_t)tiles(tiles(c.V, kXtN), run);
+    if (n > most) most = n;
+    if (t >= c.max_tokens) break;
+  }
+  return most * c.max_tokens;
 }
+
+namespace {
+
+template <typename T>
+cudaError_t prepare(const cat_plan_s* p, const XentArgs& a, Ids targets, int tokens, bool back) {
+  const XentCfg& c = p->xe;
+  Prep q = {};
+  q.targets = targets;
+  q.tokens = tokens;
+  q.per = tokens > 2048 * kThreads / 2 ? (tokens + 2047) / 2048 : kThreads / 2;
+  q.V = c.V;
+  q.D = p->D;
+  q.pitch = c.pitch;
+  q.terms = c.terms;
+  q.direct = !c.pack;
+  q.list_ctas = tiles(tokens, q.per);
+  q.x = a.x;
+  q.w = a.w;
+  q.xp = c.xp;
+  q.wp = c.wp;
+  q.rows = c.rows;
+  q.tgt = c.tgt;
+  q.inv = back ? c.inv : nullptr;
+  q.count = c.count;
+  q.loss = back ? nullptr : a.loss;
+  q.lse = back ? nullptr : a.lse;
+  q.lse_in = a.lse;
+  q.dloss = a.dloss;
+  q.dloss_each = a.dloss_each;
+  q.stat = back ? c.stat : nullptr;
+  q.status = p->status;
+  const long long wv = c.pack ? (long long)c.V * (c.pitch / 8) : 0;
+  const long long need = (wv + 2 * kThreads - 1) / (2 * kThreads), most = 16ll * p->sms;
+  const int wctas = (int)(need < most ? need : most);
+  xent_prepare_kernel<T><<<q.list_ctas + wctas, kThreads, 0, p->stream>>>(q);
+  return cudaGetLastError();
+}
+
+bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, XentMaps* m) {
+  const XentCfg& c = p->xe;
+  const int D = p->D;
+  const unsigned long long rb = (unsigned long long)c.terms * c.pitch * 2;
+  bool ok = encode_map_planes_sw128(&m->xp, c.xp, false, c.pitch, c.terms, c.rows_alloc, rb, 64);
+  if (c.pack) {
+    m->x = m->xp;
+    ok = ok && encode_map_planes_sw128(&m->w, c.wp, false, c.pitch, c.terms, c.V, rb, 64);
+  } else {
+    ok = ok && encode_map_planes_sw128(&m->x, a.x, false, D, 1, tokens, rb, 64) &&
+         encode_map_planes_sw128(&m->w, a.w, false, D, 1, c.V, rb, 64);
+  }
+  if (!ok || !back) return ok;
+  const unsigned long long db = (unsigned long long)c.terms * c.piece * 2;
+  const unsigned long long drows = (unsigned long long)c.rows_alloc * (c.pieces > 1 ? 2 : 1);
+  ok = encode_map_planes_sw128(&m->d, c.d, false, c.piece, c.terms, drows, db, 64) &&
+       encode_map_planes_sw128(&m->ds, c.d, false, c.piece, c.terms, drows, db, 32) &&
+       encode_map_planes_sw128(&m->acc, c.dxacc, true, D, 1, c.rows_alloc,
+                               (unsigned long long)c.acc_pitch * 4, 32);
+  const bool f32 = p->dtype == CAT_F32;
+  if (ok && a.dw && D % (f32 ? 4 : 8) == 0)
+    ok = encode_map_planes_sw128(&m->dw, a.dw, f32, D, 1, c.V,
+                                 (unsigned long long)D * (f32 ? 4 : 2), 32);
+  return ok;
+}
+
+template <typename T>
+cudaError_t finish_dx(const cat_plan_s* p, const XentArgs& a, int tokens) {
+  const int per = p->D >= 2048 ? 1 : 2048 / p->D;
+  return launch_dependent(xent_dx_kernel<T>, dim3(tiles(tokens, per)), dim3(kThreads), 0,
+                          p->stream, (const float*)p->xe.dxacc, p->xe.acc_pitch,
+                          (const int*)p->xe.inv, static_cast<T*>(a.dx), tokens, p->D, per);
+}
+
+}  // namespace
 
 cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens, bool back) {
   const XentCfg& c = p->xe;
   cudaStream_t st = p->stream;
-  a.V = c.V;
-  a.D = p->D;
-  a.ld = c.max_tokens;
-  a.count = c.count; a.rows = c.rows; a.tgt = c.tgt; a.stat = c.stat; a.hit = c.hit;
-  a.part = c.part;
-  xent_prepare_kernel<<<(tokens + kPrep - 1) / kPrep, kPrep, 0, st>>>(
-      targets, tokens, c.V, c.rows, c.tgt, c.count, back ? nullptr : a.loss,
-      back ? nullptr : a.lse, a.lse, a.dloss, a.dloss_each, back ? c.stat : nullptr, p->status);
-  const cudaError_t e = cudaGetLastError();
+  const bool f32 = p->dtype == CAT_F32;
+  cudaError_t e = f32 ? prepare<float>(p, a, targets, tokens, back)
+                      : prepare<__nv_bfloat16>(p, a, targets, tokens, back);
   if (e != cudaSuccess) return e;
-  if (p->dtype == CAT_BF16)
-    return back ? backward<__nv_bfloat16>(c, a, tokens, st)
-                : forward<__nv_bfloat16>(c, a, tokens, st);
-  return back ? backward<float>(c, a, tokens, st) : forward<float>(c, a, tokens, st);
+  XentMaps maps;
+  if (!make_maps(p, a, tokens, back, &maps)) return cudaErrorInvalidValue;
+  XentMma k = {};
+  k.V = c.V;
+  k.D = p->D;
+  k.rows = c.rows_alloc;
+  k.piece = c.piece;
+  k.ld = c.max_tokens;
+  k.count = c.count;
+  k.tgt = c.tgt;
+  k.rows_of = c.rows;
+  k.x = a.x;
+  k.w = a.w;
+  k.stat = c.stat;
+  k.hit = c.hit;
+  k.part = c.part;
+  k.dw = a.dw;
+  k.dw_tma = p->D % (f32 ? 4 : 8) == 0;
+  k.status = p->status;
+  k.dw_piece = k.dx_piece = k.d_piece = -1;
+  if (!back) {
+    k.lse = 1;
+    k.run = run_length(c.V, tokens, c.pairs);
+    e = launch_xent_mma(maps, k, p->dtype, c.pairs, st);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, kThreads)), dim3(kThreads), 0,
+                            st, (const float2*)c.part, 2 * tiles(tiles(c.V, kXtN), k.run),
+                            c.max_tokens, (const int*)c.count, (const int*)c.rows,
+                            (const float*)c.hit, a.loss, a.lse);
+  }
+  // Piece i's products beside d of piece i + 1.
+  for (int i = -1; i < c.pieces; ++i) {
+    k.dw_piece = i >= 0 && a.dw ? i : -1;
+    k.dx_piece = i >= 0 && a.dx ? i : -1;
+    k.d_piece = i + 1 < c.pieces ? i + 1 : -1;
+    k.first = i == 0;
+    e = launch_xent_mma(maps, k, p->dtype, c.pairs, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.dx) return cudaSuccess;
+  return f32 ? finish_dx<float>(p, a, tokens) : finish_dx<__nv_bfloat16>(p, a, tokens);
 }
 
 }  // namespace cat

@@ -1,0 +1,738 @@
+// The products of the cross entropy on the tensor cores (tcgen05), with what
+// follows them fused in:
+//   LSE  X·Wᵀ, a run of the vocabulary at a time -> maximum and sum of
+//        exponentials of each row, and the target's logit;
+//   D    X·Wᵀ again, a piece of the vocabulary -> d = g·(exp(l - lse) - [v = t]);
+//   DX   d·W over the piece, added to dX in fp32;
+//   DW   dᵀ·X over all rows of the list -> the piece's rows of dW.
+//
+// All four are tiles of 256 x 256 by one pair of CTAs (cta_group::2): each CTA
+// holds 128 rows of A and half of B in shared memory, the pair's tensor cores
+// read both halves, so that a stage of K = 64 needs 32 KB an SM instead of the
+// 48 KB of a tile of one CTA.  What is K in one product is a row in another: the
+// boxes in shared memory are the same (64 columns by 64 rows, 128-byte swizzle),
+// the matrix descriptors say which of the two is K.
+//
+// fp32 operands are three bf16 terms each, of whose products the six that matter
+// are taken, smallest first; the accumulator, which cuts instead of rounding, is
+// read out every two stages of K and added up in registers.
+//
+// Roles of a CTA: warp 0 issues copies, warp 1 (of the pair's first CTA) the
+// MMAs, warp 2 holds the tensor memory (two accumulators of 256 columns), warps
+// 4 to 11 read a finished accumulator, four of them its first and four its second
+// half of columns, while the next tile's products run.  The pairs are persistent;
+// which tiles a pair works on is computed, not handed out: a launch's kinds of
+// tiles differ in length, and each pair gets about the same number of K stages.
+// Every wait is bounded; a lost one ends its role's loop and is reported.
+#include <cuda_bf16.h>
+
+#include "elem.cuh"
+#include "tc.cuh"
+#include "xent_mma.cuh"
+#include "../../include/cat.h"
+
+namespace cat {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kStages = 6;
+constexpr int kBox = 64 * 128;                     // bytes of a box
+constexpr int kOperand = 2 * kBox;                 // A's or B's share of a stage
+constexpr int kStage = 2 * kOperand;
+constexpr int kStaging = 32 * 128;                 // a warp's box of results
+constexpr int kAccCols = 256;
+constexpr int kChunk = 2;                          // K stages between read-outs (fp32)
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStaging + 512;
+constexpr float kLog2e = 1.4426950408889634f;
+enum { LSE = 0, DLOG = 1, DX = 2, DW = 3 };
+
+// ---- pairs of CTAs ----
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// Address of the pair's first CTA's copy of a shared-memory variable.
+__device__ __forceinline__ uint32_t of_first(uint32_t a) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ void pair_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+               : "memory");
+}
+// A box into this CTA's shared memory; its bytes are reported to `bar`, which
+// may be the pair's first CTA's.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                          int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive at both CTAs' `bar` once the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((unsigned short)3)
+      : "memory");
+}
+
+// ---- results ----
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                          int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void add_box(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                        int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
+      "[%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void stores_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                            uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// One tile of a launch.
+struct Tile {
+  int kind, m0, n0, N;                             // rows and columns of the result
+  int steps;                                       // K stages
+  int v0, drow;                                    // its piece's first id, rows of d
+  int last;                                        // LSE: the run's last tile
+};
+
+// Which tiles this pair works on; the same in all of its threads.
+struct Plan {
+  int mt, nt, vt;                                  // tiles of rows, of D, of a piece (run)
+  int dk, tk, pk;                                  // K stages of D, of the list, of a piece
+  int w1, x0, x1, l0, l1;                          // DW (every pairs-th), DX, D tiles
+  int pairs, pair;
+};
+
+__device__ __forceinline__ int pieces_tiles(const XentMma& a, int piece) {
+  const int left = a.V - piece * a.piece;
+  return (min(left, a.piece) + kXtN - 1) / kXtN;
+}
+
+__device__ void make_plan(const XentMma& a, int n, Plan* p) {
+  p->pairs = gridDim.x >> 1;
+  p->pair = blockIdx.x >> 1;
+  p->mt = (n + kXtM - 1) / kXtM;
+  p->nt = (a.D + kXtN - 1) / kXtN;
+  p->dk = (a.D + kXtK - 1) / kXtK;
+  p->tk = (n + kXtK - 1) / kXtK;
+  p->w1 = p->x0 = p->x1 = p->l0 = p->l1 = 0;
+  p->vt = p->pk = 0;
+  if (a.lse) {
+    p->vt = ((a.V + kXtN - 1) / kXtN + a.run - 1) / a.run;
+    return;
+  }
+  // Tiles and their lengths in K stages; a tile of D ends in stores that no
+  // product of its own hides.
+  int nw = 0, nx = 0, nl = 0, cx = 1;
+  if (a.dw_piece >= 0) nw = pieces_tiles(a, a.dw_piece) * p->nt;
+  if (a.dx_piece >= 0) {
+    cx = pieces_tiles(a, a.dx_piece) * (kXtN / kXtK);
+    nx = p->mt * p->nt;
+  }
+  p->pk = cx;
+  if (a.d_piece >= 0) {
+    p->vt = pieces_tiles(a, a.d_piece);
+    nl = p->mt * p->vt;
+  }
+  p->w1 = nw;
+  const float cw = (float)max(p->tk, 1), cl = (float)(p->dk + 2);
+  const float tx = (nw * cw + (float)nx * cx) / p->pairs;
+  const float tl = (nw * cw + (float)nx * cx + nl * cl) / p->pairs;
+  float ax = 0.f, al = 0.f;
+  int x1 = 0, l1 = 0;
+  for (int j = 0; j <= p->pair; ++j) {
+    float load = (nw / p->pairs + (j < nw % p->pairs)) * cw;
+    p->x0 = x1;
+    ax += fmaxf(0.f, tx - load) / cx;
+    x1 = j == p->pairs - 1 ? nx : min(nx, (int)(ax + 0.5f));
+    load += (float)(x1 - p->x0) * cx;
+    p->l0 = l1;
+    al += fmaxf(0.f, tl - load) / cl;
+    l1 = j == p->pairs - 1 ? nl : min(nl, (int)(al + 0.5f));
+  }
+  p->x1 = x1;
+  p->l1 = l1;
+}
+
+// This pair's `it`-th tile; false behind the last one.
+__device__ __forceinline__ bool tile_at(const XentMma& a, const Plan& p, int it, Tile* t) {
+  t->last = 1;
+  t->v0 = t->drow = 0;
+  int i;
+  if (a.lse) {
+    // `run` tiles of the vocabulary of one part, then the next part's.
+    const int part = p.pair + p.pairs * (it / a.run), r = it % a.run;
+    if (part >= p.mt * p.vt) return false;
+    t->kind = LSE;
+    t->m0 = part % p.mt * kXtM;
+    t->n0 = (part / p.mt * a.run + r) * kXtN;
+    t->N = kXtN;
+    t->steps = t->n0 < a.V ? p.dk : 0;             // (the last run may be shorter)
+    t->last = r == a.run - 1;
+    return true;
+  }
+  const int mine = p.w1 > p.pair ? (p.w1 - p.pair + p.pairs - 1) / p.pairs : 0;
+  if (it < mine) {
+    i = p.pair + it * p.pairs;
+    t->kind = DW;
+    t->v0 = a.dw_piece * a.piece;
+    t->drow = (a.dw_piece & 1) * a.rows;
+    t->m0 = i / p.nt * kXtM;
+    t->n0 = i % p.nt * kXtN;
+    t->steps = p.tk;
+  } else if ((i = p.x0 + it - mine) < p.x1) {
+    t->kind = DX;
+    t->v0 = a.dx_piece * a.piece;
+    t->drow = (a.dx_piece & 1) * a.rows;
+    t->m0 = i / p.nt * kXtM;
+    t->n0 = i % p.nt * kXtN;
+    t->steps = p.pk;
+  } else if ((i += p.l0 - p.x1) < p.l1) {
+    t->kind = DLOG;
+    t->v0 = a.d_piece * a.piece;
+    t->drow = (a.d_piece & 1) * a.rows;
+    t->m0 = i % p.mt * kXtM;
+    t->n0 = i / p.mt * kXtN;
+    t->steps = p.dk;
+    t->N = kXtN;
+    return true;
+  } else {
+    return false;
+  }
+  t->N = a.D - t->n0 > kXtN / 2 ? kXtN : kXtN / 2;
+  return true;
+}
+
+// The terms of the six products, smallest first.
+__device__ __forceinline__ int term_a(int q) { return (0x201100 >> (4 * (5 - q))) & 3; }
+__device__ __forceinline__ int term_b(int q) { return (0x021010 >> (4 * (5 - q))) & 3; }
+
+// The stages of a tile in the order of their use: f(first K stage, term of A,
+// term of B, how the accumulator goes on: 1 starts anew, 2 is read after it).
+template <bool F32, typename F>
+__device__ __forceinline__ void each_stage(int steps, F f) {
+  if (!F32) {
+    for (int k = 0; k < steps; ++k) f(k, 0, 0, (k == 0 ? 1 : 0) | (k == steps - 1 ? 2 : 0));
+  } else {
+    for (int k0 = 0; k0 < steps; k0 += kChunk) {
+      const int kn = min(kChunk, steps - k0);
+      for (int q = 0; q < 6; ++q)
+        for (int k = 0; k < kn; ++k)
+          f(k0 + k, term_a(q), term_b(q), (q + k == 0 ? 1 : 0) | (q == 5 && k == kn - 1 ? 2 : 0));
+    }
+  }
+}
+
+struct Smem {
+  uint32_t stages, staging;                        // addresses
+  uint32_t full, empty, tfull, tempty, done;       // barriers, 8 bytes apart
+};
+
+template <bool F32>
+__device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p, const Smem& s,
+                          int direct, uint32_t rank) {
+  const CUtensorMap* mx = direct ? &maps.x : &maps.xp;
+  uint32_t limit = kMaxPolls;
+  int g = 0;
+  Tile t;
+  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+    const int half = t.N >> 1, nb = half >> 6;     // B columns of this CTA, boxes of them
+    const uint32_t bytes = 2 * (kOperand + nb * kBox);
+    const int ar = t.m0 + (int)rank * 128, br = t.n0 + (int)rank * half;
+    each_stage<F32>(t.steps, [&](int k, int ta, int tb, int) {
+      const int st = g % kStages;
+      if (g >= kStages) mbar_poll(s.empty + 8 * st, (g / kStages - 1) & 1, limit);
+      if (!limit) return;
+      const uint32_t dst = s.stages + st * kStage, full = of_first(s.full + 8 * st);
+      if (rank == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                         s.full + 8 * st),
+                     "r"(bytes)
+                     : "memory");
+      const int kk = k * kXtK;
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t to = dst + b * kBox;
+        if (t.kind <= DLOG)
+          pair_load(to, mx, kk, ta, ar + 64 * b, full);
+        else if (t.kind == DX)
+          pair_load(to, &maps.d, kk, ta, t.drow + ar + 64 * b, full);
+        else
+          pair_load(to, &maps.d, ar + 64 * b, ta, t.drow + kk, full);
+      }
+      for (int b = 0; b < nb; ++b) {
+        const uint32_t to = dst + kOperand + b * kBox;
+        if (t.kind <= DLOG)
+          pair_load(to, &maps.w, kk, tb, t.v0 + br + 64 * b, full);
+        else if (t.kind == DX)
+          pair_load(to, &maps.w, br + 64 * b, tb, t.v0 + kk, full);
+        else
+          pair_load(to, mx, br + 64 * b, tb, kk, full);
+      }
+      ++g;
+    });
+  }
+  if (!limit) {
+    // Copies under way land before the pair's memory is given back.
+    report(a.status, 0x901);
+    if (rank == 0)
+      for (int q = g > kStages ? g - kStages : 0; q < g; ++q) {
+        uint32_t some = 1u << 16;
+        mbar_poll(s.full + 8 * (q % kStages), (q / kStages) & 1, some);
+      }
+  }
+}
+
+template <bool F32>
+__device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_t tmem) {
+  uint32_t limit = kMaxPolls;
+  int g = 0, u = 0;                                // stages; accumulators used
+  Tile t;
+  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+    // Which of the operands' two directions is K: MN-major where it is the rows.
+    const uint32_t idesc = idesc_bf16_f32(kXtM, t.N) | (t.kind == DW ? 1u << 15 : 0u) |
+                           (t.kind >= DX ? 1u << 16 : 0u);
+    each_stage<F32>(t.steps, [&](int, int, int, int flags) {
+      if (!limit) return;
+      const uint32_t b = u & 1;
+      if ((flags & 1) && u >= 2) mbar_poll(s.tempty + 8 * b, ((u >> 1) - 1) & 1, limit);
+      const int st = g % kStages;
+      mbar_poll(s.full + 8 * st, (g / kStages) & 1, limit);
+      if (!limit) return;
+      tc_fence_after();
+      const uint32_t sa = s.stages + st * kStage, sb = sa + kOperand;
+      const uint64_t base = ((uint64_t)1 << 46) | ((uint64_t)2 << 61) | ((uint64_t)(1024 >> 4) << 32);
+      const uint64_t mn = (uint64_t)(kBox >> 4) << 16, km = (uint64_t)1 << 16;
+      uint64_t da = base | (t.kind == DW ? mn : km) | ((sa & 0x3FFFFu) >> 4);
+      uint64_t db = base | (t.kind >= DX ? mn : km) | ((sb & 0x3FFFFu) >> 4);
+      const uint64_t sta = t.kind == DW ? 2048 >> 4 : 32 >> 4;
+      const uint64_t stb = t.kind >= DX ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+      for (int k = 0; k < kXtK / 16; ++k)
+        pair_mma(tmem + b * kAccCols, da + k * sta, db + k * stb, idesc, k > 0 || !(flags & 1));
+      pair_commit(s.empty + 8 * st);
+      ++g;
+      if (flags & 2) {
+        pair_commit(s.tfull + 8 * b);
+        ++u;
+      }
+    });
+  }
+  pair_commit(s.done);
+  if (!limit) report(a.status, 0x902);
+}
+
+// 64 values of a row as 128 bytes (bf16) of the warp's box.
+__device__ __forceinline__ void stage_bf16(uint32_t box, int lane, const float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    st_shared16(box + lane * 128 + ((j ^ (lane & 7)) << 4), pack2(v[8 * j], v[8 * j + 1]),
+                pack2(v[8 * j + 2], v[8 * j + 3]), pack2(v[8 * j + 4], v[8 * j + 5]),
+                pack2(v[8 * j + 6], v[8 * j + 7]));
+}
+// 32 values of a row as 128 bytes (fp32).
+__device__ __forceinline__ void stage_f32(uint32_t box, int lane, const float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    st_shared16(box + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
+                __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                __float_as_uint(v[4 * j + 3]));
+}
+
+// Logits that are not finite, again by their definition: an infinity is lost in
+// the products of its terms (0 times it, or a difference).  The warp's lanes
+// with such a value, one after another; x: the lane's row, w: the column's.
+__device__ __noinline__ float exact_logit(float v, const float* x, const float* w, int D,
+                                          bool live) {
+  const int lane = threadIdx.x & 31;
+  unsigned left = __ballot_sync(0xffffffffu, live && !(fabsf(v) < INFINITY));
+  while (left) {
+    const int src = __ffs(left) - 1;
+    left &= left - 1;
+    const float* row = reinterpret_cast<const float*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), src));
+    float sum = 0.f;
+    for (int k = lane; k < D; k += 32) sum = fmaf(__ldg(row + k), __ldg(w + k), sum);
+    sum = warp_sum(sum);
+    if (lane == src) v = sum;
+  }
+  return v;
+}
+
+template <bool F32>
+__device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& p, const Smem& s,
+                            uint32_t tmem, int n, uint32_t rank) {
+  const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+  const int q = warp & 3, side = warp >> 2;        // tensor-memory lanes, half of the columns
+  const uint32_t box = s.staging + warp * kStaging;
+  const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+  const uint32_t give = of_first(s.tempty);
+  uint32_t limit = kMaxPolls;
+  int u = 0;
+  float mx = -INFINITY, sum = 0.f;                 // LSE: of the run so far
+  Tile t;
+  // The box is free, and holds these values once all lanes have written them.
+  auto box_free = [&] {
+    if (lane == 0) stores_read();
+    __syncwarp();
+  };
+  auto box_full = [&] {
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+    const int chunks = t.N >> 7;                   // of 64 columns, of this half
+    const int c0 = t.n0 + side * (t.N >> 1);       // its first column
+    const int r0 = t.m0 + (int)rank * 128 + 32 * q, row = r0 + lane;
+    const bool live = row < n;
+    const int tg = live && t.kind <= DLOG ? a.tgt[row] - t.v0 : -1;
+    float2 st = make_float2(0.f, 0.f);
+    if (t.kind == DLOG && live) st = a.stat[row];
+    float acc[F32 ? 2 : 1][64];
+    int groups = t.steps ? 1 : 0;
+    if (F32) groups = (t.steps + kChunk - 1) / kChunk;
+    // Waits for the next accumulator; false if that is lost.
+    auto taken = [&] {
+      mbar_poll(s.tfull + 8 * (u & 1), (u >> 1) & 1, limit);
+      if (!__all_sync(0xffffffffu, limit)) limit = 0;
+      if (limit) tc_fence_after();
+      return limit != 0;
+    };
+    auto given = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(give + 8 * (u & 1));
+      ++u;
+    };
+    auto at = [&](int c) {
+      return lanes + (uint32_t)((u & 1) * kAccCols + side * (t.N >> 1) + 64 * c);
+    };
+    auto read64 = [&](int c, float* v) {
+      uint32_t r[64];
+      tc_ld32(at(c), r);
+      tc_ld32(at(c) + 32, r + 32);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+    };
+    if (F32) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[F32 ? c : 0][i] = 0.f;
+      for (int g = 0; g < groups && limit; ++g) {
+        if (!taken()) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c < chunks) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              tc_ld32(at(c) + 32 * h, r);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[F32 ? c : 0][32 * h + i] += __uint_as_float(r[i]);
+            }
+          }
+        }
+        given();
+      }
+    } else if (groups) {
+      taken();
+    }
+    if (!limit) break;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (c >= chunks) continue;
+      float* v = acc[F32 ? c : 0];
+      if (!F32) {
+        if (groups) {
+          read64(c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = 0.f;
+        }
+      }
+      const int col = c0 + 64 * c;
+      if (t.kind <= DLOG) {
+        if (t.steps == 0) continue;                // behind the vocabulary
+        const int left = a.V - t.v0 - col;         // ids from this column on
+        if (F32) {
+          bool fine = true;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) fine = fine && fabsf(v[i]) < INFINITY;
+          if (__any_sync(0xffffffffu, live && !fine)) {
+            const float* x = static_cast<const float*>(a.x) + (live ? (size_t)a.rows_of[row] * a.D : 0);
+            const float* w = static_cast<const float*>(a.w) + (size_t)(t.v0 + col) * a.D;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i < left) v[i] = exact_logit(v[i], x, w + (size_t)i * a.D, a.D, live);
+          }
+        }
+        if (left < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= left) v[i] = -INFINITY;
+        }
+        const int hit = tg - col;
+        if (t.kind == LSE) {
+          if ((unsigned)hit < 64u) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i == hit) x = v[i];
+            a.hit[row] = x;
+          }
+          float top = v[0];
+#pragma unroll
+          for (int i = 1; i < 64; ++i) top = fmaxf(top, v[i]);
+          // (mx is the maximum times log2(e) as rounded: every term of the sum is
+          // scaled by the same power of two.)
+          top = fmaxf(mx, top * kLog2e);
+          const float sh = top == -INFINITY ? 0.f : top;
+          float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            e0 += ex2(fmaf(v[i], kLog2e, -sh));
+            e1 += ex2(fmaf(v[i + 1], kLog2e, -sh));
+          }
+          sum = sum * ex2(mx - sh) + (e0 + e1);
+          mx = top;
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = ex2(fmaf(v[i], kLog2e, -st.x));
+        if ((unsigned)hit < 64u) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i == hit) v[i] -= 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = live ? v[i] * st.y : 0.f;
+#pragma unroll
+        for (int term = 0; term < (F32 ? 3 : 1); ++term) {
+          box_free();
+          stage_bf16(box, lane, v);
+          box_full();
+          if (lane == 0) {
+            store_box(&maps.ds, box, col, term, t.drow + r0);
+            stores_commit();
+          }
+          if (F32 && term < 2) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+          }
+        }
+      } else if (t.kind == DX) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (col + 32 * h >= a.D) continue;
+          box_free();
+          stage_f32(box, lane, v + 32 * h);
+          box_full();
+          if (lane == 0) {
+            if (a.first)
+              store_box(&maps.acc, box, col + 32 * h, 0, r0);
+            else
+              add_box(&maps.acc, box, col + 32 * h, 0, r0);
+            stores_commit();
+          }
+        }
+      } else if (a.dw_tma) {
+#pragma unroll
+        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+          if (col + 32 * h >= a.D) continue;
+          box_free();
+          if (F32)
+            stage_f32(box, lane, v + 32 * h);
+          else
+            stage_bf16(box, lane, v);
+          box_full();
+          if (lane == 0) {
+            store_box(&maps.dw, box, col + 32 * h, 0, t.v0 + r0);
+            stores_commit();
+          }
+        }
+      } else if (t.v0 + row < a.V) {
+        const size_t to = (size_t)(t.v0 + row) * a.D + col;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (col + i < a.D) {
+            if (F32)
+              static_cast<float*>(a.dw)[to + i] = v[i];
+            else
+              static_cast<__nv_bfloat16*>(a.dw)[to + i] = __float2bfloat16_rn(v[i]);
+          }
+      }
+    }
+    if (!F32 && groups) given();
+    if (t.kind == LSE && t.last) {
+      const int run = t.n0 / (kXtN * a.run);
+      if (live) a.part[(size_t)(2 * run + side) * a.ld + row] = make_float2(mx, sum);
+      mx = -INFINITY;
+      sum = 0.f;
+    }
+  }
+  if (lane == 0) stores_done();
+  __syncwarp();
+  if (!limit && lane == 0) report(a.status, 0x903);
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ XentMma a) {
+  extern __shared__ unsigned char raw[];
+  __shared__ Plan plan;
+  __shared__ uint32_t tslot;
+  const uint32_t at = (smem_addr(raw) + 1023u) & ~1023u;
+  Smem s;
+  s.stages = at;
+  s.staging = at + kStages * kStage;
+  s.full = s.staging + kEpiWarps * kStaging;
+  s.empty = s.full + 8 * kStages;
+  s.tfull = s.empty + 8 * kStages;
+  s.tempty = s.tfull + 16;
+  s.done = s.tempty + 16;
+  const uint32_t rank = cta_rank();
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    auto init = [](uint32_t bar, uint32_t count) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+    };
+    for (int i = 0; i < kStages; ++i) {
+      init(s.full + 8 * i, 1);
+      init(s.empty + 8 * i, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      init(s.tfull + 8 * b, 1);
+      init(s.tempty + 8 * b, 2 * kEpiWarps);
+    }
+    init(s.done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 2) pair_alloc(smem_addr(&tslot), 2 * kAccCols);
+  pdl_wait();
+  const int n = __ldcg(a.count), direct = __ldcg(a.count + 1);
+  if (threadIdx.x == 0) make_plan(a, n, &plan);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tslot;
+  if (warp == 0) {
+    if (elect_one()) {
+      asm volatile("fence.proxy.async;" ::: "memory");   // (rows that kernels ahead wrote)
+      copy_role<F32>(maps, a, plan, s, direct, rank);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) mma_role<F32>(a, plan, s, tmem);
+  } else if (warp >= 4) {
+    result_role<F32>(maps, a, plan, s, tmem, n, rank);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    uint32_t limit = kMaxPolls;
+    mbar_poll(s.done, 0, limit);
+    __syncwarp();
+    tc_fence_after();
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) pair_dealloc(tmem, 2 * kAccCols);
+}
+
+}  // namespace
+
+// clusters: pairs of CTAs that the device holds at once.
+cudaError_t setup_xent_mma(int dtype, int sms, int* clusters) {
+  auto one = [&](auto kernel) {
+    cudaError_t e = allow_max_smem(kernel);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms & ~1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
+    return e == cudaSuccess && *clusters < 1 ? cudaErrorInvalidConfiguration : e;
+  };
+  return dtype == CAT_F32 ? one(xent_mma_kernel<true>) : one(xent_mma_kernel<false>);
+}
+
+cudaError_t launch_xent_mma(const XentMaps& maps, const XentMma& a, int dtype, int clusters,
+                            cudaStream_t st) {
+  if (dtype == CAT_F32)
+    return launch_dependent(xent_mma_kernel<true>, dim3(2 * clusters), dim3(kThreads), kSmem, st,
+                            maps, a);
+  return launch_dependent(xent_mma_kernel<false>, dim3(2 * clusters), dim3(kThreads), kSmem, st,
+                          maps, a);
+}
+
+}  // namespace cat

@@ -1,0 +1,54 @@
+// Products of the cross entropy on the tensor cores (xent_mma.cu).
+#pragma once
+#include <cuda.h>
+
+#include "cat_internal.h"
+
+namespace cat {
+
+constexpr int kXtM = 256;                // rows of a tile (a pair of CTAs)
+constexpr int kXtN = 256;                // its columns
+constexpr int kXtK = 64;                 // K of a stage: 128 bytes of bf16
+
+// Operands and results as tensors of bf16 terms (one, or three of fp32 values):
+// [row][term][column], boxes of 64 columns by 64 rows; results by 32 rows.
+struct XentMaps {
+  CUtensorMap x;                         // X itself (bf16 rows on 16-byte boundaries)
+  CUtensorMap xp;                        // the list's rows of X
+  CUtensorMap w;                         // W
+  CUtensorMap d;                         // d of two pieces, one after the other
+  CUtensorMap ds;                        // the same, for stores
+  CUtensorMap acc;                       // dX in fp32, a row for each of the list
+  CUtensorMap dw;                        // dW
+};
+
+// One launch: the forward's runs, or up to three kinds of a backward's work.
+struct XentMma {
+  int V, D;
+  int rows;                              // rows of X and of one piece of d (allocated)
+  int piece;                             // columns of a piece of d
+  int lse;                               // 1: the forward, `run` tiles of the vocabulary a part
+  int run;
+  int dw_piece, dx_piece, d_piece;       // pieces to work on, -1: none
+  int first, dw_tma;                     // dx_piece is the first; dW's rows fit a tensor map
+  int ld;                                // part's rows
+  const int* count;                      // [0] rows of the list, [1] 1: it is X itself
+  const int* tgt;
+  const int* rows_of;                    // the list's tokens
+  const void* x; const void* w;          // X and W as they are
+  const float2* stat;
+  float* hit;
+  float2* part;
+  void* dw;
+  unsigned int* status;
+};
+
+cudaError_t launch_xent_mma(const XentMaps& maps, const XentMma& a, int dtype, int clusters,
+                            cudaStream_t st);
+// Host: [rows][planes][width] of bf16 (or fp32) with rows row_bytes apart, boxes
+// of 128 bytes by box_rows rows, 128-byte swizzle.
+bool encode_map_planes_sw128(CUtensorMap* map, const void* base, bool f32, unsigned long long width,
+                             unsigned long long planes, unsigned long long rows,
+                             unsigned long long row_bytes, unsigned int box_rows);
+
+}  // namespace cat
