@@ -176,7 +176,8 @@ struct XentCfg {
   void* xp;                // [rows_alloc][terms][pitch] their rows of X
   void* wp;                // [V][terms][pitch]
   void* d;                 // [1 or 2 pieces][rows_alloc][terms][piece]
-  float* dxacc;            // [rows_alloc][acc_pitch]
+  int acc_tiles;           // row tiles (256) of dxacc: room for slices of few rows
+  float* dxacc;            // [acc_tiles · 256][acc_pitch]
 };
 struct AttnCfg {
   int max_tokens, max_seqs, Hq, Hkv, dh, causal;

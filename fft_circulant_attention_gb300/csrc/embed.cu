@@ -100,10 +100,20 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
   int* h = hist + warp * range;
   int below = 0;
   bool bad = false;
-#pragma unroll 4
-  for (int s = 0; s < steps; ++s) {
-    const long long t = t0 + 32 * s + lane;
-    const int id = t < tokens ? id_at(ids, t, V) : -1;
+  // Eight steps' ids are on their way at once.
+  auto each = [&](auto f) {
+    for (int s0 = 0; s0 < steps; s0 += 8) {
+      int id[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const long long t = t0 + 32 * (s0 + u) + lane;
+        id[u] = s0 + u < steps && t < tokens ? id_at(ids, t, V) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) f((int)(t0 + 32 * (s0 + u) + lane), id[u]);
+    }
+  };
+  each([&](int, int id) {
     bad |= id == -2;
     below += id >= 0 && id < lo;
     const bool mine = id >= lo && id < lo + n;
@@ -115,7 +125,7 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
       }
       __syncwarp();
     }
-  }
+  });
   if (bad && blockIdx.x == 0) report(status, 0x702);
   __syncthreads();
   int base, count = 0, own;
@@ -134,10 +144,7 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
   if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
   __syncthreads();
   if (own == 0) return;
-#pragma unroll 4
-  for (int s = 0; s < steps; ++s) {
-    const long long t = t0 + 32 * s + lane;
-    const int id = t < tokens ? id_at(ids, t, V) : -1;
+  each([&](int t, int id) {
     const bool mine = id >= lo && id < lo + n;
     const unsigned any = __ballot_sync(0xffffffffu, mine);
     if (any) {
@@ -145,14 +152,14 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
         const unsigned same = __match_any_sync(any, id);
         const int start = h[id - lo];
         const int pos = start + __popc(same & ((1u << lane) - 1));
-        order[pos] = (int)t;
+        order[pos] = t;
         sid[pos] = id;
         __syncwarp(any);
         if (lane == __ffs(same) - 1) h[id - lo] = start + __popc(same);
       }
       __syncwarp();
     }
-  }
+  });
 }
 
 // dst = scale·acc, or dst + scale·acc.
@@ -216,7 +223,7 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
   };
-  constexpr int U = 4;
+  constexpr int U = 8;                          // rows on their way at once
   for (int p = p0; p < p1; p += U) {
     typename Vc::Raw raw[U];
     int id[U];
@@ -244,34 +251,48 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   flush();
 }
 
-// A piece whose last run starts in it and goes on joins that run.
-template <typename T, int VEC, int TPR>
+// A piece whose last run starts in it and goes on joins that run: a CTA, whose
+// warps add every so-many-th partial row each, the warps' sums in order then.
+// (A thread adding a column's partial rows one after another: 38 us for 16384
+// tokens, 66 pieces of the most frequent id; 5 so.)
+constexpr int kJoinWarps = kThreads / 32;
+template <typename T>
 __global__ void __launch_bounds__(kThreads)
 embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, int V, int D, int P,
                   float scale, int add) {
-  constexpr int kGroups = kThreads / TPR;
-  const int c = (blockIdx.y * TPR + threadIdx.x % TPR) * VEC;
+  __shared__ float red[kJoinWarps][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int piece = blockIdx.x * kGroups + threadIdx.x / TPR;
-  const int total = __ldcg(first + V);
+  const int piece = blockIdx.x, total = __ldcg(first + V);
   const long long q0 = (long long)piece * P;
-  if (c >= D || q0 + P >= total) return;
+  if (q0 + P >= total) return;
   const int p0 = (int)q0, p1 = p0 + P;
   const int v = __ldcg(sid + p1 - 1);
   const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
   if (a < p0 || b <= p1) return;
-  const float* q = part + ((size_t)piece * 2 + 1) * D + c;
-  float acc[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = __ldcg(q + e);
   const int last = (b - 1) / P;
-#pragma unroll 8
-  for (int i = piece + 1; i <= last; ++i) {
-    q = part + (size_t)i * 2 * D + c;
+  for (int c0 = blockIdx.y * 128; c0 < D; c0 += gridDim.y * 128) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = piece + warp; i <= last; i += kJoinWarps) {
+      // (The run's first partial row is its piece's second.)
+      const float* q = part + ((size_t)i * 2 + (i == piece)) * D + c0 + lane;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] += __ldcg(q + e);
+      for (int e = 0; e < 4; ++e)
+        if (c0 + 32 * e + lane < D) acc[e] += __ldcg(q + 32 * e);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[warp][e][lane] = acc[e];
+    __syncthreads();
+    const int e = warp, c = c0 + 32 * e + lane;
+    if (e < 4 && c < D) {
+      float s = red[0][e][lane];
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) s += red[w][e][lane];
+      put<T, 1>(dW + (size_t)v * D + c, &s, scale, add);
+    }
+    __syncthreads();
   }
-  put<T, VEC>(dW + (size_t)v * D + c, acc, scale, add);
 }
 
 // Places of a piece: at most 1024 pieces, so that a run of them all is joined
@@ -299,7 +320,9 @@ cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) 
       (const int*)c.first, (const int*)c.order, (const int*)c.sid, static_cast<const T*>(a.x),
       static_cast<T*>(a.y), c.part, c.V, D, P, ctas, c.scale, a.add);
   if (e != cudaSuccess || pieces < 2) return e;
-  return launch_dependent(embed_join_kernel<T, VEC, TPR>, dim3(ctas, cols), dim3(kThreads), 0, st,
+  const int blocks = (D + 127) / 128;
+  return launch_dependent(embed_join_kernel<T>, dim3(pieces, blocks < 8 ? blocks : 8),
+                          dim3(kThreads), 0, st,
                           (const int*)c.first, (const int*)c.sid, (const float*)c.part,
                           static_cast<T*>(a.y), c.V, D, P, c.scale, a.add);
 }

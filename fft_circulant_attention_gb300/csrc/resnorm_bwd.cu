@@ -56,7 +56,8 @@ constexpr int per_sm() {
 }
 
 // part: [gridDim.x][kSums][D].
-template <typename T, int VEC, int TPR, int E, int POST>
+// GATE: GATE_ROW, or any other kind (a.gate_kind).
+template <typename T, int VEC, int TPR, int E, int POST, int GATE>
 __global__ void __launch_bounds__(block_threads<TPR>(), per_sm<TPR, E>())
 resnorm_bwd_kernel(ResNormArgs a) {
   using V = Vec<T, VEC>;
@@ -88,31 +89,49 @@ resnorm_bwd_kernel(ResNormArgs a) {
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* pg = static_cast<const T*>(a.pg);
   const T* pb = static_cast<const T*>(a.pb);
-  int use = 0;
-  for (int row = blockIdx.x * kRows + sub; row < a.rows; row += gridDim.x * kRows, use ^= 2) {
+  const T* gate = static_cast<const T*>(a.gate);
+  // The next row is on its way while this one is worked on.
+  Raw nh[NV], ny[NV], nb[NV], nd[NV], ng[NV];
+  float4 nst;
+  auto fetch = [&](int row) {
+    if (row >= a.rows) return;
     const size_t off = (size_t)row * D;
-    const T* H = static_cast<const T*>(a.hin) + off;
-    const T* B = static_cast<const T*>(a.b) + off;
-    const T* dH = a.dh ? static_cast<const T*>(a.dh) + off : nullptr;
-    const T* dY = static_cast<const T*>(a.dy) + off;
-    const T* G = static_cast<const T*>(a.gate);
-    if (a.gate_kind == GATE_ROW) G += off;
-    Raw rb[NV], rh[NV];
-    float xh[NV][VEC], g[NV][VEC];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
-        load<T, VEC>(H + c, xh[k]);
-        load<T, VEC>(dY + c, g[k]);
-        rb[k] = V::ldr(B + c);
-        if (dH) rh[k] = V::ldr(dH + c);
+        nh[k] = V::ldr(static_cast<const T*>(a.hin) + off + c);
+        ny[k] = V::ldr(static_cast<const T*>(a.dy) + off + c);
+        nb[k] = V::ldr(static_cast<const T*>(a.b) + off + c);
+        if (a.dh) nd[k] = V::ldr(static_cast<const T*>(a.dh) + off + c);
+        if (GATE == GATE_ROW) ng[k] = V::ldr(static_cast<const T*>(a.gate) + off + c);
       }
     }
     const float* st = a.stats + row;
-    const float mh = __ldg(st), rsh = __ldg(st + (size_t)a.rows);
-    const float mb = POST ? __ldg(st + 2 * (size_t)a.rows) : 0.f;
-    const float rsb = POST ? __ldg(st + 3 * (size_t)a.rows) : 0.f;
+    nst.x = __ldg(st);
+    nst.y = __ldg(st + (size_t)a.rows);
+    if (POST) {
+      nst.z = __ldg(st + 2 * (size_t)a.rows);
+      nst.w = __ldg(st + 3 * (size_t)a.rows);
+    }
+  };
+  int use = 0, row = blockIdx.x * kRows + sub;
+  fetch(row);
+  for (; row < a.rows; row += gridDim.x * kRows, use ^= 2) {
+    const size_t off = (size_t)row * D;
+    const bool has_dh = a.dh;
+    Raw rb[NV], rh[NV], rg[NV];
+    float xh[NV][VEC], g[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      V::widen(nh[k], xh[k]);
+      V::widen(ny[k], g[k]);
+      rb[k] = nb[k];
+      rh[k] = nd[k];
+      if (GATE == GATE_ROW) rg[k] = ng[k];
+    }
+    const float mh = nst.x, rsh = nst.y, mb = nst.z, rsb = nst.w;
+    fetch(row + gridDim.x * kRows);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -141,7 +160,7 @@ resnorm_bwd_kernel(ResNormArgs a) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
         float w[VEC], b[VEC], u[VEC];
-        if (dH) {
+        if (has_dh) {
           V::widen(rh[k], w);
         } else {
 #pragma unroll
@@ -163,7 +182,7 @@ resnorm_bwd_kernel(ResNormArgs a) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) u[e] = b[e];
         }
-        if (a.gate_kind == GATE_ROW) {
+        if (GATE == GATE_ROW) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) u[e] *= scale * g[k][e];
           if (a.dgate) V::st(static_cast<T*>(a.dgate) + off + c, u);
@@ -171,7 +190,10 @@ resnorm_bwd_kernel(ResNormArgs a) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) sum_to(S_GATE, k, c, e, scale * u[e] * g[k][e]);
         }
-        load_or<T, VEC>(G, c, 1.f, u);
+        if (GATE == GATE_ROW)
+          V::widen(rg[k], u);
+        else
+          load_or<T, VEC>(gate, c, 1.f, u);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           g[k][e] *= scale * u[e];
@@ -260,7 +282,7 @@ resnorm_reduce_kernel(const float* part, int nparts, ResNormArgs a) {
   }
 }
 
-template <typename T, int VEC, int TPR, int E, int POST>
+template <typename T, int VEC, int TPR, int E, int POST, int GATE>
 cudaError_t bwd(const ResNormArgs& a, cudaStream_t st, bool setup) {
   constexpr int BT = block_threads<TPR>();
   const int per = BT / TPR, need = (a.rows + per - 1) / per;
@@ -268,29 +290,33 @@ cudaError_t bwd(const ResNormArgs& a, cudaStream_t st, bool setup) {
   const int grid = need < most ? need : most;
   const size_t smem = (size_t)kSums * a.D * sizeof(float);
   if (setup)
-    return smem > 40 * 1024 ? allow_max_smem(resnorm_bwd_kernel<T, VEC, TPR, E, POST>)
+    return smem > 40 * 1024 ? allow_max_smem(resnorm_bwd_kernel<T, VEC, TPR, E, POST, GATE>)
                             : cudaSuccess;
-  resnorm_bwd_kernel<T, VEC, TPR, E, POST><<<grid, BT, smem, st>>>(a);
+  resnorm_bwd_kernel<T, VEC, TPR, E, POST, GATE><<<grid, BT, smem, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(resnorm_reduce_kernel<T>, dim3((a.D + 31) / 32, kSums),
                           dim3(32 * kRedWarps), 0, st, (const float*)a.part, grid, a);
 }
 
-template <typename T, int VEC, int POST>
+template <typename T, int VEC, int POST, int GATE>
 cudaError_t pick(const ResNormArgs& a, cudaStream_t st, bool setup) {
   const int D = a.D;
-  if (D <= 32 * 8) return bwd<T, VEC, 32, 8, POST>(a, st, setup);
-  if (D <= 64 * 8) return bwd<T, VEC, 64, 8, POST>(a, st, setup);
-  if (D <= 128 * 8) return bwd<T, VEC, 128, 8, POST>(a, st, setup);
-  if (D <= 256 * 8) return bwd<T, VEC, 256, 8, POST>(a, st, setup);
-  if (D <= 512 * 8) return bwd<T, VEC, 512, 8, POST>(a, st, setup);
-  return bwd<T, VEC, 512, 16, POST>(a, st, setup);
+  if (D <= 32 * 8) return bwd<T, VEC, 32, 8, POST, GATE>(a, st, setup);
+  if (D <= 64 * 8) return bwd<T, VEC, 64, 8, POST, GATE>(a, st, setup);
+  if (D <= 128 * 8) return bwd<T, VEC, 128, 8, POST, GATE>(a, st, setup);
+  if (D <= 256 * 8) return bwd<T, VEC, 256, 8, POST, GATE>(a, st, setup);
+  if (D <= 512 * 8) return bwd<T, VEC, 512, 8, POST, GATE>(a, st, setup);
+  return bwd<T, VEC, 512, 16, POST, GATE>(a, st, setup);
 }
 
 template <typename T, int VEC>
 cudaError_t by_post(const ResNormArgs& a, cudaStream_t st, bool setup) {
-  return a.post ? pick<T, VEC, 1>(a, st, setup) : pick<T, VEC, 0>(a, st, setup);
+  if (a.gate_kind == GATE_ROW)
+    return a.post ? pick<T, VEC, 1, GATE_ROW>(a, st, setup)
+                  : pick<T, VEC, 0, GATE_ROW>(a, st, setup);
+  return a.post ? pick<T, VEC, 1, GATE_NONE>(a, st, setup)
+                : pick<T, VEC, 0, GATE_NONE>(a, st, setup);
 }
 
 }  // namespace
@@ -315,7 +341,11 @@ cudaError_t setup_resnorm(int D, int dtype, int post) {
   ResNormArgs a = {};
   a.D = D;
   a.post = post;
-  return dispatch(a, dtype, nullptr, true);
+  for (a.gate_kind = GATE_NONE; a.gate_kind <= GATE_ROW; a.gate_kind += GATE_ROW) {
+    const cudaError_t e = dispatch(a, dtype, nullptr, true);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace cat

@@ -289,7 +289,7 @@ int cat_plan_create_xent(cat_plan_t* out, int max_tokens, int V, int D, int dtyp
   if (ok && grad)
     ok = alloc(p, &c.stat, n) && alloc(p, &c.inv, n) &&
          bytes(&c.d, rows * c.piece * 2 * c.terms * (c.pieces > 1 ? 2 : 1)) &&
-         alloc(p, &c.dxacc, rows * c.acc_pitch);
+         alloc(p, &c.dxacc, (size_t)c.acc_tiles * 256 * c.acc_pitch);
   if (!ok) return fail(p, CAT_ERR_ALLOC);
   std::snprintf(p->desc, sizeof(p->desc), "op=xent max_tokens=%d V=%d D=%d grad=%d piece=%d "
                 "workspace=%zu", max_tokens, V, D, grad, c.piece, p->workspace_bytes);

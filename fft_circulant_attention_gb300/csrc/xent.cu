@@ -82,11 +82,20 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.per, t1 = min(p.tokens, t0 + p.per);
   int before = 0, all = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.tokens; i += kThreads) {
-    const int held = id_at(p.targets, i, p.V) >= 0;
-    all += held;
-    before += i < t0 ? held : 0;
+  // (Sixteen ids on their way at once: a CTA has the whole list to look through.)
+  for (int i0 = 0; i0 < p.tokens; i0 += 16 * kThreads) {
+    int id[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int i = i0 + u * kThreads + threadIdx.x;
+      id[u] = i < p.tokens ? id_at(p.targets, i, p.V) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int held = id[u] >= 0;
+      all += held;
+      before += i0 + u * kThreads + (int)threadIdx.x < t0 ? held : 0;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -151,38 +160,78 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
   }
 }
 
-// loss and lse from the parts' maxima (times log2(e)) and sums.
-__global__ void __launch_bounds__(kThreads)
+// loss and lse from the parts' maxima (times log2(e)) and sums: 32 places of the
+// list a CTA, its warps every so-many-th part each (1024 tokens, 394 parts: 61 us
+// with a thread a place, 5 so).
+constexpr int kFinWarps = 16;
+__global__ void __launch_bounds__(32 * kFinWarps)
 xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, const int* rows,
                    const float* hit, float* __restrict__ loss, float* __restrict__ lse) {
-  const int pos = blockIdx.x * kThreads + threadIdx.x;
+  __shared__ float2 red[kFinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pos = blockIdx.x * 32 + lane;
   pdl_wait();
-  if (pos >= __ldcg(count)) return;
+  const int n = __ldcg(count);
+  if (blockIdx.x * 32 >= n) return;
   float top = -INFINITY, s = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < nparts; ++i) {
-    const float2 q = __ldcg(part + (size_t)i * ld + pos);
+  auto join = [&](float2 q) {
     const float m = fmaxf(top, q.x), sh = m == -INFINITY ? 0.f : m;
     s = s * exp2f(top - sh) + q.y * exp2f(q.x - sh);
     top = m;
+  };
+  if (pos < n) {
+#pragma unroll 4
+    for (int i = warp; i < nparts; i += kFinWarps) join(__ldcg(part + (size_t)i * ld + pos));
   }
+  red[warp][lane] = make_float2(top, s);
+  __syncthreads();
+  if (warp || pos >= n) return;
+  for (int w = 1; w < kFinWarps; ++w) join(red[w][lane]);
   const float z = (top + log2f(s)) * kLn2;
   const int t = __ldcg(rows + pos);
   lse[t] = z;
   loss[t] = z - __ldcg(hit + pos);
 }
 
-// dX's rows from the list's, zeros for the tokens without a target.
-template <typename T>
+// dX's rows from the sums of the list's (the slices of each, in order), zeros for
+// the tokens without a target.  Vectors of four where they divide a row.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
-xent_dx_kernel(const float* acc, int pitch, const int* inv, T* __restrict__ dX, int tokens, int D,
-               int per) {
+xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T* __restrict__ dX,
+               int tokens, int D, int per, int pairs, int piece, int acc_tiles) {
   pdl_wait();
-  const int row0 = blockIdx.x * per, n = min(per, tokens - row0) * D;
+  const int mt = (__ldcg(count) + kXtM - 1) / kXtM;
+  const int slices = mt ? xent_slices(pairs, mt, (D + kXtN - 1) / kXtN, piece, acc_tiles) : 0;
+  const size_t apart = (size_t)mt * kXtM * pitch;
+  const int nv = D / VEC, row0 = blockIdx.x * per, n = min(per, tokens - row0) * nv;
+#pragma unroll 2
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int r = i / D, c = i - r * D, pos = __ldcg(inv + row0 + r);
-    st_elem(dX + (size_t)(row0 + r) * D + c,
-            pos >= 0 ? __ldcg(acc + (size_t)pos * pitch + c) : 0.f);
+    const int r = i / nv, c = (i - r * nv) * VEC, pos = __ldcg(inv + row0 + r);
+    float v[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+    if (pos >= 0) {
+      const float* q = acc + (size_t)pos * pitch + c;
+#pragma unroll 4
+      for (int s = 0; s < slices; ++s, q += apart) {
+        if (VEC == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
+          v[0] += x.x; v[VEC > 1 ? 1 : 0] += x.y; v[VEC > 1 ? 2 : 0] += x.z; v[VEC > 1 ? 3 : 0] += x.w;
+        } else {
+          v[0] += __ldcg(q);
+        }
+      }
+    }
+    T* to = dX + (size_t)(row0 + r) * D + c;
+    if (VEC == 4 && sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(to) = make_float4(v[0], v[VEC > 1 ? 1 : 0], v[VEC > 1 ? 2 : 0], v[VEC > 1 ? 3 : 0]);
+    } else if (VEC == 4) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[VEC > 1 ? 1 : 0]),
+                             __floats2bfloat162_rn(v[VEC > 1 ? 2 : 0], v[VEC > 1 ? 3 : 0])};
+      *reinterpret_cast<uint2*>(to) = *reinterpret_cast<uint2*>(h);
+    } else {
+      st_elem(to, v[0]);
+    }
   }
 }
 
@@ -207,6 +256,7 @@ void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   c->pack = dtype == CAT_F32 || D % 8 != 0;
   c->rows_alloc = tiles(c->max_tokens, kXtM) * kXtM;
   if (c->rows_alloc == 0) c->rows_alloc = kXtM;
+  c->acc_tiles = c->rows_alloc / kXtM + pairs / tiles(D, kXtN);
   // A piece of the vocabulary: dW's tiles (of the piece by D) are the longest of a
   // launch, so that their number is a multiple of the pairs, or just below; more
   // of the vocabulary at once where there are few tokens, and less where two
@@ -290,7 +340,7 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
   const unsigned long long drows = (unsigned long long)c.rows_alloc * (c.pieces > 1 ? 2 : 1);
   ok = encode_map_planes_sw128(&m->d, c.d, false, c.piece, c.terms, drows, db, 64) &&
        encode_map_planes_sw128(&m->ds, c.d, false, c.piece, c.terms, drows, db, 32) &&
-       encode_map_planes_sw128(&m->acc, c.dxacc, true, D, 1, c.rows_alloc,
+       encode_map_planes_sw128(&m->acc, c.dxacc, true, D, 1, (unsigned long long)c.acc_tiles * kXtM,
                                (unsigned long long)c.acc_pitch * 4, 32);
   const bool f32 = p->dtype == CAT_F32;
   if (ok && a.dw && D % (f32 ? 4 : 8) == 0)
@@ -299,12 +349,14 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
   return ok;
 }
 
-template <typename T>
+template <typename T, int VEC>
 cudaError_t finish_dx(const cat_plan_s* p, const XentArgs& a, int tokens) {
-  const int per = p->D >= 2048 ? 1 : 2048 / p->D;
-  return launch_dependent(xent_dx_kernel<T>, dim3(tiles(tokens, per)), dim3(kThreads), 0,
-                          p->stream, (const float*)p->xe.dxacc, p->xe.acc_pitch,
-                          (const int*)p->xe.inv, static_cast<T*>(a.dx), tokens, p->D, per);
+  const XentCfg& c = p->xe;
+  const int nv = p->D / VEC, per = nv >= 2 * kThreads ? 1 : 2 * kThreads / nv;
+  return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, per)), dim3(kThreads), 0,
+                          p->stream, (const float*)c.dxacc, c.acc_pitch, (const int*)c.inv,
+                          (const int*)c.count, static_cast<T*>(a.dx), tokens, p->D, per, c.pairs,
+                          c.piece, c.acc_tiles);
 }
 
 }  // namespace
@@ -323,6 +375,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.D = p->D;
   k.rows = c.rows_alloc;
   k.piece = c.piece;
+  k.acc_tiles = c.acc_tiles;
   k.ld = c.max_tokens;
   k.count = c.count;
   k.tgt = c.tgt;
@@ -341,8 +394,8 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     k.run = run_length(c.V, tokens, c.pairs);
     e = launch_xent_mma(maps, k, p->dtype, c.pairs, st);
     if (e != cudaSuccess) return e;
-    return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, kThreads)), dim3(kThreads), 0,
-                            st, (const float2*)c.part, 2 * tiles(tiles(c.V, kXtN), k.run),
+    return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)),
+                            dim3(32 * kFinWarps), 0, st, (const float2*)c.part, 2 * tiles(tiles(c.V, kXtN), k.run),
                             c.max_tokens, (const int*)c.count, (const int*)c.rows,
                             (const float*)c.hit, a.loss, a.lse);
   }
@@ -356,7 +409,9 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     if (e != cudaSuccess) return e;
   }
   if (!a.dx) return cudaSuccess;
-  return f32 ? finish_dx<float>(p, a, tokens) : finish_dx<__nv_bfloat16>(p, a, tokens);
+  if (p->D % 4)
+    return f32 ? finish_dx<float, 1>(p, a, tokens) : finish_dx<__nv_bfloat16, 1>(p, a, tokens);
+  return f32 ? finish_dx<float, 4>(p, a, tokens) : finish_dx<__nv_bfloat16, 4>(p, a, tokens);
 }
 
 }  // namespace cat

@@ -37,11 +37,12 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kBox = 64 * 128;                     // bytes of a box
 constexpr int kOperand = 2 * kBox;                 // A's or B's share of a stage
 constexpr int kStage = 2 * kOperand;
-constexpr int kStaging = 32 * 128;                 // a warp's box of results
+constexpr int kResult = 32 * 128;                  // a box of results
+constexpr int kStaging = 2 * kResult;              // two for each warp
 constexpr int kAccCols = 256;
 constexpr int kChunk = 2;                          // K stages between read-outs (fp32)
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStaging + 512;
@@ -126,8 +127,9 @@ __device__ __forceinline__ void add_box(const CUtensorMap* map, uint32_t src, in
 __device__ __forceinline__ void stores_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// All but the last store's box may be written again.
 __device__ __forceinline__ void stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 __device__ __forceinline__ void stores_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -153,6 +155,7 @@ struct Tile {
   int kind, m0, n0, N;                             // rows and columns of the result
   int steps;                                       // K stages
   int v0, drow;                                    // its piece's first id, rows of d
+  int k0, arow;                                    // DX: first K stage, rows of its slice
   int last;                                        // LSE: the run's last tile
 };
 
@@ -188,7 +191,9 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
   if (a.dw_piece >= 0) nw = pieces_tiles(a, a.dw_piece) * p->nt;
   if (a.dx_piece >= 0) {
     cx = pieces_tiles(a, a.dx_piece) * (kXtN / kXtK);
-    nx = p->mt * p->nt;
+    const int slices = xent_slices(p->pairs, p->mt, p->nt, a.piece, a.acc_tiles);
+    cx = (cx + slices - 1) / slices;
+    nx = p->mt * p->nt * slices;
   }
   p->pk = cx;
   if (a.d_piece >= 0) {
@@ -218,7 +223,7 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
 // This pair's `it`-th tile; false behind the last one.
 __device__ __forceinline__ bool tile_at(const XentMma& a, const Plan& p, int it, Tile* t) {
   t->last = 1;
-  t->v0 = t->drow = 0;
+  t->v0 = t->drow = t->k0 = 0;
   int i;
   if (a.lse) {
     // `run` tiles of the vocabulary of one part, then the next part's.
@@ -245,10 +250,14 @@ __device__ __forceinline__ bool tile_at(const XentMma& a, const Plan& p, int it,
     t->kind = DX;
     t->v0 = a.dx_piece * a.piece;
     t->drow = (a.dx_piece & 1) * a.rows;
+    const int tiles = p.mt * p.nt, slice = i / tiles;
+    i -= slice * tiles;
     t->m0 = i / p.nt * kXtM;
     t->n0 = i % p.nt * kXtN;
-    t->steps = p.pk;
-  } else if ((i += p.l0 - p.x1) < p.l1) {
+    t->k0 = slice * p.pk;
+    t->steps = max(0, min(p.pk, pieces_tiles(a, a.dx_piece) * (kXtN / kXtK) - t->k0));
+    t->arow = slice * p.mt * kXtM;
+  } else if ((i = p.l0 + it - mine - (p.x1 - p.x0)) < p.l1) {
     t->kind = DLOG;
     t->v0 = a.d_piece * a.piece;
     t->drow = (a.d_piece & 1) * a.rows;
@@ -310,7 +319,7 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
                          s.full + 8 * st),
                      "r"(bytes)
                      : "memory");
-      const int kk = k * kXtK;
+      const int kk = (t.k0 + k) * kXtK;
       for (int b = 0; b < 2; ++b) {
         const uint32_t to = dst + b * kBox;
         if (t.kind <= DLOG)
@@ -424,15 +433,17 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
                             uint32_t tmem, int n, uint32_t rank) {
   const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
   const int q = warp & 3, side = warp >> 2;        // tensor-memory lanes, half of the columns
-  const uint32_t box = s.staging + warp * kStaging;
+  uint32_t box = s.staging + warp * kStaging;      // the next of the warp's two
+  const uint32_t other = 2 * box + kResult;
   const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
   const uint32_t give = of_first(s.tempty);
   uint32_t limit = kMaxPolls;
   int u = 0;
   float mx = -INFINITY, sum = 0.f;                 // LSE: of the run so far
   Tile t;
-  // The box is free, and holds these values once all lanes have written them.
+  // The other box is free, and holds these values once all lanes have written them.
   auto box_free = [&] {
+    box = other - box;
     if (lane == 0) stores_read();
     __syncwarp();
   };
@@ -508,6 +519,7 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
       if (!F32) {
         if (groups) {
           read64(c, v);
+          if (c == chunks - 1) given();
         } else {
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = 0.f;
@@ -586,15 +598,15 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
       } else if (t.kind == DX) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (col + 32 * h >= a.D) continue;
+          if (col + 32 * h >= a.D || !(groups || a.first)) continue;
           box_free();
           stage_f32(box, lane, v + 32 * h);
           box_full();
           if (lane == 0) {
             if (a.first)
-              store_box(&maps.acc, box, col + 32 * h, 0, r0);
+              store_box(&maps.acc, box, col + 32 * h, 0, t.arow + r0);
             else
-              add_box(&maps.acc, box, col + 32 * h, 0, r0);
+              add_box(&maps.acc, box, col + 32 * h, 0, t.arow + r0);
             stores_commit();
           }
         }
@@ -625,7 +637,6 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
           }
       }
     }
-    if (!F32 && groups) given();
     if (t.kind == LSE && t.last) {
       const int run = t.n0 / (kXtN * a.run);
       if (live) a.part[(size_t)(2 * run + side) * a.ld + row] = make_float2(mx, sum);

@@ -18,9 +18,18 @@ struct XentMaps {
   CUtensorMap w;                         // W
   CUtensorMap d;                         // d of two pieces, one after the other
   CUtensorMap ds;                        // the same, for stores
-  CUtensorMap acc;                       // dX in fp32, a row for each of the list
+  CUtensorMap acc;                       // dX in fp32: slices of rows of the list
   CUtensorMap dw;                        // dW
 };
+
+// Slices of a piece's K that DX is cut into where it has fewer tiles than there
+// are pairs of CTAs, each with rows of its own; at least eight K stages a slice.
+__host__ __device__ inline int xent_slices(int pairs, int mt, int nt, int piece, int acc_tiles) {
+  int s = pairs / (mt * nt);
+  if (s > acc_tiles / mt) s = acc_tiles / mt;
+  if (s > piece / (8 * kXtK)) s = piece / (8 * kXtK);
+  return s < 1 ? 1 : s;
+}
 
 // One launch: the forward's runs, or up to three kinds of a backward's work.
 struct XentMma {
@@ -30,6 +39,7 @@ struct XentMma {
   int lse;                               // 1: the forward, `run` tiles of the vocabulary a part
   int run;
   int dw_piece, dx_piece, d_piece;       // pieces to work on, -1: none
+  int acc_tiles;                         // row tiles that dX's slices have room for
   int first, dw_tma;                     // dx_piece is the first; dW's rows fit a tensor map
   int ld;                                // part's rows
   const int* count;                      // [0] rows of the list, [1] 1: it is X itself
