@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t of_first(uint32_t a) {
   return r;
 }
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 __device__ __forceinline__ void pair_alloc(uint32_t slot, uint32_t cols) {
@@ -165,6 +165,7 @@ struct Plan {
   int dk, tk, pk;                                  // K stages of D, of the list, of a piece
   int w1, x0, x1, l0, l1;                          // DW (every pairs-th), DX, D tiles
   int pairs, pair;
+  int by, rest;                                    // pairs over a row of strided tiles
 };
 
 __device__ __forceinline__ int pieces_tiles(const XentMma& a, int piece) {
@@ -183,8 +184,12 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
   p->vt = p->pk = 0;
   if (a.lse) {
     p->vt = ((a.V + kXtN - 1) / kXtN + a.run - 1) / a.run;
+    p->by = p->pairs / max(p->mt, 1);
+    p->rest = p->pairs % max(p->mt, 1);
     return;
   }
+  p->by = p->pairs / p->nt;
+  p->rest = p->pairs % p->nt;
   // Tiles and their lengths in K stages; a tile of D ends in stores that no
   // product of its own hides.
   int nw = 0, nx = 0, nl = 0, cx = 1;
@@ -220,58 +225,123 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
   p->l1 = l1;
 }
 
-// This pair's `it`-th tile; false behind the last one.
-__device__ __forceinline__ bool tile_at(const XentMma& a, const Plan& p, int it, Tile* t) {
-  t->last = 1;
-  t->v0 = t->drow = t->k0 = 0;
-  int i;
-  if (a.lse) {
-    // `run` tiles of the vocabulary of one part, then the next part's.
-    const int part = p.pair + p.pairs * (it / a.run), r = it % a.run;
-    if (part >= p.mt * p.vt) return false;
-    t->kind = LSE;
-    t->m0 = part % p.mt * kXtM;
-    t->n0 = (part / p.mt * a.run + r) * kXtN;
-    t->N = kXtN;
-    t->steps = t->n0 < a.V ? p.dk : 0;             // (the last run may be shorter)
-    t->last = r == a.run - 1;
+// This pair's tiles, one after another.  A role's next tile costs it a few
+// additions: with divisions the MMAs waited for them at every tile.
+struct Cursor {
+  int i, end, x, y;                                // place in the list of a kind; column, row
+  int r;                                           // LSE: tile of the run
+  int kind;
+  Tile t;
+
+  __device__ __forceinline__ void start(const XentMma& a, const Plan& p) {
+    if (a.lse) {
+      kind = LSE;
+      i = p.pair;
+      end = p.mt * p.vt;
+      y = p.mt ? i % p.mt : 0;                     // row of tiles, run
+      x = p.mt ? i / p.mt : 0;
+      r = 0;
+    } else {
+      kind = DW;
+      i = p.pair;
+      end = p.w1;
+      y = i / p.nt;
+      x = i % p.nt;
+    }
+  }
+  __device__ bool next(const XentMma& a, const Plan& p) {
+    t.k0 = t.arow = t.v0 = t.drow = 0;
+    t.last = 1;
+    if (a.lse) {
+      if (i >= end) return false;
+      t.kind = LSE;
+      t.m0 = y * kXtM;
+      t.n0 = (x * a.run + r) * kXtN;
+      t.N = kXtN;
+      t.steps = t.n0 < a.V ? p.dk : 0;             // (the last run may be shorter)
+      if (++r == a.run) {
+        r = 0;
+        i += p.pairs;
+        x += p.by;
+        y += p.rest;
+        if (y >= p.mt) {
+          y -= p.mt;
+          ++x;
+        }
+      } else {
+        t.last = 0;
+      }
+      return true;
+    }
+    if (kind == DW) {
+      if (i < end) {
+        t.kind = DW;
+        t.v0 = a.dw_piece * a.piece;
+        t.drow = (a.dw_piece & 1) * a.rows;
+        t.m0 = y * kXtM;
+        t.n0 = x * kXtN;
+        t.steps = p.tk;
+        t.N = a.D - t.n0 > kXtN / 2 ? kXtN : kXtN / 2;
+        i += p.pairs;
+        y += p.by;
+        x += p.rest;
+        if (x >= p.nt) {
+          x -= p.nt;
+          ++y;
+        }
+        return true;
+      }
+      kind = DX;
+      i = p.x0;
+      end = p.x1;
+      const int tiles = max(p.mt * p.nt, 1);
+      r = i / tiles;                               // slice
+      y = (i - r * tiles) / p.nt;
+      x = i - r * tiles - y * p.nt;
+    }
+    if (kind == DX) {
+      if (i < end) {
+        t.kind = DX;
+        t.v0 = a.dx_piece * a.piece;
+        t.drow = (a.dx_piece & 1) * a.rows;
+        t.m0 = y * kXtM;
+        t.n0 = x * kXtN;
+        t.k0 = r * p.pk;
+        t.steps = max(0, min(p.pk, pieces_tiles(a, a.dx_piece) * (kXtN / kXtK) - t.k0));
+        t.arow = r * p.mt * kXtM;
+        t.N = a.D - t.n0 > kXtN / 2 ? kXtN : kXtN / 2;
+        ++i;
+        if (++x == p.nt) {
+          x = 0;
+          if (++y == p.mt) {
+            y = 0;
+            ++r;
+          }
+        }
+        return true;
+      }
+      kind = DLOG;
+      i = p.l0;
+      end = p.l1;
+      x = p.mt ? i / p.mt : 0;
+      y = p.mt ? i - x * p.mt : 0;
+    }
+    if (i >= end) return false;
+    t.kind = DLOG;
+    t.v0 = a.d_piece * a.piece;
+    t.drow = (a.d_piece & 1) * a.rows;
+    t.m0 = y * kXtM;
+    t.n0 = x * kXtN;
+    t.steps = p.dk;
+    t.N = kXtN;
+    ++i;
+    if (++y == p.mt) {
+      y = 0;
+      ++x;
+    }
     return true;
   }
-  const int mine = p.w1 > p.pair ? (p.w1 - p.pair + p.pairs - 1) / p.pairs : 0;
-  if (it < mine) {
-    i = p.pair + it * p.pairs;
-    t->kind = DW;
-    t->v0 = a.dw_piece * a.piece;
-    t->drow = (a.dw_piece & 1) * a.rows;
-    t->m0 = i / p.nt * kXtM;
-    t->n0 = i % p.nt * kXtN;
-    t->steps = p.tk;
-  } else if ((i = p.x0 + it - mine) < p.x1) {
-    t->kind = DX;
-    t->v0 = a.dx_piece * a.piece;
-    t->drow = (a.dx_piece & 1) * a.rows;
-    const int tiles = p.mt * p.nt, slice = i / tiles;
-    i -= slice * tiles;
-    t->m0 = i / p.nt * kXtM;
-    t->n0 = i % p.nt * kXtN;
-    t->k0 = slice * p.pk;
-    t->steps = max(0, min(p.pk, pieces_tiles(a, a.dx_piece) * (kXtN / kXtK) - t->k0));
-    t->arow = slice * p.mt * kXtM;
-  } else if ((i = p.l0 + it - mine - (p.x1 - p.x0)) < p.l1) {
-    t->kind = DLOG;
-    t->v0 = a.d_piece * a.piece;
-    t->drow = (a.d_piece & 1) * a.rows;
-    t->m0 = i % p.mt * kXtM;
-    t->n0 = i / p.mt * kXtN;
-    t->steps = p.dk;
-    t->N = kXtN;
-    return true;
-  } else {
-    return false;
-  }
-  t->N = a.D - t->n0 > kXtN / 2 ? kXtN : kXtN / 2;
-  return true;
-}
+};
 
 // The terms of the six products, smallest first.
 __device__ __forceinline__ int term_a(int q) { return (0x201100 >> (4 * (5 - q))) & 3; }
@@ -303,17 +373,20 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
                           int direct, uint32_t rank) {
   const CUtensorMap* mx = direct ? &maps.x : &maps.xp;
   uint32_t limit = kMaxPolls;
-  int g = 0;
-  Tile t;
-  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+  const uint32_t full0 = of_first(s.full);
+  int g = 0, st = 0;
+  uint32_t phase = 1;                              // (a fresh barrier's phase ahead is over)
+  Cursor cur;
+  cur.start(a, p);
+  while (limit && cur.next(a, p)) {
+    const Tile t = cur.t;
     const int half = t.N >> 1, nb = half >> 6;     // B columns of this CTA, boxes of them
     const uint32_t bytes = 2 * (kOperand + nb * kBox);
     const int ar = t.m0 + (int)rank * 128, br = t.n0 + (int)rank * half;
     each_stage<F32>(t.steps, [&](int k, int ta, int tb, int) {
-      const int st = g % kStages;
-      if (g >= kStages) mbar_poll(s.empty + 8 * st, (g / kStages - 1) & 1, limit);
+      mbar_poll(s.empty + 8 * st, phase, limit);
       if (!limit) return;
-      const uint32_t dst = s.stages + st * kStage, full = of_first(s.full + 8 * st);
+      const uint32_t dst = s.stages + st * kStage, full = full0 + 8 * st;
       if (rank == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
                          s.full + 8 * st),
@@ -339,6 +412,10 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
           pair_load(to, mx, br + 64 * b, tb, kk, full);
       }
       ++g;
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
     });
   }
   if (!limit) {
@@ -355,23 +432,27 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
 template <bool F32>
 __device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_t tmem) {
   uint32_t limit = kMaxPolls;
-  int g = 0, u = 0;                                // stages; accumulators used
-  Tile t;
-  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+  int st = 0, u = 0;                               // stage; accumulators used
+  uint32_t phase = 0;
+  const uint64_t base = ((uint64_t)1 << 46) | ((uint64_t)2 << 61) | ((uint64_t)(1024 >> 4) << 32);
+  const uint64_t mn = (uint64_t)(kBox >> 4) << 16, km = (uint64_t)1 << 16;
+  Cursor cur;
+  cur.start(a, p);
+  bool more = cur.next(a, p);
+  while (limit && more) {
+    const Tile t = cur.t;
+    more = cur.next(a, p);                         // (while this tile's stages are awaited)
     // Which of the operands' two directions is K: MN-major where it is the rows.
     const uint32_t idesc = idesc_bf16_f32(kXtM, t.N) | (t.kind == DW ? 1u << 15 : 0u) |
                            (t.kind >= DX ? 1u << 16 : 0u);
     each_stage<F32>(t.steps, [&](int, int, int, int flags) {
       if (!limit) return;
       const uint32_t b = u & 1;
-      if ((flags & 1) && u >= 2) mbar_poll(s.tempty + 8 * b, ((u >> 1) - 1) & 1, limit);
-      const int st = g % kStages;
-      mbar_poll(s.full + 8 * st, (g / kStages) & 1, limit);
+      if (flags & 1) mbar_poll(s.tempty + 8 * b, ((u >> 1) & 1) ^ 1, limit);
+      mbar_poll(s.full + 8 * st, phase, limit);
       if (!limit) return;
       tc_fence_after();
       const uint32_t sa = s.stages + st * kStage, sb = sa + kOperand;
-      const uint64_t base = ((uint64_t)1 << 46) | ((uint64_t)2 << 61) | ((uint64_t)(1024 >> 4) << 32);
-      const uint64_t mn = (uint64_t)(kBox >> 4) << 16, km = (uint64_t)1 << 16;
       uint64_t da = base | (t.kind == DW ? mn : km) | ((sa & 0x3FFFFu) >> 4);
       uint64_t db = base | (t.kind >= DX ? mn : km) | ((sb & 0x3FFFFu) >> 4);
       const uint64_t sta = t.kind == DW ? 2048 >> 4 : 32 >> 4;
@@ -380,7 +461,10 @@ __device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_
       for (int k = 0; k < kXtK / 16; ++k)
         pair_mma(tmem + b * kAccCols, da + k * sta, db + k * stb, idesc, k > 0 || !(flags & 1));
       pair_commit(s.empty + 8 * st);
-      ++g;
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
       if (flags & 2) {
         pair_commit(s.tfull + 8 * b);
         ++u;
@@ -440,7 +524,9 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
   uint32_t limit = kMaxPolls;
   int u = 0;
   float mx = -INFINITY, sum = 0.f;                 // LSE: of the run so far
-  Tile t;
+  Cursor cur;
+  cur.start(a, p);
+  bool more = cur.next(a, p);
   // The other box is free, and holds these values once all lanes have written them.
   auto box_free = [&] {
     box = other - box;
@@ -451,7 +537,9 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
     fence_proxy_async_smem();
     __syncwarp();
   };
-  for (int it = 0; limit && tile_at(a, p, it, &t); ++it) {
+  while (limit && more) {
+    const Tile t = cur.t;
+    more = cur.next(a, p);
     const int chunks = t.N >> 7;                   // of 64 columns, of this half
     const int c0 = t.n0 + side * (t.N >> 1);       // its first column
     const int r0 = t.m0 + (int)rank * 128 + 32 * q, row = r0 + lane;
@@ -580,7 +668,11 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
             if (i == hit) v[i] -= 1.f;
         }
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = live ? v[i] * st.y : 0.f;
+        for (int i = 0; i < 64; ++i) v[i] *= st.y;
+        if (!__all_sync(0xffffffffu, live)) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = live ? v[i] : 0.f;
+        }
 #pragma unroll
         for (int term = 0; term < (F32 ? 3 : 1); ++term) {
           box_free();
