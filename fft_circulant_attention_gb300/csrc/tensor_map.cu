@@ -89,4 +89,19 @@ bool encode_map_planes_sw128(CUtensorMap* map, const void* base, bool f32, unsig
   return r == CUDA_SUCCESS;
 }
 
+bool encode_map_blocks_sw128(CUtensorMap* map, const void* base, unsigned long long width,
+                             unsigned long long planes, unsigned long long rows,
+                             unsigned long long row_bytes) {
+  std::call_once(g_once, find_encode);
+  if (!g_encode) return false;
+  cuuint64_t gd[4] = {64, rows, width / 64, planes};
+  cuuint64_t gs[3] = {row_bytes, 128, planes > 1 ? width * 2 : row_bytes};
+  cuuint32_t bx[4] = {64, 64, 2, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs,
+                        bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace cat

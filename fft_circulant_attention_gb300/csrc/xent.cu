@@ -251,7 +251,7 @@ int run_length(int V, int tokens, int pairs) {
 void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   c->pairs = pairs;
   c->terms = dtype == CAT_F32 ? 3 : 1;
-  c->pitch = (D + 7) / 8 * 8;
+  c->pitch = (D + 63) / 64 * 64;
   c->acc_pitch = (D + 3) / 4 * 4;
   c->pack = dtype == CAT_F32 || D % 8 != 0;
   c->rows_alloc = tiles(c->max_tokens, kXtM) * kXtM;
@@ -327,18 +327,26 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
   const XentCfg& c = p->xe;
   const int D = p->D;
   const unsigned long long rb = (unsigned long long)c.terms * c.pitch * 2;
-  bool ok = encode_map_planes_sw128(&m->xp, c.xp, false, c.pitch, c.terms, c.rows_alloc, rb, 64);
+  auto both = [](CUtensorMap* by_k, CUtensorMap* by_rows, const void* q, unsigned long long width,
+                 unsigned long long planes, unsigned long long rows, unsigned long long bytes) {
+    return encode_map_planes_sw128(by_k, q, false, width, planes, rows, bytes, 128) &&
+           (width % 64 == 0
+                ? encode_map_blocks_sw128(by_rows, q, width, planes, rows, bytes)
+                : encode_map_planes_sw128(by_rows, q, false, width, planes, rows, bytes, 64));
+  };
+  bool ok = both(&m->xp, &m->xpr, c.xp, c.pitch, c.terms, c.rows_alloc, rb);
   if (c.pack) {
     m->x = m->xp;
-    ok = ok && encode_map_planes_sw128(&m->w, c.wp, false, c.pitch, c.terms, c.V, rb, 64);
+    m->xr = m->xpr;
+    ok = ok && both(&m->w, &m->wr, c.wp, c.pitch, c.terms, c.V, rb);
   } else {
-    ok = ok && encode_map_planes_sw128(&m->x, a.x, false, D, 1, tokens, rb, 64) &&
-         encode_map_planes_sw128(&m->w, a.w, false, D, 1, c.V, rb, 64);
+    ok = ok && both(&m->x, &m->xr, a.x, D, 1, tokens, 2ull * D) &&
+         both(&m->w, &m->wr, a.w, D, 1, c.V, 2ull * D);
   }
   if (!ok || !back) return ok;
   const unsigned long long db = (unsigned long long)c.terms * c.piece * 2;
   const unsigned long long drows = (unsigned long long)c.rows_alloc * (c.pieces > 1 ? 2 : 1);
-  ok = encode_map_planes_sw128(&m->d, c.d, false, c.piece, c.terms, drows, db, 64) &&
+  ok = both(&m->d, &m->dr, c.d, c.piece, c.terms, drows, db) &&
        encode_map_planes_sw128(&m->ds, c.d, false, c.piece, c.terms, drows, db, 32) &&
        encode_map_planes_sw128(&m->acc, c.dxacc, true, D, 1, (unsigned long long)c.acc_tiles * kXtM,
                                (unsigned long long)c.acc_pitch * 4, 32);
@@ -386,6 +394,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.hit = c.hit;
   k.part = c.part;
   k.dw = a.dw;
+  k.two_w = !c.pack && p->D % 64;
   k.dw_tma = p->D % (f32 ? 4 : 8) == 0;
   k.status = p->status;
   k.dw_piece = k.dx_piece = k.d_piece = -1;

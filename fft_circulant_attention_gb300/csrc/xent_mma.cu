@@ -9,9 +9,13 @@
 // All four are tiles of 256 x 256 by one pair of CTAs (cta_group::2): each CTA
 // holds 128 rows of A and half of B in shared memory, the pair's tensor cores
 // read both halves, so that a stage of K = 64 needs 32 KB an SM instead of the
-// 48 KB of a tile of one CTA.  What is K in one product is a row in another: the
-// boxes in shared memory are the same (64 columns by 64 rows, 128-byte swizzle),
-// the matrix descriptors say which of the two is K.
+// 48 KB of a tile of one CTA.  What is K in one product is a row in another: an
+// operand's rows by K come as one box of 64 columns by 128 rows, its K rows by
+// 128 columns as one box of two times 64 columns by 64 rows (a third coordinate
+// counts columns by 64), both with 128-byte swizzle, and the matrix descriptors
+// say which of the two is K.  Copies of 16 KB matter: with four of 8 KB a stage
+// the products waited for copies (tensor pipe 72 % busy, 94 % with two of 16 KB;
+// sharing B's copies between two pairs by multicast did not help).
 //
 // fp32 operands are three bf16 terms each, of whose products the six that matter
 // are taken, smallest first; the accumulator, which cuts instead of rounding, is
@@ -38,12 +42,13 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kStages = 5;
-constexpr int kBox = 64 * 128;                     // bytes of a box
+constexpr int kBox = 64 * 128;                     // bytes of 64 rows of 64 columns
 constexpr int kOperand = 2 * kBox;                 // A's or B's share of a stage
 constexpr int kStage = 2 * kOperand;
 constexpr int kResult = 32 * 128;                  // a box of results
 constexpr int kStaging = 2 * kResult;              // two for each warp
 constexpr int kAccCols = 256;
+constexpr uint32_t kPolls = 1u << 20;                // of a wait (seconds)
 constexpr int kChunk = 2;                          // K stages between read-outs (fp32)
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStaging + 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -88,6 +93,25 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, 
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                          int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+// 64 rows by 128 columns from (row, column) on, the columns by 64: one box, or
+// two where the rows of the user's array are not whole blocks of 64.
+__device__ __forceinline__ void pair_load_rows(uint32_t dst, const CUtensorMap* map, int col,
+                                               int term, int row, int two, uint32_t bar) {
+  if (two) {
+    pair_load(dst, map, col, term, row, bar);
+    pair_load(dst + kBox, map, col + 64, term, row, bar);
+  } else {
+    pair_load(dst, map, 0, row, col >> 6, term, bar);
+  }
 }
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -173,7 +197,10 @@ __device__ __forceinline__ int pieces_tiles(const XentMma& a, int piece) {
   return (min(left, a.piece) + kXtN - 1) / kXtN;
 }
 
-__device__ void make_plan(const XentMma& a, int n, Plan* p) {
+// (By a warp: a thread's loop over the pairs took 6 us.)
+__device__ void make_plan(const XentMma& a, int n, Plan* to) {
+  const int lane = threadIdx.x & 31;
+  Plan mine, *p = &mine;
   p->pairs = gridDim.x >> 1;
   p->pair = blockIdx.x >> 1;
   p->mt = (n + kXtM - 1) / kXtM;
@@ -186,6 +213,7 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
     p->vt = ((a.V + kXtN - 1) / kXtN + a.run - 1) / a.run;
     p->by = p->pairs / max(p->mt, 1);
     p->rest = p->pairs % max(p->mt, 1);
+    if (lane == 0) *to = mine;
     return;
   }
   p->by = p->pairs / p->nt;
@@ -206,23 +234,34 @@ __device__ void make_plan(const XentMma& a, int n, Plan* p) {
     nl = p->mt * p->vt;
   }
   p->w1 = nw;
+  // DW's tiles go round; of DX's and then D's each pair takes so many as bring it
+  // up to the average.  In integers: pair j's end is pair j + 1's beginning.
   const float cw = (float)max(p->tk, 1), cl = (float)(p->dk + 2);
   const float tx = (nw * cw + (float)nx * cx) / p->pairs;
-  const float tl = (nw * cw + (float)nx * cx + nl * cl) / p->pairs;
-  float ax = 0.f, al = 0.f;
-  int x1 = 0, l1 = 0;
-  for (int j = 0; j <= p->pair; ++j) {
-    float load = (nw / p->pairs + (j < nw % p->pairs)) * cw;
-    p->x0 = x1;
-    ax += fmaxf(0.f, tx - load) / cx;
-    x1 = j == p->pairs - 1 ? nx : min(nx, (int)(ax + 0.5f));
-    load += (float)(x1 - p->x0) * cx;
-    p->l0 = l1;
-    al += fmaxf(0.f, tl - load) / cl;
-    l1 = j == p->pairs - 1 ? nl : min(nl, (int)(al + 0.5f));
-  }
-  p->x1 = x1;
-  p->l1 = l1;
+  const float tl = tx + nl * cl / p->pairs;
+  const int each = nw / p->pairs, more = nw % p->pairs;
+  const long long x_more = (long long)(fmaxf(0.f, tx - (each + 1) * cw) / cx * 65536.f);
+  const long long x_less = (long long)(fmaxf(0.f, tx - each * cw) / cx * 65536.f);
+  auto x_at = [&](int j) {
+    if (j == p->pairs) return nx;
+    const long long v = min(j, more) * x_more + max(0, j - more) * x_less + 32768;
+    return (int)min((long long)nx, v >> 16);
+  };
+  auto share = [&](int j) {
+    const float load = (each + (j < more)) * cw + (float)(x_at(j + 1) - x_at(j)) * cx;
+    return (long long)(fmaxf(0.f, tl - load) / cl * 65536.f);
+  };
+  long long before = 0;
+  for (int j = lane; j < p->pair; j += 32) before += share(j);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  p->x0 = x_at(p->pair);
+  p->x1 = x_at(p->pair + 1);
+  p->l0 = (int)min((long long)nl, (before + 32768) >> 16);
+  p->l1 = p->pair + 1 == p->pairs
+              ? nl
+              : (int)min((long long)nl, (before + share(p->pair) + 32768) >> 16);
+  if (lane == 0) *to = mine;
 }
 
 // This pair's tiles, one after another.  A role's next tile costs it a few
@@ -372,7 +411,9 @@ template <bool F32>
 __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p, const Smem& s,
                           int direct, uint32_t rank) {
   const CUtensorMap* mx = direct ? &maps.x : &maps.xp;
-  uint32_t limit = kMaxPolls;
+  const CUtensorMap* mxr = direct ? &maps.xr : &maps.xpr;
+  const int two_x = direct && a.D % 64, two_w = a.two_w;
+  uint32_t limit = kPolls;
   const uint32_t full0 = of_first(s.full);
   int g = 0, st = 0;
   uint32_t phase = 1;                              // (a fresh barrier's phase ahead is over)
@@ -380,9 +421,9 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
   cur.start(a, p);
   while (limit && cur.next(a, p)) {
     const Tile t = cur.t;
-    const int half = t.N >> 1, nb = half >> 6;     // B columns of this CTA, boxes of them
-    const uint32_t bytes = 2 * (kOperand + nb * kBox);
-    const int ar = t.m0 + (int)rank * 128, br = t.n0 + (int)rank * half;
+    // This CTA's rows of A and columns of B (a copy of B is always 128 of them,
+    // whether the tile has use for all or not).
+    const int ar = t.m0 + (int)rank * 128, br = t.n0 + (int)rank * (t.N >> 1);
     each_stage<F32>(t.steps, [&](int k, int ta, int tb, int) {
       mbar_poll(s.empty + 8 * st, phase, limit);
       if (!limit) return;
@@ -390,26 +431,18 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
       if (rank == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
                          s.full + 8 * st),
-                     "r"(bytes)
+                     "r"(2 * kStage)
                      : "memory");
       const int kk = (t.k0 + k) * kXtK;
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t to = dst + b * kBox;
-        if (t.kind <= DLOG)
-          pair_load(to, mx, kk, ta, ar + 64 * b, full);
-        else if (t.kind == DX)
-          pair_load(to, &maps.d, kk, ta, t.drow + ar + 64 * b, full);
-        else
-          pair_load(to, &maps.d, ar + 64 * b, ta, t.drow + kk, full);
-      }
-      for (int b = 0; b < nb; ++b) {
-        const uint32_t to = dst + kOperand + b * kBox;
-        if (t.kind <= DLOG)
-          pair_load(to, &maps.w, kk, tb, t.v0 + br + 64 * b, full);
-        else if (t.kind == DX)
-          pair_load(to, &maps.w, br + 64 * b, tb, t.v0 + kk, full);
-        else
-          pair_load(to, mx, br + 64 * b, tb, kk, full);
+      if (t.kind <= DLOG) {
+        pair_load(dst, mx, kk, ta, ar, full);
+        pair_load(dst + kOperand, &maps.w, kk, tb, t.v0 + br, full);
+      } else if (t.kind == DX) {
+        pair_load(dst, &maps.d, kk, ta, t.drow + ar, full);
+        pair_load_rows(dst + kOperand, &maps.wr, br, tb, t.v0 + kk, two_w, full);
+      } else {
+        pair_load_rows(dst, &maps.dr, ar, ta, t.drow + kk, 0, full);
+        pair_load_rows(dst + kOperand, mxr, br, tb, kk, two_x, full);
       }
       ++g;
       if (++st == kStages) {
@@ -431,7 +464,7 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
 
 template <bool F32>
 __device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_t tmem) {
-  uint32_t limit = kMaxPolls;
+  uint32_t limit = kPolls;
   int st = 0, u = 0;                               // stage; accumulators used
   uint32_t phase = 0;
   const uint64_t base = ((uint64_t)1 << 46) | ((uint64_t)2 << 61) | ((uint64_t)(1024 >> 4) << 32);
@@ -521,7 +554,7 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
   const uint32_t other = 2 * box + kResult;
   const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
   const uint32_t give = of_first(s.tempty);
-  uint32_t limit = kMaxPolls;
+  uint32_t limit = kPolls;
   int u = 0;
   float mx = -INFINITY, sum = 0.f;                 // LSE: of the run so far
   Cursor cur;
@@ -776,7 +809,7 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
   if (warp == 2) pair_alloc(smem_addr(&tslot), 2 * kAccCols);
   pdl_wait();
   const int n = __ldcg(a.count), direct = __ldcg(a.count + 1);
-  if (threadIdx.x == 0) make_plan(a, n, &plan);
+  if (warp == 3) make_plan(a, n, &plan);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -796,7 +829,7 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
-    uint32_t limit = kMaxPolls;
+    uint32_t limit = kPolls;
     mbar_poll(s.done, 0, limit);
     __syncwarp();
     tc_fence_after();

@@ -10,13 +10,16 @@ constexpr int kXtM = 256;                // rows of a tile (a pair of CTAs)
 constexpr int kXtN = 256;                // its columns
 constexpr int kXtK = 64;                 // K of a stage: 128 bytes of bf16
 
-// Operands and results as tensors of bf16 terms (one, or three of fp32 values):
-// [row][term][column], boxes of 64 columns by 64 rows; results by 32 rows.
+// Operands and results as tensors of bf16 terms (one, or three of fp32 values),
+// [row][term][column], in boxes of 64 columns by 128 rows; "r": by rows, as
+// (64 columns, row, block of 64 columns, term) in boxes of 64 by 64 rows by two
+// blocks (where the user's rows are not whole blocks: as the others, 64 rows a
+// box).  Results by 32 rows.
 struct XentMaps {
-  CUtensorMap x;                         // X itself (bf16 rows on 16-byte boundaries)
-  CUtensorMap xp;                        // the list's rows of X
-  CUtensorMap w;                         // W
-  CUtensorMap d;                         // d of two pieces, one after the other
+  CUtensorMap x, xr;                     // X itself (bf16 rows on 16-byte boundaries)
+  CUtensorMap xp, xpr;                   // the list's rows of X
+  CUtensorMap w, wr;                     // W
+  CUtensorMap d, dr;                     // d of two pieces, one after the other
   CUtensorMap ds;                        // the same, for stores
   CUtensorMap acc;                       // dX in fp32: slices of rows of the list
   CUtensorMap dw;                        // dW
@@ -40,6 +43,7 @@ struct XentMma {
   int run;
   int dw_piece, dx_piece, d_piece;       // pieces to work on, -1: none
   int acc_tiles;                         // row tiles that dX's slices have room for
+  int two_w;                             // wr takes two boxes
   int first, dw_tma;                     // dx_piece is the first; dW's rows fit a tensor map
   int ld;                                // part's rows
   const int* count;                      // [0] rows of the list, [1] 1: it is X itself
@@ -60,5 +64,11 @@ cudaError_t launch_xent_mma(const XentMaps& maps, const XentMma& a, int dtype, i
 bool encode_map_planes_sw128(CUtensorMap* map, const void* base, bool f32, unsigned long long width,
                              unsigned long long planes, unsigned long long rows,
                              unsigned long long row_bytes, unsigned int box_rows);
+
+// The same rows as (64 columns, row, block of 64 columns, plane), width a multiple
+// of 64, boxes of 64 rows by two blocks.
+bool encode_map_blocks_sw128(CUtensorMap* map, const void* base, unsigned long long width,
+                             unsigned long long planes, unsigned long long rows,
+                             unsigned long long row_bytes);
 
 }  // namespace cat
