@@ -100,15 +100,11 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
   int* h = hist + warp * range;
   int below = 0;
   bool bad = false;
-  // Eight steps' ids are on their way at once.
+  const long long end = min((long long)tokens, t0 + 32ll * steps);
   auto each = [&](auto f) {
     for (int s0 = 0; s0 < steps; s0 += 8) {
       int id[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const long long t = t0 + 32 * (s0 + u) + lane;
-        id[u] = s0 + u < steps && t < tokens ? id_at(ids, t, V) : -1;
-      }
+      ids_at<8>(ids, t0 + 32 * s0 + lane, 32, end, V, id);
 #pragma unroll
       for (int u = 0; u < 8; ++u) f((int)(t0 + 32 * (s0 + u) + lane), id[u]);
     }

@@ -20,4 +20,24 @@ __device__ __forceinline__ int id_at(const Ids& ids, long long i, int vocab) {
   return v < 0 ? -1 : v >= vocab ? -2 : v;
 }
 
+// U ids at i, i + step, .. (-1 from n on), all loads on their way at once.
+template <int U>
+__device__ __forceinline__ void ids_at(const Ids& ids, long long i, int step, long long n,
+                                       int vocab, int (&id)[U]) {
+  if (ids.wide) {
+    long long v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = i + u * step < n ? __ldg(static_cast<const long long*>(ids.p) + i + u * step) : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = v[u] < 0 ? -1 : v[u] >= vocab ? -2 : (int)v[u];
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      id[u] = i + u * step < n ? __ldg(static_cast<const int*>(ids.p) + i + u * step) : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = id[u] < 0 ? -1 : id[u] >= vocab ? -2 : id[u];
+  }
+}
+
 }  // namespace cat

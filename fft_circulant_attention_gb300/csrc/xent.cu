@@ -85,11 +85,7 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
   // (Sixteen ids on their way at once: a CTA has the whole list to look through.)
   for (int i0 = 0; i0 < p.tokens; i0 += 16 * kThreads) {
     int id[16];
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const int i = i0 + u * kThreads + threadIdx.x;
-      id[u] = i < p.tokens ? id_at(p.targets, i, p.V) : -1;
-    }
+    ids_at<16>(p.targets, i0 + threadIdx.x, kThreads, p.tokens, p.V, id);
 #pragma unroll
     for (int u = 0; u < 16; ++u) {
       const int held = id[u] >= 0;
@@ -393,6 +389,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.stat = c.stat;
   k.hit = c.hit;
   k.part = c.part;
+  k.d = c.d;
   k.dw = a.dw;
   k.two_w = !c.pack && p->D % 64;
   k.dw_tma = p->D % (f32 ? 4 : 8) == 0;

@@ -174,6 +174,12 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, 
                : "memory");
 }
 
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // One tile of a launch.
 struct Tile {
   int kind, m0, n0, N;                             // rows and columns of the result
@@ -187,7 +193,7 @@ struct Tile {
 struct Plan {
   int mt, nt, vt;                                  // tiles of rows, of D, of a piece (run)
   int dk, tk, pk;                                  // K stages of D, of the list, of a piece
-  int w1, x0, x1, l0, l1;                          // DW (every pairs-th), DX, D tiles
+  int w1, x1, l0, l1;                              // DW and DX (every pairs-th), D tiles
   int pairs, pair;
   int by, rest;                                    // pairs over a row of strided tiles
 };
@@ -207,7 +213,7 @@ __device__ void make_plan(const XentMma& a, int n, Plan* to) {
   p->nt = (a.D + kXtN - 1) / kXtN;
   p->dk = (a.D + kXtK - 1) / kXtK;
   p->tk = (n + kXtK - 1) / kXtK;
-  p->w1 = p->x0 = p->x1 = p->l0 = p->l1 = 0;
+  p->w1 = p->x1 = p->l0 = p->l1 = 0;
   p->vt = p->pk = 0;
   if (a.lse) {
     p->vt = ((a.V + kXtN - 1) / kXtN + a.run - 1) / a.run;
@@ -234,29 +240,23 @@ __device__ void make_plan(const XentMma& a, int n, Plan* to) {
     nl = p->mt * p->vt;
   }
   p->w1 = nw;
-  // DW's tiles go round; of DX's and then D's each pair takes so many as bring it
-  // up to the average.  In integers: pair j's end is pair j + 1's beginning.
+  p->x1 = nw + nx;
+  // DW's and DX's tiles go round, so that tiles that read the same rows or columns
+  // of d run side by side (of tiles one after another a pair read d again from
+  // memory for each); of D's each pair takes so many as bring it up to the
+  // average.  In integers: pair j's end is pair j + 1's beginning.
   const float cw = (float)max(p->tk, 1), cl = (float)(p->dk + 2);
-  const float tx = (nw * cw + (float)nx * cx) / p->pairs;
-  const float tl = tx + nl * cl / p->pairs;
-  const int each = nw / p->pairs, more = nw % p->pairs;
-  const long long x_more = (long long)(fmaxf(0.f, tx - (each + 1) * cw) / cx * 65536.f);
-  const long long x_less = (long long)(fmaxf(0.f, tx - each * cw) / cx * 65536.f);
-  auto x_at = [&](int j) {
-    if (j == p->pairs) return nx;
-    const long long v = min(j, more) * x_more + max(0, j - more) * x_less + 32768;
-    return (int)min((long long)nx, v >> 16);
-  };
+  const float tl = (nw * cw + (float)nx * cx + nl * cl) / p->pairs;
+  auto below = [&](int j, int n) { return n > j ? (n - j - 1) / p->pairs + 1 : 0; };
   auto share = [&](int j) {
-    const float load = (each + (j < more)) * cw + (float)(x_at(j + 1) - x_at(j)) * cx;
+    const int w = below(j, nw);
+    const float load = w * cw + (float)(below(j, nw + nx) - w) * cx;
     return (long long)(fmaxf(0.f, tl - load) / cl * 65536.f);
   };
   long long before = 0;
   for (int j = lane; j < p->pair; j += 32) before += share(j);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  p->x0 = x_at(p->pair);
-  p->x1 = x_at(p->pair + 1);
   p->l0 = (int)min((long long)nl, (before + 32768) >> 16);
   p->l1 = p->pair + 1 == p->pairs
               ? nl
@@ -283,7 +283,6 @@ struct Cursor {
     } else {
       kind = DW;
       i = p.pair;
-      end = p.w1;
       y = i / p.nt;
       x = i % p.nt;
     }
@@ -312,53 +311,43 @@ struct Cursor {
       }
       return true;
     }
-    if (kind == DW) {
-      if (i < end) {
-        t.kind = DW;
+    if (kind != DLOG && i < p.x1) {
+      if (kind == DW && i >= p.w1) {
+        kind = DX;
+        const int j = i - p.w1, tiles = p.mt * p.nt;
+        r = j / tiles;                             // slice
+        y = (j - r * tiles) / p.nt;
+        x = j - r * tiles - y * p.nt;
+      }
+      t.kind = kind;
+      t.m0 = y * kXtM;
+      t.n0 = x * kXtN;
+      t.N = a.D - t.n0 > kXtN / 2 ? kXtN : kXtN / 2;
+      if (kind == DW) {
         t.v0 = a.dw_piece * a.piece;
         t.drow = (a.dw_piece & 1) * a.rows;
-        t.m0 = y * kXtM;
-        t.n0 = x * kXtN;
         t.steps = p.tk;
-        t.N = a.D - t.n0 > kXtN / 2 ? kXtN : kXtN / 2;
-        i += p.pairs;
-        y += p.by;
-        x += p.rest;
-        if (x >= p.nt) {
-          x -= p.nt;
-          ++y;
-        }
-        return true;
-      }
-      kind = DX;
-      i = p.x0;
-      end = p.x1;
-      const int tiles = max(p.mt * p.nt, 1);
-      r = i / tiles;                               // slice
-      y = (i - r * tiles) / p.nt;
-      x = i - r * tiles - y * p.nt;
-    }
-    if (kind == DX) {
-      if (i < end) {
-        t.kind = DX;
+      } else {
         t.v0 = a.dx_piece * a.piece;
         t.drow = (a.dx_piece & 1) * a.rows;
-        t.m0 = y * kXtM;
-        t.n0 = x * kXtN;
         t.k0 = r * p.pk;
         t.steps = max(0, min(p.pk, pieces_tiles(a, a.dx_piece) * (kXtN / kXtK) - t.k0));
         t.arow = r * p.mt * kXtM;
-        t.N = a.D - t.n0 > kXtN / 2 ? kXtN : kXtN / 2;
-        ++i;
-        if (++x == p.nt) {
-          x = 0;
-          if (++y == p.mt) {
-            y = 0;
-            ++r;
-          }
-        }
-        return true;
       }
+      i += p.pairs;
+      y += p.by;
+      x += p.rest;
+      if (x >= p.nt) {
+        x -= p.nt;
+        ++y;
+      }
+      while (kind == DX && y >= p.mt) {
+        y -= p.mt;
+        ++r;
+      }
+      return true;
+    }
+    if (kind != DLOG) {
       kind = DLOG;
       i = p.l0;
       end = p.l1;
@@ -705,6 +694,20 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
         if (!__all_sync(0xffffffffu, live)) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = live ? v[i] : 0.f;
+        }
+        if (!F32) {
+          // Past shared memory, which the products' operands keep busy: a lane's
+          // 128 bytes of its row, 32 at a time.
+          uint32_t* to = static_cast<uint32_t*>(a.d) +
+                         ((size_t)(t.drow + row) * a.piece + col) / 2;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = pack2(v[16 * j + 2 * i], v[16 * j + 2 * i + 1]);
+            st_global32(to + 8 * j, h);
+          }
+          continue;
         }
 #pragma unroll
         for (int term = 0; term < (F32 ? 3 : 1); ++term) {

@@ -53,6 +53,7 @@ struct XentMma {
   const float2* stat;
   float* hit;
   float2* part;
+  void* d;
   void* dw;
   unsigned int* status;
 };
