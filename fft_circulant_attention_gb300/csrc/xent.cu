@@ -343,7 +343,6 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
   const unsigned long long db = (unsigned long long)c.terms * c.piece * 2;
   const unsigned long long drows = (unsigned long long)c.rows_alloc * (c.pieces > 1 ? 2 : 1);
   ok = both(&m->d, &m->dr, c.d, c.piece, c.terms, drows, db) &&
-       encode_map_planes_sw128(&m->ds, c.d, false, c.piece, c.terms, drows, db, 32) &&
        encode_map_planes_sw128(&m->acc, c.dxacc, true, D, 1, (unsigned long long)c.acc_tiles * kXtM,
                                (unsigned long long)c.acc_pitch * 4, 32);
   const bool f32 = p->dtype == CAT_F32;

@@ -515,23 +515,25 @@ __device__ __forceinline__ void stage_f32(uint32_t box, int lane, const float* v
 }
 
 // Logits that are not finite, again by their definition: an infinity is lost in
-// the products of its terms (0 times it, or a difference).  The warp's lanes
-// with such a value, one after another; x: the lane's row, w: the column's.
-__device__ __noinline__ float exact_logit(float v, const float* x, const float* w, int D,
+// the products of its terms (0 times it, or a difference).  n columns' values of
+// each lane's row (v, in local memory); the warp's lanes with such a value, one
+// after another; x: the lane's row, w: the first column's.
+__device__ __noinline__ void exact_logits(float* v, int n, const float* x, const float* w, int D,
                                           bool live) {
   const int lane = threadIdx.x & 31;
-  unsigned left = __ballot_sync(0xffffffffu, live && !(fabsf(v) < INFINITY));
-  while (left) {
-    const int src = __ffs(left) - 1;
-    left &= left - 1;
-    const float* row = reinterpret_cast<const float*>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), src));
-    float sum = 0.f;
-    for (int k = lane; k < D; k += 32) sum = fmaf(__ldg(row + k), __ldg(w + k), sum);
-    sum = warp_sum(sum);
-    if (lane == src) v = sum;
+  for (int i = 0; i < n; ++i, w += D) {
+    unsigned left = __ballot_sync(0xffffffffu, live && !(fabsf(v[i]) < INFINITY));
+    while (left) {
+      const int src = __ffs(left) - 1;
+      left &= left - 1;
+      const float* row = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), src));
+      float sum = 0.f;
+      for (int k = lane; k < D; k += 32) sum = fmaf(__ldg(row + k), __ldg(w + k), sum);
+      sum = warp_sum(sum);
+      if (lane == src) v[i] = sum;
+    }
   }
-  return v;
 }
 
 template <bool F32>
@@ -644,11 +646,15 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
 #pragma unroll
           for (int i = 0; i < 64; ++i) fine = fine && fabsf(v[i]) < INFINITY;
           if (__any_sync(0xffffffffu, live && !fine)) {
-            const float* x = static_cast<const float*>(a.x) + (live ? (size_t)a.rows_of[row] * a.D : 0);
-            const float* w = static_cast<const float*>(a.w) + (size_t)(t.v0 + col) * a.D;
+            float apart[64];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i < left) v[i] = exact_logit(v[i], x, w + (size_t)i * a.D, a.D, live);
+            for (int i = 0; i < 64; ++i) apart[i] = v[i];
+            exact_logits(apart, min(left, 64),
+                         static_cast<const float*>(a.x) +
+                             (live ? (size_t)a.rows_of[row] * a.D : 0),
+                         static_cast<const float*>(a.w) + (size_t)(t.v0 + col) * a.D, a.D, live);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = apart[i];
           }
         }
         if (left < 64) {
@@ -695,33 +701,28 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = live ? v[i] : 0.f;
         }
-        if (!F32) {
-          // Past shared memory, which the products' operands keep busy: a lane's
-          // 128 bytes of its row, 32 at a time.
-          uint32_t* to = static_cast<uint32_t*>(a.d) +
-                         ((size_t)(t.drow + row) * a.piece + col) / 2;
+        // Past shared memory, which the products' operands keep busy: a lane's 64
+        // values of its row, 32 bytes at a time, a term after another.
+        uint32_t* to = static_cast<uint32_t*>(a.d) +
+                       ((size_t)(t.drow + row) * (F32 ? 3 : 1) * a.piece + col) / 2;
+#pragma unroll
+        for (int term = 0; term < (F32 ? 3 : 1); ++term) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t h[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = pack2(v[16 * j + 2 * i], v[16 * j + 2 * i + 1]);
+            for (int i = 0; i < 8; ++i) {
+              float& x = v[16 * j + 2 * i];
+              float& y = v[16 * j + 2 * i + 1];
+              h[i] = pack2(x, y);
+              if (F32 && term < 2) {
+                x -= __uint_as_float(h[i] << 16);
+                y -= __uint_as_float(h[i] & 0xffff0000u);
+              }
+            }
             st_global32(to + 8 * j, h);
           }
-          continue;
-        }
-#pragma unroll
-        for (int term = 0; term < (F32 ? 3 : 1); ++term) {
-          box_free();
-          stage_bf16(box, lane, v);
-          box_full();
-          if (lane == 0) {
-            store_box(&maps.ds, box, col, term, t.drow + r0);
-            stores_commit();
-          }
-          if (F32 && term < 2) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
-          }
+          to += a.piece / 2;
         }
       } else if (t.kind == DX) {
 #pragma unroll
@@ -818,14 +819,19 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tslot;
-  if (warp == 0) {
-    if (elect_one()) {
+  // fp32 sums take 128 registers of a thread that reads results: 224 for those
+  // warps, 56 for the others (together the 168 of each that the CTA starts with).
+  // Spilled ones would go through the memory that feeds the products.
+  if (warp < 4) {
+    if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && elect_one()) {
       asm volatile("fence.proxy.async;" ::: "memory");   // (rows that kernels ahead wrote)
       copy_role<F32>(maps, a, plan, s, direct, rank);
+    } else if (warp == 1 && rank == 0 && elect_one()) {
+      mma_role<F32>(a, plan, s, tmem);
     }
-  } else if (warp == 1) {
-    if (rank == 0 && elect_one()) mma_role<F32>(a, plan, s, tmem);
-  } else if (warp >= 4) {
+  } else {
+    if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     result_role<F32>(maps, a, plan, s, tmem, n, rank);
   }
   __syncwarp();

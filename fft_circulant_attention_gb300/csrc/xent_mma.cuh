@@ -20,7 +20,6 @@ struct XentMaps {
   CUtensorMap xp, xpr;                   // the list's rows of X
   CUtensorMap w, wr;                     // W
   CUtensorMap d, dr;                     // d of two pieces, one after the other
-  CUtensorMap ds;                        // the same, for stores
   CUtensorMap acc;                       // dX in fp32: slices of rows of the list
   CUtensorMap dw;                        // dW
 };
