@@ -11,10 +11,11 @@
 //          of its own by warp (each warp has a stretch of the tokens), and puts
 //          its tokens in place, in order.  No CTA waits for another.
 //   sum:   the sorted list in pieces of equal length, a group of threads each; a
-//          run of equal ids within a piece is a finished row, a run that crosses
-//          pieces leaves partial rows (fp32).  Beside it the rows without tokens
-//          are cleared.
-//   join:  the partial rows of each run that crosses pieces, first piece first.
+//          run of equal ids that is no longer than a piece belongs to the piece it
+//          starts in and is a finished row, a longer one leaves a partial row
+//          (fp32) in each piece it touches.  Beside it the rows without tokens are
+//          cleared.
+//   join:  the partial rows of each long run, in a fixed order.
 #include "cat_internal.h"
 #include "ids.cuh"
 #include "rows.cuh"
@@ -28,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRange = 1024;        // most ids of a sorting CTA
+constexpr int kSeen = 16;
 constexpr int kZeroRows = 64;           // ids whose rows a clearing CTA looks at
 constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
 
@@ -40,21 +42,37 @@ embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens
   const int nv = D / VEC;
   const int row0 = blockIdx.x * per;
   const int n = min(per, tokens - row0) * nv;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int r = i / nv, c = (i - r * nv) * VEC, row = row0 + r;
-    const int id = id_at(ids, row, V);
-    float v[VEC];
-    if (id >= 0) {
-      load<T, VEC>(W + (size_t)id * D + c, v);
+  constexpr int U = 4;                          // vectors on their way at once
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    int id[U];
+    typename Vc::Raw raw[U];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] *= scale;
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = 0.f;
-      if (id == -2 && c == 0) report(status, 0x701);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      id[u] = i < n ? id_at(ids, row0 + i / nv, V) : -1;
     }
-    Vc::st(Y + (size_t)row * D + c, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (id[u] >= 0) raw[u] = Vc::ldr(W + (size_t)id[u] * D + (i - i / nv * nv) * VEC);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= n) break;
+      const int r = i / nv, c = (i - r * nv) * VEC;
+      float v[VEC];
+      if (id[u] >= 0) {
+        Vc::widen(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] *= scale;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+        if (id[u] == -2 && c == 0) report(status, 0x701);
+      }
+      Vc::st(Y + (size_t)(row0 + r) * D + c, v);
+    }
   }
 }
 
@@ -90,72 +108,89 @@ embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first
                   int* __restrict__ order, int* __restrict__ sid, unsigned int* status) {
   extern __shared__ int hist[];                 // [kSortWarps][range]
   __shared__ int red[kSortWarps];
+  __shared__ unsigned seen[kSortWarps][kSeen];  // which steps held tokens of this range
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lo = blockIdx.x * range, n = min(range, V - lo);
+  const unsigned lo = blockIdx.x * range, n = min((unsigned)range, V - lo);
   for (int i = threadIdx.x; i < kSortWarps * range; i += kSortThreads) hist[i] = 0;
+  for (int i = lane; i < kSeen; i += 32) seen[warp][i] = 0;
   __syncthreads();
-  // This warp's stretch of the tokens.
+  // This warp's stretch of the tokens, 32 a step, eight steps on their way at once.
   const int steps = (tokens + 32 * kSortWarps - 1) / (32 * kSortWarps);
   const long long t0 = (long long)warp * steps * 32;
+  const long long end = min((long long)tokens, t0 + 32ll * steps);
+  int shift = 3;                                // a bit of `seen`: 8 steps, or more
+  while ((steps >> shift) >= 32 * kSeen) ++shift;
   int* h = hist + warp * range;
   int below = 0;
   bool bad = false;
-  const long long end = min((long long)tokens, t0 + 32ll * steps);
-  auto each = [&](auto f) {
-    for (int s0 = 0; s0 < steps; s0 += 8) {
-      int id[8];
-      ids_at<8>(ids, t0 + 32 * s0 + lane, 32, end, V, id);
+  for (int s0 = 0; s0 < steps; s0 += 8) {
+    unsigned key[8];
+    keys_at<8>(ids, t0 + 32 * s0 + lane, 32, end, key);
+    unsigned found = 0;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) f((int)(t0 + 32 * (s0 + u) + lane), id[u]);
-    }
-  };
-  each([&](int, int id) {
-    bad |= id == -2;
-    below += id >= 0 && id < lo;
-    const bool mine = id >= lo && id < lo + n;
-    const unsigned any = __ballot_sync(0xffffffffu, mine);
-    if (any) {
-      if (mine) {
-        const unsigned same = __match_any_sync(any, id);
-        if (lane == __ffs(same) - 1) h[id - lo] += __popc(same);
+    for (int u = 0; u < 8; ++u) {
+      below += key[u] < lo;
+      if (blockIdx.x == 0) bad |= id_of(key[u], V) == -2;
+      const bool mine = key[u] - lo < n;
+      const unsigned any = __ballot_sync(0xffffffffu, mine);
+      found |= any;
+      if (any) {
+        if (mine) {
+          const unsigned same = __match_any_sync(any, key[u]);
+          if (lane == __ffs(same) - 1) h[key[u] - lo] += __popc(same);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-  });
-  if (bad && blockIdx.x == 0) report(status, 0x702);
+    const int bit = s0 >> shift;
+    if (found && lane == 0) seen[warp][bit >> 5] |= 1u << (bit & 31);
+  }
+  if (bad) report(status, 0x702);
   __syncthreads();
   int base, count = 0, own;
   block_scan(below, red, &base);
   __syncthreads();
-  for (int w = 0; (int)threadIdx.x < n && w < kSortWarps; ++w) count += hist[w * range + threadIdx.x];
+  if (threadIdx.x < n) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) count += hist[w * range + threadIdx.x];
+  }
   int at = base + block_scan(count, red, &own);
-  if ((int)threadIdx.x < n) {
+  if (threadIdx.x < n) {
     first[lo + threadIdx.x] = at;
+#pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = hist[w * range + threadIdx.x];
       hist[w * range + threadIdx.x] = at;
       at += c;
     }
   }
-  if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
+  if (threadIdx.x == 0 && lo + n == (unsigned)V) first[V] = base + own;
   __syncthreads();
   if (own == 0) return;
-  each([&](int t, int id) {
-    const bool mine = id >= lo && id < lo + n;
-    const unsigned any = __ballot_sync(0xffffffffu, mine);
-    if (any) {
-      if (mine) {
-        const unsigned same = __match_any_sync(any, id);
-        const int start = h[id - lo];
-        const int pos = start + __popc(same & ((1u << lane) - 1));
-        order[pos] = t;
-        sid[pos] = id;
-        __syncwarp(any);
-        if (lane == __ffs(same) - 1) h[id - lo] = start + __popc(same);
+  // Again over the steps with tokens of this range: their places, in order.
+  for (int s0 = 0; s0 < steps; s0 += 8) {
+    const int bit = s0 >> shift;
+    if (!(seen[warp][bit >> 5] >> (bit & 31) & 1)) continue;
+    unsigned key[8];
+    keys_at<8>(ids, t0 + 32 * s0 + lane, 32, end, key);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool mine = key[u] - lo < n;
+      const unsigned any = __ballot_sync(0xffffffffu, mine);
+      if (any) {
+        if (mine) {
+          const unsigned same = __match_any_sync(any, key[u]);
+          const int start = h[key[u] - lo];
+          const int pos = start + __popc(same & ((1u << lane) - 1));
+          order[pos] = (int)(t0 + 32 * (s0 + u) + lane);
+          sid[pos] = (int)key[u];
+          __syncwarp(any);
+          if (lane == __ffs(same) - 1) h[key[u] - lo] = start + __popc(same);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-  });
+  }
 }
 
 // dst = scale·acc, or dst + scale·acc.
@@ -187,19 +222,35 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   const bool in = c < D;
   pdl_wait();
   if ((int)blockIdx.x >= piece_ctas) {
+    __shared__ int none[kZeroRows];
     const int v0 = (blockIdx.x - piece_ctas) * kZeroRows;
+    if (threadIdx.x < kZeroRows) {
+      const int v = v0 + threadIdx.x;
+      none[threadIdx.x] = v < V && __ldcg(first + v) == __ldcg(first + v + 1);
+    }
+    __syncthreads();
     float z[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) z[e] = 0.f;
-    for (int v = v0 + threadIdx.x / TPR; v < min(V, v0 + kZeroRows); v += kGroups)
-      if (in && __ldcg(first + v) == __ldcg(first + v + 1)) Vc::st(dW + (size_t)v * D + c, z);
+    for (int r = threadIdx.x / TPR; r < kZeroRows; r += kGroups)
+      if (in && none[r]) Vc::st(dW + (size_t)(v0 + r) * D + c, z);
     return;
   }
   const int piece = blockIdx.x * kGroups + threadIdx.x / TPR;
   const int total = __ldcg(first + V);
   const long long q0 = (long long)piece * P;
   if (q0 >= total) return;
-  const int p0 = (int)q0, p1 = (int)min((long long)total, q0 + P);
+  int p0 = (int)q0, p1 = (int)min((long long)total, q0 + P);
+  // Runs of the ids at both ends of the piece.  A short one that starts ahead is
+  // the piece ahead's, one that goes on behind is taken to its end here; of a long
+  // one the places of this piece.
+  const int ida = __ldcg(sid + p0), idb = __ldcg(sid + p1 - 1);
+  const int a0 = __ldcg(first + ida), a1 = __ldcg(first + ida + 1);
+  const int b0 = __ldcg(first + idb), b1 = __ldcg(first + idb + 1);
+  const bool a_long = a1 - a0 > P, b_long = b1 - b0 > P;
+  if (a0 < p0 && !a_long) p0 = a1;
+  if (b1 > p1 && !b_long) p1 = b1;
+  if (p0 >= p1) return;
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
@@ -207,11 +258,11 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   // The run of `cur` ends here (or at the piece's end).
   auto flush = [&] {
     if (in) {
-      const int a = __ldcg(first + cur), b = __ldcg(first + cur + 1);
-      if (a >= p0 && b <= p1) {
+      if (!(a_long && cur == ida) && !(b_long && cur == idb)) {
         put<T, VEC>(dW + (size_t)cur * D + c, acc, scale, add);
       } else {
-        float* q = part + ((size_t)piece * 2 + (a >= p0)) * D + c;
+        // (A piece's first partial row, or that of a run that starts in it.)
+        float* q = part + ((size_t)piece * 2 + (cur == ida && a0 < (int)q0 ? 0 : 1)) * D + c;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) q[e] = acc[e];
       }
@@ -247,10 +298,11 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   flush();
 }
 
-// A piece whose last run starts in it and goes on joins that run: a CTA, whose
-// warps add every so-many-th partial row each, the warps' sums in order then.
-// (A thread adding a column's partial rows one after another: 38 us for 16384
-// tokens, 66 pieces of the most frequent id; 5 so.)
+// The partial rows of the long runs (more than P places: one in each piece they
+// touch).  A CTA looks at 32 pieces, a lane each, for long runs that start in them,
+// and joins those one after another: its warps add every so-many-th partial row
+// each, the warps' sums in order then.  (A thread adding a column's partial rows one
+// after another: 38 us for 16384 tokens, 66 pieces of the most frequent id.)
 constexpr int kJoinWarps = kThreads / 32;
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -259,33 +311,39 @@ embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, in
   __shared__ float red[kJoinWarps][4][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int piece = blockIdx.x, total = __ldcg(first + V);
+  const int total = __ldcg(first + V), lo = blockIdx.y * 128;
+  const int piece = blockIdx.x * 32 + lane;
   const long long q0 = (long long)piece * P;
-  if (q0 + P >= total) return;
-  const int p0 = (int)q0, p1 = p0 + P;
-  const int v = __ldcg(sid + p1 - 1);
-  const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
-  if (a < p0 || b <= p1) return;
-  const int last = (b - 1) / P;
-  for (int c0 = blockIdx.y * 128; c0 < D; c0 += gridDim.y * 128) {
+  int v = -1, last = 0;
+  if (q0 + P < total) {
+    v = __ldcg(sid + q0 + P - 1);
+    const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
+    if (a < (int)q0 || b - a <= P) v = -1;
+    last = (b - 1) / P;
+  }
+  unsigned left = __ballot_sync(0xffffffffu, v >= 0);
+  while (left) {
+    const int j = __ffs(left) - 1;
+    left &= left - 1;
+    const int id = __shfl_sync(0xffffffffu, v, j), to = __shfl_sync(0xffffffffu, last, j);
+    const int from = blockIdx.x * 32 + j;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int i = piece + warp; i <= last; i += kJoinWarps) {
-      // (The run's first partial row is its piece's second.)
-      const float* q = part + ((size_t)i * 2 + (i == piece)) * D + c0 + lane;
+    for (int i = from + warp; i <= to; i += kJoinWarps) {
+      const float* q = part + ((size_t)i * 2 + (i == from)) * D + lo + lane;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c0 + 32 * e + lane < D) acc[e] += __ldcg(q + 32 * e);
+        if (lo + 32 * e + lane < D) acc[e] += __ldcg(q + 32 * e);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[warp][e][lane] = acc[e];
     __syncthreads();
-    const int e = warp, c = c0 + 32 * e + lane;
+    const int e = warp, c = lo + 32 * e + lane;
     if (e < 4 && c < D) {
       float s = red[0][e][lane];
 #pragma unroll
       for (int w = 1; w < kJoinWarps; ++w) s += red[w][e][lane];
-      put<T, 1>(dW + (size_t)v * D + c, &s, scale, add);
+      put<T, 1>(dW + (size_t)id * D + c, &s, scale, add);
     }
     __syncthreads();
   }
@@ -316,8 +374,8 @@ cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) 
       (const int*)c.first, (const int*)c.order, (const int*)c.sid, static_cast<const T*>(a.x),
       static_cast<T*>(a.y), c.part, c.V, D, P, ctas, c.scale, a.add);
   if (e != cudaSuccess || pieces < 2) return e;
-  const int blocks = (D + 127) / 128;
-  return launch_dependent(embed_join_kernel<T>, dim3(pieces, blocks < 8 ? blocks : 8),
+  return launch_dependent(embed_join_kernel<T>,
+                          dim3((pieces + 31) / 32, (D + 127) / 128),
                           dim3(kThreads), 0, st,
                           (const int*)c.first, (const int*)c.sid, (const float*)c.part,
                           static_cast<T*>(a.y), c.V, D, P, c.scale, a.add);

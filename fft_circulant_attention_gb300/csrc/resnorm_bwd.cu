@@ -46,13 +46,15 @@ __device__ __forceinline__ void sum2(float& a, float& b, float2* red, int sub, i
   }
 }
 
+constexpr int kPerSm = 2;                // most CTAs of an SM
+
 template <int TPR>
 constexpr int block_threads() {
-  return TPR > 256 ? TPR : 256;
+  return TPR > 256 ? TPR : TPR == 96 ? 480 : 256;
 }
 template <int TPR, int E>
 constexpr int per_sm() {
-  return TPR > 256 ? 1 : 2;
+  return TPR > 256 || TPR == 96 ? 1 : 2;
 }
 
 // part: [gridDim.x][kSums][D].
@@ -286,7 +288,7 @@ template <typename T, int VEC, int TPR, int E, int POST, int GATE>
 cudaError_t bwd(const ResNormArgs& a, cudaStream_t st, bool setup) {
   constexpr int BT = block_threads<TPR>();
   const int per = BT / TPR, need = (a.rows + per - 1) / per;
-  const int most = a.max_parts / 2 * per_sm<TPR, E>();
+  const int most = a.max_parts / kPerSm * per_sm<TPR, E>();
   const int grid = need < most ? need : most;
   const size_t smem = (size_t)kSums * a.D * sizeof(float);
   if (setup)
@@ -304,6 +306,7 @@ cudaError_t pick(const ResNormArgs& a, cudaStream_t st, bool setup) {
   const int D = a.D;
   if (D <= 32 * 8) return bwd<T, VEC, 32, 8, POST, GATE>(a, st, setup);
   if (D <= 64 * 8) return bwd<T, VEC, 64, 8, POST, GATE>(a, st, setup);
+  if (VEC > 1 && D <= 96 * 8) return bwd<T, VEC, 96, 8, POST, GATE>(a, st, setup);
   if (D <= 128 * 8) return bwd<T, VEC, 128, 8, POST, GATE>(a, st, setup);
   if (D <= 256 * 8) return bwd<T, VEC, 256, 8, POST, GATE>(a, st, setup);
   if (D <= 512 * 8) return bwd<T, VEC, 512, 8, POST, GATE>(a, st, setup);
@@ -321,7 +324,7 @@ cudaError_t by_post(const ResNormArgs& a, cudaStream_t st, bool setup) {
 
 }  // namespace
 
-int resnorm_parts(int sms) { return 2 * sms; }
+int resnorm_parts(int sms) { return kPerSm * sms; }
 size_t resnorm_part_count(int sms, int D) { return (size_t)resnorm_parts(sms) * kSums * D; }
 
 // One call's launches; setup: only raises its kernel's shared-memory limit.

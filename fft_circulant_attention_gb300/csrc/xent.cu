@@ -19,6 +19,8 @@ namespace cat {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPrep = 1024;              // threads of the preparing kernel
+constexpr int kPer = 128;                // tokens of a CTA of it, at least
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What the call's first kernel prepares.
@@ -37,13 +39,41 @@ struct Prep {
   unsigned int* status;
 };
 
-// `terms` bf16 terms of 8 columns from c on of a row (zeros from D on).
+// Eight columns of a row from c on (zeros from D on; src null: zeros), in vectors
+// where rows are whole ones.
+__device__ __forceinline__ void load8(const float* src, int c, int D, bool whole, float* v) {
+  if (whole && src) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(src + c));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(src + c) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = src && c + e < D ? __ldg(src + c + e) : 0.f;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* src, int c, int D, bool whole,
+                                      float* v) {
+  if (whole && src) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src + c));
+    const unsigned int w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = src && c + e < D ? ld_elem(src + c + e) : 0.f;
+}
+
+// `terms` bf16 terms of 8 columns from c on of a row.
 template <typename T>
 __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, int D, int pitch,
                                       int terms) {
   float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = src && c + e < D ? ld_elem(src + c + e) : 0.f;
+  load8(src, c, D, D % 8 == 0 && c < D, v);
   for (int t = 0; t < terms; ++t) {
     __nv_bfloat162 h[4];
 #pragma unroll
@@ -64,12 +94,12 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 // multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
 // other CTAs pack W.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
+__global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
   const int vecs = p.pitch / 8;
   if ((int)blockIdx.x >= p.list_ctas) {
     const long long n = (long long)p.V * vecs;
-    const long long step = (long long)(gridDim.x - p.list_ctas) * kThreads;
-    for (long long i = (long long)(blockIdx.x - p.list_ctas) * kThreads + threadIdx.x; i < n;
+    const long long step = (long long)(gridDim.x - p.list_ctas) * kPrep;
+    for (long long i = (long long)(blockIdx.x - p.list_ctas) * kPrep + threadIdx.x; i < n;
          i += step) {
       const long long v = i / vecs;
       pack8(static_cast<const T*>(p.w) + v * p.D,
@@ -78,19 +108,19 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
     }
     return;
   }
-  __shared__ int red[2][kThreads / 32];
+  __shared__ int red[2][kPrep / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.per, t1 = min(p.tokens, t0 + p.per);
   int before = 0, all = 0;
-  // (Sixteen ids on their way at once: a CTA has the whole list to look through.)
-  for (int i0 = 0; i0 < p.tokens; i0 += 16 * kThreads) {
-    int id[16];
-    ids_at<16>(p.targets, i0 + threadIdx.x, kThreads, p.tokens, p.V, id);
+  // (8192 ids on their way at once: a CTA has the whole list to look through.)
+  for (int i0 = 0; i0 < p.tokens; i0 += 8 * kPrep) {
+    unsigned key[8];
+    keys_at<8>(p.targets, i0 + threadIdx.x, kPrep, p.tokens, key);
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const int held = id[u] >= 0;
+    for (int u = 0; u < 8; ++u) {
+      const int held = key[u] < (unsigned)p.V;
       all += held;
-      before += i0 + u * kThreads + (int)threadIdx.x < t0 ? held : 0;
+      before += i0 + u * kPrep + (int)threadIdx.x < t0 ? held : 0;
     }
   }
 #pragma unroll
@@ -105,13 +135,13 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
   __syncthreads();
   before = all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kPrep / 32; ++w) {
     before += red[0][w];
     all += red[1][w];
   }
   const int direct = p.direct && all == p.tokens;
   int place = before;
-  for (int b = t0; b < t1; b += kThreads) {
+  for (int b = t0; b < t1; b += kPrep) {
     const int t = b + threadIdx.x;
     const int id = t < t1 ? id_at(p.targets, t, p.V) : -1;
     if (id == -2) report(p.status, 0x801);
@@ -121,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
     __syncthreads();
     int mine = place;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kPrep / 32; ++w) {
       if (w < warp) mine += red[0][w];
       place += red[0][w];
     }
@@ -148,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) xent_prepare_kernel(Prep p) {
   const bool tail = (int)blockIdx.x == p.list_ctas - 1;
   const int end = tail ? (all + 255) / 256 * 256 : place;
   const int n = (end - before) * vecs;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += kPrep) {
     const int r = i / vecs, pos = before + r;
     const T* src = pos < all ? static_cast<const T*>(p.x) + (size_t)p.rows[pos] * p.D : nullptr;
     pack8(src, static_cast<__nv_bfloat16*>(p.xp) + (size_t)pos * p.terms * p.pitch,
@@ -290,7 +320,7 @@ cudaError_t prepare(const cat_plan_s* p, const XentArgs& a, Ids targets, int tok
   Prep q = {};
   q.targets = targets;
   q.tokens = tokens;
-  q.per = tokens > 2048 * kThreads / 2 ? (tokens + 2047) / 2048 : kThreads / 2;
+  q.per = tokens > 2048 * kPer ? (tokens + 2047) / 2048 : kPer;
   q.V = c.V;
   q.D = p->D;
   q.pitch = c.pitch;
@@ -313,9 +343,9 @@ cudaError_t prepare(const cat_plan_s* p, const XentArgs& a, Ids targets, int tok
   q.stat = back ? c.stat : nullptr;
   q.status = p->status;
   const long long wv = c.pack ? (long long)c.V * (c.pitch / 8) : 0;
-  const long long need = (wv + 2 * kThreads - 1) / (2 * kThreads), most = 16ll * p->sms;
+  const long long need = (wv + kPrep - 1) / kPrep, most = 8ll * p->sms;
   const int wctas = (int)(need < most ? need : most);
-  xent_prepare_kernel<T><<<q.list_ctas + wctas, kThreads, 0, p->stream>>>(q);
+  xent_prepare_kernel<T><<<q.list_ctas + wctas, kPrep, 0, p->stream>>>(q);
   return cudaGetLastError();
 }
 
@@ -379,6 +409,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.rows = c.rows_alloc;
   k.piece = c.piece;
   k.acc_tiles = c.acc_tiles;
+  k.pairs = c.pairs;
   k.ld = c.max_tokens;
   k.count = c.count;
   k.tgt = c.tgt;
@@ -394,10 +425,16 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.dw_tma = p->D % (f32 ? 4 : 8) == 0;
   k.status = p->status;
   k.dw_piece = k.dx_piece = k.d_piece = -1;
+  // (No more pairs than there is work for.)
+  auto go = [&](long long work) {
+    const int n = work < c.pairs ? (work < 1 ? 1 : (int)work) : c.pairs;
+    return launch_xent_mma(maps, k, p->dtype, n, st);
+  };
+  const long long mt = tiles(tokens, kXtM), nt = tiles(p->D, kXtN), pt = c.piece / kXtN;
   if (!back) {
     k.lse = 1;
     k.run = run_length(c.V, tokens, c.pairs);
-    e = launch_xent_mma(maps, k, p->dtype, c.pairs, st);
+    e = go(mt * tiles(tiles(c.V, kXtN), k.run));
     if (e != cudaSuccess) return e;
     return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)),
                             dim3(32 * kFinWarps), 0, st, (const float2*)c.part, 2 * tiles(tiles(c.V, kXtN), k.run),
@@ -410,7 +447,8 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     k.dx_piece = i >= 0 && a.dx ? i : -1;
     k.d_piece = i + 1 < c.pieces ? i + 1 : -1;
     k.first = i == 0;
-    e = launch_xent_mma(maps, k, p->dtype, c.pairs, st);
+    e = go((k.dw_piece >= 0 ? pt * nt : 0) + (k.dx_piece >= 0 ? c.acc_tiles * nt : 0) +
+           (k.d_piece >= 0 ? pt * mt : 0));
     if (e != cudaSuccess) return e;
   }
   if (!a.dx) return cudaSuccess;

@@ -230,7 +230,7 @@ __device__ void make_plan(const XentMma& a, int n, Plan* to) {
   if (a.dw_piece >= 0) nw = pieces_tiles(a, a.dw_piece) * p->nt;
   if (a.dx_piece >= 0) {
     cx = pieces_tiles(a, a.dx_piece) * (kXtN / kXtK);
-    const int slices = xent_slices(p->pairs, p->mt, p->nt, a.piece, a.acc_tiles);
+    const int slices = xent_slices(a.pairs, p->mt, p->nt, a.piece, a.acc_tiles);
     cx = (cx + slices - 1) / slices;
     nx = p->mt * p->nt * slices;
   }

@@ -24,8 +24,9 @@ struct XentMaps {
   CUtensorMap dw;                        // dW
 };
 
-// Slices of a piece's K that DX is cut into where it has fewer tiles than there
-// are pairs of CTAs, each with rows of its own; at least eight K stages a slice.
+// Slices of a piece's K that DX is cut into where it has few tiles, each with rows
+// of its own: as many as give each pair of CTAs a tile, at least eight K stages a
+// slice.
 __host__ __device__ inline int xent_slices(int pairs, int mt, int nt, int piece, int acc_tiles) {
   int s = pairs / (mt * nt);
   if (s > acc_tiles / mt) s = acc_tiles / mt;
@@ -41,6 +42,7 @@ struct XentMma {
   int lse;                               // 1: the forward, `run` tiles of the vocabulary a part
   int run;
   int dw_piece, dx_piece, d_piece;       // pieces to work on, -1: none
+  int pairs;                             // pairs of CTAs that the device holds
   int acc_tiles;                         // row tiles that dX's slices have room for
   int two_w;                             // wr takes two boxes
   int first, dw_tma;                     // dx_piece is the first; dW's rows fit a tensor map
