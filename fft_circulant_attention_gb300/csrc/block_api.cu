@@ -42,6 +42,9 @@ void free_op(cat_plan_s* p) {
   cudaFree(p->ln.part);
   cudaFree(p->cl.chunks);
   cudaFree(p->cl.part);
+  cudaFree(p->em.tok);
+  cudaFree(p->em.key);
+  cudaFree(p->em.off);
   cudaFree(p->em.first);
   cudaFree(p->em.order);
   cudaFree(p->em.sid);

@@ -149,6 +149,9 @@ enum Op {
 struct EmbedCfg {
   int max_tokens, V, range;
   float scale;
+  int* tok;                // [blocks][tokens of a block] the tokens by ranges of ids
+  int* key;                // their ids
+  int* off;                // [blocks][ranges + 1] where a range's tokens start in a block
   int* first;              // [V + 1]: where an id's tokens start in the sorted list
   int* order;              // [max_tokens] the tokens, sorted by id
   int* sid;                // [max_tokens] their ids
@@ -497,6 +500,8 @@ cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* ou
 // of the sorted list a group of threads sums.
 int embed_range(int V, int sms);
 size_t embed_part_count(int max_tokens, int D);
+size_t embed_split_count(int max_tokens);
+size_t embed_off_count(int max_tokens, int V, int sms);
 cudaError_t setup_embed();
 cudaError_t launch_embed(const cat_plan_s* p, const EmbedArgs& a, bool backward);
 

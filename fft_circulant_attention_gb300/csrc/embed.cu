@@ -5,11 +5,12 @@
 // Bound by memory: each row is read once and written once.  For the gradient
 // the tokens are first sorted by id, so that every row of dW is summed in the
 // order of its tokens and written once: no atomics on values, results repeat
-// bit for bit.  Three launches:
-//   sort:  a CTA owns a range of ids.  It reads all ids, counts those below its
-//          range (where its part of the sorted list starts) and those of each id
-//          of its own by warp (each warp has a stretch of the tokens), and puts
-//          its tokens in place, in order.  No CTA waits for another.
+// bit for bit.  Four launches:
+//   split: blocks of the tokens, each put in the order of ranges of ids;
+//   sort:  a CTA for each range takes its tokens from all blocks and puts them in
+//          the order of their ids.  Both count by warp (a warp has a stretch of
+//          the tokens) and keep the tokens' order within an id.  (One kernel whose
+//          CTAs each looked through all ids: 15 us for 16384 tokens, 33 for 65536.)
 //   sum:   the sorted list in pieces of equal length, a group of threads each; a
 //          run of equal ids that is no longer than a piece belongs to the piece it
 //          starts in and is a finished row, a longer one leaves a partial row
@@ -29,49 +30,65 @@ constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRange = 1024;        // most ids of a sorting CTA
-constexpr int kSeen = 16;
+constexpr int kBlocks = 256;            // most CTAs of the sort's first step
 constexpr int kZeroRows = 64;           // ids whose rows a clearing CTA looks at
+constexpr int kFwdPerSm = 6;            // CTAs of an SM that look up
 constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
 
-// A CTA copies `per` rows.
+// A CTA copies `per` rows at a time, its next rows' ids on their way meanwhile.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens, int V, int D,
                  int per, float scale, unsigned int* status) {
   using Vc = Vec<T, VEC>;
-  const int nv = D / VEC;
-  const int row0 = blockIdx.x * per;
-  const int n = min(per, tokens - row0) * nv;
   constexpr int U = 4;                          // vectors on their way at once
-  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-    int id[U];
-    typename Vc::Raw raw[U];
+  const int nv = D / VEC, chunk = per * nv;
+  int r[U], c[U];                               // the same place in every chunk of rows
+  for (int i0 = threadIdx.x; i0 < chunk; i0 += U * kThreads) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kThreads;
-      id[u] = i < n ? id_at(ids, row0 + i / nv, V) : -1;
+      r[u] = i < chunk ? i / nv : tokens;       // (none)
+      c[u] = (i - i / nv * nv) * VEC;
     }
+    int id[U], next[U];
+    auto fetch_as = [&](auto* p, long long row0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      if (id[u] >= 0) raw[u] = Vc::ldr(W + (size_t)id[u] * D + (i - i / nv * nv) * VEC);
-    }
+      for (int u = 0; u < U; ++u)
+        next[u] = row0 + r[u] < tokens ? id_of(id_key(__ldg(p + row0 + r[u])), V) : -1;
+    };
+    auto fetch = [&](long long row0) {
+      if (ids.wide)
+        fetch_as(static_cast<const long long*>(ids.p), row0);
+      else
+        fetch_as(static_cast<const int*>(ids.p), row0);
+    };
+    const long long step = (long long)gridDim.x * per;
+    long long row0 = (long long)blockIdx.x * per;
+    fetch(row0);
+    for (; row0 < tokens; row0 += step) {
+      typename Vc::Raw raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      if (i >= n) break;
-      const int r = i / nv, c = (i - r * nv) * VEC;
-      float v[VEC];
-      if (id[u] >= 0) {
-        Vc::widen(raw[u], v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] *= scale;
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = 0.f;
-        if (id[u] == -2 && c == 0) report(status, 0x701);
+      for (int u = 0; u < U; ++u) {
+        id[u] = next[u];
+        if (id[u] >= 0) raw[u] = Vc::ldr(W + (size_t)id[u] * D + c[u]);
       }
-      Vc::st(Y + (size_t)(row0 + r) * D + c, v);
+      fetch(row0 + step);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (row0 + r[u] >= tokens) continue;
+        float v[VEC];
+        if (id[u] >= 0) {
+          Vc::widen(raw[u], v);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] *= scale;
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+          if (id[u] == -2 && c[u] == 0) report(status, 0x701);
+        }
+        Vc::st(Y + (size_t)(row0 + r[u]) * D + c[u], v);
+      }
     }
   }
 }
@@ -101,93 +118,164 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
   return x - v + (warp ? red[warp - 1] : 0);
 }
 
-// first[v]: where id v's tokens start in the sorted list (first[V]: its length);
-// order: the tokens; sid: their ids.
-__global__ void __launch_bounds__(kSortThreads)
-embed_sort_kernel(Ids ids, int tokens, int V, int range, int* __restrict__ first,
-                  int* __restrict__ order, int* __restrict__ sid, unsigned int* status) {
-  extern __shared__ int hist[];                 // [kSortWarps][range]
-  __shared__ int red[kSortWarps];
-  __shared__ unsigned seen[kSortWarps][kSeen];  // which steps held tokens of this range
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned lo = blockIdx.x * range, n = min((unsigned)range, V - lo);
-  for (int i = threadIdx.x; i < kSortWarps * range; i += kSortThreads) hist[i] = 0;
-  for (int i = lane; i < kSeen; i += 32) seen[warp][i] = 0;
-  __syncthreads();
-  // This warp's stretch of the tokens, 32 a step, eight steps on their way at once.
-  const int steps = (tokens + 32 * kSortWarps - 1) / (32 * kSortWarps);
-  const long long t0 = (long long)warp * steps * 32;
-  const long long end = min((long long)tokens, t0 + 32ll * steps);
-  int shift = 3;                                // a bit of `seen`: 8 steps, or more
-  while ((steps >> shift) >= 32 * kSeen) ++shift;
-  int* h = hist + warp * range;
-  int below = 0;
-  bool bad = false;
-  for (int s0 = 0; s0 < steps; s0 += 8) {
-    unsigned key[8];
-    keys_at<8>(ids, t0 + 32 * s0 + lane, 32, end, key);
-    unsigned found = 0;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      below += key[u] < lo;
-      if (blockIdx.x == 0) bad |= id_of(key[u], V) == -2;
-      const bool mine = key[u] - lo < n;
-      const unsigned any = __ballot_sync(0xffffffffu, mine);
-      found |= any;
-      if (any) {
-        if (mine) {
-          const unsigned same = __match_any_sync(any, key[u]);
-          if (lane == __ffs(same) - 1) h[key[u] - lo] += __popc(same);
-        }
-        __syncwarp();
-      }
+// A warp's counts of each class (hist [kSortWarps][classes]) become where its tokens
+// of that class start: classes in order from `base` on, within a class the warps.
+// Returns the number of all tokens; *start: of class threadIdx.x.
+__device__ __forceinline__ int class_starts(int* hist, int classes, int base, int* red,
+                                            int* start) {
+  const int c = threadIdx.x;
+  int count = 0, all;
+  if (c < classes) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) count += hist[w * classes + c];
+  }
+  int at = base + block_scan(count, red, &all);
+  *start = at;
+  if (c < classes) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = hist[w * classes + c];
+      hist[w * classes + c] = at;
+      at += n;
     }
-    const int bit = s0 >> shift;
-    if (found && lane == 0) seen[warp][bit >> 5] |= 1u << (bit & 31);
+  }
+  __syncthreads();
+  return all;
+}
+
+// The lanes with `mine` of one class each (by `cls`) count (COUNT), or take their
+// places, in the order of the lanes; h: the warp's counts or starts.
+template <bool COUNT>
+__device__ __forceinline__ int warp_class(int* h, bool mine, int cls) {
+  const unsigned any = __ballot_sync(0xffffffffu, mine);
+  int pos = -1;
+  if (mine) {
+    const int lane = threadIdx.x & 31;
+    const unsigned same = __match_any_sync(any, cls);
+    const int start = h[cls];
+    if (!COUNT) pos = start + __popc(same & ((1u << lane) - 1));
+    __syncwarp(any);
+    if (lane == __ffs(same) - 1) h[cls] = start + __popc(same);
+  }
+  __syncwarp();
+  return pos;
+}
+
+// First step of the sort: a CTA puts its `per` tokens in the order of their ids'
+// ranges (`range` ids each; magic: 2^32 / range, rounded up, exact for ids below
+// 2^20).  tok, key: [blocks][per]; off: [blocks][ranges + 1].
+__global__ void __launch_bounds__(kSortThreads)
+embed_split_kernel(Ids ids, int tokens, int V, int per, int ranges, unsigned magic,
+                   int* __restrict__ tok, int* __restrict__ key_out, int* __restrict__ off,
+                   unsigned int* status) {
+  extern __shared__ int hist[];                 // [kSortWarps][ranges]
+  __shared__ int red[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b0 = blockIdx.x * per;
+  const int steps = per / kSortThreads;
+  const int t0 = b0 + warp * steps * 32;
+  int* h = hist + warp * ranges;
+  for (int i = lane; i < ranges; i += 32) h[i] = 0;
+  __syncwarp();
+  bool bad = false;
+  for (int s = 0; s < steps; ++s) {
+    const int t = t0 + 32 * s + lane;
+    const int id = t < tokens ? id_at(ids, t, V) : -1;
+    bad |= id == -2;
+    warp_class<true>(h, id >= 0, id >= 0 ? (int)__umulhi((unsigned)id, magic) : 0);
   }
   if (bad) report(status, 0x702);
   __syncthreads();
-  int base, count = 0, own;
-  block_scan(below, red, &base);
-  __syncthreads();
-  if (threadIdx.x < n) {
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) count += hist[w * range + threadIdx.x];
-  }
-  int at = base + block_scan(count, red, &own);
-  if (threadIdx.x < n) {
-    first[lo + threadIdx.x] = at;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = hist[w * range + threadIdx.x];
-      hist[w * range + threadIdx.x] = at;
-      at += c;
+  int start;
+  const int all = class_starts(hist, ranges, 0, red, &start);
+  int* o = off + (size_t)blockIdx.x * (ranges + 1);
+  if ((int)threadIdx.x < ranges) o[threadIdx.x] = start;
+  if (threadIdx.x == 0) o[ranges] = all;
+  for (int s = 0; s < steps; ++s) {
+    const int t = t0 + 32 * s + lane;
+    const int id = t < tokens ? id_at(ids, t, V) : -1;
+    const int pos =
+        warp_class<false>(h, id >= 0, id >= 0 ? (int)__umulhi((unsigned)id, magic) : 0);
+    if (pos >= 0) {
+      tok[b0 + pos] = t;
+      key_out[b0 + pos] = id;
     }
   }
-  if (threadIdx.x == 0 && lo + n == (unsigned)V) first[V] = base + own;
+}
+
+// Second step: a CTA sorts the tokens of one range, which it takes from the blocks
+// of the first step in their order.  first[v]: where id v's tokens start in the
+// sorted list (first[V]: its length); order: the tokens; sid: their ids.
+__global__ void __launch_bounds__(kSortThreads)
+embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, int per, int V,
+                  int range, int* __restrict__ first, int* __restrict__ order,
+                  int* __restrict__ sid) {
+  extern __shared__ int hist[];                 // [kSortWarps][range]
+  __shared__ int red[kSortWarps];
+  __shared__ int begin[kBlocks + 1], from[kBlocks];   // a block's tokens: first in this range's
+                                                      // list, where they lie
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ranges = gridDim.x, lo = blockIdx.x * range, n = min(range, V - lo);
+  int* h = hist + warp * n;
+  for (int i = lane; i < n; i += 32) h[i] = 0;
+  pdl_wait();
+  int below = 0, count = 0, own, base;
+  if ((int)threadIdx.x < blocks) {
+    const int* o = off + (size_t)threadIdx.x * (ranges + 1) + blockIdx.x;
+    below = __ldcg(o);
+    count = __ldcg(o + 1) - below;
+    from[threadIdx.x] = threadIdx.x * per + below;
+  }
+  const int at = block_scan(count, red, &own);
+  if ((int)threadIdx.x < blocks) begin[threadIdx.x] = at;
+  if (threadIdx.x == 0) begin[blocks] = own;
   __syncthreads();
-  if (own == 0) return;
-  // Again over the steps with tokens of this range: their places, in order.
-  for (int s0 = 0; s0 < steps; s0 += 8) {
-    const int bit = s0 >> shift;
-    if (!(seen[warp][bit >> 5] >> (bit & 31) & 1)) continue;
-    unsigned key[8];
-    keys_at<8>(ids, t0 + 32 * s0 + lane, 32, end, key);
+  block_scan(below, red, &base);
+  __syncthreads();
+  const int steps = (own + kSortThreads - 1) / kSortThreads;
+  // Where the i-th token of the range lies.
+  auto place = [&](int i) {
+    int a = 0, b = blocks;                      // begin[a] <= i < begin[b]
+    while (b - a > 1) {
+      const int m = (a + b) >> 1;
+      if (begin[m] <= i) a = m; else b = m;
+    }
+    return from[a] + i - begin[a];
+  };
+  // (Four steps' loads on their way at once: a range may hold a good part of all
+  // tokens.)
+  constexpr int U = 4;
+  for (int s0 = 0; s0 < steps; s0 += U) {
+    int id[U];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const bool mine = key[u] - lo < n;
-      const unsigned any = __ballot_sync(0xffffffffu, mine);
-      if (any) {
-        if (mine) {
-          const unsigned same = __match_any_sync(any, key[u]);
-          const int start = h[key[u] - lo];
-          const int pos = start + __popc(same & ((1u << lane) - 1));
-          order[pos] = (int)(t0 + 32 * (s0 + u) + lane);
-          sid[pos] = (int)key[u];
-          __syncwarp(any);
-          if (lane == __ffs(same) - 1) h[key[u] - lo] = start + __popc(same);
-        }
-        __syncwarp();
+    for (int u = 0; u < U; ++u) {
+      const int i = (warp * steps + s0 + u) * 32 + lane;
+      id[u] = s0 + u < steps && i < own ? __ldcg(key + place(i)) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) warp_class<true>(h, id[u] >= 0, id[u] - lo);
+  }
+  __syncthreads();
+  int start;
+  class_starts(hist, n, base, red, &start);
+  if ((int)threadIdx.x < n) first[lo + threadIdx.x] = start;
+  if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
+  for (int s0 = 0; s0 < steps; s0 += U) {
+    int id[U], t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = (warp * steps + s0 + u) * 32 + lane;
+      const bool in = s0 + u < steps && i < own;
+      const int q = in ? place(i) : 0;
+      id[u] = in ? __ldcg(key + q) : -1;
+      t[u] = in ? __ldcg(tok + q) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pos = warp_class<false>(h, id[u] >= 0, id[u] - lo);
+      if (pos >= 0) {
+        order[pos] = t[u];
+        sid[pos] = id[u];
       }
     }
   }
@@ -299,11 +387,12 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
 }
 
 // The partial rows of the long runs (more than P places: one in each piece they
-// touch).  A CTA looks at 32 pieces, a lane each, for long runs that start in them,
+// touch).  A CTA looks at kLook pieces, a lane each, for long runs that start in them,
 // and joins those one after another: its warps add every so-many-th partial row
 // each, the warps' sums in order then.  (A thread adding a column's partial rows one
 // after another: 38 us for 16384 tokens, 66 pieces of the most frequent id.)
 constexpr int kJoinWarps = kThreads / 32;
+constexpr int kLook = 8;                // pieces a CTA looks at
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, int V, int D, int P,
@@ -312,10 +401,10 @@ embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   const int total = __ldcg(first + V), lo = blockIdx.y * 128;
-  const int piece = blockIdx.x * 32 + lane;
+  const int piece = blockIdx.x * kLook + lane;
   const long long q0 = (long long)piece * P;
   int v = -1, last = 0;
-  if (q0 + P < total) {
+  if (lane < kLook && q0 + P < total) {
     v = __ldcg(sid + q0 + P - 1);
     const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
     if (a < (int)q0 || b - a <= P) v = -1;
@@ -326,7 +415,7 @@ embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, in
     const int j = __ffs(left) - 1;
     left &= left - 1;
     const int id = __shfl_sync(0xffffffffu, v, j), to = __shfl_sync(0xffffffffu, last, j);
-    const int from = blockIdx.x * 32 + j;
+    const int from = blockIdx.x * kLook + j;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = from + warp; i <= to; i += kJoinWarps) {
@@ -356,6 +445,13 @@ int piece_length(int tokens) {
   return p < 16 ? 16 : p;
 }
 
+// Tokens of a block of the sort's first step: a thread each, more where there would
+// be more than kBlocks of them.
+int block_tokens(int tokens) {
+  const int m = (tokens + kBlocks * kSortThreads - 1) / (kBlocks * kSortThreads);
+  return (m < 1 ? 1 : m) * kSortThreads;
+}
+
 // Ids of a sorting CTA: an equal share of the vocabulary, at most kSortRange.
 int sort_range(int V, int sms) {
   const int r = (V + sms - 1) / sms;
@@ -375,7 +471,7 @@ cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) 
       static_cast<T*>(a.y), c.part, c.V, D, P, ctas, c.scale, a.add);
   if (e != cudaSuccess || pieces < 2) return e;
   return launch_dependent(embed_join_kernel<T>,
-                          dim3((pieces + 31) / 32, (D + 127) / 128),
+                          dim3((pieces + kLook - 1) / kLook, (D + 127) / 128),
                           dim3(kThreads), 0, st,
                           (const int*)c.first, (const int*)c.sid, (const float*)c.part,
                           static_cast<T*>(a.y), c.V, D, P, c.scale, a.add);
@@ -383,19 +479,27 @@ cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) 
 
 template <typename T, int VEC>
 cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, unsigned int* status,
-                cudaStream_t st) {
+                int sms, cudaStream_t st) {
   const int nv = D / VEC;
   if (!backward) {
     const int per = nv >= kLookup ? 1 : kLookup / nv;
-    embed_fwd_kernel<T, VEC><<<(a.tokens + per - 1) / per, kThreads, 0, st>>>(
+    const int need = (a.tokens + per - 1) / per, most = kFwdPerSm * sms;
+    embed_fwd_kernel<T, VEC><<<need < most ? need : most, kThreads, 0, st>>>(
         a.ids, static_cast<const T*>(a.x), static_cast<T*>(a.y), a.tokens, c.V, D, per, c.scale,
         status);
     return cudaGetLastError();
   }
-  embed_sort_kernel<<<(c.V + c.range - 1) / c.range, kSortThreads,
-                      (size_t)kSortWarps * c.range * sizeof(int), st>>>(
-      a.ids, a.tokens, c.V, c.range, c.first, c.order, c.sid, status);
-  const cudaError_t e = cudaGetLastError();
+  const int per = block_tokens(a.tokens), blocks = (a.tokens + per - 1) / per;
+  const int ranges = (c.V + c.range - 1) / c.range;
+  embed_split_kernel<<<blocks, kSortThreads, (size_t)kSortWarps * ranges * sizeof(int), st>>>(
+      a.ids, a.tokens, c.V, per, ranges,
+      (unsigned)(((1ull << 32) + c.range - 1) / c.range), c.tok, c.key, c.off, status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(embed_sort_kernel, dim3(ranges), dim3(kSortThreads),
+                       (size_t)kSortWarps * c.range * sizeof(int), st, (const int*)c.tok,
+                       (const int*)c.key, (const int*)c.off, blocks, per, c.V, c.range, c.first,
+                       c.order, c.sid);
   if (e != cudaSuccess) return e;
   if (nv <= 8) return sums<T, VEC, 8>(c, a, D, st);
   if (nv <= 32) return sums<T, VEC, 32>(c, a, D, st);
@@ -406,11 +510,11 @@ cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, uns
 
 template <typename T, int FULL>
 cudaError_t by_width(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward,
-                     unsigned int* status, cudaStream_t st) {
+                     unsigned int* status, int sms, cudaStream_t st) {
   // The widest vector that divides the rows keeps every row start aligned.
-  if (D % FULL == 0) return run<T, FULL>(c, a, D, backward, status, st);
-  if (D % 2 == 0) return run<T, 2>(c, a, D, backward, status, st);
-  return run<T, 1>(c, a, D, backward, status, st);
+  if (D % FULL == 0) return run<T, FULL>(c, a, D, backward, status, sms, st);
+  if (D % 2 == 0) return run<T, 2>(c, a, D, backward, status, sms, st);
+  return run<T, 1>(c, a, D, backward, status, sms, st);
 }
 
 }  // namespace
@@ -424,12 +528,27 @@ size_t embed_part_count(int max_tokens, int D) {
   return pieces * 2 * D;
 }
 
-cudaError_t setup_embed() { return allow_max_smem(embed_sort_kernel); }
+size_t embed_split_count(int max_tokens) {
+  // (Fewer tokens have blocks no longer than these.)
+  const size_t per = block_tokens(max_tokens);
+  return (max_tokens + per - 1) / per * per;
+}
+size_t embed_off_count(int max_tokens, int V, int sms) {
+  const int per = block_tokens(max_tokens), range = sort_range(V, sms);
+  const size_t blocks = max_tokens > kSortThreads * kBlocks ? kBlocks
+                                                            : (max_tokens + per - 1) / per;
+  return blocks * ((V + range - 1) / range + 1);
+}
+
+cudaError_t setup_embed() {
+  const cudaError_t e = allow_max_smem(embed_split_kernel);
+  return e != cudaSuccess ? e : allow_max_smem(embed_sort_kernel);
+}
 
 cudaError_t launch_embed(const cat_plan_s* p, const EmbedArgs& a, bool backward) {
   return p->dtype == CAT_BF16
-             ? by_width<__nv_bfloat16, 8>(p->em, a, p->D, backward, p->status, p->stream)
-             : by_width<float, 4>(p->em, a, p->D, backward, p->status, p->stream);
+             ? by_width<__nv_bfloat16, 8>(p->em, a, p->D, backward, p->status, p->sms, p->stream)
+             : by_width<float, 4>(p->em, a, p->D, backward, p->status, p->sms, p->stream);
 }
 
 }  // namespace cat

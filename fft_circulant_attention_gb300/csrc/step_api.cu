@@ -53,7 +53,9 @@ int cat_plan_create_embed(cat_plan_t* out, int max_tokens, int V, int D, int dty
   c.V = V;
   c.scale = scale;
   c.range = cat::embed_range(V, p->sms);
-  if (!alloc_status(p) || !alloc(p, &c.first, (size_t)V + 1) ||
+  const size_t split = cat::embed_split_count(max_tokens);
+  if (!alloc_status(p) || !alloc(p, &c.tok, split) || !alloc(p, &c.key, split) ||
+      !alloc(p, &c.off, cat::embed_off_count(max_tokens, V, p->sms)) || !alloc(p, &c.first, (size_t)V + 1) ||
       !alloc(p, &c.order, (size_t)max_tokens) || !alloc(p, &c.sid, (size_t)max_tokens) ||
       !alloc(p, &c.part, cat::embed_part_count(max_tokens, D)))
     return fail(p, CAT_ERR_ALLOC);

@@ -431,7 +431,7 @@ int cat_grad_clip(cat_plan_t plan, const void *const *grads, void *const *outs,
  */
 
 /* Largest vocabulary, most tokens of an embedding and of a cross entropy call. */
-#define CAT_MAX_VOCAB (1 << 24)
+#define CAT_MAX_VOCAB (1 << 20)
 #define CAT_STEP_MAX_TOKENS (1 << 24)
 #define CAT_XENT_MAX_TOKENS (1 << 20)
 

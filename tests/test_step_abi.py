@@ -20,7 +20,7 @@ def lib():
 
 @pytest.mark.parametrize("create,args", [
     ("embed", (-1, 10, 8, 0, 1.0)), ("embed", (2**24 + 1, 10, 8, 0, 1.0)),
-    ("embed", (4, 0, 8, 0, 1.0)), ("embed", (4, 2**24 + 1, 8, 0, 1.0)),
+    ("embed", (4, 0, 8, 0, 1.0)), ("embed", (4, 2**20 + 1, 8, 0, 1.0)),
     ("embed", (4, 10, 0, 0, 1.0)), ("embed", (4, 10, 8193, 0, 1.0)), ("embed", (4, 10, 8, 2, 1.0)),
     ("embed", (4, 10, 8, 0, math.nan)), ("embed", (4, 10, 8, 0, math.inf)),
     ("resnorm", (-1, 8, 0, 0, 1e-5, 1.0)), ("resnorm", (2**30 + 1, 8, 0, 0, 1e-5, 1.0)),
@@ -29,7 +29,7 @@ def lib():
     ("resnorm", (4, 8, 0, 0, -1e-5, 1.0)), ("resnorm", (4, 8, 0, 0, math.nan, 1.0)),
     ("resnorm", (4, 8, 0, 1, 1e-5, math.inf)),
     ("xent", (-1, 10, 8, 0, 1)), ("xent", (2**20 + 1, 10, 8, 0, 1)), ("xent", (4, 0, 8, 0, 1)),
-    ("xent", (4, 2**24 + 1, 8, 0, 1)), ("xent", (4, 10, 0, 0, 1)), ("xent", (4, 10, 8193, 0, 1)),
+    ("xent", (4, 2**20 + 1, 8, 0, 1)), ("xent", (4, 10, 0, 0, 1)), ("xent", (4, 10, 8193, 0, 1)),
     ("xent", (4, 10, 8, 7, 1)), ("xent", (4, 10, 8, 0, 2)),
 ])
 def test_plans_refuse(lib, create, args):
