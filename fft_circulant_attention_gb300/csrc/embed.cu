@@ -148,6 +148,7 @@ __device__ __forceinline__ int class_starts(int* hist, int classes, int base, in
 template <bool COUNT>
 __device__ __forceinline__ int warp_class(int* h, bool mine, int cls) {
   const unsigned any = __ballot_sync(0xffffffffu, mine);
+  if (!any) return -1;
   int pos = -1;
   if (mine) {
     const int lane = threadIdx.x & 31;
@@ -212,63 +213,51 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
                   int* __restrict__ sid) {
   extern __shared__ int hist[];                 // [kSortWarps][range]
   __shared__ int red[kSortWarps];
-  __shared__ int begin[kBlocks + 1], from[kBlocks];   // a block's tokens: first in this range's
-                                                      // list, where they lie
+  __shared__ int2 part[kBlocks];                // where a block's tokens of this range lie
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranges = gridDim.x, lo = blockIdx.x * range, n = min(range, V - lo);
   int* h = hist + warp * n;
   for (int i = lane; i < n; i += 32) h[i] = 0;
   pdl_wait();
-  int below = 0, count = 0, own, base;
+  int below = 0, own, base, start;
   if ((int)threadIdx.x < blocks) {
     const int* o = off + (size_t)threadIdx.x * (ranges + 1) + blockIdx.x;
     below = __ldcg(o);
-    count = __ldcg(o + 1) - below;
-    from[threadIdx.x] = threadIdx.x * per + below;
+    const int q = threadIdx.x * per + below;
+    part[threadIdx.x] = make_int2(q, q + __ldcg(o + 1) - below);
   }
-  const int at = block_scan(count, red, &own);
-  if ((int)threadIdx.x < blocks) begin[threadIdx.x] = at;
-  if (threadIdx.x == 0) begin[blocks] = own;
-  __syncthreads();
   block_scan(below, red, &base);
   __syncthreads();
-  const int steps = (own + kSortThreads - 1) / kSortThreads;
-  // Where the i-th token of the range lies.
-  auto place = [&](int i) {
-    int a = 0, b = blocks;                      // begin[a] <= i < begin[b]
-    while (b - a > 1) {
-      const int m = (a + b) >> 1;
-      if (begin[m] <= i) a = m; else b = m;
-    }
-    return from[a] + i - begin[a];
-  };
-  // (Four steps' loads on their way at once: a range may hold a good part of all
-  // tokens.)
+  // A warp takes a stretch of the blocks; f(place, whether there is one) for its
+  // tokens, 128 at a time.  (Looking each token's block up cost more than the rest:
+  // a range may hold a good part of all tokens.)
+  const int each = (blocks + kSortWarps - 1) / kSortWarps;
+  const int first_block = warp * each, last_block = min(blocks, first_block + each);
   constexpr int U = 4;
-  for (int s0 = 0; s0 < steps; s0 += U) {
+  auto tokens_of = [&](auto f) {
+    for (int b = first_block; b < last_block; ++b) {
+      const int2 s = part[b];
+      for (int q = s.x; q < s.y; q += 32 * U) f(q + lane, s.y);
+    }
+  };
+  tokens_of([&](int q, int end) {
     int id[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = (warp * steps + s0 + u) * 32 + lane;
-      id[u] = s0 + u < steps && i < own ? __ldcg(key + place(i)) : -1;
-    }
+    for (int u = 0; u < U; ++u) id[u] = q + 32 * u < end ? __ldcg(key + q + 32 * u) : -1;
 #pragma unroll
     for (int u = 0; u < U; ++u) warp_class<true>(h, id[u] >= 0, id[u] - lo);
-  }
+  });
   __syncthreads();
-  int start;
-  class_starts(hist, n, base, red, &start);
+  own = class_starts(hist, n, base, red, &start);
   if ((int)threadIdx.x < n) first[lo + threadIdx.x] = start;
   if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
-  for (int s0 = 0; s0 < steps; s0 += U) {
+  tokens_of([&](int q, int end) {
     int id[U], t[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = (warp * steps + s0 + u) * 32 + lane;
-      const bool in = s0 + u < steps && i < own;
-      const int q = in ? place(i) : 0;
-      id[u] = in ? __ldcg(key + q) : -1;
-      t[u] = in ? __ldcg(tok + q) : 0;
+      const bool in = q + 32 * u < end;
+      id[u] = in ? __ldcg(key + q + 32 * u) : -1;
+      t[u] = in ? __ldcg(tok + q + 32 * u) : 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -278,7 +267,7 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
         sid[pos] = id[u];
       }
     }
-  }
+  });
 }
 
 // dst = scale·acc, or dst + scale·acc.
