@@ -96,6 +96,7 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 template <typename T>
 __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
   const int vecs = p.pitch / 8;
+  pdl_trigger();
   if ((int)blockIdx.x >= p.list_ctas) {
     const long long n = (long long)p.V * vecs;
     const long long step = (long long)(gridDim.x - p.list_ctas) * kPrep;
@@ -220,43 +221,40 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
 }
 
 // dX's rows from the sums of the list's (the slices of each, in order), zeros for
-// the tokens without a target.  Vectors of four where they divide a row.
+// the tokens without a target.  A warp a row, in vectors of four where they divide
+// it.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T* __restrict__ dX,
-               int tokens, int D, int per, int pairs, int piece, int acc_tiles) {
+               int tokens, int D, int pairs, int piece, int acc_tiles) {
   pdl_wait();
+  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= tokens) return;
+  const int pos = __ldcg(inv + row);
   const int mt = (__ldcg(count) + kXtM - 1) / kXtM;
-  const int slices = mt ? xent_slices(pairs, mt, (D + kXtN - 1) / kXtN, piece, acc_tiles) : 0;
+  const int slices = pos >= 0 ? xent_slices(pairs, mt, (D + kXtN - 1) / kXtN, piece, acc_tiles) : 0;
   const size_t apart = (size_t)mt * kXtM * pitch;
-  const int nv = D / VEC, row0 = blockIdx.x * per, n = min(per, tokens - row0) * nv;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int r = i / nv, c = (i - r * nv) * VEC, pos = __ldcg(inv + row0 + r);
-    float v[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = 0.f;
-    if (pos >= 0) {
-      const float* q = acc + (size_t)pos * pitch + c;
+  const float* from = acc + (pos >= 0 ? (size_t)pos * pitch : 0);
+  T* to = dX + (size_t)row * D;
 #pragma unroll 4
-      for (int s = 0; s < slices; ++s, q += apart) {
-        if (VEC == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
-          v[0] += x.x; v[VEC > 1 ? 1 : 0] += x.y; v[VEC > 1 ? 2 : 0] += x.z; v[VEC > 1 ? 3 : 0] += x.w;
-        } else {
-          v[0] += __ldcg(q);
-        }
+  for (int c = lane * VEC; c < D; c += 32 * VEC) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const float* q = from + c;
+    for (int s = 0; s < slices; ++s, q += apart) {
+      if (VEC == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      } else {
+        v[0] += __ldcg(q);
       }
     }
-    T* to = dX + (size_t)(row0 + r) * D + c;
     if (VEC == 4 && sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(to) = make_float4(v[0], v[VEC > 1 ? 1 : 0], v[VEC > 1 ? 2 : 0], v[VEC > 1 ? 3 : 0]);
+      *reinterpret_cast<float4*>(to + c) = make_float4(v[0], v[1], v[2], v[3]);
     } else if (VEC == 4) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[VEC > 1 ? 1 : 0]),
-                             __floats2bfloat162_rn(v[VEC > 1 ? 2 : 0], v[VEC > 1 ? 3 : 0])};
-      *reinterpret_cast<uint2*>(to) = *reinterpret_cast<uint2*>(h);
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+      *reinterpret_cast<uint2*>(to + c) = *reinterpret_cast<uint2*>(h);
     } else {
-      st_elem(to, v[0]);
+      st_elem(to + c, v[0]);
     }
   }
 }
@@ -385,11 +383,10 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
 template <typename T, int VEC>
 cudaError_t finish_dx(const cat_plan_s* p, const XentArgs& a, int tokens) {
   const XentCfg& c = p->xe;
-  const int nv = p->D / VEC, per = nv >= 2 * kThreads ? 1 : 2 * kThreads / nv;
-  return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, per)), dim3(kThreads), 0,
-                          p->stream, (const float*)c.dxacc, c.acc_pitch, (const int*)c.inv,
-                          (const int*)c.count, static_cast<T*>(a.dx), tokens, p->D, per, c.pairs,
-                          c.piece, c.acc_tiles);
+  return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, kThreads / 32)),
+                          dim3(kThreads), 0, p->stream, (const float*)c.dxacc, c.acc_pitch,
+                          (const int*)c.inv, (const int*)c.count, static_cast<T*>(a.dx), tokens,
+                          p->D, c.pairs, c.piece, c.acc_tiles);
 }
 
 }  // namespace

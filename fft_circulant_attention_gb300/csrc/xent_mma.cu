@@ -174,10 +174,13 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, 
                : "memory");
 }
 
-__device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// 32 bytes with an L2 policy.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* v, uint64_t policy) {
+  asm volatile(
+      "st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "l"(policy)
+      : "memory");
 }
 
 // One tile of a launch.
@@ -702,7 +705,9 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
           for (int i = 0; i < 64; ++i) v[i] = live ? v[i] : 0.f;
         }
         // Past shared memory, which the products' operands keep busy: a lane's 64
-        // values of its row, 32 bytes at a time, a term after another.
+        // values of its row, 32 bytes at a time, a term after another.  A piece's d is
+        // larger than L2: it leaves first, so that the operands stay.
+        const uint64_t first_out = policy_evict_first();
         uint32_t* to = static_cast<uint32_t*>(a.d) +
                        ((size_t)(t.drow + row) * (F32 ? 3 : 1) * a.piece + col) / 2;
 #pragma unroll
@@ -720,7 +725,7 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
                 y -= __uint_as_float(h[i] & 0xffff0000u);
               }
             }
-            st_global32(to + 8 * j, h);
+            st_global32(to + 8 * j, h, first_out);
           }
           to += a.piece / 2;
         }
@@ -811,6 +816,7 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
     mbar_fence_init();
   }
   if (warp == 2) pair_alloc(smem_addr(&tslot), 2 * kAccCols);
+  pdl_trigger();
   pdl_wait();
   const int n = __ldcg(a.count), direct = __ldcg(a.count + 1);
   if (warp == 3) make_plan(a, n, &plan);
