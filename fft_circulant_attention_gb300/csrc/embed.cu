@@ -36,7 +36,9 @@ constexpr int kFwdPerSm = 6;            // CTAs of an SM that look up
 constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
 
 // A CTA copies `per` rows at a time, its next rows' ids on their way meanwhile.
-template <typename T, int VEC>
+// COPY: the scale is 1, rows are copied as they are (16384 rows of 768 bf16 took more
+// instructions than memory).
+template <typename T, int VEC, bool COPY>
 __global__ void __launch_bounds__(kThreads)
 embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens, int V, int D,
                  int per, float scale, unsigned int* status) {
@@ -77,6 +79,11 @@ embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (row0 + r[u] >= tokens) continue;
+        T* to = Y + (size_t)(row0 + r[u]) * D + c[u];
+        if (COPY && id[u] >= 0) {
+          *reinterpret_cast<typename Vc::Raw*>(to) = raw[u];
+          continue;
+        }
         float v[VEC];
         if (id[u] >= 0) {
           Vc::widen(raw[u], v);
@@ -87,7 +94,7 @@ embed_fwd_kernel(Ids ids, const T* __restrict__ W, T* __restrict__ Y, int tokens
           for (int e = 0; e < VEC; ++e) v[e] = 0.f;
           if (id[u] == -2 && c[u] == 0) report(status, 0x701);
         }
-        Vc::st(Y + (size_t)(row0 + r[u]) * D + c[u], v);
+        Vc::st(to, v);
       }
     }
   }
@@ -476,7 +483,8 @@ cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, uns
   if (!backward) {
     const int per = nv >= kLookup ? 1 : kLookup / nv;
     const int need = (a.tokens + per - 1) / per, most = kFwdPerSm * sms;
-    embed_fwd_kernel<T, VEC><<<need < most ? need : most, kThreads, 0, st>>>(
+    auto kernel = c.scale == 1.f ? embed_fwd_kernel<T, VEC, true> : embed_fwd_kernel<T, VEC, false>;
+    kernel<<<need < most ? need : most, kThreads, 0, st>>>(
         a.ids, static_cast<const T*>(a.x), static_cast<T*>(a.y), a.tokens, c.V, D, per, c.scale,
         status);
     return cudaGetLastError();

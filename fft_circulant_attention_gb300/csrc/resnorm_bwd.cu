@@ -82,11 +82,14 @@ resnorm_bwd_kernel(ResNormArgs a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[s][kShared ? 0 : k][e] = 0.f;
   }
-  auto sum_to = [&](int s, int k, int c, int e, float v) {
-    if (kShared)
-      sm[s * D + c + e] += v;
-    else
-      acc[s][kShared ? 0 : k][e] += v;
+  // Sum s, vector k (at column c): plus a·b, plus a.
+  auto sum_dot = [&](int s, int k, int c, const float* x, const float* y) {
+    float* to = kShared ? sm + s * D + c : acc[s][kShared ? 0 : k];
+    v_fma<VEC>(to, x, y, to);
+  };
+  auto sum_add = [&](int s, int k, int c, const float* x) {
+    float* to = kShared ? sm + s * D + c : acc[s][kShared ? 0 : k];
+    v_add<VEC>(to, to, x);
   };
   const float inv = 1.f / (float)D, scale = a.scale;
   const T* gamma = static_cast<const T*>(a.gamma);
@@ -135,83 +138,84 @@ resnorm_bwd_kernel(ResNormArgs a) {
     }
     const float mh = nst.x, rsh = nst.y, mb = nst.z, rsb = nst.w;
     fetch(row + gridDim.x * kRows);
-    float s1 = 0.f, s2 = 0.f;
+    Sum2<VEC> p1, p2;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
         float w[VEC];
         load_or<T, VEC>(gamma, c, 1.f, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          xh[k][e] = (xh[k][e] - mh) * rsh;
-          sum_to(S_GAMMA, k, c, e, g[k][e] * xh[k][e]);
-          sum_to(S_BETA, k, c, e, g[k][e]);
-          g[k][e] *= w[e];
-          s1 += g[k][e];
-          s2 = fmaf(g[k][e], xh[k][e], s2);
-        }
+        v_add<VEC>(xh[k], xh[k], -mh);
+        v_mul<VEC>(xh[k], xh[k], rsh);
+        sum_dot(S_GAMMA, k, c, g[k], xh[k]);
+        sum_add(S_BETA, k, c, g[k]);
+        v_mul<VEC>(g[k], g[k], w);
+        p1.add(g[k]);
+        p2.dot(g[k], xh[k]);
       }
     }
+    float s1 = p1.total(), s2 = p2.total();
     sum2<TPR, BT>(s1, s2, red, sub, use);
     s1 *= inv;
     s2 *= inv;
     // g becomes dh, then du·pg; xh becomes b̂.
-    float t1 = 0.f, t2 = 0.f;
+    Sum2<VEC> q1, q2;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
         float w[VEC], b[VEC], u[VEC];
+        // dh = dH + rstd·((g - s1) - x̂·s2)
+        v_add<VEC>(g[k], g[k], -s1);
+        v_fma<VEC>(g[k], xh[k], -s2, g[k]);
         if (has_dh) {
           V::widen(rh[k], w);
+          v_fma<VEC>(g[k], g[k], rsh, w);
         } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) w[e] = 0.f;
+          v_mul<VEC>(g[k], g[k], rsh);
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) g[k][e] = w[e] + rsh * (g[k][e] - s1 - xh[k][e] * s2);
         V::st(static_cast<T*>(a.dr) + off + c, g[k]);
         V::widen(rb[k], b);
         if (POST) {
           load_or<T, VEC>(pg, c, 1.f, w);
           load_or<T, VEC>(pb, c, 0.f, u);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            b[e] = (b[e] - mb) * rsb;
-            u[e] = fmaf(b[e], w[e], u[e]);
-          }
+          v_add<VEC>(b, b, -mb);
+          v_mul<VEC>(b, b, rsb);
+          v_fma<VEC>(u, b, w, u);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) u[e] = b[e];
         }
+        // g: scale·dh from here on.
+        v_mul<VEC>(g[k], g[k], scale);
         if (GATE == GATE_ROW) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) u[e] *= scale * g[k][e];
+          v_mul<VEC>(u, u, g[k]);
           if (a.dgate) V::st(static_cast<T*>(a.dgate) + off + c, u);
         } else if (a.gate_kind == GATE_CHANNEL) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sum_to(S_GATE, k, c, e, scale * u[e] * g[k][e]);
+          sum_dot(S_GATE, k, c, u, g[k]);
         }
-        if (GATE == GATE_ROW)
+        if (GATE == GATE_ROW) {
           V::widen(rg[k], u);
-        else
-          load_or<T, VEC>(gate, c, 1.f, u);
+          v_mul<VEC>(g[k], g[k], u);
+        } else if (a.gate_kind == GATE_CHANNEL) {
+          load<T, VEC>(gate + c, u);
+          v_mul<VEC>(g[k], g[k], u);
+        }
+        if (POST) {
+          sum_dot(S_PG, k, c, g[k], b);
+          sum_add(S_PB, k, c, g[k]);
+          v_mul<VEC>(g[k], g[k], w);
+          q1.add(g[k]);
+          q2.dot(g[k], b);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          g[k][e] *= scale * u[e];
-          if (POST) {
-            sum_to(S_PG, k, c, e, g[k][e] * b[e]);
-            sum_to(S_PB, k, c, e, g[k][e]);
-            g[k][e] *= w[e];
-            t1 += g[k][e];
-            t2 = fmaf(g[k][e], b[e], t2);
-            xh[k][e] = b[e];
-          }
+          for (int e = 0; e < VEC; ++e) xh[k][e] = b[e];
         }
       }
     }
+    float t1 = 0.f, t2 = 0.f;
     if (POST) {
+      t1 = q1.total();
+      t2 = q2.total();
       sum2<TPR, BT>(t1, t2, red, sub, use + 1);
       t1 *= inv;
       t2 *= inv;
@@ -221,8 +225,9 @@ resnorm_bwd_kernel(ResNormArgs a) {
       const int c = (k * TPR + t) * VEC;
       if (c < D) {
         if (POST) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) g[k][e] = rsb * (g[k][e] - t1 - xh[k][e] * t2);
+          v_add<VEC>(g[k], g[k], -t1);
+          v_fma<VEC>(g[k], xh[k], -t2, g[k]);
+          v_mul<VEC>(g[k], g[k], rsb);
         }
         V::st(static_cast<T*>(a.db) + off + c, g[k]);
       }

@@ -20,24 +20,18 @@ constexpr int kThreads = kRowThreads;
 template <int VEC, int TPR, int NV>
 __device__ __forceinline__ void centre(float (&v)[NV][VEC], int t, int D, float eps, float* red,
                                        float* mean, float* rstd) {
-  float s = 0.f;
+  Sum2<VEC> s, q;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s += v[k][e];
-  const float mu = row_sum<TPR>(s, red) / (float)D;
-  float q = 0.f;
+  for (int k = 0; k < NV; ++k) s.add(v[k]);
+  const float mu = row_sum<TPR>(s.total(), red) / (float)D;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if ((k * TPR + t) * VEC < D) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[k][e] -= mu;
-        q = fmaf(v[k][e], v[k][e], q);
-      }
+      v_add<VEC>(v[k], v[k], -mu);
+      q.dot(v[k], v[k]);
     }
   *mean = mu;
-  *rstd = 1.f / sqrtf(row_sum<TPR>(q, red) / (float)D + eps);
+  *rstd = 1.f / sqrtf(row_sum<TPR>(q.total(), red) / (float)D + eps);
 }
 
 template <typename T, int VEC, int TPR, int E, int POST>
@@ -77,13 +71,13 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
       float p[VEC];
       load_or<T, VEC>(static_cast<const T*>(a.pg), c, 1.f, w);
       load_or<T, VEC>(static_cast<const T*>(a.pb), c, 0.f, p);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[k][e] = fmaf(u[k][e] * rb, w[e], p[e]);
+      v_mul<VEC>(u[k], u[k], rb);
+      v_fma<VEC>(u[k], u[k], w, p);
     }
     load_or<T, VEC>(G, c, 1.f, w);
     V::widen(rr[k], r);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) u[k][e] = fmaf(a.scale * w[e], u[k][e], r[e]);
+    v_mul<VEC>(w, w, a.scale);
+    v_fma<VEC>(u[k], u[k], w, r);
     V::st(static_cast<T*>(a.h) + off + c, u[k]);
   }
   float mh, rh;
@@ -95,8 +89,8 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
     float w[VEC], p[VEC];
     load_or<T, VEC>(static_cast<const T*>(a.gamma), c, 1.f, w);
     load_or<T, VEC>(static_cast<const T*>(a.beta), c, 0.f, p);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) p[e] = fmaf(u[k][e] * rh, w[e], p[e]);
+    v_mul<VEC>(u[k], u[k], rh);
+    v_fma<VEC>(p, u[k], w, p);
     V::st(static_cast<T*>(a.y) + off + c, p);
   }
   if (t == 0) {
