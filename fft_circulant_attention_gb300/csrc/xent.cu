@@ -89,7 +89,9 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 
 // The list of the tokens that have a target (rows, tgt; inv: a token's place in
 // it; count: its length and whether X itself serves as its rows), their
-// statistics for the backward (stat: lse·log2(e) and the upstream gradient) and
+// statistics for the backward (stat: lse·log2(e) and the upstream gradient, 1 where
+// one value serves all: results are scaled by that in fp32, so that the target's
+// entry of d, near -1, is not rounded off for the factor's sake) and
 // their rows of X, dense and, for fp32, as bf16 terms; rows of zeros up to a
 // multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
 // other CTAs pack W.
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
       p.tgt[pos] = id;
       if (p.stat)
         p.stat[pos] = make_float2(__ldg(p.lse_in + t) * kLog2e,
-                                  __ldg(p.dloss + (p.dloss_each ? t : 0)));
+                                  p.dloss_each ? __ldg(p.dloss + t) : 1.f);
     } else if (t < t1 && p.loss) {
       p.loss[t] = 0.f;
       p.lse[t] = 0.f;
@@ -226,8 +228,9 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T* __restrict__ dX,
-               int tokens, int D, int pairs, int piece, int acc_tiles) {
+               int tokens, int D, int pairs, int piece, int acc_tiles, const float* factor) {
   pdl_wait();
+  const float f = factor ? __ldg(factor) : 1.f;
   const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= tokens) return;
   const int pos = __ldcg(inv + row);
@@ -248,6 +251,10 @@ xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T*
         v[0] += __ldcg(q);
       }
     }
+    if (pos >= 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+    }
     if (VEC == 4 && sizeof(T) == 4) {
       *reinterpret_cast<float4*>(to + c) = make_float4(v[0], v[1], v[2], v[3]);
     } else if (VEC == 4) {
@@ -262,11 +269,11 @@ xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T*
 int tiles(long long n, int m) { return (int)((n + m - 1) / m); }
 
 // Tiles of the vocabulary in a forward part: as many as leave each pair of CTAs
-// eight parts, at most eight.
+// sixteen parts, at most 32.
 int run_length(int V, int tokens, int pairs) {
   const long long all = (long long)tiles(V, kXtN) * tiles(tokens, kXtM);
-  const long long r = all / (8ll * pairs);
-  return r < 1 ? 1 : r > 8 ? 8 : (int)r;
+  const long long r = all / (16ll * pairs);
+  return r < 1 ? 1 : r > 32 ? 32 : (int)r;
 }
 
 }  // namespace
@@ -386,7 +393,7 @@ cudaError_t finish_dx(const cat_plan_s* p, const XentArgs& a, int tokens) {
   return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, kThreads / 32)),
                           dim3(kThreads), 0, p->stream, (const float*)c.dxacc, c.acc_pitch,
                           (const int*)c.inv, (const int*)c.count, static_cast<T*>(a.dx), tokens,
-                          p->D, c.pairs, c.piece, c.acc_tiles);
+                          p->D, c.pairs, c.piece, c.acc_tiles, a.dloss_each ? nullptr : a.dloss);
 }
 
 }  // namespace
@@ -415,6 +422,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.w = a.w;
   k.stat = c.stat;
   k.hit = c.hit;
+  k.factor = back && !a.dloss_each ? a.dloss : nullptr;
   k.part = c.part;
   k.d = c.d;
   k.dw = a.dw;

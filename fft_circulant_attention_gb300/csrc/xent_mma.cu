@@ -744,31 +744,38 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
             stores_commit();
           }
         }
-      } else if (a.dw_tma) {
+      } else {
+        if (a.factor && groups) {                  // (no tokens: zeros, whatever the factor)
+          const float f = __ldg(a.factor);
 #pragma unroll
-        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
-          if (col + 32 * h >= a.D) continue;
-          box_free();
-          if (F32)
-            stage_f32(box, lane, v + 32 * h);
-          else
-            stage_bf16(box, lane, v);
-          box_full();
-          if (lane == 0) {
-            store_box(&maps.dw, box, col + 32 * h, 0, t.v0 + r0);
-            stores_commit();
-          }
+          for (int i = 0; i < 64; ++i) v[i] *= f;
         }
-      } else if (t.v0 + row < a.V) {
-        const size_t to = (size_t)(t.v0 + row) * a.D + col;
+        if (a.dw_tma) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (col + i < a.D) {
+          for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+            if (col + 32 * h >= a.D) continue;
+            box_free();
             if (F32)
-              static_cast<float*>(a.dw)[to + i] = v[i];
+              stage_f32(box, lane, v + 32 * h);
             else
-              static_cast<__nv_bfloat16*>(a.dw)[to + i] = __float2bfloat16_rn(v[i]);
+              stage_bf16(box, lane, v);
+            box_full();
+            if (lane == 0) {
+              store_box(&maps.dw, box, col + 32 * h, 0, t.v0 + r0);
+              stores_commit();
+            }
           }
+        } else if (t.v0 + row < a.V) {
+          const size_t to = (size_t)(t.v0 + row) * a.D + col;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (col + i < a.D) {
+              if (F32)
+                static_cast<float*>(a.dw)[to + i] = v[i];
+              else
+                static_cast<__nv_bfloat16*>(a.dw)[to + i] = __float2bfloat16_rn(v[i]);
+            }
+        }
       }
     }
     if (t.kind == LSE && t.last) {

@@ -52,6 +52,7 @@ struct XentMma {
   const int* rows_of;                    // the list's tokens
   const void* x; const void* w;          // X and W as they are
   const float2* stat;
+  const float* factor;                   // of dW (d is without it), or null: 1
   float* hit;
   float2* part;
   void* d;

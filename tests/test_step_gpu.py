@@ -634,6 +634,36 @@ def test_xent_repeats_streams_and_graph(dtype):
     plan.close()
 
 
+def test_xent_one_factor_for_all_tokens_loses_nothing():
+    # With one upstream value for all tokens dx and dw are scaled by it in fp32: as
+    # near as with the value 1, whatever its own rounding to bf16 would be; and
+    # gradients of no tokens are zero, whatever it is.
+    T, V, D = 400, 700, 64
+    x, w, targets = xent_inputs(T, V, D, "bf16", seed=16, sharp=0.5)
+    with cat.XentPlan(T, V, D, "bf16") as plan:
+        _, lse = plan.forward(dev(x), dev(w), dev(targets))
+        off = []
+        for up in (1.0, 2.0 ** -7 * (1 + 2.0 ** -8)):       # (half a step from a bf16 value)
+            up = torch.tensor(up)
+            got = plan.backward(dev(x), dev(w), dev(targets), lse, dev(up))
+            want, _, _ = ref.xent_backward(x, w, targets, lse.cpu(), up, "bf16")
+            for n, t in zip(("dx", "dw"), got):
+                check(n, t, want[n])
+                off.append(float((t.double().cpu() - want[n][0]).norm() / want[n][0].norm()))
+        # A rounding to bf16 is off by an even spread within 2^-8 / x of a value of
+        # mantissa x in 1 .. 2: in the root mean square, over mantissas spread by their
+        # logarithm, 2^-8 / sqrt(3) · sqrt(3 / (8 ln 2)) = 0.42 · 2^-8.  Two of them
+        # meet, d's and the result's: 0.60 · 2^-8.  The factor's own would add all of
+        # its 2^-8, the same way everywhere.
+        assert max(off) <= 0.75 * 2.0 ** -8, off
+        for up in (math.nan, math.inf):
+            dx, dw = plan.backward(dev(x), dev(w), torch.full_like(dev(targets), -1), lse,
+                                   torch.full((), up, device=DEV))
+            assert (dx == 0).all() and (dw == 0).all()
+        assert plan.backward(dev(x), dev(w), dev(targets), lse,
+                             torch.full((), math.nan, device=DEV))[1].isnan().all()
+
+
 def test_xent_two_plans_on_two_streams():
     T, V, D = 300, 3001, 64
     x, w, targets = (dev(t) for t in xent_inputs(T, V, D, "bf16", 0.8, seed=15))
