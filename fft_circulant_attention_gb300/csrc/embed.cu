@@ -180,7 +180,6 @@ embed_split_kernel(Ids ids, int tokens, int V, int per, int ranges, unsigned mag
   __shared__ int red[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b0 = blockIdx.x * per;
-  pdl_trigger();
   const int steps = per / kSortThreads;
   const int t0 = b0 + warp * steps * 32;
   int* h = hist + warp * ranges;
@@ -226,7 +225,6 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
   const int ranges = gridDim.x, lo = blockIdx.x * range, n = min(range, V - lo);
   int* h = hist + warp * n;
   for (int i = lane; i < n; i += 32) h[i] = 0;
-  pdl_trigger();
   pdl_wait();
   int below = 0, own, base, start;
   if ((int)threadIdx.x < blocks) {
@@ -306,7 +304,6 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   using Vc = Vec<T, VEC>;
   const int c = (blockIdx.y * TPR + threadIdx.x % TPR) * VEC;
   const bool in = c < D;
-  pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x >= piece_ctas) {
     __shared__ int none[kZeroRows];

@@ -70,7 +70,6 @@ resnorm_bwd_kernel(ResNormArgs a) {
   __shared__ float2 red[4 * (BT / 32)];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, D = a.D;
   float acc[kSums][kShared ? 1 : NV][VEC];
-  pdl_trigger();
   if (kShared) {
     for (int c = threadIdx.x; c < kSums * D; c += BT) sm[c] = 0.f;
     __syncthreads();

@@ -98,7 +98,6 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 template <typename T>
 __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
   const int vecs = p.pitch / 8;
-  pdl_trigger();
   if ((int)blockIdx.x >= p.list_ctas) {
     const long long n = (long long)p.V * vecs;
     const long long step = (long long)(gridDim.x - p.list_ctas) * kPrep;
@@ -293,7 +292,7 @@ void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   // of the vocabulary at once where there are few tokens, and less where two
   // pieces' d would take more than 2 GB.
   const int nt = tiles(D, kXtN), vt = tiles(c->V, kXtN);
-  long long w = 16384 / c->rows_alloc;
+  long long w = 32768 / c->rows_alloc;
   if (w < 1) w = 1;
   long long pt = w * pairs / nt;
   const long long tile_bytes = (long long)c->rows_alloc * kXtN * 2 * c->terms;

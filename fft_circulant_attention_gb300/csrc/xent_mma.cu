@@ -823,7 +823,6 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
     mbar_fence_init();
   }
   if (warp == 2) pair_alloc(smem_addr(&tslot), 2 * kAccCols);
-  pdl_trigger();
   pdl_wait();
   const int n = __ldcg(a.count), direct = __ldcg(a.count + 1);
   if (warp == 3) make_plan(a, n, &plan);
