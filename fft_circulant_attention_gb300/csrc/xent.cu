@@ -175,11 +175,12 @@ __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
     p.count[1] = direct;
   }
   if (direct) return;
-  __syncthreads();
+  __syncthreads();                       // (rows that this CTA's threads wrote)
   // This CTA's rows of the list, the last CTA those behind it too.
   const bool tail = (int)blockIdx.x == p.list_ctas - 1;
   const int end = tail ? (all + 255) / 256 * 256 : place;
   const int n = (end - before) * vecs;
+#pragma unroll 2
   for (int i = threadIdx.x; i < n; i += kPrep) {
     const int r = i / vecs, pos = before + r;
     const T* src = pos < all ? static_cast<const T*>(p.x) + (size_t)p.rows[pos] * p.D : nullptr;
@@ -222,45 +223,56 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
 }
 
 // dX's rows from the sums of the list's (the slices of each, in order), zeros for
-// the tokens without a target.  A warp a row, in vectors of four where they divide
-// it.
+// the tokens without a target.  A warp takes kDxRows rows side by side, in vectors of
+// four where they divide a row.
+constexpr int kDxRows = 4;
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 xent_dx_kernel(const float* acc, int pitch, const int* inv, const int* count, T* __restrict__ dX,
                int tokens, int D, int pairs, int piece, int acc_tiles, const float* factor) {
   pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int row0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kDxRows;
+  if (row0 >= tokens) return;
   const float f = factor ? __ldg(factor) : 1.f;
-  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= tokens) return;
-  const int pos = __ldcg(inv + row);
   const int mt = (__ldcg(count) + kXtM - 1) / kXtM;
-  const int slices = pos >= 0 ? xent_slices(pairs, mt, (D + kXtN - 1) / kXtN, piece, acc_tiles) : 0;
+  const int slices = mt ? xent_slices(pairs, mt, (D + kXtN - 1) / kXtN, piece, acc_tiles) : 0;
   const size_t apart = (size_t)mt * kXtM * pitch;
-  const float* from = acc + (pos >= 0 ? (size_t)pos * pitch : 0);
-  T* to = dX + (size_t)row * D;
-#pragma unroll 4
+  int pos[kDxRows];
+#pragma unroll
+  for (int r = 0; r < kDxRows; ++r) pos[r] = row0 + r < tokens ? __ldcg(inv + row0 + r) : -1;
   for (int c = lane * VEC; c < D; c += 32 * VEC) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const float* q = from + c;
-    for (int s = 0; s < slices; ++s, q += apart) {
-      if (VEC == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      } else {
-        v[0] += __ldcg(q);
+    float v[kDxRows][4] = {};
+    for (int s = 0; s < slices; ++s) {
+#pragma unroll
+      for (int r = 0; r < kDxRows; ++r) {
+        if (pos[r] < 0) continue;
+        const float* q = acc + s * apart + (size_t)pos[r] * pitch + c;
+        if (VEC == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
+          v[r][0] += x.x; v[r][1] += x.y; v[r][2] += x.z; v[r][3] += x.w;
+        } else {
+          v[r][0] += __ldcg(q);
+        }
       }
     }
-    if (pos >= 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= f;
-    }
-    if (VEC == 4 && sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(to + c) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if (VEC == 4) {
-      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
-      *reinterpret_cast<uint2*>(to + c) = *reinterpret_cast<uint2*>(h);
-    } else {
-      st_elem(to + c, v[0]);
+    for (int r = 0; r < kDxRows; ++r) {
+      if (row0 + r >= tokens) break;
+      if (pos[r] >= 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[r][e] *= f;
+      }
+      T* to = dX + (size_t)(row0 + r) * D + c;
+      if (VEC == 4 && sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(to) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+      } else if (VEC == 4) {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[r][0], v[r][1]),
+                               __floats2bfloat162_rn(v[r][2], v[r][3])};
+        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<uint2*>(h);
+      } else {
+        st_elem(to, v[r][0]);
+      }
     }
   }
 }
@@ -389,7 +401,7 @@ bool make_maps(const cat_plan_s* p, const XentArgs& a, int tokens, bool back, Xe
 template <typename T, int VEC>
 cudaError_t finish_dx(const cat_plan_s* p, const XentArgs& a, int tokens) {
   const XentCfg& c = p->xe;
-  return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, kThreads / 32)),
+  return launch_dependent(xent_dx_kernel<T, VEC>, dim3(tiles(tokens, kThreads / 32 * kDxRows)),
                           dim3(kThreads), 0, p->stream, (const float*)c.dxacc, c.acc_pitch,
                           (const int*)c.inv, (const int*)c.count, static_cast<T*>(a.dx), tokens,
                           p->D, c.pairs, c.piece, c.acc_tiles, a.dloss_each ? nullptr : a.dloss);

@@ -731,6 +731,90 @@ def test_xent_refusals():
 
 
 # --------------------------------------------------------------------- together
+def test_plans_with_a_stream_of_their_own():
+    # All calls on the plans' stream, the default stream busy; outputs that a call
+    # allocates belong to that stream.
+    g = gen(30)
+    T, V, D = 500, 900, 64
+    ids = ids_of("zipf", T, V, g).to(DEV)
+    w = ref.rnd(g, V, D, dtype="bf16").to(DEV)
+    t = {k: dev(v) for k, v in norm_inputs(T, D, "bf16", "channel", True, seed=31).items()}
+    up = torch.full((), 0.01, device=DEV)
+
+    def step(embed, res, xent):
+        x = embed.forward(ids, w)
+        h, y, stats = res.forward(x, t["b"], t["gate"], t["gamma"], t["beta"], t["pg"], t["pb"])
+        loss, lse = xent.forward(y, w, ids)
+        dy, dw = xent.backward(y, w, ids, lse, up)
+        grads = res.backward(h, t["b"], t["gate"], t["gamma"], t["pg"], t["pb"], stats, None, dy)
+        embed.backward(ids, grads[0], dW=dw, accumulate=True)
+        return (x, h, y, stats, loss, lse, dy, dw) + tuple(grads)
+
+    def plans(stream):
+        return (cat.EmbedPlan(T, V, D, "bf16", stream=stream),
+                cat.ResNormPlan(T, D, "bf16", post=True, stream=stream),
+                cat.XentPlan(T, V, D, "bf16", stream=stream))
+
+    want = step(*plans(None))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    own = plans(side)
+    for _ in range(5):
+        torch.cuda._sleep(3_000_000)
+        scratch = [torch.randn(T * D, device=DEV) for _ in range(4)]
+        del scratch
+        got = step(*own)
+        side.synchronize()
+        for p in own:
+            p.sync()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    for p in own:
+        p.close()
+    with pytest.raises(ValueError):
+        own[0].forward(ids, w)                  # closed
+
+
+def test_a_step_in_one_graph():
+    # Captured once, replayed with other ids, targets and weights.
+    T, V, D = 640, 1200, 96
+    g = gen(32)
+    ids = torch.randint(0, V, (T,), generator=g).to(DEV)
+    targets = torch.randint(0, V, (T,), generator=g).to(DEV)
+    w = ref.rnd(g, V, D, scale=0.3, dtype="bf16").to(DEV)
+    b = ref.rnd(g, T, D, dtype="bf16").to(DEV)
+    up = torch.full((), 0.01, device=DEV)
+    embed, res = cat.EmbedPlan(T, V, D, "bf16"), cat.ResNormPlan(T, D, "bf16", scale=0.5)
+    xent = cat.XentPlan(T, V, D, "bf16")
+
+    def step():
+        x = embed.forward(ids, w)
+        h, y, stats = res.forward(x, b)
+        loss, lse = xent.forward(y, w, targets)
+        dy, dw = xent.backward(y, w, targets, lse, up)
+        dr, db = res.backward(h, b, None, None, None, None, stats, None, dy)[:2]
+        return loss, dw, db, embed.backward(ids, dr)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in range(3):
+        h = gen(40 + seed)
+        ids.copy_(ids_of("zipf", T, V, h))
+        kept = torch.randint(0, V, (T,), generator=h)
+        kept[torch.rand(T, generator=h) < (0.0, 0.5, 1.0)[seed]] = -1
+        targets.copy_(kept)
+        w.copy_(ref.rnd(h, V, D, scale=0.3, dtype="bf16"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(held, step()):
+            assert torch.equal(a, c), seed
+    for p in (embed, res, xent):
+        p.sync()
+
+
 @pytest.mark.parametrize("tied", [False, True])
 def test_training_step_of_a_small_language_model(tied):
     """Embedding, a CAT layer and an attention layer with the residual stream
