@@ -28,6 +28,7 @@ struct XentMaps {
 // of its own: as many as give each pair of CTAs a tile, at least eight K stages a
 // slice.
 __host__ __device__ inline int xent_slices(int pairs, int mt, int nt, int piece, int acc_tiles) {
+  if (mt < 1) return 1;
   int s = pairs / (mt * nt);
   if (s > acc_tiles / mt) s = acc_tiles / mt;
   if (s > piece / (8 * kXtK)) s = piece / (8 * kXtK);

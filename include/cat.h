@@ -522,7 +522,10 @@ int cat_plan_create_xent(cat_plan_t *out, int max_tokens, int V, int D,
  * cat_xent_forward — for T tokens, X [T, D], W [V, D] and targets [T]:
  *   l_iv = X_i·W_v,  lse[i] = log Σ_v exp(l_iv),  loss[i] = lse[i] - l_{i,targets[i]}
  * (fp32).  Tokens without a target: both are 0, their rows of X are not read.
- * The logits are not kept.  T = 0: no-op.
+ * The logits are not kept.  Products run on the tensor cores with fp32 sums, fp32
+ * operands as three bf16 terms (errors of fp32's own size); an fp32 logit that is
+ * not finite is computed again by its definition, one by one, so that weights of
+ * minus infinity rule ids out.  T = 0: no-op.
  */
 int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
                      const void *targets, int id_type, float *loss, float *lse,
@@ -535,7 +538,11 @@ int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
  *   d_iv = dloss_i (exp(l_iv - lse_i) - [v = targets_i]),  dX = d·W,  dW = dᵀ·X.
  * The logits are made again, a piece of the vocabulary at a time.  dX [T, D]
  * and dW [V, D] are overwritten; either may be NULL (not wanted).  Tokens
- * without a target have a zero row in dX and no part in dW.
+ * without a target have a zero row in dX and no part in dW; their dloss and lse
+ * are not read.  For bf16 data d_iv is rounded to bf16 as an operand of the
+ * products (a half step of 2^-8 of each; one dloss for all tokens is applied to
+ * the results instead), for fp32 data it is three bf16 terms.  Gradients that a
+ * value takes part in that is not finite are not finite.
  * CAT_ERR_PLAN_MISMATCH too for a plan with grad = 0.
  */
 int cat_xent_backward(cat_plan_t plan, const void *X, const void *W,

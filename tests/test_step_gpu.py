@@ -494,6 +494,36 @@ def test_xent_long(dtype):
     xent_parity(260, 20011, 128, dtype, seed=6)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,kept,room", [
+    (300, 20011, 64, 1.0, 65536), (700, 9000, 520, 0.9, 65536), (5, 17000, 40, 1.0, 65536),
+    (1300, 8193, 72, 0.3, 66000), (64, 16384, 96, 0.0, 65536),
+])
+def test_xent_pieces(T, V, D, kept, room, dtype):
+    # A plan for many tokens takes its vocabulary in several pieces, here with few.
+    x, w, targets = xent_inputs(T, V, D, dtype, kept, seed=T)
+    up = torch.rand(T, generator=gen(T + 1)) + 0.1
+    with cat.XentPlan(room, V, D, dtype) as plan:
+        piece = int(plan.describe().split("piece=")[1].split()[0])
+        assert piece < V
+        for _ in range(2):
+            loss, lse = plan.forward(dev(x), dev(w), dev(targets))
+            dx, dw = plan.backward(dev(x), dev(w), dev(targets), lse, dev(up))
+        only = plan.backward(dev(x), dev(w), dev(targets), lse, dev(up), dX=False)[1]
+        assert torch.equal(only, dw)
+        only = plan.backward(dev(x), dev(w), dev(targets), lse, dev(up), dW=False)[0]
+        assert torch.equal(only, dx)
+        plan.sync()
+    for n, v in ref.xent_forward(x, w, targets).items():
+        check(n, dict(loss=loss, lse=lse)[n], v)
+    want, n_dx, n_dw = ref.xent_backward(x, w, targets, lse.cpu(), up, dtype)
+    check("dx", dx, want["dx"])
+    check("dw", dw, want["dw"])
+    if dtype == "f32":
+        near(dx, want["dx"][0], n_dx)
+        near(dw, want["dw"][0], n_dw)
+
+
 @pytest.mark.parametrize("sharp", [0.0, 30.0])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_xent_flat_and_sharp(sharp, dtype):
@@ -539,6 +569,37 @@ def test_xent_a_nan_stays_in_its_token():
         w[3, 0] = math.inf
         loss, _ = plan.forward(dev(x), dev(w), dev(targets))
         assert not (loss.isfinite() & (dev(x)[:, 0] > 0)).any()
+
+
+@pytest.mark.parametrize("where", ["x", "w"])
+def test_xent_f32_values_that_are_not_finite(where):
+    # fp32 operands go as terms: logits with an infinity or a NaN are those of their
+    # definition all the same, in every place of a tile.
+    T, V, D = 300, 600, 48
+    x, w, targets = xent_inputs(T, V, D, "f32", seed=17)
+    for i, v in ((3, math.inf), (130, -math.inf), (299, math.nan)):
+        (x if where == "x" else w)[i, i % D] = v
+    with cat.XentPlan(T, V, D, "f32") as plan:
+        loss, lse = plan.forward(dev(x), dev(w), dev(targets))
+        plan.sync()
+    if where == "w":
+        # Every token meets the NaN; without its row the infinities decide.
+        assert lse.isnan().all()
+        w[299] = 0.0
+        keep = (x[:, 3] < 0) & (x[:, 130 % D] > 0)      # both of them minus infinity
+        assert keep.any() and not keep.all()
+        rest = [i for i in range(V) if i not in (3, 130)]
+        with cat.XentPlan(T, V, D, "f32") as plan:
+            loss, lse = plan.forward(dev(x), dev(w), dev(targets))
+        val, bound = ref.xent_forward(x, w[rest], torch.zeros(T, dtype=torch.int64))["lse"]
+        check("lse", lse[dev(keep)], (val[keep], bound[keep]))
+        assert not lse[dev(~keep)].isfinite().any()
+    else:
+        bad = torch.zeros(T, dtype=torch.bool)
+        bad[[3, 130, 299]] = True
+        val, bound = ref.xent_forward(x[~bad], w, targets[~bad])["lse"]
+        check("lse", lse[dev(~bad)], (val, bound))
+        assert not lse[dev(bad)].isfinite().any()
 
 
 def test_xent_minus_infinity_is_a_logit_of_its_own():
