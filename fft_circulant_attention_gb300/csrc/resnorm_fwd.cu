@@ -17,7 +17,7 @@ constexpr int kThreads = kRowThreads;
 
 // Mean and 1/sqrt(variance + eps) of the row whose vectors are v (elements
 // from D on are 0); v is centred.
-template <int VEC, int TPR, int NV>
+template <int VEC, int TPR, int NV, bool FULL>
 __device__ __forceinline__ void centre(float (&v)[NV][VEC], int t, int D, float eps, float* red,
                                        float* mean, float* rstd) {
   Sum2<VEC> s, q;
@@ -26,7 +26,7 @@ __device__ __forceinline__ void centre(float (&v)[NV][VEC], int t, int D, float 
   const float mu = row_sum<TPR>(s.total(), red) / (float)D;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    if ((k * TPR + t) * VEC < D) {
+    if (FULL || (k * TPR + t) * VEC < D) {
       v_add<VEC>(v[k], v[k], -mu);
       q.dot(v[k], v[k]);
     }
@@ -34,7 +34,8 @@ __device__ __forceinline__ void centre(float (&v)[NV][VEC], int t, int D, float 
   *rstd = 1.f / sqrtf(row_sum<TPR>(q.total(), red) / (float)D + eps);
 }
 
-template <typename T, int VEC, int TPR, int E, int POST>
+// FULL: the threads' vectors are the row, none lies behind it.
+template <typename T, int VEC, int TPR, int E, int POST, bool FULL>
 __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
   constexpr int NV = E / VEC;
   using V = Vec<T, VEC>;
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + t) * VEC;
-    if (c < D) {
+    if (FULL || c < D) {
       load<T, VEC>(B + c, u[k]);
       rr[k] = V::ldr(R + c);
     } else {
@@ -61,11 +62,11 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
     }
   }
   float mb = 0.f, rb = 0.f;
-  if (POST) centre<VEC, TPR, NV>(u, t, D, a.eps, red, &mb, &rb);
+  if (POST) centre<VEC, TPR, NV, FULL>(u, t, D, a.eps, red, &mb, &rb);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + t) * VEC;
-    if (c >= D) continue;
+    if (!FULL && c >= D) continue;
     float w[VEC], r[VEC];
     if (POST) {
       float p[VEC];
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
     V::st(static_cast<T*>(a.h) + off + c, u[k]);
   }
   float mh, rh;
-  centre<VEC, TPR, NV>(u, t, D, a.eps, red, &mh, &rh);
+  centre<VEC, TPR, NV, FULL>(u, t, D, a.eps, red, &mh, &rh);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + t) * VEC;
-    if (c >= D) continue;
+    if (!FULL && c >= D) continue;
     float w[VEC], p[VEC];
     load_or<T, VEC>(static_cast<const T*>(a.gamma), c, 1.f, w);
     load_or<T, VEC>(static_cast<const T*>(a.beta), c, 0.f, p);
@@ -104,14 +105,19 @@ __global__ void __launch_bounds__(kThreads) resnorm_fwd_kernel(ResNormArgs a) {
   }
 }
 
-template <typename T, int VEC, int TPR, int E>
-cudaError_t fwd(const ResNormArgs& a, cudaStream_t st) {
+template <typename T, int VEC, int TPR, int E, bool FULL>
+cudaError_t go(const ResNormArgs& a, cudaStream_t st) {
   const int per = kThreads / TPR, grid = (a.rows + per - 1) / per;
   if (a.post)
-    resnorm_fwd_kernel<T, VEC, TPR, E, 1><<<grid, kThreads, 0, st>>>(a);
+    resnorm_fwd_kernel<T, VEC, TPR, E, 1, FULL><<<grid, kThreads, 0, st>>>(a);
   else
-    resnorm_fwd_kernel<T, VEC, TPR, E, 0><<<grid, kThreads, 0, st>>>(a);
+    resnorm_fwd_kernel<T, VEC, TPR, E, 0, FULL><<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int VEC, int TPR, int E>
+cudaError_t fwd(const ResNormArgs& a, cudaStream_t st) {
+  if (VEC > 1 && a.D == TPR * E) return go<T, VEC, TPR, E, VEC != 1>(a, st);
+  return go<T, VEC, TPR, E, false>(a, st);
 }
 
 // A warp a row while its lanes hold the row in at most 32 registers each (by
