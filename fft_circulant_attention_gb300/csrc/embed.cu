@@ -8,14 +8,13 @@
 // bit for bit.  Four launches:
 //   split: blocks of the tokens, each put in the order of ranges of ids;
 //   sort:  a CTA for each range takes its tokens from all blocks and puts them in
-//          the order of their ids.  Both count by warp (a warp has a stretch of
+//          the order of their ids, and clears the rows of ids without tokens.  Both count by warp (a warp has a stretch of
 //          the tokens) and keep the tokens' order within an id.  (One kernel whose
 //          CTAs each looked through all ids: 15 us for 16384 tokens, 33 for 65536.)
 //   sum:   the sorted list in pieces of equal length, a group of threads each; a
 //          run of equal ids that is no longer than a piece belongs to the piece it
 //          starts in and is a finished row, a longer one leaves a partial row
-//          (fp32) in each piece it touches.  Beside it the rows without tokens are
-//          cleared.
+//          (fp32) in each piece it touches;
 //   join:  the partial rows of each long run, in a fixed order.
 #include "cat_internal.h"
 #include "ids.cuh"
@@ -31,7 +30,6 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRange = 1024;        // most ids of a sorting CTA
 constexpr int kBlocks = 256;            // most CTAs of the sort's first step
-constexpr int kZeroRows = 64;           // ids whose rows a clearing CTA looks at
 constexpr int kFwdPerSm = 6;            // CTAs of an SM that look up
 constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
 
@@ -127,9 +125,10 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* total) {
 
 // A warp's counts of each class (hist [kSortWarps][classes]) become where its tokens
 // of that class start: classes in order from `base` on, within a class the warps.
-// Returns the number of all tokens; *start: of class threadIdx.x.
+// Returns the number of all tokens; *start, *own: of class threadIdx.x, where its
+// tokens start and how many they are.
 __device__ __forceinline__ int class_starts(int* hist, int classes, int base, int* red,
-                                            int* start) {
+                                            int* start, int* own) {
   const int c = threadIdx.x;
   int count = 0, all;
   if (c < classes) {
@@ -138,6 +137,7 @@ __device__ __forceinline__ int class_starts(int* hist, int classes, int base, in
   }
   int at = base + block_scan(count, red, &all);
   *start = at;
+  *own = count;
   if (c < classes) {
 #pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
@@ -194,8 +194,8 @@ embed_split_kernel(Ids ids, int tokens, int V, int per, int ranges, unsigned mag
   }
   if (bad) report(status, 0x702);
   __syncthreads();
-  int start;
-  const int all = class_starts(hist, ranges, 0, red, &start);
+  int start, own;
+  const int all = class_starts(hist, ranges, 0, red, &start, &own);
   int* o = off + (size_t)blockIdx.x * (ranges + 1);
   if ((int)threadIdx.x < ranges) o[threadIdx.x] = start;
   if (threadIdx.x == 0) o[ranges] = all;
@@ -217,16 +217,17 @@ embed_split_kernel(Ids ids, int tokens, int V, int per, int ranges, unsigned mag
 __global__ void __launch_bounds__(kSortThreads)
 embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, int per, int V,
                   int range, int* __restrict__ first, int* __restrict__ order,
-                  int* __restrict__ sid) {
+                  int* __restrict__ sid, unsigned char* dW, size_t row_bytes) {
   extern __shared__ int hist[];                 // [kSortWarps][range]
   __shared__ int red[kSortWarps];
+  __shared__ unsigned none[kSortRange / 32];    // ids without tokens
   __shared__ int2 part[kBlocks];                // where a block's tokens of this range lie
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranges = gridDim.x, lo = blockIdx.x * range, n = min(range, V - lo);
   int* h = hist + warp * n;
   for (int i = lane; i < n; i += 32) h[i] = 0;
   pdl_wait();
-  int below = 0, own, base, start;
+  int below = 0, own, base, start, count;
   if ((int)threadIdx.x < blocks) {
     const int* o = off + (size_t)threadIdx.x * (ranges + 1) + blockIdx.x;
     below = __ldcg(o);
@@ -255,9 +256,11 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
     for (int u = 0; u < U; ++u) warp_class<true>(h, id[u] >= 0, id[u] - lo);
   });
   __syncthreads();
-  own = class_starts(hist, n, base, red, &start);
+  own = class_starts(hist, n, base, red, &start, &count);
   if ((int)threadIdx.x < n) first[lo + threadIdx.x] = start;
   if (threadIdx.x == 0 && lo + n == V) first[V] = base + own;
+  const unsigned empty = __ballot_sync(0xffffffffu, (int)threadIdx.x < n && count == 0);
+  if (lane == 0) none[warp] = empty;
   tokens_of([&](int q, int end) {
     int id[U], t[U];
 #pragma unroll
@@ -275,6 +278,21 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
       }
     }
   });
+  // Rows of ids without tokens, where the gradient is not added to another's: the
+  // ranges with few tokens have most of them, and time while a full one sorts.
+  if (!dW) return;
+  __syncthreads();
+  for (int i = warp; i < n; i += kSortWarps) {
+    if (!(none[i >> 5] >> (i & 31) & 1)) continue;
+    unsigned char* row = dW + (size_t)(lo + i) * row_bytes;
+    if (row_bytes % 16 == 0) {
+      for (size_t c = lane * 16; c < row_bytes; c += 512)
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (size_t c = lane * 2; c < row_bytes; c += 64)
+        *reinterpret_cast<unsigned short*>(row + c) = 0;
+    }
+  }
 }
 
 // dst = scale·acc, or dst + scale·acc.
@@ -294,32 +312,16 @@ __device__ __forceinline__ void put(T* dst, const float* acc, float scale, bool 
 }
 
 // Pieces of P places of the sorted list, a group of TPR threads each (gridDim.y
-// blocks of TPR vectors cover a row), then CTAs that clear rows without tokens.
+// blocks of TPR vectors cover a row).
 template <typename T, int VEC, int TPR>
 __global__ void __launch_bounds__(kThreads)
 embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __restrict__ dY,
-                 T* dW, float* __restrict__ part, int V, int D, int P, int piece_ctas, float scale,
-                 int add) {
+                 T* dW, float* __restrict__ part, int V, int D, int P, float scale, int add) {
   constexpr int kGroups = kThreads / TPR;
   using Vc = Vec<T, VEC>;
   const int c = (blockIdx.y * TPR + threadIdx.x % TPR) * VEC;
   const bool in = c < D;
   pdl_wait();
-  if ((int)blockIdx.x >= piece_ctas) {
-    __shared__ int none[kZeroRows];
-    const int v0 = (blockIdx.x - piece_ctas) * kZeroRows;
-    if (threadIdx.x < kZeroRows) {
-      const int v = v0 + threadIdx.x;
-      none[threadIdx.x] = v < V && __ldcg(first + v) == __ldcg(first + v + 1);
-    }
-    __syncthreads();
-    float z[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) z[e] = 0.f;
-    for (int r = threadIdx.x / TPR; r < kZeroRows; r += kGroups)
-      if (in && none[r]) Vc::st(dW + (size_t)(v0 + r) * D + c, z);
-    return;
-  }
   const int piece = blockIdx.x * kGroups + threadIdx.x / TPR;
   const int total = __ldcg(first + V);
   const long long q0 = (long long)piece * P;
@@ -460,11 +462,10 @@ cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) 
   const int P = piece_length(a.tokens), pieces = (a.tokens + P - 1) / P;
   const int ctas = (pieces + groups - 1) / groups;
   const int cols = (D / VEC + TPR - 1) / TPR;
-  const int zero = a.add ? 0 : (c.V + kZeroRows - 1) / kZeroRows;
   cudaError_t e = launch_dependent(
-      embed_sum_kernel<T, VEC, TPR>, dim3(ctas + zero, cols), dim3(kThreads), 0, st,
+      embed_sum_kernel<T, VEC, TPR>, dim3(ctas, cols), dim3(kThreads), 0, st,
       (const int*)c.first, (const int*)c.order, (const int*)c.sid, static_cast<const T*>(a.x),
-      static_cast<T*>(a.y), c.part, c.V, D, P, ctas, c.scale, a.add);
+      static_cast<T*>(a.y), c.part, c.V, D, P, c.scale, a.add);
   if (e != cudaSuccess || pieces < 2) return e;
   return launch_dependent(embed_join_kernel<T>,
                           dim3((pieces + kLook - 1) / kLook, (D + 127) / 128),
@@ -496,7 +497,8 @@ cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, uns
   e = launch_dependent(embed_sort_kernel, dim3(ranges), dim3(kSortThreads),
                        (size_t)kSortWarps * c.range * sizeof(int), st, (const int*)c.tok,
                        (const int*)c.key, (const int*)c.off, blocks, per, c.V, c.range, c.first,
-                       c.order, c.sid);
+                       c.order, c.sid, a.add ? nullptr : static_cast<unsigned char*>(a.y),
+                       (size_t)D * sizeof(T));
   if (e != cudaSuccess) return e;
   if (nv <= 8) return sums<T, VEC, 8>(c, a, D, st);
   if (nv <= 32) return sums<T, VEC, 32>(c, a, D, st);
