@@ -314,7 +314,7 @@ __device__ __forceinline__ void put(T* dst, const float* acc, float scale, bool 
 // Pieces of P places of the sorted list, a group of TPR threads each (gridDim.y
 // blocks of TPR vectors cover a row).
 template <typename T, int VEC, int TPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __restrict__ dY,
                  T* dW, float* __restrict__ part, int V, int D, int P, float scale, int add) {
   constexpr int kGroups = kThreads / TPR;
