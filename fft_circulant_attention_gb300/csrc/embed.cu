@@ -12,9 +12,9 @@
 //          the tokens) and keep the tokens' order within an id.  (One kernel whose
 //          CTAs each looked through all ids: 15 us for 16384 tokens, 33 for 65536.)
 //   sum:   the sorted list in pieces of equal length, a group of threads each; a
-//          run of equal ids that is no longer than a piece belongs to the piece it
-//          starts in and is a finished row, a longer one leaves a partial row
-//          (fp32) in each piece it touches;
+//          run of equal ids within a piece, or of at most kLong places, belongs to
+//          the piece it starts in and is a finished row, a longer one leaves a
+//          partial row (fp32) in each piece it touches;
 //   join:  the partial rows of each long run, in a fixed order.
 #include "cat_internal.h"
 #include "ids.cuh"
@@ -30,6 +30,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRange = 1024;        // most ids of a sorting CTA
 constexpr int kBlocks = 256;            // most CTAs of the sort's first step
+constexpr int kLong = 16;               // places of a run that is not split
+constexpr int kSumPerSm = 4;            // CTAs of an SM that sum
 constexpr int kFwdPerSm = 6;            // CTAs of an SM that look up
 constexpr int kLookup = 1024;           // vectors of a looking-up CTA, about
 
@@ -236,12 +238,12 @@ embed_sort_kernel(const int* tok, const int* key, const int* off, int blocks, in
   }
   block_scan(below, red, &base);
   __syncthreads();
-  // A warp takes a stretch of the blocks; f(place, whether there is one) for its
-  // tokens, 128 at a time.  (Looking each token's block up cost more than the rest:
+  // A warp takes a stretch of the blocks; f(place, end of the block's) for its
+  // tokens, 256 at a time.  (Looking each token's block up cost more than the rest:
   // a range may hold a good part of all tokens.)
   const int each = (blocks + kSortWarps - 1) / kSortWarps;
   const int first_block = warp * each, last_block = min(blocks, first_block + each);
-  constexpr int U = 4;
+  constexpr int U = 8;
   auto tokens_of = [&](auto f) {
     for (int b = first_block; b < last_block; ++b) {
       const int2 s = part[b];
@@ -314,7 +316,7 @@ __device__ __forceinline__ void put(T* dst, const float* acc, float scale, bool 
 // Pieces of P places of the sorted list, a group of TPR threads each (gridDim.y
 // blocks of TPR vectors cover a row).
 template <typename T, int VEC, int TPR>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kSumPerSm)
 embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __restrict__ dY,
                  T* dW, float* __restrict__ part, int V, int D, int P, float scale, int add) {
   constexpr int kGroups = kThreads / TPR;
@@ -333,9 +335,9 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   const int ida = __ldcg(sid + p0), idb = __ldcg(sid + p1 - 1);
   const int a0 = __ldcg(first + ida), a1 = __ldcg(first + ida + 1);
   const int b0 = __ldcg(first + idb), b1 = __ldcg(first + idb + 1);
-  const bool a_long = a1 - a0 > P, b_long = b1 - b0 > P;
-  if (a0 < p0 && !a_long) p0 = a1;
-  if (b1 > p1 && !b_long) p1 = b1;
+  const bool a_part = a0 < p0 && a1 - a0 > kLong, b_part = b1 > p1 && b1 - b0 > kLong;
+  if (a0 < p0 && !a_part) p0 = a1;
+  if (b1 > p1 && !b_part) p1 = b1;
   if (p0 >= p1) return;
   float acc[VEC];
 #pragma unroll
@@ -344,11 +346,12 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   // The run of `cur` ends here (or at the piece's end).
   auto flush = [&] {
     if (in) {
-      if (!(a_long && cur == ida) && !(b_long && cur == idb)) {
+      const bool ahead = a_part && cur == ida;
+      if (!ahead && !(b_part && cur == idb)) {
         put<T, VEC>(dW + (size_t)cur * D + c, acc, scale, add);
       } else {
         // (A piece's first partial row, or that of a run that starts in it.)
-        float* q = part + ((size_t)piece * 2 + (cur == ida && a0 < (int)q0 ? 0 : 1)) * D + c;
+        float* q = part + ((size_t)piece * 2 + !ahead) * D + c;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) q[e] = acc[e];
       }
@@ -384,8 +387,8 @@ embed_sum_kernel(const int* first, const int* order, const int* sid, const T* __
   flush();
 }
 
-// The partial rows of the long runs (more than P places: one in each piece they
-// touch).  A CTA looks at kLook pieces, a lane each, for long runs that start in them,
+// The partial rows of the long runs that go over a piece's end: one in each piece
+// they touch.  A CTA looks at kLook pieces, a lane each, for long runs that start in them,
 // and joins those one after another: its warps add every so-many-th partial row
 // each, the warps' sums in order then.  (A thread adding a column's partial rows one
 // after another: 38 us for 16384 tokens, 66 pieces of the most frequent id.)
@@ -405,7 +408,7 @@ embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, in
   if (lane < kLook && q0 + P < total) {
     v = __ldcg(sid + q0 + P - 1);
     const int a = __ldcg(first + v), b = __ldcg(first + v + 1);
-    if (a < (int)q0 || b - a <= P) v = -1;
+    if (a < (int)q0 || b <= (int)q0 + P || b - a <= kLong) v = -1;
     last = (b - 1) / P;
   }
   unsigned left = __ballot_sync(0xffffffffu, v >= 0);
@@ -436,11 +439,16 @@ embed_join_kernel(const int* first, const int* sid, const float* part, T* dW, in
   }
 }
 
-// Places of a piece: at most 1024 pieces, so that a run of them all is joined
-// in a bounded time, and at least 16 places, so that partial rows stay few.
-int piece_length(int tokens) {
-  const int p = (tokens + 1023) / 1024;
-  return p < 16 ? 16 : p;
+// Places of a piece: one wave of the summing CTAs (`slots` groups of threads), at
+// most 1024 pieces, so that a run of them all is joined in a bounded time, and at
+// least kLong places, so that a short run lies in two pieces at most.  (With runs as
+// long as a piece taken whole the pieces differed by a factor of two: 77 us instead
+// of 66 for 65536 rows of 1024 fp32.)
+constexpr int kMaxPieces = 1024;
+int piece_length(int tokens, int slots) {
+  const int n = slots < 1 ? 1 : slots < kMaxPieces ? slots : kMaxPieces;
+  const int p = (tokens + n - 1) / n;
+  return p < kLong ? kLong : p;
 }
 
 // Tokens of a block of the sort's first step: a thread each, more where there would
@@ -457,11 +465,11 @@ int sort_range(int V, int sms) {
 }
 
 template <typename T, int VEC, int TPR>
-cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, cudaStream_t st) {
+cudaError_t sums(const EmbedCfg& c, const EmbedArgs& a, int D, int sms, cudaStream_t st) {
   const int groups = kThreads / TPR;
-  const int P = piece_length(a.tokens), pieces = (a.tokens + P - 1) / P;
-  const int ctas = (pieces + groups - 1) / groups;
   const int cols = (D / VEC + TPR - 1) / TPR;
+  const int P = piece_length(a.tokens, kSumPerSm * sms * groups / cols);
+  const int pieces = (a.tokens + P - 1) / P, ctas = (pieces + groups - 1) / groups;
   cudaError_t e = launch_dependent(
       embed_sum_kernel<T, VEC, TPR>, dim3(ctas, cols), dim3(kThreads), 0, st,
       (const int*)c.first, (const int*)c.order, (const int*)c.sid, static_cast<const T*>(a.x),
@@ -500,11 +508,11 @@ cudaError_t run(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward, uns
                        c.order, c.sid, a.add ? nullptr : static_cast<unsigned char*>(a.y),
                        (size_t)D * sizeof(T));
   if (e != cudaSuccess) return e;
-  if (nv <= 8) return sums<T, VEC, 8>(c, a, D, st);
-  if (nv <= 32) return sums<T, VEC, 32>(c, a, D, st);
-  if (nv <= 64) return sums<T, VEC, 64>(c, a, D, st);
-  if (nv <= 128) return sums<T, VEC, 128>(c, a, D, st);
-  return sums<T, VEC, 256>(c, a, D, st);
+  if (nv <= 8) return sums<T, VEC, 8>(c, a, D, sms, st);
+  if (nv <= 32) return sums<T, VEC, 32>(c, a, D, sms, st);
+  if (nv <= 64) return sums<T, VEC, 64>(c, a, D, sms, st);
+  if (nv <= 128) return sums<T, VEC, 128>(c, a, D, sms, st);
+  return sums<T, VEC, 256>(c, a, D, sms, st);
 }
 
 template <typename T, int FULL>
@@ -521,12 +529,10 @@ cudaError_t by_width(const EmbedCfg& c, const EmbedArgs& a, int D, bool backward
 int embed_range(int V, int sms) { return sort_range(V, sms); }
 
 size_t embed_part_count(int max_tokens, int D) {
-  const int P = piece_length(max_tokens);
-  // (Fewer tokens have at most as many pieces: below 1024 of them, one in 16.)
-  const size_t pieces = max_tokens > 16 * 1024 ? 1024 : (max_tokens + P - 1) / P;
-  return pieces * 2 * D;
+  // (Pieces have kLong places at least.)
+  const size_t most = ((size_t)max_tokens + kLong - 1) / kLong;
+  return (most < kMaxPieces ? most : kMaxPieces) * 2 * D;
 }
-
 size_t embed_split_count(int max_tokens) {
   // (Fewer tokens have blocks no longer than these.)
   const size_t per = block_tokens(max_tokens);
