@@ -452,10 +452,10 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     k.run = run_length(c.V, tokens, c.pairs);
     e = go(mt * tiles(tiles(c.V, kXtN), k.run));
     if (e != cudaSuccess) return e;
-    return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)),
-                            dim3(32 * kFinWarps), 0, st, (const float2*)c.part, 2 * tiles(tiles(c.V, kXtN), k.run),
-                            c.max_tokens, (const int*)c.count, (const int*)c.rows,
-                            (const float*)c.hit, a.loss, a.lse);
+    const int parts = 2 * tiles(tiles(c.V, kXtN), k.run);
+    return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)), dim3(32 * kFinWarps), 0,
+                            st, (const float2*)c.part, parts, c.max_tokens, (const int*)c.count,
+                            (const int*)c.rows, (const float*)c.hit, a.loss, a.lse);
   }
   // Piece i's products beside d of piece i + 1.
   for (int i = -1; i < c.pieces; ++i) {

@@ -99,6 +99,12 @@ def test_embed_adds_to_a_gradient(n, V, D, dtype):
     embed_parity(n, V, D, dtype, "one", seed=n + 1, accumulate=True)
 
 
+def test_embed_many_tokens():
+    # More tokens than blocks of the sort with a thread for each.
+    embed_parity(300001, 70, 8, "f32", "zipf", seed=5)
+    embed_parity(270000, 5000, 4, "bf16", "padded", False, seed=6, accumulate=True)
+
+
 def test_embed_large_vocabulary():
     # More ids than one sorting CTA an SM takes at its largest share.
     embed_parity(3000, 400001, 8, "bf16", "padded", seed=2)
@@ -492,6 +498,12 @@ def test_xent_long(dtype):
     # More than one piece of the vocabulary; more tokens than one block of the list.
     xent_parity(2100, 9001, 64, dtype, 0.9, seed=5)
     xent_parity(260, 20011, 128, dtype, seed=6)
+
+
+def test_xent_many_tokens():
+    # More tokens than a preparing CTA's 128 for each of its most CTAs.
+    xent_parity(270001, 40, 8, "bf16", 0.6, seed=18)
+    xent_parity(263000, 20, 12, "f32", 1.0, seed=19, each=False)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
