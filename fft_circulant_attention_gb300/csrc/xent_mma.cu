@@ -632,7 +632,8 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
       taken();
     }
     if (!limit) break;
-#pragma unroll
+    // (fp32 sums are in registers, two unrolled chunks; else the code stays small.)
+#pragma unroll (F32 ? 2 : 1)
     for (int c = 0; c < 2; ++c) {
       if (c >= chunks) continue;
       float* v = acc[F32 ? c : 0];
