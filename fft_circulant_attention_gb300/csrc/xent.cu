@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPrep = 1024;              // threads of the preparing kernel
 constexpr int kPer = 128;                // tokens of a CTA of it, at least
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // What the call's first kernel prepares.
 struct Prep {
@@ -89,11 +89,10 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 
 // The list of the tokens that have a target (rows, tgt; inv: a token's place in
 // it; count: its length and whether X itself serves as its rows), their
-// statistics for the backward (stat: lse·log2(e) and the upstream gradient, 1 where
-// one value serves all: results are scaled by that in fp32, so that the target's
-// entry of d, near -1, is not rounded off for the factor's sake) and
-// their rows of X, dense and, for fp32, as bf16 terms; rows of zeros up to a
-// multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
+// statistics for the backward (stat: lse and the upstream gradient, 1 where one
+// value serves all: results are scaled by that in fp32, so that the target's entry of
+// d, near -1, is not rounded off for the factor's sake) and their rows of X, dense
+// and, for fp32, as bf16 terms; rows of zeros up to a multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
 // other CTAs pack W.
 template <typename T>
 __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
@@ -162,8 +161,7 @@ __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
       p.rows[pos] = t;
       p.tgt[pos] = id;
       if (p.stat)
-        p.stat[pos] = make_float2(__ldg(p.lse_in + t) * kLog2e,
-                                  p.dloss_each ? __ldg(p.dloss + t) : 1.f);
+        p.stat[pos] = make_float2(__ldg(p.lse_in + t), p.dloss_each ? __ldg(p.dloss + t) : 1.f);
     } else if (t < t1 && p.loss) {
       p.loss[t] = 0.f;
       p.lse[t] = 0.f;
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
   }
 }
 
-// loss and lse from the parts' maxima (times log2(e)) and sums: 32 places of the
+// loss and lse from the parts' maxima and sums: 32 places of the
 // list a CTA, its warps every so-many-th part each (1024 tokens, 394 parts: 61 us
 // with a thread a place, 5 so).
 constexpr int kFinWarps = 16;
@@ -205,7 +203,7 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
   float top = -INFINITY, s = 0.f;
   auto join = [&](float2 q) {
     const float m = fmaxf(top, q.x), sh = m == -INFINITY ? 0.f : m;
-    s = s * exp2f(top - sh) + q.y * exp2f(q.x - sh);
+    s = s * exp2f((top - sh) * kLog2e) + q.y * exp2f((q.x - sh) * kLog2e);
     top = m;
   };
   if (pos < n) {
@@ -216,10 +214,12 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
   __syncthreads();
   if (warp || pos >= n) return;
   for (int w = 1; w < kFinWarps; ++w) join(red[w][lane]);
-  const float z = (top + log2f(s)) * kLn2;
+  // (Not lse less the target's logit, two large numbers: where the target rules its row
+  // the maximum less its logit is 0, and the loss as near as the sum is to 1.)
   const int t = __ldcg(rows + pos);
-  lse[t] = z;
-  loss[t] = z - __ldcg(hit + pos);
+  const float rest = logf(s);
+  lse[t] = top + rest;
+  loss[t] = top - __ldcg(hit + pos) + rest;
 }
 
 // dX's rows from the sums of the list's (the slices of each, in order), zeros for

@@ -525,7 +525,9 @@ int cat_plan_create_xent(cat_plan_t *out, int max_tokens, int V, int D,
  * The logits are not kept.  Products run on the tensor cores with fp32 sums, fp32
  * operands as three bf16 terms (errors of fp32's own size); an fp32 logit that is
  * not finite is computed again by its definition, one by one, so that weights of
- * minus infinity rule ids out.  T = 0: no-op.
+ * minus infinity rule ids out.  loss is (the largest logit - the target's) + log of
+ * the sum of exponentials of the differences to the largest: never negative, and no
+ * worse for large logits; lse is rounded to fp32 once.  T = 0: no-op.
  */
 int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
                      const void *targets, int id_type, float *loss, float *lse,
@@ -536,7 +538,8 @@ int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
  * gradient dloss of the losses (fp32: one value for all tokens, dloss_each = 0,
  * or [T], dloss_each = 1):
  *   d_iv = dloss_i (exp(l_iv - lse_i) - [v = targets_i]),  dX = d·W,  dW = dᵀ·X.
- * The logits are made again, a piece of the vocabulary at a time.  dX [T, D]
+ * The logits are made again, a piece of the vocabulary at a time; the probabilities
+ * of a row share the rounding of its lse (half a step, 2^-24 |lse|, relative).  dX [T, D]
  * and dW [V, D] are overwritten; either may be NULL (not wanted).  Tokens
  * without a target have a zero row in dX and no part in dW; their dloss and lse
  * are not read.  For bf16 data d_iv is rounded to bf16 as an operand of the

@@ -1,0 +1,98 @@
+"""GPU tests of the values that the training step's operators return where they are
+easily lost: differences of large logits."""
+import math
+
+import pytest
+import torch
+
+import fft_circulant_attention_gb300 as cat
+from _block_ref import H, TORCH, U, check
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def _built(cuda_device):
+    from fft_circulant_attention_gb300 import build
+    build.build()
+    cat.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# --------------------------------------------------------------- cross entropy
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D", [(1, 8), (700, 64), (300, 33)])
+def test_xent_of_a_single_id_is_zero(T, D, dtype):
+    # One id has probability one, whatever its logit (up to some 100 here).
+    g = gen(T)
+    x = (torch.randn(T, D, generator=g) * 4).to(TORCH[dtype])
+    w = torch.randn(1, D, generator=g).to(TORCH[dtype])
+    with cat.XentPlan(T, 1, D, dtype) as plan:
+        loss, lse = plan.forward(x.to(DEV), w.to(DEV), torch.zeros(T, dtype=torch.int64,
+                                                                  device=DEV))
+        assert (loss == 0).all()
+        assert lse.abs().max() > 4
+
+
+def separate_logits(T, V, dtype, seed):
+    """Logits that the products make exactly: W's rows are powers of two in columns of
+    their own.  Each row has its largest, 40 to 100, at its target or beside it, and
+    others from close behind it to far below."""
+    g = gen(seed)
+    targets = torch.randint(0, V, (T,), generator=g)
+    top = 0.5 * torch.randint(80, 201, (T, 1), generator=g).double()
+    down = 0.5 * torch.randint(0, 60, (T, V), generator=g).double()
+    logits = top - down.clamp(min=0.5) - 20 * (torch.rand(T, 1, generator=g) < 0.3)
+    at = torch.where(torch.rand(T, generator=g) < 0.8, targets, (targets + 1) % V)
+    logits[torch.arange(T), at] = top[:, 0]
+    c = 2.0 ** (torch.arange(V) % 3 - 1).double()
+    D = (V + 7) // 8 * 8
+    x, w = torch.zeros(T, D, dtype=torch.float64), torch.zeros(V, D, dtype=torch.float64)
+    x[:, :V] = logits / c
+    w[torch.arange(V), torch.arange(V)] = c
+    xt, wt = x.to(TORCH[dtype]), w.to(TORCH[dtype])
+    assert torch.equal(xt.double(), x) and torch.equal(wt.double(), w)
+    return xt, wt, targets, logits, c
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(2000, 2), (2000, 8), (500, 40), (500, 300)])
+def test_xent_of_confident_tokens(T, V, dtype):
+    # Where one logit rules its row the loss is a small difference of large numbers:
+    # it keeps its own size's accuracy all the same, and is never negative.
+    x, w, targets, l, c = separate_logits(T, V, dtype, V)
+    with cat.XentPlan(T, V, x.shape[1], dtype) as plan:
+        ins = [t.to(DEV) for t in (x, w, targets)]
+        loss, lse = plan.forward(*ins)
+        dx, _ = plan.backward(*ins, lse, torch.ones((), device=DEV))
+        plan.sync()
+    z = torch.logsumexp(l, 1)
+    down = l.amax(1, keepdim=True) - l
+    p = torch.exp(l - z[:, None])
+    # An exponential: its argument's factor and product are off by half a step each, the
+    # function by four; so is each of at most four scalings of a part's sum.  The sum:
+    # half a step for each addition one after another.  The logarithm two half steps.
+    e = torch.where(down > 0, p * (2 * down + 20) * H, torch.zeros_like(p)).sum(1) + \
+        (min(V, 32 + V // 64) + 4) * H
+    hit = l.gather(1, targets[:, None])[:, 0]
+    want = z - hit
+    e = e + 2 * H * (z - l.amax(1))
+    assert (loss >= 0).all()
+    check("loss", loss, (want, e + H * want))
+    check("lse", lse, (z, e + H * z.abs()))
+    # The gradients, from this very lse: l - lse and its product are off by three half
+    # steps, p by four; d and the result are rounded to the storage type.
+    z = lse.double().cpu()[:, None]
+    p = torch.exp(l - z)
+    hot = torch.zeros_like(p)
+    hot[torch.arange(T), targets] = 1.0
+    d = p - hot
+    e = p * (3 * (l - z).abs() + 4) * H + (4 * H + (2.1 * U[dtype] if dtype == "bf16" else 0)) * \
+        d.abs()
+    check("dx", dx[:, :V], (d * c, e * c))
