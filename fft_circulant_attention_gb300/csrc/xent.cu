@@ -202,7 +202,7 @@ xent_finish_kernel(const float2* part, int nparts, int ld, const int* count, con
   if (blockIdx.x * 32 >= n) return;
   float top = -INFINITY, s = 0.f;
   auto join = [&](float2 q) {
-    const float m = fmaxf(top, q.x), sh = m == -INFINITY ? 0.f : m;
+    const float m = fmaxf(top, q.x), sh = fabsf(m) < INFINITY ? m : 0.f;
     s = s * exp2f((top - sh) * kLog2e) + q.y * exp2f((q.x - sh) * kLog2e);
     top = m;
   };

@@ -697,7 +697,8 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
           float top = mx;
 #pragma unroll
           for (int i = 0; i < 64; ++i) top = fmaxf(top, v[i]);
-          const float sh = top == -INFINITY ? 0.f : top;
+          // (An infinite maximum is no difference to take: exp is 0 or infinite as it is.)
+          const float sh = fabsf(top) < INFINITY ? top : 0.f;
           float e0 = 0.f, e1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {

@@ -524,8 +524,8 @@ int cat_plan_create_xent(cat_plan_t *out, int max_tokens, int V, int D,
  * (fp32).  Tokens without a target: both are 0, their rows of X are not read.
  * The logits are not kept.  Products run on the tensor cores with fp32 sums, fp32
  * operands as three bf16 terms (errors of fp32's own size); an fp32 logit that is
- * not finite is computed again by its definition, one by one, so that weights of
- * minus infinity rule ids out.  loss is (the largest logit - the target's) + log of
+ * not finite is computed again by its definition, one by one.  So weights of minus
+ * infinity rule ids out, a logit of plus infinity makes lse that.  loss is (the largest logit - the target's) + log of
  * the sum of exponentials of the differences to the largest: never negative, and no
  * worse for large logits; lse is rounded to fp32 once.  T = 0: no-op.
  */

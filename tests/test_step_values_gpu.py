@@ -1,11 +1,12 @@
 """GPU tests of the values that the training step's operators return where they are
-easily lost: differences of large logits."""
+easily lost: differences of large logits, infinities."""
 import math
 
 import pytest
 import torch
 
 import fft_circulant_attention_gb300 as cat
+import _step_ref as ref
 from _block_ref import H, TORCH, U, check
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,71 @@ def test_xent_of_confident_tokens(T, V, dtype):
     e = p * (3 * (l - z).abs() + 4) * H + (4 * H + (2.1 * U[dtype] if dtype == "bf16" else 0)) * \
         d.abs()
     check("dx", dx[:, :V], (d * c, e * c))
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 64), ("bf16", 36)])
+def test_xent_infinite_weights(dtype, D):
+    # Logits of plus and minus infinity, and NaN where an infinity meets a zero: loss and
+    # lse are what the definition makes of them.
+    T, V = 400, 700
+    g = gen(D)
+    x = torch.randn(T, D, generator=g).to(TORCH[dtype])
+    w = (0.2 * torch.randn(V, D, generator=g)).to(TORCH[dtype])
+    targets = torch.randint(0, V, (T,), generator=g)
+    sign = torch.randint(-1, 2, (T, 3), generator=g)
+    sign[:200] = torch.tensor([-1, 1, -1])             # (all three are minus infinity)
+    x[:, :3] = sign.to(x.dtype) * x[:, :3].abs().clamp(min=0.1)
+    odd = {5: math.inf, 130: -math.inf, 699: math.inf}
+    for k, (v, value) in enumerate(odd.items()):
+        w[v, k] = value
+        targets[201 + k] = targets[k] = v
+    with cat.XentPlan(T, V, D, dtype) as plan:
+        loss, lse = (t.cpu() for t in plan.forward(*(t.to(DEV) for t in (x, w, targets))))
+        plan.sync()
+    l = (x.double()[:, None] * w.double()).sum(-1)
+    z = torch.logsumexp(l, 1)
+    want = z - l.gather(1, targets[:, None])[:, 0]
+    kinds = lambda t: (t.isnan(), t == math.inf, t == -math.inf)  # noqa: E731
+    for a, b in zip(kinds(z) + kinds(want), kinds(lse) + kinds(loss)):
+        assert torch.equal(a, b)
+    assert z[:200].isfinite().all()
+    assert (z == math.inf).any() and z.isnan().any() and (want[:3] == math.inf).all()
+    keep = [v for v in range(V) if v not in odd]
+    rows = torch.arange(3, 200)
+    rows = rows[torch.isin(targets[rows], torch.tensor(keep))]
+    assert len(rows) > 150 and want[rows].isfinite().all()
+    new = torch.zeros(V, dtype=torch.int64)
+    new[keep] = torch.arange(len(keep))
+    for n, v in ref.xent_forward(x[rows], w[keep], new[targets[rows]]).items():
+        check(n, dict(loss=loss, lse=lse)[n][rows], v)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_xent_infinite_hidden_states_stay_in_their_tokens(dtype):
+    T, V, D = 300, 500, 64
+    g = gen(3)
+    x = torch.randn(T, D, generator=g).to(TORCH[dtype])
+    w = (0.2 * torch.randn(V, D, generator=g)).to(TORCH[dtype])
+    targets = torch.randint(0, V, (T,), generator=g)
+    bad = [7, 140, 299]
+    dirty = x.clone()
+    for i in bad:
+        dirty[i, i % D] = math.inf
+    other = [i for i in range(T) if i not in bad]
+    one = torch.ones((), device=DEV)
+    with cat.XentPlan(T, V, D, dtype) as plan:
+        wd, td = w.to(DEV), targets.to(DEV)
+        got = []
+        for v in (x, dirty):
+            v = v.to(DEV)
+            loss, lse = plan.forward(v, wd, td)
+            got.append((loss, lse, plan.backward(v, wd, td, lse, one)[0]))
+        plan.sync()
+    for a, b in zip(*got):
+        assert torch.equal(a[other], b[other])
+    loss, lse, dx = got[1]
+    assert (lse[bad] == math.inf).all()
+    for i in bad:
+        up = float(w[targets[i], i % D]) > 0
+        assert loss[i].isnan() if up else loss[i] == math.inf
+        assert not dx[i].isfinite().any()
