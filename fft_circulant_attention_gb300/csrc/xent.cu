@@ -301,7 +301,8 @@ void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   c->acc_tiles = c->rows_alloc / kXtM + pairs / tiles(D, kXtN);
   // A piece of the vocabulary: dW's tiles (of the piece by D) are the longest of a
   // launch, so that their number is a multiple of the pairs, or just below; more
-  // of the vocabulary at once where there are few tokens, and less where two
+  // of the vocabulary at once where there are few tokens (the pairs then share a
+  // piece's ids out among slices of dX, of at most 65536 each), and less where two
   // pieces' d would take more than 2 GB.
   const int nt = tiles(D, kXtN), vt = tiles(c->V, kXtN);
   long long w = 32768 / c->rows_alloc;
@@ -444,7 +445,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   // (No more pairs than there is work for.)
   auto go = [&](long long work) {
     const int n = work < c.pairs ? (work < 1 ? 1 : (int)work) : c.pairs;
-    return launch_xent_mma(maps, k, p->dtype, n, st);
+    return launch_xent_mma(maps, k, p->dtype, n, k.dw_piece >= 0 ? tokens : 0, st);
   };
   const long long mt = tiles(tokens, kXtM), nt = tiles(p->D, kXtN), pt = c.piece / kXtN;
   if (!back) {

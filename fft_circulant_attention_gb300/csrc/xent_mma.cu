@@ -19,7 +19,11 @@
 //
 // fp32 operands are three bf16 terms each, of whose products the six that matter
 // are taken, smallest first; the accumulator, which cuts instead of rounding, is
-// read out every two stages of K and added up in registers.
+// read out every two stages of K and added up in registers.  A bf16 sum stays in its
+// accumulator for at most 65536 of K (dX's parts are never longer, see xent_shape; dW's
+// are read out and added up likewise): what is cut off summands of one sign adds up,
+// 0.0004 of the sum at that length, where half a step of the result is 0.004 (all of
+// 2^20 tokens in one: 0.0065).
 //
 // Roles of a CTA: warp 0 issues copies, warp 1 (of the pair's first CTA) the
 // MMAs, warp 2 holds the tensor memory (two accumulators of 256 columns), warps
@@ -55,6 +59,7 @@ constexpr int kStaging = 2 * kResult;              // two for each warp
 constexpr int kAccCols = 256;
 constexpr uint32_t kPolls = 1u << 20;                // of a wait (seconds)
 constexpr int kChunk = 2;                          // K stages between read-outs (fp32)
+constexpr int kLongChunk = 1024;                   // the same (bf16)
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStaging + 512;
 constexpr float kLog2e = 1.4426950408889634f;
 enum { LSE = 0, DLOG = 1, DX = 2, DW = 3 };
@@ -399,10 +404,12 @@ __device__ __forceinline__ int term_b(int q) { return (0x021010 >> (4 * (5 - q))
 
 // The stages of a tile in the order of their use: f(first K stage, term of A,
 // term of B, how the accumulator goes on: 1 starts anew, 2 is read after it).
-template <bool F32, typename F>
+template <bool F32, bool SUMS, typename F>
 __device__ __forceinline__ void each_stage(int steps, F f) {
   if (!F32) {
-    for (int k = 0; k < steps; ++k) f(k, 0, 0, (k == 0 ? 1 : 0) | (k == steps - 1 ? 2 : 0));
+    auto first = [](int k) { return SUMS ? k % kLongChunk == 0 : k == 0; };
+    for (int k = 0; k < steps; ++k)
+      f(k, 0, 0, (first(k) ? 1 : 0) | (k == steps - 1 || (SUMS && first(k + 1)) ? 2 : 0));
   } else {
     for (int k0 = 0; k0 < steps; k0 += kChunk) {
       const int kn = min(kChunk, steps - k0);
@@ -435,7 +442,7 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
     // This CTA's rows of A and columns of B (a copy of B is always 128 of them,
     // whether the tile has use for all or not).
     const int ar = t.m0 + (int)rank * 128, br = t.n0 + (int)rank * (t.N >> 1);
-    each_stage<F32>(t.steps, [&](int k, int ta, int tb, int) {
+    each_stage<F32, false>(t.steps, [&](int k, int ta, int tb, int) {
       mbar_poll(s.empty + 8 * st, phase, limit);
       if (!limit) return;
       const uint32_t dst = s.stages + st * kStage, full = full0 + 8 * st;
@@ -473,7 +480,7 @@ __device__ void copy_role(const XentMaps& maps, const XentMma& a, const Plan& p,
   }
 }
 
-template <bool F32>
+template <bool F32, bool SUMS>
 __device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_t tmem) {
   uint32_t limit = kPolls;
   int st = 0, u = 0;                               // stage; accumulators used
@@ -489,7 +496,7 @@ __device__ void mma_role(const XentMma& a, const Plan& p, const Smem& s, uint32_
     // Which of the operands' two directions is K: MN-major where it is the rows.
     const uint32_t idesc = idesc_bf16_f32(kXtM, t.N) | (t.kind == DW ? 1u << 15 : 0u) |
                            (t.kind >= DX ? 1u << 16 : 0u);
-    each_stage<F32>(t.steps, [&](int, int, int, int flags) {
+    each_stage<F32, SUMS>(t.steps, [&](int, int, int, int flags) {
       if (!limit) return;
       const uint32_t b = u & 1;
       if (flags & 1) mbar_poll(s.tempty + 8 * b, ((u >> 1) & 1) ^ 1, limit);
@@ -558,7 +565,7 @@ __device__ __noinline__ void exact_logits(float* v, int n, const float* x, const
   }
 }
 
-template <bool F32>
+template <bool F32, bool SUMS>
 __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& p, const Smem& s,
                             uint32_t tmem, int n, uint32_t rank) {
   const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
@@ -593,9 +600,10 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
     const int tg = live && t.kind <= DLOG ? a.tgt[row] - t.v0 : -1;
     float2 st = make_float2(0.f, 0.f);
     if (t.kind == DLOG && live) st = a.stat[row];
-    float acc[F32 ? 2 : 1][64];
+    float acc[SUMS ? 2 : 1][64];
     int groups = t.steps ? 1 : 0;
-    if (F32) groups = (t.steps + kChunk - 1) / kChunk;
+    constexpr int kRun = F32 ? kChunk : kLongChunk;
+    if (SUMS) groups = (t.steps + kRun - 1) / kRun;
     // Waits for the next accumulator; false if that is lost.
     auto taken = [&] {
       mbar_poll(s.tfull + 8 * (u & 1), (u >> 1) & 1, limit);
@@ -620,11 +628,11 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
     };
-    if (F32) {
+    if (SUMS) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[F32 ? c : 0][i] = 0.f;
+        for (int i = 0; i < 64; ++i) acc[SUMS ? c : 0][i] = 0.f;
       for (int g = 0; g < groups && limit; ++g) {
         if (!taken()) break;
 #pragma unroll
@@ -636,7 +644,7 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
               tc_ld32(at(c) + 32 * h, r);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[F32 ? c : 0][32 * h + i] += __uint_as_float(r[i]);
+              for (int i = 0; i < 32; ++i) acc[SUMS ? c : 0][32 * h + i] += __uint_as_float(r[i]);
             }
           }
         }
@@ -646,12 +654,12 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
       taken();
     }
     if (!limit) break;
-    // (fp32 sums are in registers, two unrolled chunks; else the code stays small.)
-#pragma unroll (F32 ? 2 : 1)
+    // (Sums are in registers, two unrolled chunks; else the code stays small.)
+#pragma unroll (SUMS ? 2 : 1)
     for (int c = 0; c < 2; ++c) {
       if (c >= chunks) continue;
-      float* v = acc[F32 ? c : 0];
-      if (!F32) {
+      float* v = acc[SUMS ? c : 0];
+      if (!SUMS) {
         if (groups) {
           read64(c, v);
           if (c == chunks - 1) given();
@@ -810,7 +818,9 @@ __device__ void result_role(const XentMaps& maps, const XentMma& a, const Plan& 
   if (!limit && lane == 0) report(a.status, 0x903);
 }
 
-template <bool F32>
+// SUMS: accumulators are read out and added up in registers (fp32, and bf16 sums that
+// are longer than kLongChunk).
+template <bool F32, bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ XentMma a) {
   extern __shared__ unsigned char raw[];
@@ -851,20 +861,20 @@ xent_mma_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ X
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tslot;
-  // fp32 sums take 128 registers of a thread that reads results: 224 for those
+  // Sums take 128 registers of a thread that reads results: 224 for those
   // warps, 56 for the others (together the 168 of each that the CTA starts with).
   // Spilled ones would go through the memory that feeds the products.
   if (warp < 4) {
-    if (F32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && elect_one()) {
       asm volatile("fence.proxy.async;" ::: "memory");   // (rows that kernels ahead wrote)
       copy_role<F32>(maps, a, plan, s, direct, rank);
     } else if (warp == 1 && rank == 0 && elect_one()) {
-      mma_role<F32>(a, plan, s, tmem);
+      mma_role<F32, SUMS>(a, plan, s, tmem);
     }
   } else {
-    if (F32) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    result_role<F32>(maps, a, plan, s, tmem, n, rank);
+    if (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    result_role<F32, SUMS>(maps, a, plan, s, tmem, n, rank);
   }
   __syncwarp();
   tc_fence_before();
@@ -900,16 +910,19 @@ cudaError_t setup_xent_mma(int dtype, int sms, int* clusters) {
     e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
     return e == cudaSuccess && *clusters < 1 ? cudaErrorInvalidConfiguration : e;
   };
-  return dtype == CAT_F32 ? one(xent_mma_kernel<true>) : one(xent_mma_kernel<false>);
+  if (dtype == CAT_F32) return one(xent_mma_kernel<true, true>);
+  const cudaError_t e = one(xent_mma_kernel<false, false>);
+  return e != cudaSuccess ? e : allow_max_smem(xent_mma_kernel<false, true>);
 }
 
 cudaError_t launch_xent_mma(const XentMaps& maps, const XentMma& a, int dtype, int clusters,
-                            cudaStream_t st) {
-  if (dtype == CAT_F32)
-    return launch_dependent(xent_mma_kernel<true>, dim3(2 * clusters), dim3(kThreads), kSmem, st,
-                            maps, a);
-  return launch_dependent(xent_mma_kernel<false>, dim3(2 * clusters), dim3(kThreads), kSmem, st,
-                          maps, a);
+                            long long longest, cudaStream_t st) {
+  auto go = [&](auto kernel) {
+    return launch_dependent(kernel, dim3(2 * clusters), dim3(kThreads), kSmem, st, maps, a);
+  };
+  if (dtype == CAT_F32) return go(xent_mma_kernel<true, true>);
+  return longest > (long long)kLongChunk * kXtK ? go(xent_mma_kernel<false, true>)
+                                                : go(xent_mma_kernel<false, false>);
 }
 
 }  // namespace cat

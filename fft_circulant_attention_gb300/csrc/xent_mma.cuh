@@ -61,8 +61,9 @@ struct XentMma {
   unsigned int* status;
 };
 
+// longest: of the sums over K that a tile takes.
 cudaError_t launch_xent_mma(const XentMaps& maps, const XentMma& a, int dtype, int clusters,
-                            cudaStream_t st);
+                            long long longest, cudaStream_t st);
 // Host: [rows][planes][width] of bf16 (or fp32) with rows row_bytes apart, boxes
 // of 128 bytes by box_rows rows, 128-byte swizzle.
 bool encode_map_planes_sw128(CUtensorMap* map, const void* base, bool f32, unsigned long long width,

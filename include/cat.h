@@ -544,7 +544,9 @@ int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
  * without a target have a zero row in dX and no part in dW; their dloss and lse
  * are not read.  For bf16 data d_iv is rounded to bf16 as an operand of the
  * products (a half step of 2^-8 of each; one dloss for all tokens is applied to
- * the results instead), for fp32 data it is three bf16 terms.  Gradients that a
+ * the results instead), for fp32 data it is three bf16 terms.  Sums over tokens and
+ * ids are fp32; of bf16 summands of one sign a run of 65536 loses 0.0004 (tensor
+ * core accumulators cut instead of rounding), longer sums no more.  Gradients that a
  * value takes part in that is not finite are not finite.
  * CAT_ERR_PLAN_MISMATCH too for a plan with grad = 0.
  */

@@ -1,5 +1,5 @@
 """GPU tests of the values that the training step's operators return where they are
-easily lost: differences of large logits, infinities."""
+easily lost: differences of large logits, infinities, sums over very many tokens."""
 import math
 
 import pytest
@@ -165,3 +165,27 @@ def test_xent_infinite_hidden_states_stay_in_their_tokens(dtype):
         up = float(w[targets[i], i % D]) > 0
         assert loss[i].isnan() if up else loss[i] == math.inf
         assert not dx[i].isfinite().any()
+
+
+@pytest.mark.parametrize("T", [65536, 600000])
+def test_xent_weights_gradient_over_many_tokens_has_no_drift(T):
+    # bf16 sums run in an accumulator that cuts instead of rounding: of summands of one
+    # sign it loses up to a step (2^-23) twice for every 16 of them, 4096 times before
+    # it is read out, far below half a step of the result however many tokens there are.
+    V, D = 40, 72
+    g = torch.Generator(DEV).manual_seed(T)
+    x = (0.5 + torch.rand(T, D, device=DEV, generator=g)).bfloat16()
+    w = (0.05 * torch.randn(V, D, device=DEV, generator=g)).bfloat16()
+    t = torch.zeros(T, dtype=torch.int64, device=DEV)
+    with cat.XentPlan(T, V, D, "bf16") as plan:
+        _, lse = plan.forward(x, w, t)
+        _, dw = plan.backward(x, w, t, lse, torch.ones((), device=DEV), dX=False)
+        plan.sync()
+    d = torch.exp(x.double() @ w.double().T - lse.double()[:, None])
+    d[:, 0] -= 1
+    want = d.float().bfloat16().double().T @ x.double()
+    off = (dw.double() - want) / want
+    drift = 2 * 4096 * 2.0 ** -23
+    assert off.abs().max() <= U["bf16"] + drift
+    # (The results' own rounding goes both ways; four standard deviations of its mean.)
+    assert off[1:].mean().abs() <= drift + 4 * 0.42 * U["bf16"] / (39 * 72) ** 0.5
