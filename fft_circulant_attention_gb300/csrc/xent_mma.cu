@@ -57,7 +57,7 @@ constexpr int kStage = 2 * kOperand;
 constexpr int kResult = 32 * 128;                  // a box of results
 constexpr int kStaging = 2 * kResult;              // two for each warp
 constexpr int kAccCols = 256;
-constexpr uint32_t kPolls = 1u << 20;                // of a wait (seconds)
+constexpr uint32_t kPolls = 1u << 20;              // of a wait: 4 s (3.8 us each)
 constexpr int kChunk = 2;                          // K stages between read-outs (fp32)
 constexpr int kLongChunk = 1024;                   // the same (bf16)
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpiWarps * kStaging + 512;
@@ -543,24 +543,100 @@ __device__ __forceinline__ void stage_f32(uint32_t box, int lane, const float* v
                 __float_as_uint(v[4 * j + 3]));
 }
 
+// A row's values by a warp, 128 on their way at once: f(value, its place) for each
+// that is not finite, in their order, while go_on() (of the whole warp).
+template <typename G, typename F>
+__device__ __forceinline__ void each_odd(const float* row, int D, G go_on, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int k0 = 0; k0 < D && go_on(); k0 += 128) {
+    float a[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      a[u] = k0 + 32 * u + lane < D ? __ldg(row + k0 + 32 * u + lane) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      for (unsigned at = __ballot_sync(0xffffffffu, !(fabsf(a[u]) < INFINITY)); at && go_on();
+           at &= at - 1) {
+        const int j = __ffs(at) - 1;
+        f(__shfl_sync(0xffffffffu, a[u], j), k0 + 32 * u + j);
+      }
+  }
+}
+
 // Logits that are not finite, again by their definition: an infinity is lost in
 // the products of its terms (0 times it, or a difference).  n columns' values of
-// each lane's row (v, in local memory); the warp's lanes with such a value, one
-// after another; x: the lane's row, w: the first column's.
+// each lane's row (v, in local memory); x: the lane's row, w: the first column's.
+// Where a row of X or of W holds values that are not finite, the products with those
+// alone decide; a sum over all of D is taken, by the warp, one after another, only where
+// finite products overflow, or kOdd such values have not decided.  (Such sums for every
+// logit: 4 ms a tile of width 512 where X had turned NaN; so 0.15.)  The other roles
+// wait meanwhile, for 4096 sums at most: 0.06 s at the largest D, where a wait lasts 4 s
+// (kPolls).
+constexpr int kOdd = 64;
 __device__ __noinline__ void exact_logits(float* v, int n, const float* x, const float* w, int D,
                                           bool live) {
+  const unsigned all = 0xffffffffu;
   const int lane = threadIdx.x & 31;
+  auto row_of = [&](int src) {
+    return reinterpret_cast<const float*>(
+        __shfl_sync(all, reinterpret_cast<unsigned long long>(x), src));
+  };
+  bool wrong = false;
+  for (int i = 0; i < n; ++i) wrong = wrong || !(fabsf(v[i]) < INFINITY);
+  wrong = wrong && live;
+  // Rows of X with such values: 32 columns a step, two of them a lane.
+  bool odd = false, full = false;                  // of the lane's row; takes sums
+  for (unsigned left = __ballot_sync(all, wrong); left; left &= left - 1) {
+    const int src = __ffs(left) - 1;
+    float s0 = 0.f, s1 = 0.f;
+    int some = 0;
+    const float* w0 = w + (size_t)lane * D;
+    each_odd(
+        row_of(src), D,
+        [&] {
+          return some < kOdd &&
+                 __any_sync(all, (lane < n && s0 == s0) || (lane + 32 < n && s1 == s1));
+        },
+        [&](float y, int k) {
+          ++some;
+          if (y != y) {
+            s0 = s1 = y;                           // (whatever it meets)
+            return;
+          }
+          if (lane < n) s0 = fmaf(y, __ldg(w0 + k), s0);
+          if (lane + 32 < n) s1 = fmaf(y, __ldg(w0 + (size_t)32 * D + k), s1);
+        });
+    if (!some) continue;
+    if (lane == src) {
+      odd = true;
+      full = some == kOdd;
+    }
+    for (int i = 0; i < n; ++i) {
+      const float s = __shfl_sync(all, i < 32 ? s0 : s1, i & 31);
+      if (lane == src) v[i] = s;
+    }
+  }
+  // And rows of W.
   for (int i = 0; i < n; ++i, w += D) {
-    unsigned left = __ballot_sync(0xffffffffu, live && !(fabsf(v[i]) < INFINITY));
-    while (left) {
+    bool mine = wrong && (odd ? v[i] == v[i] : !(fabsf(v[i]) < INFINITY));
+    if (!__any_sync(all, mine)) continue;
+    float s = odd ? v[i] : 0.f;
+    int some = 0;
+    each_odd(
+        w, D, [&] { return some < kOdd && __any_sync(all, mine && s == s); },
+        [&](float y, int k) {
+          ++some;
+          if (mine) s = y != y ? y : fmaf(__ldg(x + k), y, s);
+        });
+    if (mine && some) v[i] = s;
+    mine = mine && s == s && (full || some == kOdd || (!some && !odd));
+    for (unsigned left = __ballot_sync(all, mine); left; left &= left - 1) {
       const int src = __ffs(left) - 1;
-      left &= left - 1;
-      const float* row = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), src));
-      float sum = 0.f;
-      for (int k = lane; k < D; k += 32) sum = fmaf(__ldg(row + k), __ldg(w + k), sum);
-      sum = warp_sum(sum);
-      if (lane == src) v[i] = sum;
+      const float* row = row_of(src);
+      s = 0.f;
+      for (int k = lane; k < D; k += 32) s = fmaf(__ldg(row + k), __ldg(w + k), s);
+      s = warp_sum(s);
+      if (lane == src) v[i] = s;
     }
   }
 }

@@ -189,3 +189,82 @@ def test_xent_weights_gradient_over_many_tokens_has_no_drift(T):
     assert off.abs().max() <= U["bf16"] + drift
     # (The results' own rounding goes both ways; four standard deviations of its mean.)
     assert off[1:].mean().abs() <= drift + 4 * 0.42 * U["bf16"] / (39 * 72) ** 0.5
+
+
+def spoiled(t, rows):
+    """Rows with infinities of one and of both signs, NaN, both, and values whose
+    products overflow, in the first, the last and other places."""
+    inf, nan = math.inf, math.nan
+    kinds = ({0: inf}, {0: inf, -1: inf}, {20: -inf}, {7: inf, -1: -inf}, {-1: nan},
+             {0: nan, 150: -inf}, {5: 1e30, -1: 1e30}, {5: -1e30})
+    for r, kind in zip(rows, kinds):
+        for k, value in kind.items():
+            t[r, k] = value
+    return t
+
+
+def test_xent_f32_logits_that_are_not_finite():
+    # Each kind of row of X meets each of W: their logits are those of the definition.
+    T, V, D = 130, 300, 300
+    g = gen(21)
+    xs, ws = [0, 3, 31, 32, 77, 100, 128, 129], [0, 63, 64, 128, 191, 200, 298, 299]
+    x = spoiled(torch.randn(T, D, generator=g), xs)
+    w = spoiled(0.2 * torch.randn(V, D, generator=g), ws)
+    w[63, 20] = 0.0
+    l = (x.double()[:, None] * w.double()).sum(-1)
+    l = torch.where(l.abs() > 3.4e38, l * math.inf, l)
+    x, target = x.to(DEV), torch.zeros(T, dtype=torch.int64, device=DEV)
+
+    def agrees(rows, logits):
+        with cat.XentPlan(T, len(rows), D, "f32") as plan:
+            lse = plan.forward(x, rows.to(DEV), target)[1].cpu()
+            plan.sync()
+        want = torch.logsumexp(logits, 1)
+        assert torch.equal(lse.isnan(), want.isnan())
+        assert torch.equal(lse.isinf(), want.isinf()) and torch.equal(lse > 0, want > 0)
+
+    # Each row of W alone with an ordinary one, then all of a tile, without those that
+    # hold NaN and with them.
+    for v in ws:
+        agrees(w[[v, 1]], l[:, [v, 1]])
+    part = [v for v in range(V) if v not in ws[4:6]]
+    agrees(w[part], l[:, part])
+    agrees(w, l)
+
+
+@pytest.mark.parametrize("where", ["x", "w", "ruled out"])
+def test_xent_f32_of_values_that_are_not_finite_takes_no_age(where):
+    # Training that has diverged (NaN everywhere), or ids ruled out by the thousand: no
+    # sum of its own for every logit (50 and 100 times the clean call; 5 to 7 without).
+    T, V, D = 512, 4096, 512
+    g = torch.Generator(DEV).manual_seed(22)
+    x, w = (torch.randn(n, D, device=DEV, generator=g) for n in (T, V))
+    w *= 0.05
+    targets = torch.randint(0, V, (T,), device=DEV, generator=g) // 2 * 2
+    x[:, 0], w[:, 0] = 1.0, 0.0
+    dirty = dict(x=x, w=w)
+    if where == "ruled out":
+        dirty["w"] = w.clone()
+        dirty["w"][1::2, 0] = -math.inf
+    else:
+        dirty[where] = torch.full_like(dirty[where], math.nan)
+    with cat.XentPlan(T, V, D, "f32") as plan, cat.XentPlan(T, V // 2, D, "f32") as half:
+        def took(x, w):
+            times = []
+            for _ in range(5):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                a.record()
+                lse = plan.forward(x, w, targets)[1]
+                b.record()
+                b.synchronize()
+                times.append(a.elapsed_time(b))
+            plan.sync()
+            return sorted(times)[2], lse
+        clean, _ = took(x, w)
+        spoilt, lse = took(**dirty)
+        if where == "ruled out":
+            want = half.forward(x, w[::2].contiguous(), targets // 2)[1]
+            assert torch.allclose(lse, want, rtol=1e-6)
+        else:
+            assert lse.isnan().all()
+        assert spoilt <= 25 * clean, (spoilt, clean)
