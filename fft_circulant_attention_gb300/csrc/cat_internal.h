@@ -174,7 +174,8 @@ struct XentCfg {
   int* tgt;                // [max_tokens] their targets
   int* inv;                // [max_tokens] a token's place among them, or -1
   float* hit;              // [max_tokens] their targets' logits
-  float2* part;            // [parts][max_tokens] maximum and sum over a part of the vocabulary
+  float2* part;            // [parts][tokens of a call] maximum and sum over a part of the
+                           // vocabulary
   float2* stat;            // [max_tokens] lse and upstream gradient
   void* xp;                // [rows_alloc][terms][pitch] their rows of X
   void* wp;                // [V][terms][pitch]

@@ -287,6 +287,12 @@ int run_length(int V, int tokens, int pairs) {
   return r < 1 ? 1 : r > 32 ? 32 : (int)r;
 }
 
+// Parts of a call's rows, and how far apart one part's and the next's lie.
+int part_count(const XentCfg& c, int tokens) {
+  return 2 * tiles(tiles(c.V, kXtN), run_length(c.V, tokens, c.pairs));
+}
+int part_pitch(int tokens) { return tiles(tokens, 32) * 32; }
+
 }  // namespace
 
 // Shapes of a plan's workspace.
@@ -316,17 +322,17 @@ void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   c->piece = (int)pt * kXtN;
   c->pieces = tiles(c->V, c->piece);
 }
+// Of all calls' parts: the fewer tokens the shorter the runs and the more parts of each,
+// so neither the most tokens nor the most parts decide.  (Both at once: 1.05 GB for
+// 131072 tokens and 128256 ids, where 34 MB are used.)
 size_t xent_part_count(const XentCfg& c) {
-  // (The longest list of parts is that of the shortest runs.)
   size_t most = 0;
-  for (long long t = kXtM;; t *= 2) {
-    const long long tokens = t < c.max_tokens ? t : c.max_tokens;
-    const int run = run_length(c.V, (int)tokens, c.pairs);
-    const size_t n = 2 * (size_t)tiles(tiles(c.V, kXtN), run);
+  for (int m = 1; m <= c.rows_alloc / kXtM; ++m) {
+    const int tokens = m * kXtM < c.max_tokens ? m * kXtM : c.max_tokens;
+    const size_t n = (size_t)part_count(c, tokens) * part_pitch(tokens);
     if (n > most) most = n;
-    if (t >= c.max_tokens) break;
   }
-  return most * c.max_tokens;
+  return most;
 }
 
 namespace {
@@ -426,7 +432,7 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
   k.piece = c.piece;
   k.acc_tiles = c.acc_tiles;
   k.pairs = c.pairs;
-  k.ld = c.max_tokens;
+  k.ld = part_pitch(tokens);
   k.count = c.count;
   k.tgt = c.tgt;
   k.rows_of = c.rows;
@@ -453,9 +459,8 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     k.run = run_length(c.V, tokens, c.pairs);
     e = go(mt * tiles(tiles(c.V, kXtN), k.run));
     if (e != cudaSuccess) return e;
-    const int parts = 2 * tiles(tiles(c.V, kXtN), k.run);
     return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)), dim3(32 * kFinWarps), 0,
-                            st, (const float2*)c.part, parts, c.max_tokens, (const int*)c.count,
+                            st, (const float2*)c.part, part_count(c, tokens), k.ld, (const int*)c.count,
                             (const int*)c.rows, (const float*)c.hit, a.loss, a.lse);
   }
   // Piece i's products beside d of piece i + 1.

@@ -268,3 +268,28 @@ def test_xent_f32_of_values_that_are_not_finite_takes_no_age(where):
         else:
             assert lse.isnan().all()
         assert spoilt <= 25 * clean, (spoilt, clean)
+
+
+def test_xent_workspace_of_a_plan_for_the_loss_alone():
+    # The rows of X once more, three words a token, and the parts of the longest call.
+    T, V, D = 131072, 128256, 64
+    with cat.XentPlan(T, V, D, "bf16", grad=False) as plan:
+        size = int(plan.describe().split("workspace=")[1].split()[0])
+    assert size <= T * (2 * D + 3 * 4) + 40 * 10 ** 6, size
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_xent_calls_of_any_length_in_one_plan(dtype):
+    # As each in a plan of its own, and the largest plan's rows never run into each other.
+    T, V, D = 20000, 3000, 16
+    g = gen(23)
+    x, w = torch.randn(T, D, generator=g).to(TORCH[dtype]).to(DEV), \
+        torch.randn(V, D, generator=g).to(TORCH[dtype]).to(DEV)
+    t = torch.randint(0, V, (T,), generator=g).to(DEV)
+    with cat.XentPlan(T, V, D, dtype, grad=False) as plan:
+        for n in (20000, 1, 31, 257, 1300, 5000, 9999, 19999):
+            with cat.XentPlan(n, V, D, dtype, grad=False) as own:
+                a, b = plan.forward(x[:n], w, t[:n]), own.forward(x[:n], w, t[:n])
+                own.sync()
+            assert all(torch.equal(p, q) for p, q in zip(a, b)), n
+        plan.sync()
