@@ -26,6 +26,46 @@ def gen(seed):
     return torch.Generator().manual_seed(seed)
 
 
+# ------------------------------------------------------------------ embedding
+def zipf(n, V, g):
+    u = torch.rand(n, device=DEV, generator=g, dtype=torch.float64)
+    return (torch.exp(u * math.log(V + 1)) - 1).long().clamp(0, V - 1)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V,D,kind", [
+    (16385, 200, 16, "one"), (16385, 5000, 16, "zipf"), (50001, 3, 24, "zipf"),
+    (50001, 60000, 16, "one"), (300001, 70, 8, "zipf"), (300001, 2, 16, "one"),
+    (30000, 5000, 768, "zipf"), (40000, 900, 768, "padded"), (20001, 300, 1024, "zipf"),
+    (20001, 40, 1000, "one"), (9000, 100, 513, "zipf"), (12000, 100, 8192, "zipf"),
+    (12000, 7, 8192, "one"),
+])
+def test_embed_gradient_counts_every_token(n, V, D, kind, dtype, accumulate):
+    # Gradients of small integers: sums in fp32 are exact in any order, below 2^24, so
+    # that no part of a run that many pieces hold can be lost or counted twice.
+    g = torch.Generator(DEV).manual_seed(n + D)
+    ids = torch.full((n,), V - 1, device=DEV) if kind == "one" else zipf(n, V, g)
+    if kind == "padded":
+        ids[torch.rand(n, device=DEV, generator=g) < 0.3] = -1
+    draw = lambda *shape: torch.randint(-8, 9, shape, device=DEV, generator=g)  # noqa: E731
+    dy, base = draw(n, D), draw(V, D)
+    held = ids >= 0
+    want = torch.zeros((V, D), device=DEV, dtype=torch.float64)
+    want.index_add_(0, ids[held], dy[held].double())
+    want *= 2.0
+    assert want.abs().max() < 2 ** 24
+    there = torch.bincount(ids[held], minlength=V) > 0
+    if accumulate:
+        want += base
+    with cat.EmbedPlan(n, V, D, dtype, scale=2.0) as plan:
+        dw = plan.backward(ids, dy.to(TORCH[dtype]),
+                           dW=base.to(TORCH[dtype]) if accumulate else None,
+                           accumulate=accumulate)
+        plan.sync()
+    assert there.any() and torch.equal(dw, want.float().to(TORCH[dtype]))
+
+
 # --------------------------------------------------------------- cross entropy
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,D", [(1, 8), (700, 64), (300, 33)])
@@ -293,3 +333,36 @@ def test_xent_calls_of_any_length_in_one_plan(dtype):
                 own.sync()
             assert all(torch.equal(p, q) for p, q in zip(a, b)), n
         plan.sync()
+
+
+@pytest.mark.parametrize("each", [False, True])
+@pytest.mark.parametrize("T,V,D,kept", [(300, 2500, 256, 1.0), (1000, 777, 96, 0.9),
+                                        (2100, 9001, 64, 0.3), (40, 5000, 768, 1.0)])
+def test_xent_bf16_gradients_round_twice(T, V, D, kept, each):
+    # d once and each result once, to the nearest, all else in fp32: the error's norm is
+    # that of these two roundings made in 64 bits (the products' own errors, about 2^-20
+    # of the values, turn a rounding round now and then: a twentieth more).
+    g = gen(T)
+    x = torch.randn(T, D, generator=g).bfloat16()
+    w = (2 / math.sqrt(D) * torch.randn(V, D, generator=g)).bfloat16()
+    targets = torch.randint(0, V, (T,), generator=g)
+    targets[torch.rand(T, generator=g) >= kept] = -1
+    up = torch.rand(T if each else (), generator=g) + 0.1
+    with cat.XentPlan(T, V, D, "bf16") as plan:
+        ins = [t.to(DEV) for t in (x, w, targets)]
+        _, lse = plan.forward(*ins)
+        got = plan.backward(*ins, lse, up.to(DEV))
+        plan.sync()
+    held = targets >= 0
+    x, w, z = x.double()[held], w.double(), lse.double().cpu()[held]
+    d = torch.exp(x @ w.T - z[:, None])
+    d[torch.arange(len(d)), targets[held]] -= 1.0
+    f = up.double()
+    if each:
+        d, f = d * f[held][:, None], torch.ones(())
+    near = lambda t: t.float().bfloat16().double()  # noqa: E731
+    dx = got[0].double().cpu()
+    assert (dx[~held] == 0).all()
+    for a, exact, twice in ((dx[held], f * (d @ w), near(f * (near(d) @ w))),
+                            (got[1].double().cpu(), f * (d.T @ x), near(f * (near(d).T @ x)))):
+        assert (a - exact).norm() <= 1.05 * (twice - exact).norm()
