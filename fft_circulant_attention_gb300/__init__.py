@@ -894,9 +894,10 @@ class XentPlan(_OpPlan):
 __all__ = ["EmbedPlan", "ResNormPlan", "XentPlan", "cat_plan_create_embed", "cat_embed_forward",
            "cat_embed_backward", "cat_plan_create_resnorm", "cat_resnorm_forward",
            "cat_resnorm_backward", "cat_plan_create_xent", "cat_xent_forward",
-           "cat_xent_backward", "id_code", "CAT_I32", "CAT_I64", "AttnPlan", "LayerNormPlan", "ClipPlan", "cat_plan_create_attn", "cat_attn_forward",
-           "cat_attn_backward", "cat_plan_create_layernorm", "cat_layernorm_forward",
-           "cat_layernorm_backward", "cat_plan_create_clip", "cat_grad_norm", "cat_grad_clip",
+           "cat_xent_backward", "id_code", "CAT_I32", "CAT_I64", "AttnPlan", "LayerNormPlan",
+           "ClipPlan", "cat_plan_create_attn", "cat_attn_forward", "cat_attn_backward",
+           "cat_plan_create_layernorm", "cat_layernorm_forward", "cat_layernorm_backward",
+           "cat_plan_create_clip", "cat_grad_norm", "cat_grad_clip",
            "CatError", "Plan", "Plan2D", "lib", "dtype_code", "cat_plan_create", "cat_plan_destroy",
            "cat_plan_set_stream", "cat_forward", "cat_forward_zstar", "cat_forward_host",
            "cat_plan_sync", "cat_plan_describe", "cat_plan_timing", "cat_plan_stage_times",

@@ -497,8 +497,8 @@ int clip_grid(int sms);
 int clip_max_parts(int count, int sms);
 cudaError_t launch_clip(const ClipCfg& c, const void* const* in, void* const* out, float max_norm,
                         float* norm, bool scale, cudaStream_t st);
-// Embedding (embed.cu).  embed_range: ids a sorting CTA owns; embed_piece: places
-// of the sorted list a group of threads sums.
+// Embedding (embed.cu).  embed_range: ids a sorting CTA owns; the others: elements of a
+// plan's arrays.
 int embed_range(int V, int sms);
 size_t embed_part_count(int max_tokens, int D);
 size_t embed_split_count(int max_tokens);

@@ -77,13 +77,14 @@ bool alloc(cat_plan_s* p, T** ptr, size_t count) {
   return true;
 }
 
-// The status word, cleared; `fail` releases the half-built plan.
+// Releases a half-built plan and passes its error on.
 inline int fail(cat_plan_s* p, int st) {
   cudaGetLastError();
   cat_plan_destroy(p);
   return st;
 }
 
+// The status word, cleared.
 inline bool alloc_status(cat_plan_s* p) {
   return alloc(p, &p->status, 1) && cat::settled([&](cudaStream_t s) {
            return cudaMemsetAsync(p->status, 0, sizeof(unsigned int), s);

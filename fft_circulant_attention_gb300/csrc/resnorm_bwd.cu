@@ -27,37 +27,13 @@ namespace {
 // The sums over the rows, as they lie in a partial row.
 enum { S_GAMMA = 0, S_BETA = 1, S_GATE = 2, S_PG = 3, S_PB = 4, kSums = 5 };
 
-// a and b summed over the TPR threads of row group `sub`; `red` holds two
-// floats a warp for each of four uses in turn, so that one barrier a call is
-// enough.
-template <int TPR, int BT>
-__device__ __forceinline__ void sum2(float& a, float& b, float2* red, int sub, int use) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if (TPR > 32) {
-    red += use * (BT / 32);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(TPR) : "memory");
-    red += sub * (TPR / 32);
-    a = b = 0.f;
-#pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) {
-      a += red[i].x;
-      b += red[i].y;
-    }
-  }
-}
-
 constexpr int kPerSm = 2;                // most CTAs of an SM
 
 template <int TPR>
 constexpr int block_threads() {
   return TPR > 256 ? TPR : TPR == 96 ? 480 : 256;
 }
-template <int TPR, int E>
+template <int TPR>
 constexpr int per_sm() {
   return TPR > 256 || TPR == 96 ? 1 : 2;
 }
@@ -66,7 +42,7 @@ constexpr int per_sm() {
 // GATE: GATE_ROW, or any other kind (a.gate_kind).  FULL: the threads' vectors are
 // the row, none lies behind it.
 template <typename T, int VEC, int TPR, int E, int POST, int GATE, bool FULL>
-__global__ void __launch_bounds__(block_threads<TPR>(), per_sm<TPR, E>())
+__global__ void __launch_bounds__(block_threads<TPR>(), per_sm<TPR>())
 resnorm_bwd_kernel(ResNormArgs a) {
   using V = Vec<T, VEC>;
   using Raw = typename V::Raw;
@@ -160,7 +136,7 @@ resnorm_bwd_kernel(ResNormArgs a) {
       }
     }
     float s1 = p1.total(), s2 = p2.total();
-    sum2<TPR, BT>(s1, s2, red, sub, use);
+    row_sum2<TPR, BT>(s1, s2, red, sub, use);
     s1 *= inv;
     s2 *= inv;
     // g becomes dh, then du·pg; xh becomes b̂.
@@ -221,7 +197,7 @@ resnorm_bwd_kernel(ResNormArgs a) {
     if (POST) {
       t1 = q1.total();
       t2 = q2.total();
-      sum2<TPR, BT>(t1, t2, red, sub, use + 1);
+      row_sum2<TPR, BT>(t1, t2, red, sub, use + 1);
       t1 *= inv;
       t2 *= inv;
     }
@@ -299,7 +275,7 @@ template <typename T, int VEC, int TPR, int E, int POST, int GATE, bool FULL>
 cudaError_t go(const ResNormArgs& a, cudaStream_t st, bool setup) {
   constexpr int BT = block_threads<TPR>();
   const int per = BT / TPR, need = (a.rows + per - 1) / per;
-  const int most = a.max_parts / kPerSm * per_sm<TPR, E>();
+  const int most = a.max_parts / kPerSm * per_sm<TPR>();
   const int grid = need < most ? need : most;
   const size_t smem = (size_t)kSums * a.D * sizeof(float);
   if (setup)

@@ -111,10 +111,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// Two sums at once over the TPR threads of row group `sub`; `red` holds two
-// floats a warp for each of two uses in turn (`use`), so that one barrier a
-// call (the group's own) is enough.
-template <int TPR>
+// Two sums at once over the TPR threads of row group `sub` of a CTA of BT threads;
+// `red` holds two floats a warp for each use in turn (`use`), so that one barrier
+// a call (the group's own) is enough.
+template <int TPR, int BT = kRowThreads>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int sub, int use) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -122,7 +122,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float2* red, int su
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
   if (TPR > 32) {
-    red += use * (kRowThreads / 32);
+    red += use * (BT / 32);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
     asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(TPR) : "memory");
     red += sub * (TPR / 32);

@@ -309,7 +309,8 @@ void xent_shape(XentCfg* c, int D, int dtype, int pairs) {
   // launch, so that their number is a multiple of the pairs, or just below; more
   // of the vocabulary at once where there are few tokens (the pairs then share a
   // piece's ids out among slices of dX, of at most 65536 each), and less where two
-  // pieces' d would take more than 2 GB.
+  // pieces' d would take more than 2 GB, down to one tile of 256 ids (which takes more by
+  // itself from 2^21 rows of terms on: fp32's most tokens, 2 x 1.6 GB).
   const int nt = tiles(D, kXtN), vt = tiles(c->V, kXtN);
   long long w = 32768 / c->rows_alloc;
   if (w < 1) w = 1;
