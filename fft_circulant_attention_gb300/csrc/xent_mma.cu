@@ -33,10 +33,10 @@
 // tiles differ in length, and each pair gets about the same number of K stages.
 // Every wait is bounded; a lost one ends its role's loop and is reported.
 //
-// Measured at 16384 tokens, 50257 ids, width 768, bf16: the forward 610 to 628 us (2.0
-// to 2.07 PFLOP/s, the tensor pipe 94 % busy), d of 12800 ids 205 us (72 %), dW and dX
-// of as many beside d of the next 550 us (83 %); 2048 fp32 tokens, 32003 ids, width
-// 512: 207, 278 (63 %: d's three terms are written) and 465 us.
+// Measured at 16384 tokens, 50257 ids, width 768, bf16: the forward 597 to 628 us (2.0
+// to 2.1 PFLOP/s, the tensor pipe 93 to 95 % busy), d of 12800 ids 201 us (72 %), dW and
+// dX of as many beside d of the next 530 us (85 %); 2048 fp32 tokens, 32003 ids, width
+// 512: 206, 275 (64 %: d's three terms are written) and 458 us.
 #include <cuda_bf16.h>
 
 #include "elem.cuh"

@@ -495,7 +495,8 @@ int cat_resnorm_forward(cat_plan_t plan, const void *R, const void *B,
  *   dh = dH + (gradient of LN at H for dY),  dR = dh,
  *   dgate = scale·u·dh (summed over the rows where the gate is [D]),
  *   du = scale·gate·dh,  dB = post ? (gradient of LN at B for du) : du,
- * and the weights' gradients (fp32 sums over the rows, rounded once).  dgate and
+ * and the weights' gradients (fp32 sums over the rows, rounded once).  H enters as
+ * stored: in dgamma a bf16 H is half a step off the one whose norm Y is.  dgate and
  * the weights' gradients may each be NULL (not wanted), all are overwritten.
  * rows = 0 writes zeros to the sums over the rows.
  */

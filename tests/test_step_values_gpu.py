@@ -337,7 +337,9 @@ def test_xent_calls_of_any_length_in_one_plan(dtype):
 
 @pytest.mark.parametrize("each", [False, True])
 @pytest.mark.parametrize("T,V,D,kept", [(300, 2500, 256, 1.0), (1000, 777, 96, 0.9),
-                                        (2100, 9001, 64, 0.3), (40, 5000, 768, 1.0)])
+                                        (2100, 9001, 64, 0.3), (40, 5000, 768, 1.0),
+                                        (65537, 300, 40, 1.0), (140000, 40, 200, 0.9),
+                                        (65600, 300, 64, 0.01), (70001, 40, 64, 0.0)])
 def test_xent_bf16_gradients_round_twice(T, V, D, kept, each):
     # d once and each result once, to the nearest, all else in fp32: the error's norm is
     # that of these two roundings made in 64 bits (the products' own errors, about 2^-20
