@@ -92,8 +92,8 @@ __device__ __forceinline__ void pack8(const T* src, __nv_bfloat16* dst, int c, i
 // statistics for the backward (stat: lse and the upstream gradient, 1 where one
 // value serves all: results are scaled by that in fp32, so that the target's entry of
 // d, near -1, is not rounded off for the factor's sake) and their rows of X, dense
-// and, for fp32, as bf16 terms; rows of zeros up to a multiple of 256.  A CTA takes `per` tokens and counts the others' itself.  The
-// other CTAs pack W.
+// and, for fp32, as bf16 terms; rows of zeros up to a multiple of 256.  A CTA takes
+// `per` tokens and counts the others' itself.  The other CTAs pack W.
 template <typename T>
 __global__ void __launch_bounds__(kPrep) xent_prepare_kernel(Prep p) {
   const int vecs = p.pitch / 8;
@@ -461,8 +461,9 @@ cudaError_t launch_xent(const cat_plan_s* p, XentArgs a, Ids targets, int tokens
     e = go(mt * tiles(tiles(c.V, kXtN), k.run));
     if (e != cudaSuccess) return e;
     return launch_dependent(xent_finish_kernel, dim3(tiles(tokens, 32)), dim3(32 * kFinWarps), 0,
-                            st, (const float2*)c.part, part_count(c, tokens), k.ld, (const int*)c.count,
-                            (const int*)c.rows, (const float*)c.hit, a.loss, a.lse);
+                            st, (const float2*)c.part, part_count(c, tokens), k.ld,
+                            (const int*)c.count, (const int*)c.rows, (const float*)c.hit, a.loss,
+                            a.lse);
   }
   // Piece i's products beside d of piece i + 1.
   for (int i = -1; i < c.pieces; ++i) {

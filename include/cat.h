@@ -525,10 +525,11 @@ int cat_plan_create_xent(cat_plan_t *out, int max_tokens, int V, int D,
  * (fp32).  Tokens without a target: both are 0, their rows of X are not read.
  * The logits are not kept.  Products run on the tensor cores with fp32 sums, fp32
  * operands as three bf16 terms (errors of fp32's own size); an fp32 logit that is
- * not finite is computed again by its definition, one by one.  So weights of minus
- * infinity rule ids out, a logit of plus infinity makes lse that.  loss is (the largest logit - the target's) + log of
- * the sum of exponentials of the differences to the largest: never negative, and no
- * worse for large logits; lse is rounded to fp32 once.  T = 0: no-op.
+ * not finite is computed again by its definition.  So weights of minus infinity
+ * rule ids out, a logit of plus infinity makes lse that.  loss is (the largest
+ * logit - the target's) + log of the sum of exponentials of the differences to the
+ * largest: never negative, and no worse for large logits; lse is rounded to fp32
+ * once.  T = 0: no-op.
  */
 int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
                      const void *targets, int id_type, float *loss, float *lse,
@@ -539,16 +540,16 @@ int cat_xent_forward(cat_plan_t plan, const void *X, const void *W,
  * gradient dloss of the losses (fp32: one value for all tokens, dloss_each = 0,
  * or [T], dloss_each = 1):
  *   d_iv = dloss_i (exp(l_iv - lse_i) - [v = targets_i]),  dX = d·W,  dW = dᵀ·X.
- * The logits are made again, a piece of the vocabulary at a time; the probabilities
- * of a row share the rounding of its lse (half a step, 2^-24 |lse|, relative).  dX [T, D]
- * and dW [V, D] are overwritten; either may be NULL (not wanted).  Tokens
- * without a target have a zero row in dX and no part in dW; their dloss and lse
- * are not read.  For bf16 data d_iv is rounded to bf16 as an operand of the
- * products (a half step of 2^-8 of each; one dloss for all tokens is applied to
- * the results instead), for fp32 data it is three bf16 terms.  Sums over tokens and
- * ids are fp32; of bf16 summands of one sign a run of 65536 loses 0.0004 (tensor
- * core accumulators cut instead of rounding), longer sums no more.  Gradients that a
- * value takes part in that is not finite are not finite.
+ * The logits are made again, a piece of the vocabulary at a time; the
+ * probabilities of a row share the rounding of its lse (half a step, 2^-24 |lse|,
+ * relative).  dX [T, D] and dW [V, D] are overwritten; either may be NULL (not
+ * wanted).  Tokens without a target have a zero row in dX and no part in dW; their
+ * dloss and lse are not read.  For bf16 data d_iv is rounded to bf16 as an operand
+ * of the products (a half step of 2^-8 of each; one dloss for all tokens is applied
+ * to the results instead), for fp32 data it is three bf16 terms.  Sums over tokens
+ * and ids are fp32; of bf16 summands of one sign a run of 65536 loses 0.0004 (tensor
+ * core accumulators cut instead of rounding), longer sums no more.  Gradients that
+ * a value takes part in that is not finite are not finite.
  * CAT_ERR_PLAN_MISMATCH too for a plan with grad = 0.
  */
 int cat_xent_backward(cat_plan_t plan, const void *X, const void *W,
